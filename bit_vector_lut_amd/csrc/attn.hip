@@ -1,0 +1,505 @@
+// attn.hip -- attention of a chunk of new tokens over the paged key/value cache (gfx950).
+//
+//   y[t][h] = sum_j softmax_j(scale q . k_j) v_j over the positions j that row t sees.
+//
+// One pass over the keys with the running maximum m and sum l of the softmax: a tile of scores s
+// gives m' = max(m, s), the sums so far shrink by 2^((m - m') c), and p = 2^((s - m') c) joins them
+// (c = scale log2 e).  The query heads that share a key head are rows of one tile, row = token *
+// group + head in group, so a key is read once for all of them.
+//
+// Operands without a transpose.  Scores are computed as S^T = K Q^T and outputs as O^T = V^T P^T,
+// 16x16 matrix-core steps.  A result of the first holds, per lane, four scores of one query row;
+// the second wants, per lane, eight keys of one query row.  The order of the keys along an
+// operand is free as long as both operands agree, so the two key sub-tiles of a 32-key tile take
+// keys 8(m/4) + m%4 and the same + 4: a lane then holds keys 8g .. 8g+7 (g = lane / 16), packs
+// them to 16 bits in place, and the matching operand of V^T is one 16-byte load because the cache
+// keeps values as [D][page_size].  Neither product goes through LDS.
+#include "op.h"
+
+#include <algorithm>
+
+namespace vqmlp {
+
+namespace {
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kMaxSplit = 64;
+
+struct AttnArgs {
+    const uint16_t* q;
+    uint16_t* y;
+    float* lse;
+    const uint16_t *kc, *vc;
+    const int32_t *table, *cu, *kv_len;
+    float* opart;  // [row][split][D], row = token * heads + head (split launches only)
+    float* ml;     // [row][split][2]: maximum of the scores, sum
+    int64_t ld_table, ld_q, ld_y;
+    int T, R, heads, kv_heads, g, D, shift, n_pages, window, nsplit, split_tiles;
+    int width;     // pages per table row
+    float scale;
+};
+
+// exp2 of a difference to the maximum: fp16 probabilities carry a factor 2^12, so that keys down to
+// 2^-36 of the largest still count (binary16 ends at 2^-24; 2^12 times any sum of them stays far
+// inside fp32).  bfloat16 has the range by itself.
+template <class E>
+constexpr float kBias = __is_same(E, F16) ? 12.f : 0.f;
+
+struct Tile {       // what one workgroup works on
+    int r, n;       // request (R: the rows behind the last request), its new tokens
+    int c0;         // its first row
+    int rho0;       // first packed row of the tile
+    int kv;         // keys of the request
+    int kmin, kmax; // keys seen by any row of the tile
+    int full_lo, full_hi;  // keys seen by every row of the tile
+};
+
+// Row tiles of all requests in one launch without their lengths on the host: request r owns tile
+// numbers floor(cu[r] g / MT) + r and on, which is always enough for ceil(n g / MT) tiles, and
+// the numbers left over return.  Every wave looks the request up for itself, 64 at a time.
+template <int MT>
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, Tile& t) {
+    const int lane = threadIdx.x & 63;
+    auto row = [&](int r) { return min(max(a.cu[r], 0), a.T); };
+    auto start = [&](int c, int r) { return int(int64_t(c) * a.g / MT) + r; };
+    int count = 0;
+    for (int r0 = 0; r0 <= a.R; r0 += 64) {
+        const int r = r0 + lane;
+        const bool le = r <= a.R && start(row(r), r) <= x;
+        count += __popcll(__ballot(le));
+    }
+    t.r = max(0, count - 1);
+    t.c0 = row(t.r);
+    const int c1 = t.r < a.R ? row(t.r + 1) : a.T;
+    t.n = c1 - t.c0;
+    t.rho0 = (x - start(t.c0, t.r)) * MT;
+    if (t.rho0 < 0 || int64_t(t.rho0) >= int64_t(t.n) * a.g) return false;
+    t.kv = t.r < a.R ? max(a.kv_len[t.r], 0) : 0;
+    const int i0 = t.rho0 / a.g;
+    const int i1 = int(min(int64_t(t.rho0) + MT - 1, int64_t(t.n) * a.g - 1) / a.g);
+    const int p0 = t.kv - t.n + i0, p1 = t.kv - t.n + i1;
+    const int cap = a.width << a.shift;
+    t.kmax = t.r < a.R ? min(p1, cap - 1) : -1;
+    t.kmin = a.window ? max(0, p0 - a.window + 1) : 0;
+    t.full_hi = min(p0, cap - 1);
+    t.full_lo = a.window ? max(0, p1 - a.window + 1) : 0;
+    return true;
+}
+
+// ---------------------------------------------------------------- few rows: keys over the waves
+// NW waves share 16 NB rows of one key head and a split of the keys, tile by tile in turn, each
+// straight from the cache into its registers; their sums join in LDS at the end.
+template <class E, int DP, int NB, bool FULL, int NW>
+__global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
+    constexpr int MT = 16 * NB, KS = DP / 32, DT = DP / 16;
+    constexpr int DC = DP < 128 ? DP : 128;  // columns joined per round
+    __shared__ float obuf[NW][16][DC + 4];
+    __shared__ float mlbuf[NW][MT][2];
+    Tile t;
+    if (!find_tile<MT>(a, blockIdx.x, t)) return;
+    const int hk = blockIdx.y, split = blockIdx.z;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lr = lane & 15, g = lane >> 4;
+    const int D = FULL ? DP : a.D;
+    const int P1 = (1 << a.shift) - 1;
+
+    int lo[NB], hi[NB];
+    u32x4 qf[NB][KS];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int rho = t.rho0 + 16 * b + lr;
+        const int i = rho / a.g, hh = rho - i * a.g;
+        const bool real = i < t.n;
+        const int p = t.kv - t.n + i;
+        hi[b] = real && t.r < a.R ? p : -1;
+        lo[b] = a.window ? max(0, p - a.window + 1) : 0;
+        const uint16_t* src = a.q + (t.c0 + i) * a.ld_q + int64_t(hk * a.g + hh) * a.D + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[b][s] = u32x4{0, 0, 0, 0};
+            if (real && (FULL || 32 * s + 8 * g < D))
+                qf[b][s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
+        }
+    }
+    float m[NB], l[NB];
+    f32x4 o[NB][DT];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        m[b] = kNegInf;
+        l[b] = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[b][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const float c = a.scale * 1.4426950408889634f;
+
+    const int kt0 = t.kmin >> 5;
+    const int nt = t.kmax >= t.kmin ? (t.kmax >> 5) + 1 - kt0 : 0;
+    const int begin = kt0 + min(nt, split * a.split_tiles);
+    const int end = kt0 + (split == a.nsplit - 1 ? nt : min(nt, (split + 1) * a.split_tiles));
+    const int32_t* row = a.table + (t.r < a.R ? t.r : 0) * a.ld_table;
+    // page numbers of the lane's two K rows and of its eight V columns in a tile
+    const int krow = 8 * (lr >> 2), vcol = 8 * g;
+    auto page_of = [&](int key) { return row[min(key >> a.shift, a.width - 1)]; };
+    int kt = begin + wave;
+    int kp_next = 0, vp_next = 0;
+    if (kt < end) {
+        kp_next = page_of(kt * 32 + krow);
+        vp_next = page_of(kt * 32 + vcol);
+    }
+    for (; kt < end; kt += NW) {
+        const int k0 = kt * 32;
+        int kp = kp_next, vp = vp_next;
+        if (kt + NW < end) {
+            kp_next = page_of(k0 + 32 * NW + krow);
+            vp_next = page_of(k0 + 32 * NW + vcol);
+        }
+        const bool vbad = uint32_t(vp) >= uint32_t(a.n_pages);
+        if (uint32_t(kp) >= uint32_t(a.n_pages)) kp = 0;
+        if (vbad) vp = 0;
+        const uint16_t* kr = a.kc +
+            (((int64_t(kp) * a.kv_heads + hk) << a.shift) + ((k0 + krow) & P1) + (lr & 3)) * D;
+        const uint16_t* vr = a.vc +
+            ((int64_t(vp) * a.kv_heads + hk) * D << a.shift) + ((k0 + vcol) & P1);
+        u32x4 ka[KS], kb[KS], vf[DT];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            // columns behind D meet zeros of the query: any finite chunk will do
+            const int at = FULL || 32 * s + 8 * g < D ? 32 * s + 8 * g : 0;
+            ka[s] = *reinterpret_cast<const u32x4*>(kr + at);
+            kb[s] = *reinterpret_cast<const u32x4*>(kr + 4 * D + at);
+        }
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+            const int d = 16 * dt + lr;
+            vf[dt] = *reinterpret_cast<const u32x4*>(vr + (int64_t(FULL ? d : min(d, D - 1)) << a.shift));
+        }
+        const bool edge = k0 < t.full_lo || k0 + 31 > t.full_hi || __any(vbad);
+        if (edge) {
+            // values that no row may see can be anything in memory: make them zero
+            const int k = k0 + vcol;
+            u32x4 keep;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool x = !vbad && k + 2 * j >= t.kmin && k + 2 * j <= t.kmax;
+                const bool z = !vbad && k + 2 * j + 1 >= t.kmin && k + 2 * j + 1 <= t.kmax;
+                keep[j] = (x ? 0xFFFFu : 0u) | (z ? 0xFFFF0000u : 0u);
+            }
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) vf[dt] &= keep;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                sa = E::mfma16(ka[s], qf[b][s], sa);
+                sb = E::mfma16(kb[s], qf[b][s], sb);
+            }
+            if (edge) {
+                const int k = k0 + vcol;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (vbad || k + j > hi[b] || k + j < lo[b]) sa[j] = kNegInf;
+                    if (vbad || k + 4 + j > hi[b] || k + 4 + j < lo[b]) sb[j] = kNegInf;
+                }
+            }
+            float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
+                             fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            if (__any(mx > m[b])) {
+                const float mn = fmaxf(m[b], mx);
+                const float alpha = __builtin_amdgcn_exp2f((m[b] - (mn == kNegInf ? 0.f : mn)) * c);
+                m[b] = mn;
+                l[b] *= alpha;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) o[b][dt] *= alpha;
+            }
+            const float mc = (m[b] == kNegInf ? 0.f : m[b] * c) - kBias<E>;
+            float p[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(fmaf(sa[j], c, -mc));
+                p[4 + j] = __builtin_amdgcn_exp2f(fmaf(sb[j], c, -mc));
+            }
+            l[b] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            // the probabilities as matrix-core operands: one rounding to the type of the values
+            const u32x4 pf = {pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3]), pack16<E>(p[4], p[5]),
+                              pack16<E>(p[6], p[7])};
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) o[b][dt] = E::mfma16(vf[dt], pf, o[b][dt]);
+        }
+    }
+
+    // join the waves
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        l[b] += __shfl_xor(l[b], 16);
+        l[b] += __shfl_xor(l[b], 32);
+        if (g == 0) {
+            mlbuf[wave][16 * b + lr][0] = m[b];
+            mlbuf[wave][16 * b + lr][1] = l[b];
+        }
+    }
+    constexpr int TPR = NW * 64 / 16;  // threads per row
+    const int jr = threadIdx.x / TPR, jt = threadIdx.x % TPR;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int d0 = 0; d0 < DP; d0 += DC) {
+            __syncthreads();
+#pragma unroll
+            for (int dt = 0; dt < DC / 16; ++dt)
+                *reinterpret_cast<f32x4*>(&obuf[wave][lr][16 * dt + 4 * g]) = o[b][d0 / 16 + dt];
+            __syncthreads();
+            const int rho = t.rho0 + 16 * b + jr;
+            const int i = rho / a.g, hh = rho - i * a.g;
+            if (i >= t.n) continue;
+            float mm = kNegInf;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mlbuf[w][16 * b + jr][0]);
+            const float ms = mm == kNegInf ? 0.f : mm;
+            float wt[NW], sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                wt[w] = __builtin_amdgcn_exp2f((mlbuf[w][16 * b + jr][0] - ms) * c);
+                sum = fmaf(wt[w], mlbuf[w][16 * b + jr][1], sum);
+            }
+            const int head = hk * a.g + hh;
+            const int64_t rowi = int64_t(t.c0 + i) * a.heads + head;
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            for (int d = jt * 4; d < DC && d0 + d < D; d += TPR * 4) {
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(&obuf[w][jr][d]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = fmaf(wt[w], x[j], v[j]);
+                }
+                if (a.nsplit == 1) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] *= inv;
+                    u32x2 w2 = {pack16<E>(v[0], v[1]), pack16<E>(v[2], v[3])};
+                    *reinterpret_cast<u32x2*>(a.y + (t.c0 + i) * a.ld_y + int64_t(head) * D + d0 + d) = w2;
+                } else {
+                    *reinterpret_cast<f32x4*>(a.opart + (rowi * a.nsplit + split) * D + d0 + d) = v;
+                }
+            }
+            if (d0 == 0 && jt == 0) {
+                if (a.nsplit > 1) {
+                    a.ml[(rowi * a.nsplit + split) * 2] = mm;
+                    a.ml[(rowi * a.nsplit + split) * 2 + 1] = sum;
+                } else if (a.lse) {
+                    a.lse[rowi] = sum > 0.f ? fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f)
+                                            : kNegInf;
+                }
+            }
+        }
+    }
+}
+
+// Join the splits of a row: a wave per row, lane = split for the weights, then lanes over D.
+template <class E>
+__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (row >= int64_t(a.T) * a.heads) return;
+    float m = kNegInf, l = 0.f;
+    if (lane < a.nsplit) {
+        m = a.ml[(row * a.nsplit + lane) * 2];
+        l = a.ml[(row * a.nsplit + lane) * 2 + 1];
+    }
+    float mm = m;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+    const float c = a.scale * 1.4426950408889634f;
+    const float w = __builtin_amdgcn_exp2f((m - (mm == kNegInf ? 0.f : mm)) * c);
+    const float sum = wave_sum(w * l);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const float* src = a.opart + row * a.nsplit * a.D + 4 * lane;
+    const bool in = 4 * lane < a.D;
+    for (int s = 0; s < a.nsplit; ++s) {
+        // every lane takes part in the exchange: lanes behind D hold weights too
+        const float ws = __shfl(w, s);
+        const float ls = __shfl(l, s);
+        if (!(ls > 0.f) || !in) continue;  // a split without keys wrote no sums
+        const f32x4 x = *reinterpret_cast<const f32x4*>(src + int64_t(s) * a.D);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(ws, x[j], v[j]);
+    }
+    const int64_t tok = row / a.heads;
+    const int head = int(row % a.heads);
+    if (in) {
+        u32x2 w2 = {pack16<E>(v[0] * inv, v[1] * inv), pack16<E>(v[2] * inv, v[3] * inv)};
+        *reinterpret_cast<u32x2*>(a.y + tok * a.ld_y + int64_t(head) * a.D + 4 * lane) = w2;
+    }
+    if (lane == 0 && a.lse)
+        a.lse[row] = sum > 0.f ? fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f) : kNegInf;
+}
+
+// ---------------------------------------------------------------- host half
+
+struct AttnGeom {
+    int nb, tiles, nsplit, split_tiles;
+    size_t opart, ml, bytes;
+};
+
+AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
+    AttnGeom G;
+    const int g = d.heads / d.kv_heads;
+    const int64_t rows = std::max<int64_t>(1, (int64_t(d.T) * g + d.R - 1) / std::max(1, d.R));
+    const int most = d.D > 128 ? 2 : 4;
+    G.nb = int(std::min<int64_t>(most, (rows + 15) / 16));
+    if (G.nb == 3 && most == 4) G.nb = 4;
+    const int mt = 16 * G.nb;
+    G.tiles = int(int64_t(d.T) * g / mt) + d.R + 1;
+    const int64_t active = std::max<int64_t>(d.R, (int64_t(d.T) * g + mt - 1) / mt) * d.kv_heads;
+    const int keys = std::max(1, d.max_kv);
+    const int key_tiles = (keys + 31) / 32;
+    const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
+    const int most_split = std::max(1, key_tiles / 8);
+    G.nsplit = int(std::min<int64_t>(std::min<int64_t>(want, most_split), kMaxSplit));
+    G.split_tiles = (key_tiles + G.nsplit - 1) / G.nsplit;
+    const size_t rows_all = size_t(d.T) * d.heads;
+    G.opart = 0;
+    G.ml = align256(G.nsplit > 1 ? rows_all * G.nsplit * d.D * 4 : 0);
+    G.bytes = G.ml + align256(G.nsplit > 1 ? rows_all * G.nsplit * 8 : 0);
+    return G;
+}
+
+bool attn_page_shift(int page_size, int* shift) {
+    for (int s = 3; s <= 10; ++s)
+        if (page_size == 1 << s) return *shift = s, true;
+    return false;
+}
+
+vqmlp_status attn_check(const vqmlp_attn_desc* p, const char* who, int* shift) {
+    OP_REQUIRE(p, "%s: null description", who);
+    const vqmlp_attn_desc& d = *p;
+    OP_REQUIRE(op_dtype16(d.dtype), "%s: dtype %d is not F16 or BF16", who, d.dtype);
+    OP_REQUIRE(attn_page_shift(d.page_size, shift), "%s: page_size %d is not a power of two in 8..1024",
+               who, d.page_size);
+    OP_REQUIRE(d.T >= 0 && d.R >= 1 && d.heads >= 1 && d.kv_heads >= 1 && d.n_pages >= 1 &&
+                   d.table_width >= 1 && d.window >= 0 && d.max_kv >= 0,
+               "%s: a size is out of range", who);
+    OP_REQUIRE(d.D >= 8 && d.D <= 256 && d.D % 8 == 0, "%s: D=%d is not a multiple of 8 up to 256", who, d.D);
+    OP_REQUIRE(d.heads % d.kv_heads == 0, "%s: heads=%d is no multiple of kv_heads=%d", who, d.heads,
+               d.kv_heads);
+    if (d.heads / d.kv_heads > 64 || d.R > 65536 || d.kv_heads > 65535)
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: heads / kv_heads above 64 or R above 65536", who);
+    if (int64_t(d.T) * d.heads > 0x3FFFFFFF)
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: T * heads above 2^30 - 1", who);
+    OP_REQUIRE((int64_t(d.n_pages) << *shift) <= 0x7FFFFFFF && (int64_t(d.table_width) << *shift) <= 0x3FFFFFFF,
+               "%s: slots pass 2^31 - 1 or positions 2^30 - 1", who);
+    OP_REQUIRE(d.scale > 0.f && d.scale < __builtin_inff(), "%s: scale is not positive and finite", who);
+    return VQMLP_OK;
+}
+
+template <class E, int DP, int NB>
+void launch_wave_nb(const AttnArgs& a, int tiles, hipStream_t s) {
+    const dim3 grid(tiles, a.kv_heads, a.nsplit);
+    if (a.D == DP)
+        k_attn_wave<E, DP, NB, true, 4><<<grid, 256, 0, s>>>(a);
+    else
+        k_attn_wave<E, DP, NB, false, 4><<<grid, 256, 0, s>>>(a);
+}
+
+template <class E>
+void launch_attn(const AttnArgs& a, const AttnGeom& G, hipStream_t s) {
+    if (a.D <= 64) {
+        if (G.nb == 1) launch_wave_nb<E, 64, 1>(a, G.tiles, s);
+        else if (G.nb == 2) launch_wave_nb<E, 64, 2>(a, G.tiles, s);
+        else launch_wave_nb<E, 64, 4>(a, G.tiles, s);
+    } else if (a.D <= 128) {
+        if (G.nb == 1) launch_wave_nb<E, 128, 1>(a, G.tiles, s);
+        else if (G.nb == 2) launch_wave_nb<E, 128, 2>(a, G.tiles, s);
+        else launch_wave_nb<E, 128, 4>(a, G.tiles, s);
+    } else {
+        if (G.nb == 1) launch_wave_nb<E, 256, 1>(a, G.tiles, s);
+        else if (G.nb == 2) launch_wave_nb<E, 256, 2>(a, G.tiles, s);
+        else launch_wave_nb<E, 256, 3>(a, G.tiles, s);
+    }
+    if (a.nsplit > 1) {
+        const int64_t rows = int64_t(a.T) * a.heads;
+        k_attn_join<E><<<dim3((rows + 3) / 4), 256, 0, s>>>(a);
+    }
+}
+
+}  // namespace
+
+}  // namespace vqmlp
+
+extern "C" vqmlp_status vqmlp_paged_attn_workspace(const vqmlp_attn_desc* p, size_t* bytes) {
+    using namespace vqmlp;
+    OP_REQUIRE(bytes, "vqmlp_paged_attn_workspace: null pointer");
+    int shift = 0, cus = 0;
+    if (const vqmlp_status st = attn_check(p, "vqmlp_paged_attn_workspace", &shift)) return st;
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    *bytes = attn_geom(*p, cus).bytes;
+    return op_ok();
+}
+
+extern "C" vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc* p, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    using namespace vqmlp;
+    int shift = 0, cus = 0;
+    if (const vqmlp_status st = attn_check(p, "vqmlp_paged_attn", &shift)) return st;
+    const vqmlp_attn_desc& d = *p;
+    if (d.T == 0) return op_ok();
+    OP_REQUIRE(d.q && d.y && d.k_cache && d.v_cache && d.table && d.cu_q && d.kv_len,
+               "vqmlp_paged_attn: null pointer");
+    const int64_t row = int64_t(d.heads) * d.D;
+    OP_REQUIRE((d.T == 1 || (d.ld_q >= row && d.ld_y >= row)) && d.ld_q >= 0 && d.ld_y >= 0 &&
+                   d.ld_q <= (int64_t(1) << 40) && d.ld_y <= (int64_t(1) << 40) && d.ld_q % 8 == 0 &&
+                   d.ld_y % 8 == 0,
+               "vqmlp_paged_attn: token strides have to be multiples of 8, at least heads * D");
+    OP_REQUIRE(d.ld_table >= d.table_width, "vqmlp_paged_attn: ld_table is below table_width");
+    OP_REQUIRE(op_aligned(d.q, 16) && op_aligned(d.y, 16) && op_aligned(d.k_cache, 16) &&
+                   op_aligned(d.v_cache, 16) && op_aligned(d.table, 4) && op_aligned(d.cu_q, 4) &&
+                   op_aligned(d.kv_len, 4) && op_aligned(d.lse, 4),
+               "vqmlp_paged_attn: q, y and the caches have to be 16-byte aligned, the rest 4-byte");
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    const AttnGeom G = attn_geom(d, cus);
+    if (G.bytes) {
+        OP_REQUIRE(workspace && op_aligned(workspace, 256),
+                   "vqmlp_paged_attn: the workspace is null or not 256-byte aligned");
+        if (workspace_bytes < G.bytes)
+            OP_FAIL(VQMLP_ERR_WORKSPACE, "vqmlp_paged_attn: workspace holds %zu bytes, this call needs %zu",
+                    workspace_bytes, G.bytes);
+    }
+    AttnArgs a;
+    a.q = static_cast<const uint16_t*>(d.q);
+    a.y = static_cast<uint16_t*>(d.y);
+    a.lse = d.lse;
+    a.kc = static_cast<const uint16_t*>(d.k_cache);
+    a.vc = static_cast<const uint16_t*>(d.v_cache);
+    a.table = d.table;
+    a.cu = d.cu_q;
+    a.kv_len = d.kv_len;
+    a.opart = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + G.opart);
+    a.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + G.ml);
+    a.ld_table = d.ld_table;
+    a.ld_q = d.ld_q;
+    a.ld_y = d.ld_y;
+    a.T = d.T;
+    a.R = d.R;
+    a.heads = d.heads;
+    a.kv_heads = d.kv_heads;
+    a.g = d.heads / d.kv_heads;
+    a.D = d.D;
+    a.shift = shift;
+    a.n_pages = d.n_pages;
+    a.window = std::min(d.window, 0x3FFFFFFF);
+    a.nsplit = G.nsplit;
+    a.split_tiles = G.split_tiles;
+    a.width = d.table_width;
+    a.scale = d.scale;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (d.dtype == VQMLP_F16) launch_attn<F16>(a, G, s);
+    else launch_attn<BF16>(a, G, s);
+    if (trace_enabled())
+        trace_line("paged_attn T=%d R=%d heads=%d/%d D=%d: register tiles, %d rows, %d key splits%s", d.T,
+                   d.R, d.heads, d.kv_heads, d.D, 16 * G.nb, G.nsplit, G.nsplit > 1 ? " + join" : "");
+    return op_launched("vqmlp_paged_attn");
+}

@@ -26,6 +26,12 @@ inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Host only: record the text of a failure for vqmlp_last_error() (this thread) and return st.
 int set_last_error(int st, const char* fmt, ...);
+// Host only: VQMLP_TRACE (read on each call) and one trace line on stderr.
+bool trace_enabled();
+void trace_line(const char* fmt, ...);
+// Host only: VQMLP_OK when the current device is a gfx950, with its compute-unit count; looked up
+// once per device.
+int device_cus(int* cus);
 // Host only: the allocation-free forward's per-device scratch array (noalloc.hip): fetch this
 // device's address and zero it, once per device (called by vqmlp_create).
 void noalloc_setup();

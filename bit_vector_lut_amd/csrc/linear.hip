@@ -1,0 +1,687 @@
+// linear.hip -- linear attention with a decay per head and token (gfx950).
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   y_t = scale S_t^T q_t.
+//
+// Few tokens: the recurrence itself, state in registers (k_lin_step), bound by reading and
+// writing the FP32 states.  Many: chunks of 64 tokens.  With b_t = g_1 + .. + g_t inside a chunk
+// and S the state before it,
+//   y_t = scale (e^{b_t} S^T q_t + sum_{j <= t} e^{b_t - b_j} (q_t . k_j) v_j)
+//   S'  = e^{b_64} S + sum_j k_j (e^{b_64 - b_j} v_j)^T
+// all four products on the matrix cores (k_lin_chunk).
+#include "op.h"
+
+#include <algorithm>
+
+namespace vqmlp {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
+constexpr int kC = 64;          // tokens per chunk
+constexpr int kStepMaxQ = 16;
+
+struct LinArgs {
+    const uint16_t *q, *k, *v;
+    const float* g;
+    uint16_t* y;
+    const float* sin;
+    float* sout;
+    const int32_t *cu, *ctx, *index;
+    float* seg;   // [unit][v_heads][Dk][Dv] states of segments (split launches only)
+    float* dec;   // [unit][v_heads] decay over a segment
+    int64_t ld_q, ld_k, ld_v, ld_y, ld_g;
+    int T, R, hk, hv, Dk, Dv, n_states, L;
+    float scale;
+};
+
+__device__ __forceinline__ int lin_row(const LinArgs& a, int r) { return min(max(a.cu[r], 0), a.T); }
+
+// The state slot of a request, or -1, and whether it starts from what the slot holds.
+__device__ __forceinline__ int lin_slot(const LinArgs& a, int r, bool* old) {
+    int s = a.index ? a.index[r] : r;
+    if (uint32_t(s) >= uint32_t(a.n_states)) s = -1;
+    *old = s >= 0 && (!a.ctx || a.ctx[r] > 0);
+    return s;
+}
+
+// ---------------------------------------------------------------- the recurrence
+// A wave owns a head's Dk x 32 columns of the state: lane = (row block lane / 8, four columns of
+// lane % 8), rows of a block contiguous so that a token's q and k come as 16-byte chunks.  The sum
+// over rows is a lane's own rows, then three exchanges; no LDS and no barrier, so that a wave's
+// loads are all that is in flight.
+template <class E, int RPL>  // rows per lane: Dk <= 8 RPL
+__global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
+    const int r = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x, cb = lane & 7, rb = lane >> 3;
+    const int col = blockIdx.z * 32 + cb * 4, row0 = rb * RPL;
+    if (r == a.R) {  // rows behind the last request
+        for (int64_t t = lin_row(a, a.R) + rb; t < a.T; t += 8)
+            if (col < a.Dv) *reinterpret_cast<u32x2*>(a.y + t * a.ld_y + int64_t(h) * a.Dv + col) = u32x2{0, 0};
+        return;
+    }
+    const int c0 = lin_row(a, r), n = lin_row(a, r + 1) - c0;
+    bool old;
+    const int slot = lin_slot(a, r, &old);
+    const int64_t base = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv;
+    f32x4 s[RPL];
+    const bool cin = col < a.Dv;
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (old && cin && row0 + i < a.Dk)
+            s[i] = *reinterpret_cast<const f32x4*>(a.sin + base + int64_t(row0 + i) * a.Dv + col);
+    }
+    const int hk = h / (a.hv / a.hk);
+    constexpr int CH = RPL / 8;
+    u32x4 kn[CH], qn[CH];
+    u32x2 vn;
+    float gn;
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            kn[c] = qn[c] = u32x4{0, 0, 0, 0};
+            if (row0 + 8 * c < a.Dk) {
+                kn[c] = *reinterpret_cast<const u32x4*>(a.k + t * a.ld_k + int64_t(hk) * a.Dk + row0 + 8 * c);
+                qn[c] = *reinterpret_cast<const u32x4*>(a.q + t * a.ld_q + int64_t(hk) * a.Dk + row0 + 8 * c);
+            }
+        }
+        vn = u32x2{0, 0};
+        if (cin) vn = *reinterpret_cast<const u32x2*>(a.v + t * a.ld_v + int64_t(h) * a.Dv + col);
+        gn = a.g[t * a.ld_g + h];
+    };
+    if (n > 0) fetch(c0);
+    for (int i = 0; i < n; ++i) {
+        u32x4 kw[CH], qw[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) kw[c] = kn[c], qw[c] = qn[c];
+        const f32x4 v = {lo16<E>(vn[0]), hi16<E>(vn[0]), lo16<E>(vn[1]), hi16<E>(vn[1])};
+        const float e = expf(fmaxf(gn, kMinG));
+        if (i + 1 < n) fetch(c0 + i + 1);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float kk = j & 1 ? hi16<E>(kw[c][j / 2]) : lo16<E>(kw[c][j / 2]);
+                const float qq = j & 1 ? hi16<E>(qw[c][j / 2]) : lo16<E>(qw[c][j / 2]);
+                f32x4& x = s[8 * c + j];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    x[z] = fmaf(kk, v[z], x[z] * e);
+                    acc[z] = fmaf(qq, x[z], acc[z]);
+                }
+            }
+#pragma unroll
+        for (int o = 8; o < 64; o <<= 1)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) acc[z] += __shfl_xor(acc[z], o);
+        if (rb == 0 && cin) {
+            const u32x2 w = {pack16<E>(acc[0] * a.scale, acc[1] * a.scale),
+                             pack16<E>(acc[2] * a.scale, acc[3] * a.scale)};
+            *reinterpret_cast<u32x2*>(a.y + int64_t(c0 + i) * a.ld_y + int64_t(h) * a.Dv + col) = w;
+        }
+    }
+    if (slot >= 0 && cin) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+            if (row0 + i < a.Dk)
+                *reinterpret_cast<f32x4*>(a.sout + base + int64_t(row0 + i) * a.Dv + col) = s[i];
+    }
+}
+
+// ---------------------------------------------------------------- chunks on the matrix cores
+// A workgroup of four waves owns one head of one segment (a.L tokens at most) and goes through its
+// chunks in order; wave w owns NTV tiles of 16 value columns and the whole Dk of their state, which
+// stays in matrix-core accumulators (FP32) from chunk to chunk.
+//
+// Orders chosen so that nothing but the token axis has to be transposed:
+//   - the state product S += K^T V leaves, per lane, rows (dk) of one column (dv); the product
+//     S^T Q wants, per lane, eight dk of one dv.  The two row tiles of a pair take dk 8(m/4) + m%4
+//     and the same + 4, so a lane holds dk 8g .. 8g+7 and packs them where they are;
+//   - K^T and V^T (token runs per column) are what both token-axis products want; each thread turns
+//     an 8 x 8 block in registers on the way to LDS;
+//   - the scores are made as K Q^T, 16 keys per wave, and pass through LDS once, since every wave
+//     needs them all.
+//
+// Precision.  The state and its decays are FP32.  What joins the state is e^{..} v in FP32, handed
+// to the matrix cores as a sum of parts of the 16-bit type (two for binary16, three for bfloat16,
+// whose parts are shorter), so that the state loses nothing to the operand's type.  The scores
+// times their decays, and the state as an operand of S^T Q, are rounded once to the 16-bit type:
+// the outputs are rounded to it as well.  binary16 parts are kept in range by powers of two: value
+// parts by 2^e (e from the chunk's largest value), the state's operand by its own maximum.
+constexpr int kTok = kC + 8;  // LDS row stride in elements: 144 bytes, 16-byte chunks spread over banks
+
+struct LinSmem {
+    uint16_t kt[128][kTok];  // [dk][token]
+    uint16_t vt[128][kTok];  // [dv][token]
+    uint16_t p[kC][kTok];    // [query][key] scores
+    float eb[kC], tail[kC], bl[kC];
+    float etot;
+};
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, uint32_t(e + 127) << 23); }
+// Exponent of |x| (floor of log2), -127 for zero and subnormals.
+__device__ __forceinline__ int expo(float x) {
+    return int((__builtin_bit_cast(uint32_t, x) >> 23) & 0xFF) - 127;
+}
+
+struct LinUnit {
+    int r, c0, n, seg, nseg, first;  // request, its first row and tokens; segment; unit of segment 0
+};
+
+// Units of all requests in one launch without their lengths on the host: request r owns unit
+// numbers floor(cu[r] / L) + r and on (enough for ceil(n / L), and one where n is 0).
+__device__ __forceinline__ bool lin_unit(const LinArgs& a, int x, LinUnit& u) {
+    const int lane = threadIdx.x & 63;
+    int count = 0;
+    for (int r0 = 0; r0 <= a.R; r0 += 64) {
+        const int r = r0 + lane;
+        count += __popcll(__ballot(r <= a.R && lin_row(a, min(r, a.R)) / a.L + r <= x));
+    }
+    u.r = max(0, count - 1);
+    u.c0 = lin_row(a, u.r);
+    const int c1 = u.r < a.R ? lin_row(a, u.r + 1) : a.T;
+    u.n = max(0, c1 - u.c0);
+    u.first = u.c0 / a.L + u.r;
+    u.seg = x - u.first;
+    u.nseg = max(1, (u.n + a.L - 1) / a.L);
+    return u.seg >= 0 && u.seg < u.nseg;
+}
+
+// OUT: outputs and the final state; otherwise the states of the segments, for a later OUT launch.
+template <class E, int DKP, int NTV, bool OUT>
+__global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
+    constexpr int KS = DKP / 32;       // steps over dk, pairs of state row tiles
+    constexpr bool HALF = __is_same(E, F16);
+    constexpr int PARTS = HALF ? 2 : 3;
+    __shared__ LinSmem sm;
+    LinUnit u;
+    if (!lin_unit(a, blockIdx.x, u)) return;
+    const int h = blockIdx.y, hk = h / (a.hv / a.hk);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int lr = lane & 15, g4 = lane >> 4;
+    const int DVP = 64 * NTV;
+    const int t0 = u.seg * a.L, t1 = min(u.n, t0 + a.L);
+    if (u.r == a.R) {  // rows behind the last request
+        if (OUT)
+            for (int i = tid; i < (t1 - t0) * (a.Dv / 8); i += 256) {
+                const int64_t t = u.c0 + t0 + i / (a.Dv / 8);
+                *reinterpret_cast<u32x4*>(a.y + t * a.ld_y + int64_t(h) * a.Dv + (i % (a.Dv / 8)) * 8) =
+                    u32x4{0, 0, 0, 0};
+            }
+        return;
+    }
+    if (!OUT && u.nseg == 1) return;
+    bool old;
+    const int slot = lin_slot(a, u.r, &old);
+    const int64_t ss = int64_t(a.Dk) * a.Dv;
+    const int64_t sbase = (int64_t(max(slot, 0)) * a.hv + h) * ss;
+    auto seg_state = [&](int unit) { return a.seg + (int64_t(unit) * a.hv + h) * ss; };
+
+    // state element (pair p, tile b, column tile v, i): dk = 32 p + 8 g4 + 4 b + i, dv = dvc(v)
+    auto dvc = [&](int v, int m) {
+        return NTV == 1 ? 16 * wave + m : 32 * wave + 8 * (m >> 2) + (m & 3) + 4 * v;
+    };
+    f32x4 S[KS][2][NTV];
+    auto each_state = [&](auto&& f) {
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) {
+                    const int dk = 32 * p + 8 * g4 + 4 * b, dv = dvc(v, lr);
+                    if (dk < a.Dk && dv < a.Dv) f(S[p][b][v], int64_t(dk) * a.Dv + dv);
+                }
+    };
+    auto load_state = [&](const float* src) {
+        each_state([&](f32x4& x, int64_t at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = src[at + int64_t(i) * a.Dv];
+        });
+    };
+    auto store_state = [&](float* dst, float mul) {
+        each_state([&](f32x4& x, int64_t at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[at + int64_t(i) * a.Dv] = x[i] * mul;
+        });
+    };
+#pragma unroll
+    for (int p = 0; p < KS; ++p)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int v = 0; v < NTV; ++v) S[p][b][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!OUT) {
+        // the last segment's own state is not needed before the outputs: its place keeps the
+        // start state, which an in-place OUT launch could not read safely for segment 0
+        if (u.seg == 0 || u.seg == u.nseg - 1) {
+            if (old) load_state(a.sin + sbase);
+            if (u.seg == u.nseg - 1) {
+                store_state(seg_state(u.first + u.seg), 1.f);
+                return;
+            }
+        }
+    } else if (u.nseg == 1) {
+        if (old) load_state(a.sin + sbase);
+    } else if (u.seg == 0) {
+        load_state(seg_state(u.first + u.nseg - 1));
+    } else {
+        load_state(seg_state(u.first));
+        for (int j = 1; j < u.seg; ++j) {
+            const float dj = a.dec[int64_t(u.first + j) * a.hv + h];
+            const float* src = seg_state(u.first + j);
+            each_state([&](f32x4& x, int64_t at) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], dj, src[at + int64_t(i) * a.Dv]);
+            });
+        }
+    }
+
+    // staging: thread = one 8 x 8 block (tokens 8 bi .., columns 8 bj ..) of K or V
+    const int bi = tid & 7, bj = tid >> 3;
+    const bool isk = bj < DKP / 8;
+    const int cj = isk ? bj : bj - DKP / 8;
+    const bool stage = isk || cj < DVP / 8;
+    const bool inside = isk ? 8 * cj < a.Dk : stage && 8 * cj < a.Dv;
+    const uint16_t* src = isk ? a.k + int64_t(hk) * a.Dk + 8 * cj : a.v + int64_t(h) * a.Dv + 8 * cj;
+    const int64_t ld = isk ? a.ld_k : a.ld_v;
+    u32x4 blk[8];
+    float gv = 0.f;
+    auto fetch = [&](int t) {  // chunk at token t of the request
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int tt = t + 8 * bi + i;
+            blk[i] = u32x4{0, 0, 0, 0};
+            if (inside && tt < t1) blk[i] = *reinterpret_cast<const u32x4*>(src + (u.c0 + tt) * ld);
+        }
+        if (wave == 0) gv = t + lane < t1 ? fmaxf(a.g[(u.c0 + t + lane) * a.ld_g + h], kMinG) : 0.f;
+    };
+    float decay = 1.f;  // over the segment so far (!OUT)
+    int e = 0;          // S is kept in units of 2^-e
+    if (t0 < t1) fetch(t0);
+    for (int t = t0; t < t1; t += kC) {
+        if (stage) {
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) {
+                const uint32_t sel = cc & 1 ? 0x07060302u : 0x05040100u;
+                u32x4 w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = __builtin_amdgcn_perm(blk[2 * i + 1][cc / 2], blk[2 * i][cc / 2], sel);
+                uint16_t* dst = isk ? &sm.kt[8 * cj + cc][8 * bi] : &sm.vt[8 * cj + cc][8 * bi];
+                *reinterpret_cast<u32x4*>(dst) = w;
+            }
+        }
+        if (wave == 0) {
+            // lane = token: sums from the front for e^{b}, from the back for the tails, each
+            // accurate against its own size
+            float b = gv, z = gv;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const float x = __shfl_up(b, o), y = __shfl_down(z, o);
+                if (lane >= o) b += x;
+                if (lane + o < 64) z += y;
+            }
+            z = __shfl_down(z, 1);
+            sm.eb[lane] = expf(b);
+            sm.bl[lane] = b * kLog2e;
+            sm.tail[lane] = expf(lane == 63 ? 0.f : z);
+            if (lane == 63) sm.etot = expf(b);
+        }
+        if (t + kC < t1) fetch(t + kC);
+        u32x4 qf[OUT ? 4 : 1][KS];
+        u32x4 kf[KS];
+        if constexpr (OUT) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bool in = 32 * s + 8 * g4 < a.Dk;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int tt = t + 16 * x + lr;
+                    qf[x][s] = u32x4{0, 0, 0, 0};
+                    if (in && tt < t1)
+                        qf[x][s] = *reinterpret_cast<const u32x4*>(a.q + (u.c0 + tt) * a.ld_q +
+                                                                   int64_t(hk) * a.Dk + 32 * s + 8 * g4);
+                }
+                const int tt = t + 16 * wave + lr;
+                kf[s] = u32x4{0, 0, 0, 0};
+                if (in && tt < t1)
+                    kf[s] = *reinterpret_cast<const u32x4*>(a.k + (u.c0 + tt) * a.ld_k + int64_t(hk) * a.Dk +
+                                                            32 * s + 8 * g4);
+            }
+        }
+        __syncthreads();
+        f32x4 o[NTV][4];
+        if constexpr (OUT) {
+            // scores of this wave's 16 keys with all queries from there on
+            const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&sm.bl[16 * wave + 4 * g4]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (x < (wave & 2)) continue;
+                f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[x][s], sc);
+                const float bt = sm.bl[16 * x + lr];
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool see = 16 * wave + 4 * g4 + i <= 16 * x + lr;
+                    p[i] = see ? sc[i] * a.scale * __builtin_amdgcn_exp2f(bt - bj4[i]) : 0.f;
+                }
+                *reinterpret_cast<u32x2*>(&sm.p[16 * x + lr][16 * wave + 4 * g4]) =
+                    u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
+            }
+            // e^{b} S^T Q
+            int f = 0;
+            if constexpr (HALF) {
+                float mx = 0.f;
+#pragma unroll
+                for (int p = 0; p < KS; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[p][b][v][i]));
+                mx = wave_max(mx);
+                f = min(max(13 - expo(mx), -100), 100);
+            }
+            const float up = pow2(f), down = a.scale * pow2(-f) * pow2(-e);
+#pragma unroll
+            for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[v][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < KS; ++p)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) {
+                    f32x4 s0 = S[p][0][v], s1 = S[p][1][v];
+                    if constexpr (HALF) s0 *= up, s1 *= up;
+                    const u32x4 sf = {pack16<E>(s0[0], s0[1]), pack16<E>(s0[2], s0[3]),
+                                      pack16<E>(s1[0], s1[1]), pack16<E>(s1[2], s1[3])};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[v][x] = E::mfma16(sf, qf[x][p], o[v][x]);
+                }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float eb = sm.eb[16 * x + lr] * down;
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) o[v][x] *= eb;
+            }
+            __syncthreads();
+        }
+        u32x4 vf[NTV][2];
+#pragma unroll
+        for (int v = 0; v < NTV; ++v)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[dvc(v, lr)][32 * c + 8 * g4]);
+        if constexpr (OUT) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int c = 0; c <= x / 2; ++c) {
+                    const u32x4 pf = *reinterpret_cast<const u32x4*>(&sm.p[16 * x + lr][32 * c + 8 * g4]);
+#pragma unroll
+                    for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
+                }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int tt = t + 16 * x + lr;
+                if (tt >= t1) continue;
+                uint16_t* dst = a.y + (u.c0 + tt) * a.ld_y + int64_t(h) * a.Dv;
+                if constexpr (NTV == 2) {
+                    const int dv = 32 * wave + 8 * g4;
+                    const u32x4 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3]),
+                                     pack16<E>(o[1][x][0], o[1][x][1]), pack16<E>(o[1][x][2], o[1][x][3])};
+                    if (dv < a.Dv) *reinterpret_cast<u32x4*>(dst + dv) = w;
+                } else {
+                    const int dv = 16 * wave + 4 * g4;
+                    const u32x2 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3])};
+                    if (dv < a.Dv) *reinterpret_cast<u32x2*>(dst + dv) = w;
+                }
+            }
+        }
+        // the state after the chunk
+        int en = e;
+        if constexpr (HALF) {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = vf[v][c][i];
+                        mx = max(mx, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
+                    }
+#pragma unroll
+            for (int o2 = 32; o2; o2 >>= 1) mx = max(mx, uint32_t(__shfl_xor(int(mx), o2)));
+            en = mx ? 13 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^13, 2^14)
+        }
+        const float lift = pow2(en);
+        const float keep = sm.etot * pow2(en - e);
+        e = en;
+        decay *= sm.etot;
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) S[p][b][v] *= keep;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sm.tail[32 * c + 8 * g4]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sm.tail[32 * c + 8 * g4 + 4]);
+            u32x4 part[NTV][PARTS];
+#pragma unroll
+            for (int v = 0; v < NTV; ++v) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = lo16<E>(vf[v][c][i]) * ((i < 2 ? w0[2 * i] : w1[2 * i - 4]) * lift);
+                    x[2 * i + 1] = hi16<E>(vf[v][c][i]) * ((i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]) * lift);
+                }
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w = pack16<E>(x[2 * i], x[2 * i + 1]);
+                        // one rounded value for the operand and for what is left of x: otherwise
+                        // the compiler rounds x twice, once fused with its product, and the two
+                        // may differ by a step
+                        asm("" : "+v"(w));
+                        part[v][q][i] = w;
+                        x[2 * i] -= lo16<E>(w);
+                        x[2 * i + 1] -= hi16<E>(w);
+                    }
+            }
+#pragma unroll
+            for (int p = 0; p < KS; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const u32x4 kk = *reinterpret_cast<const u32x4*>(
+                        &sm.kt[32 * p + 8 * (lr >> 2) + (lr & 3) + 4 * b][32 * c + 8 * g4]);
+#pragma unroll
+                    for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+                        for (int v = 0; v < NTV; ++v) S[p][b][v] = E::mfma16(kk, part[v][q], S[p][b][v]);
+                }
+        }
+        __syncthreads();
+    }
+    if (!OUT) {
+        store_state(seg_state(u.first + u.seg), pow2(-e));
+        if (tid == 0) a.dec[int64_t(u.first + u.seg) * a.hv + h] = decay;
+    } else if (u.seg == u.nseg - 1 && slot >= 0) {
+        store_state(a.sout + sbase, pow2(-e));
+    }
+}
+
+// ---------------------------------------------------------------- host half
+
+struct LinGeom {
+    bool step;
+    int L, units;  // tokens per segment (the whole request when not split), unit numbers
+    bool split;
+    size_t dec, bytes;
+};
+
+LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
+    LinGeom G{};
+    G.step = d.max_q <= kStepMaxQ;
+    if (G.step) return G;
+    const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
+    const int64_t heads = int64_t(d.R) * d.v_heads;
+    int nseg = int(std::min<int64_t>(32, (2 * int64_t(cus) + heads - 1) / heads));
+    nseg = std::max(1, std::min(nseg, most / 256));
+    G.split = nseg > 1;
+    const int chunks = (most + kC - 1) / kC;
+    // not split: a segment holds all T tokens, so any request fits, whatever max_q says
+    G.L = G.split ? (chunks + nseg - 1) / nseg * kC : std::max(1, (d.T + kC - 1) / kC) * kC;
+    G.units = d.T / G.L + d.R + 1;
+    if (G.split) {
+        G.dec = align256(size_t(G.units) * d.v_heads * d.Dk * d.Dv * 4);
+        G.bytes = G.dec + align256(size_t(G.units) * d.v_heads * 4);
+    }
+    return G;
+}
+
+vqmlp_status lin_check(const vqmlp_linear_desc* p, const char* who) {
+    OP_REQUIRE(p, "%s: null description", who);
+    const vqmlp_linear_desc& d = *p;
+    OP_REQUIRE(op_dtype16(d.dtype), "%s: dtype %d is not F16 or BF16", who, d.dtype);
+    OP_REQUIRE(d.T >= 0 && d.R >= 1 && d.k_heads >= 1 && d.v_heads >= 1 && d.n_states >= 0 && d.max_q >= 0,
+               "%s: a size is out of range", who);
+    OP_REQUIRE(d.v_heads % d.k_heads == 0, "%s: v_heads=%d is no multiple of k_heads=%d", who, d.v_heads,
+               d.k_heads);
+    OP_REQUIRE(d.Dk >= 8 && d.Dk <= 128 && d.Dk % 8 == 0 && d.Dv >= 8 && d.Dv <= 128 && d.Dv % 8 == 0,
+               "%s: Dk=%d, Dv=%d are not multiples of 8 up to 128", who, d.Dk, d.Dv);
+    if (d.R > 65535 || d.v_heads > 65535 || d.T > 0x3FFFFFFF)
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: R or v_heads above 65535, or T above 2^30 - 1", who);
+    OP_REQUIRE(d.scale == d.scale && d.scale - d.scale == 0.f, "%s: scale is not finite", who);
+    return VQMLP_OK;
+}
+
+template <class E>
+void launch_step(const LinArgs& a, hipStream_t s) {
+    const dim3 grid(a.R + 1, a.hv, (a.Dv + 31) / 32);
+    if (a.Dk <= 64) k_lin_step<E, 8><<<grid, 64, 0, s>>>(a);
+    else k_lin_step<E, 16><<<grid, 64, 0, s>>>(a);
+}
+
+template <class E, bool OUT>
+void launch_chunk(const LinArgs& a, int units, hipStream_t s) {
+    const dim3 grid(units, a.hv);
+    if (a.Dk <= 64) {
+        if (a.Dv <= 64) k_lin_chunk<E, 64, 1, OUT><<<grid, 256, 0, s>>>(a);
+        else k_lin_chunk<E, 64, 2, OUT><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (a.Dv <= 64) k_lin_chunk<E, 128, 1, OUT><<<grid, 256, 0, s>>>(a);
+        else k_lin_chunk<E, 128, 2, OUT><<<grid, 256, 0, s>>>(a);
+    }
+}
+
+template <class E>
+void launch_linear(const LinArgs& a, const LinGeom& G, hipStream_t s) {
+    if (G.step) return launch_step<E>(a, s);
+    if (G.split) launch_chunk<E, false>(a, G.units, s);
+    launch_chunk<E, true>(a, G.units, s);
+}
+
+}  // namespace
+
+}  // namespace vqmlp
+
+extern "C" vqmlp_status vqmlp_linear_attn_workspace(const vqmlp_linear_desc* p, size_t* bytes) {
+    using namespace vqmlp;
+    OP_REQUIRE(bytes, "vqmlp_linear_attn_workspace: null pointer");
+    int cus = 0;
+    if (const vqmlp_status st = lin_check(p, "vqmlp_linear_attn_workspace")) return st;
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    *bytes = lin_geom(*p, cus).bytes;
+    return op_ok();
+}
+
+extern "C" vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc* p, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    using namespace vqmlp;
+    int cus = 0;
+    if (const vqmlp_status st = lin_check(p, "vqmlp_linear_attn")) return st;
+    const vqmlp_linear_desc& d = *p;
+    OP_REQUIRE(d.cu_q && op_aligned(d.cu_q, 4) && op_aligned(d.ctx_len, 4) && op_aligned(d.state_index, 4),
+               "vqmlp_linear_attn: null cu_q or an unaligned index array");
+    OP_REQUIRE((d.state_in && d.state_out) || d.n_states == 0, "vqmlp_linear_attn: null state");
+    OP_REQUIRE(op_aligned(d.state_in, 16) && op_aligned(d.state_out, 16),
+               "vqmlp_linear_attn: states have to be 16-byte aligned");
+    if (d.T > 0) {
+        OP_REQUIRE(d.q && d.k && d.v && d.g && d.y, "vqmlp_linear_attn: null pointer");
+        OP_REQUIRE(op_aligned(d.q, 16) && op_aligned(d.k, 16) && op_aligned(d.v, 16) && op_aligned(d.y, 16) &&
+                       op_aligned(d.g, 4),
+                   "vqmlp_linear_attn: q, k, v and y have to be 16-byte aligned, g 4-byte");
+        const int64_t rows[] = {int64_t(d.k_heads) * d.Dk, int64_t(d.k_heads) * d.Dk,
+                                int64_t(d.v_heads) * d.Dv, int64_t(d.v_heads) * d.Dv, d.v_heads};
+        const int64_t lds[] = {d.ld_q, d.ld_k, d.ld_v, d.ld_y, d.ld_g};
+        for (int i = 0; i < 5; ++i)
+            OP_REQUIRE((d.T == 1 || lds[i] >= rows[i]) && lds[i] >= 0 && lds[i] <= (int64_t(1) << 40) &&
+                           (i == 4 || lds[i] % 8 == 0),
+                       "vqmlp_linear_attn: token strides have to cover the heads, those of q, k, v and y be "
+                       "multiples of 8");
+    }
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    const LinGeom G = lin_geom(d, cus);
+    if (G.bytes) {
+        OP_REQUIRE(workspace && op_aligned(workspace, 256),
+                   "vqmlp_linear_attn: the workspace is null or not 256-byte aligned");
+        if (workspace_bytes < G.bytes)
+            OP_FAIL(VQMLP_ERR_WORKSPACE, "vqmlp_linear_attn: workspace holds %zu bytes, this call needs %zu",
+                    workspace_bytes, G.bytes);
+    }
+    LinArgs a;
+    a.q = static_cast<const uint16_t*>(d.q);
+    a.k = static_cast<const uint16_t*>(d.k);
+    a.v = static_cast<const uint16_t*>(d.v);
+    a.g = d.g;
+    a.y = static_cast<uint16_t*>(d.y);
+    a.sin = d.state_in;
+    a.sout = d.state_out;
+    a.cu = d.cu_q;
+    a.ctx = d.ctx_len;
+    a.index = d.state_index;
+    a.seg = static_cast<float*>(workspace);
+    a.dec = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + G.dec);
+    a.ld_q = d.ld_q;
+    a.ld_k = d.ld_k;
+    a.ld_v = d.ld_v;
+    a.ld_y = d.ld_y;
+    a.ld_g = d.ld_g;
+    a.T = d.T;
+    a.R = d.R;
+    a.hk = d.k_heads;
+    a.hv = d.v_heads;
+    a.Dk = d.Dk;
+    a.Dv = d.Dv;
+    a.n_states = d.n_states;
+    a.L = G.L;
+    a.scale = d.scale;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (d.dtype == VQMLP_F16) launch_linear<F16>(a, G, s);
+    else launch_linear<BF16>(a, G, s);
+    if (trace_enabled()) {
+        if (G.step)
+            trace_line("linear_attn T=%d R=%d heads=%d/%d: recurrence", d.T, d.R, d.v_heads, d.k_heads);
+        else
+            trace_line("linear_attn T=%d R=%d heads=%d/%d: %schunks, segments of %d tokens", d.T, d.R,
+                       d.v_heads, d.k_heads, G.split ? "segment states, then " : "", G.L);
+    }
+    return op_launched("vqmlp_linear_attn");
+}

@@ -4,6 +4,7 @@
 #include "internal.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -199,6 +200,36 @@ vqmlp_status check_device() {
 }
 
 }  // namespace
+
+bool vqmlp::trace_enabled() { return trace_on(); }
+
+void vqmlp::trace_line(const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    fprintf(stderr, "vqmlp: %s\n", buf);
+}
+
+int vqmlp::device_cus(int* cus) {
+    constexpr int kMax = 64;
+    static std::atomic<int> known[kMax];  // compute units of a gfx950 device, 0 = not looked up
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    int n = dev < kMax ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (!n) {
+        const vqmlp_status st = check_device();
+        if (st) return st;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+            n < 1)
+            n = 256;
+        if (dev < kMax) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *cus = n;
+    return VQMLP_OK;
+}
 
 // ==================================================================== plan
 

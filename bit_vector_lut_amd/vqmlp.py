@@ -31,6 +31,47 @@ class _Desc(C.Structure):
                 ("s_in", C.c_void_p), ("sign_h", C.c_void_p), ("sign_i", C.c_void_p)]
 
 
+class _NormDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("res_dtype", C.c_int), ("kind", C.c_int), ("T", C.c_int),
+                ("H", C.c_int), ("eps", C.c_float), ("res_scale", C.c_float),
+                ("w_offset", C.c_float),
+                ("y", C.c_void_p), ("ld_y", C.c_int64), ("res", C.c_void_p), ("ld_res", C.c_int64),
+                ("gate", C.c_void_p), ("ld_gate", C.c_int64),
+                ("post_w", C.c_void_p), ("post_b", C.c_void_p), ("pre_w", C.c_void_p),
+                ("pre_b", C.c_void_p), ("res_out", C.c_void_p), ("ld_res_out", C.c_int64),
+                ("x", C.c_void_p), ("ld_x", C.c_int64)]
+
+
+class _PagesDesc(C.Structure):
+    _fields_ = [("R", C.c_int), ("max_tokens", C.c_int), ("page_size", C.c_int),
+                ("n_pages", C.c_int), ("n_free", C.c_int), ("table_width", C.c_int),
+                ("ld_table", C.c_int64), ("ctx_len", C.c_void_p), ("q_len", C.c_void_p),
+                ("free_pages", C.c_void_p), ("free_head", C.c_void_p), ("table", C.c_void_p),
+                ("seq_len", C.c_void_p), ("cu_q", C.c_void_p), ("slot", C.c_void_p),
+                ("position", C.c_void_p), ("status", C.c_void_p), ("free_head_out", C.c_void_p)]
+
+
+class _AttnDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("T", C.c_int), ("R", C.c_int), ("heads", C.c_int),
+                ("kv_heads", C.c_int), ("D", C.c_int), ("page_size", C.c_int),
+                ("n_pages", C.c_int), ("window", C.c_int), ("max_kv", C.c_int),
+                ("scale", C.c_float), ("table_width", C.c_int), ("ld_table", C.c_int64),
+                ("ld_q", C.c_int64), ("ld_y", C.c_int64), ("q", C.c_void_p), ("y", C.c_void_p),
+                ("lse", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p),
+                ("table", C.c_void_p), ("cu_q", C.c_void_p), ("kv_len", C.c_void_p)]
+
+
+class _LinearDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("T", C.c_int), ("R", C.c_int), ("k_heads", C.c_int),
+                ("v_heads", C.c_int), ("Dk", C.c_int), ("Dv", C.c_int), ("n_states", C.c_int),
+                ("max_q", C.c_int), ("scale", C.c_float), ("ld_q", C.c_int64),
+                ("ld_k", C.c_int64), ("ld_v", C.c_int64), ("ld_y", C.c_int64),
+                ("ld_g", C.c_int64), ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("g", C.c_void_p), ("y", C.c_void_p), ("state_in", C.c_void_p),
+                ("state_out", C.c_void_p), ("cu_q", C.c_void_p), ("ctx_len", C.c_void_p),
+                ("state_index", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -74,6 +115,13 @@ def lib():
             "vqmlp_vq2_create": [I, I, P, C.POINTER(P)],
             "vqmlp_vq2_destroy": [P],
             "vqmlp_vq2_plan_forward": [P, I, P, P, P],
+            "vqmlp_block_norm": [P, P],
+            "vqmlp_page_plan": [P, P],
+            "vqmlp_paged_store": [I, I, I, I, I, I, P, C.c_int64, P, C.c_int64, P, P, P, P],
+            "vqmlp_paged_attn_workspace": [P, C.POINTER(S)],
+            "vqmlp_paged_attn": [P, P, S, P],
+            "vqmlp_linear_attn_workspace": [P, C.POINTER(S)],
+            "vqmlp_linear_attn": [P, P, S, P],
         }
         for name, args in sigs.items():
             f = getattr(L, name)
@@ -421,3 +469,399 @@ class VQ2Projection:
             _lib.vqmlp_vq2_destroy(self._plan)
             self._plan = None
 
+
+
+# ------------------------------------------------------------------ around the MLP
+# Operators of a serving step over requests packed one after another (include/vqmlp.h, "around the
+# MLP").  Each class keeps what stays from call to call; a call checks its tensors, allocates what
+# the caller did not pass on the call's stream, and enqueues.
+
+
+class _OnStream:
+    """The stream of a call and the context in which its temporaries are allocated: memory comes
+    from that stream's pool, so it cannot be handed to another stream while the call runs."""
+
+    def __init__(self, stream, device):
+        import torch
+
+        if device.type != "cuda":
+            _bad("tensors are on %s, not on a GPU" % device)
+        if stream is None:
+            self.raw, self.ctx = torch.cuda.current_stream(device).cuda_stream, None
+        else:
+            self.raw, self.ctx = stream.cuda_stream, torch.cuda.stream(stream)
+
+    def empty(self, shape, dtype, device):
+        import torch
+
+        if self.ctx is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with self.ctx:
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _bad(msg):
+    raise VqmlpError(ERR_INVALID_ARG, msg)
+
+
+_DTYPES = None
+
+
+def _dtype(t, name):
+    """vqmlp_dtype of a tensor (int16 holds binary16 bits)."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+
+        _DTYPES = {torch.float16: 0, torch.int16: 0, torch.bfloat16: 1, torch.float32: 2}
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        _bad("%s: unsupported type %s" % (name, t.dtype))
+    return d
+
+
+def _need(t, name, device, dtype=None, shape=None, contiguous=True):
+    """A tensor on device, of a torch type and shape (None entries are free)."""
+    if t.device != device:
+        _bad("%s is on %s, not on %s" % (name, t.device, device))
+    if dtype is not None and t.dtype != dtype:
+        _bad("%s is %s, not %s" % (name, t.dtype, dtype))
+    if shape is not None and (t.dim() != len(shape) or any(
+            s is not None and s != n for s, n in zip(shape, t.shape))):
+        _bad("%s has shape %s, wanted %s" % (name, tuple(t.shape), shape))
+    if contiguous and not t.is_contiguous():
+        _bad("%s is not contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, name, device, shape):
+    """Pointer and token stride of [T, heads, D] (or [T, H]) whose rows are dense."""
+    _need(t, name, device, None, shape, contiguous=False)
+    inner = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != inner:
+            _bad("%s: a token's elements do not lie one after another" % name)
+        inner *= n
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
+
+
+def _work_ptr(workspace, nbytes, where, device):
+    import torch
+
+    if workspace is None:
+        return where.empty((nbytes,), torch.uint8, device) if nbytes else None
+    if workspace.device != device or not workspace.is_contiguous():
+        _bad("workspace: not contiguous, or not on %s" % device)
+    return workspace
+
+
+class BlockNorm:
+    """r = residual + residual_scale * gate * N_post(y); x = N_pre(r): the norms, the gate and the
+    residual sum between two blocks in one pass.  Weights [H] of y's type (None: that norm, or its
+    bias, is left out); kind "rms" or "layer"; weight_offset is added to both weights."""
+
+    KINDS = {"rms": 0, "layer": 1}
+
+    def __init__(self, pre_weight=None, pre_bias=None, *, post_weight=None, post_bias=None,
+                 kind="rms", eps=1e-6, residual_scale=1.0, weight_offset=0.0):
+        if kind not in self.KINDS:
+            _bad("unknown norm kind %r" % (kind,))
+        ws = {"pre_w": pre_weight, "pre_b": pre_bias, "post_w": post_weight, "post_b": post_bias}
+        if (pre_bias is not None and pre_weight is None) or (post_bias is not None and post_weight is None):
+            _bad("a bias needs its weight")
+        self._keep = [w for w in ws.values() if w is not None]
+        self.has_pre, self.has_post = pre_weight is not None, post_weight is not None
+        self._desc = dict(kind=self.KINDS[kind], eps=eps, res_scale=residual_scale,
+                          w_offset=weight_offset)
+        for name, w in ws.items():
+            if w is not None:
+                self._desc[name] = _need(w, name, self._keep[0].device, self._keep[0].dtype,
+                                         (self._keep[0].shape[0],))
+
+    def forward(self, y, residual=None, gate=None, residual_out=None, out=None, stream=None):
+        """y [T, H] (None: only the norm of residual), residual [T, H] of y's type or float32, gate
+        [T, H] or [H] -> (r of residual's type, x of y's type; None without pre_weight).
+        residual_out may be residual and out may be y."""
+        import torch
+
+        base = y if y is not None else residual
+        if base is None:
+            _bad("neither y nor residual")
+        dev, shape = base.device, tuple(base.shape)
+        if len(shape) != 2:
+            _bad("y and residual are [T, H]")
+        T, H = shape
+        x_dtype = y.dtype if y is not None else self._keep[0].dtype if self._keep else residual.dtype
+        if self._keep and (self._keep[0].shape[0] != H or self._keep[0].device != dev or
+                           _dtype(self._keep[0], "weight") != _DTYPES.get(x_dtype)):
+            _bad("the weights do not fit y (H, type or device)")
+        if y is None and self.has_post:
+            _bad("post_weight without y")
+        d = _NormDesc(T=T, H=H, **self._desc)
+        on = _OnStream(stream, dev)
+        if y is not None:
+            d.dtype = _dtype(y, "y")
+            d.y, d.ld_y = _rows(y, "y", dev, shape)
+        else:
+            d.dtype = _DTYPES[x_dtype] if self._keep else _dtype(residual, "residual")
+        if residual is not None:
+            d.res_dtype = _dtype(residual, "residual")
+            d.res, d.ld_res = _rows(residual, "residual", dev, shape)
+        elif residual_out is not None:
+            d.res_dtype = _dtype(residual_out, "residual_out")
+        else:
+            d.res_dtype = d.dtype
+        if gate is not None:
+            if _dtype(gate, "gate") != d.dtype:
+                _bad("gate and y differ in type")
+            if gate.dim() == 1:
+                d.gate, d.ld_gate = _need(gate, "gate", dev, None, (H,)), 0
+            else:
+                d.gate, d.ld_gate = _rows(gate, "gate", dev, shape)
+        if residual_out is None:
+            residual_out = on.empty(shape, residual.dtype if residual is not None else x_dtype, dev)
+        elif _dtype(residual_out, "residual_out") != d.res_dtype:
+            _bad("residual_out and residual differ in type")
+        d.res_out, d.ld_res_out = _rows(residual_out, "residual_out", dev, shape)
+        if self.has_pre:
+            if out is None:
+                out = on.empty(shape, x_dtype, dev)
+            elif _dtype(out, "out") != d.dtype:
+                _bad("out and y differ in type")
+            d.x, d.ld_x = _rows(out, "out", dev, shape)
+        elif out is not None:
+            _bad("out without pre_weight")
+        with torch.cuda.device(dev):
+            _check(lib().vqmlp_block_norm(C.byref(d), on.raw))
+        return residual_out, out
+
+
+class PagePlan:
+    """One step's plan on the device (all int32): seq_len [R], cu_q [R + 1], slot and position
+    [max_tokens] (-1 behind the last token), status [4] = error bits, tokens, pages taken, 0."""
+
+    __slots__ = ("seq_len", "cu_q", "slot", "position", "status")
+
+    def __init__(self, *parts):
+        self.seq_len, self.cu_q, self.slot, self.position, self.status = parts
+
+
+class PagePlanner:
+    """Block tables and slot maps from request lengths, made on the device.  table [R, width] int32
+    is kept up to date in place; free_pages [n] int32 is the free list, taken from free_head (int32
+    [1] on the device, None: 0) on.  See include/vqmlp.h for the error bits."""
+
+    def __init__(self, table, free_pages, page_size, n_pages, max_tokens, free_head=None):
+        import torch
+
+        dev = table.device
+        _need(table, "table", dev, torch.int32, (None, None), contiguous=False)
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            _bad("table: a row's entries do not lie one after another")
+        self.R, self.device, self.max_tokens = table.shape[0], dev, max_tokens
+        self.table, self.free_pages, self.free_head = table, free_pages, free_head
+        self.page_size, self.n_pages = page_size, n_pages
+        self._desc = dict(R=self.R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
+                          n_free=free_pages.numel(), table_width=table.shape[1],
+                          ld_table=table.stride(0) if self.R > 1 else table.shape[1],
+                          free_pages=_need(free_pages, "free_pages", dev, torch.int32, (None,)),
+                          table=table.data_ptr())
+        if free_head is not None:
+            self._desc["free_head"] = _need(free_head, "free_head", dev, torch.int32, (1,))
+
+    def empty_plan(self, stream=None):
+        import torch
+
+        on, i = _OnStream(stream, self.device), torch.int32
+        return PagePlan(*(on.empty((n,), i, self.device) for n in (
+            self.R, self.R + 1, self.max_tokens, self.max_tokens, 4)))
+
+    def forward(self, ctx_len, q_len, plan=None, free_head_out=None, stream=None):
+        """ctx_len, q_len [R] int32 on the device -> PagePlan (plan: buffers to reuse)."""
+        import torch
+
+        i, dev = torch.int32, self.device
+        d = _PagesDesc(**self._desc)
+        d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (self.R,))
+        d.q_len = _need(q_len, "q_len", dev, i, (self.R,))
+        if plan is None:
+            plan = self.empty_plan(stream)
+        d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self.R,))
+        d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self.R + 1,))
+        d.slot = _need(plan.slot, "slot", dev, i, (self.max_tokens,))
+        d.position = _need(plan.position, "position", dev, i, (self.max_tokens,))
+        d.status = _need(plan.status, "status", dev, i, (4,))
+        if free_head_out is not None:
+            d.free_head_out = _need(free_head_out, "free_head_out", dev, i, (1,))
+        with torch.cuda.device(dev):
+            _check(lib().vqmlp_page_plan(C.byref(d), _OnStream(stream, dev).raw))
+        return plan
+
+
+class PagedCache:
+    """A paged key/value cache: k [pages, kv_heads, page_size, D], v [pages, kv_heads, D, page_size]
+    (float16, int16 as binary16 bits, or bfloat16)."""
+
+    def __init__(self, k, v):
+        _need(k, "k", k.device, None, (None,) * 4)
+        n, h, p, D = k.shape
+        _need(v, "v", k.device, k.dtype, (n, h, D, p))
+        self.k, self.v, self.device = k, v, k.device
+        self.n_pages, self.kv_heads, self.page_size, self.D = n, h, p, D
+        self.dtype = _dtype(k, "k")
+
+    @classmethod
+    def empty(cls, n_pages, kv_heads, page_size, D, dtype, device="cuda"):
+        import torch
+
+        return cls(torch.empty((n_pages, kv_heads, page_size, D), dtype=dtype, device=device),
+                   torch.empty((n_pages, kv_heads, D, page_size), dtype=dtype, device=device))
+
+    def store(self, k, v, slot, stream=None):
+        """k, v [T, kv_heads, D] into slot[t] (int32 [T]; a slot outside the cache is skipped)."""
+        import torch
+
+        T, dev = k.shape[0], self.device
+        shape = (T, self.kv_heads, self.D)
+        if _dtype(k, "k") != self.dtype or _dtype(v, "v") != self.dtype:
+            _bad("k, v and the cache differ in type")
+        kp, ld_k = _rows(k, "k", dev, shape)
+        vp, ld_v = _rows(v, "v", dev, shape)
+        sp = _need(slot, "slot", dev, torch.int32, (None,))
+        if slot.shape[0] < T:
+            _bad("slot has %d entries for %d tokens" % (slot.shape[0], T))
+        with torch.cuda.device(dev):
+            _check(lib().vqmlp_paged_store(self.dtype, T, self.kv_heads, self.D, self.page_size,
+                                           self.n_pages, kp, ld_k, vp, ld_v, sp,
+                                           self.k.data_ptr(), self.v.data_ptr(),
+                                           _OnStream(stream, dev).raw))
+
+    def _attn_desc(self, T, R, heads, table_width, window, max_kv, scale):
+        return _AttnDesc(dtype=self.dtype, T=T, R=R, heads=heads, kv_heads=self.kv_heads, D=self.D,
+                         page_size=self.page_size, n_pages=self.n_pages, window=window,
+                         max_kv=table_width * self.page_size if max_kv is None else max_kv,
+                         scale=self.D ** -0.5 if scale is None else scale, table_width=table_width)
+
+    def workspace_bytes(self, T, R, heads, table_width, max_kv=None):
+        n = C.c_size_t()
+        d = self._attn_desc(T, R, heads, table_width, 0, max_kv, None)
+        _check(lib().vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
+        return n.value
+
+    def attention(self, q, table, cu_q, kv_len, *, scale=None, window=0, max_kv=None, y=None,
+                  lse=None, with_lse=False, workspace=None, stream=None):
+        """q [T, heads, D] against the cached positions of each request: table [R, width], cu_q
+        [R + 1], kv_len [R] int32 on the device (kv_len counts the new tokens, stored before).
+        scale: 1 / sqrt(D) if None.  max_kv: the longest kv_len expected (None: what the table
+        holds).  Returns y, or (y, lse float32 [T, heads]) with with_lse or lse."""
+        import torch
+
+        dev, i = self.device, torch.int32
+        if q.dim() != 3:
+            _bad("q is [T, heads, D]")
+        if _dtype(q, "q") != self.dtype:
+            _bad("q and the cache differ in type")
+        T, heads, R = q.shape[0], q.shape[1], kv_len.shape[0]
+        _need(table, "table", dev, i, (R, None), contiguous=False)
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            _bad("table: a row's entries do not lie one after another")
+        on = _OnStream(stream, dev)
+        d = self._attn_desc(T, R, heads, table.shape[1], window, max_kv, scale)
+        d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self.D))
+        if y is None:
+            y = on.empty((T, heads, self.D), q.dtype, dev)
+        elif _dtype(y, "y") != self.dtype:
+            _bad("y and the cache differ in type")
+        d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self.D))
+        if lse is None and with_lse:
+            lse = on.empty((T, heads), torch.float32, dev)
+        if lse is not None:
+            d.lse = _need(lse, "lse", dev, torch.float32, (T, heads))
+        d.k_cache, d.v_cache = self.k.data_ptr(), self.v.data_ptr()
+        d.table, d.ld_table = table.data_ptr(), table.stride(0) if R > 1 else table.shape[1]
+        d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
+        d.kv_len = _need(kv_len, "kv_len", dev, i, (R,))
+        L = lib()
+        with torch.cuda.device(dev):
+            n = C.c_size_t()
+            _check(L.vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
+            work = _work_ptr(workspace, n.value, on, dev)
+            _check(L.vqmlp_paged_attn(C.byref(d), None if work is None else work.data_ptr(),
+                                      0 if work is None else work.numel() * work.element_size(), on.raw))
+        return y if lse is None else (y, lse)
+
+
+class LinearAttention:
+    """S_t = exp(g_t) S_{t-1} + k_t v_t^T, y_t = scale * S_t^T q_t per value head (which shares key
+    head h // (v_heads // k_heads)).  scale: 1 / sqrt(Dk) if None."""
+
+    def __init__(self, k_heads, v_heads, Dk, Dv, scale=None):
+        self.k_heads, self.v_heads, self.Dk, self.Dv = k_heads, v_heads, Dk, Dv
+        self.scale = Dk ** -0.5 if scale is None else scale
+
+    def state(self, n, device="cuda"):
+        """Zero states for n requests."""
+        import torch
+
+        return torch.zeros((n, self.v_heads, self.Dk, self.Dv), dtype=torch.float32, device=device)
+
+    def workspace_bytes(self, T, R, max_q):
+        n = C.c_size_t()
+        d = _LinearDesc(dtype=0, T=T, R=R, k_heads=self.k_heads, v_heads=self.v_heads, Dk=self.Dk,
+                        Dv=self.Dv, max_q=max_q, scale=self.scale)
+        _check(lib().vqmlp_linear_attn_workspace(C.byref(d), C.byref(n)))
+        return n.value
+
+    def forward(self, q, k, v, g, state, cu_q, *, ctx_len=None, state_index=None, state_out=None,
+                max_q=None, y=None, workspace=None, stream=None):
+        """q, k [T, k_heads, Dk], v [T, v_heads, Dv], g float32 [T, v_heads], state float32 [slots,
+        v_heads, Dk, Dv], cu_q int32 [R + 1]; ctx_len int32 [R]: a request with 0 starts from zero;
+        state_index int32 [R]: its slot (None: r).  max_q: the most new tokens of one request that
+        are expected (None: T).  state_out may be state; slots that no request uses are left as
+        they are (a new state_out starts as a copy of state where there are such slots).  Returns
+        (y [T, v_heads, Dv], state_out)."""
+        import torch
+
+        dev, i, f = q.device, torch.int32, torch.float32
+        T, R = q.shape[0], cu_q.shape[0] - 1
+        dt = _dtype(q, "q")
+        if _dtype(k, "k") != dt or _dtype(v, "v") != dt:
+            _bad("q, k and v differ in type")
+        on = _OnStream(stream, dev)
+        d = _LinearDesc(dtype=dt, T=T, R=R, k_heads=self.k_heads, v_heads=self.v_heads, Dk=self.Dk,
+                        Dv=self.Dv, n_states=state.shape[0], max_q=T if max_q is None else max_q,
+                        scale=self.scale)
+        d.q, d.ld_q = _rows(q, "q", dev, (T, self.k_heads, self.Dk))
+        d.k, d.ld_k = _rows(k, "k", dev, (T, self.k_heads, self.Dk))
+        d.v, d.ld_v = _rows(v, "v", dev, (T, self.v_heads, self.Dv))
+        _need(g, "g", dev, f, (T, self.v_heads), contiguous=False)
+        d.g, d.ld_g = _rows(g, "g", dev, (T, self.v_heads))
+        if y is None:
+            y = on.empty((T, self.v_heads, self.Dv), q.dtype, dev)
+        elif _dtype(y, "y") != dt:
+            _bad("y and q differ in type")
+        d.y, d.ld_y = _rows(y, "y", dev, (T, self.v_heads, self.Dv))
+        shape = (state.shape[0], self.v_heads, self.Dk, self.Dv)
+        d.state_in = _need(state, "state", dev, f, shape)
+        if state_out is None:
+            state_out = on.empty(shape, f, dev)
+            if state_index is not None or shape[0] > R:
+                if on.ctx is None:
+                    state_out.copy_(state)
+                else:
+                    with on.ctx:
+                        state_out.copy_(state)
+        d.state_out = _need(state_out, "state_out", dev, f, shape)
+        d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
+        if ctx_len is not None:
+            d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (R,))
+        if state_index is not None:
+            d.state_index = _need(state_index, "state_index", dev, i, (R,))
+        L = lib()
+        with torch.cuda.device(dev):
+            n = C.c_size_t()
+            _check(L.vqmlp_linear_attn_workspace(C.byref(d), C.byref(n)))
+            work = _work_ptr(workspace, n.value, on, dev)
+            _check(L.vqmlp_linear_attn(C.byref(d), None if work is None else work.data_ptr(),
+                                       0 if work is None else work.numel() * work.element_size(), on.raw))
+        return y, state_out

@@ -286,6 +286,143 @@ vqmlp_status vqmlp_vq2_destroy(vqmlp_vq2_plan *plan);
 vqmlp_status vqmlp_vq2_plan_forward(const vqmlp_vq2_plan *plan, int T, const void *x, void *y,
                                     void *stream);
 
+/* ==================================================================== around the MLP
+ * The rest of a decoder layer, forward only, for a step over R requests whose new tokens are
+ * packed one after another: request r owns rows cu_q[r] .. cu_q[r+1]-1 of every [T] array.
+ * The mathematics stands in each section; sums, norms, softmax statistics and states are FP32,
+ * and each output is rounded once.  These calls take no plan: they check their arguments, enqueue
+ * on `stream` and allocate nothing; lengths, tables and indices are read on the device, so a call
+ * can be captured into a graph and replayed with other lengths.  Arguments that the host can see
+ * are refused with VQMLP_ERR_INVALID_ARG (shape, pointer, alignment), VQMLP_ERR_UNSUPPORTED
+ * (a size beyond the stated limits, or not a gfx950) or VQMLP_ERR_WORKSPACE; values read on the
+ * device are bounds-checked there as each section states. */
+typedef enum { VQMLP_F16 = 0, VQMLP_BF16 = 1, VQMLP_F32 = 2 } vqmlp_dtype;
+
+/* ------------------------------------------------------------------ norms around a block
+ * One pass between the block before (its output y) and the block after (its input x):
+ *   u = N(y; post_w, post_b)  (post_w NULL: u = y),   u = u * gate  (gate NULL: no gate)
+ *   r = res + res_scale * u   (res NULL: r = res_scale * u; y NULL: r = res)
+ *   x = N(r; pre_w, pre_b)    (x NULL: not computed)
+ *   VQMLP_NORM_RMS:   N(z; w, b) = z / sqrt(mean(z^2) + eps) * (w + w_offset) + b
+ *   VQMLP_NORM_LAYER: the same of z - mean(z).
+ * r reaches the second norm unrounded.  y, gate, weights and x have type dtype (F16 or BF16); res
+ * and res_out have res_dtype (dtype or F32).  Rows are ld_* elements apart; ld_gate 0 shares one
+ * gate row.  Any H in [1, 2^20]; every pointer 16-byte aligned and ld and H multiples of 8 take
+ * the vector kernel up to H = 16384, others an element-wise one (pointers aligned to their
+ * element).  res_out may be res and x may be y (the same pointer and row stride); no other
+ * overlap.  T == 0 is a no-op. */
+typedef enum { VQMLP_NORM_RMS = 0, VQMLP_NORM_LAYER = 1 } vqmlp_norm_kind;
+typedef struct {
+    int dtype, res_dtype, kind;
+    int T, H;
+    float eps, res_scale, w_offset;
+    const void *y;      int64_t ld_y;
+    const void *res;    int64_t ld_res;
+    const void *gate;   int64_t ld_gate;
+    const void *post_w, *post_b;    /* [H]; post_b, pre_b may be NULL */
+    const void *pre_w, *pre_b;
+    void *res_out;      int64_t ld_res_out;   /* NULL: r is not stored */
+    void *x;            int64_t ld_x;
+} vqmlp_norm_desc;
+vqmlp_status vqmlp_block_norm(const vqmlp_norm_desc *desc, void *stream);
+
+/* ------------------------------------------------------------------ block tables and slot maps
+ * A paged cache holds n_pages pages of page_size positions (a power of two, 8..1024).  Position p
+ * of request r stands in page table[r][p / page_size] at offset p % page_size; its slot is
+ * page * page_size + offset.  From the cached length ctx_len[r] and the new tokens q_len[r]
+ * (DEVICE int32 [R], R <= 4096) one launch makes
+ *   seq_len[r] = ctx_len[r] + q_len[r];  cu_q[r] = q_len[0] + .. + q_len[r-1] (R + 1 entries);
+ *   table[r][..]: pages ceil(ctx/page_size) .. ceil(seq/page_size)-1 are taken from the free list
+ *     in order of request and position, free_pages[head], free_pages[head+1], ..  (head =
+ *     *free_head, or 0 when free_head is NULL); the entries before them are left as they are;
+ *   slot[t], position[t] for each new token t, -1 for t in [cu_q[R], max_tokens);
+ *   status[0] error bits, [1] tokens, [2] pages taken, [3] 0; *free_head_out = head + taken
+ *     (NULL: not stored; not the same word as free_head).
+ * All or nothing: an error (1 = a negative length or one beyond table_width * page_size, 2 = too
+ * few free pages or a head outside [0, n_free], 4 = more than max_tokens tokens) leaves table as
+ * it is, makes cu_q all 0, every slot and position -1, seq_len = ctx_len, and the head stays;
+ * status then holds what was wanted (up to 2^31 - 1).  A page number outside [0, n_pages) makes
+ * its tokens' slots -1.  The free list itself is not changed. */
+typedef struct {
+    int R, max_tokens, page_size, n_pages, n_free;
+    int table_width;                /* entries per row in use; rows are ld_table apart */
+    int64_t ld_table;
+    const int32_t *ctx_len, *q_len;
+    const int32_t *free_pages, *free_head;
+    int32_t *table;
+    int32_t *seq_len, *cu_q, *slot, *position, *status, *free_head_out;
+} vqmlp_pages_desc;
+vqmlp_status vqmlp_page_plan(const vqmlp_pages_desc *desc, void *stream);
+
+/* ------------------------------------------------------------------ the paged cache
+ * k_cache [n_pages][kv_heads][page_size][D] and v_cache [n_pages][kv_heads][D][page_size], 16-byte
+ * aligned, F16 or BF16, D a multiple of 8 up to 256 (values lie transposed: the matrix-core
+ * operand of the value product then is eight neighbouring positions, one 16-byte load).
+ * vqmlp_paged_store: k, v [T][kv_heads][D] with token strides ld_k, ld_v (elements, multiples of
+ * 8; 16-byte aligned) go to slot[t]; a slot outside [0, n_pages * page_size) is skipped, and two
+ * tokens may not share a slot. */
+vqmlp_status vqmlp_paged_store(int dtype, int T, int kv_heads, int D, int page_size, int n_pages,
+                               const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                               const int32_t *slot, void *k_cache, void *v_cache, void *stream);
+
+/* Attention of the new tokens over the cache.  Row i of request r (n = cu_q[r+1] - cu_q[r] rows)
+ * stands at position p = kv_len[r] - n + i and sees positions max(0, p - window + 1) .. p (window
+ * 0: from 0); query head h reads key head h / (heads / kv_heads):
+ *   y[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,   lse[t][h] = log sum_j exp(..)
+ * kv_len counts the new tokens, whose keys and values are in the cache already.  A row that sees
+ * nothing (p < 0, or every page of it outside the cache) gives y = 0, lse = -inf.  Positions
+ * beyond table_width * page_size and pages outside [0, n_pages) are not seen; cu_q is clamped to
+ * [0, T]; rows from cu_q[R] on give y = 0, lse = -inf.  Cached values a row does not see may be
+ * anything where no row of its request sees them; elsewhere they have to be finite.
+ * q, y [T][heads][D] with token strides ld_q, ld_y (elements, multiples of 8; 16-byte aligned);
+ * lse FP32 [T][heads] or NULL.  heads / kv_heads up to 64, R <= 65536.  max_kv: the longest kv_len
+ * that is expected; it chooses the split of the keys, and any value gives a right answer.  The
+ * workspace (256-byte aligned, no zero fill) follows vqmlp_paged_attn_workspace of the same
+ * description on the same device; two calls that overlap in time need one each. */
+typedef struct {
+    int dtype, T, R, heads, kv_heads, D, page_size, n_pages, window, max_kv;
+    float scale;
+    int table_width;
+    int64_t ld_table, ld_q, ld_y;
+    const void *q;
+    void *y;
+    float *lse;
+    const void *k_cache, *v_cache;
+    const int32_t *table, *cu_q, *kv_len;
+} vqmlp_attn_desc;
+vqmlp_status vqmlp_paged_attn_workspace(const vqmlp_attn_desc *desc, size_t *bytes);
+vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* ------------------------------------------------------------------ linear attention with decay
+ * Per request and value head h (key head h / (v_heads / k_heads)), from the state S [Dk][Dv]:
+ *   S_t = exp(g[t][h]) S_{t-1} + k_t v_t^T,   y_t = scale * S_t^T q_t.
+ * q, k [T][k_heads][Dk], v, y [T][v_heads][Dv] (F16 or BF16, token strides ld_*: multiples of 8,
+ * 16-byte aligned), g FP32 [T][v_heads] (token stride ld_g), the log of the decay: at most 0, -inf
+ * forgets everything before (below -80 it is taken as -80, a factor of 2e-35).  Dk and Dv are
+ * multiples of 8 up to 128.  state_in, state_out FP32 [slots][v_heads][Dk][Dv], 16-byte aligned;
+ * they may be the same array.  Request r uses slot state_index[r] (NULL: r); a slot outside
+ * [0, n_states) starts from zero and its final state is dropped; no two requests share a slot.
+ * ctx_len (DEVICE int32 [R] or NULL): a request with ctx_len[r] <= 0 starts from zero, whatever
+ * its slot holds.  A request without new tokens copies its start state.  cu_q is clamped to
+ * [0, T]; rows from cu_q[R] on give y = 0.  max_q: the most new tokens of one request that are
+ * expected; it chooses the kernel (up to 16: the recurrence token by token; above: chunks of 64
+ * tokens on the matrix cores), and any value gives a right answer.  R <= 65536. */
+typedef struct {
+    int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
+    float scale;
+    int64_t ld_q, ld_k, ld_v, ld_y, ld_g;
+    const void *q, *k, *v;
+    const float *g;
+    void *y;
+    const float *state_in;
+    float *state_out;
+    const int32_t *cu_q, *ctx_len, *state_index;
+} vqmlp_linear_desc;
+vqmlp_status vqmlp_linear_attn_workspace(const vqmlp_linear_desc *desc, size_t *bytes);
+vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
