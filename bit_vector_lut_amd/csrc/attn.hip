@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
         const int i = rho / a.g, hh = rho - i * a.g;
         const bool real = i < t.n;
         const int p = t.kv - t.n + i;
-        hi[b] = real && t.r < a.R ? p : -1;
+        hi[b] = real && t.r < a.R ? min(p, (a.width << a.shift) - 1) : -1;
         lo[b] = a.window ? max(0, p - a.window + 1) : 0;
         const uint16_t* src = a.q + (t.c0 + i) * a.ld_q + int64_t(hk * a.g + hh) * a.D + 8 * g;
 #pragma unroll
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
             }
             const int head = hk * a.g + hh;
             const int64_t rowi = int64_t(t.c0 + i) * a.heads + head;
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
             for (int d = jt * 4; d < DC && d0 + d < D; d += TPR * 4) {
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
                     a.ml[(rowi * a.nsplit + split) * 2] = mm;
                     a.ml[(rowi * a.nsplit + split) * 2 + 1] = sum;
                 } else if (a.lse) {
-                    a.lse[rowi] = sum > 0.f ? fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f)
-                                            : kNegInf;
+                    a.lse[rowi] = sum == 0.f ? kNegInf
+                                             : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
                 }
             }
         }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
     const float c = a.scale * 1.4426950408889634f;
     const float w = __builtin_amdgcn_exp2f((m - (mm == kNegInf ? 0.f : mm)) * c);
     const float sum = wave_sum(w * l);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     const float* src = a.opart + row * a.nsplit * a.D + 4 * lane;
     const bool in = 4 * lane < a.D;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
         // every lane takes part in the exchange: lanes behind D hold weights too
         const float ws = __shfl(w, s);
         const float ls = __shfl(l, s);
-        if (!(ls > 0.f) || !in) continue;  // a split without keys wrote no sums
+        if (ls == 0.f || !in) continue;  // a split without keys
         const f32x4 x = *reinterpret_cast<const f32x4*>(src + int64_t(s) * a.D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf(ws, x[j], v[j]);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
         *reinterpret_cast<u32x2*>(a.y + tok * a.ld_y + int64_t(head) * a.D + 4 * lane) = w2;
     }
     if (lane == 0 && a.lse)
-        a.lse[row] = sum > 0.f ? fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f) : kNegInf;
+        a.lse[row] = sum == 0.f ? kNegInf : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
 }
 
 // ---------------------------------------------------------------- host half
@@ -351,7 +351,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t rows = std::max<int64_t>(1, (int64_t(d.T) * g + d.R - 1) / std::max(1, d.R));
     const int most = d.D > 128 ? 2 : 4;
     G.nb = int(std::min<int64_t>(most, (rows + 15) / 16));
-    if (G.nb == 3 && most == 4) G.nb = 4;
+    if (G.nb == 3) G.nb = 4;
     const int mt = 16 * G.nb;
     G.tiles = int(int64_t(d.T) * g / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (int64_t(d.T) * g + mt - 1) / mt) * d.kv_heads;
@@ -417,8 +417,7 @@ void launch_attn(const AttnArgs& a, const AttnGeom& G, hipStream_t s) {
         else launch_wave_nb<E, 128, 4>(a, G.tiles, s);
     } else {
         if (G.nb == 1) launch_wave_nb<E, 256, 1>(a, G.tiles, s);
-        else if (G.nb == 2) launch_wave_nb<E, 256, 2>(a, G.tiles, s);
-        else launch_wave_nb<E, 256, 3>(a, G.tiles, s);
+        else launch_wave_nb<E, 256, 2>(a, G.tiles, s);
     }
     if (a.nsplit > 1) {
         const int64_t rows = int64_t(a.T) * a.heads;

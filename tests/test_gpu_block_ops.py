@@ -482,6 +482,23 @@ def test_paged_attention_many_far_keys_count(vq, torch_dev):
     assert abs(float(y[0, 0, 0]) - ref) <= 3 * 2.0 ** -11, (float(y[0, 0, 0]), ref)
 
 
+@pytest.mark.parametrize("lens", [[(3, 40)], [(2, 3000)], [(200, 700)]])
+def test_paged_attention_nan_queries_give_nan(vq, torch_dev, lens):
+    """A NaN query makes its own outputs NaN, with and without a split of the keys; others keep theirs."""
+    torch = torch_dev
+    q, k, v, table, cu = _attn_case(torch, torch.bfloat16, lens, 4, 2, 64, 16, 6)
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = vq.PagedCache(k.cuda(), v.cuda())
+    args = (table.cuda(), i(cu), i([kv for _, kv in lens]))
+    y, lse = cache.attention(q.cuda(), *args, with_lse=True)
+    q[1, 2, 5] = float("nan")
+    y2, lse2 = cache.attention(q.cuda(), *args, with_lse=True)
+    assert y2[1, 2].isnan().all() and lse2[1, 2].isnan()
+    keep = torch.ones(y.shape[:2], dtype=torch.bool, device="cuda")
+    keep[1, 2] = False
+    assert torch.equal(y2[keep], y[keep]) and torch.equal(lse2[keep], lse[keep])
+
+
 def test_paged_attention_strides_streams_and_graphs(vq, torch_dev):
     torch = torch_dev
     dt = torch.bfloat16
