@@ -14,77 +14,13 @@
 // keys 8(m/4) + m%4 and the same + 4: a lane then holds keys 8g .. 8g+7 (g = lane / 16), packs
 // them to 16 bits in place, and the matching operand of V^T is one 16-byte load because the cache
 // keeps values as [D][page_size].  Neither product goes through LDS.
-#include "op.h"
+#include "attn.h"
 
 #include <algorithm>
 
 namespace vqmlp {
 
 namespace {
-
-constexpr float kNegInf = -__builtin_inff();
-constexpr int kMaxSplit = 64;
-
-struct AttnArgs {
-    const uint16_t* q;
-    uint16_t* y;
-    float* lse;
-    const uint16_t *kc, *vc;
-    const int32_t *table, *cu, *kv_len;
-    float* opart;  // [row][split][D], row = token * heads + head (split launches only)
-    float* ml;     // [row][split][2]: maximum of the scores, sum
-    int64_t ld_table, ld_q, ld_y;
-    int T, R, heads, kv_heads, g, D, shift, n_pages, window, nsplit, split_tiles;
-    int width;     // pages per table row
-    float scale;
-};
-
-// exp2 of a difference to the maximum: fp16 probabilities carry a factor 2^12, so that keys down to
-// 2^-36 of the largest still count (binary16 ends at 2^-24; 2^12 times any sum of them stays far
-// inside fp32).  bfloat16 has the range by itself.
-template <class E>
-constexpr float kBias = __is_same(E, F16) ? 12.f : 0.f;
-
-struct Tile {       // what one workgroup works on
-    int r, n;       // request (R: the rows behind the last request), its new tokens
-    int c0;         // its first row
-    int rho0;       // first packed row of the tile
-    int kv;         // keys of the request
-    int kmin, kmax; // keys seen by any row of the tile
-    int full_lo, full_hi;  // keys seen by every row of the tile
-};
-
-// Row tiles of all requests in one launch without their lengths on the host: request r owns tile
-// numbers floor(cu[r] g / MT) + r and on, which is always enough for ceil(n g / MT) tiles, and
-// the numbers left over return.  Every wave looks the request up for itself, 64 at a time.
-template <int MT>
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, Tile& t) {
-    const int lane = threadIdx.x & 63;
-    auto row = [&](int r) { return min(max(a.cu[r], 0), a.T); };
-    auto start = [&](int c, int r) { return int(int64_t(c) * a.g / MT) + r; };
-    int count = 0;
-    for (int r0 = 0; r0 <= a.R; r0 += 64) {
-        const int r = r0 + lane;
-        const bool le = r <= a.R && start(row(r), r) <= x;
-        count += __popcll(__ballot(le));
-    }
-    t.r = max(0, count - 1);
-    t.c0 = row(t.r);
-    const int c1 = t.r < a.R ? row(t.r + 1) : a.T;
-    t.n = c1 - t.c0;
-    t.rho0 = (x - start(t.c0, t.r)) * MT;
-    if (t.rho0 < 0 || int64_t(t.rho0) >= int64_t(t.n) * a.g) return false;
-    t.kv = t.r < a.R ? max(a.kv_len[t.r], 0) : 0;
-    const int i0 = t.rho0 / a.g;
-    const int i1 = int(min(int64_t(t.rho0) + MT - 1, int64_t(t.n) * a.g - 1) / a.g);
-    const int p0 = t.kv - t.n + i0, p1 = t.kv - t.n + i1;
-    const int cap = a.width << a.shift;
-    t.kmax = t.r < a.R ? min(p1, cap - 1) : -1;
-    t.kmin = a.window ? max(0, p0 - a.window + 1) : 0;
-    t.full_hi = min(p0, cap - 1);
-    t.full_lo = a.window ? max(0, p1 - a.window + 1) : 0;
-    return true;
-}
 
 // ---------------------------------------------------------------- few rows: keys over the waves
 // NW waves share 16 NB rows of one key head and a split of the keys, tile by tile in turn, each
@@ -341,27 +277,52 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 // ---------------------------------------------------------------- host half
 
 struct AttnGeom {
-    int nb, tiles, nsplit, split_tiles;
+    int nb;         // register tiles: blocks of 16 rows
+    int rb;         // LDS tiles: blocks of 32 rows per wave, 0 = register tiles
+    int tiles, nsplit, split_tiles;
     size_t opart, ml, bytes;
 };
 
 AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
-    AttnGeom G;
+    AttnGeom G{};
     const int g = d.heads / d.kv_heads;
-    const int64_t rows = std::max<int64_t>(1, (int64_t(d.T) * g + d.R - 1) / std::max(1, d.R));
-    const int most = d.D > 128 ? 2 : 4;
-    G.nb = int(std::min<int64_t>(most, (rows + 15) / 16));
-    if (G.nb == 3) G.nb = 4;
-    const int mt = 16 * G.nb;
-    G.tiles = int(int64_t(d.T) * g / mt) + d.R + 1;
-    const int64_t active = std::max<int64_t>(d.R, (int64_t(d.T) * g + mt - 1) / mt) * d.kv_heads;
-    const int keys = std::max(1, d.max_kv);
-    const int key_tiles = (keys + 31) / 32;
-    const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
-    const int most_split = std::max(1, key_tiles / 8);
-    G.nsplit = int(std::min<int64_t>(std::min<int64_t>(want, most_split), kMaxSplit));
-    G.split_tiles = (key_tiles + G.nsplit - 1) / G.nsplit;
+    const int64_t all = int64_t(d.T) * g;
+    const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
+    const int keys = std::max(1, d.max_kv);
+    if (rows > 64) G.rb = 1;
+    if (G.rb && (all / (128 * G.rb) + d.R + 1) * d.kv_heads * kMaxSplit >= (1 << 24)) G.rb = 0;
+    int mt, key_tiles;
+    if (G.rb) {
+        mt = 128 * G.rb;
+        key_tiles = (keys + 63) / 64;
+    } else {
+        const int most = d.D > 128 ? 2 : 4;
+        G.nb = int(std::min<int64_t>(most, (rows + 15) / 16));
+        if (G.nb == 3) G.nb = 4;
+        mt = 16 * G.nb;
+        key_tiles = (keys + 31) / 32;
+    }
+    G.tiles = int(all / mt) + d.R + 1;
+    const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
+    if (G.rb) {
+        // The time in passes over a 64-key tile (about 2.4 us for 256 rows of D = 128): rounds of
+        // workgroups over the compute units, two tiles' worth to start and end each, and what the
+        // join moves.
+        G.nsplit = 1;
+        double best = 1e300;
+        for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
+            const double rounds = double((active * ns + cus - 1) / cus);
+            const double join = ns > 1 ? 2 + ns * double(rows_all) * d.D * 8 / 4e12 / 2.4e-6 : 0;
+            const double cost = rounds * ((key_tiles + ns - 1) / ns + 2) + join;
+            if (cost < best) best = cost, G.nsplit = ns;
+        }
+    } else {
+        const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
+        const int most_split = std::max(1, key_tiles / 8);
+        G.nsplit = int(std::min<int64_t>(std::min<int64_t>(want, most_split), kMaxSplit));
+    }
+    G.split_tiles = (key_tiles + G.nsplit - 1) / G.nsplit;
     G.opart = 0;
     G.ml = align256(G.nsplit > 1 ? rows_all * G.nsplit * d.D * 4 : 0);
     G.bytes = G.ml + align256(G.nsplit > 1 ? rows_all * G.nsplit * 8 : 0);
@@ -406,8 +367,10 @@ void launch_wave_nb(const AttnArgs& a, int tiles, hipStream_t s) {
 }
 
 template <class E>
-void launch_attn(const AttnArgs& a, const AttnGeom& G, hipStream_t s) {
-    if (a.D <= 64) {
+void launch_attn(const AttnArgs& a, const AttnGeom& G, int dtype, hipStream_t s) {
+    if (G.rb) {
+        launch_attn_tile(a, dtype, G.rb, G.tiles, s);
+    } else if (a.D <= 64) {
         if (G.nb == 1) launch_wave_nb<E, 64, 1>(a, G.tiles, s);
         else if (G.nb == 2) launch_wave_nb<E, 64, 2>(a, G.tiles, s);
         else launch_wave_nb<E, 64, 4>(a, G.tiles, s);
@@ -495,10 +458,11 @@ extern "C" vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc* p, void* workspa
     a.width = d.table_width;
     a.scale = d.scale;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (d.dtype == VQMLP_F16) launch_attn<F16>(a, G, s);
-    else launch_attn<BF16>(a, G, s);
+    if (d.dtype == VQMLP_F16) launch_attn<F16>(a, G, d.dtype, s);
+    else launch_attn<BF16>(a, G, d.dtype, s);
     if (trace_enabled())
-        trace_line("paged_attn T=%d R=%d heads=%d/%d D=%d: register tiles, %d rows, %d key splits%s", d.T,
-                   d.R, d.heads, d.kv_heads, d.D, 16 * G.nb, G.nsplit, G.nsplit > 1 ? " + join" : "");
+        trace_line("paged_attn T=%d R=%d heads=%d/%d D=%d: %s tiles, %d rows, %d key splits%s", d.T, d.R,
+                   d.heads, d.kv_heads, d.D, G.rb ? "LDS" : "register", G.rb ? 128 * G.rb : 16 * G.nb,
+                   G.nsplit, G.nsplit > 1 ? " + join" : "");
     return op_launched("vqmlp_paged_attn");
 }
