@@ -69,7 +69,8 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, Tile& t) {
     return true;
 }
 
-// The rows of many tokens (attn_tile.hip): rb blocks of 32 rows per wave.
-void launch_attn_tile(const AttnArgs& a, int dtype, int rb, int tiles, hipStream_t s);
+// Many rows (attn_tile.hip): tiles of kAttnTileRows.
+constexpr int kAttnTileRows = 128;
+void launch_attn_tile(const AttnArgs& a, int dtype, int tiles, hipStream_t s);
 
 }  // namespace vqmlp

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 
 struct AttnGeom {
     int nb;         // register tiles: blocks of 16 rows
-    int rb;         // LDS tiles: blocks of 32 rows per wave, 0 = register tiles
+    bool lds;       // tiles of kAttnTileRows with the keys in LDS, otherwise register tiles
     int tiles, nsplit, split_tiles;
     size_t opart, ml, bytes;
 };
@@ -290,11 +290,10 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
     const int keys = std::max(1, d.max_kv);
-    if (rows > 64) G.rb = 1;
-    if (G.rb && (all / (128 * G.rb) + d.R + 1) * d.kv_heads * kMaxSplit >= (1 << 24)) G.rb = 0;
+    G.lds = rows > 64 && (all / kAttnTileRows + d.R + 1) * d.kv_heads * kMaxSplit < (1 << 24);
     int mt, key_tiles;
-    if (G.rb) {
-        mt = 128 * G.rb;
+    if (G.lds) {
+        mt = kAttnTileRows;
         key_tiles = (keys + 63) / 64;
     } else {
         const int most = d.D > 128 ? 2 : 4;
@@ -305,7 +304,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     }
     G.tiles = int(all / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
-    if (G.rb) {
+    if (G.lds) {
         // The time in passes over a 64-key tile (about 2.4 us for 256 rows of D = 128): rounds of
         // workgroups over the compute units, two tiles' worth to start and end each, and what the
         // join moves.
@@ -368,8 +367,8 @@ void launch_wave_nb(const AttnArgs& a, int tiles, hipStream_t s) {
 
 template <class E>
 void launch_attn(const AttnArgs& a, const AttnGeom& G, int dtype, hipStream_t s) {
-    if (G.rb) {
-        launch_attn_tile(a, dtype, G.rb, G.tiles, s);
+    if (G.lds) {
+        launch_attn_tile(a, dtype, G.tiles, s);
     } else if (a.D <= 64) {
         if (G.nb == 1) launch_wave_nb<E, 64, 1>(a, G.tiles, s);
         else if (G.nb == 2) launch_wave_nb<E, 64, 2>(a, G.tiles, s);
@@ -462,7 +461,7 @@ extern "C" vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc* p, void* workspa
     else launch_attn<BF16>(a, G, d.dtype, s);
     if (trace_enabled())
         trace_line("paged_attn T=%d R=%d heads=%d/%d D=%d: %s tiles, %d rows, %d key splits%s", d.T, d.R,
-                   d.heads, d.kv_heads, d.D, G.rb ? "LDS" : "register", G.rb ? 128 * G.rb : 16 * G.nb,
+                   d.heads, d.kv_heads, d.D, G.lds ? "LDS" : "register", G.lds ? kAttnTileRows : 16 * G.nb,
                    G.nsplit, G.nsplit > 1 ? " + join" : "");
     return op_launched("vqmlp_paged_attn");
 }

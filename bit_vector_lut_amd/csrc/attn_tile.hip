@@ -1,7 +1,7 @@
 // attn_tile.hip -- paged attention for many rows: prompts and prompt chunks (gfx950).
 //
 // The mathematics, the packing of rows and the transposed products are those of attn.hip; here
-// four waves share a tile of 64 keys in LDS and each has 32 RB rows of its own, 32x32x16
+// four waves share a tile of 64 keys in LDS and each has 32 rows of its own, 32x32x16
 // matrix-core steps.  Bound by the matrix cores and, beside them, by the exponentials.
 #include "attn.h"
 
@@ -9,59 +9,82 @@ namespace vqmlp {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
+constexpr int kKT = 64;   // keys of a tile
 
-constexpr int kKT = 64;  // keys of a tile
+// 16 bytes per lane from base + off to LDS, lane after lane from byte `at` on, without passing
+// registers.  As the compiler's builtin it would make every later LDS read wait for all loads in
+// flight, since the two might meet; here the loop's own wait and barrier order them.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
+                 :: "s"(base), "v"(off), "s"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(at) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_byte(const void* p) {
+    return __builtin_amdgcn_readfirstlane(
+        uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p)));
+}
+// f(0), f(1), .., f(N - 1) with the number known at compile time
+template <class F, int... Z>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, Z...>) {
+    (f(std::integral_constant<int, Z>{}), ...);
+}
+// x as if it were new here: what is made of it in a loop is made there and holds no registers across it
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-template <class E, int DP, int RB, bool FULL>
-__global__ void __launch_bounds__(256, DP == 64 || RB == 1 ? 2 : 1) k_attn_tile(AttnArgs a) {
+template <class E, int DP, bool FULL>
+__global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a) {
     constexpr int KS = DP / 16, DB = DP / 32, NI = DP / 32;
-    constexpr int MT = 128 * RB;
-    constexpr int RPI = 512 / DP;  // key rows per load instruction
-    __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2][kKT * DP * 2];
-    __shared__ __attribute__((aligned(1024))) uint8_t vbuf[2][kKT * DP * 2];
+    constexpr int RPI = 512 / DP;        // key rows per load instruction
+    constexpr int TILE = kKT * DP * 2;   // bytes
+    __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2 * TILE];
+    __shared__ __attribute__((aligned(1024))) uint8_t vbuf[2 * TILE];
     const int groups = a.kv_heads * a.nsplit;
     const int x = blockIdx.x / groups, gi = blockIdx.x % groups;
     const int hk = gi % a.kv_heads, split = gi / a.kv_heads;
     Tile t;
-    if (!find_tile<MT>(a, x, t)) return;
+    if (!find_tile<kAttnTileRows>(a, x, t)) return;
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = uniform(threadIdx.x >> 6);
     const int lr = lane & 31, lh = lane >> 5;
     const int D = FULL ? DP : a.D;
     const int P1 = (1 << a.shift) - 1;
 
-    int lo[RB], hi[RB];
-    u32x4 qf[RB][KS];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const int rho = t.rho0 + 32 * (RB * wave + b) + lr;
-        const int i = rho / a.g, hh = rho - i * a.g;
-        const bool real = i < t.n;
-        const int p = t.kv - t.n + i;
-        hi[b] = real && t.r < a.R ? min(p, (a.width << a.shift) - 1) : -1;
-        lo[b] = a.window ? max(0, p - a.window + 1) : 0;
-        const uint16_t* src = a.q + (t.c0 + i) * a.ld_q + int64_t(hk * a.g + hh) * a.D + 8 * lh;
+    // this lane's query row: its token in the request (from t.n on: none) and its head
+    auto query = [&](int lane32, int* head) {
+        const int rho = t.rho0 + 32 * wave + lane32;
+        const int i = rho / a.g;
+        *head = hk * a.g + rho - i * a.g;
+        return i;
+    };
+    int head;
+    int qi = query(lr, &head);
+    const bool real = qi < t.n;
+    const int pos = t.kv - t.n + qi;
+    const int hi = real && t.r < a.R ? min(pos, (a.width << a.shift) - 1) : -1;
+    const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+    u32x4 qf[KS];
+    {
+        const uint16_t* src = a.q + (t.c0 + qi) * a.ld_q + int64_t(head) * a.D + 8 * lh;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            qf[b][s] = u32x4{0, 0, 0, 0};
-            if (real && (FULL || 16 * s + 8 * lh < D))
-                qf[b][s] = *reinterpret_cast<const u32x4*>(src + 16 * s);
+            qf[s] = u32x4{0, 0, 0, 0};
+            if (real && (FULL || 16 * s + 8 * lh < D)) qf[s] = *reinterpret_cast<const u32x4*>(src + 16 * s);
         }
     }
-    float m[RB], l[RB];
-    f32x16 o[RB][DB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        m[b] = kNegInf;
-        l[b] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[b][d][i] = 0.f;
-    }
     const float c = a.scale * 1.4426950408889634f;
+    float m = kNegInf, l = 0.f;
+    f32x16 o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
     const int kt0 = t.kmin / kKT;
     const int nt = t.kmax >= t.kmin ? t.kmax / kKT + 1 - kt0 : 0;
@@ -69,229 +92,274 @@ __global__ void __launch_bounds__(256, DP == 64 || RB == 1 ? 2 : 1) k_attn_tile(
     const int end = kt0 + (split == a.nsplit - 1 ? nt : min(nt, (split + 1) * a.split_tiles));
     const int32_t* row = a.table + (t.r < a.R ? t.r : 0) * a.ld_table;
     auto page_of = [&](int key) { return row[min(key >> a.shift, a.width - 1)]; };
+    auto in_cache = [&](int page) { return uint32_t(page) < uint32_t(a.n_pages); };
 
     // Staging.  A load instruction writes 1 KB of LDS, 16 bytes a lane in order.  K lies there as
-    // [key][D] and V as [d][64 keys], the 16-byte chunks of a row permuted by an exclusive or so
-    // that eight neighbouring lanes of an operand read touch all banks.
-    const int krow = lane / (DP / 8), kslot = lane % (DP / 8);
-    const int vrow = lane >> 3, vchunk = (lane & 7) ^ vrow;
-    auto kf = [](int key) { return (key & 3) | ((key >> 1) & 4); };
-    int vp_n = 0, kp_n[2] = {0, 0};
-    auto pages = [&](int kt) {
-        vp_n = page_of(kt * kKT + 8 * vchunk);
-        kp_n[0] = page_of(kt * kKT + 16 * wave);
-        kp_n[1] = page_of(kt * kKT + 16 * wave + 8);
+    // [key][D] and V as [d][64 keys], the 16-byte chunks of a row permuted by an exclusive or, so
+    // that sixteen neighbouring lanes of an operand read touch all 64 banks.
+    auto kf = [](int key) { return DP == 64 ? (key >> 1) & 7 : key & 15; };
+    const uint32_t klds = lds_byte(kbuf) + wave * NI * 1024, vlds = lds_byte(vbuf) + wave * NI * 1024;
+    const int vrow = lane >> 3;
+    const int vchunk = (lane & 7) ^ (vrow >> 1);  // of even loads; odd ones are four chunks away
+    int kp[2] = {0, 0}, vp[2] = {0, 0};
+    auto pages_k = [&](int kt) {
+        kp[0] = page_of(kt * kKT + 16 * wave);
+        kp[1] = page_of(kt * kKT + 16 * wave + 8);
     };
-    auto stage = [&](int kt, int buf) -> bool {  // true: a page of the tile is outside the cache
-        const int k0 = kt * kKT;
-        const bool bad = uint32_t(vp_n) >= uint32_t(a.n_pages);
-        const int vp = bad ? 0 : vp_n;
+    auto pages_v = [&](int kt) {
+        vp[0] = page_of(kt * kKT + 8 * vchunk);
+        vp[1] = page_of(kt * kKT + 8 * (vchunk ^ 4));
+    };
+    auto stage_k = [&](int kt, int buf, int lane) {
+        const uint8_t* base[2];  // of the first of a page's eight keys
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int page = uniform(in_cache(kp[h]) ? kp[h] : 0);
+            const int key = kt * kKT + 16 * wave + 8 * h;
+            base[h] = reinterpret_cast<const uint8_t*>(
+                a.kc + (((int64_t(page) * a.kv_heads + hk) << a.shift) + (key & P1)) * D);
+        }
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
-            const int key = 16 * wave + j * RPI + krow;
-            const int kp = uint32_t(kp_n[j * 2 / NI]) >= uint32_t(a.n_pages) ? 0 : kp_n[j * 2 / NI];
-            int chunk = kslot ^ kf(key);
+            const int krow = j * RPI + lane / (DP / 8);
+            int chunk = (lane % (DP / 8)) ^ kf(krow);
             if (!FULL && 8 * chunk >= D) chunk = 0;  // meets zeros of the query
-            const uint16_t* src = a.kc + (((int64_t(kp) * a.kv_heads + hk) << a.shift) + ((k0 + key) & P1)) * D + 8 * chunk;
-            __builtin_amdgcn_global_load_lds((global_void*)src, (lds_void*)&kbuf[buf][(wave * NI + j) * 1024], 16, 0, 0);
+            load_lds16(base[j * 2 / NI], (krow & 7) * D * 2 + chunk * 16, klds + buf * TILE + j * 1024);
         }
-        const uint16_t* vsrc = a.vc + ((int64_t(vp) * a.kv_heads + hk) * D << a.shift) + ((k0 + 8 * vchunk) & P1);
+    };
+    auto stage_v = [&](int kt, int buf) -> bool {  // true: a page of the tile is outside the cache
+        const uint16_t* src[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int page = in_cache(vp[h]) ? vp[h] : 0;
+            src[h] = a.vc + ((int64_t(page) * a.kv_heads + hk) * D << a.shift) +
+                     ((kt * kKT + 8 * (vchunk ^ (4 * h))) & P1);
+        }
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             int d = (wave * NI + j) * 8 + vrow;
             if (!FULL) d = min(d, D - 1);
-            __builtin_amdgcn_global_load_lds((global_void*)(vsrc + (int64_t(d) << a.shift)),
-                                             (lds_void*)&vbuf[buf][(wave * NI + j) * 1024], 16, 0, 0);
+            // the parity of wave * NI + j; NI is even
+            load_lds16(src[j & 1] + (int64_t(d) << a.shift), vlds + buf * TILE + j * 1024);
         }
-        return __any(bad);
+        return __any(!in_cache(vp[0]));
     };
 
-    // operand addresses: row m of the K operand takes key 16(a/2) + 8h + 4(a%2) + b, m = 8a + 4h + b,
+    // Operand addresses.  Row m = 8a + 4h + b of the K operand takes key 16(a/2) + 8h + 4(a%2) + b,
     // so that a lane's sixteen scores are keys 8 lh .. 8 lh + 7 of both 16-key steps.
     const int key_m = 16 * (lr >> 4) + 8 * ((lr >> 2) & 1) + 4 * ((lr >> 3) & 1) + (lr & 3);
-    int kaddr[4], vaddr[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        kaddr[s] = key_m * DP * 2 + (((2 * s + lh) ^ kf(key_m)) * 16);
-        vaddr[s] = lr * 128 + (((2 * s + lh) ^ (lr & 7)) * 16);
-    }
+    const int kbase = key_m * DP * 2 + (lh ^ kf(key_m)) * 16;  // step st: its chunk number gains 2 st
+    const int vbase = lr * 128 + (lh ^ (lr >> 1 & 7)) * 16;
+    constexpr int KA = DP == 64 ? 4 : 8;  // steps that the exclusive or reaches
+    auto kread = [&](int base, int sb, int st) {
+        return *reinterpret_cast<const u32x4*>(&kbuf[(base ^ (st % KA * 32)) + st / KA * (KA * 32) + sb * 32 * DP * 2]);
+    };
+    auto vread = [&](int base, int d, int q) {
+        return *reinterpret_cast<const u32x4*>(&vbuf[(base ^ (q * 32)) + d * 4096]);
+    };
 
-    // one tile: EDGE where some row does not see all its keys
-    auto compute = [&](int kt, int buf, auto edge_c) {
-        constexpr bool EDGE = decltype(edge_c)::value;
-        const int k0 = kt * kKT;
-        f32x16 s[RB][2];
+    auto edge = [&](int kt, bool bad) { return kt * kKT < t.full_lo || kt * kKT + kKT - 1 > t.full_hi || bad; };
+    // masks and the running maximum, before the tile's exponentials
+    auto maximum = [&](int kt, bool cut, f32x16* s, float mx) {
+        if (cut) {
+            mx = kNegInf;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int key = kt * kKT + 16 * q + 8 * lh;
+                const bool gone = !in_cache(page_of(key));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float z = s[q >> 1][8 * (q & 1) + j];
+                    s[q >> 1][8 * (q & 1) + j] = (gone | (key + j > hi) | (key + j < lo)) ? kNegInf : z;
+                    mx = fmaxf(mx, s[q >> 1][8 * (q & 1) + j]);
+                }
+            }
+        }
+        {
+            // the other half's maximum; the operands are two values to the compiler, which takes both
+            // results for one otherwise
+            const auto z = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, mx),
+                                                            uint32_t(fresh(__builtin_bit_cast(int, mx))), false, false);
+            const uint32_t z0 = z[0], z1 = z[1];
+            mx = fmaxf(__builtin_bit_cast(float, z0), __builtin_bit_cast(float, z1));
+        }
+        // the sums shrink only when a score outgrows the maximum by 2^3: probabilities then stay
+        // below 2^3 (2^15 with binary16's factor), and most tiles leave the outputs alone
+        if (__any((mx - m) * c > 3.f)) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = __builtin_amdgcn_exp2f((m - (mn == kNegInf ? 0.f : mn)) * c);
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+        }
+    };
+
+    // Iteration i: the exponentials of tile i (scores `s`) on the vector unit while the matrix cores
+    // make the scores of tile i + 1 (`sn`), then the value product of tile i.  K of i + 2 and V of
+    // i + 1 are on their way meanwhile.
+    bool bad_v = false;  // a page of the tile staged last is outside the cache
+    auto iteration = [&](int i, int buf, f32x16* s, f32x16* sn) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads are in LDS
+        __syncthreads();
+        if (edge(i, bad_v)) {
+            // values that no row may see can be anything in memory: make them zero
+            for (int e = threadIdx.x; e < DP * 8; e += 256) {
+                const int d = e >> 3, key = i * kKT + 8 * ((e & 7) ^ (d >> 1 & 7));
+                const bool there = in_cache(page_of(key));
+                u32x4* at = reinterpret_cast<u32x4*>(&vbuf[buf * TILE + e * 16]);
+                u32x4 v = *at;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool x0 = there & (key + 2 * j >= t.kmin) & (key + 2 * j <= t.kmax);
+                    const bool x1 = there & (key + 2 * j + 1 >= t.kmin) & (key + 2 * j + 1 <= t.kmax);
+                    v[j] &= (x0 ? 0xFFFFu : 0u) | (x1 ? 0xFFFF0000u : 0u);
+                }
+                *at = v;
+            }
+            __syncthreads();
+        }
+        const float mc = (m == kNegInf ? 0.f : m * c) - kBias<E>;
+        // One straight run of matrix-core steps, the scores' (of what the buffer held, unused, behind
+        // the last tile) and then the value product's.  Their operands are read from LDS four steps
+        // ahead, since a read takes longer than a step, and the vector work stands between them: the
+        // exponentials of keys 16 q .. 16 q + 15 before the value product of those keys.  The barriers
+        // keep the compiler from gathering the reads right in front of their steps.
+        constexpr int QK = 2 * KS, STEPS = QK + 4 * DB, SPREAD = QK + DB, MAX = 32 / (2 * DB);
+        u32x4 pf[4], fr[2][4];
+        float sum[2] = {0.f, 0.f}, p[2];
+        float mx[2] = {kNegInf, kNegInf};
+        const int kb = DP == 128 ? fresh(kbase) : kbase, vb = DP == 128 ? fresh(vbase) : vbase;
+        auto operand = [&](int z) {
+            return z < QK ? kread(kb + (buf ^ 1) * TILE, z & 1, z >> 1)
+                          : vread(vb + buf * TILE, (z - QK) % DB, (z - QK) / DB);
+        };
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sn[0][e] = sn[1][e] = 0.f;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) fr[0][y] = operand(y);
+        each([&](auto zc) __attribute__((always_inline)) {
+            constexpr int z = decltype(zc)::value;
+            if constexpr (z % 4 == 0 && z + 4 < STEPS) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) fr[(z / 4 + 1) & 1][y] = operand(z + 4 + y);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const u32x4 f = fr[z / 4 & 1][z % 4];
+            if constexpr (z < QK) sn[z & 1] = E::mfma32(f, qf[z >> 1], sn[z & 1]);
+            else o[(z - QK) % DB] = E::mfma32(f, pf[(z - QK) / DB], o[(z - QK) % DB]);
+            constexpr int e0 = (z * 32 + SPREAD - 1) / SPREAD, e1 = ((z + 1) * 32 + SPREAD - 1) / SPREAD;
+#pragma unroll
+            for (int e = e0; e < e1 && e < 32; ++e) {
+                p[e & 1] = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], c, -mc));
+                sum[e & 1] += p[e & 1];
+                if (e & 1) pf[e >> 3][(e & 7) >> 1] = pack16<E>(p[0], p[1]);
+            }
+            if constexpr (z >= SPREAD && z < SPREAD + 2 * DB) {
+#pragma unroll
+                for (int e = (z - SPREAD) * MAX; e < (z - SPREAD + 1) * MAX; ++e)
+                    mx[e & 1] = fmaxf(mx[e & 1], sn[e >> 4][e & 15]);
+            }
+            // tiles behind the last one are the last again: their buffers are not read
+            if constexpr (z == 2) stage_k(min(i + 2, end - 1), buf, DP == 128 ? fresh(lane) : lane);
+            if constexpr (z == 6) bad_v = stage_v(min(i + 1, end - 1), buf ^ 1);
+            if constexpr (z == 7) pages_k(min(i + 3, end - 1)), pages_v(min(i + 2, end - 1));
+            __builtin_amdgcn_sched_barrier(0);
+        }, std::make_integer_sequence<int, STEPS>{});
+        l += sum[0] + sum[1];
+        if (i + 1 < end) maximum(i + 1, edge(i + 1, bad_v), sn, fmaxf(mx[0], mx[1]));
+    };
+
+    if (begin < end) {
+        f32x16 s0[2], s1[2];
+        pages_k(begin);
+        pages_v(begin);
+        stage_k(begin, 0, lane);
+        bad_v = stage_v(begin, 0);
+        pages_k(min(begin + 1, end - 1));
+        stage_k(min(begin + 1, end - 1), 1, lane);
+        pages_k(min(begin + 2, end - 1));
+        pages_v(min(begin + 1, end - 1));
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
+            for (int e = 0; e < 16; ++e) s0[sb][e] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[b][sb][i] = 0.f;
-#pragma unroll
-            for (int st = 0; st < KS; ++st) {
-                const u32x4 k = *reinterpret_cast<const u32x4*>(&kbuf[buf][kaddr[st & 3] + (st >> 2) * 128 + sb * 32 * DP * 2]);
-#pragma unroll
-                for (int b = 0; b < RB; ++b) s[b][sb] = E::mfma32(k, qf[b][st], s[b][sb]);
-            }
+            for (int st = 0; st < KS; ++st)
+                s0[sb] = E::mfma32(kread(kbase, sb, st), qf[st], s0[sb]);
         }
-        u32x4 pf[RB][4];
-        bool there[4];
-        if constexpr (EDGE) {
+        float mx = kNegInf;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                there[q] = uint32_t(page_of(k0 + 16 * q + 8 * lh)) < uint32_t(a.n_pages);
+        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, s0[e >> 4][e & 15]);
+        maximum(begin, edge(begin, bad_v), s0, mx);
+        for (int i = begin; i < end; i += 2) {
+            iteration(i, 0, s0, s1);
+            if (i + 1 < end) iteration(i + 1, 1, s1, s0);
         }
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            if constexpr (EDGE) {
-#pragma unroll
-                for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int k = k0 + 32 * sb + 16 * (i >> 3) + 8 * lh + (i & 7);
-                        if (!there[2 * sb + (i >> 3)] || k > hi[b] || k < lo[b]) s[b][sb][i] = kNegInf;
-                    }
-            }
-            float mx = s[b][0][0];
-#pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][sb][i]);
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            if (__any((mx - m[b]) * c > 3.f)) {
-                const float mn = fmaxf(m[b], mx);
-                const float alpha = __builtin_amdgcn_exp2f((m[b] - (mn == kNegInf ? 0.f : mn)) * c);
-                m[b] = mn;
-                l[b] *= alpha;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][d][i] *= alpha;
-            }
-            const float mc = (m[b] == kNegInf ? 0.f : m[b] * c) - kBias<E>;
-            float sum = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float p[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = __builtin_amdgcn_exp2f(fmaf(s[b][q >> 1][8 * (q & 1) + j], c, -mc));
-                    sum += p[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) pf[b][q][j] = pack16<E>(p[2 * j], p[2 * j + 1]);
-            }
-            l[b] += sum;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u32x4 keep;
-            if constexpr (EDGE) {
-                const int k = k0 + 16 * q + 8 * lh;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool x0 = there[q] && k + 2 * j >= t.kmin && k + 2 * j <= t.kmax;
-                    const bool x1 = there[q] && k + 2 * j + 1 >= t.kmin && k + 2 * j + 1 <= t.kmax;
-                    keep[j] = (x0 ? 0xFFFFu : 0u) | (x1 ? 0xFFFF0000u : 0u);
-                }
-            }
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                u32x4 v = *reinterpret_cast<const u32x4*>(&vbuf[buf][vaddr[q] + d * 4096]);
-                if constexpr (EDGE) v &= keep;
-#pragma unroll
-                for (int b = 0; b < RB; ++b) o[b][d] = E::mfma32(v, pf[b][q], o[b][d]);
-            }
-        }
-    };
-
-    bool bad = false, bad_n = false;
-    if (begin < end) {
-        pages(begin);
-        bad_n = stage(begin, 0);
-        if (begin + 1 < end) pages(begin + 1);
-    }
-    for (int kt = begin; kt < end; ++kt) {
-        const int buf = (kt - begin) & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of the tile is in LDS
-        __syncthreads();
-        bad = bad_n;
-        if (kt + 1 < end) {
-            bad_n = stage(kt + 1, buf ^ 1);
-            if (kt + 2 < end) pages(kt + 2);
-        }
-        const int k0 = kt * kKT;
-        if (k0 < t.full_lo || k0 + kKT - 1 > t.full_hi || bad) compute(kt, buf, std::true_type{});
-        else compute(kt, buf, std::false_type{});
+        // no load may still be writing LDS when the workgroup ends
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
+    l += __shfl_xor(l, 32);
+    qi = query(fresh(lr), &head);
+    if (qi >= t.n) return;
+    const int64_t rowi = int64_t(t.c0 + qi) * a.heads + head;
+    if (a.nsplit > 1) {
+        float* dst = a.opart + (rowi * a.nsplit + split) * D;
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        l[b] += __shfl_xor(l[b], 32);
-        const int rho = t.rho0 + 32 * (RB * wave + b) + lr;
-        const int i = rho / a.g, hh = rho - i * a.g;
-        if (i >= t.n) continue;
-        const int head = hk * a.g + hh;
-        const int64_t rowi = int64_t(t.c0 + i) * a.heads + head;
-        if (a.nsplit > 1) {
-            float* dst = a.opart + (rowi * a.nsplit + split) * D;
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = 32 * d + 8 * j + 4 * lh;
-                    if (FULL || at < D)
-                        *reinterpret_cast<f32x4*>(dst + at) =
-                            f32x4{o[b][d][4 * j], o[b][d][4 * j + 1], o[b][d][4 * j + 2], o[b][d][4 * j + 3]};
-                }
-            if (lh == 0) {
-                a.ml[(rowi * a.nsplit + split) * 2] = m[b];
-                a.ml[(rowi * a.nsplit + split) * 2 + 1] = l[b];
+            for (int j = 0; j < 4; ++j) {
+                const int at = 32 * d + 8 * j + 4 * lh;
+                if (FULL || at < D)
+                    *reinterpret_cast<f32x4*>(dst + at) =
+                        f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
             }
-        } else {
-            const float inv = l[b] == 0.f ? 0.f : 1.f / l[b];  // NaN stays NaN
-            uint16_t* dst = a.y + (t.c0 + i) * a.ld_y + int64_t(head) * D;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = 32 * d + 8 * j + 4 * lh;
-                    if (FULL || at < D)
-                        *reinterpret_cast<u32x2*>(dst + at) =
-                            u32x2{pack16<E>(o[b][d][4 * j] * inv, o[b][d][4 * j + 1] * inv),
-                                  pack16<E>(o[b][d][4 * j + 2] * inv, o[b][d][4 * j + 3] * inv)};
-                }
-            if (lh == 0 && a.lse)
-                a.lse[rowi] = l[b] == 0.f ? kNegInf
-                                          : fmaf(m[b], a.scale, logf(l[b]) - kBias<E> * 0.6931471805599453f);
+        if (lh == 0) {
+            a.ml[(rowi * a.nsplit + split) * 2] = m;
+            a.ml[(rowi * a.nsplit + split) * 2 + 1] = l;
         }
+    } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+        uint16_t* dst = a.y + (t.c0 + qi) * a.ld_y + int64_t(head) * D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = 32 * d + 8 * j + 4 * lh;
+                if (FULL || at < D)
+                    *reinterpret_cast<u32x2*>(dst + at) =
+                        u32x2{pack16<E>(o[d][4 * j] * inv, o[d][4 * j + 1] * inv),
+                              pack16<E>(o[d][4 * j + 2] * inv, o[d][4 * j + 3] * inv)};
+            }
+        if (lh == 0 && a.lse)
+            a.lse[rowi] = l == 0.f ? kNegInf : fmaf(m, a.scale, logf(l) - kBias<E> * 0.6931471805599453f);
     }
 }
 
 template <class E, int DP>
-void launch_dp(const AttnArgs& a, int rb, unsigned blocks, hipStream_t s) {
-    if (a.D == DP) {
-        if (rb == 1) k_attn_tile<E, DP, 1, true><<<blocks, 256, 0, s>>>(a);
-        else k_attn_tile<E, DP, 2, true><<<blocks, 256, 0, s>>>(a);
-    } else {
-        if (rb == 1) k_attn_tile<E, DP, 1, false><<<blocks, 256, 0, s>>>(a);
-        else k_attn_tile<E, DP, 2, false><<<blocks, 256, 0, s>>>(a);
-    }
+void launch_dp(const AttnArgs& a, unsigned blocks, hipStream_t s) {
+    if (a.D == DP) k_attn_tile<E, DP, true><<<blocks, 256, 0, s>>>(a);
+    else k_attn_tile<E, DP, false><<<blocks, 256, 0, s>>>(a);
 }
 
 template <class E>
-void launch_e(const AttnArgs& a, int rb, unsigned blocks, hipStream_t s) {
-    if (a.D <= 64) launch_dp<E, 64>(a, rb, blocks, s);
-    else if (a.D <= 128) launch_dp<E, 128>(a, rb, blocks, s);
-    else launch_dp<E, 256>(a, rb, blocks, s);
+void launch_e(const AttnArgs& a, unsigned blocks, hipStream_t s) {
+    if (a.D <= 64) launch_dp<E, 64>(a, blocks, s);
+    else if (a.D <= 128) launch_dp<E, 128>(a, blocks, s);
+    else launch_dp<E, 256>(a, blocks, s);
 }
 
 }  // namespace
 
-void launch_attn_tile(const AttnArgs& a, int dtype, int rb, int tiles, hipStream_t s) {
+void launch_attn_tile(const AttnArgs& a, int dtype, int tiles, hipStream_t s) {
     const unsigned blocks = unsigned(tiles) * a.kv_heads * a.nsplit;
-    if (dtype == VQMLP_F16) launch_e<F16>(a, rb, blocks, s);
-    else launch_e<BF16>(a, rb, blocks, s);
+    if (dtype == VQMLP_F16) launch_e<F16>(a, blocks, s);
+    else launch_e<BF16>(a, blocks, s);
 }
 
 }  // namespace vqmlp
