@@ -69,7 +69,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, Tile& t) {
     return true;
 }
 
-// Many rows (attn_tile.hip): tiles of kAttnTileRows.
+// Many rows (attn_tile.hip).
 constexpr int kAttnTileRows = 128;
 void launch_attn_tile(const AttnArgs& a, int dtype, int tiles, hipStream_t s);
 

@@ -305,14 +305,18 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     G.tiles = int(all / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
     if (G.lds) {
-        // The time in passes over a 64-key tile (about 2.4 us for 256 rows of D = 128): rounds of
-        // workgroups over the compute units, two tiles' worth to start and end each, and what the
-        // join moves.
+        // The time in passes over a 64-key tile (2.4 us at D = 128 with two workgroups on every
+        // compute unit): rounds of workgroups, two tiles' worth to start and end each, and the join,
+        // which writes and reads FP32 sums at about 4 TB/s.  512 rows of 40/8 heads of 128 over
+        // 33,001 keys: 436 us with the three splits that this chooses, 539 / 477 / 453 / 457 with
+        // 2 / 4 / 6 / 8.
+        const int64_t slots = int64_t(cus) * (d.D <= 128 ? 2 : 1);
+        const double tile = 2.4e-6 * d.D / 128;
         G.nsplit = 1;
         double best = 1e300;
         for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
-            const double rounds = double((active * ns + cus - 1) / cus);
-            const double join = ns > 1 ? 2 + ns * double(rows_all) * d.D * 8 / 4e12 / 2.4e-6 : 0;
+            const double rounds = double((active * ns + slots - 1) / slots);
+            const double join = ns > 1 ? (4e-6 + ns * double(rows_all) * d.D * 8 / 4e12) / tile : 0;
             const double cost = rounds * ((key_tiles + ns - 1) / ns + 2) + join;
             if (cost < best) best = cost, G.nsplit = ns;
         }

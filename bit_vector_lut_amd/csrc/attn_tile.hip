@@ -46,7 +46,9 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2 * TILE];
     __shared__ __attribute__((aligned(1024))) uint8_t vbuf[2 * TILE];
     const int groups = a.kv_heads * a.nsplit;
-    const int x = blockIdx.x / groups, gi = blockIdx.x % groups;
+    // the last tiles of a prompt, which see the most keys, come first; workgroups that read the same
+    // keys are a multiple of 8 apart wherever kv_heads * splits is one: on the same XCD
+    const int x = (gridDim.x - 1 - blockIdx.x) / groups, gi = blockIdx.x % groups;
     const int hk = gi % a.kv_heads, split = gi / a.kv_heads;
     Tile t;
     if (!find_tile<kAttnTileRows>(a, x, t)) return;
