@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         return NTV == 1 ? 16 * wave + m : 32 * wave + 8 * (m >> 2) + (m & 3) + 4 * v;
     };
     f32x4 S[KS][2][NTV];
-    auto each_state = [&](auto&& f) {
+    auto each_state = [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < KS; ++p)
 #pragma unroll
@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                     if (dk < a.Dk && dv < a.Dv) f(S[p][b][v], int64_t(dk) * a.Dv + dv);
                 }
     };
-    auto load_state = [&](const float* src) {
+    auto load_state = [&](const float* src) __attribute__((always_inline)) {
         each_state([&](f32x4& x, int64_t at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = src[at + int64_t(i) * a.Dv];
         });
     };
-    auto store_state = [&](float* dst, float mul) {
+    auto store_state = [&](float* dst, float mul) __attribute__((always_inline)) {
         each_state([&](f32x4& x, int64_t at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[at + int64_t(i) * a.Dv] = x[i] * mul;
