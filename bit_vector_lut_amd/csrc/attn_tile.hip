@@ -11,33 +11,6 @@ namespace {
 
 constexpr int kKT = 64;   // keys of a tile
 
-// 16 bytes per lane from base + off to LDS, lane after lane from byte `at` on, without passing
-// registers.  As the compiler's builtin it would make every later LDS read wait for all loads in
-// flight, since the two might meet; here the loop's own wait and barrier order them.
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
-                 :: "s"(base), "v"(off), "s"(at) : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds16(const void* src, uint32_t at) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :: "v"(src), "s"(at) : "memory", "m0");
-}
-__device__ __forceinline__ uint32_t lds_byte(const void* p) {
-    return __builtin_amdgcn_readfirstlane(
-        uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p)));
-}
-// f(0), f(1), .., f(N - 1) with the number known at compile time
-template <class F, int... Z>
-__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, Z...>) {
-    (f(std::integral_constant<int, Z>{}), ...);
-}
-// x as if it were new here: what is made of it in a loop is made there and holds no registers across it
-__device__ __forceinline__ int fresh(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 template <class E, int DP, bool FULL>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a) {
     constexpr int KS = DP / 16, DB = DP / 32, NI = DP / 32;
@@ -204,7 +177,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     // i + 1 are on their way meanwhile.
     bool bad_v = false;  // a page of the tile staged last is outside the cache
     auto iteration = [&](int i, int buf, f32x16* s, f32x16* sn) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's loads are in LDS
+        wait_loads();  // this wave's loads are in LDS
         __syncthreads();
         if (edge(i, bad_v)) {
             // values that no row may see can be anything in memory: make them zero
@@ -284,7 +257,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         stage_k(min(begin + 1, end - 1), 1, lane);
         pages_k(min(begin + 2, end - 1));
         pages_v(min(begin + 1, end - 1));
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        wait_loads();
         __syncthreads();
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
@@ -303,7 +276,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
             if (i + 1 < end) iteration(i + 1, 1, s1, s0);
         }
         // no load may still be writing LDS when the workgroup ends
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        wait_loads();
     }
 
     l += __shfl_xor(l, 32);

@@ -152,18 +152,41 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // parts by 2^e (e from the chunk's largest value), the state's operand by its own maximum.
 constexpr int kTok = kC + 8;  // LDS row stride in elements: 144 bytes, 16-byte chunks spread over banks
 
+struct LinDecay {            // of one chunk; b = sum of g up to a token
+    float eb[kC], bl[kC];    // e^b, b log2 e
+    float tail[kC];          // e^(sum behind the token)
+    float etot;              // e^(sum of the chunk)
+};
 struct LinSmem {
     uint16_t kt[128][kTok];  // [dk][token]
     uint16_t vt[128][kTok];  // [dv][token]
-    uint16_t p[kC][kTok];    // [query][key] scores
-    float eb[kC], tail[kC], bl[kC];
-    float etot;
+    LinDecay d[2];           // of this chunk and the next
+};
+struct LinOutSmem {
+    uint16_t p[kC][kTok];                        // [query][key] scores
+    __attribute__((aligned(1024))) uint16_t q[kC * 128], k[kC * 128];  // rows of tokens, chunks permuted
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+// Prefix over the 64 lanes with data-parallel moves: within rows of 16 lanes, then across them.
+template <class T, class F>
+__device__ __forceinline__ T lane_scan(T v, T none, F&& op) {
+    auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+        const int n = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
+                                                  decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+        v = op(v, __builtin_bit_cast(T, n));
+    };
+    typedef std::integral_constant<int, 0xF> all;
+    step(std::integral_constant<int, 0x111>{}, all{});  // from 1, 2, 4 and 8 lanes below in the row
+    step(std::integral_constant<int, 0x112>{}, all{});
+    step(std::integral_constant<int, 0x114>{}, all{});
+    step(std::integral_constant<int, 0x118>{}, all{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // a row's last lane to the next row
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // lane 31 to the upper half
     return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = lane_scan(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+    return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 
 // 2^e, e in [-126, 127]
@@ -203,6 +226,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     constexpr bool HALF = __is_same(E, F16);
     constexpr int PARTS = HALF ? 2 : 3;
     __shared__ LinSmem sm;
+    __shared__ __attribute__((aligned(1024))) std::conditional_t<OUT, LinOutSmem, char> so;
     LinUnit u;
     if (!lin_unit(a, blockIdx.x, u)) return;
     const int h = blockIdx.y, hk = h / (a.hv / a.hk);
@@ -295,20 +319,65 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     const uint16_t* src = isk ? a.k + int64_t(hk) * a.Dk + 8 * cj : a.v + int64_t(h) * a.Dv + 8 * cj;
     const int64_t ld = isk ? a.ld_k : a.ld_v;
     u32x4 blk[8];
-    float gv = 0.f;
-    auto fetch = [&](int t) {  // chunk at token t of the request
+    float gv = 0.f, gr = 0.f;  // wave 0, of the chunk after the one in work: g of token `lane`, of 63 - `lane`
+    auto fetch = [&](int t) __attribute__((always_inline)) {  // chunk at token t of the request
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int tt = t + 8 * bi + i;
             blk[i] = u32x4{0, 0, 0, 0};
             if (inside && tt < t1) blk[i] = *reinterpret_cast<const u32x4*>(src + (u.c0 + tt) * ld);
         }
-        if (wave == 0) gv = t + lane < t1 ? fmaxf(a.g[(u.c0 + t + lane) * a.ld_g + h], kMinG) : 0.f;
+    };
+    auto fetch_g = [&](int t) __attribute__((always_inline)) {
+        if (wave != 0) return;
+        gv = t + lane < t1 ? fmaxf(a.g[(u.c0 + t + lane) * a.ld_g + h], kMinG) : 0.f;
+        gr = t + 63 - lane < t1 ? fmaxf(a.g[(u.c0 + t + 63 - lane) * a.ld_g + h], kMinG) : 0.f;
+    };
+    // sums from the front for e^{b}, from the back for the tails, each accurate against its own size
+    auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
+        if (wave != 0) return;
+        auto add = [](float x, float y) { return x + y; };
+        const float b = lane_scan(gv, 0.f, add), z = lane_scan(gr, 0.f, add);
+        const float eb = expf(b);
+        d.eb[lane] = eb;
+        d.bl[lane] = b * kLog2e;
+        // lane's z reaches back to token 63 - lane: it is what lies behind token 62 - lane
+        d.tail[lane == 63 ? 63 : 62 - lane] = lane == 63 ? 1.f : expf(z);
+        if (lane == 63) d.etot = eb;
+    };
+    // Q and K rows of a chunk, token by token, straight to LDS; behind the last token the last again
+    constexpr int RPI = 512 / DKP, NI = kC / RPI / 4;  // rows per load, loads per wave of one of the two
+    auto swz = [](int row) { return DKP == 64 ? (row >> 1) & 7 : row & 15; };
+    auto stage_qk = [&](int t) __attribute__((always_inline)) {
+        if constexpr (OUT) {
+            const uint32_t ql = lds_byte(so.q), kl = lds_byte(so.k);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int r = (wave * NI + j) * RPI + lane / (DKP / 8);
+                int chunk = (lane % (DKP / 8)) ^ swz(r);
+                if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros on the other side
+                const int64_t tok = u.c0 + min(t + r, t1 - 1);
+                const int64_t col = int64_t(hk) * a.Dk + 8 * chunk;
+                load_lds16(a.q + tok * a.ld_q + col, ql + (wave * NI + j) * 1024);
+                load_lds16(a.k + tok * a.ld_k + col, kl + (wave * NI + j) * 1024);
+            }
+        }
+    };
+    // 8 chunk columns 32 s + 8 g4 of token row r
+    auto qk_read = [&](const uint16_t* p, int r, int s) {
+        return *reinterpret_cast<const u32x4*>(p + r * DKP + 8 * ((4 * s + g4) ^ swz(r)));
     };
     float decay = 1.f;  // over the segment so far (!OUT)
     int e = 0;          // S is kept in units of 2^-e
-    if (t0 < t1) fetch(t0);
+    if (t0 < t1) {
+        fetch_g(t0);
+        fetch(t0);
+        stage_qk(t0);
+        decays(sm.d[0]);
+        fetch_g(t0 + kC);
+    }
     for (int t = t0; t < t1; t += kC) {
+        const LinDecay& dc = sm.d[(t - t0) / kC & 1];
         if (stage) {
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
@@ -321,63 +390,35 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 *reinterpret_cast<u32x4*>(dst) = w;
             }
         }
-        if (wave == 0) {
-            // lane = token: sums from the front for e^{b}, from the back for the tails, each
-            // accurate against its own size
-            float b = gv, z = gv;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const float x = __shfl_up(b, o), y = __shfl_down(z, o);
-                if (lane >= o) b += x;
-                if (lane + o < 64) z += y;
-            }
-            z = __shfl_down(z, 1);
-            sm.eb[lane] = expf(b);
-            sm.bl[lane] = b * kLog2e;
-            sm.tail[lane] = expf(lane == 63 ? 0.f : z);
-            if (lane == 63) sm.etot = expf(b);
-        }
-        if (t + kC < t1) fetch(t + kC);
-        u32x4 qf[OUT ? 4 : 1][KS];
-        u32x4 kf[KS];
-        if constexpr (OUT) {
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const bool in = 32 * s + 8 * g4 < a.Dk;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int tt = t + 16 * x + lr;
-                    qf[x][s] = u32x4{0, 0, 0, 0};
-                    if (in && tt < t1)
-                        qf[x][s] = *reinterpret_cast<const u32x4*>(a.q + (u.c0 + tt) * a.ld_q +
-                                                                   int64_t(hk) * a.Dk + 32 * s + 8 * g4);
-                }
-                const int tt = t + 16 * wave + lr;
-                kf[s] = u32x4{0, 0, 0, 0};
-                if (in && tt < t1)
-                    kf[s] = *reinterpret_cast<const u32x4*>(a.k + (u.c0 + tt) * a.ld_k + int64_t(hk) * a.Dk +
-                                                            32 * s + 8 * g4);
-            }
-        }
+        wait_loads();  // this wave's part of Q and K is in LDS
+        fetch(t + kC);
         __syncthreads();
         f32x4 o[NTV][4];
         if constexpr (OUT) {
             // scores of this wave's 16 keys with all queries from there on
-            const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&sm.bl[16 * wave + 4 * g4]);
+            u32x4 qf[4][KS], kf[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                kf[s] = qk_read(so.k, 16 * wave + lr, s);
+                if (32 * s + 8 * g4 >= a.Dk) kf[s] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) qf[x][s] = qk_read(so.q, 16 * x + lr, s);
+            }
+            const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if (x < (wave & 2)) continue;
                 f32x4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[x][s], sc);
-                const float bt = sm.bl[16 * x + lr];
+                const float bt = dc.bl[16 * x + lr];
                 float p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool see = 16 * wave + 4 * g4 + i <= 16 * x + lr;
                     p[i] = see ? sc[i] * a.scale * __builtin_amdgcn_exp2f(bt - bj4[i]) : 0.f;
                 }
-                *reinterpret_cast<u32x2*>(&sm.p[16 * x + lr][16 * wave + 4 * g4]) =
+                *reinterpret_cast<u32x2*>(&so.p[16 * x + lr][16 * wave + 4 * g4]) =
                     u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
             }
             // e^{b} S^T Q
@@ -392,7 +433,8 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                         for (int v = 0; v < NTV; ++v)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[p][b][v][i]));
-                mx = wave_max(mx);
+                // of values that are not negative, the bits are in the values' order
+                mx = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, mx)));
                 f = min(max(13 - expo(mx), -100), 100);
             }
             const float up = pow2(f), down = a.scale * pow2(-f) * pow2(-e);
@@ -413,11 +455,16 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float eb = sm.eb[16 * x + lr] * down;
+                const float eb = dc.eb[16 * x + lr] * down;
 #pragma unroll
                 for (int v = 0; v < NTV; ++v) o[v][x] *= eb;
             }
             __syncthreads();
+            if (t + kC < t1) stage_qk(t + kC);  // every wave is done with this chunk's
+        }
+        if (t + kC < t1) {
+            decays(sm.d[((t - t0) / kC + 1) & 1]);
+            fetch_g(t + 2 * kC);
         }
         u32x4 vf[NTV][2];
 #pragma unroll
@@ -430,7 +477,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int c = 0; c <= x / 2; ++c) {
-                    const u32x4 pf = *reinterpret_cast<const u32x4*>(&sm.p[16 * x + lr][32 * c + 8 * g4]);
+                    const u32x4 pf = *reinterpret_cast<const u32x4*>(&so.p[16 * x + lr][32 * c + 8 * g4]);
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
                 }
@@ -464,14 +511,13 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                         const uint32_t w = vf[v][c][i];
                         mx = max(mx, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
                     }
-#pragma unroll
-            for (int o2 = 32; o2; o2 >>= 1) mx = max(mx, uint32_t(__shfl_xor(int(mx), o2)));
+            mx = wave_max(mx);
             en = mx ? 13 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^13, 2^14)
         }
         const float lift = pow2(en);
-        const float keep = sm.etot * pow2(en - e);
+        const float keep = dc.etot * pow2(en - e);
         e = en;
-        decay *= sm.etot;
+        decay *= dc.etot;
 #pragma unroll
         for (int p = 0; p < KS; ++p)
 #pragma unroll
@@ -480,8 +526,8 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 for (int v = 0; v < NTV; ++v) S[p][b][v] *= keep;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sm.tail[32 * c + 8 * g4]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sm.tail[32 * c + 8 * g4 + 4]);
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4 + 4]);
             u32x4 part[NTV][PARTS];
 #pragma unroll
             for (int v = 0; v < NTV; ++v) {
@@ -519,6 +565,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         }
         __syncthreads();
     }
+    // no load to LDS is in flight here: each was waited for in the chunk that it was made for
     if (!OUT) {
         store_state(seg_state(u.first + u.seg), pow2(-e));
         if (tid == 0) a.dec[int64_t(u.first + u.seg) * a.hv + h] = decay;

@@ -61,6 +61,37 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
+// A value that all lanes share, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// 16 bytes per lane from base + off (or src) to LDS, lane after lane from byte `at` on, without
+// passing registers.  As the compiler's builtin it would make every later LDS read wait for all
+// loads in flight, since the two might meet; here the caller's own wait and barrier order them.  m0
+// has no other use in kernels that neither index registers nor send messages.
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
+                 :: "s"(base), "v"(off), "s"(uniform(at)) : "memory");
+}
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(uniform(at)) : "memory");
+}
+// All of this wave's loads are done.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_byte(const void* p) {
+    return __builtin_amdgcn_readfirstlane(
+        uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p)));
+}
+// f(0), f(1), .., f(N - 1) with the number known at compile time
+template <class F, int... Z>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, Z...>) {
+    (f(std::integral_constant<int, Z>{}), ...);
+}
+// x as if it were new here: what is made of it in a loop is made there and holds no registers across it
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // ---- host half
 
 inline bool op_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
