@@ -17,6 +17,7 @@
 #include "attn.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace vqmlp {
 
@@ -290,7 +291,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
     const int keys = std::max(1, d.max_kv);
-    G.lds = rows > 64 && (all / kAttnTileRows + d.R + 1) * d.kv_heads * kMaxSplit < (1 << 24);
+    G.lds = rows > (getenv("ATTN_MIN") ? atoi(getenv("ATTN_MIN")) : 64) && (all / kAttnTileRows + d.R + 1) * d.kv_heads * kMaxSplit < (1 << 24);
     int mt, key_tiles;
     if (G.lds) {
         mt = kAttnTileRows;
@@ -314,6 +315,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
         const double tile = 2.4e-6 * d.D / 128;
         G.nsplit = 1;
         double best = 1e300;
+        if (getenv("ATTN_NS")) G.nsplit = atoi(getenv("ATTN_NS")); else
         for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
             const double rounds = double((active * ns + slots - 1) / slots);
             const double join = ns > 1 ? (4e-6 + ns * double(rows_all) * d.D * 8 / 4e12) / tile : 0;

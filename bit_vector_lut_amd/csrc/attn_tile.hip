@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     // Iteration i: the exponentials of tile i (scores `s`) on the vector unit while the matrix cores
     // make the scores of tile i + 1 (`sn`), then the value product of tile i.  K of i + 2 and V of
     // i + 1 are on their way meanwhile.
+    const bool idle = t.rho0 + 32 * wave >= t.n * a.g;
     bool bad_v = false;  // a page of the tile staged last is outside the cache
     auto iteration = [&](int i, int buf, f32x16* s, f32x16* sn) {
         wait_loads();  // this wave's loads are in LDS
@@ -195,6 +196,12 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
                 *at = v;
             }
             __syncthreads();
+        }
+        if (idle) {  // no rows: only its share of the loads
+            stage_k(min(i + 2, end - 1), buf, lane);
+            bad_v = stage_v(min(i + 1, end - 1), buf ^ 1);
+            pages_k(min(i + 3, end - 1)), pages_v(min(i + 2, end - 1));
+            return;
         }
         const float mc = (m == kNegInf ? 0.f : m * c) - kBias<E>;
         // One straight run of matrix-core steps, the scores' (of what the buffer held, unused, behind

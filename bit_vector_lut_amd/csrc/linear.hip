@@ -20,6 +20,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kStepMaxQ = 16;
+constexpr int64_t kMaxLd = 1 << 24;  // 63 tokens apart still is a 32-bit number of bytes
 
 struct LinArgs {
     const uint16_t *q, *k, *v;
@@ -32,6 +33,7 @@ struct LinArgs {
     float* dec;   // [unit][v_heads] decay over a segment
     int64_t ld_q, ld_k, ld_v, ld_y, ld_g;
     int T, R, hk, hv, Dk, Dv, n_states, L;
+    int id0;      // number of the launch's first workgroup
     float scale;
 };
 
@@ -150,7 +152,17 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // times their decays, and the state as an operand of S^T Q, are rounded once to the 16-bit type:
 // the outputs are rounded to it as well.  binary16 parts are kept in range by powers of two: value
 // parts by 2^e (e from the chunk's largest value), the state's operand by its own maximum.
-constexpr int kTok = kC + 8;  // LDS row stride in elements: 144 bytes, 16-byte chunks spread over banks
+constexpr int kTok = kC + 8;  // LDS row stride of the scores: 144 bytes, 16-byte chunks spread over banks
+
+// K^T and V^T in LDS: rows of 64 tokens, the eight 16-byte chunks of a row permuted by an exclusive or
+// with bits 1, 3 and 2 ^ 4 of the row number.  An operand read takes one chunk number from sixteen
+// rows, either m = 0 .. 15 or 8 (m / 4) + m % 4; two rows fill the 64 banks, and rows of one parity get
+// eight different chunks either way.  In bytes; the permutation is linear, so a constant row or chunk
+// is an exclusive or with tok_bits of it, and a multiple of 32 rows an offset.
+__device__ __forceinline__ constexpr int tok_bits(int row, int chunk) {
+    return 16 * (chunk ^ ((row >> 1 & 1) | (row >> 2 & 2) | ((row ^ (row >> 2)) & 4)));
+}
+__device__ __forceinline__ constexpr int tok_at(int row, int chunk) { return row * kC * 2 + tok_bits(row, chunk); }
 
 struct LinDecay {            // of one chunk; b = sum of g up to a token
     float eb[kC], bl[kC];    // e^b, b log2 e
@@ -158,8 +170,8 @@ struct LinDecay {            // of one chunk; b = sum of g up to a token
     float etot;              // e^(sum of the chunk)
 };
 struct LinSmem {
-    uint16_t kt[128][kTok];  // [dk][token]
-    uint16_t vt[128][kTok];  // [dv][token]
+    __attribute__((aligned(256))) uint8_t kt[128 * kC * 2];  // [dk][token], tok_at
+    __attribute__((aligned(256))) uint8_t vt[128 * kC * 2];  // [dv][token]
     LinDecay d[2];           // of this chunk and the next
 };
 struct LinOutSmem {
@@ -227,10 +239,14 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     constexpr int PARTS = HALF ? 2 : 3;
     __shared__ LinSmem sm;
     __shared__ __attribute__((aligned(1024))) std::conditional_t<OUT, LinOutSmem, char> so;
+    // Workgroups go round the eight XCDs; those of the value heads that read the same queries and keys
+    // are 8 apart, on one XCD, one after another.
+    const int heads = a.hv / a.hk;
+    const int id = a.id0 + blockIdx.x, pair = id / (8 * heads) * 8 + id % 8;  // (unit, key head)
+    const int hk = pair % a.hk, h = hk * heads + id / 8 % heads;
     LinUnit u;
-    if (!lin_unit(a, blockIdx.x, u)) return;
-    const int h = blockIdx.y, hk = h / (a.hv / a.hk);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (!lin_unit(a, pair / a.hk, u)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int lr = lane & 15, g4 = lane >> 4;
     const int DVP = 64 * NTV;
     const int t0 = u.seg * a.L, t1 = min(u.n, t0 + a.L);
@@ -310,56 +326,75 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         }
     }
 
-    // staging: thread = one 8 x 8 block (tokens 8 bi .., columns 8 bj ..) of K or V
-    const int bi = tid & 7, bj = tid >> 3;
-    const bool isk = bj < DKP / 8;
+    // Addresses: a base that the wave shares plus 32-bit offsets of the lanes.
+    // staging: thread = one 8 x 8 block (tokens 8 bi .., columns 8 bj ..) of K or V; a wave has one of
+    // them, eight neighbouring lanes 128 bytes of a token
+    const int bi = lane >> 3, bj = 8 * wave + (lane & 7);
+    const bool isk = 8 * wave < DKP / 8;
     const int cj = isk ? bj : bj - DKP / 8;
     const bool stage = isk || cj < DVP / 8;
     const bool inside = isk ? 8 * cj < a.Dk : stage && 8 * cj < a.Dv;
-    const uint16_t* src = isk ? a.k + int64_t(hk) * a.Dk + 8 * cj : a.v + int64_t(h) * a.Dv + 8 * cj;
-    const int64_t ld = isk ? a.ld_k : a.ld_v;
+    const int64_t ld = 2 * (isk ? a.ld_k : a.ld_v);  // bytes
+    const uint8_t* const src =
+        reinterpret_cast<const uint8_t*>(isk ? a.k + int64_t(hk) * a.Dk : a.v + int64_t(h) * a.Dv) + u.c0 * ld;
+    const uint32_t src_off = uint32_t(8 * bi) * uint32_t(ld) + 16 * cj;
+    const int kget = tok_at(8 * (lr >> 2) + (lr & 3), g4), vget = tok_at(dvc(0, lr), g4);
+    const int put = tok_at(8 * cj, bi);
     u32x4 blk[8];
-    float gv = 0.f, gr = 0.f;  // wave 0, of the chunk after the one in work: g of token `lane`, of 63 - `lane`
+    // of the chunk after the one in work: g of token `lane` (wave 0), of token 63 - `lane` (wave 1)
+    float gv = 0.f;
     auto fetch = [&](int t) __attribute__((always_inline)) {  // chunk at token t of the request
+        const uint8_t* const base = src + t * ld;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int tt = t + 8 * bi + i;
             blk[i] = u32x4{0, 0, 0, 0};
-            if (inside && tt < t1) blk[i] = *reinterpret_cast<const u32x4*>(src + (u.c0 + tt) * ld);
+            if (inside && t + 8 * bi + i < t1) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
         }
     };
     auto fetch_g = [&](int t) __attribute__((always_inline)) {
-        if (wave != 0) return;
-        gv = t + lane < t1 ? fmaxf(a.g[(u.c0 + t + lane) * a.ld_g + h], kMinG) : 0.f;
-        gr = t + 63 - lane < t1 ? fmaxf(a.g[(u.c0 + t + 63 - lane) * a.ld_g + h], kMinG) : 0.f;
+        if (wave > 1) return;
+        const uint8_t* const base = reinterpret_cast<const uint8_t*>(a.g + (u.c0 + t) * a.ld_g + h);
+        const int i = wave ? 63 - lane : lane;
+        gv = t + i < t1 ? fmaxf(*reinterpret_cast<const float*>(base + uint32_t(i) * uint32_t(a.ld_g) * 4), kMinG) : 0.f;
     };
     // sums from the front for e^{b}, from the back for the tails, each accurate against its own size
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
-        if (wave != 0) return;
-        auto add = [](float x, float y) { return x + y; };
-        const float b = lane_scan(gv, 0.f, add), z = lane_scan(gr, 0.f, add);
+        if (wave > 1) return;
+        const float b = lane_scan(gv, 0.f, [](float x, float y) { return x + y; });
         const float eb = expf(b);
-        d.eb[lane] = eb;
-        d.bl[lane] = b * kLog2e;
-        // lane's z reaches back to token 63 - lane: it is what lies behind token 62 - lane
-        d.tail[lane == 63 ? 63 : 62 - lane] = lane == 63 ? 1.f : expf(z);
-        if (lane == 63) d.etot = eb;
+        if (wave == 0) {
+            d.eb[lane] = eb;
+            d.bl[lane] = b * kLog2e;
+            if (lane == 63) d.etot = eb;
+        } else {
+            // from the back b reaches to token 63 - lane: what lies behind token 62 - lane
+            d.tail[lane == 63 ? 63 : 62 - lane] = lane == 63 ? 1.f : eb;
+        }
     };
     // Q and K rows of a chunk, token by token, straight to LDS; behind the last token the last again
     constexpr int RPI = 512 / DKP, NI = kC / RPI / 4;  // rows per load, loads per wave of one of the two
     auto swz = [](int row) { return DKP == 64 ? (row >> 1) & 7 : row & 15; };
     auto stage_qk = [&](int t) __attribute__((always_inline)) {
         if constexpr (OUT) {
-            const uint32_t ql = lds_byte(so.q), kl = lds_byte(so.k);
+            const uint32_t ql = lds_byte(so.q) + wave * NI * 1024, kl = lds_byte(so.k) + wave * NI * 1024;
+            const uint8_t* const q = reinterpret_cast<const uint8_t*>(a.q + (u.c0 + t) * a.ld_q + int64_t(hk) * a.Dk);
+            const uint8_t* const k = reinterpret_cast<const uint8_t*>(a.k + (u.c0 + t) * a.ld_k + int64_t(hk) * a.Dk);
+            const uint32_t lq = uint32_t(a.ld_q) * 2, lk = uint32_t(a.ld_k) * 2;
+            const int r0 = lane / (DKP / 8);
+            const bool whole = t + kC <= t1;
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
-                const int r = (wave * NI + j) * RPI + lane / (DKP / 8);
-                int chunk = (lane % (DKP / 8)) ^ swz(r);
+                const int first = (wave * NI + j) * RPI;  // a multiple of RPI: its low bits are j's
+                int chunk = (lane % (DKP / 8)) ^ swz(r0) ^ swz(j * RPI);
                 if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros on the other side
-                const int64_t tok = u.c0 + min(t + r, t1 - 1);
-                const int64_t col = int64_t(hk) * a.Dk + 8 * chunk;
-                load_lds16(a.q + tok * a.ld_q + col, ql + (wave * NI + j) * 1024);
-                load_lds16(a.k + tok * a.ld_k + col, kl + (wave * NI + j) * 1024);
+                if (whole) {
+                    load_lds16(q + int64_t(first) * lq, r0 * lq + 16 * chunk, ql + j * 1024);
+                    load_lds16(k + int64_t(first) * lk, r0 * lk + 16 * chunk, kl + j * 1024);
+                } else {
+                    const int r = min(first + r0, t1 - 1 - t);
+                    load_lds16(q, r * lq + 16 * chunk, ql + j * 1024);
+                    load_lds16(k, r * lk + 16 * chunk, kl + j * 1024);
+                }
             }
         }
     };
@@ -386,13 +421,14 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     w[i] = __builtin_amdgcn_perm(blk[2 * i + 1][cc / 2], blk[2 * i][cc / 2], sel);
-                uint16_t* dst = isk ? &sm.kt[8 * cj + cc][8 * bi] : &sm.vt[8 * cj + cc][8 * bi];
-                *reinterpret_cast<u32x4*>(dst) = w;
+                *reinterpret_cast<u32x4*>(&(isk ? sm.kt : sm.vt)[(put ^ tok_bits(cc, 0)) + cc * kC * 2]) = w;
             }
         }
         wait_loads();  // this wave's part of Q and K is in LDS
         fetch(t + kC);
         __syncthreads();
+        decays(sm.d[((t - t0) / kC + 1) & 1]);
+        fetch_g(t + 2 * kC);
         f32x4 o[NTV][4];
         if constexpr (OUT) {
             // scores of this wave's 16 keys with all queries from there on
@@ -404,6 +440,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) qf[x][s] = qk_read(so.q, 16 * x + lr, s);
             }
+            __builtin_amdgcn_sched_barrier(0);  // all reads on their way before the first product waits
             const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -422,7 +459,6 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                     u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
             }
             // e^{b} S^T Q
-            int f = 0;
             if constexpr (HALF) {
                 float mx = 0.f;
 #pragma unroll
@@ -435,9 +471,20 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[p][b][v][i]));
                 // of values that are not negative, the bits are in the values' order
                 mx = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, mx)));
-                f = min(max(13 - expo(mx), -100), 100);
+                // outside the range in which binary16 holds all that matters of S: other units
+                if (mx >= 32768.f || (mx < 0.25f && mx > 0.f)) {
+                    const int f = min(max(10 - expo(mx), -100 - e), 100 - e);
+                    const float up = pow2(min(max(f, -126), 126));
+                    e += min(max(f, -126), 126);
+#pragma unroll
+                    for (int p = 0; p < KS; ++p)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int v = 0; v < NTV; ++v) S[p][b][v] *= up;
+                }
             }
-            const float up = pow2(f), down = a.scale * pow2(-f) * pow2(-e);
+            const float down = a.scale * pow2(-e);
 #pragma unroll
             for (int v = 0; v < NTV; ++v)
 #pragma unroll
@@ -446,8 +493,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             for (int p = 0; p < KS; ++p)
 #pragma unroll
                 for (int v = 0; v < NTV; ++v) {
-                    f32x4 s0 = S[p][0][v], s1 = S[p][1][v];
-                    if constexpr (HALF) s0 *= up, s1 *= up;
+                    const f32x4 s0 = S[p][0][v], s1 = S[p][1][v];
                     const u32x4 sf = {pack16<E>(s0[0], s0[1]), pack16<E>(s0[2], s0[3]),
                                       pack16<E>(s1[0], s1[1]), pack16<E>(s1[2], s1[3])};
 #pragma unroll
@@ -462,16 +508,12 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             __syncthreads();
             if (t + kC < t1) stage_qk(t + kC);  // every wave is done with this chunk's
         }
-        if (t + kC < t1) {
-            decays(sm.d[((t - t0) / kC + 1) & 1]);
-            fetch_g(t + 2 * kC);
-        }
         u32x4 vf[NTV][2];
 #pragma unroll
         for (int v = 0; v < NTV; ++v)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[dvc(v, lr)][32 * c + 8 * g4]);
+                vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[(vget ^ tok_bits(4 * v, 4 * c)) + 4 * v * kC * 2]);
         if constexpr (OUT) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
@@ -483,18 +525,18 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int tt = t + 16 * x + lr;
-                if (tt >= t1) continue;
-                uint16_t* dst = a.y + (u.c0 + tt) * a.ld_y + int64_t(h) * a.Dv;
+                if (t + 16 * x + lr >= t1) continue;
+                uint8_t* const dst = reinterpret_cast<uint8_t*>(a.y + (u.c0 + t + 16 * x) * a.ld_y + int64_t(h) * a.Dv);
+                const uint32_t off = uint32_t(lr) * uint32_t(a.ld_y) * 2;
                 if constexpr (NTV == 2) {
                     const int dv = 32 * wave + 8 * g4;
                     const u32x4 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3]),
                                      pack16<E>(o[1][x][0], o[1][x][1]), pack16<E>(o[1][x][2], o[1][x][3])};
-                    if (dv < a.Dv) *reinterpret_cast<u32x4*>(dst + dv) = w;
+                    if (dv < a.Dv) *reinterpret_cast<u32x4*>(dst + (off + 2 * dv)) = w;
                 } else {
                     const int dv = 16 * wave + 4 * g4;
                     const u32x2 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3])};
-                    if (dv < a.Dv) *reinterpret_cast<u32x2*>(dst + dv) = w;
+                    if (dv < a.Dv) *reinterpret_cast<u32x2*>(dst + (off + 2 * dv)) = w;
                 }
             }
         }
@@ -512,10 +554,10 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                         mx = max(mx, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
                     }
             mx = wave_max(mx);
-            en = mx ? 13 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^13, 2^14)
+            en = mx ? 10 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^10, 2^11)
         }
         const float lift = pow2(en);
-        const float keep = dc.etot * pow2(en - e);
+        const float keep = dc.etot * pow2(max(en - e, -126));
         e = en;
         decay *= dc.etot;
 #pragma unroll
@@ -524,45 +566,59 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int v = 0; v < NTV; ++v) S[p][b][v] *= keep;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        // K^T operands are read two steps (of four products and more) ahead; the parts of the second 32 tokens are made between
+        // the products of the first
+        u32x4 part[2][NTV][PARTS], kk[2][2];
+        auto parts = [&](int c, int v) __attribute__((always_inline)) {
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4]);
             const f32x4 w1 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4 + 4]);
-            u32x4 part[NTV][PARTS];
+            float x[8];
 #pragma unroll
-            for (int v = 0; v < NTV; ++v) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = lo16<E>(vf[v][c][i]) * ((i < 2 ? w0[2 * i] : w1[2 * i - 4]) * lift);
-                    x[2 * i + 1] = hi16<E>(vf[v][c][i]) * ((i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]) * lift);
-                }
-#pragma unroll
-                for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w = pack16<E>(x[2 * i], x[2 * i + 1]);
-                        // one rounded value for the operand and for what is left of x: otherwise
-                        // the compiler rounds x twice, once fused with its product, and the two
-                        // may differ by a step
-                        asm("" : "+v"(w));
-                        part[v][q][i] = w;
-                        x[2 * i] -= lo16<E>(w);
-                        x[2 * i + 1] -= hi16<E>(w);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = fmaf(lo16<E>(vf[v][c][i]), (i < 2 ? w0[2 * i] : w1[2 * i - 4]) * lift, 0.f);
+                x[2 * i + 1] = fmaf(hi16<E>(vf[v][c][i]), (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]) * lift, 0.f);
             }
 #pragma unroll
-            for (int p = 0; p < KS; ++p)
+            for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const u32x4 kk = *reinterpret_cast<const u32x4*>(
-                        &sm.kt[32 * p + 8 * (lr >> 2) + (lr & 3) + 4 * b][32 * c + 8 * g4]);
-#pragma unroll
-                    for (int q = PARTS - 1; q >= 0; --q)
-#pragma unroll
-                        for (int v = 0; v < NTV; ++v) S[p][b][v] = E::mfma16(kk, part[v][q], S[p][b][v]);
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w = pack16<E>(x[2 * i], x[2 * i + 1]);
+                    // one rounded value for the operand and for what is left of x: otherwise
+                    // the compiler rounds x twice, once fused with its product, and the two
+                    // may differ by a step
+                    asm("" : "+v"(w));
+                    part[c][v][q][i] = w;
+                    if (q + 1 < PARTS) {
+                        x[2 * i] = fmaf(lo16<E>(w), -1.f, x[2 * i]);
+                        x[2 * i + 1] = fmaf(hi16<E>(w), -1.f, x[2 * i + 1]);
+                    }
                 }
-        }
+        };
+        constexpr int STEPS = 4 * KS;  // (c, p, b)
+        auto k_read = [&](int z) {
+            const int c = z / (2 * KS), p = z / 2 % KS, b = z & 1;
+            return *reinterpret_cast<const u32x4*>(
+                &sm.kt[(kget ^ tok_bits(4 * b, 4 * c)) + (32 * p + 4 * b) * kC * 2]);
+        };
+#pragma unroll
+        for (int y = 0; y < 2; ++y) kk[0][y] = k_read(y);
+#pragma unroll
+        for (int v = 0; v < NTV; ++v) parts(0, v);
+        each([&](auto zc) __attribute__((always_inline)) {
+            constexpr int z = decltype(zc)::value;
+            constexpr int c = z / (2 * KS), p = z / 2 % KS, b = z & 1;
+            if constexpr (z % 2 == 0 && z + 2 < STEPS) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) kk[(z / 2 + 1) & 1][y] = k_read(z + 2 + y);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v)
+                    S[p][b][v] = E::mfma16(kk[z / 2 & 1][z & 1], part[c][v][q], S[p][b][v]);
+            if constexpr (z < 2 * KS && z % KS == 0 && z / KS < NTV) parts(1, z / KS);
+        }, std::make_integer_sequence<int, STEPS>{});
         __syncthreads();
     }
     // no load to LDS is in flight here: each was waited for in the chunk that it was made for
@@ -587,14 +643,23 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     LinGeom G{};
     G.step = d.max_q <= kStepMaxQ;
     if (G.step) return G;
+    // Segments of a request go through at once, at the price of a pass for their states first (0.6 of
+    // the time of the outputs' pass), of three chunks' worth of time to start and end each, and of 0.6
+    // for each earlier segment whose state an output segment takes in.  The unit is a chunk in a round
+    // of two workgroups on every compute unit.  8,000 tokens of 48 heads of 128 x 128: 178 us with the
+    // 13 chunks that this chooses, 220 / 197 / 189 / 208 with 9 / 12 / 16 / 18.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
-    const int64_t heads = int64_t(d.R) * d.v_heads;
-    int nseg = int(std::min<int64_t>(32, (2 * int64_t(cus) + heads - 1) / heads));
-    nseg = std::max(1, std::min(nseg, most / 256));
-    G.split = nseg > 1;
     const int chunks = (most + kC - 1) / kC;
+    const int64_t slots = 2 * int64_t(cus);
+    auto rounds = [&](int64_t units) { return double((units * d.v_heads + slots - 1) / slots); };
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
-    G.L = G.split ? (chunks + nseg - 1) / nseg * kC : std::max(1, (d.T + kC - 1) / kC) * kC;
+    G.L = std::max(1, (d.T + kC - 1) / kC) * kC;
+    double best = rounds(d.R) * (chunks + 3);
+    for (int n = 4; n < chunks; ++n) {
+        const int64_t units = d.R == 1 ? (chunks + n - 1) / n : d.T / (n * kC) + d.R / 2;
+        const double cost = rounds(std::max<int64_t>(units, d.R)) * (1.6 * n + 6) + 0.6 * ((chunks - 1) / n);
+        if (cost < best) best = cost, G.split = true, G.L = n * kC;
+    }
     G.units = d.T / G.L + d.R + 1;
     if (G.split) {
         G.dec = align256(size_t(G.units) * d.v_heads * d.Dk * d.Dv * 4);
@@ -627,14 +692,18 @@ void launch_step(const LinArgs& a, hipStream_t s) {
 }
 
 template <class E, bool OUT>
-void launch_chunk(const LinArgs& a, int units, hipStream_t s) {
-    const dim3 grid(units, a.hv);
-    if (a.Dk <= 64) {
-        if (a.Dv <= 64) k_lin_chunk<E, 64, 1, OUT><<<grid, 256, 0, s>>>(a);
-        else k_lin_chunk<E, 64, 2, OUT><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (a.Dv <= 64) k_lin_chunk<E, 128, 1, OUT><<<grid, 256, 0, s>>>(a);
-        else k_lin_chunk<E, 128, 2, OUT><<<grid, 256, 0, s>>>(a);
+void launch_chunk(LinArgs a, int units, hipStream_t s) {
+    const int64_t all = (int64_t(units) * a.hk + 7) / 8 * 8 * (a.hv / a.hk), most = 8 << 20;
+    for (int64_t at = 0; at < all; at += most) {  // a launch holds fewer than 2^32 threads
+        const unsigned grid = unsigned(std::min(most, all - at));
+        a.id0 = int(at);
+        if (a.Dk <= 64) {
+            if (a.Dv <= 64) k_lin_chunk<E, 64, 1, OUT><<<grid, 256, 0, s>>>(a);
+            else k_lin_chunk<E, 64, 2, OUT><<<grid, 256, 0, s>>>(a);
+        } else {
+            if (a.Dv <= 64) k_lin_chunk<E, 128, 1, OUT><<<grid, 256, 0, s>>>(a);
+            else k_lin_chunk<E, 128, 2, OUT><<<grid, 256, 0, s>>>(a);
+        }
     }
 }
 
@@ -679,10 +748,10 @@ extern "C" vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc* p, void* work
                                 int64_t(d.v_heads) * d.Dv, int64_t(d.v_heads) * d.Dv, d.v_heads};
         const int64_t lds[] = {d.ld_q, d.ld_k, d.ld_v, d.ld_y, d.ld_g};
         for (int i = 0; i < 5; ++i)
-            OP_REQUIRE((d.T == 1 || lds[i] >= rows[i]) && lds[i] >= 0 && lds[i] <= (int64_t(1) << 40) &&
+            OP_REQUIRE((d.T == 1 || lds[i] >= rows[i]) && lds[i] >= 0 && lds[i] <= kMaxLd &&
                            (i == 4 || lds[i] % 8 == 0),
-                       "vqmlp_linear_attn: token strides have to cover the heads, those of q, k, v and y be "
-                       "multiples of 8");
+                       "vqmlp_linear_attn: token strides have to cover the heads and be at most 2^24, those of q, k, "
+                       "v and y be multiples of 8");
     }
     if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
     const LinGeom G = lin_geom(d, cus);
