@@ -17,20 +17,21 @@
 #include "attn.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace vqmlp {
 
 namespace {
 
 // ---------------------------------------------------------------- few rows: keys over the waves
-// NW waves share 16 NB rows of one key head and a split of the keys, tile by tile in turn, each
-// straight from the cache into its registers; their sums join in LDS at the end.
-template <class E, int DP, int NB, bool FULL, int NW>
-__global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
-    constexpr int MT = 16 * NB, KS = DP / 32, DT = DP / 16;
-    constexpr int DC = DP < 128 ? DP : 128;  // columns joined per round
-    __shared__ float obuf[NW][16][DC + 4];
+// D in 129 .. 256.  Four waves share 16 rows of one key head and a split of the keys, tile by tile in
+// turn, each straight from the cache into its registers; their sums join in LDS at the end.  Bound by
+// reading the cache.  A tile ahead in registers measured the same, 256 registers for two waves a SIMD
+// spill (177 against 123 us at 32 requests of up to 8,000 keys, 24/4 heads of 256).
+template <class E, bool FULL>
+__global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
+    constexpr int DP = 256, NW = 4, MT = 16, KS = DP / 32, DT = DP / 16;
+    constexpr int DC = 128;  // columns joined per round
+    __shared__ float obuf[NW][MT][DC + 4];
     __shared__ float mlbuf[NW][MT][2];
     Tile t;
     if (!find_tile<MT>(a, blockIdx.x, t)) return;
@@ -40,33 +41,23 @@ __global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
     const int D = FULL ? DP : a.D;
     const int P1 = (1 << a.shift) - 1;
 
-    int lo[NB], hi[NB];
-    u32x4 qf[NB][KS];
+    const int rho = t.rho0 + lr;
+    const int qi = rho / a.g, hh = rho - qi * a.g;
+    const bool real = qi < t.n;
+    const int pos = t.kv - t.n + qi;
+    const int hi = real && t.r < a.R ? min(pos, (a.width << a.shift) - 1) : -1;
+    const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+    const uint16_t* src = a.q + (t.c0 + qi) * a.ld_q + int64_t(hk * a.g + hh) * a.D + 8 * g;
+    u32x4 qf[KS];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int rho = t.rho0 + 16 * b + lr;
-        const int i = rho / a.g, hh = rho - i * a.g;
-        const bool real = i < t.n;
-        const int p = t.kv - t.n + i;
-        hi[b] = real && t.r < a.R ? min(p, (a.width << a.shift) - 1) : -1;
-        lo[b] = a.window ? max(0, p - a.window + 1) : 0;
-        const uint16_t* src = a.q + (t.c0 + i) * a.ld_q + int64_t(hk * a.g + hh) * a.D + 8 * g;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qf[b][s] = u32x4{0, 0, 0, 0};
-            if (real && (FULL || 32 * s + 8 * g < D))
-                qf[b][s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
-        }
+    for (int s = 0; s < KS; ++s) {
+        qf[s] = u32x4{0, 0, 0, 0};
+        if (real && (FULL || 32 * s + 8 * g < D)) qf[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
     }
-    float m[NB], l[NB];
-    f32x4 o[NB][DT];
+    float m = kNegInf, l = 0.f;
+    f32x4 o[DT];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        m[b] = kNegInf;
-        l[b] = 0.f;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[b][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int dt = 0; dt < DT; ++dt) o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
     const float c = a.scale * 1.4426950408889634f;
 
     const int kt0 = t.kmin >> 5;
@@ -77,159 +68,149 @@ __global__ void __launch_bounds__(NW * 64) k_attn_wave(AttnArgs a) {
     // page numbers of the lane's two K rows and of its eight V columns in a tile
     const int krow = 8 * (lr >> 2), vcol = 8 * g;
     auto page_of = [&](int key) { return row[min(key >> a.shift, a.width - 1)]; };
-    int kt = begin + wave;
-    int kp_next = 0, vp_next = 0;
-    if (kt < end) {
-        kp_next = page_of(kt * 32 + krow);
-        vp_next = page_of(kt * 32 + vcol);
-    }
-    for (; kt < end; kt += NW) {
+    struct Keys {
+        u32x4 a[KS], b[KS], v[DT];
+        bool bad;
+    } cur;
+    int kp = 0, vp = 0;  // pages of the tile loaded next
+    auto pages = [&](int kt) {
+        kp = page_of(kt * 32 + krow);
+        vp = page_of(kt * 32 + vcol);
+    };
+    auto load = [&](int kt, Keys& x) __attribute__((always_inline)) {
         const int k0 = kt * 32;
-        int kp = kp_next, vp = vp_next;
-        if (kt + NW < end) {
-            kp_next = page_of(k0 + 32 * NW + krow);
-            vp_next = page_of(k0 + 32 * NW + vcol);
-        }
-        const bool vbad = uint32_t(vp) >= uint32_t(a.n_pages);
-        if (uint32_t(kp) >= uint32_t(a.n_pages)) kp = 0;
-        if (vbad) vp = 0;
+        x.bad = uint32_t(vp) >= uint32_t(a.n_pages);
+        const int kq = uint32_t(kp) >= uint32_t(a.n_pages) ? 0 : kp, vq = x.bad ? 0 : vp;
         const uint16_t* kr = a.kc +
-            (((int64_t(kp) * a.kv_heads + hk) << a.shift) + ((k0 + krow) & P1) + (lr & 3)) * D;
-        const uint16_t* vr = a.vc +
-            ((int64_t(vp) * a.kv_heads + hk) * D << a.shift) + ((k0 + vcol) & P1);
-        u32x4 ka[KS], kb[KS], vf[DT];
+            (((int64_t(kq) * a.kv_heads + hk) << a.shift) + ((k0 + krow) & P1) + (lr & 3)) * D;
+        const uint16_t* vr = a.vc + ((int64_t(vq) * a.kv_heads + hk) * D << a.shift) + ((k0 + vcol) & P1);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             // columns behind D meet zeros of the query: any finite chunk will do
             const int at = FULL || 32 * s + 8 * g < D ? 32 * s + 8 * g : 0;
-            ka[s] = *reinterpret_cast<const u32x4*>(kr + at);
-            kb[s] = *reinterpret_cast<const u32x4*>(kr + 4 * D + at);
+            x.a[s] = *reinterpret_cast<const u32x4*>(kr + at);
+            x.b[s] = *reinterpret_cast<const u32x4*>(kr + 4 * D + at);
         }
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
             const int d = 16 * dt + lr;
-            vf[dt] = *reinterpret_cast<const u32x4*>(vr + (int64_t(FULL ? d : min(d, D - 1)) << a.shift));
+            x.v[dt] = *reinterpret_cast<const u32x4*>(vr + (int64_t(FULL ? d : min(d, D - 1)) << a.shift));
         }
-        const bool edge = k0 < t.full_lo || k0 + 31 > t.full_hi || __any(vbad);
+    };
+    auto compute = [&](int kt, Keys& x) __attribute__((always_inline)) {
+        const int k0 = kt * 32, key = k0 + vcol;
+        const bool edge = k0 < t.full_lo || k0 + 31 > t.full_hi || __any(x.bad);
+        f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            sa = E::mfma16(x.a[s], qf[s], sa);
+            sb = E::mfma16(x.b[s], qf[s], sb);
+        }
         if (edge) {
             // values that no row may see can be anything in memory: make them zero
-            const int k = k0 + vcol;
             u32x4 keep;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool x = !vbad && k + 2 * j >= t.kmin && k + 2 * j <= t.kmax;
-                const bool z = !vbad && k + 2 * j + 1 >= t.kmin && k + 2 * j + 1 <= t.kmax;
-                keep[j] = (x ? 0xFFFFu : 0u) | (z ? 0xFFFF0000u : 0u);
+                const bool y = !x.bad & (key + 2 * j >= t.kmin) & (key + 2 * j <= t.kmax);
+                const bool z = !x.bad & (key + 2 * j + 1 >= t.kmin) & (key + 2 * j + 1 <= t.kmax);
+                keep[j] = (y ? 0xFFFFu : 0u) | (z ? 0xFFFF0000u : 0u);
+                if (x.bad | (key + j > hi) | (key + j < lo)) sa[j] = kNegInf;
+                if (x.bad | (key + 4 + j > hi) | (key + 4 + j < lo)) sb[j] = kNegInf;
             }
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) vf[dt] &= keep;
+            for (int dt = 0; dt < DT; ++dt) x.v[dt] &= keep;
         }
+        float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
+                         fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (__any(mx > m)) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = __builtin_amdgcn_exp2f((m - (mn == kNegInf ? 0.f : mn)) * c);
+            m = mn;
+            l *= alpha;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+            for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
+        }
+        const float mc = (m == kNegInf ? 0.f : m * c) - kBias<E>;
+        float p[8];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                sa = E::mfma16(ka[s], qf[b][s], sa);
-                sb = E::mfma16(kb[s], qf[b][s], sb);
-            }
-            if (edge) {
-                const int k = k0 + vcol;
+        for (int j = 0; j < 4; ++j) {
+            p[j] = __builtin_amdgcn_exp2f(fmaf(sa[j], c, -mc));
+            p[4 + j] = __builtin_amdgcn_exp2f(fmaf(sb[j], c, -mc));
+        }
+        l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        // the probabilities as matrix-core operands: one rounding to the type of the values
+        const u32x4 pf = {pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3]), pack16<E>(p[4], p[5]),
+                          pack16<E>(p[6], p[7])};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (vbad || k + j > hi[b] || k + j < lo[b]) sa[j] = kNegInf;
-                    if (vbad || k + 4 + j > hi[b] || k + 4 + j < lo[b]) sb[j] = kNegInf;
-                }
-            }
-            float mx = fmaxf(fmaxf(fmaxf(sa[0], sa[1]), fmaxf(sa[2], sa[3])),
-                             fmaxf(fmaxf(sb[0], sb[1]), fmaxf(sb[2], sb[3])));
-            mx = fmaxf(mx, __shfl_xor(mx, 16));
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            if (__any(mx > m[b])) {
-                const float mn = fmaxf(m[b], mx);
-                const float alpha = __builtin_amdgcn_exp2f((m[b] - (mn == kNegInf ? 0.f : mn)) * c);
-                m[b] = mn;
-                l[b] *= alpha;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) o[b][dt] *= alpha;
-            }
-            const float mc = (m[b] == kNegInf ? 0.f : m[b] * c) - kBias<E>;
-            float p[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(fmaf(sa[j], c, -mc));
-                p[4 + j] = __builtin_amdgcn_exp2f(fmaf(sb[j], c, -mc));
-            }
-            l[b] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-            // the probabilities as matrix-core operands: one rounding to the type of the values
-            const u32x4 pf = {pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3]), pack16<E>(p[4], p[5]),
-                              pack16<E>(p[6], p[7])};
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) o[b][dt] = E::mfma16(vf[dt], pf, o[b][dt]);
+        for (int dt = 0; dt < DT; ++dt) o[dt] = E::mfma16(x.v[dt], pf, o[dt]);
+    };
+    int kt = begin + wave;
+    if (kt < end) {
+        // tiles behind the last one are the last again
+        auto clip = [&](int k) { return min(k, end - 1); };
+        pages(kt);
+        for (; kt < end; kt += NW) {
+            load(kt, cur);
+            pages(clip(kt + NW));
+            compute(kt, cur);
         }
     }
 
     // join the waves
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        l[b] += __shfl_xor(l[b], 16);
-        l[b] += __shfl_xor(l[b], 32);
-        if (g == 0) {
-            mlbuf[wave][16 * b + lr][0] = m[b];
-            mlbuf[wave][16 * b + lr][1] = l[b];
-        }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        mlbuf[wave][lr][0] = m;
+        mlbuf[wave][lr][1] = l;
     }
-    constexpr int TPR = NW * 64 / 16;  // threads per row
+    constexpr int TPR = NW * 64 / MT;  // threads per row
     const int jr = threadIdx.x / TPR, jt = threadIdx.x % TPR;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int d0 = 0; d0 < DP; d0 += DC) {
+        __syncthreads();
 #pragma unroll
-        for (int d0 = 0; d0 < DP; d0 += DC) {
-            __syncthreads();
+        for (int dt = 0; dt < DC / 16; ++dt)
+            *reinterpret_cast<f32x4*>(&obuf[wave][lr][16 * dt + 4 * g]) = o[d0 / 16 + dt];
+        __syncthreads();
+        const int i = (t.rho0 + jr) / a.g;
+        if (i >= t.n) continue;
+        float mm = kNegInf;
 #pragma unroll
-            for (int dt = 0; dt < DC / 16; ++dt)
-                *reinterpret_cast<f32x4*>(&obuf[wave][lr][16 * dt + 4 * g]) = o[b][d0 / 16 + dt];
-            __syncthreads();
-            const int rho = t.rho0 + 16 * b + jr;
-            const int i = rho / a.g, hh = rho - i * a.g;
-            if (i >= t.n) continue;
-            float mm = kNegInf;
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mlbuf[w][jr][0]);
+        const float ms = mm == kNegInf ? 0.f : mm;
+        float wt[NW], sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mlbuf[w][16 * b + jr][0]);
-            const float ms = mm == kNegInf ? 0.f : mm;
-            float wt[NW], sum = 0.f;
+        for (int w = 0; w < NW; ++w) {
+            wt[w] = __builtin_amdgcn_exp2f((mlbuf[w][jr][0] - ms) * c);
+            sum = fmaf(wt[w], mlbuf[w][jr][1], sum);
+        }
+        const int head = hk * a.g + t.rho0 + jr - i * a.g;
+        const int64_t rowi = int64_t(t.c0 + i) * a.heads + head;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+        for (int d = jt * 4; d < DC && d0 + d < D; d += TPR * 4) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                wt[w] = __builtin_amdgcn_exp2f((mlbuf[w][16 * b + jr][0] - ms) * c);
-                sum = fmaf(wt[w], mlbuf[w][16 * b + jr][1], sum);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&obuf[w][jr][d]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(wt[w], x[j], v[j]);
             }
-            const int head = hk * a.g + hh;
-            const int64_t rowi = int64_t(t.c0 + i) * a.heads + head;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-            for (int d = jt * 4; d < DC && d0 + d < D; d += TPR * 4) {
-                f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const f32x4 x = *reinterpret_cast<const f32x4*>(&obuf[w][jr][d]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = fmaf(wt[w], x[j], v[j]);
-                }
-                if (a.nsplit == 1) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] *= inv;
-                    u32x2 w2 = {pack16<E>(v[0], v[1]), pack16<E>(v[2], v[3])};
-                    *reinterpret_cast<u32x2*>(a.y + (t.c0 + i) * a.ld_y + int64_t(head) * D + d0 + d) = w2;
-                } else {
-                    *reinterpret_cast<f32x4*>(a.opart + (rowi * a.nsplit + split) * D + d0 + d) = v;
-                }
+            if (a.nsplit == 1) {
+                const u32x2 w2 = {pack16<E>(v[0] * inv, v[1] * inv), pack16<E>(v[2] * inv, v[3] * inv)};
+                *reinterpret_cast<u32x2*>(a.y + (t.c0 + i) * a.ld_y + int64_t(head) * D + d0 + d) = w2;
+            } else {
+                *reinterpret_cast<f32x4*>(a.opart + (rowi * a.nsplit + split) * D + d0 + d) = v;
             }
-            if (d0 == 0 && jt == 0) {
-                if (a.nsplit > 1) {
-                    a.ml[(rowi * a.nsplit + split) * 2] = mm;
-                    a.ml[(rowi * a.nsplit + split) * 2 + 1] = sum;
-                } else if (a.lse) {
-                    a.lse[rowi] = sum == 0.f ? kNegInf
-                                             : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
-                }
+        }
+        if (d0 == 0 && jt == 0) {
+            if (a.nsplit > 1) {
+                a.ml[(rowi * a.nsplit + split) * 2] = mm;
+                a.ml[(rowi * a.nsplit + split) * 2 + 1] = sum;
+            } else if (a.lse) {
+                a.lse[rowi] = sum == 0.f ? kNegInf
+                                         : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
             }
         }
     }
@@ -278,12 +259,16 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 // ---------------------------------------------------------------- host half
 
 struct AttnGeom {
-    int nb;         // register tiles: blocks of 16 rows
-    bool lds;       // tiles of kAttnTileRows with the keys in LDS, otherwise register tiles
+    bool lds;       // tiles of kAttnTileRows with the keys in LDS, otherwise register tiles of 16 rows
     int tiles, nsplit, split_tiles;
     size_t opart, ml, bytes;
 };
 
+// Up to 16 rows of D > 128 take register tiles: their 64 KB tiles leave the LDS kernel one workgroup a
+// compute unit, which cannot hide the cache's latency (32 requests of up to 8,000 keys, 24/4 heads of
+// 256: 123 against 184 us).  Everything else takes LDS tiles: 64 requests of one token, D = 64: 416
+// against 467 us; 8 tokens over 65,472 keys, 40/8 heads of 128: 64 against 144 us, 24/4 heads of 256:
+// 80 against 218 us.
 AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     AttnGeom G{};
     const int g = d.heads / d.kv_heads;
@@ -291,38 +276,35 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
     const int keys = std::max(1, d.max_kv);
-    G.lds = rows > (getenv("ATTN_MIN") ? atoi(getenv("ATTN_MIN")) : 64) && (all / kAttnTileRows + d.R + 1) * d.kv_heads * kMaxSplit < (1 << 24);
-    int mt, key_tiles;
-    if (G.lds) {
-        mt = kAttnTileRows;
-        key_tiles = (keys + 63) / 64;
-    } else {
-        const int most = d.D > 128 ? 2 : 4;
-        G.nb = int(std::min<int64_t>(most, (rows + 15) / 16));
-        if (G.nb == 3) G.nb = 4;
-        mt = 16 * G.nb;
-        key_tiles = (keys + 31) / 32;
-    }
+    G.lds = d.D <= 128 || rows > 16;
+    const int mt = G.lds ? kAttnTileRows : 16, key_tile = G.lds ? 64 : 32;
+    const int key_tiles = (keys + key_tile - 1) / key_tile;
     G.tiles = int(all / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
     if (G.lds) {
-        // The time in passes over a 64-key tile (2.4 us at D = 128 with two workgroups on every
-        // compute unit): rounds of workgroups, two tiles' worth to start and end each, and the join,
-        // which writes and reads FP32 sums at about 4 TB/s.  512 rows of 40/8 heads of 128 over
-        // 33,001 keys: 436 us with the three splits that this chooses, 539 / 477 / 453 / 457 with
-        // 2 / 4 / 6 / 8.
+        // Times in us.  A workgroup passes over a tile in 1 us and 0.35 more for each wave with rows (D =
+        // 128), if all of them together stay below 5 TB/s of keys and values (which the row tiles of a
+        // request share); two tiles' worth to start and end each; the join writes and reads FP32 sums
+        // at about 4 TB/s.  512 rows of 40/8 heads of
+        // 128 over 33,001 keys: 436 us with the three splits that this chooses, 539 / 477 / 453 / 457
+        // with 2 / 4 / 6 / 8.  max_kv is the longest of several requests: half of the estimate is for
+        // all being as long, half for that one alone.
         const int64_t slots = int64_t(cus) * (d.D <= 128 ? 2 : 1);
-        const double tile = 2.4e-6 * d.D / 128;
+        const double alone = (1.0 + 0.35 * double(std::min<int64_t>(4, (rows + 31) / 32))) * d.D / 128;
         G.nsplit = 1;
         double best = 1e300;
-        if (getenv("ATTN_NS")) G.nsplit = atoi(getenv("ATTN_NS")); else
         for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
-            const double rounds = double((active * ns + slots - 1) / slots);
-            const double join = ns > 1 ? (4e-6 + ns * double(rows_all) * d.D * 8 / 4e12) / tile : 0;
-            const double cost = rounds * ((key_tiles + ns - 1) / ns + 2) + join;
+            const int64_t blocks = active * ns;
+            const int64_t busy = std::min((blocks + cus - 1) / cus * cus, slots);  // as full as the fullest
+            const double tile = std::max(alone, double(busy) * key_tile * d.D * 4 / 5e6 * d.R * d.kv_heads / active);
+            const double tiles = (key_tiles + ns - 1) / ns + 2;
+            double cost = double((blocks + slots - 1) / slots) * tiles * tile;
+            if (d.R > 1) cost = 0.5 * cost + 0.5 * tiles * alone;
+            if (ns > 1) cost += 4 + ns * double(rows_all) * d.D * 8 / 4e6;
             if (cost < best) best = cost, G.nsplit = ns;
         }
     } else {
+        // four workgroups a compute unit: 123 us at the sizes above, 127 / 130 / 147 with 3 / 6 / 12
         const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
         const int most_split = std::max(1, key_tiles / 8);
         G.nsplit = int(std::min<int64_t>(std::min<int64_t>(want, most_split), kMaxSplit));
@@ -356,36 +338,23 @@ vqmlp_status attn_check(const vqmlp_attn_desc* p, const char* who, int* shift) {
         OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: heads / kv_heads above 64 or R above 65536", who);
     if (int64_t(d.T) * d.heads > 0x3FFFFFFF)
         OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: T * heads above 2^30 - 1", who);
+    // workgroups of any split: a launch holds fewer than 2^32 threads
+    if ((int64_t(d.T) * (d.heads / d.kv_heads) / kAttnTileRows + d.R + 1) * d.kv_heads > (1 << 24))
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: (T * heads / 128 + R * kv_heads) above 2^24", who);
     OP_REQUIRE((int64_t(d.n_pages) << *shift) <= 0x7FFFFFFF && (int64_t(d.table_width) << *shift) <= 0x3FFFFFFF,
                "%s: slots pass 2^31 - 1 or positions 2^30 - 1", who);
     OP_REQUIRE(d.scale > 0.f && d.scale < __builtin_inff(), "%s: scale is not positive and finite", who);
     return VQMLP_OK;
 }
 
-template <class E, int DP, int NB>
-void launch_wave_nb(const AttnArgs& a, int tiles, hipStream_t s) {
-    const dim3 grid(tiles, a.kv_heads, a.nsplit);
-    if (a.D == DP)
-        k_attn_wave<E, DP, NB, true, 4><<<grid, 256, 0, s>>>(a);
-    else
-        k_attn_wave<E, DP, NB, false, 4><<<grid, 256, 0, s>>>(a);
-}
-
 template <class E>
 void launch_attn(const AttnArgs& a, const AttnGeom& G, int dtype, hipStream_t s) {
     if (G.lds) {
         launch_attn_tile(a, dtype, G.tiles, s);
-    } else if (a.D <= 64) {
-        if (G.nb == 1) launch_wave_nb<E, 64, 1>(a, G.tiles, s);
-        else if (G.nb == 2) launch_wave_nb<E, 64, 2>(a, G.tiles, s);
-        else launch_wave_nb<E, 64, 4>(a, G.tiles, s);
-    } else if (a.D <= 128) {
-        if (G.nb == 1) launch_wave_nb<E, 128, 1>(a, G.tiles, s);
-        else if (G.nb == 2) launch_wave_nb<E, 128, 2>(a, G.tiles, s);
-        else launch_wave_nb<E, 128, 4>(a, G.tiles, s);
     } else {
-        if (G.nb == 1) launch_wave_nb<E, 256, 1>(a, G.tiles, s);
-        else launch_wave_nb<E, 256, 2>(a, G.tiles, s);
+        const dim3 grid(G.tiles, a.kv_heads, a.nsplit);
+        if (a.D == 256) k_attn_wave<E, true><<<grid, 256, 0, s>>>(a);
+        else k_attn_wave<E, false><<<grid, 256, 0, s>>>(a);
     }
     if (a.nsplit > 1) {
         const int64_t rows = int64_t(a.T) * a.heads;
@@ -467,7 +436,7 @@ extern "C" vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc* p, void* workspa
     else launch_attn<BF16>(a, G, d.dtype, s);
     if (trace_enabled())
         trace_line("paged_attn T=%d R=%d heads=%d/%d D=%d: %s tiles, %d rows, %d key splits%s", d.T, d.R,
-                   d.heads, d.kv_heads, d.D, G.lds ? "LDS" : "register", G.lds ? kAttnTileRows : 16 * G.nb,
+                   d.heads, d.kv_heads, d.D, G.lds ? "LDS" : "register", G.lds ? kAttnTileRows : 16,
                    G.nsplit, G.nsplit > 1 ? " + join" : "");
     return op_launched("vqmlp_paged_attn");
 }
