@@ -477,27 +477,43 @@ class VQ2Projection:
 # the caller did not pass on the call's stream, and enqueues.
 
 
+# A call of these costs the host less than the launch that it makes, where it can: a step has dozens of
+# them.  Checks take the usual case first, and descriptions start as copies of what does not change.
+
+
 class _OnStream:
     """The stream of a call and the context in which its temporaries are allocated: memory comes
     from that stream's pool, so it cannot be handed to another stream while the call runs."""
+
+    __slots__ = ("raw", "stream", "device")
 
     def __init__(self, stream, device):
         import torch
 
         if device.type != "cuda":
             _bad("tensors are on %s, not on a GPU" % device)
-        if stream is None:
-            self.raw, self.ctx = torch.cuda.current_stream(device).cuda_stream, None
-        else:
-            self.raw, self.ctx = stream.cuda_stream, torch.cuda.stream(stream)
+        self.device, self.stream = device, stream
+        self.raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
-    def empty(self, shape, dtype, device):
+    def empty(self, shape, dtype):
         import torch
 
-        if self.ctx is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with self.ctx:
-            return torch.empty(shape, dtype=dtype, device=device)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def call(self, f, *args):
+        """f(*args, stream) with the tensors' device current."""
+        import torch
+
+        if torch._C._cuda_getDevice() == self.device.index:
+            status = f(*args, self.raw)
+        else:
+            with torch.cuda.device(self.device):
+                status = f(*args, self.raw)
+        if status != OK:
+            _check(status)
 
 
 def _bad(msg):
@@ -526,7 +542,7 @@ def _need(t, name, device, dtype=None, shape=None, contiguous=True):
         _bad("%s is on %s, not on %s" % (name, t.device, device))
     if dtype is not None and t.dtype != dtype:
         _bad("%s is %s, not %s" % (name, t.dtype, dtype))
-    if shape is not None and (t.dim() != len(shape) or any(
+    if shape is not None and t.shape != shape and (t.dim() != len(shape) or any(
             s is not None and s != n for s, n in zip(shape, t.shape))):
         _bad("%s has shape %s, wanted %s" % (name, tuple(t.shape), shape))
     if contiguous and not t.is_contiguous():
@@ -536,23 +552,31 @@ def _need(t, name, device, dtype=None, shape=None, contiguous=True):
 
 def _rows(t, name, device, shape):
     """Pointer and token stride of [T, heads, D] (or [T, H]) whose rows are dense."""
-    _need(t, name, device, None, shape, contiguous=False)
-    inner = 1
+    if t.device != device or t.shape != shape:
+        _need(t, name, device, None, shape, contiguous=False)
+    inner = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), inner
+    at = 1
     for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and st != inner:
+        if n != 1 and st != at:
             _bad("%s: a token's elements do not lie one after another" % name)
-        inner *= n
+        at *= n
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
 
 
-def _work_ptr(workspace, nbytes, where, device):
+def _work(on, workspace, nbytes):
+    """Pointer and size of a call's workspace: the caller's, or a new one on the call's stream (held
+    by the third value until the call has been enqueued)."""
     import torch
 
     if workspace is None:
-        return where.empty((nbytes,), torch.uint8, device) if nbytes else None
-    if workspace.device != device or not workspace.is_contiguous():
-        _bad("workspace: not contiguous, or not on %s" % device)
-    return workspace
+        if not nbytes:
+            return None, 0, None
+        workspace = on.empty((nbytes,), torch.uint8)
+    elif workspace.device != on.device or not workspace.is_contiguous():
+        _bad("workspace: not contiguous, or not on %s" % on.device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 class BlockNorm:
@@ -571,19 +595,17 @@ class BlockNorm:
             _bad("a bias needs its weight")
         self._keep = [w for w in ws.values() if w is not None]
         self.has_pre, self.has_post = pre_weight is not None, post_weight is not None
-        self._desc = dict(kind=self.KINDS[kind], eps=eps, res_scale=residual_scale,
-                          w_offset=weight_offset)
+        self._desc = _NormDesc(kind=self.KINDS[kind], eps=eps, res_scale=residual_scale,
+                               w_offset=weight_offset)
         for name, w in ws.items():
             if w is not None:
-                self._desc[name] = _need(w, name, self._keep[0].device, self._keep[0].dtype,
-                                         (self._keep[0].shape[0],))
+                setattr(self._desc, name, _need(w, name, self._keep[0].device, self._keep[0].dtype,
+                                                (self._keep[0].shape[0],)))
 
     def forward(self, y, residual=None, gate=None, residual_out=None, out=None, stream=None):
         """y [T, H] (None: only the norm of residual), residual [T, H] of y's type or float32, gate
         [T, H] or [H] -> (r of residual's type, x of y's type; None without pre_weight).
         residual_out may be residual and out may be y."""
-        import torch
-
         base = y if y is not None else residual
         if base is None:
             _bad("neither y nor residual")
@@ -592,47 +614,48 @@ class BlockNorm:
             _bad("y and residual are [T, H]")
         T, H = shape
         x_dtype = y.dtype if y is not None else self._keep[0].dtype if self._keep else residual.dtype
-        if self._keep and (self._keep[0].shape[0] != H or self._keep[0].device != dev or
-                           _dtype(self._keep[0], "weight") != _DTYPES.get(x_dtype)):
-            _bad("the weights do not fit y (H, type or device)")
+        if self._keep:
+            w = self._keep[0]
+            if w.shape[0] != H or w.device != dev or _dtype(w, "weight") != _DTYPES.get(x_dtype):
+                _bad("the weights do not fit y (H, type or device)")
         if y is None and self.has_post:
             _bad("post_weight without y")
-        d = _NormDesc(T=T, H=H, **self._desc)
+        d = _NormDesc.from_buffer_copy(self._desc)
+        d.T, d.H = T, H
         on = _OnStream(stream, dev)
         if y is not None:
-            d.dtype = _dtype(y, "y")
+            kind = _dtype(y, "y")
             d.y, d.ld_y = _rows(y, "y", dev, shape)
         else:
-            d.dtype = _DTYPES[x_dtype] if self._keep else _dtype(residual, "residual")
+            kind = _DTYPES[x_dtype] if self._keep else _dtype(residual, "residual")
+        d.dtype = res_kind = kind
         if residual is not None:
-            d.res_dtype = _dtype(residual, "residual")
+            res_kind = _dtype(residual, "residual")
             d.res, d.ld_res = _rows(residual, "residual", dev, shape)
         elif residual_out is not None:
-            d.res_dtype = _dtype(residual_out, "residual_out")
-        else:
-            d.res_dtype = d.dtype
+            res_kind = _dtype(residual_out, "residual_out")
+        d.res_dtype = res_kind
         if gate is not None:
-            if _dtype(gate, "gate") != d.dtype:
+            if _dtype(gate, "gate") != kind:
                 _bad("gate and y differ in type")
             if gate.dim() == 1:
                 d.gate, d.ld_gate = _need(gate, "gate", dev, None, (H,)), 0
             else:
                 d.gate, d.ld_gate = _rows(gate, "gate", dev, shape)
         if residual_out is None:
-            residual_out = on.empty(shape, residual.dtype if residual is not None else x_dtype, dev)
-        elif _dtype(residual_out, "residual_out") != d.res_dtype:
+            residual_out = on.empty(shape, residual.dtype if residual is not None else x_dtype)
+        elif _dtype(residual_out, "residual_out") != res_kind:
             _bad("residual_out and residual differ in type")
         d.res_out, d.ld_res_out = _rows(residual_out, "residual_out", dev, shape)
         if self.has_pre:
             if out is None:
-                out = on.empty(shape, x_dtype, dev)
-            elif _dtype(out, "out") != d.dtype:
+                out = on.empty(shape, x_dtype)
+            elif _dtype(out, "out") != kind:
                 _bad("out and y differ in type")
             d.x, d.ld_x = _rows(out, "out", dev, shape)
         elif out is not None:
             _bad("out without pre_weight")
-        with torch.cuda.device(dev):
-            _check(lib().vqmlp_block_norm(C.byref(d), on.raw))
+        on.call(lib().vqmlp_block_norm, C.byref(d))
         return residual_out, out
 
 
@@ -661,40 +684,45 @@ class PagePlanner:
         self.R, self.device, self.max_tokens = table.shape[0], dev, max_tokens
         self.table, self.free_pages, self.free_head = table, free_pages, free_head
         self.page_size, self.n_pages = page_size, n_pages
-        self._desc = dict(R=self.R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
-                          n_free=free_pages.numel(), table_width=table.shape[1],
-                          ld_table=table.stride(0) if self.R > 1 else table.shape[1],
-                          free_pages=_need(free_pages, "free_pages", dev, torch.int32, (None,)),
-                          table=table.data_ptr())
+        self._desc = _PagesDesc(R=self.R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
+                                n_free=free_pages.numel(), table_width=table.shape[1],
+                                ld_table=table.stride(0) if self.R > 1 else table.shape[1],
+                                free_pages=_need(free_pages, "free_pages", dev, torch.int32, (None,)),
+                                table=table.data_ptr())
         if free_head is not None:
-            self._desc["free_head"] = _need(free_head, "free_head", dev, torch.int32, (1,))
+            self._desc.free_head = _need(free_head, "free_head", dev, torch.int32, (1,))
 
     def empty_plan(self, stream=None):
+        return self._empty_plan(_OnStream(stream, self.device))
+
+    def _empty_plan(self, on):
         import torch
 
-        on, i = _OnStream(stream, self.device), torch.int32
-        return PagePlan(*(on.empty((n,), i, self.device) for n in (
-            self.R, self.R + 1, self.max_tokens, self.max_tokens, 4)))
+        sizes = [self.R, self.R + 1, self.max_tokens, self.max_tokens, 4]
+        return PagePlan(*on.empty((sum(sizes),), torch.int32).split(sizes))
 
     def forward(self, ctx_len, q_len, plan=None, free_head_out=None, stream=None):
         """ctx_len, q_len [R] int32 on the device -> PagePlan (plan: buffers to reuse)."""
         import torch
 
         i, dev = torch.int32, self.device
-        d = _PagesDesc(**self._desc)
+        d = _PagesDesc.from_buffer_copy(self._desc)
         d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (self.R,))
         d.q_len = _need(q_len, "q_len", dev, i, (self.R,))
+        on = _OnStream(stream, dev)
         if plan is None:
-            plan = self.empty_plan(stream)
-        d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self.R,))
-        d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self.R + 1,))
-        d.slot = _need(plan.slot, "slot", dev, i, (self.max_tokens,))
-        d.position = _need(plan.position, "position", dev, i, (self.max_tokens,))
-        d.status = _need(plan.status, "status", dev, i, (4,))
+            plan = self._empty_plan(on)
+            d.seq_len, d.cu_q, d.slot, d.position, d.status = (
+                x.data_ptr() for x in (plan.seq_len, plan.cu_q, plan.slot, plan.position, plan.status))
+        else:
+            d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self.R,))
+            d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self.R + 1,))
+            d.slot = _need(plan.slot, "slot", dev, i, (self.max_tokens,))
+            d.position = _need(plan.position, "position", dev, i, (self.max_tokens,))
+            d.status = _need(plan.status, "status", dev, i, (4,))
         if free_head_out is not None:
             d.free_head_out = _need(free_head_out, "free_head_out", dev, i, (1,))
-        with torch.cuda.device(dev):
-            _check(lib().vqmlp_page_plan(C.byref(d), _OnStream(stream, dev).raw))
+        on.call(lib().vqmlp_page_plan, C.byref(d))
         return plan
 
 
@@ -709,6 +737,8 @@ class PagedCache:
         self.k, self.v, self.device = k, v, k.device
         self.n_pages, self.kv_heads, self.page_size, self.D = n, h, p, D
         self.dtype = _dtype(k, "k")
+        self._kp, self._vp = k.data_ptr(), v.data_ptr()
+        self._work = {}  # workspace bytes of a description's sizes
 
     @classmethod
     def empty(cls, n_pages, kv_heads, page_size, D, dtype, device="cuda"):
@@ -730,23 +760,31 @@ class PagedCache:
         sp = _need(slot, "slot", dev, torch.int32, (None,))
         if slot.shape[0] < T:
             _bad("slot has %d entries for %d tokens" % (slot.shape[0], T))
-        with torch.cuda.device(dev):
-            _check(lib().vqmlp_paged_store(self.dtype, T, self.kv_heads, self.D, self.page_size,
-                                           self.n_pages, kp, ld_k, vp, ld_v, sp,
-                                           self.k.data_ptr(), self.v.data_ptr(),
-                                           _OnStream(stream, dev).raw))
+        _OnStream(stream, dev).call(lib().vqmlp_paged_store, self.dtype, T, self.kv_heads, self.D,
+                                    self.page_size, self.n_pages, kp, ld_k, vp, ld_v, sp, self._kp,
+                                    self._vp)
 
     def _attn_desc(self, T, R, heads, table_width, window, max_kv, scale):
-        return _AttnDesc(dtype=self.dtype, T=T, R=R, heads=heads, kv_heads=self.kv_heads, D=self.D,
-                         page_size=self.page_size, n_pages=self.n_pages, window=window,
-                         max_kv=table_width * self.page_size if max_kv is None else max_kv,
-                         scale=self.D ** -0.5 if scale is None else scale, table_width=table_width)
+        return _AttnDesc(self.dtype, T, R, heads, self.kv_heads, self.D, self.page_size, self.n_pages,
+                         window, table_width * self.page_size if max_kv is None else max_kv,
+                         self.D ** -0.5 if scale is None else scale, table_width)
+
+    def _work_bytes(self, d):
+        key = (d.T, d.R, d.heads, d.max_kv, d.table_width)
+        n = self._work.get(key)
+        if n is None:
+            import torch
+
+            n = C.c_size_t()
+            with torch.cuda.device(self.device):
+                _check(lib().vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
+            if len(self._work) >= 4096:
+                self._work.clear()
+            n = self._work[key] = n.value
+        return n
 
     def workspace_bytes(self, T, R, heads, table_width, max_kv=None):
-        n = C.c_size_t()
-        d = self._attn_desc(T, R, heads, table_width, 0, max_kv, None)
-        _check(lib().vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
-        return n.value
+        return self._work_bytes(self._attn_desc(T, R, heads, table_width, 0, max_kv, None))
 
     def attention(self, q, table, cu_q, kv_len, *, scale=None, window=0, max_kv=None, y=None,
                   lse=None, with_lse=False, workspace=None, stream=None):
@@ -769,25 +807,20 @@ class PagedCache:
         d = self._attn_desc(T, R, heads, table.shape[1], window, max_kv, scale)
         d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self.D))
         if y is None:
-            y = on.empty((T, heads, self.D), q.dtype, dev)
+            y = on.empty((T, heads, self.D), q.dtype)
         elif _dtype(y, "y") != self.dtype:
             _bad("y and the cache differ in type")
         d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self.D))
         if lse is None and with_lse:
-            lse = on.empty((T, heads), torch.float32, dev)
+            lse = on.empty((T, heads), torch.float32)
         if lse is not None:
             d.lse = _need(lse, "lse", dev, torch.float32, (T, heads))
-        d.k_cache, d.v_cache = self.k.data_ptr(), self.v.data_ptr()
+        d.k_cache, d.v_cache = self._kp, self._vp
         d.table, d.ld_table = table.data_ptr(), table.stride(0) if R > 1 else table.shape[1]
         d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
         d.kv_len = _need(kv_len, "kv_len", dev, i, (R,))
-        L = lib()
-        with torch.cuda.device(dev):
-            n = C.c_size_t()
-            _check(L.vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
-            work = _work_ptr(workspace, n.value, on, dev)
-            _check(L.vqmlp_paged_attn(C.byref(d), None if work is None else work.data_ptr(),
-                                      0 if work is None else work.numel() * work.element_size(), on.raw))
+        work, nbytes, _hold = _work(on, workspace, self._work_bytes(d))
+        on.call(lib().vqmlp_paged_attn, C.byref(d), work, nbytes)
         return y if lse is None else (y, lse)
 
 
@@ -798,6 +831,7 @@ class LinearAttention:
     def __init__(self, k_heads, v_heads, Dk, Dv, scale=None):
         self.k_heads, self.v_heads, self.Dk, self.Dv = k_heads, v_heads, Dk, Dv
         self.scale = Dk ** -0.5 if scale is None else scale
+        self._work = {}  # workspace bytes of (device, T, R, max_q)
 
     def state(self, n, device="cuda"):
         """Zero states for n requests."""
@@ -805,12 +839,27 @@ class LinearAttention:
 
         return torch.zeros((n, self.v_heads, self.Dk, self.Dv), dtype=torch.float32, device=device)
 
+    def _desc(self, dtype, T, R, n_states, max_q):
+        return _LinearDesc(dtype, T, R, self.k_heads, self.v_heads, self.Dk, self.Dv, n_states, max_q,
+                           self.scale)
+
     def workspace_bytes(self, T, R, max_q):
         n = C.c_size_t()
-        d = _LinearDesc(dtype=0, T=T, R=R, k_heads=self.k_heads, v_heads=self.v_heads, Dk=self.Dk,
-                        Dv=self.Dv, max_q=max_q, scale=self.scale)
-        _check(lib().vqmlp_linear_attn_workspace(C.byref(d), C.byref(n)))
+        _check(lib().vqmlp_linear_attn_workspace(C.byref(self._desc(0, T, R, 0, max_q)), C.byref(n)))
         return n.value
+
+    def _work_bytes(self, d, device):
+        key = (device.index, d.T, d.R, d.max_q)
+        n = self._work.get(key)
+        if n is None:
+            import torch
+
+            with torch.cuda.device(device):
+                n = self.workspace_bytes(d.T, d.R, d.max_q)
+            if len(self._work) >= 4096:
+                self._work.clear()
+            self._work[key] = n
+        return n
 
     def forward(self, q, k, v, g, state, cu_q, *, ctx_len=None, state_index=None, state_out=None,
                 max_q=None, y=None, workspace=None, stream=None):
@@ -828,28 +877,27 @@ class LinearAttention:
         if _dtype(k, "k") != dt or _dtype(v, "v") != dt:
             _bad("q, k and v differ in type")
         on = _OnStream(stream, dev)
-        d = _LinearDesc(dtype=dt, T=T, R=R, k_heads=self.k_heads, v_heads=self.v_heads, Dk=self.Dk,
-                        Dv=self.Dv, n_states=state.shape[0], max_q=T if max_q is None else max_q,
-                        scale=self.scale)
+        d = self._desc(dt, T, R, state.shape[0], T if max_q is None else max_q)
         d.q, d.ld_q = _rows(q, "q", dev, (T, self.k_heads, self.Dk))
         d.k, d.ld_k = _rows(k, "k", dev, (T, self.k_heads, self.Dk))
         d.v, d.ld_v = _rows(v, "v", dev, (T, self.v_heads, self.Dv))
-        _need(g, "g", dev, f, (T, self.v_heads), contiguous=False)
+        if g.dtype != f:
+            _bad("g is %s, not %s" % (g.dtype, f))
         d.g, d.ld_g = _rows(g, "g", dev, (T, self.v_heads))
         if y is None:
-            y = on.empty((T, self.v_heads, self.Dv), q.dtype, dev)
+            y = on.empty((T, self.v_heads, self.Dv), q.dtype)
         elif _dtype(y, "y") != dt:
             _bad("y and q differ in type")
         d.y, d.ld_y = _rows(y, "y", dev, (T, self.v_heads, self.Dv))
         shape = (state.shape[0], self.v_heads, self.Dk, self.Dv)
         d.state_in = _need(state, "state", dev, f, shape)
         if state_out is None:
-            state_out = on.empty(shape, f, dev)
+            state_out = on.empty(shape, f)
             if state_index is not None or shape[0] > R:
-                if on.ctx is None:
+                if stream is None:
                     state_out.copy_(state)
                 else:
-                    with on.ctx:
+                    with torch.cuda.stream(stream):
                         state_out.copy_(state)
         d.state_out = _need(state_out, "state_out", dev, f, shape)
         d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
@@ -857,11 +905,6 @@ class LinearAttention:
             d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (R,))
         if state_index is not None:
             d.state_index = _need(state_index, "state_index", dev, i, (R,))
-        L = lib()
-        with torch.cuda.device(dev):
-            n = C.c_size_t()
-            _check(L.vqmlp_linear_attn_workspace(C.byref(d), C.byref(n)))
-            work = _work_ptr(workspace, n.value, on, dev)
-            _check(L.vqmlp_linear_attn(C.byref(d), None if work is None else work.data_ptr(),
-                                       0 if work is None else work.numel() * work.element_size(), on.raw))
+        work, nbytes, _hold = _work(on, workspace, self._work_bytes(d, dev))
+        on.call(lib().vqmlp_linear_attn, C.byref(d), work, nbytes)
         return y, state_out
