@@ -21,20 +21,18 @@ struct NormArgs {
 
 // Sum over the workgroup, in every thread.  Two alternating slots in LDS: a slot is written again
 // only two reductions later, with the barrier of the one between them in front of it.
-template <int NT>
+constexpr int kMaxWaves = 16;
 struct RowSum {
-    float* part;  // [2][NT / 64]
-    int at = 0;
+    float* part;  // [2][kMaxWaves]
+    int waves, at = 0;
     __device__ __forceinline__ float operator()(float v) {
         v = wave_sum(v);
-        if constexpr (NT > 64) {
-            constexpr int NW = NT / 64;
-            float* p = part + at * NW;
+        if (waves > 1) {
+            float* p = part + at * kMaxWaves;
             if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
             __syncthreads();
             v = 0.f;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) v += p[i];
+            for (int i = 0; i < waves; ++i) v += p[i];
             at ^= 1;
         }
         return v;
@@ -79,11 +77,12 @@ __device__ __forceinline__ void store_res8(void* p, int64_t i, const float* f) {
     }
 }
 
-// NT threads, CH chunks of 8 elements each: H <= NT * CH * 8.
-template <class E, bool RES32, int NT, int CH>
-__global__ void __launch_bounds__(NT) k_norm(vqmlp_norm_desc d) {
-    __shared__ float part[2 * (NT / 64)];
-    RowSum<NT> row_sum{part};
+// CH chunks of 8 elements a thread: H <= threads * CH * 8.
+template <class E, bool RES32, int CH>
+__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) k_norm(vqmlp_norm_desc d) {
+    __shared__ float part[2 * kMaxWaves];
+    const int NT = blockDim.x;
+    RowSum row_sum{part, NT / 64};
     const int64_t t = blockIdx.x;
     const int H = d.H;
     const float inv = 1.f / float(H);
@@ -181,8 +180,8 @@ __global__ void __launch_bounds__(NT) k_norm(vqmlp_norm_desc d) {
 // L2 after the first).  Every output element is written by the thread that reads it last.
 template <class E, bool RES32>
 __global__ void __launch_bounds__(256) k_norm_any(vqmlp_norm_desc d) {
-    __shared__ float part[2 * 4];
-    RowSum<256> row_sum{part};
+    __shared__ float part[2 * kMaxWaves];
+    RowSum row_sum{part, 4};
     const int64_t t = blockIdx.x;
     const int H = d.H;
     const float inv = 1.f / float(H);
@@ -234,25 +233,22 @@ __global__ void __launch_bounds__(256) k_norm_any(vqmlp_norm_desc d) {
 }
 
 template <class E, bool RES32>
-const char* launch_norm(const vqmlp_norm_desc& d, bool vec, hipStream_t s) {
-    const dim3 grid(d.T);
+const char* launch_norm(const vqmlp_norm_desc& d, bool vec, int cus, hipStream_t s) {
     const int chunks = d.H / 8;
-#define VQMLP_NORM(NT, CH)                                                     \
-    do {                                                                       \
-        k_norm<E, RES32, NT, CH><<<grid, NT, 0, s>>>(d);                       \
-        return "vector kernel, " #NT " threads x " #CH " chunks";              \
-    } while (0)
     if (!vec || chunks > 2048) {
-        k_norm_any<E, RES32><<<grid, 256, 0, s>>>(d);
+        k_norm_any<E, RES32><<<d.T, 256, 0, s>>>(d);
         return "element kernel";
     }
-    if (chunks <= 64) VQMLP_NORM(64, 1);
-    if (chunks <= 256) VQMLP_NORM(256, 1);
-    if (chunks <= 512) VQMLP_NORM(256, 2);
-    if (chunks <= 768) VQMLP_NORM(256, 3);
-    if (chunks <= 1024) VQMLP_NORM(256, 4);
-    VQMLP_NORM(512, 4);
-#undef VQMLP_NORM
+    // Few rows: latency, so a chunk a thread (8 rows of 5120: 4.1 us in a graph, 4.9 / 5.7 with 2 / 3
+    // chunks).  Many: two (8192 rows of 5120 with gates and an FP32 residual: 120 us, 127 / 126 / 130
+    // with 1 / 3 / 4); from 2 chunks a thread on a workgroup has at most 512 threads.
+    const int ch = chunks > 1024 ? 4 : chunks <= 64 || d.T <= 2 * cus ? 1 : 2;
+    const unsigned nt = unsigned((chunks + 64 * ch - 1) / (64 * ch)) * 64;
+    switch (ch) {
+        case 1: k_norm<E, RES32, 1><<<d.T, nt, 0, s>>>(d); return "vector kernel, 1 chunk a thread";
+        case 2: k_norm<E, RES32, 2><<<d.T, nt, 0, s>>>(d); return "vector kernel, 2 chunks a thread";
+        default: k_norm<E, RES32, 4><<<d.T, nt, 0, s>>>(d); return "vector kernel, 4 chunks a thread";
+    }
 }
 
 }  // namespace
@@ -300,8 +296,8 @@ extern "C" vqmlp_status vqmlp_block_norm(const vqmlp_norm_desc* p, void* stream)
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool r32 = d.res_dtype == VQMLP_F32;
     const char* what =
-        d.dtype == VQMLP_F16 ? (r32 ? launch_norm<F16, true>(d, vec, s) : launch_norm<F16, false>(d, vec, s))
-                             : (r32 ? launch_norm<BF16, true>(d, vec, s) : launch_norm<BF16, false>(d, vec, s));
+        d.dtype == VQMLP_F16 ? (r32 ? launch_norm<F16, true>(d, vec, cus, s) : launch_norm<F16, false>(d, vec, cus, s))
+                             : (r32 ? launch_norm<BF16, true>(d, vec, cus, s) : launch_norm<BF16, false>(d, vec, cus, s));
     if (trace_enabled()) trace_line("block_norm T=%d H=%d: %s", d.T, d.H, what);
     return op_launched("vqmlp_block_norm");
 }
