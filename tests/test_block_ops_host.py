@@ -107,6 +107,7 @@ def _attn(vq, **kw):
     (dict(scale=float("inf")), "scale", 1), (dict(q=None), "null", 1), (dict(kv_len=None), "null", 1),
     (dict(ld_q=376), "at least", 1), (dict(ld_y=388), "multiples of 8", 1), (dict(ld_table=3), "ld_table", 1),
     (dict(q=PTR + 8), "aligned", 1), (dict(lse=PTR + 2), "aligned", 1),
+    (dict(R=65536, heads=600, kv_heads=300), "2^24", 2),
 ])
 def test_paged_attn_refusals(vq, kw, text, want):
     _refused(vq, vq.lib().vqmlp_paged_attn(C.byref(_attn(vq, **kw)), None, 0, None), text, want)
@@ -127,6 +128,7 @@ def _linear(vq, **kw):
     (dict(scale=float("inf")), "scale", 1), (dict(cu_q=None), "cu_q", 1), (dict(state_in=None), "null state", 1),
     (dict(state_out=PTR + 4), "16-byte", 1), (dict(g=None), "null", 1), (dict(v=PTR + 8), "16-byte", 1),
     (dict(ld_k=120), "strides", 1), (dict(ld_q=132), "strides", 1), (dict(ld_g=3), "strides", 1),
+    (dict(ld_v=(1 << 24) + 8), "2^24", 1), (dict(ld_g=(1 << 24) + 1), "2^24", 1),
 ])
 def test_linear_attn_refusals(vq, kw, text, want):
     _refused(vq, vq.lib().vqmlp_linear_attn(C.byref(_linear(vq, **kw)), None, 0, None), text, want)

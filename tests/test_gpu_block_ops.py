@@ -416,6 +416,60 @@ def test_paged_attention(vq, torch_dev, dtype, lens, heads, kv_heads, D, page, w
     _attn_check(vq, torch_dev, _t(torch_dev, dtype), lens, heads, kv_heads, D, page, window, seed=D)
 
 
+# many rows (keys in LDS), few rows of D > 128 (keys in registers), key splits, odd page and head sizes
+TILE_CASES = [
+    ([(128, 128)], 1, 1, 64, 16, 0), ([(129, 4100)], 3, 1, 128, 16, 0), ([(64, 2049)], 10, 2, 256, 32, 0),
+    ([(17, 4000), (200, 200)], 8, 8, 72, 8, 0), ([(90, 3000)], 5, 1, 136, 64, 700),
+    ([(33, 6000)], 4, 4, 128, 1024, 64), ([(1, 9000), (2, 17)], 12, 2, 256, 16, 0),
+    ([(3, 5000)], 5, 1, 200, 8, 1000), ([(1, 0), (1, 1), (1, 31), (1, 32), (1, 33), (1, 65)], 2, 1, 128, 16, 0),
+    ([(0, 7), (250, 260), (0, 0), (1, 64)], 6, 3, 96, 16, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,heads,kv_heads,D,page,window", TILE_CASES)
+def test_paged_attention_tiles(vq, torch_dev, dtype, lens, heads, kv_heads, D, page, window):
+    _attn_check(vq, torch_dev, _t(torch_dev, dtype), lens, heads, kv_heads, D, page, window, seed=D + 1, pad=3)
+
+
+@pytest.mark.parametrize("lens,D", [([(150, 700), (40, 900)], 128), ([(60, 1500)], 256), ([(2, 1500)], 256)])
+def test_paged_attention_tiles_skip_pages_outside_the_cache(vq, torch_dev, lens, D):
+    """Holes inside a request's keys, at its start and at its end, next to whole tiles."""
+
+    def edit(table, kv_len):
+        for r in range(len(kv_len)):
+            last = (kv_len[r] + 15) // 16 - 1
+            table[r, 0], table[r, 7], table[r, 20], table[r, 21] = -1, 2 ** 31 - 1, 10 ** 6, -2 ** 31
+            table[r, last] = -5
+
+    _attn_check(vq, torch_dev, torch_dev.float16, lens, 4, 2, D, 16, edit=edit, seed=9)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("D", [64, 256])
+def test_paged_attention_far_pages(vq, torch_dev, D, rows):
+    """Pages whose first element lies beyond 2^32 elements of the cache give what near ones give."""
+    torch = torch_dev
+    dt, page = torch.bfloat16, 1024
+    n = 2 ** 32 // (page * D) + 4
+    k = torch.empty((n, 1, page, D), dtype=dt, device="cuda")
+    v = torch.empty((n, 1, D, page), dtype=dt, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for near, far in ((0, n - 1), (1, n - 3)):
+        k[near].normal_(generator=g)
+        v[near].normal_(generator=g)
+        k[far], v[far] = k[near], v[near]
+    q = torch.randn((rows, 2, D), generator=g, device="cuda").to(dt)
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache, cu, kv = vq.PagedCache(k, v), i([0, rows]), i([2000])
+    near = cache.attention(q, i([[0, 1]]), cu, kv)
+    assert torch.equal(near, cache.attention(q, i([[n - 1, n - 3]]), cu, kv))
+    # and the store reaches them
+    kv_new = torch.randn((1, 1, D), generator=g, device="cuda").to(dt)
+    cache.store(kv_new, kv_new, i([(n - 1) * page + 5]))
+    assert torch.equal(k[n - 1, 0, 5], kv_new[0, 0]) and torch.equal(v[n - 1, 0, :, 5], kv_new[0, 0])
+
+
 def test_paged_attention_rows_that_see_nothing(vq, torch_dev):
     """More rows than keys, no keys at all, rows behind the last request (NaN queries)."""
     torch = torch_dev
@@ -645,6 +699,36 @@ def test_linear_attention_scales(vq, torch_dev, std, max_q):
     """Small and large values and states keep FP32 accuracy in the state, and y its type's."""
     _linear_check(vq, torch_dev, "f16", [150, 3], 1, 2, 128, 64, max_q, std=std,
                   scale=1.0 if std < 1 else 0.01)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("max_q", [16, 900])
+def test_linear_attention_growing_states(vq, torch_dev, dtype, max_q):
+    """Keys that all point one way and no decay: the state outgrows the values by the number of tokens;
+    then values of one part in a million: it stays while they come in."""
+    torch = torch_dev
+    dt, T = _t(torch, dtype), 900
+    k = torch.full((T, 1, 64), 0.125, dtype=dt)
+    q = _randn(torch, (T, 1, 64), dt, 1, 0.125)
+    v = _randn(torch, (T, 2, 64), dt, 2).abs() + 1
+    v[600:] *= 2.0 ** -14
+    g = torch.zeros(T, 2)
+    g[:, 1] = -1e-3
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    op = vq.LinearAttention(1, 2, 64, 64)
+    state = op.state(1)
+    y, out = op.forward(q.cuda(), k.cuda(), v.cuda(), g.cuda(), state, i([0, T]), max_q=max_q)
+    ry, z, rs, size = _linear_ref(torch, q, k, v, g, state.cpu(), [0, T], None, None, op.scale, 1)
+    u = _u(torch, dt)
+    _close(torch, y, ry, u * ry.abs() + (2 * u + (100 + T / 16) * W) * z + 2.0 ** -25, "y")
+    _close(torch, out, rs, (100 + T / 8) * W * size, "state")
+
+
+@pytest.mark.parametrize("hk,hv", [(3, 9), (16, 16), (5, 5)])
+def test_linear_attention_many_heads_and_requests(vq, torch_dev, hk, hv):
+    """Every workgroup number meets its request, segment and head, whatever divides by what."""
+    _linear_check(vq, torch_dev, "f16", [70, 3, 0, 65, 130, 64, 1, 257, 40], hk, hv, 24, 16, seed=5, pad=5)
+    _linear_check(vq, torch_dev, "bf16", [1100, 700], hk, hv, 16, 8, seed=6)
 
 
 def test_linear_attention_strides_streams_and_graphs(vq, torch_dev):
