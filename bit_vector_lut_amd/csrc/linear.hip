@@ -37,6 +37,13 @@ struct LinArgs {
     float scale;
 };
 
+// e^x to about two roundings: the hardware's 2^h with h = x log2 e, and what h lost as a factor 1 + r.
+__device__ __forceinline__ float exp_f32(float x) {
+    const float h = x * kLog2e;
+    const float r = fmaf(x, kLog2e, -h) + x * 1.925963033500e-8f;  // log2 e - float(log2 e)
+    return __builtin_amdgcn_exp2f(h) * fmaf(r, 0.6931471805599453f, 1.f);
+}
+
 __device__ __forceinline__ int lin_row(const LinArgs& a, int r) { return min(max(a.cu[r], 0), a.T); }
 
 // The state slot of a request, or -1, and whether it starts from what the slot holds.
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
     };
     auto token = [&](int t, const Token& x) __attribute__((always_inline)) {
         const f32x4 v = {lo16<E>(x.v[0]), hi16<E>(x.v[0]), lo16<E>(x.v[1]), hi16<E>(x.v[1])};
-        const float e = expf(fmaxf(x.g, kMinG));
+        const float e = exp_f32(fmaxf(x.g, kMinG));
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -351,8 +358,9 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     const int bi = lane >> 3, bj = 8 * wave + (lane & 7);
     const bool isk = 8 * wave < DKP / 8;
     const int cj = isk ? bj : bj - DKP / 8;
-    const bool stage = isk || cj < DVP / 8;
+    const bool stage = isk || 8 * wave - DKP / 8 < DVP / 8;
     const bool inside = isk ? 8 * cj < a.Dk : stage && 8 * cj < a.Dv;
+    const bool dense = stage && (isk ? a.Dk == DKP : a.Dv == DVP);  // all lanes of the wave load
     const int64_t ld = 2 * (isk ? a.ld_k : a.ld_v);  // bytes
     const uint8_t* const src =
         reinterpret_cast<const uint8_t*>(isk ? a.k + int64_t(hk) * a.Dk : a.v + int64_t(h) * a.Dv) + u.c0 * ld;
@@ -364,10 +372,15 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     float gv = 0.f;
     auto fetch = [&](int t) __attribute__((always_inline)) {  // chunk at token t of the request
         const uint8_t* const base = src + t * ld;
+        if (dense && t + kC <= t1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            blk[i] = u32x4{0, 0, 0, 0};
-            if (inside && t + 8 * bi + i < t1) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
+            for (int i = 0; i < 8; ++i) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                blk[i] = u32x4{0, 0, 0, 0};
+                if (inside && t + 8 * bi + i < t1) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
+            }
         }
     };
     auto fetch_g = [&](int t) __attribute__((always_inline)) {
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
         if (wave > 1) return;
         const float b = lane_scan(gv, 0.f, [](float x, float y) { return x + y; });
-        const float eb = expf(b);
+        const float eb = exp_f32(b);
         if (wave == 0) {
             d.eb[lane] = eb;
             d.bl[lane] = b * kLog2e;
@@ -464,15 +477,18 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if (x < (wave & 2)) continue;
-                f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+                float p[4] = {0.f, 0.f, 0.f, 0.f};  // keys behind the queries' block
+                if (x >= wave) {
+                    f32x4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[x][s], sc);
-                const float bt = dc.bl[16 * x + lr];
-                float p[4];
+                    for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[x][s], sc);
+                    const float bt = dc.bl[16 * x + lr];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool see = 16 * wave + 4 * g4 + i <= 16 * x + lr;
-                    p[i] = see ? sc[i] * a.scale * __builtin_amdgcn_exp2f(bt - bj4[i]) : 0.f;
+                    for (int i = 0; i < 4; ++i) p[i] = sc[i] * a.scale * __builtin_amdgcn_exp2f(bt - bj4[i]);
+                    if (x == wave) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[i] = 4 * g4 + i <= lr ? p[i] : 0.f;
+                    }
                 }
                 *reinterpret_cast<u32x2*>(&so.p[16 * x + lr][16 * wave + 4 * g4]) =
                     u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
