@@ -216,12 +216,27 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
     }
 }
 
-// Join the splits of a row: a wave per row, lane = split for the weights, then lanes over D.
-template <class E>
+// Join the splits of a row, which all have been written, zeros where a split had no keys: one wave a row
+// where they are few, else four (64 splits of 192 rows of 256 columns: 24 us with one, 5 with four).
+// Lane = split for the weights, then four columns.  Bound by the latency of the loads, so eight are on
+// their way at once.
+template <class E, int WPR>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    __shared__ float buf[WPR][256];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * 4 + wave : blockIdx.x;
     if (row >= int64_t(a.T) * a.heads) return;
+    const bool in = 4 * lane < a.D;
+    const float* src = a.opart + row * a.nsplit * a.D + (in ? 4 * lane : 0);
+    const int s0 = WPR == 1 ? 0 : wave;
+    f32x4 x[8];
+    auto load = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (s + WPR * j < a.nsplit)
+                x[j] = *reinterpret_cast<const f32x4*>(src + int64_t(s + WPR * j) * a.D);
+    };
+    load(s0);
     float m = kNegInf, l = 0.f;
     if (lane < a.nsplit) {
         m = a.ml[(row * a.nsplit + lane) * 2];
@@ -234,25 +249,37 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
     const float w = __builtin_amdgcn_exp2f((m - (mm == kNegInf ? 0.f : mm)) * c);
     const float sum = wave_sum(w * l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const float* src = a.opart + row * a.nsplit * a.D + 4 * lane;
-    const bool in = 4 * lane < a.D;
-    for (int s = 0; s < a.nsplit; ++s) {
-        // every lane takes part in the exchange: lanes behind D hold weights too
-        const float ws = __shfl(w, s);
-        const float ls = __shfl(l, s);
-        if (ls == 0.f || !in) continue;  // a split without keys
-        const f32x4 x = *reinterpret_cast<const f32x4*>(src + int64_t(s) * a.D);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = s0; s < a.nsplit; s += 8 * WPR) {
+        if (s != s0) load(s);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(ws, x[j], v[j]);
+        for (int j = 0; j < 8; ++j) {
+            const int at = s + WPR * j;
+            if (at >= a.nsplit) break;
+            const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), at));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(ws, x[j][i], v[i]);
+        }
     }
     const int64_t tok = row / a.heads;
     const int head = int(row % a.heads);
-    if (in) {
-        u32x2 w2 = {pack16<E>(v[0] * inv, v[1] * inv), pack16<E>(v[2] * inv, v[3] * inv)};
-        *reinterpret_cast<u32x2*>(a.y + tok * a.ld_y + int64_t(head) * a.D + 4 * lane) = w2;
+    uint16_t* dst = a.y + tok * a.ld_y + int64_t(head) * a.D;
+    if constexpr (WPR == 1) {
+        if (in)
+            *reinterpret_cast<u32x2*>(dst + 4 * lane) =
+                u32x2{pack16<E>(v[0] * inv, v[1] * inv), pack16<E>(v[2] * inv, v[3] * inv)};
+    } else {
+        *reinterpret_cast<f32x4*>(&buf[wave][4 * lane]) = v;
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d < a.D) {
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) z += buf[i][d];
+            dst[d] = uint16_t(bits16<E>(z * inv));
+        }
     }
-    if (lane == 0 && a.lse)
+    if (lane == 0 && (WPR == 1 || wave == 0) && a.lse)
         a.lse[row] = sum == 0.f ? kNegInf : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
 }
 
@@ -358,7 +385,8 @@ void launch_attn(const AttnArgs& a, const AttnGeom& G, int dtype, hipStream_t s)
     }
     if (a.nsplit > 1) {
         const int64_t rows = int64_t(a.T) * a.heads;
-        k_attn_join<E><<<dim3((rows + 3) / 4), 256, 0, s>>>(a);
+        if (a.nsplit <= 8 || rows >= (1 << 24)) k_attn_join<E, 1><<<dim3((rows + 3) / 4), 256, 0, s>>>(a);
+        else k_attn_join<E, 4><<<dim3(rows), 256, 0, s>>>(a);
     }
 }
 
