@@ -15,7 +15,8 @@ struct AttnArgs {
     const uint16_t *kc, *vc;
     const int32_t *table, *cu, *kv_len;
     float* opart;  // [row][split][D], row = token * heads + head (split launches only)
-    float* ml;     // [row][split][2]: maximum of the scores, sum
+    float* ml;     // [row][split][2]: maximum of the scores, sum (-1: this split has no keys and wrote
+                   // nothing; in split 0: the row is done)
     int64_t ld_table, ld_q, ld_y;
     int T, R, heads, kv_heads, g, D, shift, n_pages, window, nsplit, split_tiles;
     int width;     // pages per table row
@@ -67,6 +68,29 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, Tile& t) {
     t.full_hi = min(p0, cap - 1);
     t.full_lo = a.window ? max(0, p1 - a.window + 1) : 0;
     return true;
+}
+
+// The key tiles of a split: a request of up to split_tiles of them is done in one, whatever the others
+// need.  `used` splits have keys; the last one takes what is left.
+struct Split {
+    int begin, end, used;
+};
+__device__ __forceinline__ Split key_split(const AttnArgs& a, const Tile& t, int split, int shift) {
+    const int kt0 = t.kmin >> shift;
+    const int nt = t.kmax >= t.kmin ? (t.kmax >> shift) + 1 - kt0 : 0;
+    Split s;
+    s.used = max(1, min(a.nsplit, (nt + a.split_tiles - 1) / a.split_tiles));
+    s.begin = kt0 + min(nt, split * a.split_tiles);
+    s.end = kt0 + (split == a.nsplit - 1 ? nt : min(nt, (split + 1) * a.split_tiles));
+    return s;
+}
+// What the join reads of a row besides the sums themselves.
+__device__ __forceinline__ void put_ml(const AttnArgs& a, int64_t row, int split, const Split& s, float m, float l) {
+    float* ml = a.ml + row * a.nsplit * 2;
+    ml[2 * split] = m;
+    ml[2 * split + 1] = s.used == 1 ? -1.f : l;
+    if (split == 0 && s.used > 1)
+        for (int i = s.used; i < a.nsplit; ++i) ml[2 * i + 1] = -1.f;
 }
 
 // Many rows (attn_tile.hip).

@@ -34,8 +34,11 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
     __shared__ float obuf[NW][MT][DC + 4];
     __shared__ float mlbuf[NW][MT][2];
     Tile t;
-    if (!find_tile<MT>(a, blockIdx.x, t)) return;
     const int hk = blockIdx.y, split = blockIdx.z;
+    if (!find_tile<MT>(a, blockIdx.x, t)) return;
+    const Split ks = key_split(a, t, split, 5);
+    const int begin = ks.begin, end = ks.end;
+    if (split >= ks.used) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, g = lane >> 4;
     const int D = FULL ? DP : a.D;
@@ -60,10 +63,6 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
     for (int dt = 0; dt < DT; ++dt) o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
     const float c = a.scale * 1.4426950408889634f;
 
-    const int kt0 = t.kmin >> 5;
-    const int nt = t.kmax >= t.kmin ? (t.kmax >> 5) + 1 - kt0 : 0;
-    const int begin = kt0 + min(nt, split * a.split_tiles);
-    const int end = kt0 + (split == a.nsplit - 1 ? nt : min(nt, (split + 1) * a.split_tiles));
     const int32_t* row = a.table + (t.r < a.R ? t.r : 0) * a.ld_table;
     // page numbers of the lane's two K rows and of its eight V columns in a tile
     const int krow = 8 * (lr >> 2), vcol = 8 * g;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = fmaf(wt[w], x[j], v[j]);
             }
-            if (a.nsplit == 1) {
+            if (ks.used == 1) {
                 const u32x2 w2 = {pack16<E>(v[0] * inv, v[1] * inv), pack16<E>(v[2] * inv, v[3] * inv)};
                 *reinterpret_cast<u32x2*>(a.y + (t.c0 + i) * a.ld_y + int64_t(head) * D + d0 + d) = w2;
             } else {
@@ -205,10 +204,8 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
             }
         }
         if (d0 == 0 && jt == 0) {
-            if (a.nsplit > 1) {
-                a.ml[(rowi * a.nsplit + split) * 2] = mm;
-                a.ml[(rowi * a.nsplit + split) * 2 + 1] = sum;
-            } else if (a.lse) {
+            if (a.nsplit > 1) put_ml(a, rowi, split, ks, mm, sum);
+            if (ks.used == 1 && a.lse) {
                 a.lse[rowi] = sum == 0.f ? kNegInf
                                          : fmaf(mm, a.scale, logf(sum) - kBias<E> * 0.6931471805599453f);
             }
@@ -216,10 +213,10 @@ __global__ void __launch_bounds__(256) k_attn_wave(AttnArgs a) {
     }
 }
 
-// Join the splits of a row, which all have been written, zeros where a split had no keys: one wave a row
-// where they are few, else four (64 splits of 192 rows of 256 columns: 24 us with one, 5 with four).
-// Lane = split for the weights, then four columns.  Bound by the latency of the loads, so eight are on
-// their way at once.
+// Join the splits of a row: one wave a row where they are few, else four (64 splits of 192 rows of 256
+// columns: 24 us with one, 5 with four).  Lane = split for the weights, then four columns.  Bound by the
+// latency of the loads, so eight are on their way at once; four waves issue them before they know which
+// splits have keys, and use what those wrote only.
 template <class E, int WPR>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
     __shared__ float buf[WPR][256];
@@ -230,18 +227,23 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
     const float* src = a.opart + row * a.nsplit * a.D + (in ? 4 * lane : 0);
     const int s0 = WPR == 1 ? 0 : wave;
     f32x4 x[8];
-    auto load = [&](int s) {
+    auto load = [&](int s, int end) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (s + WPR * j < a.nsplit)
+            if (s + WPR * j < end)
                 x[j] = *reinterpret_cast<const f32x4*>(src + int64_t(s + WPR * j) * a.D);
     };
-    load(s0);
-    float m = kNegInf, l = 0.f;
+    if (WPR > 1) load(s0, a.nsplit);
+    float m = kNegInf, l = -1.f;
     if (lane < a.nsplit) {
         m = a.ml[(row * a.nsplit + lane) * 2];
         l = a.ml[(row * a.nsplit + lane) * 2 + 1];
     }
+    if (__builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, l))) < 0.f)
+        return;  // done in one split, which wrote no more than this
+    const int used = __popcll(__ballot(!(l < 0.f)));  // the first ones
+    if (lane >= used) m = kNegInf, l = 0.f;
+    if (WPR == 1) load(s0, used);
     float mm = m;
 #pragma unroll
     for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
@@ -250,12 +252,12 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
     const float sum = wave_sum(w * l);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = s0; s < a.nsplit; s += 8 * WPR) {
-        if (s != s0) load(s);
+    for (int s = s0; s < used; s += 8 * WPR) {
+        if (s != s0) load(s, used);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int at = s + WPR * j;
-            if (at >= a.nsplit) break;
+            if (at >= used) break;
             const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), at));
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = fmaf(ws, x[j][i], v[i]);
@@ -327,7 +329,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
             const double tiles = (key_tiles + ns - 1) / ns + 2;
             double cost = double((blocks + slots - 1) / slots) * tiles * tile;
             if (d.R > 1) cost = 0.5 * cost + 0.5 * tiles * alone;
-            if (ns > 1) cost += 4 + ns * double(rows_all) * d.D * 8 / 4e6;
+            if (ns > 1) cost += 4 + ns * double(rows_all) * d.D * 8 / 4e6 * (d.R > 1 ? 0.5 : 1.0);
             if (cost < best) best = cost, G.nsplit = ns;
         }
     } else {

@@ -25,6 +25,9 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     const int hk = gi % a.kv_heads, split = gi / a.kv_heads;
     Tile t;
     if (!find_tile<kAttnTileRows>(a, x, t)) return;
+    const Split ks = key_split(a, t, split, 6);
+    const int begin = ks.begin, end = ks.end;
+    if (split >= ks.used) return;
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
     const int lr = lane & 31, lh = lane >> 5;
@@ -61,10 +64,6 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
-    const int kt0 = t.kmin / kKT;
-    const int nt = t.kmax >= t.kmin ? t.kmax / kKT + 1 - kt0 : 0;
-    const int begin = kt0 + min(nt, split * a.split_tiles);
-    const int end = kt0 + (split == a.nsplit - 1 ? nt : min(nt, (split + 1) * a.split_tiles));
     const int32_t* row = a.table + (t.r < a.R ? t.r : 0) * a.ld_table;
     auto page_of = [&](int key) { return row[min(key >> a.shift, a.width - 1)]; };
     auto in_cache = [&](int page) { return uint32_t(page) < uint32_t(a.n_pages); };
@@ -290,7 +289,8 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     qi = query(fresh(lr), &head);
     if (qi >= t.n) return;
     const int64_t rowi = int64_t(t.c0 + qi) * a.heads + head;
-    if (a.nsplit > 1) {
+    if (a.nsplit > 1 && lh == 0) put_ml(a, rowi, split, ks, m, l);
+    if (ks.used > 1) {
         float* dst = a.opart + (rowi * a.nsplit + split) * D;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -301,10 +301,6 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
                     *reinterpret_cast<f32x4*>(dst + at) =
                         f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
             }
-        if (lh == 0) {
-            a.ml[(rowi * a.nsplit + split) * 2] = m;
-            a.ml[(rowi * a.nsplit + split) * 2 + 1] = l;
-        }
     } else {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
         uint16_t* dst = a.y + (t.c0 + qi) * a.ld_y + int64_t(head) * D;

@@ -770,6 +770,34 @@ def test_linear_attention_strides_streams_and_graphs(vq, torch_dev):
 # ------------------------------------------------------------------ together
 
 
+def test_poisoned_workspaces_change_nothing(vq, torch_dev):
+    """Workspaces need no fill: all bits set gives the values of a fresh call, with short requests (done
+    in one split) next to long ones, and with segments."""
+    torch = torch_dev
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    for lens, D in (([(1, 5000), (1, 20), (2, 700), (0, 9)], 64), ([(150, 4000), (3, 30)], 128),
+                    ([(2, 3000), (1, 10)], 256)):
+        q, k, v, table, cu = _attn_case(torch, torch.float16, lens, 4, 2, D, 16, 7)
+        cache = vq.PagedCache(k.cuda(), v.cuda())
+        args = (q.cuda(), table.cuda(), i(cu), i([kv for _, kv in lens]))
+        want = cache.attention(*args, with_lse=True)
+        work = torch.full((cache.workspace_bytes(q.shape[0], len(lens), 4, table.shape[1]),), 255,
+                          dtype=torch.uint8, device="cuda")
+        assert work.numel() > 0
+        for _ in range(2):
+            got = cache.attention(*args, with_lse=True, workspace=work)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    op = vq.LinearAttention(1, 2, 64, 64)
+    x = [_randn(torch, (2600, h, 64), torch.float16, s, 0.2).cuda() for h, s in ((1, 1), (1, 2), (2, 3))]
+    g = -torch.rand(2600, 2, device="cuda")
+    state = torch.randn(2, 2, 64, 64, device="cuda")
+    want = op.forward(*x, g, state, i([0, 2000, 2600]))
+    work = torch.full((op.workspace_bytes(2600, 2, 2600),), 255, dtype=torch.uint8, device="cuda")
+    assert work.numel() > 0
+    got = op.forward(*x, g, state, i([0, 2000, 2600]), workspace=work)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_small_workspaces_are_refused(vq, torch_dev):
     torch = torch_dev
     q, k, v, table, cu = _attn_case(torch, torch.float16, [(2, 3000)], 2, 1, 64, 16, 0)
