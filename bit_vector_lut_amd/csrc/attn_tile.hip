@@ -84,39 +84,60 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         vp[0] = page_of(kt * kKT + 8 * vchunk);
         vp[1] = page_of(kt * kKT + 8 * (vchunk ^ 4));
     };
-    auto stage_k = [&](int kt, int buf, int lane) {
-        const uint8_t* base[2];  // of the first of a page's eight keys
+    struct Source {
+        const uint8_t* k[2];   // of the first of a page's eight keys
+        const uint16_t* v[2];  // this lane's eight keys in row vrow of V, in even and odd loads
+    };
+    auto find_k = [&](int kt, Source& x) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int page = uniform(in_cache(kp[h]) ? kp[h] : 0);
             const int key = kt * kKT + 16 * wave + 8 * h;
-            base[h] = reinterpret_cast<const uint8_t*>(
+            x.k[h] = reinterpret_cast<const uint8_t*>(
                 a.kc + (((int64_t(page) * a.kv_heads + hk) << a.shift) + (key & P1)) * D);
         }
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int krow = j * RPI + lane / (DP / 8);
-            int chunk = (lane % (DP / 8)) ^ kf(krow);
-            if (!FULL && 8 * chunk >= D) chunk = 0;  // meets zeros of the query
-            load_lds16(base[j * 2 / NI], (krow & 7) * D * 2 + chunk * 16, klds + buf * TILE + j * 1024);
-        }
     };
-    auto stage_v = [&](int kt, int buf) -> bool {  // true: a page of the tile is outside the cache
-        const uint16_t* src[2];
+    // row j * RPI + krow of the wave's sixteen; its permutation is that of j * RPI or-ed with krow's
+    const int krow = lane / (DP / 8), kchunk = (lane % (DP / 8)) ^ kf(krow);
+    const int koff = krow * DP * 2 + kchunk * 16;
+    auto load_k = [&](int j, const Source& x, int buf) __attribute__((always_inline)) {
+        int off;
+        if constexpr (FULL) {
+            off = (koff ^ (kf(j * RPI) * 16)) + (j * RPI & 7) * DP * 2;
+        } else {
+            int chunk = kchunk ^ kf(j * RPI);
+            if (8 * chunk >= D) chunk = 0;  // meets zeros of the query
+            off = ((j * RPI + krow) & 7) * D * 2 + chunk * 16;
+        }
+        load_lds16(x.k[j * 2 / NI], off, klds + buf * TILE + j * 1024);
+    };
+    auto find_v = [&](int kt, Source& x) __attribute__((always_inline)) -> bool {  // true: a page is outside the cache
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int page = in_cache(vp[h]) ? vp[h] : 0;
-            src[h] = a.vc + ((int64_t(page) * a.kv_heads + hk) * D << a.shift) +
+            x.v[h] = a.vc + ((int64_t(page) * a.kv_heads + hk) * D << a.shift) +
                      ((kt * kKT + 8 * (vchunk ^ (4 * h))) & P1);
         }
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            int d = (wave * NI + j) * 8 + vrow;
-            if (!FULL) d = min(d, D - 1);
-            // the parity of wave * NI + j; NI is even
-            load_lds16(src[j & 1] + (int64_t(d) << a.shift), vlds + buf * TILE + j * 1024);
-        }
         return __any(!in_cache(vp[0]));
+    };
+    auto load_v = [&](int j, const Source& x, int buf) __attribute__((always_inline)) {
+        int d = (wave * NI + j) * 8 + vrow;
+        if (!FULL) d = min(d, D - 1);
+        // even or odd as wave * NI + j is; NI is even
+        load_lds16(x.v[j & 1] + (int64_t(d) << a.shift), vlds + buf * TILE + j * 1024);
+    };
+    auto stage_k = [&](int kt, int buf) {
+        Source x;
+        find_k(kt, x);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) load_k(j, x, buf);
+    };
+    auto stage_v = [&](int kt, int buf) {
+        Source x;
+        const bool bad = find_v(kt, x);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) load_v(j, x, buf);
+        return bad;
     };
 
     // Operand addresses.  Row m = 8a + 4h + b of the K operand takes key 16(a/2) + 8h + 4(a%2) + b,
@@ -197,7 +218,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
             __syncthreads();
         }
         if (idle) {  // no rows: only its share of the loads
-            stage_k(min(i + 2, end - 1), buf, lane);
+            stage_k(min(i + 2, end - 1), buf);
             bad_v = stage_v(min(i + 1, end - 1), buf ^ 1);
             pages_k(min(i + 3, end - 1)), pages_v(min(i + 2, end - 1));
             return;
@@ -210,6 +231,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         // keep the compiler from gathering the reads right in front of their steps.
         constexpr int QK = 2 * KS, STEPS = QK + 4 * DB, SPREAD = QK + DB, MAX = 32 / (2 * DB);
         u32x4 pf[4], fr[2][4];
+        Source where;
         float sum[2] = {0.f, 0.f}, p[2];
         float mx[2] = {kNegInf, kNegInf};
         const int kb = DP == 128 ? fresh(kbase) : kbase, vb = DP == 128 ? fresh(vbase) : vbase;
@@ -243,12 +265,17 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
                 for (int e = (z - SPREAD) * MAX; e < (z - SPREAD + 1) * MAX; ++e)
                     mx[e & 1] = fmaxf(mx[e & 1], sn[e >> 4][e & 15]);
             }
-            // tiles behind the last one are the last again: their buffers are not read
-            if constexpr (z == 2) stage_k(min(i + 2, end - 1), buf, DP == 128 ? fresh(lane) : lane);
-            if constexpr (z == 6) bad_v = stage_v(min(i + 1, end - 1), buf ^ 1);
-            if constexpr (z == 7) pages_k(min(i + 3, end - 1)), pages_v(min(i + 2, end - 1));
+            // The loads one by one: together they would hold up the steps behind them.  Tiles behind the
+            // last one are the last again: their buffers are not read.
+            constexpr int GAP = (STEPS - 2) / (2 * NI), at = z - 1;
+            if constexpr (at == 0) find_k(min(i + 2, end - 1), where), pages_k(min(i + 3, end - 1));
+            if constexpr (at == NI * GAP) bad_v = find_v(min(i + 1, end - 1), where), pages_v(min(i + 2, end - 1));
+            if constexpr (at >= 0 && at % GAP == 0 && at / GAP < NI)
+                load_k(at / GAP, where, buf);
+            if constexpr (at >= NI * GAP && at % GAP == 0 && at / GAP < 2 * NI) load_v(at / GAP - NI, where, buf ^ 1);
             __builtin_amdgcn_sched_barrier(0);
         }, std::make_integer_sequence<int, STEPS>{});
+        asm volatile("" : "+v"(mx[0]), "+v"(mx[1]));  // made above, not where it turns out to be needed
         l += sum[0] + sum[1];
         if (i + 1 < end) maximum(i + 1, edge(i + 1, bad_v), sn, fmaxf(mx[0], mx[1]));
     };
@@ -257,10 +284,10 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         f32x16 s0[2], s1[2];
         pages_k(begin);
         pages_v(begin);
-        stage_k(begin, 0, lane);
+        stage_k(begin, 0);
         bad_v = stage_v(begin, 0);
         pages_k(min(begin + 1, end - 1));
-        stage_k(min(begin + 1, end - 1), 1, lane);
+        stage_k(min(begin + 1, end - 1), 1);
         pages_k(min(begin + 2, end - 1));
         pages_v(min(begin + 1, end - 1));
         wait_loads();
