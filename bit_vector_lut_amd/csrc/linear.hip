@@ -370,17 +370,15 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     u32x4 blk[8];
     // of the chunk after the one in work: g of token `lane` (wave 0), of token 63 - `lane` (wave 1)
     float gv = 0.f;
-    auto fetch = [&](int t) __attribute__((always_inline)) {  // chunk at token t of the request
-        const uint8_t* const base = src + t * ld;
+    // One of the eight loads of the chunk at token t.  A wave's loads go out one by one between its
+    // matrix-core steps: eight in a row keep it from issuing anything else for over a thousand cycles.
+    auto fetch = [&](int t, int i) __attribute__((always_inline)) {
+        const uint8_t* const base = src + t * ld + i * ld;
         if (dense && t + kC <= t1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
+            blk[i] = *reinterpret_cast<const u32x4*>(base + src_off);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                blk[i] = u32x4{0, 0, 0, 0};
-                if (inside && t + 8 * bi + i < t1) blk[i] = *reinterpret_cast<const u32x4*>(base + i * ld + src_off);
-            }
+            blk[i] = u32x4{0, 0, 0, 0};
+            if (inside && t + 8 * bi + i < t1) blk[i] = *reinterpret_cast<const u32x4*>(base + src_off);
         }
     };
     auto fetch_g = [&](int t) __attribute__((always_inline)) {
@@ -406,27 +404,23 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     // Q and K rows of a chunk, token by token, straight to LDS; behind the last token the last again
     constexpr int RPI = 512 / DKP, NI = kC / RPI / 4;  // rows per load, loads per wave of one of the two
     auto swz = [](int row) { return DKP == 64 ? (row >> 1) & 7 : row & 15; };
-    auto stage_qk = [&](int t) __attribute__((always_inline)) {
+    auto stage_qk = [&](int t, int j) __attribute__((always_inline)) {  // load j of NI of each
         if constexpr (OUT) {
-            const uint32_t ql = lds_byte(so.q) + wave * NI * 1024, kl = lds_byte(so.k) + wave * NI * 1024;
+            const uint32_t ql = lds_byte(so.q) + (wave * NI + j) * 1024, kl = lds_byte(so.k) + (wave * NI + j) * 1024;
             const uint8_t* const q = reinterpret_cast<const uint8_t*>(a.q + (u.c0 + t) * a.ld_q + int64_t(hk) * a.Dk);
             const uint8_t* const k = reinterpret_cast<const uint8_t*>(a.k + (u.c0 + t) * a.ld_k + int64_t(hk) * a.Dk);
             const uint32_t lq = uint32_t(a.ld_q) * 2, lk = uint32_t(a.ld_k) * 2;
             const int r0 = lane / (DKP / 8);
-            const bool whole = t + kC <= t1;
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                const int first = (wave * NI + j) * RPI;  // a multiple of RPI: its low bits are j's
-                int chunk = (lane % (DKP / 8)) ^ swz(r0) ^ swz(j * RPI);
-                if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros on the other side
-                if (whole) {
-                    load_lds16(q + int64_t(first) * lq, r0 * lq + 16 * chunk, ql + j * 1024);
-                    load_lds16(k + int64_t(first) * lk, r0 * lk + 16 * chunk, kl + j * 1024);
-                } else {
-                    const int r = min(first + r0, t1 - 1 - t);
-                    load_lds16(q, r * lq + 16 * chunk, ql + j * 1024);
-                    load_lds16(k, r * lk + 16 * chunk, kl + j * 1024);
-                }
+            const int first = (wave * NI + j) * RPI;  // a multiple of RPI: its low bits are j's
+            int chunk = (lane % (DKP / 8)) ^ swz(r0) ^ swz(j * RPI);
+            if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros on the other side
+            if (t + kC <= t1) {
+                load_lds16(q + int64_t(first) * lq, r0 * lq + 16 * chunk, ql);
+                load_lds16(k + int64_t(first) * lk, r0 * lk + 16 * chunk, kl);
+            } else {
+                const int r = min(first + r0, t1 - 1 - t);
+                load_lds16(q, r * lq + 16 * chunk, ql);
+                load_lds16(k, r * lk + 16 * chunk, kl);
             }
         }
     };
@@ -438,8 +432,10 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     int e = 0;          // S is kept in units of 2^-e
     if (t0 < t1) {
         fetch_g(t0);
-        fetch(t0);
-        stage_qk(t0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fetch(t0, i);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) stage_qk(t0, j);
         decays(sm.d[0]);
         fetch_g(t0 + kC);
     }
@@ -457,7 +453,6 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             }
         }
         wait_loads();  // this wave's part of Q and K is in LDS
-        fetch(t + kC);
         __syncthreads();
         decays(sm.d[((t - t0) / kC + 1) & 1]);
         fetch_g(t + 2 * kC);
@@ -533,6 +528,11 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                                       pack16<E>(s1[0], s1[1]), pack16<E>(s1[2], s1[3])};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[v][x] = E::mfma16(sf, qf[x][p], o[v][x]);
+                    constexpr int N = 8 / (KS * NTV);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) fetch(t + kC, (p * NTV + v) * N + i);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 for (int v = 0; v < NTV; ++v) o[v][x] *= eb;
             }
             __syncthreads();
-            if (t + kC < t1) stage_qk(t + kC);  // every wave is done with this chunk's
+            // every wave is done with this chunk's queries and keys
         }
         u32x4 vf[NTV][2];
 #pragma unroll
@@ -551,13 +551,16 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[(vget ^ tok_bits(4 * v, 4 * c)) + 4 * v * kC * 2]);
         if constexpr (OUT) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x) {
+                if (x < NI && t + kC < t1) stage_qk(t + kC, x);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int c = 0; c <= x / 2; ++c) {
                     const u32x4 pf = *reinterpret_cast<const u32x4*>(&so.p[16 * x + lr][32 * c + 8 * g4]);
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
                 }
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if (t + 16 * x + lr >= t1) continue;
@@ -653,6 +656,10 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 for (int v = 0; v < NTV; ++v)
                     S[p][b][v] = E::mfma16(kk[z / 2 & 1][z & 1], part[c][v][q], S[p][b][v]);
             if constexpr (z < 2 * KS && z % KS == 0 && z / KS < NTV) parts(1, z / KS);
+            if constexpr (!OUT && z < 8) {
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(t + kC, z);
+            }
         }, std::make_integer_sequence<int, STEPS>{});
         __syncthreads();
     }
