@@ -190,7 +190,7 @@ __device__ __forceinline__ constexpr int tok_bits(int row, int chunk) {
 }
 __device__ __forceinline__ constexpr int tok_at(int row, int chunk) { return row * kC * 2 + tok_bits(row, chunk); }
 
-struct LinDecay {            // of one chunk; b = sum of g up to a token
+struct alignas(16) LinDecay {  // of one chunk; b = sum of g up to a token
     float eb[kC], bl[kC];    // e^b, b log2 e
     float tail[kC];          // e^(sum behind the token)
     float etot;              // e^(sum of the chunk)
@@ -454,8 +454,6 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         }
         wait_loads();  // this wave's part of Q and K is in LDS
         __syncthreads();
-        decays(sm.d[((t - t0) / kC + 1) & 1]);
-        fetch_g(t + 2 * kC);
         f32x4 o[NTV][4];
         if constexpr (OUT) {
             // scores of this wave's 16 keys with all queries from there on
@@ -581,17 +579,17 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         // the state after the chunk
         int en = e;
         if constexpr (HALF) {
-            uint32_t mx = 0;
+            typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 both = {0, 0};  // magnitudes are in the order of their bits
 #pragma unroll
             for (int v = 0; v < NTV; ++v)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = vf[v][c][i];
-                        mx = max(mx, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
-                    }
-            mx = wave_max(mx);
+                    for (int i = 0; i < 4; ++i)
+                        both = __builtin_elementwise_max(
+                            both, __builtin_bit_cast(u16x2, uint32_t(vf[v][c][i] & 0x7FFF7FFFu)));
+            const uint32_t mx = wave_max(uint32_t(max(both[0], both[1])));
             en = mx ? 10 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^10, 2^11)
         }
         const float lift = pow2(en);
@@ -656,6 +654,10 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 for (int v = 0; v < NTV; ++v)
                     S[p][b][v] = E::mfma16(kk[z / 2 & 1][z & 1], part[c][v][q], S[p][b][v]);
             if constexpr (z < 2 * KS && z % KS == 0 && z / KS < NTV) parts(1, z / KS);
+            if constexpr (z == 2 * KS) {  // between products, which hide the lane moves' waits
+                decays(sm.d[((t - t0) / kC + 1) & 1]);
+                fetch_g(t + 2 * kC);
+            }
             if constexpr (!OUT && z < 8) {
                 __builtin_amdgcn_sched_barrier(0);
                 fetch(t + kC, z);
