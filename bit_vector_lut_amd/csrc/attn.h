@@ -95,6 +95,6 @@ __device__ __forceinline__ void put_ml(const AttnArgs& a, int64_t row, int split
 
 // Many rows (attn_tile.hip).
 constexpr int kAttnTileRows = 128;
-void launch_attn_tile(const AttnArgs& a, int dtype, int tiles, hipStream_t s);
+void launch_attn_tile(const AttnArgs& a, int dtype, bool few, int tiles, hipStream_t s);
 
 }  // namespace vqmlp

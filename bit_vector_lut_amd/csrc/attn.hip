@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 
 struct AttnGeom {
     bool lds;       // tiles of kAttnTileRows with the keys in LDS, otherwise register tiles of 16 rows
+    bool few;       // few rows a request: the loads of a tile before its matrix-core steps
     int tiles, nsplit, split_tiles;
     size_t opart, ml, bytes;
 };
@@ -306,6 +307,9 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const size_t rows_all = size_t(d.T) * d.heads;
     const int keys = std::max(1, d.max_kv);
     G.lds = d.D <= 128 || rows > 16;
+    // with loads first 8 tokens over 65,472 keys take 53 us for 40/8 heads of 128 (58 with loads between
+    // the steps), but 62 (60) for 24/4 heads of 256
+    G.few = rows * d.D <= 64 * 128;
     const int mt = G.lds ? kAttnTileRows : 16, key_tile = G.lds ? 64 : 32;
     const int key_tiles = (keys + key_tile - 1) / key_tile;
     G.tiles = int(all / mt) + d.R + 1;
@@ -379,7 +383,7 @@ vqmlp_status attn_check(const vqmlp_attn_desc* p, const char* who, int* shift) {
 template <class E>
 void launch_attn(const AttnArgs& a, const AttnGeom& G, int dtype, hipStream_t s) {
     if (G.lds) {
-        launch_attn_tile(a, dtype, G.tiles, s);
+        launch_attn_tile(a, dtype, G.few, G.tiles, s);
     } else {
         const dim3 grid(G.tiles, a.kv_heads, a.nsplit);
         if (a.D == 256) k_attn_wave<E, true><<<grid, 256, 0, s>>>(a);

@@ -11,17 +11,24 @@ namespace {
 
 constexpr int kKT = 64;   // keys of a tile
 
-template <class E, int DP, bool FULL>
+// Places for the splits of a row tile: with several requests an odd number, so that the splits that have
+// keys in every request do not all meet on the same engines as workgroups go round them (four prompts of
+// 37 to 1,000 rows: 197 us with four places, 98 with three).  A single request fills all of its splits.
+__host__ __device__ inline int split_slots(int nsplit, int requests) { return requests == 1 ? nsplit : nsplit | 1; }
+
+// FEW: few rows a request, so that the time goes into reading keys and values.
+template <class E, int DP, bool FULL, bool FEW>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a) {
     constexpr int KS = DP / 16, DB = DP / 32, NI = DP / 32;
     constexpr int RPI = 512 / DP;        // key rows per load instruction
     constexpr int TILE = kKT * DP * 2;   // bytes
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2 * TILE];
     __shared__ __attribute__((aligned(1024))) uint8_t vbuf[2 * TILE];
-    const int groups = a.kv_heads * a.nsplit;
-    // the last tiles of a prompt, which see the most keys, come first; workgroups that read the same
-    // keys are a multiple of 8 apart wherever kv_heads * splits is one: on the same XCD
-    const int x = (gridDim.x - 1 - blockIdx.x) / groups, gi = blockIdx.x % groups;
+    // The last tiles of a prompt, which see the most keys, come first; but one tile of one request stands in
+    // front of those that turn out to be empty, so that each of its splits finds a compute unit of its own.
+    const int groups = a.kv_heads * split_slots(a.nsplit, a.R), gi = blockIdx.x % groups;
+    const bool single = a.R == 1 && a.T * a.g <= kAttnTileRows;
+    const int x = (single ? blockIdx.x : gridDim.x - 1 - blockIdx.x) / groups;
     const int hk = gi % a.kv_heads, split = gi / a.kv_heads;
     Tile t;
     if (!find_tile<kAttnTileRows>(a, x, t)) return;
@@ -265,14 +272,18 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
                 for (int e = (z - SPREAD) * MAX; e < (z - SPREAD + 1) * MAX; ++e)
                     mx[e & 1] = fmaxf(mx[e & 1], sn[e >> 4][e & 15]);
             }
-            // The loads one by one: together they would hold up the steps behind them.  Tiles behind the
-            // last one are the last again: their buffers are not read.
-            constexpr int GAP = (STEPS - 2) / (2 * NI), at = z - 1;
+            // The loads one by one: together they would hold up the steps behind them.  With FEW it is the
+            // loads that take the time, and they go first.  Tiles behind the last one are the last again:
+            // their buffers are not read.
+            constexpr int GAP = FEW ? 0 : (STEPS - 2) / (2 * NI), at = z - 1;
             if constexpr (at == 0) find_k(min(i + 2, end - 1), where), pages_k(min(i + 3, end - 1));
             if constexpr (at == NI * GAP) bad_v = find_v(min(i + 1, end - 1), where), pages_v(min(i + 2, end - 1));
-            if constexpr (at >= 0 && at % GAP == 0 && at / GAP < NI)
-                load_k(at / GAP, where, buf);
-            if constexpr (at >= NI * GAP && at % GAP == 0 && at / GAP < 2 * NI) load_v(at / GAP - NI, where, buf ^ 1);
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                if (at == j * GAP) load_k(j, where, buf);
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                if (at == (NI + j) * GAP) load_v(j, where, buf ^ 1);
             __builtin_amdgcn_sched_barrier(0);
         }, std::make_integer_sequence<int, STEPS>{});
         asm volatile("" : "+v"(mx[0]), "+v"(mx[1]));  // made above, not where it turns out to be needed
@@ -346,25 +357,25 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     }
 }
 
-template <class E, int DP>
+template <class E, int DP, bool FEW>
 void launch_dp(const AttnArgs& a, unsigned blocks, hipStream_t s) {
-    if (a.D == DP) k_attn_tile<E, DP, true><<<blocks, 256, 0, s>>>(a);
-    else k_attn_tile<E, DP, false><<<blocks, 256, 0, s>>>(a);
+    if (a.D == DP) k_attn_tile<E, DP, true, FEW><<<blocks, 256, 0, s>>>(a);
+    else k_attn_tile<E, DP, false, FEW><<<blocks, 256, 0, s>>>(a);
 }
 
-template <class E>
+template <class E, bool FEW>
 void launch_e(const AttnArgs& a, unsigned blocks, hipStream_t s) {
-    if (a.D <= 64) launch_dp<E, 64>(a, blocks, s);
-    else if (a.D <= 128) launch_dp<E, 128>(a, blocks, s);
-    else launch_dp<E, 256>(a, blocks, s);
+    if (a.D <= 64) launch_dp<E, 64, FEW>(a, blocks, s);
+    else if (a.D <= 128) launch_dp<E, 128, FEW>(a, blocks, s);
+    else launch_dp<E, 256, FEW>(a, blocks, s);
 }
 
 }  // namespace
 
-void launch_attn_tile(const AttnArgs& a, int dtype, int tiles, hipStream_t s) {
-    const unsigned blocks = unsigned(tiles) * a.kv_heads * a.nsplit;
-    if (dtype == VQMLP_F16) launch_e<F16>(a, blocks, s);
-    else launch_e<BF16>(a, blocks, s);
+void launch_attn_tile(const AttnArgs& a, int dtype, bool few, int tiles, hipStream_t s) {
+    const unsigned blocks = unsigned(tiles) * a.kv_heads * split_slots(a.nsplit, a.R);
+    if (dtype == VQMLP_F16) few ? launch_e<F16, true>(a, blocks, s) : launch_e<F16, false>(a, blocks, s);
+    else few ? launch_e<BF16, true>(a, blocks, s) : launch_e<BF16, false>(a, blocks, s);
 }
 
 }  // namespace vqmlp
