@@ -1,8 +1,16 @@
-// attn_tile.hip -- paged attention for many rows: prompts and prompt chunks (gfx950).
+// attn_tile.hip -- paged attention with the keys in LDS: anything but up to 16 rows of D > 128 (gfx950).
 //
-// The mathematics, the packing of rows and the transposed products are those of attn.hip; here
-// four waves share a tile of 64 keys in LDS and each has 32 rows of its own, 32x32x16
-// matrix-core steps.  Bound by the matrix cores and, beside them, by the exponentials.
+// The mathematics, the packing of rows and the transposed products are those of attn.hip; here four
+// waves share a tile of 64 keys in LDS and each has 32 rows of its own, 32x32x16 matrix-core steps.
+// Every tile goes straight from the cache to LDS, one ahead (keys two ahead), and while the matrix
+// cores make the scores of tile i + 1, the vector unit makes the exponentials of tile i.
+//
+// 128 rows a workgroup and two workgroups a compute unit (one for D > 128): 64 rows a wave would
+// halve the LDS reads, but leave one wave a SIMD and its scores in registers that the vector unit
+// cannot read (630 against 788 TFLOP/s).  512 rows over 33,001 keys, 40/8 heads of 128, FP16: 376 us with
+// the join, 912 TFLOP/s, 83% of a large library product; bound by the clock that the power leaves
+// (1.8 GHz of 2.4) and by exponentials beside the matrix cores, which are busy 45% of the time.  64
+// requests of one token and up to 16,252 keys, BF16: 391 us, 5.5 TB/s, bound by the cache.
 #include "attn.h"
 
 namespace vqmlp {

@@ -375,7 +375,8 @@ vqmlp_status vqmlp_paged_store(int dtype, int T, int kv_heads, int D, int page_s
  * [0, T]; rows from cu_q[R] on give y = 0, lse = -inf.  Cached values a row does not see may be
  * anything where no row of its request sees them; elsewhere they have to be finite.
  * q, y [T][heads][D] with token strides ld_q, ld_y (elements, multiples of 8; 16-byte aligned);
- * lse FP32 [T][heads] or NULL.  heads / kv_heads up to 64, R <= 65536.  max_kv: the longest kv_len
+ * lse FP32 [T][heads] or NULL.  heads / kv_heads up to 64, R <= 65536, T * heads < 2^30 and
+ * T * heads / 128 + R * kv_heads up to 2^24.  max_kv: the longest kv_len
  * that is expected; it chooses the split of the keys, and any value gives a right answer.  The
  * workspace (256-byte aligned, no zero fill) follows vqmlp_paged_attn_workspace of the same
  * description on the same device; two calls that overlap in time need one each. */
@@ -397,8 +398,8 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
 /* ------------------------------------------------------------------ linear attention with decay
  * Per request and value head h (key head h / (v_heads / k_heads)), from the state S [Dk][Dv]:
  *   S_t = exp(g[t][h]) S_{t-1} + k_t v_t^T,   y_t = scale * S_t^T q_t.
- * q, k [T][k_heads][Dk], v, y [T][v_heads][Dv] (F16 or BF16, token strides ld_*: multiples of 8,
- * 16-byte aligned), g FP32 [T][v_heads] (token stride ld_g), the log of the decay: at most 0, -inf
+ * q, k [T][k_heads][Dk], v, y [T][v_heads][Dv] (F16 or BF16, token strides ld_*: multiples of 8 up
+ * to 2^24, 16-byte aligned), g FP32 [T][v_heads] (token stride ld_g), the log of the decay: at most 0, -inf
  * forgets everything before (below -80 it is taken as -80, a factor of 2e-35).  Dk and Dv are
  * multiples of 8 up to 128.  state_in, state_out FP32 [slots][v_heads][Dk][Dv], 16-byte aligned;
  * they may be the same array.  Request r uses slot state_index[r] (NULL: r); a slot outside
@@ -407,7 +408,8 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
  * its slot holds.  A request without new tokens copies its start state.  cu_q is clamped to
  * [0, T]; rows from cu_q[R] on give y = 0.  max_q: the most new tokens of one request that are
  * expected; it chooses the kernel (up to 16: the recurrence token by token; above: chunks of 64
- * tokens on the matrix cores), and any value gives a right answer.  R <= 65536. */
+ * tokens on the matrix cores), and any value gives a right answer.  In chunks scale * (q . k) times
+ * its decay is rounded to dtype once: with F16 it has to stay below 65504.  R <= 65535. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
     float scale;
