@@ -503,6 +503,15 @@ class _OnStream:
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def like(self, t):
+        """A new tensor of t's shape and type, dense whatever t's token stride."""
+        import torch
+
+        if self.stream is None:
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
+        with torch.cuda.stream(self.stream):
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
+
     def call(self, f, *args):
         """f(*args, stream) with the tensors' device current."""
         import torch
@@ -544,7 +553,7 @@ def _need(t, name, device, dtype=None, shape=None, contiguous=True):
         _bad("%s is %s, not %s" % (name, t.dtype, dtype))
     if shape is not None and t.shape != shape and (t.dim() != len(shape) or any(
             s is not None and s != n for s, n in zip(shape, t.shape))):
-        _bad("%s has shape %s, wanted %s" % (name, tuple(t.shape), shape))
+        _bad("%s has shape %s, wanted %s" % (name, tuple(t.shape), tuple(shape)))
     if contiguous and not t.is_contiguous():
         _bad("%s is not contiguous" % name)
     return t.data_ptr()
@@ -609,7 +618,7 @@ class BlockNorm:
         base = y if y is not None else residual
         if base is None:
             _bad("neither y nor residual")
-        dev, shape = base.device, tuple(base.shape)
+        dev, shape = base.device, base.shape
         if len(shape) != 2:
             _bad("y and residual are [T, H]")
         T, H = shape
@@ -643,16 +652,20 @@ class BlockNorm:
             else:
                 d.gate, d.ld_gate = _rows(gate, "gate", dev, shape)
         if residual_out is None:
-            residual_out = on.empty(shape, residual.dtype if residual is not None else x_dtype)
-        elif _dtype(residual_out, "residual_out") != res_kind:
-            _bad("residual_out and residual differ in type")
-        d.res_out, d.ld_res_out = _rows(residual_out, "residual_out", dev, shape)
+            residual_out = on.like(residual if residual is not None else y)
+            d.res_out, d.ld_res_out = residual_out.data_ptr(), H
+        else:
+            if _dtype(residual_out, "residual_out") != res_kind:
+                _bad("residual_out and residual differ in type")
+            d.res_out, d.ld_res_out = _rows(residual_out, "residual_out", dev, shape)
         if self.has_pre:
             if out is None:
-                out = on.empty(shape, x_dtype)
-            elif _dtype(out, "out") != kind:
-                _bad("out and y differ in type")
-            d.x, d.ld_x = _rows(out, "out", dev, shape)
+                out = on.like(y) if y is not None else on.empty(shape, x_dtype)
+                d.x, d.ld_x = out.data_ptr(), H
+            else:
+                if _dtype(out, "out") != kind:
+                    _bad("out and y differ in type")
+                d.x, d.ld_x = _rows(out, "out", dev, shape)
         elif out is not None:
             _bad("out without pre_weight")
         on.call(lib().vqmlp_block_norm, C.byref(d))
@@ -684,6 +697,8 @@ class PagePlanner:
         self.R, self.device, self.max_tokens = table.shape[0], dev, max_tokens
         self.table, self.free_pages, self.free_head = table, free_pages, free_head
         self.page_size, self.n_pages = page_size, n_pages
+        self._sizes = [self.R, self.R + 1, max_tokens, max_tokens, 4]  # of a plan's parts
+        self._total = sum(self._sizes)
         self._desc = _PagesDesc(R=self.R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
                                 n_free=free_pages.numel(), table_width=table.shape[1],
                                 ld_table=table.stride(0) if self.R > 1 else table.shape[1],
@@ -698,8 +713,8 @@ class PagePlanner:
     def _empty_plan(self, on):
         import torch
 
-        sizes = [self.R, self.R + 1, self.max_tokens, self.max_tokens, 4]
-        return PagePlan(*on.empty((sum(sizes),), torch.int32).split(sizes))
+        buf = on.empty((self._total,), torch.int32)
+        return PagePlan(*torch.split_with_sizes(buf, self._sizes))
 
     def forward(self, ctx_len, q_len, plan=None, free_head_out=None, stream=None):
         """ctx_len, q_len [R] int32 on the device -> PagePlan (plan: buffers to reuse)."""
@@ -712,8 +727,11 @@ class PagePlanner:
         on = _OnStream(stream, dev)
         if plan is None:
             plan = self._empty_plan(on)
-            d.seq_len, d.cu_q, d.slot, d.position, d.status = (
-                x.data_ptr() for x in (plan.seq_len, plan.cu_q, plan.slot, plan.position, plan.status))
+            at = d.seq_len = plan.seq_len.data_ptr()
+            d.cu_q = at = at + 4 * self.R
+            d.slot = at = at + 4 * (self.R + 1)
+            d.position = at = at + 4 * self.max_tokens
+            d.status = at + 4 * self.max_tokens
         else:
             d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self.R,))
             d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self.R + 1,))
@@ -807,10 +825,12 @@ class PagedCache:
         d = self._attn_desc(T, R, heads, table.shape[1], window, max_kv, scale)
         d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self.D))
         if y is None:
-            y = on.empty((T, heads, self.D), q.dtype)
-        elif _dtype(y, "y") != self.dtype:
-            _bad("y and the cache differ in type")
-        d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self.D))
+            y = on.like(q)
+            d.y, d.ld_y = y.data_ptr(), heads * self.D
+        else:
+            if _dtype(y, "y") != self.dtype:
+                _bad("y and the cache differ in type")
+            d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self.D))
         if lse is None and with_lse:
             lse = on.empty((T, heads), torch.float32)
         if lse is not None:
@@ -885,21 +905,25 @@ class LinearAttention:
             _bad("g is %s, not %s" % (g.dtype, f))
         d.g, d.ld_g = _rows(g, "g", dev, (T, self.v_heads))
         if y is None:
-            y = on.empty((T, self.v_heads, self.Dv), q.dtype)
-        elif _dtype(y, "y") != dt:
-            _bad("y and q differ in type")
-        d.y, d.ld_y = _rows(y, "y", dev, (T, self.v_heads, self.Dv))
+            y = on.like(v) if v.dtype == q.dtype else on.empty(v.shape, q.dtype)
+            d.y, d.ld_y = y.data_ptr(), self.v_heads * self.Dv
+        else:
+            if _dtype(y, "y") != dt:
+                _bad("y and q differ in type")
+            d.y, d.ld_y = _rows(y, "y", dev, (T, self.v_heads, self.Dv))
         shape = (state.shape[0], self.v_heads, self.Dk, self.Dv)
         d.state_in = _need(state, "state", dev, f, shape)
         if state_out is None:
-            state_out = on.empty(shape, f)
+            state_out = on.like(state)
             if state_index is not None or shape[0] > R:
                 if stream is None:
                     state_out.copy_(state)
                 else:
                     with torch.cuda.stream(stream):
                         state_out.copy_(state)
-        d.state_out = _need(state_out, "state_out", dev, f, shape)
+            d.state_out = state_out.data_ptr()
+        else:
+            d.state_out = _need(state_out, "state_out", dev, f, shape)
         d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
         if ctx_len is not None:
             d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (R,))
