@@ -29,7 +29,7 @@ struct LinArgs {
     const float* sin;
     float* sout;
     const int32_t *cu, *ctx, *index;
-    float* seg;   // [unit][v_heads][Dk][Dv] states of segments (split launches only)
+    float* seg;   // [unit][v_heads] states of segments, padded and in pieces (split launches only)
     float* dec;   // [unit][v_heads] decay over a segment
     int64_t ld_q, ld_k, ld_v, ld_y, ld_g;
     int T, R, hk, hv, Dk, Dv, n_states, L;
@@ -296,7 +296,11 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     const int slot = lin_slot(a, u.r, &old);
     const int64_t ss = int64_t(a.Dk) * a.Dv;
     const int64_t sbase = (int64_t(max(slot, 0)) * a.hv + h) * ss;
-    auto seg_state = [&](int unit) { return a.seg + (int64_t(unit) * a.hv + h) * ss; };
+    // A segment's state: what a lane holds as 16-byte pieces, a wave's 1 KB pieces one after another.
+    const uint32_t seg_off = (wave * KS * 2 * NTV * 64 + lane) * 16;
+    auto seg_state = [&](int unit) {
+        return reinterpret_cast<uint8_t*>(a.seg) + (int64_t(unit) * a.hv + h) * (DKP * 64 * NTV * 4);
+    };
 
     // state element (pair p, tile b, column tile v, i): dk = 32 p + 8 g4 + 4 b + i, dv = dvc(v)
     auto dvc = [&](int v, int m) {
@@ -313,6 +317,22 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                     const int dk = 32 * p + 8 * g4 + 4 * b, dv = dvc(v, lr);
                     if (dk < a.Dk && dv < a.Dv) f(S[p][b][v], int64_t(dk) * a.Dv + dv);
                 }
+    };
+    auto each_piece = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) f(S[p][b][v], ((p * 2 + b) * NTV + v) * 1024);
+    };
+    auto store_seg = [&](int unit, float mul) __attribute__((always_inline)) {
+        uint8_t* const dst = seg_state(unit);
+        each_piece([&](f32x4& x, int at) { *reinterpret_cast<f32x4*>(dst + at + seg_off) = x * mul; });
+    };
+    auto load_seg = [&](int unit) __attribute__((always_inline)) {
+        const uint8_t* const src = seg_state(unit);
+        each_piece([&](f32x4& x, int at) { x = *reinterpret_cast<const f32x4*>(src + at + seg_off); });
     };
     auto load_state = [&](const float* src) __attribute__((always_inline)) {
         each_state([&](f32x4& x, int64_t at) {
@@ -338,22 +358,23 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         if (u.seg == 0 || u.seg == u.nseg - 1) {
             if (old) load_state(a.sin + sbase);
             if (u.seg == u.nseg - 1) {
-                store_state(seg_state(u.first + u.seg), 1.f);
+                store_seg(u.first + u.seg, 1.f);
                 return;
             }
         }
     } else if (u.nseg == 1) {
         if (old) load_state(a.sin + sbase);
     } else if (u.seg == 0) {
-        load_state(seg_state(u.first + u.nseg - 1));
+        load_seg(u.first + u.nseg - 1);
     } else {
-        load_state(seg_state(u.first));
+        load_seg(u.first);
         for (int j = 1; j < u.seg; ++j) {
             const float dj = a.dec[int64_t(u.first + j) * a.hv + h];
-            const float* src = seg_state(u.first + j);
-            each_state([&](f32x4& x, int64_t at) {
+            const uint8_t* const src = seg_state(u.first + j);
+            each_piece([&](f32x4& x, int at) {
+                const f32x4 z = *reinterpret_cast<const f32x4*>(src + at + seg_off);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], dj, src[at + int64_t(i) * a.Dv]);
+                for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], dj, z[i]);
             });
         }
     }
@@ -434,6 +455,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     auto qk_read = [&](const uint16_t* p, int r, int s) {
         return *reinterpret_cast<const u32x4*>(p + r * DKP + 8 * ((4 * s + g4) ^ swz(r)));
     };
+    const bool last = uniform(u.seg == u.nseg - 1 && slot >= 0);  // has the request's final state to write
     float decay = 1.f;  // over the segment so far (!OUT)
     int e = 0;          // S is kept in units of 2^-e
     if (t0 < t1) {
@@ -582,7 +604,8 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 }
             }
         }
-        // the state after the chunk
+        // the state after the chunk, which nobody needs behind a segment's last unless it is the request's
+        if (OUT && t + kC >= t1 && !last) continue;
         int en = e;
         if constexpr (HALF) {
             typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -673,9 +696,9 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     }
     // no load to LDS is in flight here: each was waited for in the chunk that it was made for
     if (!OUT) {
-        store_state(seg_state(u.first + u.seg), pow2(-e));
+        store_seg(u.first + u.seg, pow2(-e));
         if (tid == 0) a.dec[int64_t(u.first + u.seg) * a.hv + h] = decay;
-    } else if (u.seg == u.nseg - 1 && slot >= 0) {
+    } else if (last) {
         store_state(a.sout + sbase, pow2(-e));
     }
 }
@@ -712,7 +735,7 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     }
     G.units = d.T / G.L + d.R + 1;
     if (G.split) {
-        G.dec = align256(size_t(G.units) * d.v_heads * d.Dk * d.Dv * 4);
+        G.dec = align256(size_t(G.units) * d.v_heads * (d.Dk <= 64 ? 64 : 128) * (d.Dv <= 64 ? 64 : 128) * 4);
         G.bytes = G.dec + align256(size_t(G.units) * d.v_heads * 4);
     }
     return G;
