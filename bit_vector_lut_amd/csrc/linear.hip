@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     const int kget = tok_at(8 * (lr >> 2) + (lr & 3), g4), vget = tok_at(dvc(0, lr), g4);
     const int put = tok_at(8 * cj, bi);
     u32x4 blk[8];
-    // of the chunk after the one in work: g of token `lane` (wave 0), of token 63 - `lane` (wave 1)
+    // of the chunk after the one in work: g of token `lane` (wave 2), of token 63 - `lane` (wave 3)
     float gv = 0.f;
     // One of the eight loads of the chunk at token t.  A wave's loads go out one by one between its
     // matrix-core steps: eight in a row keep it from issuing anything else for over a thousand cycles.
@@ -409,17 +409,17 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         }
     };
     auto fetch_g = [&](int t) __attribute__((always_inline)) {
-        if (wave > 1) return;
+        if (wave < 2) return;
         const uint8_t* const base = reinterpret_cast<const uint8_t*>(a.g + (u.c0 + t) * a.ld_g + h);
-        const int i = wave ? 63 - lane : lane;
+        const int i = wave == 3 ? 63 - lane : lane;
         gv = t + i < t1 ? fmaxf(*reinterpret_cast<const float*>(base + uint32_t(i) * uint32_t(a.ld_g) * 4), kMinG) : 0.f;
     };
     // sums from the front for e^{b}, from the back for the tails, each accurate against its own size
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
-        if (wave > 1) return;
+        if (wave < 2) return;
         const float b = lane_scan(gv, 0.f, [](float x, float y) { return x + y; });
         const float eb = exp_f32(b);
-        if (wave == 0) {
+        if (wave == 2) {
             d.eb[lane] = eb;
             d.bl[lane] = b * kLog2e;
             if (lane == 63) d.etot = eb;
@@ -428,26 +428,23 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
             d.tail[lane == 63 ? 63 : 62 - lane] = lane == 63 ? 1.f : eb;
         }
     };
-    // Q and K rows of a chunk, token by token, straight to LDS; behind the last token the last again
-    constexpr int RPI = 512 / DKP, NI = kC / RPI / 4;  // rows per load, loads per wave of one of the two
+    // Q rows of a chunk, token by token, straight to LDS; behind the last token the last again
+    constexpr int RPI = 512 / DKP, NI = kC / RPI / 4;  // rows per load, loads per wave
     auto swz = [](int row) { return DKP == 64 ? (row >> 1) & 7 : row & 15; };
-    auto stage_qk = [&](int t, int j) __attribute__((always_inline)) {  // load j of NI of each
+    auto stage_q = [&](int t, int j) __attribute__((always_inline)) {  // load j of NI
         if constexpr (OUT) {
-            const uint32_t ql = lds_byte(so.q) + (wave * NI + j) * 1024, kl = lds_byte(so.k) + (wave * NI + j) * 1024;
+            const uint32_t ql = lds_byte(so.q) + (wave * NI + j) * 1024;
             const uint8_t* const q = reinterpret_cast<const uint8_t*>(a.q + (u.c0 + t) * a.ld_q + int64_t(hk) * a.Dk);
-            const uint8_t* const k = reinterpret_cast<const uint8_t*>(a.k + (u.c0 + t) * a.ld_k + int64_t(hk) * a.Dk);
-            const uint32_t lq = uint32_t(a.ld_q) * 2, lk = uint32_t(a.ld_k) * 2;
+            const uint32_t lq = uint32_t(a.ld_q) * 2;
             const int r0 = lane / (DKP / 8);
             const int first = (wave * NI + j) * RPI;  // a multiple of RPI: its low bits are j's
             int chunk = (lane % (DKP / 8)) ^ swz(r0) ^ swz(j * RPI);
-            if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros on the other side
+            if (8 * chunk >= a.Dk) chunk = 0;  // meets zeros of K
             if (t + kC <= t1) {
                 load_lds16(q + int64_t(first) * lq, r0 * lq + 16 * chunk, ql);
-                load_lds16(k + int64_t(first) * lk, r0 * lk + 16 * chunk, kl);
             } else {
                 const int r = min(first + r0, t1 - 1 - t);
                 load_lds16(q, r * lq + 16 * chunk, ql);
-                load_lds16(k, r * lk + 16 * chunk, kl);
             }
         }
     };
@@ -463,7 +460,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) fetch(t0, i);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) stage_qk(t0, j);
+        for (int j = 0; j < NI; ++j) stage_q(t0, j);
         decays(sm.d[0]);
         fetch_g(t0 + kC);
     }
@@ -479,8 +476,15 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                     w[i] = __builtin_amdgcn_perm(blk[2 * i + 1][cc / 2], blk[2 * i][cc / 2], sel);
                 *reinterpret_cast<u32x4*>(&(isk ? sm.kt : sm.vt)[(put ^ tok_bits(cc, 0)) + cc * kC * 2]) = w;
             }
+            if constexpr (OUT) {
+                if (isk) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<u32x4*>(so.k + (8 * bi + i) * DKP + 8 * (cj ^ swz(8 * bi + i))) = blk[i];
+                }
+            }
         }
-        wait_loads();  // this wave's part of Q and K is in LDS
+        wait_loads();  // this wave's part of Q is in LDS
         __syncthreads();
         f32x4 o[NTV][4];
         if constexpr (OUT) {
@@ -489,7 +493,6 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 kf[s] = qk_read(so.k, 16 * wave + lr, s);
-                if (32 * s + 8 * g4 >= a.Dk) kf[s] = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) qf[x][s] = qk_read(so.q, 16 * x + lr, s);
             }
@@ -514,6 +517,9 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 *reinterpret_cast<u32x2*>(&so.p[16 * x + lr][16 * wave + 4 * g4]) =
                     u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
             }
+            // the next chunk's decays, by the waves with the fewest scores
+            decays(sm.d[((t - t0) / kC + 1) & 1]);
+            fetch_g(t + 2 * kC);
             // e^{b} S^T Q
             if constexpr (HALF) {
                 float mx = 0.f;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
         if constexpr (OUT) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                if (x < NI && t + kC < t1) stage_qk(t + kC, x);
+                if (x < NI && t + kC < t1) stage_q(t + kC, x);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int c = 0; c <= x / 2; ++c) {
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
                 for (int v = 0; v < NTV; ++v)
                     S[p][b][v] = E::mfma16(kk[z / 2 & 1][z & 1], part[c][v][q], S[p][b][v]);
             if constexpr (z < 2 * KS && z % KS == 0 && z / KS < NTV) parts(1, z / KS);
-            if constexpr (z == 2 * KS) {  // between products, which hide the lane moves' waits
+            if constexpr (!OUT && z == 2 * KS) {  // between products, which hide the lane moves' waits
                 decays(sm.d[((t - t0) / kC + 1) & 1]);
                 fetch_g(t + 2 * kC);
             }
