@@ -201,14 +201,16 @@ struct alignas(16) LinDecay {  // of one chunk; b = sum of g up to a token
     float tail[kC];          // e^(sum behind the token)
     float etot;              // e^(sum of the chunk)
 };
+template <int DKP, int DVP>
 struct LinSmem {
-    __attribute__((aligned(256))) uint8_t kt[128 * kC * 2];  // [dk][token], tok_at
-    __attribute__((aligned(256))) uint8_t vt[128 * kC * 2];  // [dv][token]
+    __attribute__((aligned(256))) uint8_t kt[DKP * kC * 2];  // [dk][token], tok_at
+    __attribute__((aligned(256))) uint8_t vt[DVP * kC * 2];  // [dv][token]
     LinDecay d[2];           // of this chunk and the next
 };
+template <int DKP>
 struct LinOutSmem {
     uint16_t p[kC][kTok];                        // [query][key] scores
-    __attribute__((aligned(1024))) uint16_t q[kC * 128], k[kC * 128];  // rows of tokens, chunks permuted
+    __attribute__((aligned(1024))) uint16_t q[kC * DKP], k[kC * DKP];  // rows of tokens, chunks permuted
 };
 
 // Prefix over the 64 lanes with data-parallel moves: within rows of 16 lanes, then across them.
@@ -263,14 +265,19 @@ __device__ __forceinline__ bool lin_unit(const LinArgs& a, int x, LinUnit& u) {
     return u.seg >= 0 && u.seg < u.nseg;
 }
 
+// Workgroups a compute unit holds: three where LDS allows it.  48 heads of 64 x 64, 12,000 tokens: 116 us
+// with two, 98 with three; of 64 x 128, 5,000 tokens: 75 and 73, though a few registers go to memory.
+constexpr int lin_resident(int dkp) { return dkp == 64 ? 3 : 2; }
+
 // OUT: outputs and the final state; otherwise the states of the segments, for a later OUT launch.
 template <class E, int DKP, int NTV, bool OUT>
-__global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
+__global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a) {
     constexpr int KS = DKP / 32;       // steps over dk, pairs of state row tiles
+    constexpr int DVP = 64 * NTV;
     constexpr bool HALF = __is_same(E, F16);
     constexpr int PARTS = HALF ? 2 : 3;
-    __shared__ LinSmem sm;
-    __shared__ __attribute__((aligned(1024))) std::conditional_t<OUT, LinOutSmem, char> so;
+    __shared__ LinSmem<DKP, DVP> sm;
+    __shared__ __attribute__((aligned(1024))) std::conditional_t<OUT, LinOutSmem<DKP>, char> so;
     // Workgroups go round the eight XCDs; those of the value heads that read the same queries and keys
     // are 8 apart, on one XCD, one after another.
     const int heads = a.hv / a.hk;
@@ -280,7 +287,6 @@ __global__ void __launch_bounds__(256, 2) k_lin_chunk(LinArgs a) {
     if (!lin_unit(a, pair / a.hk, u)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int lr = lane & 15, g4 = lane >> 4;
-    const int DVP = 64 * NTV;
     const int t0 = u.seg * a.L, t1 = min(u.n, t0 + a.L);
     if (u.r == a.R) {  // rows behind the last request
         if (OUT)
@@ -723,20 +729,25 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     G.step = d.max_q <= kStepMaxQ;
     if (G.step) return G;
     // Segments of a request go through at once, at the price of a pass for their states first (0.6 of
-    // the time of the outputs' pass), of three chunks' worth of time to start and end each, and of 0.6
+    // the time of the outputs' pass), of three chunks' worth of time to start and end each, and of 0.13
     // for each earlier segment whose state an output segment takes in.  The unit is a chunk in a round
-    // of two workgroups on every compute unit.  8,000 tokens of 48 heads of 128 x 128: 178 us with the
-    // 13 chunks that this chooses, 220 / 197 / 189 / 208 with 9 / 12 / 16 / 18.
+    // that fills every compute unit; one workgroup alone on a unit gets through it in 3/4 of the time of
+    // two together.  8,000 tokens of heads of 128 x 128, 48 heads: 149 us with the 13 chunks that this
+    // chooses, 161 / 177 / 160 / 176 with 8 / 10 / 15 / 18; 4 heads: 55 with 4, 59 / 67 / 86 with 6 / 8 / 12.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
-    const int chunks = (most + kC - 1) / kC;
-    const int64_t slots = 2 * int64_t(cus);
-    auto rounds = [&](int64_t units) { return double((units * d.v_heads + slots - 1) / slots); };
+    const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128);
+    const int64_t slots = held * int64_t(cus);
+    auto rounds = [&](int64_t units) {
+        const int64_t n = units * d.v_heads, rest = n % slots, per = (5 * rest + 4 * cus - 1) / (4 * cus);
+        return double(n / slots) + (rest ? 0.5 + 0.5 * double(std::min<int64_t>(per, held)) / held : 0.0);
+    };
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kC - 1) / kC) * kC;
     double best = rounds(d.R) * (chunks + 3);
+    const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
     for (int n = 4; n < chunks; ++n) {
-        const int64_t units = d.R == 1 ? (chunks + n - 1) / n : d.T / (n * kC) + d.R / 2;
-        const double cost = rounds(std::max<int64_t>(units, d.R)) * (1.6 * n + 6) + 0.6 * ((chunks - 1) / n);
+        const int64_t units = even ? int64_t(d.R) * ((chunks + n - 1) / n) : d.T / (n * kC) + d.R / 2;
+        const double cost = rounds(std::max<int64_t>(units, d.R)) * (1.6 * n + 6 + 0.13 * ((chunks - 1) / n));
         if (cost < best) best = cost, G.split = true, G.L = n * kC;
     }
     G.units = d.T / G.L + d.R + 1;
