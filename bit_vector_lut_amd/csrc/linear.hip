@@ -55,20 +55,21 @@ __device__ __forceinline__ int lin_slot(const LinArgs& a, int r, bool* old) {
 }
 
 // ---------------------------------------------------------------- the recurrence
-// A wave owns a head's Dk x 32 columns of the state: lane = (row block lane / 8, four columns of
-// lane % 8), rows of a block contiguous so that a token's q and k come as 16-byte chunks.  The sum
+// A wave owns a head's Dk x 32 (or 16) columns of the state: lane = (row block, four columns), the eight
+// (or sixteen) row blocks' rows contiguous so that a token's q and k come as 16-byte chunks.  The sum
 // over rows is a lane's own rows, then lane swaps; no LDS and no barrier, so that a wave's loads are
 // all that is in flight.
-// Two tokens are on their way while one is in work (8 tokens of 48 heads of 128 x 128: 10.9 us in a
-// graph, 11.7 with four, which leave two waves a SIMD; with single tokens one is as good).  64 requests
-// of one token: 88 us, 4.6 TB/s, the rate of a large copy.
-template <class E, int RPL>  // rows per lane: Dk <= 8 RPL
+// Two tokens are on their way while one is in work (8 tokens of 48 heads of 128 x 128, 32 columns a
+// wave: 10.9 us in a graph, 11.7 with four, which leave two waves a SIMD; with single tokens one is as
+// good).  64 requests of one token: 88 us, 4.6 TB/s, the rate of a large copy.
+template <class E, int RPL, int RB>  // rows per lane, row blocks: Dk <= RPL RB
 __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
+    constexpr int CB = 64 / RB;
     const int r = blockIdx.x, h = blockIdx.y;
-    const int lane = threadIdx.x, cb = lane & 7, rb = lane >> 3;
-    const int col = blockIdx.z * 32 + cb * 4, row0 = rb * RPL;
+    const int lane = threadIdx.x, cb = lane % CB, rb = lane / CB;
+    const int col = (blockIdx.z * CB + cb) * 4, row0 = rb * RPL;
     if (r == a.R) {  // rows behind the last request
-        for (int64_t t = lin_row(a, a.R) + rb; t < a.T; t += 8)
+        for (int64_t t = lin_row(a, a.R) + rb; t < a.T; t += RB)
             if (col < a.Dv) *reinterpret_cast<u32x2*>(a.y + t * a.ld_y + int64_t(h) * a.Dv + col) = u32x2{0, 0};
         return;
     }
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
                     acc[i] = fmaf(qq, z[i], acc[i]);
                 }
             }
-        // Sums over the eight row blocks, four columns at once: a swap of halves (then of rows of 16
+        // Sums over the row blocks, four columns at once: a swap of halves (then of rows of 16
         // lanes) puts the two parts of one sum side by side with those of another.
         auto pair = [](float x, float y, auto&& swap) __attribute__((always_inline)) {
             const auto z = swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
@@ -126,8 +127,10 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
         auto row = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
         float sum = pair(pair(acc[0], acc[1], half), pair(acc[2], acc[3], half), row);
         sum += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, sum), 0x128, 0xF, 0xF, false));
-        // 16-lane row 0, 1, 2, 3 has column 0, 2, 1, 3 of the lane's four, twice
-        if (!(lane & 8) && cin)
+        if constexpr (RB == 16)
+            sum += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, sum), 0x124, 0xF, 0xF, false));
+        // 16-lane row 0, 1, 2, 3 has column 0, 2, 1, 3 of the lane's four, RB / 4 times
+        if ((lane & 15) < CB && cin)
             a.y[int64_t(t) * a.ld_y + int64_t(h) * a.Dv + col + (lane >> 4 & 1) * 2 + (lane >> 5)] =
                 uint16_t(bits16<E>(sum * a.scale));
     };
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
 // ---------------------------------------------------------------- host half
 
 struct LinGeom {
-    bool step;
+    bool step, narrow;  // recurrence; of it, 16 columns a wave
     int L, units;  // tokens per segment (the whole request when not split), unit numbers
     bool split;
     size_t dec, bytes;
@@ -727,7 +730,13 @@ struct LinGeom {
 LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     LinGeom G{};
     G.step = d.max_q <= kStepMaxQ;
-    if (G.step) return G;
+    if (G.step) {
+        // Half the columns and rows a lane where waves of 32 columns are fewer than the chip's SIMDs: one
+        // request of 8 tokens, 48 heads of 128 x 128: 11.0 -> 9.5 us in a graph, of 16: 16.7 -> 13.0, four of
+        // one: 8.0 -> 7.5; beyond, half lines of the state cost more: 16 of one 18.8 -> 21.2, 64: 88 -> 126.
+        G.narrow = d.Dk > 64 && int64_t(d.R) * d.v_heads * ((d.Dv + 31) / 32) <= 4 * int64_t(cus);
+        return G;
+    }
     // Segments of a request go through at once, at the price of a pass for their states first (0.6 of
     // the time of the outputs' pass), of three chunks' worth of time to start and end each, and of 0.13
     // for each earlier segment whose state an output segment takes in.  The unit is a chunk in a round
@@ -775,10 +784,11 @@ vqmlp_status lin_check(const vqmlp_linear_desc* p, const char* who) {
 }
 
 template <class E>
-void launch_step(const LinArgs& a, hipStream_t s) {
+void launch_step(const LinArgs& a, bool narrow, hipStream_t s) {
     const dim3 grid(a.R + 1, a.hv, (a.Dv + 31) / 32);
-    if (a.Dk <= 64) k_lin_step<E, 8><<<grid, 64, 0, s>>>(a);
-    else k_lin_step<E, 16><<<grid, 64, 0, s>>>(a);
+    if (a.Dk <= 64) k_lin_step<E, 8, 8><<<grid, 64, 0, s>>>(a);
+    else if (narrow) k_lin_step<E, 8, 16><<<dim3(a.R + 1, a.hv, (a.Dv + 15) / 16), 64, 0, s>>>(a);
+    else k_lin_step<E, 16, 8><<<grid, 64, 0, s>>>(a);
 }
 
 template <class E, bool OUT>
@@ -799,7 +809,7 @@ void launch_chunk(LinArgs a, int units, hipStream_t s) {
 
 template <class E>
 void launch_linear(const LinArgs& a, const LinGeom& G, hipStream_t s) {
-    if (G.step) return launch_step<E>(a, s);
+    if (G.step) return launch_step<E>(a, G.narrow, s);
     if (G.split) launch_chunk<E, false>(a, G.units, s);
     launch_chunk<E, true>(a, G.units, s);
 }

@@ -671,6 +671,19 @@ def test_linear_attention_segments(vq, torch_dev, dtype, in_place):
     _linear_check(vq, torch_dev, dtype, [1290], 1, 1, 128, 128, max_q=512, in_place=in_place)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(72, 40), (40, 128), (128, 40), (128, 128), (64, 64)])
+def test_linear_attention_segments_of_odd_heads(vq, torch_dev, dtype, dk, dv):
+    _linear_check(vq, torch_dev, dtype, [1290, 77, 700], 1, 2, dk, dv, ctx=[2, 0, 1], seed=11, pad=1)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (104, 96), (72, 40), (128, 8)])
+def test_linear_attention_recurrence_few_and_many_waves(vq, torch_dev, dtype, dk, dv):
+    _linear_check(vq, torch_dev, dtype, [8, 1, 0, 16], 1, 2, dk, dv, 16, ctx=[1, 0, 3, 7], seed=12, pad=2)
+    _linear_check(vq, torch_dev, dtype, [1, 2, 0] * 23, 2, 16, dk, dv, 2, seed=13)
+
+
 @pytest.mark.parametrize("lens,max_q", [([5, 1, 3], 8), ([100, 1, 66], 100)])
 def test_linear_attention_slots_and_fresh_requests(vq, torch_dev, lens, max_q):
     torch = torch_dev
