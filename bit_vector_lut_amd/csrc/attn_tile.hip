@@ -24,10 +24,11 @@ constexpr int kKT = 64;   // keys of a tile
 // 37 to 1,000 rows: 197 us with four places, 98 with three).  A single request fills all of its splits.
 __host__ __device__ inline int split_slots(int nsplit, int requests) { return requests == 1 ? nsplit : nsplit | 1; }
 
-// FEW: few rows a request, so that the time goes into reading keys and values.
-template <class E, int DP, bool FULL, bool FEW>
+// DP: a row of keys in LDS, DM: the part of it that the products take in (D <= DM).  FEW: few rows a request,
+// so that the time goes into reading keys and values.
+template <class E, int DP, int DM, bool FULL, bool FEW>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a) {
-    constexpr int KS = DP / 16, DB = DP / 32, NI = DP / 32;
+    constexpr int KS = DM / 16, DB = DM / 32, NI = DP / 32;
     constexpr int RPI = 512 / DP;        // key rows per load instruction
     constexpr int TILE = kKT * DP * 2;   // bytes
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2 * TILE];
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         return __any(!in_cache(vp[0]));
     };
     auto load_v = [&](int j, const Source& x, int buf) __attribute__((always_inline)) {
+        if (DM < DP && wave == 3) return;  // rows that no product reads
         int d = (wave * NI + j) * 8 + vrow;
         if (!FULL) d = min(d, D - 1);
         // even or odd as wave * NI + j is; NI is even
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         // ahead, since a read takes longer than a step, and the vector work stands between them: the
         // exponentials of keys 16 q .. 16 q + 15 before the value product of those keys.  The barriers
         // keep the compiler from gathering the reads right in front of their steps.
-        constexpr int QK = 2 * KS, STEPS = QK + 4 * DB, SPREAD = QK + DB, MAX = 32 / (2 * DB);
+        constexpr int QK = 2 * KS, STEPS = QK + 4 * DB, SPREAD = QK + DB, MAX = (32 + 2 * DB - 1) / (2 * DB);
         u32x4 pf[4], fr[2][4];
         Source where;
         float sum[2] = {0.f, 0.f}, p[2];
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
             }
             if constexpr (z >= SPREAD && z < SPREAD + 2 * DB) {
 #pragma unroll
-                for (int e = (z - SPREAD) * MAX; e < (z - SPREAD + 1) * MAX; ++e)
+                for (int e = (z - SPREAD) * MAX; e < (z - SPREAD + 1) * MAX && e < 32; ++e)
                     mx[e & 1] = fmaxf(mx[e & 1], sn[e >> 4][e & 15]);
             }
             // The loads one by one: together they would hold up the steps behind them.  With FEW it is the
@@ -367,8 +369,13 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
 
 template <class E, int DP, bool FEW>
 void launch_dp(const AttnArgs& a, unsigned blocks, hipStream_t s) {
-    if (a.D == DP) k_attn_tile<E, DP, true, FEW><<<blocks, 256, 0, s>>>(a);
-    else k_attn_tile<E, DP, false, FEW><<<blocks, 256, 0, s>>>(a);
+    // Heads of up to three quarters of the LDS row leave the last quarter's products out: 512 rows over 16,001
+    // keys, 24/4 heads of 192: 297 -> 254 us, of 96: 138 -> 120.  Where loads bound it, the wave that has
+    // fewer of them costs more (64 requests of one token, heads of 96: 325 -> 348).
+    constexpr int DM = !FEW && DP > 64 ? DP / 4 * 3 : DP;
+    if (a.D == DP) k_attn_tile<E, DP, DP, true, FEW><<<blocks, 256, 0, s>>>(a);
+    else if (a.D <= DM) k_attn_tile<E, DP, DM, false, FEW><<<blocks, 256, 0, s>>>(a);
+    else k_attn_tile<E, DP, DP, false, FEW><<<blocks, 256, 0, s>>>(a);
 }
 
 template <class E, bool FEW>

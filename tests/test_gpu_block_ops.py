@@ -432,6 +432,14 @@ def test_paged_attention_tiles(vq, torch_dev, dtype, lens, heads, kv_heads, D, p
     _attn_check(vq, torch_dev, _t(torch_dev, dtype), lens, heads, kv_heads, D, page, window, seed=D + 1, pad=3)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [72, 80, 96, 104, 136, 160, 192, 208])
+def test_paged_attention_tiles_of_odd_heads(vq, torch_dev, dtype, D):
+    """Heads that leave a part of a tile's row empty, a little or more than a quarter."""
+    _attn_check(vq, torch_dev, _t(torch_dev, dtype), [(150, 700), (70, 70), (1, 9)], 4, 2, D, 16, seed=D, pad=2)
+    _attn_check(vq, torch_dev, _t(torch_dev, dtype), [(129, 300)], 2, 2, D, 32, window=50, seed=D + 1)
+
+
 @pytest.mark.parametrize("lens,D", [([(150, 700), (40, 900)], 128), ([(60, 1500)], 256), ([(2, 1500)], 256)])
 def test_paged_attention_tiles_skip_pages_outside_the_cache(vq, torch_dev, lens, D):
     """Holes inside a request's keys, at its start and at its end, next to whole tiles."""
