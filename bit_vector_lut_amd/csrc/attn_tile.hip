@@ -28,7 +28,7 @@ __host__ __device__ inline int split_slots(int nsplit, int requests) { return re
 // so that the time goes into reading keys and values.
 template <class E, int DP, int DM, bool FULL, bool FEW>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a) {
-    constexpr int KS = DM / 16, DB = DM / 32, NI = DP / 32;
+    constexpr int KS = DM / 16, DB = DM / 32, NI = DP / 32, NV = DM / 32;  // loads of K and V a wave and tile
     constexpr int RPI = 512 / DP;        // key rows per load instruction
     constexpr int TILE = kKT * DP * 2;   // bytes
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf[2 * TILE];
@@ -88,9 +88,10 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
     // [key][D] and V as [d][64 keys], the 16-byte chunks of a row permuted by an exclusive or, so
     // that sixteen neighbouring lanes of an operand read touch all 64 banks.
     auto kf = [](int key) { return DP == 64 ? (key >> 1) & 7 : key & 15; };
-    const uint32_t klds = lds_byte(kbuf) + wave * NI * 1024, vlds = lds_byte(vbuf) + wave * NI * 1024;
+    const uint32_t klds = lds_byte(kbuf) + wave * NI * 1024, vlds = lds_byte(vbuf) + wave * NV * 1024;
     const int vrow = lane >> 3;
-    const int vchunk = (lane & 7) ^ (vrow >> 1);  // of even loads; odd ones are four chunks away
+    // of a wave's even loads; odd ones are four chunks away, as are rows that are eight apart
+    const int vchunk = (lane & 7) ^ (vrow >> 1) ^ (wave * NV & 1) * 4;
     int kp[2] = {0, 0}, vp[2] = {0, 0};
     auto pages_k = [&](int kt) {
         kp[0] = page_of(kt * kKT + 16 * wave);
@@ -137,10 +138,8 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         return __any(!in_cache(vp[0]));
     };
     auto load_v = [&](int j, const Source& x, int buf) __attribute__((always_inline)) {
-        if (DM < DP && wave == 3) return;  // rows that no product reads
-        int d = (wave * NI + j) * 8 + vrow;
+        int d = (wave * NV + j) * 8 + vrow;
         if (!FULL) d = min(d, D - 1);
-        // even or odd as wave * NI + j is; NI is even
         load_lds16(x.v[j & 1] + (int64_t(d) << a.shift), vlds + buf * TILE + j * 1024);
     };
     auto stage_k = [&](int kt, int buf) {
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         Source x;
         const bool bad = find_v(kt, x);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) load_v(j, x, buf);
+        for (int j = 0; j < NV; ++j) load_v(j, x, buf);
         return bad;
     };
 
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
         __syncthreads();
         if (edge(i, bad_v)) {
             // values that no row may see can be anything in memory: make them zero
-            for (int e = threadIdx.x; e < DP * 8; e += 256) {
+            for (int e = threadIdx.x; e < DM * 8; e += 256) {
                 const int d = e >> 3, key = i * kKT + 8 * ((e & 7) ^ (d >> 1 & 7));
                 const bool there = in_cache(page_of(key));
                 u32x4* at = reinterpret_cast<u32x4*>(&vbuf[buf * TILE + e * 16]);
@@ -285,14 +284,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
             // The loads one by one: together they would hold up the steps behind them.  With FEW it is the
             // loads that take the time, and they go first.  Tiles behind the last one are the last again:
             // their buffers are not read.
-            constexpr int GAP = FEW ? 0 : (STEPS - 2) / (2 * NI), at = z - 1;
+            constexpr int GAP = FEW ? 0 : (STEPS - 2) / (NI + NV), at = z - 1;
             if constexpr (at == 0) find_k(min(i + 2, end - 1), where), pages_k(min(i + 3, end - 1));
             if constexpr (at == NI * GAP) bad_v = find_v(min(i + 1, end - 1), where), pages_v(min(i + 2, end - 1));
 #pragma unroll
             for (int j = 0; j < NI; ++j)
                 if (at == j * GAP) load_k(j, where, buf);
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
+            for (int j = 0; j < NV; ++j)
                 if (at == (NI + j) * GAP) load_v(j, where, buf ^ 1);
             __builtin_amdgcn_sched_barrier(0);
         }, std::make_integer_sequence<int, STEPS>{});
@@ -369,10 +368,10 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) k_attn_tile(AttnArgs a)
 
 template <class E, int DP, bool FEW>
 void launch_dp(const AttnArgs& a, unsigned blocks, hipStream_t s) {
-    // Heads of up to three quarters of the LDS row leave the last quarter's products out: 512 rows over 16,001
-    // keys, 24/4 heads of 192: 297 -> 254 us, of 96: 138 -> 120.  Where loads bound it, the wave that has
-    // fewer of them costs more (64 requests of one token, heads of 96: 325 -> 348).
-    constexpr int DM = !FEW && DP > 64 ? DP / 4 * 3 : DP;
+    // Heads of up to three quarters of the LDS row leave the last quarter's products and values out: 512 rows
+    // over 16,001 keys, 24/4 heads of 192: 293 -> 247 us, of 96: 137 -> 114; 64 requests of 8 tokens and up to
+    // 16,252 keys, 40/8 heads of 192: 834 -> 762.
+    constexpr int DM = DP > 64 ? DP / 4 * 3 : DP;
     if (a.D == DP) k_attn_tile<E, DP, DP, true, FEW><<<blocks, 256, 0, s>>>(a);
     else if (a.D <= DM) k_attn_tile<E, DP, DM, false, FEW><<<blocks, 256, 0, s>>>(a);
     else k_attn_tile<E, DP, DP, false, FEW><<<blocks, 256, 0, s>>>(a);
