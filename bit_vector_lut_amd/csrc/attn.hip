@@ -305,42 +305,51 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t all = int64_t(d.T) * g;
     const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
-    const int keys = std::max(1, d.max_kv);
     G.lds = d.D <= 128 || rows > 16;
     // with loads first 8 tokens over 65,472 keys take 53 us for 40/8 heads of 128 (58 with loads between
     // the steps), but 62 (60) for 24/4 heads of 256
     G.few = rows * d.D <= 64 * 128;
     const int mt = G.lds ? kAttnTileRows : 16, key_tile = G.lds ? 64 : 32;
-    const int key_tiles = (keys + key_tile - 1) / key_tile;
     G.tiles = int(all / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
-    if (G.lds) {
-        // Times in us.  A workgroup passes over a tile in 1 us and 0.35 more for each wave with rows (D =
-        // 128), if all of them together stay below 5 TB/s of keys and values (which the row tiles of a
-        // request share); two tiles' worth to start and end each; the join writes and reads FP32 sums
-        // at about 4 TB/s.  512 rows of 40/8 heads of
-        // 128 over 33,001 keys: 436 us with the three splits that this chooses, 539 / 477 / 453 / 457
-        // with 2 / 4 / 6 / 8.  max_kv is the longest of several requests: half of the estimate is for
-        // all being as long, half for that one alone.
-        const int64_t slots = int64_t(cus) * (d.D <= 128 ? 2 : 1);
-        const double alone = (1.0 + 0.35 * double(std::min<int64_t>(4, (rows + 31) / 32))) * d.D / 128;
-        G.nsplit = 1;
-        double best = 1e300;
-        for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
-            const int64_t blocks = active * ns;
-            const int64_t busy = std::min((blocks + cus - 1) / cus * cus, slots);  // as full as the fullest
-            const double tile = std::max(alone, double(busy) * key_tile * d.D * 4 / 5e6 * d.R * d.kv_heads / active);
-            const double tiles = (key_tiles + ns - 1) / ns + 2;
-            double cost = double((blocks + slots - 1) / slots) * tiles * tile;
-            if (d.R > 1) cost = 0.5 * cost + 0.5 * tiles * alone;
-            if (ns > 1) cost += 4 + ns * double(rows_all) * d.D * 8 / 4e6 * (d.R > 1 ? 0.5 : 1.0);
-            if (cost < best) best = cost, G.nsplit = ns;
+    auto splits = [&](int key_tiles) {
+        if (G.lds) {
+            // Times in us.  A workgroup passes over a tile in 1 us and 0.35 more for each wave with rows
+            // (D = 128), if all of them together stay below 5 TB/s of keys and values (which the row tiles
+            // of a request share); two tiles' worth to start and end each; the join writes and reads FP32
+            // sums at about 4 TB/s.  512 rows of 40/8 heads of 128 over 33,001 keys: 436 us with the three
+            // splits that this chooses, 539 / 477 / 453 / 457 with 2 / 4 / 6 / 8.  max_kv is the longest of
+            // several requests: half of the estimate is for all being as long, half for that one alone.
+            const int64_t slots = int64_t(cus) * (d.D <= 128 ? 2 : 1);
+            const double alone = (1.0 + 0.35 * double(std::min<int64_t>(4, (rows + 31) / 32))) * d.D / 128;
+            int nsplit = 1;
+            double best = 1e300;
+            for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
+                const int64_t blocks = active * ns;
+                const int64_t busy = std::min((blocks + cus - 1) / cus * cus, slots);  // as full as the fullest
+                const double tile = std::max(alone, double(busy) * key_tile * d.D * 4 / 5e6 * d.R * d.kv_heads / active);
+                const double tiles = (key_tiles + ns - 1) / ns + 2;
+                double cost = double((blocks + slots - 1) / slots) * tiles * tile;
+                if (d.R > 1) cost = 0.5 * cost + 0.5 * tiles * alone;
+                if (ns > 1) cost += 4 + ns * double(rows_all) * d.D * 8 / 4e6 * (d.R > 1 ? 0.5 : 1.0);
+                if (cost < best) best = cost, nsplit = ns;
+            }
+            return nsplit;
         }
-    } else {
         // four workgroups a compute unit: 123 us at the sizes above, 127 / 130 / 147 with 3 / 6 / 12
         const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
-        const int most_split = std::max(1, key_tiles / 8);
-        G.nsplit = int(std::min<int64_t>(std::min<int64_t>(want, most_split), kMaxSplit));
+        return int(std::min<int64_t>(std::min<int64_t>(want, std::max(1, key_tiles / 8)), kMaxSplit));
+    };
+    // Through a window a row tile sees that many keys and one for each of its tokens: one request of a
+    // token over 32,000 keys, 40/8 heads of 128, window 4,096: 15 us, 27 with splits for all 32,000; 64
+    // ragged requests, window 1,024: 53 and 75.  No more splits than without it, so that a workspace made
+    // without it holds.
+    int key_tiles = (std::max(1, d.max_kv) - 1) / key_tile + 1;
+    G.nsplit = splits(key_tiles);
+    if (d.window) {
+        const int64_t reach = int64_t(d.window) + std::min(d.T, (mt + g - 1) / g);  // from any key on
+        key_tiles = int(std::min<int64_t>(key_tiles, (reach + key_tile - 2) / key_tile + 1));
+        G.nsplit = std::min(G.nsplit, splits(key_tiles));
     }
     G.split_tiles = (key_tiles + G.nsplit - 1) / G.nsplit;
     G.opart = 0;

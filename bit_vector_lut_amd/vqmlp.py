@@ -788,7 +788,7 @@ class PagedCache:
                          self.D ** -0.5 if scale is None else scale, table_width)
 
     def _work_bytes(self, d):
-        key = (d.T, d.R, d.heads, d.max_kv, d.table_width)
+        key = (d.T, d.R, d.heads, d.max_kv, d.table_width, d.window)
         n = self._work.get(key)
         if n is None:
             import torch

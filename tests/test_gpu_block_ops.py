@@ -506,6 +506,25 @@ def test_paged_attention_any_key_bound(vq, torch_dev, max_kv):
     _attn_check(vq, torch, torch.float16, [(200, 1500)], 6, 2, 64, 16, max_kv=max_kv)
 
 
+@pytest.mark.parametrize("lens,heads,D", [([(1, 9000)], 10, 128), ([(3, 9000), (1, 4000)], 4, 256),
+                                          ([(150, 3000), (9, 9)], 4, 64)])
+def test_paged_attention_windows_over_long_contexts(vq, torch_dev, lens, heads, D):
+    """Windows from one key to more than there are, in one cache; a workspace made without the window holds."""
+    torch = torch_dev
+    for window in (1, 63, 64, 1000, 5000, 2 ** 31 - 1):
+        _attn_check(vq, torch, torch.float16, lens, heads, 2, D, 16, window=window, seed=window % 100)
+    q, k, v, table, cu = _attn_case(torch, torch.float16, lens, heads, 2, D, 16, 3)
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = vq.PagedCache(k.cuda(), v.cuda())
+    args = (q.cuda(), table.cuda(), i(cu), i([n for _, n in lens]))
+    small = cache.attention(*args, window=100)
+    whole = cache.attention(*args)
+    n = cache.workspace_bytes(q.shape[0], len(lens), heads, table.shape[1])
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    assert torch.equal(small, cache.attention(*args, window=100, workspace=ws))
+    assert torch.equal(whole, cache.attention(*args, workspace=ws))
+
+
 def test_paged_attention_extreme_scores(vq, torch_dev):
     """One key far above the others, all keys equal, and scores of thousands."""
     torch = torch_dev
