@@ -183,10 +183,12 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // and state share: 2^e puts the chunk's largest value in [2^10, 2^11), and takes the state down or up
 // where that leaves [2^-2, 2^15).
 //
-// Bound by a chunk's vector and matrix work in turn: two workgroups a compute unit (registers), each
-// 64 x 64 scores, 124 matrix-core steps and about 500 vector instructions a wave and chunk.  Three
-// prompts of 5003, 1021 and 2049 tokens, 48 value and 16 key heads of 128 x 128: 54 us for the
-// segments' states, 110 for the outputs, 200 TFLOP/s of the recurrence's operations.
+// Bound by the latencies of a chunk: two workgroups a compute unit (registers), each 64 x 64 scores,
+// 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
+// busy 19% of the time, the vector unit 36%, LDS 25%.  Eight waves of 16 columns, four a SIMD, read twice
+// as much LDS and took 193 us instead of 160.  Three prompts of 5003, 1021 and 2049 tokens, 48 value and
+// 16 key heads of 128 x 128: 53 us for the segments' states, 98 for the outputs, 217 TFLOP/s of the
+// recurrence's operations (146 us back to back).
 constexpr int kTok = kC + 8;  // LDS row stride of the scores: 144 bytes, 16-byte chunks spread over banks
 
 // K^T and V^T in LDS: rows of 64 tokens, the eight 16-byte chunks of a row permuted by an exclusive or
@@ -646,8 +648,8 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int v = 0; v < NTV; ++v) S[p][b][v] *= keep;
-        // K^T operands are read two steps (of four products and more) ahead; the parts of the second 32 tokens are made between
-        // the products of the first
+        // K^T operands are read two steps (of four products and more) ahead; the parts of the second 32
+        // tokens are made between the products of the first
         u32x4 part[2][NTV][PARTS], kk[2][2];
         auto parts = [&](int c, int v) __attribute__((always_inline)) {
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4]);
