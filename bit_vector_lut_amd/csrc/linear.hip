@@ -423,12 +423,13 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
         if (wave < 2) return;
         const uint8_t* const base = reinterpret_cast<const uint8_t*>(a.g + (u.c0 + t) * a.ld_g + h);
         const int i = wave == 3 ? 63 - lane : lane;
-        gv = t + i < t1 ? fmaxf(*reinterpret_cast<const float*>(base + uint32_t(i) * uint32_t(a.ld_g) * 4), kMinG) : 0.f;
+        gv = t + i < t1 ? *reinterpret_cast<const float*>(base + uint32_t(i) * uint32_t(a.ld_g) * 4) : 0.f;
     };
     // sums from the front for e^{b}, from the back for the tails, each accurate against its own size
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
         if (wave < 2) return;
-        const float b = lane_scan(gv, 0.f, [](float x, float y) { return x + y; });
+        // the bound here, not where g is loaded: it would wait for the load
+        const float b = lane_scan(fmaxf(gv, kMinG), 0.f, [](float x, float y) { return x + y; });
         const float eb = exp_f32(b);
         if (wave == 2) {
             d.eb[lane] = eb;
@@ -700,7 +701,9 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
                 for (int v = 0; v < NTV; ++v)
                     S[p][b][v] = E::mfma16(kk[z / 2 & 1][z & 1], part[c][v][q], S[p][b][v]);
             if constexpr (z < 2 * KS && z % KS == 0 && z / KS < NTV) parts(1, z / KS);
-            if constexpr (!OUT && z == 2 * KS) {  // between products, which hide the lane moves' waits
+            // Behind products, which hide the lane moves' waits, and before this chunk's first load: which of
+            // those were made the compiler does not know, so behind them it would wait for all.
+            if constexpr (!OUT && z == 0) {
                 decays(sm.d[((t - t0) / kC + 1) & 1]);
                 fetch_g(t + 2 * kC);
             }
