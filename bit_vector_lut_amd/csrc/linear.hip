@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
 // busy 19% of the time, the vector unit 36%, LDS 25%.  Eight waves of 16 columns, four a SIMD, read twice
 // as much LDS and took 193 us instead of 160.  Three prompts of 5003, 1021 and 2049 tokens, 48 value and
-// 16 key heads of 128 x 128: 53 us for the segments' states, 98 for the outputs, 217 TFLOP/s of the
-// recurrence's operations (146 us back to back).
+// 16 key heads of 128 x 128: 50 us for the segments' states, 98 for the outputs, 226 TFLOP/s of the
+// recurrence's operations (140 us back to back).
 constexpr int kTok = kC + 8;  // LDS row stride of the scores: 144 bytes, 16-byte chunks spread over banks
 
 // K^T and V^T in LDS: rows of 64 tokens, the eight 16-byte chunks of a row permuted by an exclusive or

@@ -82,7 +82,7 @@ def test_page_plan_refusals(vq, kw, text, want):
     (3, 264, "D=264"), (5, 0, "n_pages=0"), (5, 1 << 28, "2^31"), (6, None, "null"), (7, 120, "stride"),
     (7, 132, "multiples of 8"), (9, 64, "stride"), (6, PTR + 8, "aligned"), (11, PTR + 2, "aligned"),
     (10, PTR + 2, "aligned"), (12, None, "null"),
-])
+], ids=lambda v: "PTR+%d" % (v - PTR) if isinstance(v, int) and v >= PTR else None)
 def test_paged_store_refusals(vq, at, value, text):
     args = [0, 3, 2, 64, 16, 4, PTR, 128, PTR, 128, PTR, PTR, PTR, None]
     args[at] = value
