@@ -181,7 +181,10 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // times their decays, and the state as an operand of S^T Q, are rounded once to the 16-bit type:
 // the outputs are rounded to it as well.  binary16 is kept in range by a power of two that value parts
 // and state share: 2^e puts the chunk's largest value in [2^10, 2^11), and takes the state down or up
-// where that leaves [2^-2, 2^15).
+// where that leaves [2^-2, 2^15).  Scores have a power of two of their own, 2^su, which the outputs give back
+// in FP32: su is the chunk's before as long as the largest score stays in [2^5, 2^15), so that scores down to
+// 2^-19 of it keep all bits; otherwise the chunk's scores are made once more (three packed prompts: 2% slower than
+// without a unit, where scores below 2^-14 lost bits and those beyond 65504 were infinite).
 //
 // Bound by the latencies of a chunk: two workgroups a compute unit (registers), each 64 x 64 scores,
 // 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
@@ -211,6 +214,7 @@ struct LinSmem {
     __attribute__((aligned(256))) uint8_t kt[DKP * kC * 2];  // [dk][token], tok_at
     __attribute__((aligned(256))) uint8_t vt[DVP * kC * 2];  // [dv][token]
     LinDecay d[2];           // of this chunk and the next
+    __attribute__((aligned(16))) uint32_t top[4];  // largest score of each wave's keys
 };
 template <int DKP>
 struct LinOutSmem {
@@ -467,6 +471,36 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
     const bool last = uniform(u.seg == u.nseg - 1 && slot >= 0);  // has the request's final state to write
     float decay = 1.f;  // over the segment so far (!OUT)
     int e = 0;          // S is kept in units of 2^-e
+    // Scores are kept in units of 2^-su (binary16), the same in all waves: first those of queries and keys
+    // of length one, then the chunk's before.
+    auto clip = [](int x) { return min(max(x, -60), 60); };
+    int su = HALF ? clip(11 - expo(a.scale)) : 0;
+    // This wave's 16 keys with queries 16 x .., times their decays; the lane's largest so far.
+    auto scores = [&](const LinDecay& dc, int x, const u32x4* kf, const u32x4* qf, const f32x4& bj4, float unit,
+                      float& top) __attribute__((always_inline)) {
+        if constexpr (OUT) {
+            if (x < (wave & 2)) return;
+            float p[4] = {0.f, 0.f, 0.f, 0.f};  // keys behind the queries' block
+            if (x >= wave) {
+                f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[s], sc);
+                const float bt = dc.bl[16 * x + lr];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = sc[i] * unit * __builtin_amdgcn_exp2f(bt - bj4[i]);
+                if (x == wave) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = 4 * g4 + i <= lr ? p[i] : 0.f;
+                }
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(p[i]));
+                }
+            }
+            *reinterpret_cast<u32x2*>(&so.p[16 * x + lr][16 * wave + 4 * g4]) =
+                u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
+        }
+    };
     if (t0 < t1) {
         fetch_g(t0);
 #pragma unroll
@@ -500,7 +534,6 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
         __syncthreads();
         f32x4 o[NTV][4];
         if constexpr (OUT) {
-            // scores of this wave's 16 keys with all queries from there on
             u32x4 qf[4][KS], kf[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -510,24 +543,15 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             }
             __builtin_amdgcn_sched_barrier(0);  // all reads on their way before the first product waits
             const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
+            const float unit = a.scale * pow2(su);
+            float top = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (x < (wave & 2)) continue;
-                float p[4] = {0.f, 0.f, 0.f, 0.f};  // keys behind the queries' block
-                if (x >= wave) {
-                    f32x4 sc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[x][s], sc);
-                    const float bt = dc.bl[16 * x + lr];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = sc[i] * a.scale * __builtin_amdgcn_exp2f(bt - bj4[i]);
-                    if (x == wave) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) p[i] = 4 * g4 + i <= lr ? p[i] : 0.f;
-                    }
-                }
-                *reinterpret_cast<u32x2*>(&so.p[16 * x + lr][16 * wave + 4 * g4]) =
-                    u32x2{pack16<E>(p[0], p[1]), pack16<E>(p[2], p[3])};
+            for (int x = 0; x < 4; ++x) scores(dc, x, kf, qf[x], bj4, unit, top);
+            if constexpr (HALF) {
+                // an infinite score is no measure of the others; of values that are not negative, the bits are
+                // in the values' order
+                const uint32_t w = wave_max(__builtin_bit_cast(uint32_t, top < __builtin_inff() ? top : 0.f));
+                if (lane == 0) sm.top[wave] = w;
             }
             // the next chunk's decays, by the waves with the fewest scores
             decays(sm.d[((t - t0) / kC + 1) & 1]);
@@ -543,7 +567,6 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
                         for (int v = 0; v < NTV; ++v)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[p][b][v][i]));
-                // of values that are not negative, the bits are in the values' order
                 mx = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, mx)));
                 // outside the range in which binary16 holds all that matters of S: other units
                 if (mx >= 32768.f || (mx < 0.25f && mx > 0.f)) {
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
                             for (int v = 0; v < NTV; ++v) S[p][b][v] *= up;
                 }
             }
-            const float down = a.scale * pow2(-e);
+            const float down = unit * pow2(-e);
 #pragma unroll
             for (int v = 0; v < NTV; ++v)
 #pragma unroll
@@ -586,6 +609,34 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             }
             __syncthreads();
             // every wave is done with this chunk's queries and keys
+            if constexpr (HALF) {
+                // The largest score has to lie where binary16 holds it and those 2^-15 of it with all bits: else
+                // once more, in units that put it into [2^10, 2^11).
+                const u32x4 w = *reinterpret_cast<const u32x4*>(sm.top);
+                const float mx = __builtin_bit_cast(float, uniform(int(max(max(w[0], w[1]), max(w[2], w[3])))));
+                const int to = clip(su + 10 - expo(mx));
+                if ((mx >= 32768.f || (mx < 32.f && mx > 0.f)) && to != su) {
+                    const float by = pow2(to - su);
+#pragma unroll
+                    for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[v][x] *= by;
+                    su = to;
+                    u32x4 qf[KS], kf[KS];
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) kf[s] = qk_read(so.k, 16 * wave + lr, s);
+                    const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
+                    float top = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) qf[s] = qk_read(so.q, 16 * x + lr, s);
+                        scores(dc, x, kf, qf, bj4, a.scale * pow2(su), top);
+                        __builtin_amdgcn_sched_barrier(0);  // few registers: S, o and the next chunk's loads stay
+                    }
+                    __syncthreads();
+                }
+            }
         }
         u32x4 vf[NTV][2];
 #pragma unroll
@@ -604,6 +655,13 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
                 }
+            }
+            if constexpr (HALF) {
+                const float by = pow2(-su);
+#pragma unroll
+                for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[v][x] *= by;
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {

@@ -409,7 +409,7 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
  * [0, T]; rows from cu_q[R] on give y = 0.  max_q: the most new tokens of one request that are
  * expected; it chooses the kernel (up to 16: the recurrence token by token; above: chunks of 64
  * tokens on the matrix cores), and any value gives a right answer.  In chunks scale * (q . k) times
- * its decay is rounded to dtype once: with F16 it has to stay below 65504.  R <= 65535. */
+ * its decay is rounded to dtype once, with F16 in a unit that follows the chunk's largest.  R <= 65535. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
     float scale;

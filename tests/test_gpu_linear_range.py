@@ -1,0 +1,62 @@
+"""GPU: linear attention where its sizes, decays and values lie far apart.
+
+Tolerances.  u = 2^-11 (binary16) or 2^-8 (bfloat16) is one rounding, W = 2^-24 one of FP32.  z is the
+output of the recurrence with absolute values.  An output is rounded once (u |y|); scores times decay
+and the state as an operand are rounded once each (2 u z at most); FP32 sums and exponentials count 100 W
+of z and a chunk's worth more for each 64 tokens (W / 16 a token).  2^-25 is half a step of the
+smallest binary16.  The state is FP32: 100 W and W / 8 a token of its recurrence of absolute values.
+"""
+import pytest
+
+from test_gpu_block_ops import W, _close, _linear_ref, _randn, _t, _u, torch_dev, vq  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(vq, torch, q, k, v, g, state, lens, max_q, scale=None):
+    """The operator's outputs and state, checked against the 64-bit recurrence."""
+    hk, dk, hv, dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
+    cu = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    op = vq.LinearAttention(hk, hv, dk, dv, scale)
+    print("linear", q.dtype, lens, hk, hv, dk, dv, max_q, flush=True)
+    y, out = op.forward(q.cuda(), k.cuda(), v.cuda(), g.cuda(), state.cuda(),
+                        torch.tensor(cu, dtype=torch.int32, device="cuda"), max_q=max_q)
+    torch.cuda.synchronize()
+    ry, z, rs, size = _linear_ref(torch, q, k, v, g, state, cu, None, None, op.scale, len(lens))
+    u, n = _u(torch, q.dtype), max(lens)
+    _close(torch, y, ry, u * ry.abs() + (2 * u + (100 + n / 16) * W) * z + 2.0 ** -25, "y")
+    _close(torch, out, rs, (100 + n / 8) * W * size + 2.0 ** -100, "state")
+    return y, out
+
+
+def _decays(torch, T, hv, seed):
+    return -torch.rand((T, hv), generator=torch.Generator().manual_seed(seed)) * 0.1
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("max_q", [16, 200])
+@pytest.mark.parametrize("std,vstd,scale", [(1e-3, 1000.0, None), (3e-3, 1000.0, None), (1e-4, 30000.0, 1.0),
+                                            (30.0, 1.0, None), (150.0, 0.01, None), (1.0, 1.0, 1e-6),
+                                            (0.1, 1.0, -1000.0)])
+def test_scores_of_any_size(vq, torch_dev, dtype, max_q, std, vstd, scale):
+    """Queries and keys from 1e-4 to 150: scores far below and above 1 keep the outputs' accuracy."""
+    torch, dt, T = torch_dev, _t(torch_dev, dtype), 200
+    q, k = _randn(torch, (T, 2, 128), dt, 1, std), _randn(torch, (T, 2, 128), dt, 2, std)
+    v = _randn(torch, (T, 4, 64), dt, 3, vstd).clamp(-6e4, 6e4)
+    state = _randn(torch, (2, 4, 128, 64), torch.float32, 4, 0.1 * std * vstd)
+    _run(vq, torch, q, k, v, _decays(torch, T, 4, 5), state, [137, 63], max_q, scale)
+
+
+@pytest.mark.parametrize("max_q", [16, 700])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_scores_that_change_size(vq, torch_dev, max_q, dk, dv):
+    """Queries of one token in three 2^-12 of the others', and keys that go from 2^-10 to 2^5 and back
+    from chunk to chunk, in segments too; values go the other way."""
+    torch, dt, T = torch_dev, torch_dev.float16, 700
+    q, k = _randn(torch, (T, 1, dk), dt, 1, dk ** -0.5), _randn(torch, (T, 1, dk), dt, 2, dk ** -0.5)
+    v = _randn(torch, (T, 2, dv), dt, 3)
+    q[::3] *= 2.0 ** -12
+    for a, e in zip(range(0, T, 64), [0, -10, 5, 5, -10, -10, 0, 5, 0, -10, 0]):
+        k[a:a + 64] *= 2.0 ** e
+        v[a:a + 64] *= 2.0 ** -e
+    _run(vq, torch, q, k, v, _decays(torch, T, 2, 5), torch.zeros(1, 2, dk, dv), [T], max_q, 64.0)
