@@ -176,15 +176,19 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 //     needs them all.
 //
 // Precision.  The state and its decays are FP32.  What joins the state is e^{..} v in FP32, handed
-// to the matrix cores as a sum of parts of the 16-bit type (two for binary16, three for bfloat16,
-// whose parts are shorter), so that the state loses nothing to the operand's type.  The scores
-// times their decays, and the state as an operand of S^T Q, are rounded once to the 16-bit type:
-// the outputs are rounded to it as well.  binary16 is kept in range by a power of two that value parts
-// and state share: 2^e puts the chunk's largest value in [2^10, 2^11), and takes the state down or up
-// where that leaves [2^-2, 2^15).  Scores have a power of two of their own, 2^su, which the outputs give back
-// in FP32: su is the chunk's before as long as the largest score stays in [2^5, 2^15), so that scores down to
-// 2^-19 of it keep all bits; otherwise the chunk's scores are made once more (three packed prompts: 2% slower than
-// without a unit, where scores below 2^-14 lost bits and those beyond 65504 were infinite).
+// to the matrix cores as a sum of parts of the 16-bit type, three for bfloat16 and two for binary16 (its 22 bits:
+// off by 2^-23 of the value or 2^-39 of the column's sum, whichever is more).  The scores times their decays, and
+// the state as an operand of S^T Q, are rounded once to the 16-bit type: the outputs are rounded to it as well.
+// In binary16 the parts and the state of each value column share a power of two 2^e, so that columns of any sizes
+// stand side by side.  It puts the sum over the chunk's tokens of e^{..} |v|, decays included, into [2^14, 2^15);
+// the matrix cores make that sum, of 2^15 e^{..} in binary16 and |v| (a maximum by vector instructions took 57
+// instead of 53 us for the states of three packed prompts).  The state is taken up or down where its largest
+// element leaves [2^-2, 2^15).  One unit for all of a wave's columns took 160 instead of 166 us for those prompts,
+// but where columns lie 2^20 apart it cost the smaller ones' states 12 bits.
+// Binary16 scores have a power of two of their own, 2^su, which the outputs give back in FP32: su is the chunk's
+// before as long as the largest score stays in [2^5, 2^15), so that scores down to 2^-19 of it keep all bits;
+// otherwise the chunk's scores are made once more (2% of the time; without a unit scores below 2^-14 lose bits
+// and those beyond 65504 are infinite).
 //
 // Bound by the latencies of a chunk: two workgroups a compute unit (registers), each 64 x 64 scores,
 // 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
@@ -207,6 +211,7 @@ __device__ __forceinline__ constexpr int tok_at(int row, int chunk) { return row
 struct alignas(16) LinDecay {  // of one chunk; b = sum of g up to a token
     float eb[kC], bl[kC];    // e^b, b log2 e
     float tail[kC];          // e^(sum behind the token)
+    uint16_t weight[kC];     // 2^15 tail in binary16 (of binary16 values)
     float etot;              // e^(sum of the chunk)
 };
 template <int DKP, int DVP>
@@ -244,6 +249,16 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 
+// Maximum over the lanes with the same lane % 16, in all of them.  The operands of a swap are two values to
+// the compiler, which takes both results for one otherwise.
+__device__ __forceinline__ float column_max(float v) {
+    uint32_t x = __builtin_bit_cast(uint32_t, v);  // not negative: the bits are in the values' order
+    const auto a = __builtin_amdgcn_permlane32_swap(x, uint32_t(fresh(int(x))), false, false);
+    x = max(uint32_t(a[0]), uint32_t(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(x, uint32_t(fresh(int(x))), false, false);
+    return __builtin_bit_cast(float, max(uint32_t(b[0]), uint32_t(b[1])));
+}
+
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, uint32_t(e + 127) << 23); }
 // Exponent of |x| (floor of log2), -127 for zero and subnormals.
@@ -274,13 +289,16 @@ __device__ __forceinline__ bool lin_unit(const LinArgs& a, int x, LinUnit& u) {
     return u.seg >= 0 && u.seg < u.nseg;
 }
 
-// Workgroups a compute unit holds: three where LDS allows it.  48 heads of 64 x 64, 12,000 tokens: 116 us
-// with two, 98 with three; of 64 x 128, 5,000 tokens: 75 and 73, though a few registers go to memory.
-constexpr int lin_resident(int dkp) { return dkp == 64 ? 3 : 2; }
+// Workgroups a compute unit holds: three where LDS and registers allow it.  48 heads of 64 x 64, 12,000 tokens:
+// 116 us with two, 98 with three.  64 x 128 in binary16 with three puts 18 registers into memory: 5,000 tokens
+// 85 us, 79 with two; in bfloat16, 7 registers, 73 and 75.
+__host__ __device__ constexpr int lin_resident(int dkp, int ntv, bool half) {
+    return dkp == 64 && !(half && ntv == 2) ? 3 : 2;
+}
 
 // OUT: outputs and the final state; otherwise the states of the segments, for a later OUT launch.
 template <class E, int DKP, int NTV, bool OUT>
-__global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a) {
+__global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))) k_lin_chunk(LinArgs a) {
     constexpr int KS = DKP / 32;       // steps over dk, pairs of state row tiles
     constexpr int DVP = 64 * NTV;
     constexpr bool HALF = __is_same(E, F16);
@@ -341,9 +359,9 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
 #pragma unroll
                 for (int v = 0; v < NTV; ++v) f(S[p][b][v], ((p * 2 + b) * NTV + v) * 1024);
     };
-    auto store_seg = [&](int unit, float mul) __attribute__((always_inline)) {
+    auto store_seg = [&](int unit) __attribute__((always_inline)) {
         uint8_t* const dst = seg_state(unit);
-        each_piece([&](f32x4& x, int at) { *reinterpret_cast<f32x4*>(dst + at + seg_off) = x * mul; });
+        each_piece([&](f32x4& x, int at) { *reinterpret_cast<f32x4*>(dst + at + seg_off) = x; });
     };
     auto load_seg = [&](int unit) __attribute__((always_inline)) {
         const uint8_t* const src = seg_state(unit);
@@ -355,10 +373,10 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             for (int i = 0; i < 4; ++i) x[i] = src[at + int64_t(i) * a.Dv];
         });
     };
-    auto store_state = [&](float* dst, float mul) __attribute__((always_inline)) {
+    auto store_state = [&](float* dst) __attribute__((always_inline)) {
         each_state([&](f32x4& x, int64_t at) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[at + int64_t(i) * a.Dv] = x[i] * mul;
+            for (int i = 0; i < 4; ++i) dst[at + int64_t(i) * a.Dv] = x[i];
         });
     };
 #pragma unroll
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
         if (u.seg == 0 || u.seg == u.nseg - 1) {
             if (old) load_state(a.sin + sbase);
             if (u.seg == u.nseg - 1) {
-                store_seg(u.first + u.seg, 1.f);
+                store_seg(u.first + u.seg);
                 return;
             }
         }
@@ -441,7 +459,10 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             if (lane == 63) d.etot = eb;
         } else {
             // from the back b reaches to token 63 - lane: what lies behind token 62 - lane
-            d.tail[lane == 63 ? 63 : 62 - lane] = lane == 63 ? 1.f : eb;
+            const int at = lane == 63 ? 63 : 62 - lane;
+            const float tail = lane == 63 ? 1.f : eb;
+            d.tail[at] = tail;
+            if constexpr (HALF) d.weight[at] = uint16_t(bits16<F16>(fminf(tail * 32768.f, 65504.f)));
         }
     };
     // Q rows of a chunk, token by token, straight to LDS; behind the last token the last again
@@ -470,7 +491,15 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
     };
     const bool last = uniform(u.seg == u.nseg - 1 && slot >= 0);  // has the request's final state to write
     float decay = 1.f;  // over the segment so far (!OUT)
-    int e = 0;          // S is kept in units of 2^-e
+    int e[NTV] = {};    // a lane's columns of S are kept in units of 2^-e
+    auto scale_state = [&](const float* by) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) S[p][b][v] *= by[v];
+    };
     // Scores are kept in units of 2^-su (binary16), the same in all waves: first those of queries and keys
     // of length one, then the chunk's before.
     auto clip = [](int x) { return min(max(x, -60), 60); };
@@ -558,30 +587,32 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
             fetch_g(t + 2 * kC);
             // e^{b} S^T Q
             if constexpr (HALF) {
-                float mx = 0.f;
+                float mx[NTV], up[NTV];
+                bool out = false;
 #pragma unroll
-                for (int p = 0; p < KS; ++p)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int v = 0; v < NTV; ++v)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(S[p][b][v][i]));
-                mx = __builtin_bit_cast(float, wave_max(__builtin_bit_cast(uint32_t, mx)));
-                // outside the range in which binary16 holds all that matters of S: other units
-                if (mx >= 32768.f || (mx < 0.25f && mx > 0.f)) {
-                    const int f = min(max(10 - expo(mx), -100 - e), 100 - e);
-                    const float up = pow2(min(max(f, -126), 126));
-                    e += min(max(f, -126), 126);
+                for (int v = 0; v < NTV; ++v) {
+                    mx[v] = 0.f;
 #pragma unroll
                     for (int p = 0; p < KS; ++p)
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
-                            for (int v = 0; v < NTV; ++v) S[p][b][v] *= up;
+                            for (int i = 0; i < 4; ++i) mx[v] = fmaxf(mx[v], fabsf(S[p][b][v][i]));
+                    mx[v] = column_max(mx[v]);
+                    out |= mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
+                }
+                // outside the range in which binary16 holds all that matters of a column: other units
+                if (__any(out)) {
+#pragma unroll
+                    for (int v = 0; v < NTV; ++v) {
+                        const bool mine = mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
+                        const int f = mine ? min(max(min(max(10 - expo(mx[v]), -100 - e[v]), 100 - e[v]), -126), 126) : 0;
+                        up[v] = pow2(f);
+                        e[v] += f;
+                    }
+                    scale_state(up);
                 }
             }
-            const float down = unit * pow2(-e);
 #pragma unroll
             for (int v = 0; v < NTV; ++v)
 #pragma unroll
@@ -601,11 +632,18 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
                     for (int i = 0; i < N; ++i) fetch(t + kC, (p * NTV + v) * N + i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+            float eb[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float eb = dc.eb[16 * x + lr] * down;
+            for (int x = 0; x < 4; ++x) eb[x] = dc.eb[16 * x + lr];
 #pragma unroll
-                for (int v = 0; v < NTV; ++v) o[v][x] *= eb;
+            for (int v = 0; v < NTV; ++v) {
+                f32x4 down = {unit, unit, unit, unit};  // of the columns whose outputs the lane holds
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) down[i] *= pow2(-__shfl(e[v], 4 * g4 + i));
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[v][x] *= down * eb[x];
             }
             __syncthreads();
             // every wave is done with this chunk's queries and keys
@@ -644,9 +682,32 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[(vget ^ tok_bits(4 * v, 4 * c)) + 4 * v * kC * 2]);
+        // sum over the tokens of e^{..} |v| of the lane's columns, times 2^15
+        f32x4 sum[NTV];
+        if constexpr (HALF) {
+#pragma unroll
+            for (int v = 0; v < NTV; ++v) sum[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(&dc.weight[32 * c + 8 * g4]);
+#pragma unroll
+                for (int v = 0; v < NTV; ++v) sum[v] = E::mfma16(w, vf[v][c] & 0x7FFF7FFFu, sum[v]);
+            }
+        }
+        int en[NTV];
+        auto new_units = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int v = 0; v < NTV; ++v) {
+                // bounds: states of up to 2^97 stay finite, parts keep what is above 2^-55
+                const float z = sum[v][0];
+                en[v] = z > 0.f ? min(max(14 + 15 - expo(z), max(e[v] - 126, -100)), min(e[v] + 126, 30)) : e[v];
+            }
+        };
+        if (HALF && !OUT) new_units();
         if constexpr (OUT) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
+                if (HALF && x == 1) new_units();
                 if (x < NI && t + kC < t1) stage_q(t + kC, x);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -682,42 +743,38 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
         }
         // the state after the chunk, which nobody needs behind a segment's last unless it is the request's
         if (OUT && t + kC >= t1 && !last) continue;
-        int en = e;
+        // What joins it: e^{..} v, in units that put a column's sum of magnitudes into [2^14, 2^15).
+        auto tail = [&](int c, float* w) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 z = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4 + 4 * j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * j + i] = z[i];
+            }
+        };
+        float lift[NTV], keep[NTV];
+#pragma unroll
+        for (int v = 0; v < NTV; ++v) lift[v] = 1.f, keep[v] = dc.etot;
         if constexpr (HALF) {
-            typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-            u16x2 both = {0, 0};  // magnitudes are in the order of their bits
 #pragma unroll
-            for (int v = 0; v < NTV; ++v)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        both = __builtin_elementwise_max(
-                            both, __builtin_bit_cast(u16x2, uint32_t(vf[v][c][i] & 0x7FFF7FFFu)));
-            const uint32_t mx = wave_max(uint32_t(max(both[0], both[1])));
-            en = mx ? 10 - (int(mx >> 10) - 15) : e;  // the largest value lands in [2^10, 2^11)
+            for (int v = 0; v < NTV; ++v) {
+                lift[v] = pow2(en[v]);
+                keep[v] *= pow2(en[v] - e[v]);
+                e[v] = en[v];
+            }
         }
-        const float lift = pow2(en);
-        const float keep = dc.etot * pow2(max(en - e, -126));
-        e = en;
         decay *= dc.etot;
-#pragma unroll
-        for (int p = 0; p < KS; ++p)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int v = 0; v < NTV; ++v) S[p][b][v] *= keep;
+        scale_state(keep);
         // K^T operands are read two steps (of four products and more) ahead; the parts of the second 32
         // tokens are made between the products of the first
         u32x4 part[2][NTV][PARTS], kk[2][2];
         auto parts = [&](int c, int v) __attribute__((always_inline)) {
-            const f32x4 w0 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4*>(&dc.tail[32 * c + 8 * g4 + 4]);
             float x[8];
+            tail(c, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = fmaf(lo16<E>(vf[v][c][i]), (i < 2 ? w0[2 * i] : w1[2 * i - 4]) * lift, 0.f);
-                x[2 * i + 1] = fmaf(hi16<E>(vf[v][c][i]), (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]) * lift, 0.f);
+                x[2 * i] = fmaf(lo16<E>(vf[v][c][i]), x[2 * i] * lift[v], 0.f);
+                x[2 * i + 1] = fmaf(hi16<E>(vf[v][c][i]), x[2 * i + 1] * lift[v], 0.f);
             }
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
@@ -773,11 +830,17 @@ __global__ void __launch_bounds__(256, lin_resident(DKP)) k_lin_chunk(LinArgs a)
         __syncthreads();
     }
     // no load to LDS is in flight here: each was waited for in the chunk that it was made for
+    if (HALF && (!OUT || last)) {
+        float by[NTV];
+#pragma unroll
+        for (int v = 0; v < NTV; ++v) by[v] = pow2(-e[v]);
+        scale_state(by);
+    }
     if (!OUT) {
-        store_seg(u.first + u.seg, pow2(-e));
+        store_seg(u.first + u.seg);
         if (tid == 0) a.dec[int64_t(u.first + u.seg) * a.hv + h] = decay;
     } else if (last) {
-        store_state(a.sout + sbase, pow2(-e));
+        store_state(a.sout + sbase);
     }
 }
 
@@ -807,7 +870,7 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     // two together.  8,000 tokens of heads of 128 x 128, 48 heads: 149 us with the 13 chunks that this
     // chooses, 161 / 177 / 160 / 176 with 8 / 10 / 15 / 18; 4 heads: 55 with 4, 59 / 67 / 86 with 6 / 8 / 12.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
-    const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128);
+    const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128, d.Dv <= 64 ? 1 : 2, d.dtype == VQMLP_F16);
     const int64_t slots = held * int64_t(cus);
     auto rounds = [&](int64_t units) {
         const int64_t n = units * d.v_heads, rest = n % slots, per = (5 * rest + 4 * cus - 1) / (4 * cus);

@@ -60,3 +60,30 @@ def test_scores_that_change_size(vq, torch_dev, max_q, dk, dv):
         k[a:a + 64] *= 2.0 ** e
         v[a:a + 64] *= 2.0 ** -e
     _run(vq, torch, q, k, v, _decays(torch, T, 2, 5), torch.zeros(1, 2, dk, dv), [T], max_q, 64.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("dv", [40, 64, 128])
+@pytest.mark.parametrize("apart", [14, 20, 24])
+def test_value_columns_far_apart(vq, torch_dev, dtype, max_q, dv, apart):
+    """Columns 2^14 to 2^24 larger than their neighbours: each keeps its own accuracy, outputs and state."""
+    torch, dt, T = torch_dev, _t(torch_dev, dtype), 300
+    q, k = _randn(torch, (T, 1, 128), dt, 1, 1.0), _randn(torch, (T, 1, 128), dt, 2, 128 ** -0.5)
+    v = _randn(torch, (T, 2, dv), dt, 3, 2.0 ** (12 - apart))
+    state = _randn(torch, (1, 2, 128, dv), torch.float32, 4, 2.0 ** (10 - apart))
+    for c in (3, dv // 2 + 1, dv - 1):
+        v[:, :, c] *= 2.0 ** apart
+        state[:, :, :, c] *= 2.0 ** apart
+    _run(vq, torch, q, k, v, _decays(torch, T, 2, 5), state, [T], max_q, 1.0)
+
+
+@pytest.mark.parametrize("max_q", [16, 1300])
+def test_large_values_that_decay_at_once(vq, torch_dev, max_q):
+    """A token of large values with strong decay behind it, once a chunk, leaves the small ones' accuracy."""
+    torch, dt, T = torch_dev, torch_dev.float16, 1300
+    q, k = _randn(torch, (T, 1, 64), dt, 1, 1.0), _randn(torch, (T, 1, 64), dt, 2, 0.125)
+    v, g = _randn(torch, (T, 2, 64), dt, 3, 0.01), _decays(torch, T, 2, 5)
+    v[10::64] *= 2.0 ** 20
+    g[11::64] = -30.0
+    _run(vq, torch, q, k, v, g, torch.zeros(1, 2, 64, 64), [T], max_q, 1.0)
