@@ -44,6 +44,9 @@ __device__ __forceinline__ float exp_f32(float x) {
     return __builtin_amdgcn_exp2f(h) * fmaf(r, 0.6931471805599453f, 1.f);
 }
 
+// The log of a decay from kMinG on; NaN stays NaN.
+__device__ __forceinline__ float bounded(float g) { return g < kMinG ? kMinG : g; }
+
 __device__ __forceinline__ int lin_row(const LinArgs& a, int r) { return min(max(a.cu[r], 0), a.T); }
 
 // The state slot of a request, or -1, and whether it starts from what the slot holds.
@@ -101,7 +104,7 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
     };
     auto token = [&](int t, const Token& x) __attribute__((always_inline)) {
         const f32x4 v = {lo16<E>(x.v[0]), hi16<E>(x.v[0]), lo16<E>(x.v[1]), hi16<E>(x.v[1])};
-        const float e = exp_f32(fmaxf(x.g, kMinG));
+        const float e = exp_f32(bounded(x.g));
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
         if (wave < 2) return;
         // the bound here, not where g is loaded: it would wait for the load
-        const float b = lane_scan(fmaxf(gv, kMinG), 0.f, [](float x, float y) { return x + y; });
+        const float b = lane_scan(bounded(gv), 0.f, [](float x, float y) { return x + y; });
         const float eb = exp_f32(b);
         if (wave == 2) {
             d.eb[lane] = eb;

@@ -87,3 +87,23 @@ def test_large_values_that_decay_at_once(vq, torch_dev, max_q):
     v[10::64] *= 2.0 ** 20
     g[11::64] = -30.0
     _run(vq, torch, q, k, v, g, torch.zeros(1, 2, 64, 64), [T], max_q, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,max_q", [([9, 30, 5], 16), ([9, 130, 70], 130), ([700, 900, 20], 900)])
+def test_nan_decays_stay_nan(vq, torch_dev, dtype, lens, max_q):
+    """A NaN decay: NaN in its head from that token on and in its state, nothing else changes."""
+    torch, dt, T = torch_dev, _t(torch_dev, dtype), sum(lens)
+    q, k = _randn(torch, (T, 2, 64), dt, 1, 0.125).cuda(), _randn(torch, (T, 2, 64), dt, 2, 0.125).cuda()
+    v, g = _randn(torch, (T, 4, 64), dt, 3).cuda(), _decays(torch, T, 4, 5).cuda()
+    state = _randn(torch, (3, 4, 64, 64), torch.float32, 4).cuda()
+    cu = torch.tensor([sum(lens[:i]) for i in range(4)], dtype=torch.int32, device="cuda")
+    op = vq.LinearAttention(2, 4, 64, 64)
+    y, out = op.forward(q, k, v, g, state, cu, max_q=max_q)
+    at = lens[0] + 2 * lens[1] // 3
+    g[at, 2] = float("nan")
+    y2, out2 = op.forward(q, k, v, g, state, cu, max_q=max_q)
+    end = lens[0] + lens[1]
+    assert y2[at:end, 2].isnan().all() and out2[1, 2].isnan().all()
+    y2[at:end, 2], out2[1, 2] = y[at:end, 2], out[1, 2]
+    assert torch.equal(y2, y) and torch.equal(out2, out)
