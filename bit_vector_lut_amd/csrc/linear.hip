@@ -16,7 +16,7 @@ namespace vqmlp {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kStepMaxQ = 16;
@@ -41,7 +41,7 @@ struct LinArgs {
 __device__ __forceinline__ float exp_f32(float x) {
     const float h = x * kLog2e;
     const float r = fmaf(x, kLog2e, -h) + x * 1.925963033500e-8f;  // log2 e - float(log2 e)
-    return __builtin_amdgcn_exp2f(h) * fmaf(r, 0.6931471805599453f, 1.f);
+    return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
 }
 
 // The log of a decay from kMinG on; NaN stays NaN.
@@ -212,7 +212,8 @@ __device__ __forceinline__ constexpr int tok_bits(int row, int chunk) {
 __device__ __forceinline__ constexpr int tok_at(int row, int chunk) { return row * kC * 2 + tok_bits(row, chunk); }
 
 struct alignas(16) LinDecay {  // of one chunk; b = sum of g up to a token
-    float eb[kC], bl[kC];    // e^b, b log2 e
+    float eb[kC];            // e^b
+    float bl[kC], lo[kC];    // b log2 e and what it lost in rounding
     float tail[kC];          // e^(sum behind the token)
     uint16_t weight[kC];     // 2^15 tail in binary16 (of binary16 values)
     float etot;              // e^(sum of the chunk)
@@ -234,8 +235,12 @@ struct LinOutSmem {
 template <class T, class F>
 __device__ __forceinline__ T lane_scan(T v, T none, F&& op) {
     auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
-        const int n = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
-                                                  decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+        struct Words { int w[sizeof(T) / 4]; };
+        Words n = __builtin_bit_cast(Words, none);
+        const Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+        for (size_t i = 0; i < sizeof(T) / 4; ++i)
+            n.w[i] = __builtin_amdgcn_update_dpp(n.w[i], x.w[i], decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
         v = op(v, __builtin_bit_cast(T, n));
     };
     typedef std::integral_constant<int, 0xF> all;
@@ -450,15 +455,18 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
         const int i = wave == 3 ? 63 - lane : lane;
         gv = t + i < t1 ? *reinterpret_cast<const float*>(base + uint32_t(i) * uint32_t(a.ld_g) * 4) : 0.f;
     };
-    // sums from the front for e^{b}, from the back for the tails, each accurate against its own size
+    // Sums from the front for e^{b}, from the back for the tails, in FP64: behind strong decays b reaches thousands,
+    // and the scores take differences of neighbours (in FP32 they kept 3e-4, less than binary16 holds).
     auto decays = [&](LinDecay& d) __attribute__((always_inline)) {
         if (wave < 2) return;
         // the bound here, not where g is loaded: it would wait for the load
-        const float b = lane_scan(bounded(gv), 0.f, [](float x, float y) { return x + y; });
-        const float eb = exp_f32(b);
+        const double b = lane_scan(double(bounded(gv)) * 1.4426950408889634, 0., [](double x, double y) { return x + y; });
+        const float bl = float(b), lo = float(b - bl);
+        const float eb = __builtin_amdgcn_exp2f(bl) * fmaf(lo, kLn2, 1.f);
         if (wave == 2) {
             d.eb[lane] = eb;
-            d.bl[lane] = b * kLog2e;
+            d.bl[lane] = bl;
+            d.lo[lane] = lo;
             if (lane == 63) d.etot = eb;
         } else {
             // from the back b reaches to token 63 - lane: what lies behind token 62 - lane
@@ -508,8 +516,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
     auto clip = [](int x) { return min(max(x, -60), 60); };
     int su = HALF ? clip(11 - expo(a.scale)) : 0;
     // This wave's 16 keys with queries 16 x .., times their decays; the lane's largest so far.
-    auto scores = [&](const LinDecay& dc, int x, const u32x4* kf, const u32x4* qf, const f32x4& bj4, float unit,
-                      float& top) __attribute__((always_inline)) {
+    auto scores = [&](const LinDecay& dc, int x, const u32x4* kf, const u32x4* qf, float unit, float& top) __attribute__((always_inline)) {
         if constexpr (OUT) {
             if (x < (wave & 2)) return;
             float p[4] = {0.f, 0.f, 0.f, 0.f};  // keys behind the queries' block
@@ -517,9 +524,11 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 f32x4 sc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) sc = E::mfma16(kf[s], qf[s], sc);
-                const float bt = dc.bl[16 * x + lr];
+                const float bt = dc.bl[16 * x + lr], one = unit * fmaf(dc.lo[16 * x + lr], kLn2, 1.f);
+                const f32x4 bj = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
+                const f32x4 lj = *reinterpret_cast<const f32x4*>(&dc.lo[16 * wave + 4 * g4]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = sc[i] * unit * __builtin_amdgcn_exp2f(bt - bj4[i]);
+                for (int i = 0; i < 4; ++i) p[i] = sc[i] * one * __builtin_amdgcn_exp2f((bt - bj[i]) - lj[i]);
                 if (x == wave) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) p[i] = 4 * g4 + i <= lr ? p[i] : 0.f;
@@ -574,11 +583,10 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 for (int x = 0; x < 4; ++x) qf[x][s] = qk_read(so.q, 16 * x + lr, s);
             }
             __builtin_amdgcn_sched_barrier(0);  // all reads on their way before the first product waits
-            const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
             const float unit = a.scale * pow2(su);
             float top = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) scores(dc, x, kf, qf[x], bj4, unit, top);
+            for (int x = 0; x < 4; ++x) scores(dc, x, kf, qf[x], unit, top);
             if constexpr (HALF) {
                 // an infinite score is no measure of the others; of values that are not negative, the bits are
                 // in the values' order
@@ -666,13 +674,12 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                     u32x4 qf[KS], kf[KS];
 #pragma unroll
                     for (int s = 0; s < KS; ++s) kf[s] = qk_read(so.k, 16 * wave + lr, s);
-                    const f32x4 bj4 = *reinterpret_cast<const f32x4*>(&dc.bl[16 * wave + 4 * g4]);
                     float top = 0.f;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
 #pragma unroll
                         for (int s = 0; s < KS; ++s) qf[s] = qk_read(so.q, 16 * x + lr, s);
-                        scores(dc, x, kf, qf, bj4, a.scale * pow2(su), top);
+                        scores(dc, x, kf, qf, a.scale * pow2(su), top);
                         __builtin_amdgcn_sched_barrier(0);  // few registers: S, o and the next chunk's loads stay
                     }
                     __syncthreads();

@@ -6,6 +6,8 @@ and the state as an operand are rounded once each (2 u z at most); FP32 sums and
 of z and a chunk's worth more for each 64 tokens (W / 16 a token).  2^-25 is half a step of the
 smallest binary16.  The state is FP32: 100 W and W / 8 a token of its recurrence of absolute values.
 """
+import math
+
 import pytest
 
 from test_gpu_block_ops import W, _close, _linear_ref, _randn, _t, _u, torch_dev, vq  # noqa: F401
@@ -107,3 +109,25 @@ def test_nan_decays_stay_nan(vq, torch_dev, dtype, lens, max_q):
     assert y2[at:end, 2].isnan().all() and out2[1, 2].isnan().all()
     y2[at:end, 2], out2[1, 2] = y[at:end, 2], out[1, 2]
     assert torch.equal(y2, y) and torch.equal(out2, out)
+
+
+@pytest.mark.parametrize("max_q", [16, 200])
+@pytest.mark.parametrize("strong", [-math.inf, -79.37, -33.3])
+def test_decays_behind_strong_ones(vq, torch_dev, max_q, strong):
+    """Forty tokens that forget nearly everything, then weak decays: with one-hot keys and values each
+    output is one score times its decay, rounded once, and 20 W for scale and exponential."""
+    torch, T, n = torch_dev, 104, 64
+    g = torch.full((T, 1), strong)
+    g[40:, 0] = -0.02 * torch.rand(T - 40, generator=torch.Generator().manual_seed(3))
+    q = torch.ones(T, 1, n, dtype=torch.float16)
+    k, v = torch.zeros(T, 1, n, dtype=torch.float16), torch.zeros(T, 1, n, dtype=torch.float16)
+    for j in range(n):
+        k[40 + j, 0, j] = v[40 + j, 0, j] = 1.0
+    i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    # 64 tokens are one chunk: no state of a chunk before plays a part
+    op = vq.LinearAttention(1, 1, n, n, 1.0)
+    y, _ = op.forward(q[:64].cuda(), k[:64].cuda(), v[:64].cuda(), g[:64].cuda(), op.state(1), i([0, 64]), max_q=max_q)
+    b = g[40:64, 0].double().cumsum(0)
+    ref = torch.exp(b[:, None] - b[None, :]).tril()
+    got = y[40:, 0, :24].double().cpu()
+    _close(torch, got, ref, (2.0 ** -11 + 20 * W) * ref, "y")
