@@ -53,6 +53,7 @@ class Decoder:
         self.planners = [vqmlp.PagePlanner(self.table, free, page_size, pages, t_max, free_head=h)
                          for h in self.free_head]
         self.ctx_len = torch.zeros(requests, **i32)
+        self.errors = torch.zeros(1, **i32)  # the error bits of all plans so far
 
         self.layers = []
         pre = [weight(H) for _ in range(2 * layers + 1)]  # norms in front of each mixer, MLP, the head
@@ -100,7 +101,8 @@ class Decoder:
 
     def step(self, tokens, lens):
         """tokens: the requests' new tokens one after another (device, [sum of lens]); lens: how many each
-        request brings (host).  Returns (hidden states [T, H] in front of the head, the PagePlan)."""
+        request brings (host).  Returns (hidden states [T, H] in front of the head, the PagePlan).  A plan
+        that fails (a request beyond max_len) leaves the requests as they are and its bits in `errors`."""
         import torch
 
         T = tokens.shape[0]
@@ -110,6 +112,7 @@ class Decoder:
         planner = self.planners[0]
         q_len = torch.tensor(lens, dtype=torch.int32, device=self.device)
         plan = planner.forward(self.ctx_len, q_len, free_head_out=then)
+        self.errors |= plan.status[:1]
         self.free_head.reverse()
         self.planners.reverse()
         r = self.embed[tokens].float()
@@ -125,8 +128,13 @@ class Decoder:
         return self.first.forward(None, r)[1]
 
     def next_tokens(self, x, plan):
-        """Greedy next token of each request from the hidden states of its last row."""
-        return self.head.argmax(x[(plan.cu_q[1:] - 1).long()].contiguous())[0]
+        """Greedy next token of each request from the hidden states of its last row; -1 for a request
+        without new tokens in this step, and for all of them after a plan that failed (int32)."""
+        import torch
+
+        end = plan.cu_q[1:]
+        tokens = self.head.argmax(x[(end - 1).clamp(min=0).long()].contiguous())[0]
+        return torch.where(end > plan.cu_q[:-1], tokens, -1)
 
 
 def main(steps=16, seed=0):
@@ -140,6 +148,8 @@ def main(steps=16, seed=0):
         x, plan = model.step(tokens, lens)
         tokens, lens = model.next_tokens(x, plan).long(), [1] * len(lens)
         out.append(tokens)
+    if model.errors.item():
+        raise RuntimeError("a plan failed, error bits %d" % model.errors.item())
     print("status of the last plan (errors, tokens, new pages, 0):", plan.status.tolist())
     for r, row in enumerate(torch.stack(out, 1).tolist()):
         print("request %d:" % r, row)

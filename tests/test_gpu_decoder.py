@@ -57,3 +57,26 @@ def test_step_refuses_what_does_not_fit():
         model.step(torch.zeros(4, dtype=torch.long, device="cuda"), [1, 1, 1])
     with pytest.raises(ValueError):
         model.step(torch.zeros(2, dtype=torch.long, device="cuda"), [1, 1])
+
+
+def test_idle_requests_and_failed_plans_give_no_token():
+    """A request without new tokens has no next token (-1), nor has any after a plan that failed."""
+    import torch
+
+    from bit_vector_lut_amd import decoder
+
+    model = decoder.Decoder(layers=1, max_len=32, seed=2)
+    tokens = torch.randint(0, 4096, (9,), generator=torch.Generator().manual_seed(2)).cuda()
+    x, plan = model.step(tokens[:9], [4, 0, 5])
+    got = model.next_tokens(x, plan)
+    want = model.head.argmax(x[[3, 8]].contiguous())[0]
+    assert got.tolist() == [want[0].item(), -1, want[1].item()]
+    x, plan = model.step(tokens[:3], [0, 3, 0])
+    got = model.next_tokens(x, plan).tolist()
+    assert got[0] == -1 and got[2] == -1 and got[1] >= 0
+    assert model.errors.item() == 0
+    x, plan = model.step(torch.zeros(29, dtype=torch.long, device="cuda"), [29, 0, 0])  # 33 of 32 positions
+    assert plan.status[0].item() == 1 and model.next_tokens(x, plan).tolist() == [-1, -1, -1]
+    x, plan = model.step(tokens[:3], [1, 1, 1])  # the step after it works, and the error is remembered
+    assert plan.status[0].item() == 0 and min(model.next_tokens(x, plan).tolist()) >= 0
+    assert model.errors.item() == 1
