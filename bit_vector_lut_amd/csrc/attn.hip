@@ -312,6 +312,10 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int mt = G.lds ? kAttnTileRows : 16, key_tile = G.lds ? 64 : 32;
     G.tiles = int(all / mt) + d.R + 1;
     const int64_t active = std::max<int64_t>(d.R, (all + mt - 1) / mt) * d.kv_heads;
+    // A launch holds fewer than 2^32 threads: the places of all tiles' splits, the join's rows.
+    const int64_t places = ((1 << 24) - 1) / (int64_t(G.tiles) * d.kv_heads);
+    const int most = rows_all >= size_t(1) << 26
+                         ? 1 : int(std::min<int64_t>(kMaxSplit, std::max<int64_t>(1, d.R > 1 ? (places - 1) | 1 : places)));
     auto splits = [&](int key_tiles) {
         if (G.lds) {
             // Times in us.  A workgroup passes over a tile in 1 us and 0.35 more for each wave with rows
@@ -324,7 +328,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
             const double alone = (1.0 + 0.35 * double(std::min<int64_t>(4, (rows + 31) / 32))) * d.D / 128;
             int nsplit = 1;
             double best = 1e300;
-            for (int ns = 1; ns <= std::min(kMaxSplit, std::max(1, key_tiles / 4)); ++ns) {
+            for (int ns = 1; ns <= std::min(most, std::max(1, key_tiles / 4)); ++ns) {
                 const int64_t blocks = active * ns;
                 const int64_t busy = std::min((blocks + cus - 1) / cus * cus, slots);  // as full as the fullest
                 const double tile = std::max(alone, double(busy) * key_tile * d.D * 4 / 5e6 * d.R * d.kv_heads / active);
@@ -338,7 +342,7 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
         }
         // four workgroups a compute unit: 123 us at the sizes above, 127 / 130 / 147 with 3 / 6 / 12
         const int64_t want = (int64_t(cus) * 4 + active - 1) / active;
-        return int(std::min<int64_t>(std::min<int64_t>(want, std::max(1, key_tiles / 8)), kMaxSplit));
+        return int(std::min<int64_t>(std::min<int64_t>(want, std::max(1, key_tiles / 8)), most));
     };
     // Through a window a row tile sees that many keys and one for each of its tokens: one request of a
     // token over 32,000 keys, 40/8 heads of 128, window 4,096: 15 us, 27 with splits for all 32,000; 64
@@ -380,9 +384,9 @@ vqmlp_status attn_check(const vqmlp_attn_desc* p, const char* who, int* shift) {
         OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: heads / kv_heads above 64 or R above 65536", who);
     if (int64_t(d.T) * d.heads > 0x3FFFFFFF)
         OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: T * heads above 2^30 - 1", who);
-    // workgroups of any split: a launch holds fewer than 2^32 threads
-    if ((int64_t(d.T) * (d.heads / d.kv_heads) / kAttnTileRows + d.R + 1) * d.kv_heads > (1 << 24))
-        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: (T * heads / 128 + R * kv_heads) above 2^24", who);
+    // a launch holds fewer than 2^32 threads; attn_geom splits no further than that
+    if ((int64_t(d.T) * (d.heads / d.kv_heads) / kAttnTileRows + d.R + 1) * d.kv_heads >= (1 << 24))
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: (T * heads / kv_heads / 128 + R + 1) * kv_heads is not below 2^24", who);
     OP_REQUIRE((int64_t(d.n_pages) << *shift) <= 0x7FFFFFFF && (int64_t(d.table_width) << *shift) <= 0x3FFFFFFF,
                "%s: slots pass 2^31 - 1 or positions 2^30 - 1", who);
     OP_REQUIRE(d.scale > 0.f && d.scale < __builtin_inff(), "%s: scale is not positive and finite", who);

@@ -376,7 +376,7 @@ vqmlp_status vqmlp_paged_store(int dtype, int T, int kv_heads, int D, int page_s
  * anything where no row of its request sees them; elsewhere they have to be finite.
  * q, y [T][heads][D] with token strides ld_q, ld_y (elements, multiples of 8; 16-byte aligned);
  * lse FP32 [T][heads] or NULL.  heads / kv_heads up to 64, R <= 65536, T * heads < 2^30 and
- * T * heads / 128 + R * kv_heads up to 2^24.  max_kv: the longest kv_len
+ * (T * heads / kv_heads / 128 + R + 1) * kv_heads below 2^24.  max_kv: the longest kv_len
  * that is expected; it chooses the split of the keys, and any value gives a right answer.  The
  * workspace (256-byte aligned, no zero fill) follows vqmlp_paged_attn_workspace of the same
  * description on the same device; two calls that overlap in time need one each. */
