@@ -16,10 +16,6 @@ namespace vqmlp {
 
 namespace {
 
-struct NormArgs {
-    vqmlp_norm_desc d;
-};
-
 // Sum over the workgroup, in every thread.  Two alternating slots in LDS: a slot is written again
 // only two reductions later, with the barrier of the one between them in front of it.
 constexpr int kMaxWaves = 16;
@@ -234,22 +230,37 @@ __global__ void __launch_bounds__(256) k_norm_any(vqmlp_norm_desc d) {
 }
 
 template <class E, bool RES32>
-const char* launch_norm(const vqmlp_norm_desc& d, bool vec, int cus, hipStream_t s) {
+const char* launch_norm(vqmlp_norm_desc d, bool vec, int cus, hipStream_t s) {
     const int chunks = d.H / 8;
-    if (!vec || chunks > 2048) {
-        k_norm_any<E, RES32><<<d.T, 256, 0, s>>>(d);
-        return "element kernel";
-    }
     // Few rows: latency, so a chunk a thread (8 rows of 5120: 4.1 us in a graph, 4.9 / 5.7 with 2 / 3
     // chunks).  Many: two (8192 rows of 5120 with gates and an FP32 residual: 120 us, 127 / 126 / 130
     // with 1 / 3 / 4); from 2 chunks a thread on a workgroup has at most 512 threads.
-    const int ch = chunks > 1024 ? 4 : chunks <= 64 || d.T <= 2 * cus ? 1 : 2;
-    const unsigned nt = unsigned((chunks + 64 * ch - 1) / (64 * ch)) * 64;
-    switch (ch) {
-        case 1: k_norm<E, RES32, 1><<<d.T, nt, 0, s>>>(d); return "vector kernel, 1 chunk a thread";
-        case 2: k_norm<E, RES32, 2><<<d.T, nt, 0, s>>>(d); return "vector kernel, 2 chunks a thread";
-        default: k_norm<E, RES32, 4><<<d.T, nt, 0, s>>>(d); return "vector kernel, 4 chunks a thread";
+    const int ch = !vec || chunks > 2048 ? 0 : chunks > 1024 ? 4 : chunks <= 64 || d.T <= 2 * cus ? 1 : 2;
+    const unsigned nt = ch ? unsigned((chunks + 64 * ch - 1) / (64 * ch)) * 64 : 256;
+    // a launch of 2^32 threads or more drops rows without an error
+    const int most = int((0xFFFFFFFFull / nt) & ~7ull);
+    auto behind = [&](const void* p, int64_t ld, int bytes) {
+        return p ? reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) + most * ld * bytes) : nullptr;
+    };
+    const int re = RES32 ? 4 : 2;
+    for (int left = d.T; left > 0; left -= most) {
+        d.T = std::min(left, most);
+        switch (ch) {
+            case 0: k_norm_any<E, RES32><<<d.T, nt, 0, s>>>(d); break;
+            case 1: k_norm<E, RES32, 1><<<d.T, nt, 0, s>>>(d); break;
+            case 2: k_norm<E, RES32, 2><<<d.T, nt, 0, s>>>(d); break;
+            default: k_norm<E, RES32, 4><<<d.T, nt, 0, s>>>(d);
+        }
+        d.y = behind(d.y, d.ld_y, 2);
+        d.res = behind(d.res, d.ld_res, re);
+        d.gate = behind(d.gate, d.ld_gate, 2);
+        d.res_out = behind(d.res_out, d.ld_res_out, re);
+        d.x = behind(d.x, d.ld_x, 2);
     }
+    return ch == 0   ? "element kernel"
+           : ch == 1 ? "vector kernel, 1 chunk a thread"
+           : ch == 2 ? "vector kernel, 2 chunks a thread"
+                     : "vector kernel, 4 chunks a thread";
 }
 
 }  // namespace

@@ -28,3 +28,24 @@ def test_attention_splits_fit_a_launch(R, T, heads, kv_heads, max_kv):
     print("splits", splits, flush=True)
     assert tiles * kv_heads * places * 256 < 2 ** 32
     assert splits == 1 or (T * heads + 3) // 4 * 256 < 2 ** 32  # the join
+
+
+@pytest.mark.parametrize("T,H", [(2 ** 26 + 5, 8), (2 ** 24 + 9, 3)])
+def test_norms_of_more_rows_than_a_launch_holds(T, H):
+    """Rows in front of, around and behind the end of the first launch give what a call of their own gives."""
+    import torch
+
+    from bit_vector_lut_amd import vqmlp
+
+    h = dict(dtype=torch.float16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    y, res = torch.empty(T, H, **h).normal_(generator=g), torch.empty(T, H, dtype=torch.float32, device="cuda").normal_(generator=g)
+    gate = torch.empty(T, H, **h).normal_(generator=g)
+    op = vqmlp.BlockNorm(torch.rand(H, generator=g, **h), post_weight=torch.rand(H, generator=g, **h))
+    print("norm", T, H, flush=True)
+    r, x = op.forward(y, res, gate)
+    torch.cuda.synchronize()
+    for a in (0, T // 2, T - 5 - 16, T - 8):
+        rows = slice(a, min(T, a + 16))
+        r2, x2 = op.forward(y[rows], res[rows], gate[rows])
+        assert torch.equal(r[rows], r2) and torch.equal(x[rows], x2)
