@@ -915,6 +915,9 @@ vqmlp_status lin_check(const vqmlp_linear_desc* p, const char* who) {
                "%s: Dk=%d, Dv=%d are not multiples of 8 up to 128", who, d.Dk, d.Dv);
     if (d.R > 65535 || d.v_heads > 65535 || d.T > 0x3FFFFFFF)
         OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: R or v_heads above 65535, or T above 2^30 - 1", who);
+    // workgroup numbers are 32-bit (segments have four chunks or more; rounded up to whole rounds of XCDs)
+    if ((int64_t(d.T) / (4 * kC) + d.R + 1 + 8) * d.v_heads > 0x7FFFFFFF)
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: (T / 256 + R + 9) * v_heads above 2^31 - 1", who);
     OP_REQUIRE(d.scale == d.scale && d.scale - d.scale == 0.f, "%s: scale is not finite", who);
     return VQMLP_OK;
 }

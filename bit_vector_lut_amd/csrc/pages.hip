@@ -197,6 +197,7 @@ extern "C" vqmlp_status vqmlp_page_plan(const vqmlp_pages_desc* p, void* stream)
     OP_REQUIRE(d.R >= 1 && d.max_tokens >= 0 && d.n_pages >= 1 && d.n_free >= 0 && d.table_width >= 1,
                "vqmlp_page_plan: a size is out of range");
     if (d.R > kPlanMaxR) OP_FAIL(VQMLP_ERR_UNSUPPORTED, "vqmlp_page_plan: R=%d above %d", d.R, kPlanMaxR);
+    if (d.max_tokens > 0x3FFFFFFF) OP_FAIL(VQMLP_ERR_UNSUPPORTED, "vqmlp_page_plan: max_tokens above 2^30 - 1");
     OP_REQUIRE((int64_t(d.n_pages) << shift) <= 0x7FFFFFFF && (int64_t(d.table_width) << shift) <= 0x7FFFFFFF,
                "vqmlp_page_plan: positions or slots pass 2^31 - 1");
     OP_REQUIRE(d.ld_table >= d.table_width, "vqmlp_page_plan: ld_table is below table_width");
@@ -235,6 +236,8 @@ extern "C" vqmlp_status vqmlp_paged_store(int dtype, int T, int kv_heads, int D,
     OP_REQUIRE(T >= 0 && kv_heads >= 1 && kv_heads <= 65535 && D >= 8 && D <= 256 && D % 8 == 0 && n_pages >= 1,
                "vqmlp_paged_store: T=%d, kv_heads=%d, D=%d, n_pages=%d", T, kv_heads, D, n_pages);
     OP_REQUIRE((int64_t(n_pages) << shift) <= 0x7FFFFFFF, "vqmlp_paged_store: slots pass 2^31 - 1");
+    // a launch holds fewer than 2^32 threads
+    if (T > 0x3FFFFFFF) OP_FAIL(VQMLP_ERR_UNSUPPORTED, "vqmlp_paged_store: T above 2^30 - 1");
     if (T == 0) return op_ok();
     OP_REQUIRE(k && v && slot && k_cache && v_cache, "vqmlp_paged_store: null pointer");
     const int64_t row = int64_t(kv_heads) * D;

@@ -330,7 +330,7 @@ vqmlp_status vqmlp_block_norm(const vqmlp_norm_desc *desc, void *stream);
  * A paged cache holds n_pages pages of page_size positions (a power of two, 8..1024).  Position p
  * of request r stands in page table[r][p / page_size] at offset p % page_size; its slot is
  * page * page_size + offset.  From the cached length ctx_len[r] and the new tokens q_len[r]
- * (DEVICE int32 [R], R <= 4096) one launch makes
+ * (DEVICE int32 [R], R <= 4096; max_tokens < 2^30) one launch makes
  *   seq_len[r] = ctx_len[r] + q_len[r];  cu_q[r] = q_len[0] + .. + q_len[r-1] (R + 1 entries);
  *   table[r][..]: pages ceil(ctx/page_size) .. ceil(seq/page_size)-1 are taken from the free list
  *     in order of request and position, free_pages[head], free_pages[head+1], ..  (head =
@@ -360,7 +360,7 @@ vqmlp_status vqmlp_page_plan(const vqmlp_pages_desc *desc, void *stream);
  * operand of the value product then is eight neighbouring positions, one 16-byte load).
  * vqmlp_paged_store: k, v [T][kv_heads][D] with token strides ld_k, ld_v (elements, multiples of
  * 8; 16-byte aligned) go to slot[t]; a slot outside [0, n_pages * page_size) is skipped, and two
- * tokens may not share a slot. */
+ * tokens may not share a slot.  T < 2^30. */
 vqmlp_status vqmlp_paged_store(int dtype, int T, int kv_heads, int D, int page_size, int n_pages,
                                const void *k, int64_t ld_k, const void *v, int64_t ld_v,
                                const int32_t *slot, void *k_cache, void *v_cache, void *stream);
@@ -410,7 +410,8 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
  * [0, T]; rows from cu_q[R] on give y = 0.  max_q: the most new tokens of one request that are
  * expected; it chooses the kernel (up to 16: the recurrence token by token; above: chunks of 64
  * tokens on the matrix cores), and any value gives a right answer.  In chunks scale * (q . k) times
- * its decay is rounded to dtype once, with F16 in a unit that follows the chunk's largest.  R <= 65535. */
+ * its decay is rounded to dtype once, with F16 in a unit that follows the chunk's largest.  R <= 65535,
+ * T < 2^30, (T / 256 + R + 9) * v_heads < 2^31. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
     float scale;

@@ -171,3 +171,14 @@ def test_binding_refuses_what_does_not_fit(vq):
     q, v, g = torch.zeros(3, 2, 64, dtype=h), torch.zeros(3, 4, 32, dtype=h), torch.zeros(3, 4)
     with pytest.raises(E, match="differ"):
         lin.forward(q, q, v.float(), g, lin.state(1, "cpu"), slot[:2])
+
+
+def test_sizes_that_pass_32_bit_workgroup_numbers_are_refused(vq):
+    """Sizes whose launch would hold 2^32 threads or more, or whose rounding up passes 2^31."""
+    L, top = vq.lib(), 2 ** 31 - 1
+    for n in (top, 2 ** 30):
+        _refused(vq, L.vqmlp_page_plan(C.byref(_pages(vq, max_tokens=n)), None), "max_tokens above", 2)
+        _refused(vq, L.vqmlp_paged_store(0, n, 2, 64, 16, 4, PTR, 128, PTR, 128, PTR, PTR, PTR, None), "T above", 2)
+    for kw in (dict(R=65535, v_heads=65534), dict(T=2 ** 30 - 1, v_heads=2048, ld_v=1 << 16, ld_y=1 << 16, ld_g=2048)):
+        d = _linear(vq, **dict(dict(ld_v=65534 * 32, ld_y=65534 * 32, ld_g=65534), **kw))
+        _refused(vq, L.vqmlp_linear_attn(C.byref(d), None, 0, None), "2^31 - 1", 2)
