@@ -588,6 +588,11 @@ def _work(on, workspace, nbytes):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+def _fixed(name):
+    """An attribute set once: the library was given its pointer or size."""
+    return property(lambda self: getattr(self, "_" + name))
+
+
 class BlockNorm:
     """r = residual + residual_scale * gate * N_post(y); x = N_pre(r): the norms, the gate and the
     residual sum between two blocks in one pass.  Weights [H] of y's type (None: that norm, or its
@@ -687,6 +692,10 @@ class PagePlanner:
     is kept up to date in place; free_pages [n] int32 is the free list, taken from free_head (int32
     [1] on the device, None: 0) on.  See include/vqmlp.h for the error bits."""
 
+    R, device, max_tokens = _fixed("R"), _fixed("device"), _fixed("max_tokens")
+    table, free_pages, free_head = _fixed("table"), _fixed("free_pages"), _fixed("free_head")
+    page_size, n_pages = _fixed("page_size"), _fixed("n_pages")
+
     def __init__(self, table, free_pages, page_size, n_pages, max_tokens, free_head=None):
         import torch
 
@@ -694,21 +703,21 @@ class PagePlanner:
         _need(table, "table", dev, torch.int32, (None, None), contiguous=False)
         if table.shape[1] > 1 and table.stride(1) != 1:
             _bad("table: a row's entries do not lie one after another")
-        self.R, self.device, self.max_tokens = table.shape[0], dev, max_tokens
-        self.table, self.free_pages, self.free_head = table, free_pages, free_head
-        self.page_size, self.n_pages = page_size, n_pages
-        self._sizes = [self.R, self.R + 1, max_tokens, max_tokens, 4]  # of a plan's parts
+        self._R, self._device, self._max_tokens = table.shape[0], dev, max_tokens
+        self._table, self._free_pages, self._free_head = table, free_pages, free_head
+        self._page_size, self._n_pages = page_size, n_pages
+        self._sizes = [self._R, self._R + 1, max_tokens, max_tokens, 4]  # of a plan's parts
         self._total = sum(self._sizes)
-        self._desc = _PagesDesc(R=self.R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
+        self._desc = _PagesDesc(R=self._R, max_tokens=max_tokens, page_size=page_size, n_pages=n_pages,
                                 n_free=free_pages.numel(), table_width=table.shape[1],
-                                ld_table=table.stride(0) if self.R > 1 else table.shape[1],
+                                ld_table=table.stride(0) if self._R > 1 else table.shape[1],
                                 free_pages=_need(free_pages, "free_pages", dev, torch.int32, (None,)),
                                 table=table.data_ptr())
         if free_head is not None:
             self._desc.free_head = _need(free_head, "free_head", dev, torch.int32, (1,))
 
     def empty_plan(self, stream=None):
-        return self._empty_plan(_OnStream(stream, self.device))
+        return self._empty_plan(_OnStream(stream, self._device))
 
     def _empty_plan(self, on):
         import torch
@@ -720,23 +729,23 @@ class PagePlanner:
         """ctx_len, q_len [R] int32 on the device -> PagePlan (plan: buffers to reuse)."""
         import torch
 
-        i, dev = torch.int32, self.device
+        i, dev = torch.int32, self._device
         d = _PagesDesc.from_buffer_copy(self._desc)
-        d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (self.R,))
-        d.q_len = _need(q_len, "q_len", dev, i, (self.R,))
+        d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (self._R,))
+        d.q_len = _need(q_len, "q_len", dev, i, (self._R,))
         on = _OnStream(stream, dev)
         if plan is None:
             plan = self._empty_plan(on)
             at = d.seq_len = plan.seq_len.data_ptr()
-            d.cu_q = at = at + 4 * self.R
-            d.slot = at = at + 4 * (self.R + 1)
-            d.position = at = at + 4 * self.max_tokens
-            d.status = at + 4 * self.max_tokens
+            d.cu_q = at = at + 4 * self._R
+            d.slot = at = at + 4 * (self._R + 1)
+            d.position = at = at + 4 * self._max_tokens
+            d.status = at + 4 * self._max_tokens
         else:
-            d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self.R,))
-            d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self.R + 1,))
-            d.slot = _need(plan.slot, "slot", dev, i, (self.max_tokens,))
-            d.position = _need(plan.position, "position", dev, i, (self.max_tokens,))
+            d.seq_len = _need(plan.seq_len, "seq_len", dev, i, (self._R,))
+            d.cu_q = _need(plan.cu_q, "cu_q", dev, i, (self._R + 1,))
+            d.slot = _need(plan.slot, "slot", dev, i, (self._max_tokens,))
+            d.position = _need(plan.position, "position", dev, i, (self._max_tokens,))
             d.status = _need(plan.status, "status", dev, i, (4,))
         if free_head_out is not None:
             d.free_head_out = _need(free_head_out, "free_head_out", dev, i, (1,))
@@ -748,13 +757,16 @@ class PagedCache:
     """A paged key/value cache: k [pages, kv_heads, page_size, D], v [pages, kv_heads, D, page_size]
     (float16, int16 as binary16 bits, or bfloat16)."""
 
+    k, v, device, dtype = _fixed("k"), _fixed("v"), _fixed("device"), _fixed("dtype")
+    n_pages, kv_heads, page_size, D = _fixed("n_pages"), _fixed("kv_heads"), _fixed("page_size"), _fixed("D")
+
     def __init__(self, k, v):
         _need(k, "k", k.device, None, (None,) * 4)
         n, h, p, D = k.shape
         _need(v, "v", k.device, k.dtype, (n, h, D, p))
-        self.k, self.v, self.device = k, v, k.device
-        self.n_pages, self.kv_heads, self.page_size, self.D = n, h, p, D
-        self.dtype = _dtype(k, "k")
+        self._k, self._v, self._device = k, v, k.device
+        self._n_pages, self._kv_heads, self._page_size, self._D = n, h, p, D
+        self._dtype = _dtype(k, "k")
         self._kp, self._vp = k.data_ptr(), v.data_ptr()
         self._work = {}  # workspace bytes of a description's sizes
 
@@ -769,23 +781,23 @@ class PagedCache:
         """k, v [T, kv_heads, D] into slot[t] (int32 [T]; a slot outside the cache is skipped)."""
         import torch
 
-        T, dev = k.shape[0], self.device
-        shape = (T, self.kv_heads, self.D)
-        if _dtype(k, "k") != self.dtype or _dtype(v, "v") != self.dtype:
+        T, dev = k.shape[0], self._device
+        shape = (T, self._kv_heads, self._D)
+        if _dtype(k, "k") != self._dtype or _dtype(v, "v") != self._dtype:
             _bad("k, v and the cache differ in type")
         kp, ld_k = _rows(k, "k", dev, shape)
         vp, ld_v = _rows(v, "v", dev, shape)
         sp = _need(slot, "slot", dev, torch.int32, (None,))
         if slot.shape[0] < T:
             _bad("slot has %d entries for %d tokens" % (slot.shape[0], T))
-        _OnStream(stream, dev).call(lib().vqmlp_paged_store, self.dtype, T, self.kv_heads, self.D,
-                                    self.page_size, self.n_pages, kp, ld_k, vp, ld_v, sp, self._kp,
+        _OnStream(stream, dev).call(lib().vqmlp_paged_store, self._dtype, T, self._kv_heads, self._D,
+                                    self._page_size, self._n_pages, kp, ld_k, vp, ld_v, sp, self._kp,
                                     self._vp)
 
     def _attn_desc(self, T, R, heads, table_width, window, max_kv, scale):
-        return _AttnDesc(self.dtype, T, R, heads, self.kv_heads, self.D, self.page_size, self.n_pages,
-                         window, table_width * self.page_size if max_kv is None else max_kv,
-                         self.D ** -0.5 if scale is None else scale, table_width)
+        return _AttnDesc(self._dtype, T, R, heads, self._kv_heads, self._D, self._page_size, self._n_pages,
+                         window, table_width * self._page_size if max_kv is None else max_kv,
+                         self._D ** -0.5 if scale is None else scale, table_width)
 
     def _work_bytes(self, d):
         key = (d.T, d.R, d.heads, d.max_kv, d.table_width, d.window)
@@ -794,7 +806,7 @@ class PagedCache:
             import torch
 
             n = C.c_size_t()
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self._device):
                 _check(lib().vqmlp_paged_attn_workspace(C.byref(d), C.byref(n)))
             if len(self._work) >= 4096:
                 self._work.clear()
@@ -812,10 +824,10 @@ class PagedCache:
         holds).  Returns y, or (y, lse float32 [T, heads]) with with_lse or lse."""
         import torch
 
-        dev, i = self.device, torch.int32
+        dev, i = self._device, torch.int32
         if q.dim() != 3:
             _bad("q is [T, heads, D]")
-        if _dtype(q, "q") != self.dtype:
+        if _dtype(q, "q") != self._dtype:
             _bad("q and the cache differ in type")
         T, heads, R = q.shape[0], q.shape[1], kv_len.shape[0]
         _need(table, "table", dev, i, (R, None), contiguous=False)
@@ -823,14 +835,14 @@ class PagedCache:
             _bad("table: a row's entries do not lie one after another")
         on = _OnStream(stream, dev)
         d = self._attn_desc(T, R, heads, table.shape[1], window, max_kv, scale)
-        d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self.D))
+        d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self._D))
         if y is None:
             y = on.like(q)
-            d.y, d.ld_y = y.data_ptr(), heads * self.D
+            d.y, d.ld_y = y.data_ptr(), heads * self._D
         else:
-            if _dtype(y, "y") != self.dtype:
+            if _dtype(y, "y") != self._dtype:
                 _bad("y and the cache differ in type")
-            d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self.D))
+            d.y, d.ld_y = _rows(y, "y", dev, (T, heads, self._D))
         if lse is None and with_lse:
             lse = on.empty((T, heads), torch.float32)
         if lse is not None:

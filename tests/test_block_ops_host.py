@@ -182,3 +182,20 @@ def test_sizes_that_pass_32_bit_workgroup_numbers_are_refused(vq):
     for kw in (dict(R=65535, v_heads=65534), dict(T=2 ** 30 - 1, v_heads=2048, ld_v=1 << 16, ld_y=1 << 16, ld_g=2048)):
         d = _linear(vq, **dict(dict(ld_v=65534 * 32, ld_y=65534 * 32, ld_g=65534), **kw))
         _refused(vq, L.vqmlp_linear_attn(C.byref(d), None, 0, None), "2^31 - 1", 2)
+
+
+def test_tensors_that_the_library_points_to_are_not_replaced(vq):
+    """A planner's and a cache's tensors and sizes are given to the library once: assigning others is refused,
+    where a call would have gone on with the old memory."""
+    import torch
+
+    i = torch.int32
+    planner = vq.PagePlanner(torch.zeros(2, 4, dtype=i), torch.zeros(3, dtype=i), 16, 8, 10, torch.zeros(1, dtype=i))
+    cache = vq.PagedCache.empty(4, 2, 16, 64, torch.float16, "cpu")
+    for what, names in ((planner, ("table", "free_pages", "free_head", "R", "max_tokens", "page_size", "n_pages", "device")),
+                        (cache, ("k", "v", "n_pages", "kv_heads", "page_size", "D", "dtype", "device"))):
+        for name in names:
+            value = getattr(what, name)
+            with pytest.raises(AttributeError):
+                setattr(what, name, value)
+            assert getattr(what, name) is value
