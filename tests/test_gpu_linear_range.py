@@ -131,3 +131,20 @@ def test_decays_behind_strong_ones(vq, torch_dev, max_q, strong):
     ref = torch.exp(b[:, None] - b[None, :]).tril()
     got = y[40:, 0, :24].double().cpu()
     _close(torch, got, ref, (2.0 ** -11 + 20 * W) * ref, "y")
+
+
+@pytest.mark.parametrize("heads,dk,dv", [(48, 64, 128), (48, 64, 64), (4, 128, 128), (16, 40, 96)])
+def test_workspaces_hold_for_both_types(vq, torch_dev, heads, dk, dv):
+    """A workspace of workspace_bytes is large enough whichever 16-bit type the call has."""
+    import ctypes as C
+
+    torch = torch_dev
+    torch.cuda.init()
+    op = vq.LinearAttention(heads, heads, dk, dv)
+    for T in list(range(100, 4000, 100)) + [5000, 8000, 12000, 20000, 40000]:
+        for R in (1, 2, 5):
+            have = op.workspace_bytes(T, R, T)
+            for dtype in (0, 1):
+                n = C.c_size_t()
+                assert vq.lib().vqmlp_linear_attn_workspace(C.byref(op._desc(dtype, T, R, 0, T)), C.byref(n)) == 0
+                assert n.value <= have, (T, R, dtype)
