@@ -529,6 +529,12 @@ def _bad(msg):
     raise VqmlpError(ERR_INVALID_ARG, msg)
 
 
+def _fits(value, what):
+    """value: sizes or-ed together.  ctypes cuts an integer to 32 bits without a word."""
+    if value >> 31:
+        _bad("%s: a size is negative or beyond 2^31 - 1" % what)
+
+
 _DTYPES = None
 
 
@@ -634,6 +640,7 @@ class BlockNorm:
                 _bad("the weights do not fit y (H, type or device)")
         if y is None and self.has_post:
             _bad("post_weight without y")
+        _fits(T | H, "block norm")
         d = _NormDesc.from_buffer_copy(self._desc)
         d.T, d.H = T, H
         on = _OnStream(stream, dev)
@@ -701,6 +708,7 @@ class PagePlanner:
 
         dev = table.device
         _need(table, "table", dev, torch.int32, (None, None), contiguous=False)
+        _fits(table.shape[0] | table.shape[1] | page_size | n_pages | max_tokens | free_pages.numel(), "page plan")
         if table.shape[1] > 1 and table.stride(1) != 1:
             _bad("table: a row's entries do not lie one after another")
         self._R, self._device, self._max_tokens = table.shape[0], dev, max_tokens
@@ -763,6 +771,7 @@ class PagedCache:
     def __init__(self, k, v):
         _need(k, "k", k.device, None, (None,) * 4)
         n, h, p, D = k.shape
+        _fits(n | h | p | D, "paged cache")
         _need(v, "v", k.device, k.dtype, (n, h, D, p))
         self._k, self._v, self._device = k, v, k.device
         self._n_pages, self._kv_heads, self._page_size, self._D = n, h, p, D
@@ -782,6 +791,7 @@ class PagedCache:
         import torch
 
         T, dev = k.shape[0], self._device
+        _fits(T, "store")
         shape = (T, self._kv_heads, self._D)
         if _dtype(k, "k") != self._dtype or _dtype(v, "v") != self._dtype:
             _bad("k, v and the cache differ in type")
@@ -795,9 +805,11 @@ class PagedCache:
                                     self._vp)
 
     def _attn_desc(self, T, R, heads, table_width, window, max_kv, scale):
+        if max_kv is None:
+            max_kv = table_width * self._page_size
+        _fits(T | R | heads | table_width | window | max_kv, "attention")
         return _AttnDesc(self._dtype, T, R, heads, self._kv_heads, self._D, self._page_size, self._n_pages,
-                         window, table_width * self._page_size if max_kv is None else max_kv,
-                         self._D ** -0.5 if scale is None else scale, table_width)
+                         window, max_kv, self._D ** -0.5 if scale is None else scale, table_width)
 
     def _work_bytes(self, d):
         key = (d.T, d.R, d.heads, d.max_kv, d.table_width, d.window)
@@ -833,8 +845,8 @@ class PagedCache:
         _need(table, "table", dev, i, (R, None), contiguous=False)
         if table.shape[1] > 1 and table.stride(1) != 1:
             _bad("table: a row's entries do not lie one after another")
-        on = _OnStream(stream, dev)
         d = self._attn_desc(T, R, heads, table.shape[1], window, max_kv, scale)
+        on = _OnStream(stream, dev)
         d.q, d.ld_q = _rows(q, "q", dev, (T, heads, self._D))
         if y is None:
             y = on.like(q)
@@ -872,6 +884,7 @@ class LinearAttention:
         return torch.zeros((n, self.v_heads, self.Dk, self.Dv), dtype=torch.float32, device=device)
 
     def _desc(self, dtype, T, R, n_states, max_q):
+        _fits(T | R | n_states | max_q, "linear attention")
         return _LinearDesc(dtype, T, R, self.k_heads, self.v_heads, self.Dk, self.Dv, n_states, max_q,
                            self.scale)
 

@@ -199,3 +199,24 @@ def test_tensors_that_the_library_points_to_are_not_replaced(vq):
             with pytest.raises(AttributeError):
                 setattr(what, name, value)
             assert getattr(what, name) is value
+
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32 + 5, -1, -2 ** 32 + 5])
+def test_sizes_beyond_32_bits_are_not_cut(vq, size):
+    """A window of 2^32 + 5 is refused, not taken for one of 5; and so for every size that is passed on."""
+    import torch
+
+    i, h = torch.int32, torch.float16
+    z = lambda *s, t=i: torch.zeros(s, dtype=t)  # noqa: E731
+    cache, lin = vq.PagedCache.empty(4, 2, 16, 64, h, "cpu"), vq.LinearAttention(2, 2, 64, 64)
+    q = z(3, 2, 64, t=h)
+    for call in (lambda: cache.attention(q, z(1, 4), z(2), z(1), window=size),
+                 lambda: cache.attention(q, z(1, 4), z(2), z(1), max_kv=size),
+                 lambda: cache.workspace_bytes(3, 1, 2, 4, size), lambda: cache.workspace_bytes(size, 1, 2, 4),
+                 lambda: lin.workspace_bytes(3, 1, size), lambda: lin.workspace_bytes(3, size, 3),
+                 lambda: lin._desc(0, 3, 1, size, 3),
+                 lambda: vq.PagePlanner(z(2, 4), z(3), 16, size, 10), lambda: vq.PagePlanner(z(2, 4), z(3), 16, 8, size),
+                 lambda: vq.PagePlanner(z(2, 4), z(3), size, 8, 10),
+                 lambda: vq.BlockNorm(torch.ones(1, dtype=h)).forward(z(1, 1, t=h).expand(2 ** 32 + 5, 1))):
+        with pytest.raises(vq.VqmlpError, match="2\\^31"):
+            call()
