@@ -224,6 +224,8 @@ struct LinSmem {
     __attribute__((aligned(256))) uint8_t vt[DVP * kC * 2];  // [dv][token]
     LinDecay d[2];           // of this chunk and the next
     __attribute__((aligned(16))) uint32_t top[4];  // largest score of each wave's keys
+    // Values that are not finite: whether a wave that stages V met one, and for its columns 64 - the first token.
+    uint32_t odd[4], late[DVP];
 };
 template <int DKP>
 struct LinOutSmem {
@@ -551,6 +553,36 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
         decays(sm.d[0]);
         fetch_g(t0 + kC);
     }
+    // A value that is not finite would reach its block's tokens before it, as zero times itself.  Where outputs
+    // are made it is taken out of LDS, and its column gets no number from its token on.  Zero times all values
+    // finds one: 32 vector instructions of the waves that stage V, which have fewer scores to make than wave 0.
+    auto take_out = [&]() __attribute__((always_inline)) {
+        float z[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j & 1] = E::dot2(blk[i][j], 0u, z[j & 1]);
+        const bool odd = __any(!(z[0] + z[1] == 0.f));
+        if (lane == 0) sm.odd[wave] = odd;
+        if (__builtin_expect(!odd, 1)) return;
+        constexpr uint32_t top = HALF ? 0x7C00u : 0x7F80u;
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {  // the lane's eight tokens of a column
+            u32x4* const at = reinterpret_cast<u32x4*>(&sm.vt[(put ^ tok_bits(cc, 0)) + cc * kC * 2]);
+            u32x4 w = *at;
+            int late = 0;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                if ((w[i] >> 16 & 0x7FFFu) >= top) w[i] &= 0xFFFFu, late = 63 - (8 * bi + 2 * i);
+                if ((w[i] & 0x7FFFu) >= top) w[i] &= 0xFFFF0000u, late = 64 - (8 * bi + 2 * i);
+            }
+            *at = w;
+#pragma unroll
+            for (int by = 8; by < 64; by *= 2) late = max(late, __shfl_xor(late, by));
+            if (bi == 0) sm.late[8 * cj + cc] = uint32_t(late);
+        }
+    };
+    const int vwave = DKP / 64 + (NTV == 2 ? wave / 2 : 0);  // that stages the columns of this wave
     for (int t = t0; t < t1; t += kC) {
         const LinDecay& dc = sm.d[(t - t0) / kC & 1];
         if (stage) {
@@ -573,6 +605,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
         }
         wait_loads();  // this wave's part of Q is in LDS
         __syncthreads();
+        if (OUT && stage && !isk) take_out();  // V is read behind the next barrier
         f32x4 o[NTV][4];
         if constexpr (OUT) {
             u32x4 qf[4][KS], kf[KS];
@@ -613,7 +646,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                     out |= mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
                 }
                 // outside the range in which binary16 holds all that matters of a column: other units
-                if (__any(out)) {
+                if (__builtin_expect(__any(out), 0)) {
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) {
                         const bool mine = mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
@@ -664,7 +697,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 const u32x4 w = *reinterpret_cast<const u32x4*>(sm.top);
                 const float mx = __builtin_bit_cast(float, uniform(int(max(max(w[0], w[1]), max(w[2], w[3])))));
                 const int to = clip(su + 10 - expo(mx));
-                if ((mx >= 32768.f || (mx < 32.f && mx > 0.f)) && to != su) {
+                if (__builtin_expect((mx >= 32768.f || (mx < 32.f && mx > 0.f)) && to != su, 0)) {
                     const float by = pow2(to - su);
 #pragma unroll
                     for (int v = 0; v < NTV; ++v)
@@ -714,6 +747,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
             }
         };
         if (HALF && !OUT) new_units();
+        int odd = 0;
         if constexpr (OUT) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -726,6 +760,18 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
                 }
+            }
+            odd = uniform(int(sm.odd[vwave]));
+            if (__builtin_expect(odd, 0)) {
+#pragma unroll
+                for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int from = 64 - int(sm.late[dvc(v, 4 * g4 + i)]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            o[v][x][i] = 16 * x + lr >= from ? __builtin_nanf("") : o[v][x][i];
+                    }
             }
             if constexpr (HALF) {
                 const float by = pow2(-su);
@@ -764,7 +810,10 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
         };
         float lift[NTV], keep[NTV];
 #pragma unroll
-        for (int v = 0; v < NTV; ++v) lift[v] = 1.f, keep[v] = dc.etot;
+        for (int v = 0; v < NTV; ++v) {
+            lift[v] = 1.f;
+            keep[v] = odd && sm.late[dvc(v, lr)] ? __builtin_nanf("") : dc.etot;
+        }
         if constexpr (HALF) {
 #pragma unroll
             for (int v = 0; v < NTV; ++v) {

@@ -14,6 +14,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // rounds to nearest even; the hardware does both.
 struct F16 {
     typedef _Float16 T;
+    static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+        typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2, a), __builtin_bit_cast(half2, b), c, false);
+    }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
                                                       __builtin_bit_cast(half8, b), c, 0, 0, 0);
@@ -25,6 +29,10 @@ struct F16 {
 };
 struct BF16 {
     typedef __bf16 T;
+    static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+        typedef __bf16 bhalf2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bhalf2, a), __builtin_bit_cast(bhalf2, b), c, false);
+    }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bhalf8, a),
                                                        __builtin_bit_cast(bhalf8, b), c, 0, 0, 0);

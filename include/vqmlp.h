@@ -401,7 +401,8 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
  * q, k [T][k_heads][Dk], v, y [T][v_heads][Dv] (F16 or BF16, token strides ld_*: multiples of 8 up
  * to 2^24, 16-byte aligned), g FP32 [T][v_heads] (token stride ld_g), the log of the decay: at most 0, -inf
  * forgets everything before (below -80 it is taken as -80, a factor of 2e-35; NaN makes the
- * outputs from its token on and the state NaN).  Dk and Dv are
+ * outputs from its token on and the state NaN).  What is not finite in k or v reaches the outputs from its
+ * token on (of v: of its column) and the state, in q its own outputs, and nothing else.  Dk and Dv are
  * multiples of 8 up to 128.  state_in, state_out FP32 [slots][v_heads][Dk][Dv], 16-byte aligned;
  * they may be the same array.  Request r uses slot state_index[r] (NULL: r); a slot outside
  * [0, n_states) starts from zero and its final state is dropped; no two requests share a slot.

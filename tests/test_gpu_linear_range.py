@@ -148,3 +148,35 @@ def test_workspaces_hold_for_both_types(vq, torch_dev, heads, dk, dv):
                 n = C.c_size_t()
                 assert vq.lib().vqmlp_linear_attn_workspace(C.byref(op._desc(dtype, T, R, 0, T)), C.byref(n)) == 0
                 assert n.value <= have, (T, R, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+@pytest.mark.parametrize("lens,max_q", [([9, 30, 5], 16), ([9, 130, 70], 130), ([700, 900, 20], 900)])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 72)])
+def test_values_that_are_not_finite_stay_behind_their_token(vq, torch_dev, dtype, what, lens, max_q, dk, dv):
+    """A NaN or infinity in v: in its column no number from that token on and in the state; nothing else
+    changes.  The same for a whole key, in every column of the heads that read it."""
+    torch, dt, T = torch_dev, _t(torch_dev, dtype), sum(lens)
+    q, k = _randn(torch, (T, 2, dk), dt, 1, 0.125).cuda(), _randn(torch, (T, 2, dk), dt, 2, 0.125).cuda()
+    v, g = _randn(torch, (T, 4, dv), dt, 3).cuda(), _decays(torch, T, 4, 5).cuda()
+    state = _randn(torch, (3, 4, dk, dv), torch.float32, 4).cuda()
+    cu = torch.tensor([sum(lens[:i]) for i in range(4)], dtype=torch.int32, device="cuda")
+    op = vq.LinearAttention(2, 4, dk, dv)
+    y, out = op.forward(q, k, v, g, state, cu, max_q=max_q)
+    end = lens[0] + lens[1]
+    for at in (lens[0], lens[0] + 1, lens[0] + 2 * lens[1] // 3, end - 2, end - 1):
+        print("linear", dtype, lens, max_q, what, at, flush=True)
+        for col in (0, 5, dv - 1):
+            w = v.clone()
+            w[at, 2, col] = float(what)
+            y2, out2 = op.forward(q, k, w, g, state, cu, max_q=max_q)
+            assert not y2[at:end, 2, col].isfinite().any() and not out2[1, 2, :, col].isfinite().any()
+            y2[at:end, 2, col], out2[1, 2, :, col] = y[at:end, 2, col], out[1, 2, :, col]
+            assert torch.equal(y2, y) and torch.equal(out2, out)
+        w = k.clone()
+        w[at, 1] = float(what)
+        y2, out2 = op.forward(q, w, v, g, state, cu, max_q=max_q)
+        assert not y2[at:end, 2:].isfinite().any() and not out2[1, 2:].isfinite().any()
+        y2[at:end, 2:], out2[1, 2:] = y[at:end, 2:], out[1, 2:]
+        assert torch.equal(y2, y) and torch.equal(out2, out)
