@@ -186,12 +186,12 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // stand side by side.  It puts the sum over the chunk's tokens of e^{..} |v|, decays included, into [2^14, 2^15);
 // the matrix cores make that sum, of 2^15 e^{..} in binary16 and |v| (a maximum by vector instructions took 57
 // instead of 53 us for the states of three packed prompts).  The state is taken up or down where its largest
-// element leaves [2^-2, 2^15).  One unit for all of a wave's columns took 160 instead of 166 us for those prompts,
-// but where columns lie 2^20 apart it cost the smaller ones' states 12 bits.
-// Binary16 scores have a power of two of their own, 2^su, which the outputs give back in FP32: su is the chunk's
-// before as long as the largest score stays in [2^5, 2^15), so that scores down to 2^-19 of it keep all bits;
-// otherwise the chunk's scores are made once more (2% of the time; without a unit scores below 2^-14 lose bits
-// and those beyond 65504 are infinite).
+// element leaves [2^-2, 2^15).  One unit for all of a wave's columns is 3% faster, but where columns lie 2^20 apart
+// it cost the smaller ones' states 12 bits.
+// Binary16 scores have a power of two of their own, 2^su, which the outputs give back with their rounding: su is the
+// chunk's before as long as the largest score stays in [2^5, 2^15), so that scores down to 2^-19 of it keep all
+// bits; otherwise the chunk's scores are made once more (2% of the time; without a unit scores below 2^-14 lose
+// bits and those beyond 65504 are infinite).
 //
 // Bound by the latencies of a chunk: two workgroups a compute unit (registers), each 64 x 64 scores,
 // 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
@@ -226,6 +226,7 @@ struct LinSmem {
     __attribute__((aligned(16))) uint32_t top[4];  // largest score of each wave's keys
     // Values that are not finite: whether a wave that stages V met one, and for its columns 64 - the first token.
     uint32_t odd[4], late[DVP];
+    __attribute__((aligned(16))) float unit[DVP];  // 2^-e of a column
 };
 template <int DKP>
 struct LinOutSmem {
@@ -505,6 +506,10 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
     const bool last = uniform(u.seg == u.nseg - 1 && slot >= 0);  // has the request's final state to write
     float decay = 1.f;  // over the segment so far (!OUT)
     int e[NTV] = {};    // a lane's columns of S are kept in units of 2^-e
+    if constexpr (HALF && OUT) {  // no other wave reads its columns
+#pragma unroll
+        for (int v = 0; v < NTV; ++v) sm.unit[dvc(v, lr)] = 1.f;
+    }
     auto scale_state = [&](const float* by) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < KS; ++p)
@@ -607,6 +612,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
         __syncthreads();
         if (OUT && stage && !isk) take_out();  // V is read behind the next barrier
         f32x4 o[NTV][4];
+        int odd = 0;
         if constexpr (OUT) {
             u32x4 qf[4][KS], kf[KS];
 #pragma unroll
@@ -642,17 +648,18 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mx[v] = fmaxf(mx[v], fabsf(S[p][b][v][i]));
-                    mx[v] = column_max(mx[v]);
                     out |= mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
                 }
                 // outside the range in which binary16 holds all that matters of a column: other units
                 if (__builtin_expect(__any(out), 0)) {
 #pragma unroll
                     for (int v = 0; v < NTV; ++v) {
+                        mx[v] = column_max(mx[v]);
                         const bool mine = mx[v] >= 32768.f || (mx[v] < 0.25f && mx[v] > 0.f);
                         const int f = mine ? min(max(min(max(10 - expo(mx[v]), -100 - e[v]), 100 - e[v]), -126), 126) : 0;
                         up[v] = pow2(f);
                         e[v] += f;
+                        sm.unit[dvc(v, lr)] = pow2(-e[v]);
                     }
                     scale_state(up);
                 }
@@ -678,19 +685,22 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 }
             float eb[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) eb[x] = dc.eb[16 * x + lr];
+            for (int x = 0; x < 4; ++x) eb[x] = dc.eb[16 * x + lr] * unit;
 #pragma unroll
             for (int v = 0; v < NTV; ++v) {
-                f32x4 down = {unit, unit, unit, unit};  // of the columns whose outputs the lane holds
                 if constexpr (HALF) {
+                    // of the columns whose outputs the lane holds
+                    const f32x4 down = *reinterpret_cast<const f32x4*>(&sm.unit[dvc(v, 4 * g4)]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) down[i] *= pow2(-__shfl(e[v], 4 * g4 + i));
+                    for (int x = 0; x < 4; ++x) o[v][x] *= down * eb[x];
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[v][x] *= eb[x];
                 }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) o[v][x] *= down * eb[x];
             }
             __syncthreads();
             // every wave is done with this chunk's queries and keys
+            odd = uniform(int(sm.odd[vwave]));
             if constexpr (HALF) {
                 // The largest score has to lie where binary16 holds it and those 2^-15 of it with all bits: else
                 // once more, in units that put it into [2^10, 2^11).
@@ -747,7 +757,6 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
             }
         };
         if (HALF && !OUT) new_units();
-        int odd = 0;
         if constexpr (OUT) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -761,7 +770,6 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                     for (int v = 0; v < NTV; ++v) o[v][x] = E::mfma16(vf[v][c], pf, o[v][x]);
                 }
             }
-            odd = uniform(int(sm.odd[vwave]));
             if (__builtin_expect(odd, 0)) {
 #pragma unroll
                 for (int v = 0; v < NTV; ++v)
@@ -773,13 +781,11 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                             o[v][x][i] = 16 * x + lr >= from ? __builtin_nanf("") : o[v][x][i];
                     }
             }
-            if constexpr (HALF) {
-                const float by = pow2(-su);
-#pragma unroll
-                for (int v = 0; v < NTV; ++v)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) o[v][x] *= by;
-            }
+            const float by = pow2(-su);  // one rounding of the product
+            auto out16 = [&](const f32x4& z, int i) __attribute__((always_inline)) {
+                if constexpr (HALF) return pack16<E>(fmaf(z[i], by, -0.f), fmaf(z[i + 1], by, -0.f));
+                else return pack16<E>(z[i], z[i + 1]);
+            };
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if (t + 16 * x + lr >= t1) continue;
@@ -787,12 +793,11 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 const uint32_t off = uint32_t(lr) * uint32_t(a.ld_y) * 2;
                 if constexpr (NTV == 2) {
                     const int dv = 32 * wave + 8 * g4;
-                    const u32x4 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3]),
-                                     pack16<E>(o[1][x][0], o[1][x][1]), pack16<E>(o[1][x][2], o[1][x][3])};
+                    const u32x4 w = {out16(o[0][x], 0), out16(o[0][x], 2), out16(o[NTV - 1][x], 0), out16(o[NTV - 1][x], 2)};
                     if (dv < a.Dv) *reinterpret_cast<u32x4*>(dst + (off + 2 * dv)) = w;
                 } else {
                     const int dv = 16 * wave + 4 * g4;
-                    const u32x2 w = {pack16<E>(o[0][x][0], o[0][x][1]), pack16<E>(o[0][x][2], o[0][x][3])};
+                    const u32x2 w = {out16(o[0][x], 0), out16(o[0][x], 2)};
                     if (dv < a.Dv) *reinterpret_cast<u32x2*>(dst + (off + 2 * dv)) = w;
                 }
             }
@@ -812,7 +817,8 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
 #pragma unroll
         for (int v = 0; v < NTV; ++v) {
             lift[v] = 1.f;
-            keep[v] = odd && sm.late[dvc(v, lr)] ? __builtin_nanf("") : dc.etot;
+            keep[v] = dc.etot;
+            if (__builtin_expect(odd, 0)) keep[v] = sm.late[dvc(v, lr)] ? __builtin_nanf("") : keep[v];
         }
         if constexpr (HALF) {
 #pragma unroll
@@ -820,6 +826,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))
                 lift[v] = pow2(en[v]);
                 keep[v] *= pow2(en[v] - e[v]);
                 e[v] = en[v];
+                if (OUT) sm.unit[dvc(v, lr)] = pow2(-en[v]);
             }
         }
         decay *= dc.etot;
