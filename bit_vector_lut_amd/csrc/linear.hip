@@ -301,15 +301,13 @@ __device__ __forceinline__ bool lin_unit(const LinArgs& a, int x, LinUnit& u) {
 }
 
 // Workgroups a compute unit holds: three where LDS and registers allow it.  48 heads of 64 x 64, 12,000 tokens:
-// 116 us with two, 98 with three.  64 x 128 in binary16 with three puts 18 registers into memory: 5,000 tokens
-// 85 us, 79 with two; in bfloat16, 7 registers, 73 and 75.
-__host__ __device__ constexpr int lin_resident(int dkp, int ntv, bool half) {
-    return dkp == 64 && !(half && ntv == 2) ? 3 : 2;
-}
+// 116 us with two, 98 with three.  64 x 128, 12,000 tokens: 168 and 171 in bfloat16, 177 and 185 in binary16, since
+// three put 16 registers into memory.
+__host__ __device__ constexpr int lin_resident(int dkp, int ntv) { return dkp == 64 && ntv == 1 ? 3 : 2; }
 
 // OUT: outputs and the final state; otherwise the states of the segments, for a later OUT launch.
 template <class E, int DKP, int NTV, bool OUT>
-__global__ void __launch_bounds__(256, lin_resident(DKP, NTV, __is_same(E, F16))) k_lin_chunk(LinArgs a) {
+__global__ void __launch_bounds__(256, lin_resident(DKP, NTV)) k_lin_chunk(LinArgs a) {
     constexpr int KS = DKP / 32;       // steps over dk, pairs of state row tiles
     constexpr int DVP = 64 * NTV;
     constexpr bool HALF = __is_same(E, F16);
@@ -936,7 +934,7 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     // two together.  8,000 tokens of heads of 128 x 128, 48 heads: 149 us with the 13 chunks that this
     // chooses, 161 / 177 / 160 / 176 with 8 / 10 / 15 / 18; 4 heads: 55 with 4, 59 / 67 / 86 with 6 / 8 / 12.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
-    const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128, d.Dv <= 64 ? 1 : 2, d.dtype == VQMLP_F16);
+    const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128, d.Dv <= 64 ? 1 : 2);
     const int64_t slots = held * int64_t(cus);
     auto rounds = [&](int64_t units) {
         const int64_t n = units * d.v_heads, rest = n % slots, per = (5 * rest + 4 * cus - 1) / (4 * cus);

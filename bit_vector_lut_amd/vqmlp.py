@@ -889,12 +889,9 @@ class LinearAttention:
                            self.scale)
 
     def workspace_bytes(self, T, R, max_q):
-        """Enough for either 16-bit type, whose segments may differ."""
-        n, most = C.c_size_t(), 0
-        for dtype in (0, 1):
-            _check(lib().vqmlp_linear_attn_workspace(C.byref(self._desc(dtype, T, R, 0, max_q)), C.byref(n)))
-            most = max(most, n.value)
-        return most
+        n = C.c_size_t()
+        _check(lib().vqmlp_linear_attn_workspace(C.byref(self._desc(0, T, R, 0, max_q)), C.byref(n)))
+        return n.value
 
     def _work_bytes(self, d, device):
         key = (device.index, d.T, d.R, d.max_q)
