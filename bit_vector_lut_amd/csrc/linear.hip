@@ -611,6 +611,14 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV)) k_lin_chunk(LinAr
         if (OUT && stage && !isk) take_out();  // V is read behind the next barrier
         f32x4 o[NTV][4];
         int odd = 0;
+        u32x4 vf[NTV][2];
+        auto read_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int v = 0; v < NTV; ++v)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[(vget ^ tok_bits(4 * v, 4 * c)) + 4 * v * kC * 2]);
+        };
         if constexpr (OUT) {
             u32x4 qf[4][KS], kf[KS];
 #pragma unroll
@@ -698,11 +706,14 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV)) k_lin_chunk(LinAr
             }
             __syncthreads();
             // every wave is done with this chunk's queries and keys
-            odd = uniform(int(sm.odd[vwave]));
+            const u32x4 w = *reinterpret_cast<const u32x4*>(sm.top);
+            const uint32_t found = sm.odd[vwave];
+            read_v();
+            __builtin_amdgcn_sched_barrier(0);  // all on their way before the first is waited for
+            odd = uniform(int(found));
             if constexpr (HALF) {
                 // The largest score has to lie where binary16 holds it and those 2^-15 of it with all bits: else
                 // once more, in units that put it into [2^10, 2^11).
-                const u32x4 w = *reinterpret_cast<const u32x4*>(sm.top);
                 const float mx = __builtin_bit_cast(float, uniform(int(max(max(w[0], w[1]), max(w[2], w[3])))));
                 const int to = clip(su + 10 - expo(mx));
                 if (__builtin_expect((mx >= 32768.f || (mx < 32.f && mx > 0.f)) && to != su, 0)) {
@@ -727,12 +738,7 @@ __global__ void __launch_bounds__(256, lin_resident(DKP, NTV)) k_lin_chunk(LinAr
                 }
             }
         }
-        u32x4 vf[NTV][2];
-#pragma unroll
-        for (int v = 0; v < NTV; ++v)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                vf[v][c] = *reinterpret_cast<const u32x4*>(&sm.vt[(vget ^ tok_bits(4 * v, 4 * c)) + 4 * v * kC * 2]);
+        if constexpr (!OUT) read_v();
         // sum over the tokens of e^{..} |v| of the lane's columns, times 2^15
         f32x4 sum[NTV];
         if constexpr (HALF) {
