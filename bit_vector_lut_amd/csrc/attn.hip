@@ -296,9 +296,9 @@ struct AttnGeom {
 
 // Up to 16 rows of D > 128 take register tiles: their 64 KB tiles leave the LDS kernel one workgroup a
 // compute unit, which cannot hide the cache's latency (32 requests of up to 8,000 keys, 24/4 heads of
-// 256: 123 against 184 us).  Everything else takes LDS tiles: 64 requests of one token, D = 64: 416
-// against 467 us; 8 tokens over 65,472 keys, 40/8 heads of 128: 64 against 144 us, 24/4 heads of 256:
-// 80 against 218 us.
+// 256: 121 against 153 us).  Everything else takes LDS tiles: 64 requests of one token, D = 64: 415
+// against 837 us; 8 tokens over 65,472 keys, 40/8 heads of 128: 53 against 200 us, 24/4 heads of 256:
+// 59 against 153 us.
 AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     AttnGeom G{};
     const int g = d.heads / d.kv_heads;
@@ -306,8 +306,8 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
     const int64_t rows = std::max<int64_t>(1, (all + d.R - 1) / std::max(1, d.R));
     const size_t rows_all = size_t(d.T) * d.heads;
     G.lds = d.D <= 128 || rows > 16;
-    // with loads first 8 tokens over 65,472 keys take 53 us for 40/8 heads of 128 (58 with loads between
-    // the steps), but 62 (60) for 24/4 heads of 256
+    // with loads first 8 tokens over 65,472 keys take 54 us for 40/8 heads of 128 (58 with loads between
+    // the steps), 64 ragged requests of one token 403 (420), but 24/4 heads of 256 take 63 (59)
     G.few = rows * d.D <= 64 * 128;
     const int mt = G.lds ? kAttnTileRows : 16, key_tile = G.lds ? 64 : 32;
     G.tiles = int(all / mt) + d.R + 1;
@@ -321,8 +321,8 @@ AttnGeom attn_geom(const vqmlp_attn_desc& d, int cus) {
             // Times in us.  A workgroup passes over a tile in 1 us and 0.35 more for each wave with rows
             // (D = 128), if all of them together stay below 5 TB/s of keys and values (which the row tiles
             // of a request share); two tiles' worth to start and end each; the join writes and reads FP32
-            // sums at about 4 TB/s.  512 rows of 40/8 heads of 128 over 33,001 keys: 436 us with the three
-            // splits that this chooses, 539 / 477 / 453 / 457 with 2 / 4 / 6 / 8.  max_kv is the longest of
+            // sums at about 4 TB/s.  512 rows of 40/8 heads of 128 over 33,001 keys: 425 us with the three
+            // splits that this chooses, 618 / 507 / 454 / 430 / 432 with 1 / 2 / 4 / 6 / 8.  max_kv is the longest of
             // several requests: half of the estimate is for all being as long, half for that one alone.
             const int64_t slots = int64_t(cus) * (d.D <= 128 ? 2 : 1);
             const double alone = (1.0 + 0.35 * double(std::min<int64_t>(4, (rows + 31) / 32))) * d.D / 128;

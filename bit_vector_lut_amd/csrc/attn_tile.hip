@@ -8,7 +8,7 @@
 // 128 rows a workgroup and two workgroups a compute unit (one for D > 128): 64 rows a wave would
 // halve the LDS reads, but leave one wave a SIMD and its scores in registers that the vector unit
 // cannot read (630 against 788 TFLOP/s).  512 rows over 33,001 keys, 40/8 heads of 128, FP16: 376 to
-// 396 us with the join, 866 to 912 TFLOP/s, 79 to 83% of a large library product; bound by the clock that
+// 425 us with the join on different cards, 808 to 912 TFLOP/s, 74 to 83% of a large library product; bound by the clock that
 // the power leaves (1.8 GHz of 2.4) and by exponentials beside the matrix cores, which are busy 45% of the
 // time.  64 requests of one token and up to 16,252 keys, BF16: 391 us, 5.5 TB/s, bound by the cache.
 #include "attn.h"

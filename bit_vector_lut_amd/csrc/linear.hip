@@ -40,7 +40,7 @@ struct LinArgs {
 // e^x to about two roundings: the hardware's 2^h with h = x log2 e, and what h lost as a factor 1 + r.
 __device__ __forceinline__ float exp_f32(float x) {
     const float h = x * kLog2e;
-    const float r = fmaf(x, kLog2e, -h) + x * 1.925963033500e-8f;  // log2 e - float(log2 e)
+    const float r = fmaf(x, kLog2e, -h) + x * float(1.4426950408889634 - double(kLog2e));
     return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
 }
 
@@ -194,11 +194,11 @@ __global__ void __launch_bounds__(64) k_lin_step(LinArgs a) {
 // bits and those beyond 65504 are infinite).
 //
 // Bound by the latencies of a chunk: two workgroups a compute unit (registers), each 64 x 64 scores,
-// 113 matrix-core steps and about 600 vector instructions a wave and chunk, which keep the matrix cores
-// busy 19% of the time, the vector unit 36%, LDS 25%.  Eight waves of 16 columns, four a SIMD, read twice
+// 118 matrix-core steps and about 900 vector instructions a wave and chunk, which keep the matrix cores
+// busy 18% of the time, the vector unit 36%, LDS 25%.  Eight waves of 16 columns, four a SIMD, read twice
 // as much LDS and took 193 us instead of 160.  Three prompts of 5003, 1021 and 2049 tokens, 48 value and
-// 16 key heads of 128 x 128: 50 us for the segments' states, 98 for the outputs, 226 TFLOP/s of the
-// recurrence's operations (140 us back to back).
+// 16 key heads of 128 x 128: 51 us for the segments' states, 106 for the outputs; 152 us back to back,
+// 208 TFLOP/s of the recurrence's operations.
 constexpr int kTok = kC + 8;  // LDS row stride of the scores: 144 bytes, 16-byte chunks spread over banks
 
 // K^T and V^T in LDS: rows of 64 tokens, the eight 16-byte chunks of a row permuted by an exclusive or
@@ -937,8 +937,8 @@ LinGeom lin_geom(const vqmlp_linear_desc& d, int cus) {
     // the time of the outputs' pass), of three chunks' worth of time to start and end each, and of 0.13
     // for each earlier segment whose state an output segment takes in.  The unit is a chunk in a round
     // that fills every compute unit; one workgroup alone on a unit gets through it in 3/4 of the time of
-    // two together.  8,000 tokens of heads of 128 x 128, 48 heads: 149 us with the 13 chunks that this
-    // chooses, 161 / 177 / 160 / 176 with 8 / 10 / 15 / 18; 4 heads: 55 with 4, 59 / 67 / 86 with 6 / 8 / 12.
+    // two together.  8,000 tokens of heads of 128 x 128, 48 heads: 159 us with the 13 chunks that this
+    // chooses, 172 / 188 / 173 / 187 with 8 / 10 / 15 / 18; 4 heads: 56 with 4, 61 / 69 / 89 with 6 / 8 / 12.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T)));
     const int chunks = (most + kC - 1) / kC, held = lin_resident(d.Dk <= 64 ? 64 : 128, d.Dv <= 64 ? 1 : 2);
     const int64_t slots = held * int64_t(cus);

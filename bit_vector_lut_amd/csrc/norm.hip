@@ -174,7 +174,9 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) k_norm(vqmlp_norm_desc d
 }
 
 // Any H, stride and element alignment: the row is not kept, each reduction reads it again (from
-// L2 after the first).  Every output element is written by the thread that reads it last.
+// L2 after the first).  Every output element is written by the thread that reads it last.  Bound by its
+// 2-byte loads and by making r three times: 8,192 rows of 5121, with gates, biases and an FP32 residual:
+// 519 us, 4.3 times what a large copy would take.
 template <class E, bool RES32>
 __global__ void __launch_bounds__(256) k_norm_any(vqmlp_norm_desc d) {
     __shared__ float part[2 * kMaxWaves];

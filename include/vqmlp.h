@@ -288,11 +288,13 @@ vqmlp_status vqmlp_vq2_plan_forward(const vqmlp_vq2_plan *plan, int T, const voi
 
 /* ==================================================================== around the MLP
  * The rest of a decoder layer, forward only, for a step over R requests whose new tokens are
- * packed one after another: request r owns rows cu_q[r] .. cu_q[r+1]-1 of every [T] array.
- * The mathematics stands in each section; sums, norms, softmax statistics and states are FP32,
- * and each output is rounded once.  These calls take no plan: they check their arguments, enqueue
- * on `stream` and allocate nothing; lengths, tables and indices are read on the device, so a call
- * can be captured into a graph and replayed with other lengths.  Arguments that the host can see
+ * packed one after another: request r owns rows cu_q[r] .. cu_q[r+1]-1 of every [T] array.  cu_q[0] is
+ * 0 and the entries do not fall (rows in front of a cu_q[0] above 0 are not written).  The mathematics
+ * stands in each section; sums, norms, softmax statistics and states are FP32, and each output is
+ * rounded once.  Operands of the matrix cores are rounded to dtype once: the softmax's probabilities, in
+ * linear attention's chunks the scores and, for the outputs, the state.  These calls take no plan:
+ * they check their arguments, enqueue on `stream` and allocate nothing; lengths, tables and indices are
+ * read on the device, so a call can be captured into a graph and replayed with other lengths.  Arguments that the host can see
  * are refused with VQMLP_ERR_INVALID_ARG (shape, pointer, alignment), VQMLP_ERR_UNSUPPORTED
  * (a size beyond the stated limits, or not a gfx950) or VQMLP_ERR_WORKSPACE; values read on the
  * device are bounds-checked there as each section states. */
