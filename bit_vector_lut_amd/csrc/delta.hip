@@ -1,0 +1,244 @@
+// delta.hip -- gated delta rule (gfx950).
+//
+//   S' = e^{g_t} S_{t-1},  u_t = beta_t (v_t - S'^T k_t),  S_t = S' + k_t u_t^T,  y_t = scale S_t^T q_t.
+#include "op.h"
+
+#include <algorithm>
+
+namespace vqmlp {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
+constexpr int64_t kMaxLd = 1 << 24;
+
+struct DeltaArgs {
+    const uint16_t *q, *k, *v;
+    const float *g, *beta;
+    uint16_t* y;
+    const float* sin;
+    float* sout;
+    Packed p;
+    int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_b;
+    int hk, hv, Dk, Dv;
+    float scale;
+};
+
+// e^x to about two roundings: the hardware's 2^h with h = x log2 e, and what h lost as a factor 1 + r.
+__device__ __forceinline__ float exp_f32(float x) {
+    const float h = x * kLog2e;
+    const float r = fmaf(x, kLog2e, -h) + x * float(1.4426950408889634 - double(kLog2e));
+    return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
+}
+
+// The log of a decay from kMinG on; NaN stays NaN.
+__device__ __forceinline__ float bounded(float g) { return g < kMinG ? kMinG : g; }
+
+// ---------------------------------------------------------------- the recurrence
+// A wave owns a head's Dk x 32 (or 16) columns of the state: lane = (row block, four columns), a row block's
+// rows contiguous so that a token's q and k come as 16-byte chunks.  Both sums over the rows are taken over
+// the state before the token: y_t = scale (e^{g} S^T q + (k . q) u), so one round of lane moves serves both.
+// No LDS and no barrier.
+template <class E, int RPL, int RB>  // rows per lane, row blocks: Dk <= RPL RB
+__global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
+    constexpr int CB = 64 / RB;
+    const int r = blockIdx.x, h = blockIdx.y;
+    const int lane = threadIdx.x, cb = lane % CB, rb = lane / CB;
+    const int col = (blockIdx.z * CB + cb) * 4, row0 = rb * RPL;
+    const bool cin = col < a.Dv;
+    if (r == a.p.R) {  // rows behind the last request
+        for (int64_t t = packed_row(a.p, r) + rb; t < a.p.T; t += RB)
+            if (cin) *reinterpret_cast<u32x2*>(a.y + t * a.ld_y + int64_t(h) * a.Dv + col) = u32x2{0, 0};
+        return;
+    }
+    const int c0 = packed_row(a.p, r), n = packed_row(a.p, r + 1) - c0;
+    bool old;
+    const int slot = packed_slot(a.p, r, &old);
+    const int64_t base = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv;
+    const int hk = h / (a.hv / a.hk);
+    f32x4 s[RPL];
+    constexpr int CH = RPL / 8, AHEAD = 2;
+    struct Token {
+        u32x4 k[CH], q[CH];
+        u32x2 v;
+        float g, beta;
+    } ring[AHEAD];
+    auto fetch = [&](int t, Token& x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            x.k[c] = x.q[c] = u32x4{0, 0, 0, 0};
+            if (row0 + 8 * c < a.Dk) {
+                x.k[c] = *reinterpret_cast<const u32x4*>(a.k + t * a.ld_k + int64_t(hk) * a.Dk + row0 + 8 * c);
+                x.q[c] = *reinterpret_cast<const u32x4*>(a.q + t * a.ld_q + int64_t(hk) * a.Dk + row0 + 8 * c);
+            }
+        }
+        x.v = u32x2{0, 0};
+        if (cin) x.v = *reinterpret_cast<const u32x2*>(a.v + t * a.ld_v + int64_t(h) * a.Dv + col);
+        x.g = a.g[t * a.ld_g + h];
+        x.beta = a.beta[t * a.ld_b + h];
+    };
+    // Sum over the row blocks, in all lanes.  The operands of a swap are two values to the compiler.
+    auto swapped = [](float v, auto&& swap) __attribute__((always_inline)) {
+        const int x = __builtin_bit_cast(int, v);
+        const auto z = swap(uint32_t(x), uint32_t(fresh(x)));
+        const uint32_t z0 = z[0], z1 = z[1];
+        return __builtin_bit_cast(float, z0) + __builtin_bit_cast(float, z1);
+    };
+    auto half = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
+    auto row = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
+    auto all = [&](float v) __attribute__((always_inline)) {
+        v = swapped(swapped(v, half), row);
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, false));
+        if constexpr (RB == 16)
+            v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x124, 0xF, 0xF, false));
+        return v;
+    };
+    auto token = [&](int t, const Token& x) __attribute__((always_inline)) {
+        const f32x4 v = {lo16<E>(x.v[0]), hi16<E>(x.v[0]), lo16<E>(x.v[1]), hi16<E>(x.v[1])};
+        const float e = exp_f32(bounded(x.g));
+        f32x4 sk = {0.f, 0.f, 0.f, 0.f}, sq = sk, u;
+        float kq = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float kk = j & 1 ? hi16<E>(x.k[c][j / 2]) : lo16<E>(x.k[c][j / 2]);
+                const float qq = j & 1 ? hi16<E>(x.q[c][j / 2]) : lo16<E>(x.q[c][j / 2]);
+                kq = fmaf(kk, qq, kq);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sk[i] = fmaf(kk, s[8 * c + j][i], sk[i]);
+                    sq[i] = fmaf(qq, s[8 * c + j][i], sq[i]);
+                }
+            }
+        kq = all(kq);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = x.beta * fmaf(-e, all(sk[i]), v[i]);
+            sq[i] = a.scale * fmaf(kq, u[i], e * all(sq[i]));
+        }
+        if (rb == 0 && cin)
+            *reinterpret_cast<u32x2*>(a.y + int64_t(t) * a.ld_y + int64_t(h) * a.Dv + col) =
+                u32x2{pack16<E>(sq[0], sq[1]), pack16<E>(sq[2], sq[3])};
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float kk = j & 1 ? hi16<E>(x.k[c][j / 2]) : lo16<E>(x.k[c][j / 2]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[8 * c + j][i] = fmaf(kk, u[i], s[8 * c + j][i] * e);
+            }
+    };
+    if (n > 0) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) fetch(c0 + min(j, n - 1), ring[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (old && cin && row0 + i < a.Dk)
+            s[i] = *reinterpret_cast<const f32x4*>(a.sin + base + int64_t(row0 + i) * a.Dv + col);
+    }
+    for (int i = 0; i < n; i += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (i + j >= n) break;
+            const Token x = ring[j];
+            if (i + j + AHEAD < n) fetch(c0 + i + j + AHEAD, ring[j]);
+            token(c0 + i + j, x);
+        }
+    }
+    if (slot >= 0 && cin) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+            if (row0 + i < a.Dk)
+                *reinterpret_cast<f32x4*>(a.sout + base + int64_t(row0 + i) * a.Dv + col) = s[i];
+    }
+}
+
+// ---------------------------------------------------------------- host half
+
+vqmlp_status delta_check(const vqmlp_delta_desc* p, const char* who) {
+    OP_REQUIRE(p, "%s: null description", who);
+    const vqmlp_delta_desc& d = *p;
+    OP_REQUIRE(op_dtype16(d.dtype), "%s: dtype %d is not F16 or BF16", who, d.dtype);
+    OP_REQUIRE(d.T >= 0 && d.R >= 1 && d.k_heads >= 1 && d.v_heads >= 1 && d.n_states >= 0 && d.max_q >= 0,
+               "%s: a size is out of range", who);
+    OP_REQUIRE(d.v_heads % d.k_heads == 0, "%s: v_heads=%d is no multiple of k_heads=%d", who, d.v_heads,
+               d.k_heads);
+    OP_REQUIRE(d.Dk >= 8 && d.Dk <= 128 && d.Dk % 8 == 0 && d.Dv >= 8 && d.Dv <= 128 && d.Dv % 8 == 0,
+               "%s: Dk=%d, Dv=%d are not multiples of 8 up to 128", who, d.Dk, d.Dv);
+    if (d.R > 65535 || d.v_heads > 65535 || d.T > 0x3FFFFFFF)
+        OP_FAIL(VQMLP_ERR_UNSUPPORTED, "%s: R or v_heads above 65535, or T above 2^30 - 1", who);
+    OP_REQUIRE(d.scale - d.scale == 0.f, "%s: scale is not finite", who);
+    return VQMLP_OK;
+}
+
+template <class E>
+void launch_step(const DeltaArgs& a, int cus, hipStream_t s) {
+    const dim3 grid(a.p.R + 1, a.hv, (a.Dv + 31) / 32), narrow(a.p.R + 1, a.hv, (a.Dv + 15) / 16);
+    if (a.Dk <= 64) k_delta_step<E, 8, 8><<<grid, 64, 0, s>>>(a);
+    // half the columns and rows a lane where waves of 32 columns are fewer than the chip's SIMDs
+    else if (int64_t(a.p.R) * a.hv * grid.z <= 4 * int64_t(cus)) k_delta_step<E, 8, 16><<<narrow, 64, 0, s>>>(a);
+    else k_delta_step<E, 16, 8><<<grid, 64, 0, s>>>(a);
+}
+
+}  // namespace
+
+}  // namespace vqmlp
+
+extern "C" vqmlp_status vqmlp_delta_rule_workspace(const vqmlp_delta_desc* p, size_t* bytes) {
+    using namespace vqmlp;
+    OP_REQUIRE(bytes, "vqmlp_delta_rule_workspace: null pointer");
+    int cus = 0;
+    if (const vqmlp_status st = delta_check(p, "vqmlp_delta_rule_workspace")) return st;
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    *bytes = 0;
+    return op_ok();
+}
+
+extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+    using namespace vqmlp;
+    int cus = 0;
+    if (const vqmlp_status st = delta_check(p, "vqmlp_delta_rule")) return st;
+    const vqmlp_delta_desc& d = *p;
+    OP_REQUIRE(d.cu_q && op_aligned(d.cu_q, 4) && op_aligned(d.ctx_len, 4) && op_aligned(d.state_index, 4),
+               "vqmlp_delta_rule: null cu_q or an unaligned index array");
+    OP_REQUIRE((d.state_in && d.state_out) || d.n_states == 0, "vqmlp_delta_rule: null state");
+    OP_REQUIRE(op_aligned(d.state_in, 16) && op_aligned(d.state_out, 16),
+               "vqmlp_delta_rule: states have to be 16-byte aligned");
+    if (d.T > 0) {
+        OP_REQUIRE(d.q && d.k && d.v && d.g && d.beta && d.y, "vqmlp_delta_rule: null pointer");
+        OP_REQUIRE(op_aligned(d.q, 16) && op_aligned(d.k, 16) && op_aligned(d.v, 16) && op_aligned(d.y, 16) &&
+                       op_aligned(d.g, 4) && op_aligned(d.beta, 4),
+                   "vqmlp_delta_rule: q, k, v and y have to be 16-byte aligned, g and beta 4-byte");
+        const int64_t rows[] = {int64_t(d.k_heads) * d.Dk, int64_t(d.k_heads) * d.Dk, int64_t(d.v_heads) * d.Dv,
+                                int64_t(d.v_heads) * d.Dv, d.v_heads, d.v_heads};
+        const int64_t lds[] = {d.ld_q, d.ld_k, d.ld_v, d.ld_y, d.ld_g, d.ld_beta};
+        for (int i = 0; i < 6; ++i)
+            OP_REQUIRE((d.T == 1 || lds[i] >= rows[i]) && lds[i] >= 0 && lds[i] <= kMaxLd && (i >= 4 || lds[i] % 8 == 0),
+                       "vqmlp_delta_rule: token strides have to cover the heads and be at most 2^24, those of q, k, "
+                       "v and y be multiples of 8");
+    }
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    DeltaArgs a{};
+    a.q = static_cast<const uint16_t*>(d.q);
+    a.k = static_cast<const uint16_t*>(d.k);
+    a.v = static_cast<const uint16_t*>(d.v);
+    a.g = d.g;
+    a.beta = d.beta;
+    a.y = static_cast<uint16_t*>(d.y);
+    a.sin = d.state_in;
+    a.sout = d.state_out;
+    a.p = Packed{d.cu_q, d.ctx_len, d.state_index, d.T, d.R, d.n_states};
+    a.ld_q = d.ld_q, a.ld_k = d.ld_k, a.ld_v = d.ld_v, a.ld_y = d.ld_y, a.ld_g = d.ld_g, a.ld_b = d.ld_beta;
+    a.hk = d.k_heads, a.hv = d.v_heads, a.Dk = d.Dk, a.Dv = d.Dv;
+    a.scale = d.scale;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
+    else launch_step<BF16>(a, cus, s);
+    if (trace_enabled()) trace_line("delta_rule T=%d R=%d heads=%d/%d: recurrence", d.T, d.R, d.v_heads, d.k_heads);
+    return op_launched("vqmlp_delta_rule");
+}

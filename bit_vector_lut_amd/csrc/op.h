@@ -100,6 +100,47 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
+// ---- packed requests: first rows, state slots
+
+// What the operators with a state per request share.
+struct Packed {
+    const int32_t *cu, *ctx, *index;
+    int T, R, n_states;
+};
+__device__ __forceinline__ int packed_row(const Packed& p, int r) { return min(max(p.cu[r], 0), p.T); }
+// The state slot of a request, or -1, and whether it starts from what the slot holds.
+__device__ __forceinline__ int packed_slot(const Packed& p, int r, bool* old) {
+    int s = p.index ? p.index[r] : r;
+    if (uint32_t(s) >= uint32_t(p.n_states)) s = -1;
+    *old = s >= 0 && (!p.ctx || p.ctx[r] > 0);
+    return s;
+}
+
+// Units of at most L tokens of all requests in one launch without their lengths on the host: request r
+// owns unit numbers floor(cu[r] / L) + r and on (enough for ceil(n / L), and one where n is 0); number R
+// owns the rows behind the last.  T / L + R + 1 numbers in all.
+struct PackedUnit {
+    int r, c0, n, seg, nseg, first;  // request, its first row and tokens; unit of it, units; its first's number
+};
+// For a whole wave.  The owner of number x is found 64 requests a step; numbers of nobody give false.
+__device__ __forceinline__ bool packed_unit(const Packed& p, int L, int x, PackedUnit& u) {
+    const int lane = threadIdx.x & 63;
+    int r = 0;
+    for (int step = p.R >= 4096 ? 4096 : p.R >= 64 ? 64 : 1; step; step /= 64) {
+        const int i = r + lane * step;
+        const int owned = __popcll(__ballot(i <= p.R && packed_row(p, min(i, p.R)) / L + i <= x));
+        r += max(0, owned - 1) * step;
+    }
+    u.r = r;
+    u.c0 = packed_row(p, r);
+    const int c1 = r < p.R ? packed_row(p, r + 1) : p.T;
+    u.n = max(0, c1 - u.c0);
+    u.first = u.c0 / L + r;
+    u.seg = x - u.first;
+    u.nseg = max(1, (u.n + L - 1) / L);
+    return u.seg >= 0 && u.seg < u.nseg;
+}
+
 // ---- host half
 
 inline bool op_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -72,6 +72,38 @@ class _LinearDesc(C.Structure):
                 ("state_index", C.c_void_p)]
 
 
+class _AppendDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("T", C.c_int), ("heads", C.c_int), ("kv_heads", C.c_int),
+                ("D", C.c_int), ("rot", C.c_int), ("pairs", C.c_int), ("page_size", C.c_int),
+                ("n_pages", C.c_int), ("eps", C.c_float), ("w_offset", C.c_float),
+                ("q", C.c_void_p), ("ld_q", C.c_int64), ("hs_q", C.c_int64),
+                ("k", C.c_void_p), ("ld_k", C.c_int64), ("hs_k", C.c_int64),
+                ("v", C.c_void_p), ("ld_v", C.c_int64), ("hs_v", C.c_int64),
+                ("q_out", C.c_void_p), ("ld_q_out", C.c_int64), ("q_w", C.c_void_p),
+                ("k_w", C.c_void_p), ("inv_freq", C.c_void_p), ("position", C.c_void_p),
+                ("slot", C.c_void_p), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p)]
+
+
+class _ConvDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("T", C.c_int), ("R", C.c_int), ("C", C.c_int), ("W", C.c_int),
+                ("silu", C.c_int), ("unit_heads", C.c_int), ("unit_dim", C.c_int),
+                ("n_states", C.c_int), ("eps", C.c_float), ("ld_x", C.c_int64), ("ld_y", C.c_int64),
+                ("x", C.c_void_p), ("weight", C.c_void_p), ("bias", C.c_void_p), ("y", C.c_void_p),
+                ("state_in", C.c_void_p), ("state_out", C.c_void_p), ("cu_q", C.c_void_p),
+                ("ctx_len", C.c_void_p), ("state_index", C.c_void_p)]
+
+
+class _DeltaDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("T", C.c_int), ("R", C.c_int), ("k_heads", C.c_int),
+                ("v_heads", C.c_int), ("Dk", C.c_int), ("Dv", C.c_int), ("n_states", C.c_int),
+                ("max_q", C.c_int), ("scale", C.c_float), ("ld_q", C.c_int64),
+                ("ld_k", C.c_int64), ("ld_v", C.c_int64), ("ld_y", C.c_int64),
+                ("ld_g", C.c_int64), ("ld_beta", C.c_int64), ("q", C.c_void_p), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("g", C.c_void_p), ("beta", C.c_void_p), ("y", C.c_void_p),
+                ("state_in", C.c_void_p), ("state_out", C.c_void_p), ("cu_q", C.c_void_p),
+                ("ctx_len", C.c_void_p), ("state_index", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -122,6 +154,10 @@ def lib():
             "vqmlp_paged_attn": [P, P, S, P],
             "vqmlp_linear_attn_workspace": [P, C.POINTER(S)],
             "vqmlp_linear_attn": [P, P, S, P],
+            "vqmlp_paged_append": [P, P],
+            "vqmlp_short_conv": [P, P],
+            "vqmlp_delta_rule_workspace": [P, C.POINTER(S)],
+            "vqmlp_delta_rule": [P, P, S, P],
         }
         for name, args in sigs.items():
             f = getattr(L, name)
@@ -580,6 +616,29 @@ def _rows(t, name, device, shape):
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
 
 
+def _heads(t, name, device, shape):
+    """Pointer, token stride and head stride of [T, heads, D] whose heads are dense."""
+    if t.device != device or t.shape != shape:
+        _need(t, name, device, None, shape, contiguous=False)
+    ld, hs, at = t.stride()
+    if at != 1 and shape[2] > 1:
+        _bad("%s: a head's elements do not lie one after another" % name)
+    return t.data_ptr(), ld if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+
+
+def _copy_of(state, on):
+    """A new tensor of state's values, made on the call's stream."""
+    import torch
+
+    out = on.like(state)
+    if on.stream is None:
+        out.copy_(state)
+    else:
+        with torch.cuda.stream(on.stream):
+            out.copy_(state)
+    return out
+
+
 def _work(on, workspace, nbytes):
     """Pointer and size of a call's workspace: the caller's, or a new one on the call's stream (held
     by the third value until the call has been enqueued)."""
@@ -804,6 +863,52 @@ class PagedCache:
                                     self._page_size, self._n_pages, kp, ld_k, vp, ld_v, sp, self._kp,
                                     self._vp)
 
+    def append(self, q, k, v, position, slot, rotary, *, q_out=None, stream=None):
+        """store() with the heads of q and k normed and turned on the way, by `rotary` (a Rotary): q [T,
+        heads, D] (None: no queries), k, v [T, kv_heads, D], heads dense, any token and head stride that is
+        a multiple of 8; position, slot int32 [T].  A token at a position below 0 is skipped.  q_out may be
+        q.  Returns q_out (None without q)."""
+        import torch
+
+        T, dev, i = k.shape[0], self._device, torch.int32
+        _fits(T, "append")
+        if rotary.device != dev or rotary.dtype not in (None, self._dtype) or 2 * rotary.half > self._D:
+            _bad("rotary does not fit the cache (device, type or D)")
+        if _dtype(k, "k") != self._dtype or _dtype(v, "v") != self._dtype:
+            _bad("k, v and the cache differ in type")
+        d = _AppendDesc.from_buffer_copy(rotary._desc)
+        if rotary.D not in (None, self._D):
+            _bad("the norms' weights have %d elements for heads of %d" % (rotary.D, self._D))
+        d.dtype, d.T, d.kv_heads, d.D = self._dtype, T, self._kv_heads, self._D
+        d.page_size, d.n_pages, d.k_cache, d.v_cache = self._page_size, self._n_pages, self._kp, self._vp
+        shape = (T, self._kv_heads, self._D)
+        d.k, d.ld_k, d.hs_k = _heads(k, "k", dev, shape)
+        d.v, d.ld_v, d.hs_v = _heads(v, "v", dev, shape)
+        d.position = _need(position, "position", dev, i, (None,))
+        d.slot = _need(slot, "slot", dev, i, (None,))
+        if position.shape[0] < T or slot.shape[0] < T:
+            _bad("position has %d entries, slot %d for %d tokens" % (position.shape[0], slot.shape[0], T))
+        if q is None and q_out is not None:
+            _bad("q_out without q")
+        on = _OnStream(stream, dev)
+        if q is not None:
+            if q.dim() != 3 or _dtype(q, "q") != self._dtype:
+                _bad("q is [T, heads, D] of the cache's type")
+            heads = q.shape[1]
+            _fits(heads, "append")
+            shape = (T, heads, self._D)
+            d.heads = heads
+            d.q, d.ld_q, d.hs_q = _heads(q, "q", dev, shape)
+            if q_out is None:
+                q_out = on.like(q)
+                d.q_out, d.ld_q_out = q_out.data_ptr(), heads * self._D
+            else:
+                if _dtype(q_out, "q_out") != self._dtype:
+                    _bad("q_out and the cache differ in type")
+                d.q_out, d.ld_q_out = _rows(q_out, "q_out", dev, shape)
+        on.call(lib().vqmlp_paged_append, C.byref(d))
+        return q_out
+
     def _attn_desc(self, T, R, heads, table_width, window, max_kv, scale):
         if max_kv is None:
             max_kv = table_width * self._page_size
@@ -866,6 +971,101 @@ class PagedCache:
         work, nbytes, _hold = _work(on, workspace, self._work_bytes(d))
         on.call(lib().vqmlp_paged_attn, C.byref(d), work, nbytes)
         return y if lse is None else (y, lse)
+
+
+class Rotary:
+    """How PagedCache.append norms and turns the heads of q and k: inv_freq float32 [rot / 2] on the device
+    (pair p turns by position * inv_freq[p]; None: no rotation), pairs (p, p + rot / 2) or, interleaved,
+    (2p, 2p + 1); q_weight, k_weight [D]: RMS norms of each head in front (None: not)."""
+
+    device, dtype, half, D = _fixed("device"), _fixed("dtype"), _fixed("half"), _fixed("D")
+
+    def __init__(self, inv_freq=None, *, interleaved=False, q_weight=None, k_weight=None, eps=1e-6,
+                 weight_offset=0.0):
+        import torch
+
+        given = [t for t in (inv_freq, q_weight, k_weight) if t is not None]
+        if not given:
+            _bad("neither inv_freq nor a norm's weight")
+        self._device = given[0].device
+        self._half = 0 if inv_freq is None else inv_freq.shape[0]
+        self._desc = _AppendDesc(rot=2 * self._half, pairs=int(bool(interleaved)), eps=eps, w_offset=weight_offset)
+        self._keep = given
+        if inv_freq is not None:
+            self._desc.inv_freq = _need(inv_freq, "inv_freq", self._device, torch.float32, (None,))
+        ws = [w for w in (q_weight, k_weight) if w is not None]
+        self._dtype = self._D = None
+        if ws:
+            self._dtype, self._D = _dtype(ws[0], "weight"), ws[0].shape[0]
+            for name, w in (("q_w", q_weight), ("k_w", k_weight)):
+                if w is not None:
+                    setattr(self._desc, name, _need(w, name, self._device, ws[0].dtype, (self._D,)))
+
+
+class ShortConv:
+    """y = silu(bias + sum_w weight[:, w] x[t - W + 1 + w]) over each request's tokens, channel by channel;
+    the first unit_heads heads of unit_dim channels are brought to length one.  weight [C, W], bias [C] or
+    None; activation "silu" or None."""
+
+    def __init__(self, weight, bias=None, *, activation="silu", unit_heads=0, unit_dim=0, eps=1e-6):
+        if activation not in ("silu", None):
+            _bad("unknown activation %r" % (activation,))
+        _need(weight, "weight", weight.device, None, (None, None))
+        self._keep = weight, bias
+        self.C, self.W = weight.shape
+        _fits(self.C | self.W | unit_heads | unit_dim, "short convolution")
+        self._desc = _ConvDesc(dtype=_dtype(weight, "weight"), C=self.C, W=self.W, silu=int(activation == "silu"),
+                               unit_heads=unit_heads, unit_dim=unit_dim, eps=eps, weight=weight.data_ptr())
+        if bias is not None:
+            self._desc.bias = _need(bias, "bias", weight.device, weight.dtype, (self.C,))
+
+    def state(self, n):
+        """Zero states for n requests."""
+        import torch
+
+        w = self._keep[0]
+        return torch.zeros((n, self.W - 1, self.C), dtype=w.dtype, device=w.device)
+
+    def forward(self, x, state, cu_q, *, ctx_len=None, state_index=None, state_out=None, y=None, stream=None):
+        """x [T, C], state [slots, W - 1, C] of the weight's type (rows in front of a request's first, oldest
+        first), cu_q int32 [R + 1]; ctx_len, state_index, state_out as LinearAttention.forward.  Returns
+        (y [T, C], state_out)."""
+        import torch
+
+        dev, i, w = x.device, torch.int32, self._keep[0]
+        if x.dim() != 2 or w.device != dev:
+            _bad("x is [T, C] on the weight's device")
+        T, R = x.shape[0], cu_q.shape[0] - 1
+        _fits(T | R | state.shape[0], "short convolution")
+        d = _ConvDesc.from_buffer_copy(self._desc)
+        if _dtype(x, "x") != d.dtype or _dtype(state, "state") != d.dtype:
+            _bad("x, state and weight differ in type")
+        d.T, d.R, d.n_states = T, R, state.shape[0]
+        d.x, d.ld_x = _rows(x, "x", dev, (T, self.C))
+        on = _OnStream(stream, dev)
+        if y is None:
+            y = on.like(x)
+            d.y, d.ld_y = y.data_ptr(), self.C
+        else:
+            if _dtype(y, "y") != d.dtype:
+                _bad("y and x differ in type")
+            d.y, d.ld_y = _rows(y, "y", dev, (T, self.C))
+        shape = (state.shape[0], self.W - 1, self.C)
+        d.state_in = _need(state, "state", dev, None, shape)
+        if state_out is None:
+            state_out = _copy_of(state, on) if state_index is not None or shape[0] > R else on.like(state)
+            d.state_out = state_out.data_ptr()
+        else:
+            if _dtype(state_out, "state_out") != d.dtype:
+                _bad("state_out and x differ in type")
+            d.state_out = _need(state_out, "state_out", dev, None, shape)
+        d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
+        if ctx_len is not None:
+            d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (R,))
+        if state_index is not None:
+            d.state_index = _need(state_index, "state_index", dev, i, (R,))
+        on.call(lib().vqmlp_short_conv, C.byref(d))
+        return y, state_out
 
 
 class LinearAttention:
@@ -956,4 +1156,93 @@ class LinearAttention:
             d.state_index = _need(state_index, "state_index", dev, i, (R,))
         work, nbytes, _hold = _work(on, workspace, self._work_bytes(d, dev))
         on.call(lib().vqmlp_linear_attn, C.byref(d), work, nbytes)
+        return y, state_out
+
+
+class DeltaRule:
+    """S' = exp(g_t) S_{t-1}, u_t = beta_t (v_t - S'^T k_t), S_t = S' + k_t u_t^T, y_t = scale * S_t^T q_t per
+    value head (which shares key head h // (v_heads // k_heads)).  scale: 1 / sqrt(Dk) if None."""
+
+    k_heads, v_heads, Dk, Dv = _fixed("k_heads"), _fixed("v_heads"), _fixed("Dk"), _fixed("Dv")
+    scale = _fixed("scale")
+
+    def __init__(self, k_heads, v_heads, Dk, Dv, scale=None):
+        _fits(k_heads | v_heads | Dk | Dv, "delta rule")
+        self._k_heads, self._v_heads, self._Dk, self._Dv = k_heads, v_heads, Dk, Dv
+        self._scale = Dk ** -0.5 if scale is None else scale
+        self._work = {}  # workspace bytes of (device, type, T, R, max_q)
+
+    def state(self, n, device="cuda"):
+        """Zero states for n requests."""
+        import torch
+
+        return torch.zeros((n, self._v_heads, self._Dk, self._Dv), dtype=torch.float32, device=device)
+
+    def _desc(self, dtype, T, R, n_states, max_q):
+        _fits(T | R | n_states | max_q, "delta rule")
+        return _DeltaDesc(dtype, T, R, self._k_heads, self._v_heads, self._Dk, self._Dv, n_states, max_q,
+                          self._scale)
+
+    def workspace_bytes(self, T, R, max_q):
+        """Bytes that hold for calls of either type on the current device."""
+        n = [C.c_size_t(), C.c_size_t()]
+        for dtype in (0, 1):
+            _check(lib().vqmlp_delta_rule_workspace(C.byref(self._desc(dtype, T, R, 0, max_q)), C.byref(n[dtype])))
+        return max(n[0].value, n[1].value)
+
+    def _work_bytes(self, d, device):
+        key = (device.index, d.dtype, d.T, d.R, d.max_q)
+        n = self._work.get(key)
+        if n is None:
+            import torch
+
+            n = C.c_size_t()
+            with torch.cuda.device(device):
+                _check(lib().vqmlp_delta_rule_workspace(C.byref(d), C.byref(n)))
+            if len(self._work) >= 4096:
+                self._work.clear()
+            n = self._work[key] = n.value
+        return n
+
+    def forward(self, q, k, v, g, beta, state, cu_q, *, ctx_len=None, state_index=None, state_out=None,
+                max_q=None, y=None, workspace=None, stream=None):
+        """q, k [T, k_heads, Dk], v [T, v_heads, Dv], g and beta float32 [T, v_heads], state float32 [slots,
+        v_heads, Dk, Dv]; the other arguments and the result as LinearAttention.forward."""
+        import torch
+
+        dev, i, f = q.device, torch.int32, torch.float32
+        T, R = q.shape[0], cu_q.shape[0] - 1
+        dt = _dtype(q, "q")
+        if _dtype(k, "k") != dt or _dtype(v, "v") != dt:
+            _bad("q, k and v differ in type")
+        if g.dtype != f or beta.dtype != f:
+            _bad("g is %s and beta %s, not %s" % (g.dtype, beta.dtype, f))
+        on = _OnStream(stream, dev)
+        d = self._desc(dt, T, R, state.shape[0], T if max_q is None else max_q)
+        d.q, d.ld_q = _rows(q, "q", dev, (T, self._k_heads, self._Dk))
+        d.k, d.ld_k = _rows(k, "k", dev, (T, self._k_heads, self._Dk))
+        d.v, d.ld_v = _rows(v, "v", dev, (T, self._v_heads, self._Dv))
+        d.g, d.ld_g = _rows(g, "g", dev, (T, self._v_heads))
+        d.beta, d.ld_beta = _rows(beta, "beta", dev, (T, self._v_heads))
+        if y is None:
+            y = on.like(v) if v.dtype == q.dtype else on.empty(v.shape, q.dtype)
+            d.y, d.ld_y = y.data_ptr(), self._v_heads * self._Dv
+        else:
+            if _dtype(y, "y") != dt:
+                _bad("y and q differ in type")
+            d.y, d.ld_y = _rows(y, "y", dev, (T, self._v_heads, self._Dv))
+        shape = (state.shape[0], self._v_heads, self._Dk, self._Dv)
+        d.state_in = _need(state, "state", dev, f, shape)
+        if state_out is None:
+            state_out = _copy_of(state, on) if state_index is not None or shape[0] > R else on.like(state)
+            d.state_out = state_out.data_ptr()
+        else:
+            d.state_out = _need(state_out, "state_out", dev, f, shape)
+        d.cu_q = _need(cu_q, "cu_q", dev, i, (R + 1,))
+        if ctx_len is not None:
+            d.ctx_len = _need(ctx_len, "ctx_len", dev, i, (R,))
+        if state_index is not None:
+            d.state_index = _need(state_index, "state_index", dev, i, (R,))
+        work, nbytes, _hold = _work(on, workspace, self._work_bytes(d, dev))
+        on.call(lib().vqmlp_delta_rule, C.byref(d), work, nbytes)
         return y, state_out

@@ -397,6 +397,62 @@ vqmlp_status vqmlp_paged_attn_workspace(const vqmlp_attn_desc *desc, size_t *byt
 vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size_t workspace_bytes,
                               void *stream);
 
+/* ------------------------------------------------------------------ append with norm and rotation
+ * The new tokens' queries, keys and values on their way to the attention: each head of q and k is
+ * normed (q_w, k_w [D]; NULL: not) and turned by its token's position, keys and values go to the
+ * paged cache above at slot[t], queries to q_out:
+ *   z = x / sqrt(mean(x^2) + eps) * (w + w_offset)
+ *   (z_a, z_b) -> (z_a cos f - z_b sin f, z_b cos f + z_a sin f),  f = position[t] * inv_freq[p]
+ * for the pairs p < rot / 2: VQMLP_PAIRS_HALF turns elements (p, p + rot / 2), VQMLP_PAIRS_NEXT (2p, 2p + 1);
+ * elements from rot on are not turned.  rot is a multiple of 8 up to D (0: no rotation, inv_freq may be
+ * NULL).  Angles are reduced in FP64, so that far positions keep their low digits; norm and rotation are
+ * FP32, each output is rounded once; values are copied.
+ * q [T][heads][D], k and v [T][kv_heads][D] with token strides ld_* and head strides hs_* (elements,
+ * multiples of 8, from 0 up to 2^40 and 2^24; 16-byte aligned); q_out [T][heads][D] with token stride
+ * ld_q_out of at least heads * D; it may be q (the same strides), no other overlap.  heads 0: no queries
+ * (q and q_out may be NULL); else any number: it need not be a multiple of kv_heads here.  heads, kv_heads
+ * up to 65535.  A token with position[t] < 0 is skipped: its row of q_out stays as it is and nothing is
+ * stored.  A slot outside [0, n_pages * page_size) is not stored to, its query is made.  Two tokens may
+ * not share a slot.  T < 2^30. */
+typedef enum { VQMLP_PAIRS_HALF = 0, VQMLP_PAIRS_NEXT = 1 } vqmlp_pairs;
+typedef struct {
+    int dtype, T, heads, kv_heads, D, rot, pairs, page_size, n_pages;
+    float eps, w_offset;
+    const void *q; int64_t ld_q, hs_q;
+    const void *k; int64_t ld_k, hs_k;
+    const void *v; int64_t ld_v, hs_v;
+    void *q_out;   int64_t ld_q_out;
+    const void *q_w, *k_w;
+    const float *inv_freq;              /* [rot / 2] */
+    const int32_t *position, *slot;     /* [T] */
+    void *k_cache, *v_cache;
+} vqmlp_append_desc;
+vqmlp_status vqmlp_paged_append(const vqmlp_append_desc *desc, void *stream);
+
+/* ------------------------------------------------------------------ short convolution
+ * Causal, over the tokens of each request, a filter for each channel, W = 2..4 taps:
+ *   z[t][c] = bias[c] + sum_w weight[c][w] x[t - W + 1 + w][c],  y = z or (silu != 0) z / (1 + e^-z)
+ * Rows in front of a request's first are the last rows of its state, state_in [slots][W-1][C], oldest
+ * first; state_out receives the last W - 1 rows of x (with the state's rows where the request has fewer
+ * tokens), bit for bit.  The first unit_heads heads of unit_dim channels are brought to length one:
+ *   y -> y / sqrt(sum over the head of y^2 + eps)
+ * x, y [T][C] (F16 or BF16, token strides ld_*: multiples of 8 up to 2^24, 16-byte aligned), weight
+ * [C][W], bias [C] or NULL and the states of the same type, 16-byte aligned.  C is a multiple of 8 up to
+ * 2^20, unit_dim one up to 256, unit_heads * unit_dim at most C.  x and y do not overlap.
+ * state_index, ctx_len, cu_q, slots and rows behind the last request as in the linear attention below;
+ * state_in and state_out may be the same array.  R <= 65535, T < 2^30. */
+typedef struct {
+    int dtype, T, R, C, W, silu, unit_heads, unit_dim, n_states;
+    float eps;
+    int64_t ld_x, ld_y;
+    const void *x, *weight, *bias;
+    void *y;
+    const void *state_in;
+    void *state_out;
+    const int32_t *cu_q, *ctx_len, *state_index;
+} vqmlp_conv_desc;
+vqmlp_status vqmlp_short_conv(const vqmlp_conv_desc *desc, void *stream);
+
 /* ------------------------------------------------------------------ linear attention with decay
  * Per request and value head h (key head h / (v_heads / k_heads)), from the state S [Dk][Dv]:
  *   S_t = exp(g[t][h]) S_{t-1} + k_t v_t^T,   y_t = scale * S_t^T q_t.
@@ -429,6 +485,30 @@ typedef struct {
 vqmlp_status vqmlp_linear_attn_workspace(const vqmlp_linear_desc *desc, size_t *bytes);
 vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ gated delta rule
+ * Per request and value head h (key head h / (v_heads / k_heads)), from the state S [Dk][Dv]:
+ *   S' = exp(g[t][h]) S_{t-1},  u_t = beta[t][h] (v_t - S'^T k_t),
+ *   S_t = S' + k_t u_t^T,       y_t = scale * S_t^T q_t.
+ * beta FP32 [T][v_heads] (token stride ld_beta).  Everything else as in the linear attention above: the arrays, their
+ * strides and types, g and its bounds, states, slots, ctx_len, cu_q, rows behind the last request, max_q,
+ * the workspace's rules and the limits.  Keys are meant to have length one and beta to lie in [0, 2];
+ * beyond, the recurrence itself may grow without bound.  What is not finite in k, g or beta makes the outputs
+ * of its head from its token on and the state NaN, in v those of its column, in q its own outputs. */
+typedef struct {
+    int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
+    float scale;
+    int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_beta;
+    const void *q, *k, *v;
+    const float *g, *beta;
+    void *y;
+    const float *state_in;
+    float *state_out;
+    const int32_t *cu_q, *ctx_len, *state_index;
+} vqmlp_delta_desc;
+vqmlp_status vqmlp_delta_rule_workspace(const vqmlp_delta_desc *desc, size_t *bytes);
+vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc *desc, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 #ifdef __cplusplus
 }
