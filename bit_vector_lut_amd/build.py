@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvqmlp.so")
 SOURCES = ["vqmlp_host.cpp", "kernels.hip", "fused.hip", "tiled.hip", "vq3mm.hip", "lut8.hip",
            "vq2.hip", "noalloc.hip", "norm.hip", "pages.hip", "attn.hip", "attn_tile.hip", "linear.hip",
-           "delta.hip", "conv.hip", "rotary.hip"]
+           "delta.hip", "delta_chunk.hip", "conv.hip", "rotary.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 VALU forms are kept out of the generated code: hipcc -O3 would otherwise form

@@ -1,0 +1,29 @@
+// delta.h -- shared by the gated delta rule's kernels (delta.hip, delta_chunk.hip).
+#pragma once
+#include "op.h"
+
+namespace vqmlp {
+
+constexpr int kDeltaC = 64;  // tokens of a chunk
+constexpr int kDeltaBlock = 20480;  // bytes of a chunk and value head in the workspace
+
+struct DeltaArgs {
+    const uint16_t *q, *k, *v;
+    const float *g, *beta;
+    uint16_t* y;
+    const float* sin;
+    float* sout;
+    Packed p;
+    uint8_t* blocks;   // [unit][v_heads][kDeltaBlock]
+    uint16_t* images;  // [unit][k_heads][k, q][64][Dk padded] in binary16 (of bfloat16 inputs only)
+    int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_b;
+    int64_t id0;       // number of the launch's first workgroup
+    int hk, hv, Dk, Dv;
+    float scale;
+};
+
+// Chunks of 64 tokens on the matrix cores; units = T / 64 + R + 1.
+template <class E>
+void launch_delta_chunks(const DeltaArgs& a, hipStream_t s);
+
+}  // namespace vqmlp

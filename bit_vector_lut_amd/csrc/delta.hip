@@ -1,7 +1,7 @@
 // delta.hip -- gated delta rule (gfx950).
 //
 //   S' = e^{g_t} S_{t-1},  u_t = beta_t (v_t - S'^T k_t),  S_t = S' + k_t u_t^T,  y_t = scale S_t^T q_t.
-#include "op.h"
+#include "delta.h"
 
 #include <algorithm>
 
@@ -9,31 +9,8 @@ namespace vqmlp {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
 constexpr int64_t kMaxLd = 1 << 24;
-
-struct DeltaArgs {
-    const uint16_t *q, *k, *v;
-    const float *g, *beta;
-    uint16_t* y;
-    const float* sin;
-    float* sout;
-    Packed p;
-    int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_b;
-    int hk, hv, Dk, Dv;
-    float scale;
-};
-
-// e^x to about two roundings: the hardware's 2^h with h = x log2 e, and what h lost as a factor 1 + r.
-__device__ __forceinline__ float exp_f32(float x) {
-    const float h = x * kLog2e;
-    const float r = fmaf(x, kLog2e, -h) + x * float(1.4426950408889634 - double(kLog2e));
-    return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
-}
-
-// The log of a decay from kMinG on; NaN stays NaN.
-__device__ __forceinline__ float bounded(float g) { return g < kMinG ? kMinG : g; }
+constexpr int kStepMaxQ = 16;  // up to here token by token
 
 // ---------------------------------------------------------------- the recurrence
 // A wave owns a head's Dk x 32 (or 16) columns of the state: lane = (row block, four columns), a row block's
@@ -159,6 +136,21 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
 
 // ---------------------------------------------------------------- host half
 
+struct DeltaGeom {
+    bool step;
+    size_t images, bytes;  // where they start; in all
+};
+
+DeltaGeom delta_geom(const vqmlp_delta_desc& d) {
+    DeltaGeom G{};
+    G.step = d.max_q <= kStepMaxQ;
+    if (G.step) return G;
+    const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
+    G.bytes = G.images = units * d.v_heads * kDeltaBlock;
+    if (d.dtype == VQMLP_BF16) G.bytes += units * d.k_heads * (2 * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
+    return G;
+}
+
 vqmlp_status delta_check(const vqmlp_delta_desc* p, const char* who) {
     OP_REQUIRE(p, "%s: null description", who);
     const vqmlp_delta_desc& d = *p;
@@ -191,10 +183,8 @@ void launch_step(const DeltaArgs& a, int cus, hipStream_t s) {
 extern "C" vqmlp_status vqmlp_delta_rule_workspace(const vqmlp_delta_desc* p, size_t* bytes) {
     using namespace vqmlp;
     OP_REQUIRE(bytes, "vqmlp_delta_rule_workspace: null pointer");
-    int cus = 0;
     if (const vqmlp_status st = delta_check(p, "vqmlp_delta_rule_workspace")) return st;
-    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
-    *bytes = 0;
+    *bytes = delta_geom(*p).bytes;
     return op_ok();
 }
 
@@ -223,6 +213,13 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
                        "v and y be multiples of 8");
     }
     if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    const DeltaGeom G = delta_geom(d);
+    if (G.bytes) {
+        OP_REQUIRE(workspace && op_aligned(workspace, 256), "vqmlp_delta_rule: the workspace is null or not 256-byte aligned");
+        if (workspace_bytes < G.bytes)
+            OP_FAIL(VQMLP_ERR_WORKSPACE, "vqmlp_delta_rule: workspace holds %zu bytes, this call needs %zu", workspace_bytes,
+                    G.bytes);
+    }
     DeltaArgs a{};
     a.q = static_cast<const uint16_t*>(d.q);
     a.k = static_cast<const uint16_t*>(d.k);
@@ -236,9 +233,17 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
     a.ld_q = d.ld_q, a.ld_k = d.ld_k, a.ld_v = d.ld_v, a.ld_y = d.ld_y, a.ld_g = d.ld_g, a.ld_b = d.ld_beta;
     a.hk = d.k_heads, a.hv = d.v_heads, a.Dk = d.Dk, a.Dv = d.Dv;
     a.scale = d.scale;
+    a.blocks = static_cast<uint8_t*>(workspace);
+    a.images = reinterpret_cast<uint16_t*>(a.blocks + G.images);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
-    else launch_step<BF16>(a, cus, s);
-    if (trace_enabled()) trace_line("delta_rule T=%d R=%d heads=%d/%d: recurrence", d.T, d.R, d.v_heads, d.k_heads);
+    if (G.step) {
+        if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
+        else launch_step<BF16>(a, cus, s);
+    } else {
+        if (d.dtype == VQMLP_F16) launch_delta_chunks<F16>(a, s);
+        else launch_delta_chunks<BF16>(a, s);
+    }
+    if (trace_enabled())
+        trace_line("delta_rule T=%d R=%d heads=%d/%d: %s", d.T, d.R, d.v_heads, d.k_heads, G.step ? "recurrence" : "chunks");
     return op_launched("vqmlp_delta_rule");
 }

@@ -1,0 +1,684 @@
+// delta_chunk.hip -- gated delta rule over chunks of 64 tokens on the matrix cores (gfx950).
+//
+// With b_t = g_1 + .. + g_t inside a chunk and S the state before it,
+//   A_tj = beta_t e^{b_t - b_j} k_t . k_j  (j < t),   T = (I + A)^-1 diag(beta)
+//   U  = T (V - diag(e^b) K S)
+//   y  = scale (diag(e^b) Q S + P U),  P_tj = e^{b_t - b_j} q_t . k_j  (j <= t)
+//   S' = e^{b_64} S + K^T diag(e^{b_64 - b}) U.
+// T and P do not depend on the state: k_delta_prep makes them for all chunks at once.  k_delta_scan goes
+// through a request's chunks in order.  There a wave owns 16 value columns of the state and all that
+// follows from them, so that the chain S -> K S -> U -> S' stays in its registers: each product's result
+// lies, per lane, as eight neighbouring rows of one column, which is the next product's operand.
+//
+// Precision.  What reaches the state keeps FP32 accuracy: matrix-core operands made here (S, V - K S, T, U)
+// are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
+// element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
+// binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  For
+// the outputs, which have 16 bits, P, U and S are one binary16 part.  The triangular system is
+// solved in FP32.
+#include "delta.h"
+
+#include <algorithm>
+
+namespace vqmlp {
+
+namespace {
+
+constexpr int kC = kDeltaC;
+
+// A block of the workspace: parts of T and P as the lanes of the matrix cores take them (1 KB each), then
+// factors for each token.
+struct DeltaBlock {
+    u32x4 th[6][64], tl[6][64], p[6][64];
+    float xf[kC];  // e^b 2^kexp: of K S
+    float uf[kC];  // the unit of T's row
+    float tf[kC];  // e^(b_64 - b) 2^kexp: of U where it joins the state
+    float qf[kC];  // e^b 2^qexp in units of P's row: of Q S
+    float pf[kC];  // scale times the unit of P's row
+    float etot;    // e^b_64
+    int bad;       // first token with something not finite in k, g or beta, or 64
+    float pad[190];
+};
+static_assert(sizeof(DeltaBlock) == kDeltaBlock, "block");
+
+__device__ uint32_t kZeros[4] = {0, 0, 0, 0};  // where rows and columns that do not exist are read
+
+// Rows of K in LDS: 16-byte chunks, their order within a row changed by an exclusive or so that both ways
+// of reading an operand (16 rows 8 (m / 4) + m % 4 of one chunk; four neighbouring rows of four chunks,
+// transposed) touch all banks evenly.
+template <int DKP>
+__device__ __forceinline__ int kkey(int r) {
+    return DKP == 64 ? (r & 2) << 1 | (r >> 3 & 1) | (r >> 3 & 2) : (r & 3) << 2 | (r >> 3 & 3);
+}
+template <int DKP>
+__device__ __forceinline__ int qkey(int r) { return DKP == 64 ? (r >> 1) & 7 : r & 15; }
+__device__ __forceinline__ int vkey(int r) { return (r & 3) << 1; }
+// Row m of tile b of a pair of row tiles: a lane's four results of both are eight neighbours.
+__device__ __forceinline__ int pair_row(int m, int b) { return 8 * (m >> 2) + 4 * b + (m & 3); }
+
+// e^x of a log in base 2
+__device__ __forceinline__ float exp_b(double b) {
+    const float h = float(b), r = float(b - double(h));
+    return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
+}
+
+// Parts of eight values: hi + lo, the latter of what rounding left.
+__device__ __forceinline__ u32x4 pack_hi(const float* x) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t z = pack16<F16>(x[2 * i], x[2 * i + 1]);
+        // one rounded value for the operand and for what is left of x
+        asm("" : "+v"(z));
+        w[i] = z;
+    }
+    return w;
+}
+__device__ __forceinline__ u32x4 pack_lo(const float* x, u32x4 hi) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = pack16<F16>(fmaf(lo16<F16>(hi[i]), -1.f, x[2 * i]), fmaf(hi16<F16>(hi[i]), -1.f, x[2 * i + 1]));
+    return w;
+}
+
+// Largest bits of eight 16-bit magnitudes
+__device__ __forceinline__ uint32_t top8(u32x4 x) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = max(t, max(x[i] & 0x7FFFu, x[i] >> 16 & 0x7FFFu));
+    return t;
+}
+template <class E>
+constexpr uint32_t kInf16 = __is_same(E, F16) ? 0x7C00u : 0x7F80u;
+
+// bfloat16 to binary16 in units of 2^e
+__device__ __forceinline__ u32x4 to_half(u32x4 x, float by) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = lo16<BF16>(x[i]) * by, f[2 * i + 1] = hi16<BF16>(x[i]) * by;
+    return pack_hi(f);
+}
+__device__ __forceinline__ int bf_expo(uint32_t top) {
+    return top >= 0x80u && top < 0x7F80u ? int(top >> 7) - 127 : 0;
+}
+
+template <int DKP>
+struct PrepSmem {
+    __attribute__((aligned(256))) uint16_t k[kC * DKP];
+    float A[kC][kC + 4], T[kC][kC + 4];
+    double b[kC];
+    float beta[kC];
+    int kexp[kC];
+    int bad;
+};
+
+template <class E, int DKP>
+__global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
+    constexpr int KS = DKP / 32;
+    constexpr bool HALF = __is_same(E, F16);
+    __shared__ PrepSmem<DKP> sm;
+    const int heads = a.hv / a.hk;
+    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * heads) * 8 + id % 8;
+    const int hk = int(pair % a.hk), h = hk * heads + int(id / 8 % heads);
+    const int x = int(pair / a.hk);
+    PackedUnit u;
+    if (!packed_unit(a.p, kC, x, u)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int lr = lane & 15, g4 = lane >> 4;
+    const int64_t t0 = u.c0 + int64_t(u.seg) * kC;
+    const int m = min(kC, u.n - u.seg * kC);
+    if (u.r == a.p.R) {  // rows behind the last request
+        for (int i = tid; i < m * (a.Dv / 8); i += 256)
+            *reinterpret_cast<u32x4*>(a.y + (t0 + i / (a.Dv / 8)) * a.ld_y + int64_t(h) * a.Dv + i % (a.Dv / 8) * 8) =
+                u32x4{0, 0, 0, 0};
+        return;
+    }
+    if (m <= 0) return;
+    DeltaBlock& blk = reinterpret_cast<DeltaBlock*>(a.blocks)[int64_t(x) * a.hv + h];
+    uint16_t* const image = HALF ? nullptr : a.images + (int64_t(x) * a.hk + hk) * (2 * kC * DKP);
+    const bool first = h % heads == 0;
+    const u32x4 none = {0, 0, 0, 0};
+
+    // keys
+    constexpr int LPR = DKP / 8, RPP = 256 / LPR;
+    if (tid == 0) sm.bad = kC;
+    u32x4 kr[kC / RPP];
+    const int kc = tid % LPR;
+#pragma unroll
+    for (int i = 0; i < kC / RPP; ++i) {
+        const int r = i * RPP + tid / LPR;
+        kr[i] = none;
+        if (r < m && 8 * kc < a.Dk) kr[i] = *reinterpret_cast<const u32x4*>(a.k + (t0 + r) * a.ld_k + int64_t(hk) * a.Dk + 8 * kc);
+    }
+    float gv = 0.f, bv = 0.f;
+    if (tid < m) {
+        gv = bounded(a.g[(t0 + tid) * a.ld_g + h]);
+        bv = a.beta[(t0 + tid) * a.ld_b + h];
+    }
+    // this wave's 16 queries
+    u32x4 qf[KS];
+    uint32_t qtop = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        qf[s] = none;
+        if (16 * wave + lr < m && 32 * s + 8 * g4 < a.Dk)
+            qf[s] = *reinterpret_cast<const u32x4*>(a.q + (t0 + 16 * wave + lr) * a.ld_q + int64_t(hk) * a.Dk + 32 * s + 8 * g4);
+        if constexpr (!HALF) qtop = max(qtop, top8(qf[s]));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kC / RPP; ++i) {
+        const int r = i * RPP + tid / LPR;
+        uint32_t top = top8(kr[i]);
+        if constexpr (!HALF) {
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) top = max(top, uint32_t(__shfl_xor(int(top), o)));
+            const int e = bf_expo(top);
+            kr[i] = to_half(kr[i], pow2(-e));
+            if (kc == 0) sm.kexp[r] = e;
+            if (first) *reinterpret_cast<u32x4*>(image + r * DKP + 8 * kc) = kr[i];
+        } else if (kc == 0) {
+            sm.kexp[r] = 0;
+        }
+        if (top >= kInf16<E>) atomicMin(&sm.bad, r);
+        *reinterpret_cast<u32x4*>(&sm.k[r * DKP + 8 * (kc ^ kkey<DKP>(r))]) = kr[i];
+    }
+    int qe = 0;
+    if constexpr (!HALF) {
+        // the lanes of a row are 16 apart
+        qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 16)));
+        qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 32)));
+        qe = bf_expo(qtop);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[s] = to_half(qf[s], pow2(-qe));
+            if (first) *reinterpret_cast<u32x4*>(image + kC * DKP + (16 * wave + lr) * DKP + 32 * s + 8 * g4) = qf[s];
+        }
+    }
+    if (wave == 0) {
+        if (!(fabsf(gv) < __builtin_inff() && fabsf(bv) < __builtin_inff())) atomicMin(&sm.bad, lane);
+        // sums in FP64: behind strong decays b reaches thousands, and T and P take differences of neighbours
+        sm.b[lane] = lane_scan(double(gv) * 1.4426950408889634, 0., [](double p, double q) { return p + q; });
+        sm.beta[lane] = bv;
+    }
+    __syncthreads();
+    const int bad = sm.bad;
+    auto k_read = [&](int r, int s) {
+        return *reinterpret_cast<const u32x4*>(&sm.k[r * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(r))]);
+    };
+
+    // A, by rows of tiles
+    {
+        u32x4 kf[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[s] = k_read(16 * wave + lr, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j > wave) break;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) acc = F16::mfma16(kf[s], k_read(16 * j + lr, s), acc);
+            const int cj = 16 * j + lr;
+            const double bj = sm.b[cj] - double(sm.kexp[cj]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 16 * wave + 4 * g4 + i;
+                const float v = acc[i] * sm.beta[t] * exp_b(sm.b[t] + double(sm.kexp[t]) - bj);
+                sm.A[t][cj] = cj < t && t < bad ? v : 0.f;
+            }
+        }
+    }
+    // (I + A)^-1 of this wave's diagonal tile: a lane makes one column
+    {
+        float col[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = lr == i ? 1.f : 0.f;
+#pragma unroll
+            for (int q = 0; q < (i + 3) / 4; ++q) {
+                const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.A[16 * wave + i][16 * wave + 4 * q]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * q + j < i) v = fmaf(-r[j], col[4 * q + j], v);
+            }
+            col[i] = v;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (g4 == i / 4) sm.T[16 * wave + i][16 * wave + lr] = col[i];
+    }
+    __syncthreads();
+    // the tiles below it: T_ij = -T_ii sum_m A_im T_mj.  A step of the FP32 products takes one row of each lane
+    // group's four, so that a result is the next product's operand.
+    {
+        f32x4 tc[4];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            if (j != wave) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc[j][i] = sm.T[16 * j + 4 * g4 + i][16 * j + lr];
+#pragma unroll
+            for (int i = j + 1; i < 4; ++i) {
+                f32x4 y = {0.f, 0.f, 0.f, 0.f}, z = y;
+#pragma unroll
+                for (int k = j; k < i; ++k) {
+                    const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.A[16 * i + lr][16 * k + 4 * g4]);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) y = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], tc[k][s], y, 0, 0, 0);
+                }
+                const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.T[16 * i + lr][16 * i + 4 * g4]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], -y[s], z, 0, 0, 0);
+                tc[i] = z;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) sm.T[16 * i + 4 * g4 + s][16 * j + lr] = z[s];
+            }
+        }
+    }
+    // P of this wave's queries, made as K Q^T: a lane has eight neighbouring keys of one query
+    {
+        const int t = 16 * wave + lr;
+        const double bt = sm.b[t] + double(qe);
+        float p[2][8], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                if (c <= wave / 2) {
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) acc = F16::mfma16(k_read(32 * c + pair_row(lr, b), s), qf[s], acc);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 32 * c + 8 * g4 + 4 * b + i;
+                    const float v = acc[i] * exp_b(bt - sm.b[j] + double(sm.kexp[j]));
+                    p[c][4 * b + i] = j <= t && j < bad ? v : 0.f;
+                    top = fmaxf(top, fabsf(p[c][4 * b + i]));
+                }
+            }
+        top = column_max(top);
+        const int e = top > 0.f ? min(max(14 - expo(top), -60), 60) : 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (c > wave / 2) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[c][i] *= pow2(e);
+            blk.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
+        }
+        if (g4 == 0) {
+            blk.qf[t] = exp_b(bt + double(e));
+            blk.pf[t] = a.scale * pow2(-e);
+        }
+    }
+    __syncthreads();
+    // T as operands
+    {
+        const int c1 = wave / 2, t = 32 * c1 + pair_row(lr, wave & 1);
+        float v[2][8], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = 32 * c + 8 * g4 + i;
+                v[c][i] = j <= t && j < bad ? sm.T[t][j] * sm.beta[j] : 0.f;
+                top = fmaxf(top, fabsf(v[c][i]));
+            }
+        top = column_max(top);
+        const int e = top > 0.f ? min(max(13 - expo(top), -120), 100) : 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (c > c1) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c][i] *= pow2(e);
+            const u32x4 hi = pack_hi(v[c]);
+            const int at = wave < 2 ? wave : 2 * wave - 2 + c;
+            blk.th[at][lane] = hi;
+            blk.tl[at][lane] = pack_lo(v[c], hi);
+        }
+        if (g4 == 0) blk.uf[t] = pow2(-e);
+    }
+    if (wave == 0) {
+        const double all = sm.b[kC - 1], ke = double(sm.kexp[lane]);
+        blk.xf[lane] = exp_b(sm.b[lane] + ke);
+        blk.tf[lane] = exp_b(all - sm.b[lane] + ke);
+        if (lane == 0) blk.etot = exp_b(all), blk.bad = bad;
+    }
+}
+
+// ---------------------------------------------------------------- the chunks in order
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int DKP>
+struct ScanStage {
+    __attribute__((aligned(1024))) uint16_t k[kC * DKP], q[kC * DKP], v[kC * 64];
+    DeltaBlock d;
+};
+
+template <class E, int DKP>
+__global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
+    constexpr int KS = DKP / 32;
+    constexpr bool HALF = __is_same(E, F16);
+    __shared__ ScanStage<DKP> stage[2];  // of this chunk and the next
+    const int heads = a.hv / a.hk, halves = (a.Dv + 63) / 64, group = heads * halves;
+    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * group) * 8 + id % 8;
+    const int hk = int(pair % a.hk), j0 = int(id / 8 % group);
+    const int h = hk * heads + j0 / halves, v0 = j0 % halves * 64, r = int(pair / a.hk);
+    if (r >= a.p.R) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int lr = lane & 15, g4 = lane >> 4;
+    const int c0 = packed_row(a.p, r), n = max(0, packed_row(a.p, r + 1) - c0);
+    bool old;
+    const int slot = packed_slot(a.p, r, &old);
+    const int dv = v0 + 16 * wave + lr;
+    const int64_t sbase = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv + dv;
+
+    // state element (p, b, i): dk = 32 p + 8 g4 + 4 b + i of column dv, in units of 2^-e
+    f32x4 S[KS][2];
+    int e = 0;
+#pragma unroll
+    for (int p = 0; p < KS; ++p)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int dk = 32 * p + 8 * g4 + 4 * b + i;
+                S[p][b][i] = old && dv < a.Dv && dk < a.Dk ? a.sin[sbase + int64_t(dk) * a.Dv] : 0.f;
+            }
+    auto scale_state = [&](float by) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) S[p][b] *= by;
+    };
+
+    // loads of a chunk straight to LDS
+    constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4;
+    const int first = c0 / kC + r;  // number of the request's first unit
+    auto issue = [&](int c, ScanStage<DKP>& st) __attribute__((always_inline)) {
+        const int m = min(kC, n - c * kC);
+        const int64_t t0 = c0 + int64_t(c) * kC;
+        const uint16_t *kp, *qp;
+        int64_t ldk, ldq;
+        if constexpr (HALF) {
+            kp = a.k + t0 * a.ld_k + int64_t(hk) * a.Dk, ldk = a.ld_k;
+            qp = a.q + t0 * a.ld_q + int64_t(hk) * a.Dk, ldq = a.ld_q;
+        } else {
+            kp = a.images + (int64_t(first + c) * a.hk + hk) * (2 * kC * DKP), ldk = DKP;
+            qp = kp + kC * DKP, ldq = DKP;
+        }
+        const uint16_t* const zeros = reinterpret_cast<const uint16_t*>(kZeros);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int row0 = (wave * NI + i) * RPI, row = row0 + lane / LPR;
+            const int kc = lane % LPR ^ kkey<DKP>(row), qc = lane % LPR ^ qkey<DKP>(row);
+            load_lds16(row < m && 8 * kc < a.Dk ? kp + row * ldk + 8 * kc : zeros, lds_byte(st.k + row0 * DKP));
+            load_lds16(row < m && 8 * qc < a.Dk ? qp + row * ldq + 8 * qc : zeros, lds_byte(st.q + row0 * DKP));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row0 = (wave * 2 + i) * 8, row = row0 + lane / 8, vc = v0 + 8 * (lane % 8 ^ vkey(row));
+            load_lds16(row < m && vc < a.Dv ? a.v + (t0 + row) * a.ld_v + int64_t(h) * a.Dv + vc : zeros,
+                       lds_byte(st.v + row0 * 64));
+        }
+        const uint8_t* const blk = a.blocks + (int64_t(first + c) * a.hv + h) * kDeltaBlock;
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            load_lds16(blk, (wave * 5 + i) * 1024 + lane * 16, lds_byte(reinterpret_cast<uint8_t*>(&st.d) + (wave * 5 + i) * 1024));
+    };
+    auto tr_read = [](const uint16_t* p) __attribute__((always_inline)) {
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p)));
+    };
+
+    const int nch = (n + kC - 1) / kC;
+    if (nch > 0) {
+        issue(0, stage[0]);
+        wait_loads();
+    }
+    bool lost = false;  // the column has met something that is not finite
+    for (int c = 0; c < nch; ++c) {
+        __syncthreads();  // this chunk's loads, which every wave has waited for; the other buffer's readers
+        const ScanStage<DKP>& st = stage[c & 1];
+        if (c + 1 < nch) issue(c + 1, stage[c + 1 & 1]);
+        const int m = min(kC, n - c * kC);
+
+        // values: token 32 p + 8 g4 + 4 b + i of the lane's column
+        u32x2 vb[2][2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int row = 32 * p + 8 * g4 + 4 * b + lr / 4, ch = 2 * wave + lr % 4 / 2;
+                vb[p][b] = tr_read(st.v + row * 64 + 8 * (ch ^ vkey(row)) + lr % 2 * 4);
+            }
+        int late = st.d.bad;  // first token that the column gets no number from
+        float top = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w = vb[p][b][i];
+                    const bool l = (w & 0x7FFFu) >= kInf16<E>, g = (w >> 16 & 0x7FFFu) >= kInf16<E>;
+                    odd |= l | g;
+                    top = fmaxf(top, l ? 0.f : fabsf(lo16<E>(w)));
+                    top = fmaxf(top, g ? 0.f : fabsf(hi16<E>(w)));
+                }
+        if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = 32 * p + 8 * g4 + 4 * b + 2 * i;
+                        if ((vb[p][b][i] & 0x7FFFu) >= kInf16<E>) late = min(late, t);
+                        if ((vb[p][b][i] >> 16 & 0x7FFFu) >= kInf16<E>) late = min(late, t + 1);
+                    }
+            late = min(late, __shfl_xor(late, 16));
+            late = min(late, __shfl_xor(late, 32));
+        }
+        const bool any_late = __any(late < kC);
+
+        // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
+        float big = 0.f;
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(S[p][b][i]));
+        const int none = -1000;
+        int level = max(top > 0.f ? expo(top) + e : none, big > 0.f ? expo(big) : none);
+        level = max(level, __shfl_xor(level, 16));
+        level = max(level, __shfl_xor(level, 32));
+        bool move = level >= 11 || (level < 5 && level != none);
+        int to = min(max(e + 10 - level, -120), 100);
+        f32x4 U[2][2];
+        u32x4 sh[KS];
+        for (int again = 0;; ++again) {
+            if (__any(move)) {
+                const int by = move ? to - e : 0;
+                scale_state(pow2(min(max(by, -126), 126)));
+                e += min(max(by, -126), 126);
+            }
+            u32x4 sl[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const float x[8] = {S[s][0][0], S[s][0][1], S[s][0][2], S[s][0][3], S[s][1][0], S[s][1][1], S[s][1][2], S[s][1][3]};
+                sh[s] = pack_hi(x);
+                sl[s] = pack_lo(x, sh[s]);
+            }
+            const float unit = pow2(e);
+            u32x4 rh[2], rl[2];
+            float most = 0.f;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float x[8];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                    const int row = 32 * p + pair_row(lr, b);
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        const u32x4 kf = *reinterpret_cast<const u32x4*>(st.k + row * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(row)));
+                        acc = F16::mfma16(kf, sl[s], acc);
+                        acc = F16::mfma16(kf, sh[s], acc);
+                    }
+                    const f32x4 xf = *reinterpret_cast<const f32x4*>(&st.d.xf[32 * p + 8 * g4 + 4 * b]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = vb[p][b][i / 2];
+                        const float v = i & 1 ? hi16<E>(w) : lo16<E>(w);
+                        x[4 * b + i] = fmaf(v, unit, -xf[i] * acc[i]);
+                    }
+                }
+                if (__builtin_expect(any_late, 0)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = 32 * p + 8 * g4 + i >= late ? 0.f : x[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i]));
+                rh[p] = pack_hi(x);
+                rl[p] = pack_lo(x, rh[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k <= p; ++k) {
+                        const int at = p ? 2 + 2 * b + k : b;
+                        acc = F16::mfma16(st.d.tl[at][lane], rh[k], acc);
+                        acc = F16::mfma16(st.d.th[at][lane], rl[k], acc);
+                        acc = F16::mfma16(st.d.th[at][lane], rh[k], acc);
+                    }
+                    const f32x4 uf = *reinterpret_cast<const f32x4*>(&st.d.uf[32 * p + 8 * g4 + 4 * b]);
+                    U[p][b] = acc * uf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(U[p][b][i]));
+                }
+            // beyond binary16: once more in larger units
+            most = column_max(most);
+            move = most >= 32768.f && e > -120;
+            if (__builtin_expect(!__any(move), 1) || again == 12) break;
+            to = max(e - 10, -120);
+        }
+
+        // outputs: queries 16 x + lr of columns 4 g4 + i
+        f32x4 o[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int row = 16 * y + lr;
+            o[y] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                o[y] = F16::mfma16(sh[s], *reinterpret_cast<const u32x4*>(st.q + row * DKP + 8 * ((4 * s + g4) ^ qkey<DKP>(row))), o[y]);
+            o[y] *= st.d.qf[row];
+        }
+        u32x4 uo[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
+            uo[p] = pack_hi(x);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int k = 0; k <= y / 2; ++k)
+                o[y] = F16::mfma16(uo[k], st.d.p[y < 2 ? y : 2 * y - 2 + k][lane], o[y]);
+        float down[4];
+        int from[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            down[i] = pow2(-__shfl(e, 4 * g4 + i));
+            from[i] = __shfl(lost ? 0 : late, 4 * g4 + i);
+        }
+        wait_loads();  // the next chunk's; before the stores, which need not be waited for
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int t = 16 * y + lr, col = v0 + 16 * wave + 4 * g4;
+            const float pf = st.d.pf[t];
+            float z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = t >= from[i] ? __builtin_nanf("") : o[y][i] * pf * down[i];
+            if (t < m && col < a.Dv)
+                *reinterpret_cast<u32x2*>(a.y + (c0 + int64_t(c) * kC + t) * a.ld_y + int64_t(h) * a.Dv + col) =
+                    u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
+        }
+
+        // the state
+        lost |= late < kC;
+        scale_state(lost ? __builtin_nanf("") : st.d.etot);
+        u32x4 uh[2], ul[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float x[8];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * b + i] = U[p][b][i] * tf[i];
+            }
+            uh[p] = pack_hi(x);
+            ul[p] = pack_lo(x, uh[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    u32x4 kt;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int row = 32 * k + 8 * g4 + 4 * z + lr / 4;
+                        const u32x2 w = tr_read(st.k + row * DKP + 8 * ((4 * p + lr % 4) ^ kkey<DKP>(row)) + 4 * b);
+                        kt[2 * z] = w[0], kt[2 * z + 1] = w[1];
+                    }
+                    S[p][b] = F16::mfma16(kt, ul[k], S[p][b]);
+                    S[p][b] = F16::mfma16(kt, uh[k], S[p][b]);
+                }
+    }
+    if (slot >= 0 && dv < a.Dv) {
+        const float by = pow2(-e);
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int dk = 32 * p + 8 * g4 + 4 * b + i;
+                    if (dk < a.Dk) a.sout[sbase + int64_t(dk) * a.Dv] = S[p][b][i] * by;
+                }
+    }
+}
+
+template <class E, int DKP>
+void launch(DeltaArgs a, hipStream_t s) {
+    constexpr int64_t most = 8 << 20;  // a launch holds fewer than 2^32 threads
+    const int64_t units = int64_t(a.p.T) / kC + a.p.R + 1, heads = a.hv / a.hk, halves = (a.Dv + 63) / 64;
+    const int64_t prep = (units * a.hk + 7) / 8 * 8 * heads;
+    for (a.id0 = 0; a.id0 < prep; a.id0 += most)
+        k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a);
+    const int64_t scan = (int64_t(a.p.R) * a.hk + 7) / 8 * 8 * heads * halves;
+    for (a.id0 = 0; a.id0 < scan; a.id0 += most)
+        k_delta_scan<E, DKP><<<unsigned(std::min(most, scan - a.id0)), 256, 0, s>>>(a);
+}
+
+}  // namespace
+
+template <class E>
+void launch_delta_chunks(const DeltaArgs& a, hipStream_t s) {
+    if (a.Dk <= 64) launch<E, 64>(a, s);
+    else launch<E, 128>(a, s);
+}
+template void launch_delta_chunks<F16>(const DeltaArgs&, hipStream_t);
+template void launch_delta_chunks<BF16>(const DeltaArgs&, hipStream_t);
+
+}  // namespace vqmlp

@@ -16,8 +16,6 @@ namespace vqmlp {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMinG = -80.f;  // e^-80 = 2e-35: nothing of the state before survives it in FP32
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kStepMaxQ = 16;
 constexpr int64_t kMaxLd = 1 << 24;  // 63 tokens apart still is a 32-bit number of bytes
@@ -36,16 +34,6 @@ struct LinArgs {
     int id0;      // number of the launch's first workgroup
     float scale;
 };
-
-// e^x to about two roundings: the hardware's 2^h with h = x log2 e, and what h lost as a factor 1 + r.
-__device__ __forceinline__ float exp_f32(float x) {
-    const float h = x * kLog2e;
-    const float r = fmaf(x, kLog2e, -h) + x * float(1.4426950408889634 - double(kLog2e));
-    return __builtin_amdgcn_exp2f(h) * fmaf(r, kLn2, 1.f);
-}
-
-// The log of a decay from kMinG on; NaN stays NaN.
-__device__ __forceinline__ float bounded(float g) { return g < kMinG ? kMinG : g; }
 
 __device__ __forceinline__ int lin_row(const LinArgs& a, int r) { return min(max(a.cu[r], 0), a.T); }
 
@@ -234,47 +222,9 @@ struct LinOutSmem {
     __attribute__((aligned(1024))) uint16_t q[kC * DKP], k[kC * DKP];  // rows of tokens, chunks permuted
 };
 
-// Prefix over the 64 lanes with data-parallel moves: within rows of 16 lanes, then across them.
-template <class T, class F>
-__device__ __forceinline__ T lane_scan(T v, T none, F&& op) {
-    auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
-        struct Words { int w[sizeof(T) / 4]; };
-        Words n = __builtin_bit_cast(Words, none);
-        const Words x = __builtin_bit_cast(Words, v);
-#pragma unroll
-        for (size_t i = 0; i < sizeof(T) / 4; ++i)
-            n.w[i] = __builtin_amdgcn_update_dpp(n.w[i], x.w[i], decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-        v = op(v, __builtin_bit_cast(T, n));
-    };
-    typedef std::integral_constant<int, 0xF> all;
-    step(std::integral_constant<int, 0x111>{}, all{});  // from 1, 2, 4 and 8 lanes below in the row
-    step(std::integral_constant<int, 0x112>{}, all{});
-    step(std::integral_constant<int, 0x114>{}, all{});
-    step(std::integral_constant<int, 0x118>{}, all{});
-    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // a row's last lane to the next row
-    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // lane 31 to the upper half
-    return v;
-}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = lane_scan(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
     return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
-}
-
-// Maximum over the lanes with the same lane % 16, in all of them.  The operands of a swap are two values to
-// the compiler, which takes both results for one otherwise.
-__device__ __forceinline__ float column_max(float v) {
-    uint32_t x = __builtin_bit_cast(uint32_t, v);  // not negative: the bits are in the values' order
-    const auto a = __builtin_amdgcn_permlane32_swap(x, uint32_t(fresh(int(x))), false, false);
-    x = max(uint32_t(a[0]), uint32_t(a[1]));
-    const auto b = __builtin_amdgcn_permlane16_swap(x, uint32_t(fresh(int(x))), false, false);
-    return __builtin_bit_cast(float, max(uint32_t(b[0]), uint32_t(b[1])));
-}
-
-// 2^e, e in [-126, 127]
-__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, uint32_t(e + 127) << 23); }
-// Exponent of |x| (floor of log2), -127 for zero and subnormals.
-__device__ __forceinline__ int expo(float x) {
-    return int((__builtin_bit_cast(uint32_t, x) >> 23) & 0xFF) - 127;
 }
 
 struct LinUnit {
