@@ -74,12 +74,18 @@ __device__ __forceinline__ u32x4 pack_hi(const float* x) {
     }
     return w;
 }
-__device__ __forceinline__ u32x4 pack_lo(const float* x, u32x4 hi) {
+// minus: -1, unknown to the compiler, which then makes a mixed multiply-add that rounds to binary16 itself.
+__device__ __forceinline__ u32x4 pack_lo(const float* x, u32x4 hi, float minus) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = pack16<F16>(fmaf(lo16<F16>(hi[i]), -1.f, x[2 * i]), fmaf(hi16<F16>(hi[i]), -1.f, x[2 * i + 1]));
+        w[i] = pack16<F16>(fmaf(lo16<F16>(hi[i]), minus, x[2 * i]), fmaf(hi16<F16>(hi[i]), minus, x[2 * i + 1]));
     return w;
+}
+__device__ __forceinline__ float minus_one() {
+    float m = -1.f;
+    asm("" : "+v"(m));
+    return m;
 }
 
 // Largest bits of eight 16-bit magnitudes
@@ -88,6 +94,19 @@ __device__ __forceinline__ uint32_t top8(u32x4 x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) t = max(t, max(x[i] & 0x7FFFu, x[i] >> 16 & 0x7FFFu));
     return t;
+}
+// ... of a lane's values of a chunk
+__device__ __forceinline__ uint32_t largest(const u32x2 (&x)[2][2]) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 t = {0, 0};
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, x[p][b][i] & 0x7FFF7FFFu));
+    return max(t[0], t[1]);
 }
 template <class E>
 constexpr uint32_t kInf16 = __is_same(E, F16) ? 0x7C00u : 0x7F80u;
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
             const u32x4 hi = pack_hi(v[c]);
             const int at = wave < 2 ? wave : 2 * wave - 2 + c;
             blk.th[at][lane] = hi;
-            blk.tl[at][lane] = pack_lo(v[c], hi);
+            blk.tl[at][lane] = pack_lo(v[c], hi, minus_one());
         }
         if (g4 == 0) blk.uf[t] = pow2(-e);
     }
@@ -350,6 +369,14 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
 // ---------------------------------------------------------------- the chunks in order
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Maximum over the lanes with the same lane % 16, in all of them
+__device__ __forceinline__ int column_max(int v) {
+    const auto x = __builtin_amdgcn_permlane32_swap(uint32_t(v), uint32_t(fresh(v)), false, false);
+    v = max(int(x[0]), int(x[1]));
+    const auto y = __builtin_amdgcn_permlane16_swap(uint32_t(v), uint32_t(fresh(v)), false, false);
+    return max(int(y[0]), int(y[1]));
+}
+
 template <int DKP>
 struct ScanStage {
     __attribute__((aligned(1024))) uint16_t k[kC * DKP], q[kC * DKP], v[kC * 64];
@@ -357,7 +384,7 @@ struct ScanStage {
 };
 
 template <class E, int DKP>
-__global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
+__global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
     constexpr int KS = DKP / 32;
     constexpr bool HALF = __is_same(E, F16);
     __shared__ ScanStage<DKP> stage[2];  // of this chunk and the next
@@ -393,40 +420,73 @@ __global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
             for (int b = 0; b < 2; ++b) S[p][b] *= by;
     };
 
-    // loads of a chunk straight to LDS
-    constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4;
-    const int first = c0 / kC + r;  // number of the request's first unit
-    auto issue = [&](int c, ScanStage<DKP>& st) __attribute__((always_inline)) {
-        const int m = min(kC, n - c * kC);
-        const int64_t t0 = c0 + int64_t(c) * kC;
-        const uint16_t *kp, *qp;
-        int64_t ldk, ldq;
-        if constexpr (HALF) {
-            kp = a.k + t0 * a.ld_k + int64_t(hk) * a.Dk, ldk = a.ld_k;
-            qp = a.q + t0 * a.ld_q + int64_t(hk) * a.Dk, ldq = a.ld_q;
+    // Loads straight to LDS, 1 KB each, kLoads of them a wave and chunk: bases that the wave shares plus
+    // 32-bit offsets of the lanes, which stay the same from chunk to chunk.
+    constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4, kLoads = 2 * NI + 7;
+    constexpr int kStage = sizeof(ScanStage<DKP>), kQ = offsetof(ScanStage<DKP>, q), kV = offsetof(ScanStage<DKP>, v),
+                  kD = offsetof(ScanStage<DKP>, d);
+    const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldq = 2 * (HALF ? a.ld_q : DKP), ldv = 2 * a.ld_v;  // bytes
+    const int64_t unit0 = c0 / kC + r;  // number of the request's first unit
+    const uint8_t *kp, *qp, *vp, *dp;   // of the next chunk to be loaded
+    if constexpr (HALF) {
+        kp = reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk;
+        qp = reinterpret_cast<const uint8_t*>(a.q + int64_t(hk) * a.Dk) + c0 * ldq;
+    } else {
+        kp = reinterpret_cast<const uint8_t*>(a.images + (unit0 * a.hk + hk) * (2 * kC * DKP));
+        qp = kp + kC * DKP * 2;
+    }
+    vp = reinterpret_cast<const uint8_t*>(a.v + int64_t(h) * a.Dv + v0) + c0 * ldv;
+    dp = a.blocks + (unit0 * a.hv + h) * kDeltaBlock + wave * 5120;
+    const int64_t kstep = HALF ? kC * ldk : int64_t(a.hk) * (2 * kC * DKP) * 2, qstep = HALF ? kC * ldq : kstep;
+    const int64_t vstep = kC * ldv, dstep = int64_t(a.hv) * kDeltaBlock;
+    uint32_t koff[NI], qoff[NI], voff[2];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int row = (wave * NI + i) * RPI + lane / LPR;
+        koff[i] = uint32_t(row) * uint32_t(ldk) + 16 * uint32_t(lane % LPR ^ kkey<DKP>(row));
+        qoff[i] = uint32_t(row) * uint32_t(ldq) + 16 * uint32_t(lane % LPR ^ qkey<DKP>(row));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = (wave * 2 + i) * 8 + lane / 8;
+        voff[i] = uint32_t(row) * uint32_t(ldv) + 16 * uint32_t(lane % 8 ^ vkey(row));
+    }
+    const uint32_t lds0 = lds_byte(stage);
+    const bool wide = (!HALF || a.Dk == DKP) && v0 + 64 <= a.Dv;  // every column is there
+    // loads from .. to - 1 of a chunk of m tokens into buffer `buf`
+    auto issue = [&](int from, int to, int m, int buf) __attribute__((always_inline)) {
+        const uint32_t at = lds0 + buf * kStage;
+        if (__builtin_expect(wide && m == kC, 1)) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                if (i < from || i >= to) continue;
+                if (i < NI) load_lds16(kp, koff[i], at + (wave * NI + i) * 1024);
+                else if (i < 2 * NI) load_lds16(qp, qoff[i - NI], at + kQ + (wave * NI + i - NI) * 1024);
+                else if (i < 2 * NI + 2) load_lds16(vp, voff[i - 2 * NI], at + kV + (wave * 2 + i - 2 * NI) * 1024);
+                else load_lds16(dp + (i - 2 * NI - 2) * 1024, lane * 16, at + kD + (wave * 5 + i - 2 * NI - 2) * 1024);
+            }
         } else {
-            kp = a.images + (int64_t(first + c) * a.hk + hk) * (2 * kC * DKP), ldk = DKP;
-            qp = kp + kC * DKP, ldq = DKP;
-        }
-        const uint16_t* const zeros = reinterpret_cast<const uint16_t*>(kZeros);
+            // rows and columns that are not there are zeros
+            const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(kZeros);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int row0 = (wave * NI + i) * RPI, row = row0 + lane / LPR;
-            const int kc = lane % LPR ^ kkey<DKP>(row), qc = lane % LPR ^ qkey<DKP>(row);
-            load_lds16(row < m && 8 * kc < a.Dk ? kp + row * ldk + 8 * kc : zeros, lds_byte(st.k + row0 * DKP));
-            load_lds16(row < m && 8 * qc < a.Dk ? qp + row * ldq + 8 * qc : zeros, lds_byte(st.q + row0 * DKP));
+            for (int i = 0; i < kLoads; ++i) {
+                if (i < from || i >= to) continue;
+                if (i < 2 * NI) {
+                    const int j = i % NI, row = (wave * NI + j) * RPI + lane / LPR;
+                    const int ch = lane % LPR ^ (i < NI ? kkey<DKP>(row) : qkey<DKP>(row));
+                    const bool there = row < m && (!HALF || 8 * ch < a.Dk);
+                    if (i < NI) load_lds16(there ? kp + koff[j] : zeros, at + (wave * NI + j) * 1024);
+                    else load_lds16(there ? qp + qoff[j] : zeros, at + kQ + (wave * NI + j) * 1024);
+                } else if (i < 2 * NI + 2) {
+                    const int j = i - 2 * NI, row = (wave * 2 + j) * 8 + lane / 8, ch = lane % 8 ^ vkey(row);
+                    load_lds16(row < m && v0 + 8 * ch < a.Dv ? vp + voff[j] : zeros, at + kV + (wave * 2 + j) * 1024);
+                } else {
+                    load_lds16(dp + (i - 2 * NI - 2) * 1024, lane * 16, at + kD + (wave * 5 + i - 2 * NI - 2) * 1024);
+                }
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row0 = (wave * 2 + i) * 8, row = row0 + lane / 8, vc = v0 + 8 * (lane % 8 ^ vkey(row));
-            load_lds16(row < m && vc < a.Dv ? a.v + (t0 + row) * a.ld_v + int64_t(h) * a.Dv + vc : zeros,
-                       lds_byte(st.v + row0 * 64));
-        }
-        const uint8_t* const blk = a.blocks + (int64_t(first + c) * a.hv + h) * kDeltaBlock;
-#pragma unroll
-        for (int i = 0; i < 5; ++i)
-            load_lds16(blk, (wave * 5 + i) * 1024 + lane * 16, lds_byte(reinterpret_cast<uint8_t*>(&st.d) + (wave * 5 + i) * 1024));
     };
+    auto advance = [&]() __attribute__((always_inline)) { kp += kstep, qp += qstep, vp += vstep, dp += dstep; };
     auto tr_read = [](const uint16_t* p) __attribute__((always_inline)) {
         return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p)));
@@ -434,15 +494,22 @@ __global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
 
     const int nch = (n + kC - 1) / kC;
     if (nch > 0) {
-        issue(0, stage[0]);
+        issue(0, kLoads, min(kC, n), 0);
+        advance();
         wait_loads();
     }
+    uint8_t* yp = reinterpret_cast<uint8_t*>(a.y + c0 * a.ld_y + int64_t(h) * a.Dv + v0);
+    const uint32_t yoff = uint32_t(lr) * uint32_t(2 * a.ld_y) + 2 * (16 * wave + 4 * g4);
+    const bool out = v0 + 16 * wave + 4 * g4 < a.Dv;
+    const float minus = minus_one();
     bool lost = false;  // the column has met something that is not finite
     for (int c = 0; c < nch; ++c) {
         __syncthreads();  // this chunk's loads, which every wave has waited for; the other buffer's readers
         const ScanStage<DKP>& st = stage[c & 1];
-        if (c + 1 < nch) issue(c + 1, stage[c + 1 & 1]);
-        const int m = min(kC, n - c * kC);
+        const int m = min(kC, n - c * kC), left = n - (c + 1) * kC;
+        auto part = [&](int from, int to) __attribute__((always_inline)) {
+            if (left > 0) issue(from, to, min(kC, left), c + 1 & 1);
+        };
 
         // values: token 32 p + 8 g4 + 4 b + i of the lane's column
         u32x2 vb[2][2];
@@ -453,37 +520,22 @@ __global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
                 const int row = 32 * p + 8 * g4 + 4 * b + lr / 4, ch = 2 * wave + lr % 4 / 2;
                 vb[p][b] = tr_read(st.v + row * 64 + 8 * (ch ^ vkey(row)) + lr % 2 * 4);
             }
-        int late = st.d.bad;  // first token that the column gets no number from
-        float top = 0.f;
-        bool odd = false;
+        u32x4 kf[KS][2][2];
+        auto read_k = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = vb[p][b][i];
-                    const bool l = (w & 0x7FFFu) >= kInf16<E>, g = (w >> 16 & 0x7FFFu) >= kInf16<E>;
-                    odd |= l | g;
-                    top = fmaxf(top, l ? 0.f : fabsf(lo16<E>(w)));
-                    top = fmaxf(top, g ? 0.f : fabsf(hi16<E>(w)));
-                }
-        if (__builtin_expect(__any(odd), 0)) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int t = 32 * p + 8 * g4 + 4 * b + 2 * i;
-                        if ((vb[p][b][i] & 0x7FFFu) >= kInf16<E>) late = min(late, t);
-                        if ((vb[p][b][i] >> 16 & 0x7FFFu) >= kInf16<E>) late = min(late, t + 1);
+                    for (int b = 0; b < 2; ++b) {
+                        const int row = 32 * p + pair_row(lr, b);
+                        kf[s][p][b] = *reinterpret_cast<const u32x4*>(st.k + row * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(row)));
                     }
-            late = min(late, __shfl_xor(late, 16));
-            late = min(late, __shfl_xor(late, 32));
-        }
-        const bool any_late = __any(late < kC);
-
+        };
+        read_k();
+        int late = st.d.bad;  // first token that the column gets no number from
+        __builtin_amdgcn_sched_barrier(0);  // all on their way
+        part(0, NI + 2);
         // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
         float big = 0.f;
 #pragma unroll
@@ -492,51 +544,84 @@ __global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(S[p][b][i]));
+        uint32_t vtop = largest(vb);
+        if (__builtin_expect(__any(vtop >= kInf16<E>), 0)) {
+            // of the finite ones, and the first of the others
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = 32 * p + 8 * g4 + 4 * b + 2 * i;
+                        uint32_t w = vb[p][b][i];
+                        if ((w >> 16 & 0x7FFFu) >= kInf16<E>) late = min(late, t + 1), w &= 0xFFFFu;
+                        if ((w & 0x7FFFu) >= kInf16<E>) late = min(late, t), w &= 0xFFFF0000u;
+                        vb[p][b][i] = w;
+                    }
+            late = min(late, __shfl_xor(late, 16));
+            late = min(late, __shfl_xor(late, 32));
+            vtop = largest(vb);
+        }
+        const float top = lo16<E>(vtop);
+        const bool any_late = __any(late < kC);
         const int none = -1000;
         int level = max(top > 0.f ? expo(top) + e : none, big > 0.f ? expo(big) : none);
-        level = max(level, __shfl_xor(level, 16));
-        level = max(level, __shfl_xor(level, 32));
+        level = column_max(level);
         bool move = level >= 11 || (level < 5 && level != none);
         int to = min(max(e + 10 - level, -120), 100);
         f32x4 U[2][2];
         u32x4 sh[KS];
         for (int again = 0;; ++again) {
-            if (__any(move)) {
-                const int by = move ? to - e : 0;
-                scale_state(pow2(min(max(by, -126), 126)));
-                e += min(max(by, -126), 126);
+            if (__builtin_expect(__any(move), 0)) {
+                const int by = min(max(move ? to - e : 0, -126), 126);
+                scale_state(pow2(by));
+                e += by;
             }
             u32x4 sl[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const float x[8] = {S[s][0][0], S[s][0][1], S[s][0][2], S[s][0][3], S[s][1][0], S[s][1][1], S[s][1][2], S[s][1][3]};
                 sh[s] = pack_hi(x);
-                sl[s] = pack_lo(x, sh[s]);
+                sl[s] = pack_lo(x, sh[s], minus);
             }
             const float unit = pow2(e);
+            f32x4 acc[2][2], xf[2][2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    acc[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    xf[p][b] = *reinterpret_cast<const f32x4*>(&st.d.xf[32 * p + 8 * g4 + 4 * b]);
+                }
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) acc[p][b] = F16::mfma16(kf[s][p][b], sl[s], acc[p][b]);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) acc[p][b] = F16::mfma16(kf[s][p][b], sh[s], acc[p][b]);
+            }
+            u32x4 th[6], tl[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) th[i] = st.d.th[i][lane], tl[i] = st.d.tl[i][lane];
+            __builtin_amdgcn_sched_barrier(0);
             u32x4 rh[2], rl[2];
             float most = 0.f;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float x[8];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                    const int row = 32 * p + pair_row(lr, b);
-#pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        const u32x4 kf = *reinterpret_cast<const u32x4*>(st.k + row * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(row)));
-                        acc = F16::mfma16(kf, sl[s], acc);
-                        acc = F16::mfma16(kf, sh[s], acc);
-                    }
-                    const f32x4 xf = *reinterpret_cast<const f32x4*>(&st.d.xf[32 * p + 8 * g4 + 4 * b]);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t w = vb[p][b][i / 2];
                         const float v = i & 1 ? hi16<E>(w) : lo16<E>(w);
-                        x[4 * b + i] = fmaf(v, unit, -xf[i] * acc[i]);
+                        x[4 * b + i] = fmaf(v, unit, -xf[p][b][i] * acc[p][b][i]);
                     }
-                }
                 if (__builtin_expect(any_late, 0)) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = 32 * p + 8 * g4 + i >= late ? 0.f : x[i];
@@ -544,106 +629,128 @@ __global__ void __launch_bounds__(256) k_delta_scan(DeltaArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i]));
                 rh[p] = pack_hi(x);
-                rl[p] = pack_lo(x, rh[p]);
+                rl[p] = pack_lo(x, rh[p], minus);
             }
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                for (int b = 0; b < 2; ++b) U[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int k = 0; k <= p; ++k) {
-                        const int at = p ? 2 + 2 * b + k : b;
-                        acc = F16::mfma16(st.d.tl[at][lane], rh[k], acc);
-                        acc = F16::mfma16(st.d.th[at][lane], rl[k], acc);
-                        acc = F16::mfma16(st.d.th[at][lane], rh[k], acc);
-                    }
-                    const f32x4 uf = *reinterpret_cast<const f32x4*>(&st.d.uf[32 * p + 8 * g4 + 4 * b]);
-                    U[p][b] = acc * uf;
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int z = 0; z < 3; ++z)
+#pragma unroll
+                    for (int p = k; p < 2; ++p)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int at = p ? 2 + 2 * b + k : b;
+                            U[p][b] = F16::mfma16(z == 0 ? tl[at] : th[at], z == 1 ? rl[k] : rh[k], U[p][b]);
+                        }
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    U[p][b] *= *reinterpret_cast<const f32x4*>(&st.d.uf[32 * p + 8 * g4 + 4 * b]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(U[p][b][i]));
                 }
             // beyond binary16: once more in larger units
-            most = column_max(most);
             move = most >= 32768.f && e > -120;
             if (__builtin_expect(!__any(move), 1) || again == 12) break;
+            move = column_max(move);
             to = max(e - 10, -120);
+            read_k();
         }
 
         // outputs: queries 16 x + lr of columns 4 g4 + i
-        f32x4 o[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int row = 16 * y + lr;
-            o[y] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                o[y] = F16::mfma16(sh[s], *reinterpret_cast<const u32x4*>(st.q + row * DKP + 8 * ((4 * s + g4) ^ qkey<DKP>(row))), o[y]);
-            o[y] *= st.d.qf[row];
-        }
-        u32x4 uo[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
-            uo[p] = pack_hi(x);
-        }
+        u32x4 qr[4][KS], pr[6], kt[KS][2][2];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int k = 0; k <= y / 2; ++k)
-                o[y] = F16::mfma16(uo[k], st.d.p[y < 2 ? y : 2 * y - 2 + k][lane], o[y]);
-        float down[4];
-        int from[4];
+            for (int s = 0; s < KS; ++s) {
+                const int row = 16 * y + lr;
+                qr[y][s] = *reinterpret_cast<const u32x4*>(st.q + row * DKP + 8 * ((4 * s + g4) ^ qkey<DKP>(row)));
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            down[i] = pow2(-__shfl(e, 4 * g4 + i));
-            from[i] = __shfl(lost ? 0 : late, 4 * g4 + i);
-        }
-        wait_loads();  // the next chunk's; before the stores, which need not be waited for
+        for (int i = 0; i < 6; ++i) pr[i] = st.d.p[i][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        part(NI + 2, 2 * NI);
+        f32x4 o[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int t = 16 * y + lr, col = v0 + 16 * wave + 4 * g4;
-            const float pf = st.d.pf[t];
-            float z[4];
+        for (int y = 0; y < 4; ++y) o[y] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = t >= from[i] ? __builtin_nanf("") : o[y][i] * pf * down[i];
-            if (t < m && col < a.Dv)
-                *reinterpret_cast<u32x2*>(a.y + (c0 + int64_t(c) * kC + t) * a.ld_y + int64_t(h) * a.Dv + col) =
-                    u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
-        }
-
-        // the state
-        lost |= late < kC;
-        scale_state(lost ? __builtin_nanf("") : st.d.etot);
-        u32x4 uh[2], ul[2];
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[y] = F16::mfma16(sh[s], qr[y][s], o[y]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[y] *= st.d.qf[16 * y + lr];
+        u32x4 uo[2], uh[2], ul[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            float x[8];
+            float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
+            uo[p] = pack_hi(x);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * b + i] = U[p][b][i] * tf[i];
+                for (int i = 0; i < 4; ++i) x[4 * b + i] *= tf[i];
             }
             uh[p] = pack_hi(x);
-            ul[p] = pack_lo(x, uh[p]);
+            ul[p] = pack_lo(x, uh[p], minus);
         }
 #pragma unroll
-        for (int p = 0; p < KS; ++p)
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int k = 0; k <= y / 2; ++k) o[y] = F16::mfma16(uo[k], pr[y < 2 ? y : 2 * y - 2 + k], o[y]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    u32x4 kt;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int p = 0; p < KS; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int row = 32 * k + 8 * g4 + 4 * z + lr / 4;
                         const u32x2 w = tr_read(st.k + row * DKP + 8 * ((4 * p + lr % 4) ^ kkey<DKP>(row)) + 4 * b);
-                        kt[2 * z] = w[0], kt[2 * z + 1] = w[1];
+                        kt[p][b][k][2 * z] = w[0], kt[p][b][k][2 * z + 1] = w[1];
                     }
-                    S[p][b] = F16::mfma16(kt, ul[k], S[p][b]);
-                    S[p][b] = F16::mfma16(kt, uh[k], S[p][b]);
                 }
+        __builtin_amdgcn_sched_barrier(0);
+        part(2 * NI, kLoads);
+        advance();
+        // the state
+        const bool was = lost;
+        lost |= late < kC;
+        scale_state(lost ? __builtin_nanf("") : st.d.etot);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int p = 0; p < KS; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) S[p][b] = F16::mfma16(kt[p][b][k], z ? uh[k] : ul[k], S[p][b]);
+        float down[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) down[i] = pow2(-__shfl(e, 4 * g4 + i));
+        wait_loads();  // the next chunk's; before the stores, which need not be waited for
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[y] *= st.d.pf[16 * y + lr];
+        if (__builtin_expect(__any(lost), 0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int from = __shfl(was ? 0 : late, 4 * g4 + i);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[y][i] = 16 * y + lr >= from ? __builtin_nanf("") : o[y][i];
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (16 * y + lr < m && out)
+                *reinterpret_cast<u32x2*>(yp + 32 * y * a.ld_y + yoff) =
+                    u32x2{pack16<E>(o[y][0] * down[0], o[y][1] * down[1]), pack16<E>(o[y][2] * down[2], o[y][3] * down[3])};
+        }
+        yp += 2 * kC * a.ld_y;
     }
     if (slot >= 0 && dv < a.Dv) {
         const float by = pow2(-e);
