@@ -26,20 +26,28 @@ namespace {
 
 constexpr int kC = kDeltaC;
 
-// A block of the workspace: parts of T and P as the lanes of the matrix cores take them (1 KB each), then
-// factors for each token.
-struct DeltaBlock {
-    u32x4 th[6][64], tl[6][64], p[6][64];
+// A block of the workspace: parts of T and P as the lanes of the matrix cores take them (1 KB each) and
+// factors for each token; what the state's chain takes, then what the outputs take.
+struct StateBlock {
+    u32x4 th[6][64], tl[6][64];
     float xf[kC];  // e^b 2^kexp: of K S
     float uf[kC];  // the unit of T's row
     float tf[kC];  // e^(b_64 - b) 2^kexp: of U where it joins the state
-    float qf[kC];  // e^b 2^qexp in units of P's row: of Q S
-    float pf[kC];  // scale times the unit of P's row
     float etot;    // e^b_64
     int bad;       // first token with something not finite in k, g or beta, or 64
-    float pad[190];
+    int pad[62];
 };
-static_assert(sizeof(DeltaBlock) == kDeltaBlock, "block");
+struct OutBlock {
+    u32x4 p[6][64];
+    float qf[kC];  // e^b 2^qexp in units of P's row: of Q S
+    float pf[kC];  // scale times the unit of P's row
+    int pad[128];
+};
+struct DeltaBlock {
+    StateBlock s;
+    OutBlock o;
+};
+static_assert(sizeof(StateBlock) == 13 * 1024 && sizeof(DeltaBlock) == kDeltaBlock, "block");
 
 __device__ uint32_t kZeros[4] = {0, 0, 0, 0};  // where rows and columns that do not exist are read
 
@@ -324,11 +332,11 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
             if (c > wave / 2) break;
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[c][i] *= pow2(e);
-            blk.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
+            blk.o.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
         }
         if (g4 == 0) {
-            blk.qf[t] = exp_b(bt + double(e));
-            blk.pf[t] = a.scale * pow2(-e);
+            blk.o.qf[t] = exp_b(bt + double(e));
+            blk.o.pf[t] = a.scale * pow2(-e);
         }
     }
     __syncthreads();
@@ -353,16 +361,16 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
             for (int i = 0; i < 8; ++i) v[c][i] *= pow2(e);
             const u32x4 hi = pack_hi(v[c]);
             const int at = wave < 2 ? wave : 2 * wave - 2 + c;
-            blk.th[at][lane] = hi;
-            blk.tl[at][lane] = pack_lo(v[c], hi, minus_one());
+            blk.s.th[at][lane] = hi;
+            blk.s.tl[at][lane] = pack_lo(v[c], hi, minus_one());
         }
-        if (g4 == 0) blk.uf[t] = pow2(-e);
+        if (g4 == 0) blk.s.uf[t] = pow2(-e);
     }
     if (wave == 0) {
         const double all = sm.b[kC - 1], ke = double(sm.kexp[lane]);
-        blk.xf[lane] = exp_b(sm.b[lane] + ke);
-        blk.tf[lane] = exp_b(all - sm.b[lane] + ke);
-        if (lane == 0) blk.etot = exp_b(all), blk.bad = bad;
+        blk.s.xf[lane] = exp_b(sm.b[lane] + ke);
+        blk.s.tf[lane] = exp_b(all - sm.b[lane] + ke);
+        if (lane == 0) blk.s.etot = exp_b(all), blk.s.bad = bad;
     }
 }
 
@@ -377,30 +385,191 @@ __device__ __forceinline__ int column_max(int v) {
     return max(int(y[0]), int(y[1]));
 }
 
+// What the state's chain reads of a chunk, what the outputs read, and what the chain hands to the outputs.
 template <int DKP>
-struct ScanStage {
-    __attribute__((aligned(1024))) uint16_t k[kC * DKP], q[kC * DKP], v[kC * 64];
-    DeltaBlock d;
+struct ChainStage {
+    __attribute__((aligned(1024))) uint16_t k[kC * DKP], v[kC * 64];
+    StateBlock d;
+};
+template <int DKP>
+struct OutStage {
+    __attribute__((aligned(1024))) uint16_t q[kC * DKP];
+    OutBlock d;
+};
+template <int DKP>
+struct ScanSmem {
+    ChainStage<DKP> chain[2];  // of this chunk and the next
+    OutStage<DKP> out[2];      // of the chunk before and this one
+    u32x4 sh[4][DKP / 32][64], uo[4][2][64];  // of each wave: the state before the chunk, U
+    __attribute__((aligned(16))) int unit[64], from[64];  // of a column: e, first token without a number
 };
 
+// Two waves for each 16 columns of the state, on one SIMD: one has the chain from state to state, the other the
+// outputs of the chunk before it and all loads.  A wave issues an instruction every four cycles at most: in one
+// wave outputs and loads took longer than the chain, with little under the matrix cores' steps.
 template <class E, int DKP>
-__global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
+__global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
     constexpr int KS = DKP / 32;
     constexpr bool HALF = __is_same(E, F16);
-    __shared__ ScanStage<DKP> stage[2];  // of this chunk and the next
+    __shared__ ScanSmem<DKP> sm;
     const int heads = a.hv / a.hk, halves = (a.Dv + 63) / 64, group = heads * halves;
     const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * group) * 8 + id % 8;
     const int hk = int(pair % a.hk), j0 = int(id / 8 % group);
     const int h = hk * heads + j0 / halves, v0 = j0 % halves * 64, r = int(pair / a.hk);
     if (r >= a.p.R) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, both = uniform(tid >> 6), wave = both & 3;
     const int lr = lane & 15, g4 = lane >> 4;
     const int c0 = packed_row(a.p, r), n = max(0, packed_row(a.p, r + 1) - c0);
+    const int nch = (n + kC - 1) / kC;
+
+    if (both >= 4) {
+        // ---- loads and outputs.  Loads straight to LDS, 1 KB each: bases that the wave shares plus 32-bit offsets of the
+        // lanes, which stay the same from chunk to chunk.
+        constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4;
+        const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldq = 2 * (HALF ? a.ld_q : DKP), ldv = 2 * a.ld_v;  // bytes
+        const int64_t unit0 = c0 / kC + r;  // number of the request's first unit
+        const uint8_t *kp, *qp;             // of the next chunk to be loaded
+        if constexpr (HALF) {
+            kp = reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk;
+            qp = reinterpret_cast<const uint8_t*>(a.q + int64_t(hk) * a.Dk) + c0 * ldq;
+        } else {
+            kp = reinterpret_cast<const uint8_t*>(a.images + (unit0 * a.hk + hk) * (2 * kC * DKP));
+            qp = kp + kC * DKP * 2;
+        }
+        const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v + int64_t(h) * a.Dv + v0) + c0 * ldv;
+        const uint8_t *dp = a.blocks + (unit0 * a.hv + h) * kDeltaBlock, *pp = dp + sizeof(StateBlock);
+        const int64_t kstep = HALF ? kC * ldk : int64_t(a.hk) * (2 * kC * DKP) * 2, qstep = HALF ? kC * ldq : kstep;
+        const int64_t vstep = kC * ldv, dstep = int64_t(a.hv) * kDeltaBlock;
+        uint32_t koff[NI], qoff[NI], voff[2];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int row = (wave * NI + i) * RPI + lane / LPR;
+            koff[i] = uint32_t(row) * uint32_t(ldk) + 16 * uint32_t(lane % LPR ^ kkey<DKP>(row));
+            qoff[i] = uint32_t(row) * uint32_t(ldq) + 16 * uint32_t(lane % LPR ^ qkey<DKP>(row));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = (wave * 2 + i) * 8 + lane / 8;
+            voff[i] = uint32_t(row) * uint32_t(ldv) + 16 * uint32_t(lane % 8 ^ vkey(row));
+        }
+        const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(kZeros);  // rows and columns that are not there
+        const bool kwide = !HALF || a.Dk == DKP, vwide = v0 + 64 <= a.Dv;
+        auto load_chain = [&](int c) __attribute__((always_inline)) {
+            const int m = min(kC, n - c * kC);
+            const uint32_t at = lds_byte(&sm.chain[c & 1]);
+            if (__builtin_expect(kwide && vwide && m == kC, 1)) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) load_lds16(kp, koff[i], at + (wave * NI + i) * 1024);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    load_lds16(vp, voff[i], at + int(offsetof(ChainStage<DKP>, v)) + (wave * 2 + i) * 1024);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int row = (wave * NI + i) * RPI + lane / LPR, ch = lane % LPR ^ kkey<DKP>(row);
+                    load_lds16(row < m && (!HALF || 8 * ch < a.Dk) ? kp + koff[i] : zeros, at + (wave * NI + i) * 1024);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = (wave * 2 + i) * 8 + lane / 8, ch = lane % 8 ^ vkey(row);
+                    load_lds16(row < m && v0 + 8 * ch < a.Dv ? vp + voff[i] : zeros,
+                               at + int(offsetof(ChainStage<DKP>, v)) + (wave * 2 + i) * 1024);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = wave + 4 * i;
+                if (j < 13) load_lds16(dp + j * 1024, lane * 16, at + int(offsetof(ChainStage<DKP>, d)) + j * 1024);
+            }
+            kp += kstep, vp += vstep, dp += dstep;
+        };
+        auto load_out = [&](int c) __attribute__((always_inline)) {
+            const int m = min(kC, n - c * kC);
+            const uint32_t at = lds_byte(&sm.out[c & 1]);
+            if (__builtin_expect(kwide && m == kC, 1)) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) load_lds16(qp, qoff[i], at + (wave * NI + i) * 1024);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int row = (wave * NI + i) * RPI + lane / LPR, ch = lane % LPR ^ qkey<DKP>(row);
+                    load_lds16(row < m && (!HALF || 8 * ch < a.Dk) ? qp + qoff[i] : zeros, at + (wave * NI + i) * 1024);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 3 - wave + 4 * i;  // the waves that have less of the chain's
+                if (j < 7) load_lds16(pp + j * 1024, lane * 16, at + int(offsetof(OutStage<DKP>, d)) + j * 1024);
+            }
+            qp += qstep, pp += dstep;
+        };
+        uint8_t* yp = reinterpret_cast<uint8_t*>(a.y + c0 * a.ld_y + int64_t(h) * a.Dv + v0);
+        const uint32_t yoff = uint32_t(lr) * uint32_t(2 * a.ld_y) + 2 * (16 * wave + 4 * g4);
+        const int qat = lr * 2 * DKP + 16 * (g4 ^ qkey<DKP>(lr));
+        const bool inside = v0 + 16 * wave + 4 * g4 < a.Dv;
+        if (nch > 0) {
+            load_chain(0);
+            wait_loads();
+        }
+        for (int c = 0; c <= nch; ++c) {
+            __syncthreads();
+            const OutStage<DKP>& st = sm.out[c + 1 & 1];  // of chunk c - 1
+            u32x4 sh[KS], uo[2];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) uo[k] = sm.uo[wave][k][lane];
+            int unit[4], from[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unit[i] = sm.unit[16 * wave + 4 * g4 + i], from[i] = sm.from[16 * wave + 4 * g4 + i];
+            __syncthreads();  // read: the chain may write the next
+            if (c + 1 < nch) load_chain(c + 1);
+            if (c < nch) load_out(c);
+            if (c > 0) {
+                // queries 16 x + lr of columns 4 g4 + i
+                const int m = min(kC, n - (c - 1) * kC);
+                f32x4 o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        o[x] = F16::mfma16(sh[s], *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(st.q) + (qat ^ 64 * s) + 32 * x * DKP), o[x]);
+                    o[x] *= st.d.qf[16 * x + lr];
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], st.d.p[x < 2 ? x : 2 * x - 2 + k][lane], o[x]);
+                float down[4];
+                bool all = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) down[i] = pow2(-unit[i]), all &= from[i] >= kC;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float pf = st.d.pf[16 * x + lr];
+                    float z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf * down[i];
+                    if (__builtin_expect(__any(!all), 0)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[i] = 16 * x + lr >= from[i] ? __builtin_nanf("") : z[i];
+                    }
+                    if (16 * x + lr < m && inside)
+                        *reinterpret_cast<u32x2*>(yp + 32 * x * a.ld_y + yoff) = u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
+                }
+                yp += 2 * kC * a.ld_y;
+            }
+            wait_loads();
+        }
+        return;
+    }
+
+    // ---- the chain
     bool old;
     const int slot = packed_slot(a.p, r, &old);
     const int dv = v0 + 16 * wave + lr;
     const int64_t sbase = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv + dv;
-
     // state element (p, b, i): dk = 32 p + 8 g4 + 4 b + i of column dv, in units of 2^-e
     f32x4 S[KS][2];
     int e = 0;
@@ -419,123 +588,42 @@ __global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) S[p][b] *= by;
     };
-
-    // Loads straight to LDS, 1 KB each, kLoads of them a wave and chunk: bases that the wave shares plus
-    // 32-bit offsets of the lanes, which stay the same from chunk to chunk.
-    constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4, kLoads = 2 * NI + 7;
-    constexpr int kStage = sizeof(ScanStage<DKP>), kQ = offsetof(ScanStage<DKP>, q), kV = offsetof(ScanStage<DKP>, v),
-                  kD = offsetof(ScanStage<DKP>, d);
-    const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldq = 2 * (HALF ? a.ld_q : DKP), ldv = 2 * a.ld_v;  // bytes
-    const int64_t unit0 = c0 / kC + r;  // number of the request's first unit
-    const uint8_t *kp, *qp, *vp, *dp;   // of the next chunk to be loaded
-    if constexpr (HALF) {
-        kp = reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk;
-        qp = reinterpret_cast<const uint8_t*>(a.q + int64_t(hk) * a.Dk) + c0 * ldq;
-    } else {
-        kp = reinterpret_cast<const uint8_t*>(a.images + (unit0 * a.hk + hk) * (2 * kC * DKP));
-        qp = kp + kC * DKP * 2;
-    }
-    vp = reinterpret_cast<const uint8_t*>(a.v + int64_t(h) * a.Dv + v0) + c0 * ldv;
-    dp = a.blocks + (unit0 * a.hv + h) * kDeltaBlock + wave * 5120;
-    const int64_t kstep = HALF ? kC * ldk : int64_t(a.hk) * (2 * kC * DKP) * 2, qstep = HALF ? kC * ldq : kstep;
-    const int64_t vstep = kC * ldv, dstep = int64_t(a.hv) * kDeltaBlock;
-    uint32_t koff[NI], qoff[NI], voff[2];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int row = (wave * NI + i) * RPI + lane / LPR;
-        koff[i] = uint32_t(row) * uint32_t(ldk) + 16 * uint32_t(lane % LPR ^ kkey<DKP>(row));
-        qoff[i] = uint32_t(row) * uint32_t(ldq) + 16 * uint32_t(lane % LPR ^ qkey<DKP>(row));
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = (wave * 2 + i) * 8 + lane / 8;
-        voff[i] = uint32_t(row) * uint32_t(ldv) + 16 * uint32_t(lane % 8 ^ vkey(row));
-    }
-    const uint32_t lds0 = lds_byte(stage);
-    const bool wide = (!HALF || a.Dk == DKP) && v0 + 64 <= a.Dv;  // every column is there
-    // loads from .. to - 1 of a chunk of m tokens into buffer `buf`
-    auto issue = [&](int from, int to, int m, int buf) __attribute__((always_inline)) {
-        const uint32_t at = lds0 + buf * kStage;
-        if (__builtin_expect(wide && m == kC, 1)) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                if (i < from || i >= to) continue;
-                if (i < NI) load_lds16(kp, koff[i], at + (wave * NI + i) * 1024);
-                else if (i < 2 * NI) load_lds16(qp, qoff[i - NI], at + kQ + (wave * NI + i - NI) * 1024);
-                else if (i < 2 * NI + 2) load_lds16(vp, voff[i - 2 * NI], at + kV + (wave * 2 + i - 2 * NI) * 1024);
-                else load_lds16(dp + (i - 2 * NI - 2) * 1024, lane * 16, at + kD + (wave * 5 + i - 2 * NI - 2) * 1024);
-            }
-        } else {
-            // rows and columns that are not there are zeros
-            const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(kZeros);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                if (i < from || i >= to) continue;
-                if (i < 2 * NI) {
-                    const int j = i % NI, row = (wave * NI + j) * RPI + lane / LPR;
-                    const int ch = lane % LPR ^ (i < NI ? kkey<DKP>(row) : qkey<DKP>(row));
-                    const bool there = row < m && (!HALF || 8 * ch < a.Dk);
-                    if (i < NI) load_lds16(there ? kp + koff[j] : zeros, at + (wave * NI + j) * 1024);
-                    else load_lds16(there ? qp + qoff[j] : zeros, at + kQ + (wave * NI + j) * 1024);
-                } else if (i < 2 * NI + 2) {
-                    const int j = i - 2 * NI, row = (wave * 2 + j) * 8 + lane / 8, ch = lane % 8 ^ vkey(row);
-                    load_lds16(row < m && v0 + 8 * ch < a.Dv ? vp + voff[j] : zeros, at + kV + (wave * 2 + j) * 1024);
-                } else {
-                    load_lds16(dp + (i - 2 * NI - 2) * 1024, lane * 16, at + kD + (wave * 5 + i - 2 * NI - 2) * 1024);
-                }
-            }
-        }
-    };
-    auto advance = [&]() __attribute__((always_inline)) { kp += kstep, qp += qstep, vp += vstep, dp += dstep; };
-    auto tr_read = [](const uint16_t* p) __attribute__((always_inline)) {
+    // four tokens of one column: lanes 4 i .. 4 i + 3 of 16 give the addresses of 16 columns of token i
+    auto tr_read = [](const uint8_t* p) __attribute__((always_inline)) {
         return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p)));
+            (__attribute__((address_space(3))) s16x4*)const_cast<uint8_t*>(p)));
     };
-
-    const int nch = (n + kC - 1) / kC;
-    if (nch > 0) {
-        issue(0, kLoads, min(kC, n), 0);
-        advance();
-        wait_loads();
-    }
-    uint8_t* yp = reinterpret_cast<uint8_t*>(a.y + c0 * a.ld_y + int64_t(h) * a.Dv + v0);
-    const uint32_t yoff = uint32_t(lr) * uint32_t(2 * a.ld_y) + 2 * (16 * wave + 4 * g4);
-    const bool out = v0 + 16 * wave + 4 * g4 < a.Dv;
+    // Where a lane reads K by rows (pair_row of a tile), K by columns and V: the swizzles do not depend on the tile,
+    // so that tiles are constants away, or an exclusive or with a multiple of 64.
+    const int krow = pair_row(lr, 0), trow = 8 * g4 + lr / 4;
+    const int kat = krow * 2 * DKP + 16 * (g4 ^ kkey<DKP>(krow));
+    const int tat = trow * 2 * DKP + 16 * (lr % 4 ^ kkey<DKP>(trow));
+    const int vat = trow * 128 + 16 * ((2 * wave + lr % 4 / 2) ^ vkey(trow)) + lr % 2 * 8;
     const float minus = minus_one();
     bool lost = false;  // the column has met something that is not finite
     for (int c = 0; c < nch; ++c) {
-        __syncthreads();  // this chunk's loads, which every wave has waited for; the other buffer's readers
-        const ScanStage<DKP>& st = stage[c & 1];
-        const int m = min(kC, n - c * kC), left = n - (c + 1) * kC;
-        auto part = [&](int from, int to) __attribute__((always_inline)) {
-            if (left > 0) issue(from, to, min(kC, left), c + 1 & 1);
-        };
-
+        __syncthreads();  // this chunk's loads are there
+        const ChainStage<DKP>& st = sm.chain[c & 1];
+        const uint8_t* const kb = reinterpret_cast<const uint8_t*>(st.k);
         // values: token 32 p + 8 g4 + 4 b + i of the lane's column
         u32x2 vb[2][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int row = 32 * p + 8 * g4 + 4 * b + lr / 4, ch = 2 * wave + lr % 4 / 2;
-                vb[p][b] = tr_read(st.v + row * 64 + 8 * (ch ^ vkey(row)) + lr % 2 * 4);
-            }
+            for (int b = 0; b < 2; ++b) vb[p][b] = tr_read(reinterpret_cast<const uint8_t*>(st.v) + vat + (32 * p + 4 * b) * 128);
         u32x4 kf[KS][2][2];
-        auto read_k = [&]() __attribute__((always_inline)) {
+        auto read_k = [&](int s0, int s1) __attribute__((always_inline)) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
+            for (int s = s0; s < s1; ++s)
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int row = 32 * p + pair_row(lr, b);
-                        kf[s][p][b] = *reinterpret_cast<const u32x4*>(st.k + row * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(row)));
-                    }
+                    for (int b = 0; b < 2; ++b)
+                        kf[s][p][b] = *reinterpret_cast<const u32x4*>(kb + (kat ^ 64 * s) + (32 * p + 4 * b) * 2 * DKP);
         };
-        read_k();
+        read_k(0, 2);
         int late = st.d.bad;  // first token that the column gets no number from
-        __builtin_amdgcn_sched_barrier(0);  // all on their way
-        part(0, NI + 2);
+        __syncthreads();  // the outputs' waves have taken the chunk before
         // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
         float big = 0.f;
 #pragma unroll
@@ -585,6 +673,7 @@ __global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
                 sh[s] = pack_hi(x);
                 sl[s] = pack_lo(x, sh[s], minus);
             }
+            if constexpr (KS > 2) read_k(2, KS);
             const float unit = pow2(e);
             f32x4 acc[2][2], xf[2][2];
 #pragma unroll
@@ -659,31 +748,22 @@ __global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
             if (__builtin_expect(!__any(move), 1) || again == 12) break;
             move = column_max(move);
             to = max(e - 10, -120);
-            read_k();
+            read_k(0, 2);
         }
-
-        // outputs: queries 16 x + lr of columns 4 g4 + i
-        u32x4 qr[4][KS], pr[6], kt[KS][2][2];
+        u32x4 kt[2][KS][2];
+        auto read_kt = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
+            for (int p = 0; p < KS; ++p)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int row = 16 * y + lr;
-                qr[y][s] = *reinterpret_cast<const u32x4*>(st.q + row * DKP + 8 * ((4 * s + g4) ^ qkey<DKP>(row)));
-            }
+                for (int b = 0; b < 2; ++b) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i) pr[i] = st.d.p[i][lane];
-        __builtin_amdgcn_sched_barrier(0);
-        part(NI + 2, 2 * NI);
-        f32x4 o[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[y] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[y] = F16::mfma16(sh[s], qr[y][s], o[y]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[y] *= st.d.qf[16 * y + lr];
+                    for (int z = 0; z < 2; ++z) {
+                        const u32x2 w = tr_read(kb + (tat ^ 64 * p) + (32 * k + 4 * z) * 2 * DKP + 8 * b);
+                        kt[k][p][b][2 * z] = w[0], kt[k][p][b][2 * z + 1] = w[1];
+                    }
+                }
+        };
+        read_kt(0);
         u32x4 uo[2], uh[2], ul[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -699,29 +779,14 @@ __global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
             ul[p] = pack_lo(x, uh[p], minus);
         }
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
+        for (int s = 0; s < KS; ++s) sm.sh[wave][s][lane] = sh[s];
 #pragma unroll
-            for (int k = 0; k <= y / 2; ++k) o[y] = F16::mfma16(uo[k], pr[y < 2 ? y : 2 * y - 2 + k], o[y]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int p = 0; p < KS; ++p)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int row = 32 * k + 8 * g4 + 4 * z + lr / 4;
-                        const u32x2 w = tr_read(st.k + row * DKP + 8 * ((4 * p + lr % 4) ^ kkey<DKP>(row)) + 4 * b);
-                        kt[p][b][k][2 * z] = w[0], kt[p][b][k][2 * z + 1] = w[1];
-                    }
-                }
-        __builtin_amdgcn_sched_barrier(0);
-        part(2 * NI, kLoads);
-        advance();
-        // the state
-        const bool was = lost;
+        for (int k = 0; k < 2; ++k) sm.uo[wave][k][lane] = uo[k];
+        if (g4 == 0) sm.unit[16 * wave + lr] = e, sm.from[16 * wave + lr] = lost ? 0 : late;
         lost |= late < kC;
         scale_state(lost ? __builtin_nanf("") : st.d.etot);
+        read_kt(1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -729,29 +794,10 @@ __global__ void __launch_bounds__(256, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
                 for (int p = 0; p < KS; ++p)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) S[p][b] = F16::mfma16(kt[p][b][k], z ? uh[k] : ul[k], S[p][b]);
-        float down[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) down[i] = pow2(-__shfl(e, 4 * g4 + i));
-        wait_loads();  // the next chunk's; before the stores, which need not be waited for
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[y] *= st.d.pf[16 * y + lr];
-        if (__builtin_expect(__any(lost), 0)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int from = __shfl(was ? 0 : late, 4 * g4 + i);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) o[y][i] = 16 * y + lr >= from ? __builtin_nanf("") : o[y][i];
-            }
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            if (16 * y + lr < m && out)
-                *reinterpret_cast<u32x2*>(yp + 32 * y * a.ld_y + yoff) =
-                    u32x2{pack16<E>(o[y][0] * down[0], o[y][1] * down[1]), pack16<E>(o[y][2] * down[2], o[y][3] * down[3])};
-        }
-        yp += 2 * kC * a.ld_y;
+                    for (int b = 0; b < 2; ++b) S[p][b] = F16::mfma16(kt[k][p][b], z ? uh[k] : ul[k], S[p][b]);
     }
+    __syncthreads();
+    __syncthreads();
     if (slot >= 0 && dv < a.Dv) {
         const float by = pow2(-e);
 #pragma unroll
@@ -775,7 +821,7 @@ void launch(DeltaArgs a, hipStream_t s) {
         k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a);
     const int64_t scan = (int64_t(a.p.R) * a.hk + 7) / 8 * 8 * heads * halves;
     for (a.id0 = 0; a.id0 < scan; a.id0 += most)
-        k_delta_scan<E, DKP><<<unsigned(std::min(most, scan - a.id0)), 256, 0, s>>>(a);
+        k_delta_scan<E, DKP><<<unsigned(std::min(most, scan - a.id0)), 512, 0, s>>>(a);
 }
 
 }  // namespace
