@@ -24,6 +24,6 @@ struct DeltaArgs {
 
 // Chunks of 64 tokens on the matrix cores; units = T / 64 + R + 1.
 template <class E>
-void launch_delta_chunks(const DeltaArgs& a, hipStream_t s);
+void launch_delta_chunks(const DeltaArgs& a, int cus, hipStream_t s);
 
 }  // namespace vqmlp

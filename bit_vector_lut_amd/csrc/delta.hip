@@ -240,8 +240,8 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
         if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
         else launch_step<BF16>(a, cus, s);
     } else {
-        if (d.dtype == VQMLP_F16) launch_delta_chunks<F16>(a, s);
-        else launch_delta_chunks<BF16>(a, s);
+        if (d.dtype == VQMLP_F16) launch_delta_chunks<F16>(a, cus, s);
+        else launch_delta_chunks<BF16>(a, cus, s);
     }
     if (trace_enabled())
         trace_line("delta_rule T=%d R=%d heads=%d/%d: %s", d.T, d.R, d.v_heads, d.k_heads, G.step ? "recurrence" : "chunks");

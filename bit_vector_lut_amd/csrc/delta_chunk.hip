@@ -132,22 +132,38 @@ __device__ __forceinline__ int bf_expo(uint32_t top) {
 
 template <int DKP>
 struct PrepSmem {
-    __attribute__((aligned(256))) uint16_t k[kC * DKP];
-    float A[kC][kC + 4], T[kC][kC + 4];
-    double b[kC];
+    union {
+        __attribute__((aligned(256))) uint16_t k[kC * DKP];
+        __attribute__((aligned(256))) float AT[2][kC][kC + 4];  // A and T of a value head
+    };
+    float b[kC], lo[kC];  // b log2 e and what it lost in rounding
     float beta[kC];
     int kexp[kC];
-    int bad;
+    int kbad, bad;  // first token with something not finite in k; or in g or beta
 };
 
+// c ? v : 0 without a branch around what made v
+__device__ __forceinline__ float only(bool c, float v) {
+    asm("" : "+v"(v));
+    return c ? v : 0.f;
+}
+
+// 2^(b_t - b_j + e) from the two parts of the b's
+__device__ __forceinline__ float decayed(float bt, float lt, float bj, float lj, int e) {
+    return __builtin_amdgcn_exp2f((bt - bj) + (lt - lj) + float(e));
+}
+
+// A workgroup makes the blocks of `per` value heads that share a key head: K K^T and Q K^T are theirs together.
+// Tiles of 16 x 16: each wave has one on the diagonal of A and one or two of the six below.
 template <class E, int DKP>
-__global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
+__global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
     constexpr int KS = DKP / 32;
     constexpr bool HALF = __is_same(E, F16);
     __shared__ PrepSmem<DKP> sm;
-    const int heads = a.hv / a.hk;
-    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * heads) * 8 + id % 8;
-    const int hk = int(pair % a.hk), h = hk * heads + int(id / 8 % heads);
+    float (*const A)[kC + 4] = sm.AT[0], (*const T)[kC + 4] = sm.AT[1];
+    const int heads = a.hv / a.hk, parts = heads / per;
+    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * parts) * 8 + id % 8;
+    const int hk = int(pair % a.hk), h0 = hk * heads + int(id / 8 % parts) * per;
     const int x = int(pair / a.hk);
     PackedUnit u;
     if (!packed_unit(a.p, kC, x, u)) return;
@@ -156,20 +172,18 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
     const int64_t t0 = u.c0 + int64_t(u.seg) * kC;
     const int m = min(kC, u.n - u.seg * kC);
     if (u.r == a.p.R) {  // rows behind the last request
-        for (int i = tid; i < m * (a.Dv / 8); i += 256)
-            *reinterpret_cast<u32x4*>(a.y + (t0 + i / (a.Dv / 8)) * a.ld_y + int64_t(h) * a.Dv + i % (a.Dv / 8) * 8) =
-                u32x4{0, 0, 0, 0};
+        const int row = per * a.Dv / 8;
+        for (int i = tid; i < m * row; i += 256)
+            *reinterpret_cast<u32x4*>(a.y + (t0 + i / row) * a.ld_y + int64_t(h0) * a.Dv + i % row * 8) = u32x4{0, 0, 0, 0};
         return;
     }
     if (m <= 0) return;
-    DeltaBlock& blk = reinterpret_cast<DeltaBlock*>(a.blocks)[int64_t(x) * a.hv + h];
     uint16_t* const image = HALF ? nullptr : a.images + (int64_t(x) * a.hk + hk) * (2 * kC * DKP);
-    const bool first = h % heads == 0;
+    const bool first = h0 % heads == 0;
     const u32x4 none = {0, 0, 0, 0};
 
     // keys
     constexpr int LPR = DKP / 8, RPP = 256 / LPR;
-    if (tid == 0) sm.bad = kC;
     u32x4 kr[kC / RPP];
     const int kc = tid % LPR;
 #pragma unroll
@@ -177,11 +191,6 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
         const int r = i * RPP + tid / LPR;
         kr[i] = none;
         if (r < m && 8 * kc < a.Dk) kr[i] = *reinterpret_cast<const u32x4*>(a.k + (t0 + r) * a.ld_k + int64_t(hk) * a.Dk + 8 * kc);
-    }
-    float gv = 0.f, bv = 0.f;
-    if (tid < m) {
-        gv = bounded(a.g[(t0 + tid) * a.ld_g + h]);
-        bv = a.beta[(t0 + tid) * a.ld_b + h];
     }
     // this wave's 16 queries
     u32x4 qf[KS];
@@ -191,8 +200,16 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
         qf[s] = none;
         if (16 * wave + lr < m && 32 * s + 8 * g4 < a.Dk)
             qf[s] = *reinterpret_cast<const u32x4*>(a.q + (t0 + 16 * wave + lr) * a.ld_q + int64_t(hk) * a.Dk + 32 * s + 8 * g4);
-        if constexpr (!HALF) qtop = max(qtop, top8(qf[s]));
     }
+    float gv = 0.f, bv = 0.f;  // of token `lane` of the next head (wave 0)
+    auto gates = [&](int h) __attribute__((always_inline)) {
+        if (wave == 0 && lane < m) {
+            gv = a.g[(t0 + lane) * a.ld_g + h];
+            bv = a.beta[(t0 + lane) * a.ld_b + h];
+        }
+    };
+    gates(h0);
+    if (tid == 0) sm.kbad = kC;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kC / RPP; ++i) {
@@ -205,14 +222,14 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
             kr[i] = to_half(kr[i], pow2(-e));
             if (kc == 0) sm.kexp[r] = e;
             if (first) *reinterpret_cast<u32x4*>(image + r * DKP + 8 * kc) = kr[i];
-        } else if (kc == 0) {
-            sm.kexp[r] = 0;
         }
-        if (top >= kInf16<E>) atomicMin(&sm.bad, r);
+        if (top >= kInf16<E>) atomicMin(&sm.kbad, r);
         *reinterpret_cast<u32x4*>(&sm.k[r * DKP + 8 * (kc ^ kkey<DKP>(r))]) = kr[i];
     }
     int qe = 0;
     if constexpr (!HALF) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qtop = max(qtop, top8(qf[s]));
         // the lanes of a row are 16 apart
         qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 16)));
         qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 32)));
@@ -223,154 +240,198 @@ __global__ void __launch_bounds__(256) k_delta_prep(DeltaArgs a) {
             if (first) *reinterpret_cast<u32x4*>(image + kC * DKP + (16 * wave + lr) * DKP + 32 * s + 8 * g4) = qf[s];
         }
     }
-    if (wave == 0) {
-        if (!(fabsf(gv) < __builtin_inff() && fabsf(bv) < __builtin_inff())) atomicMin(&sm.bad, lane);
-        // sums in FP64: behind strong decays b reaches thousands, and T and P take differences of neighbours
-        sm.b[lane] = lane_scan(double(gv) * 1.4426950408889634, 0., [](double p, double q) { return p + q; });
-        sm.beta[lane] = bv;
-    }
     __syncthreads();
-    const int bad = sm.bad;
+    const int kbad = sm.kbad;
     auto k_read = [&](int r, int s) {
         return *reinterpret_cast<const u32x4*>(&sm.k[r * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(r))]);
     };
+    // K K^T: tile (wave, wave), then (1, 0) and (3, 1); (2, 0) and (3, 2); (2, 1); (3, 0)
+    const int bi[3] = {wave, wave == 0 ? 1 : wave == 3 ? 3 : 2, 3}, bj[3] = {wave, wave == 2 ? 1 : 0, wave + 1};
+    f32x4 kk[3];
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+        kk[z] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (z == 2 && wave > 1) continue;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kk[z] = F16::mfma16(k_read(16 * bi[z] + lr, s), k_read(16 * bj[z] + lr, s), kk[z]);
+    }
+    // K Q^T of this wave's queries: a lane has eight neighbouring keys of one query
+    f32x4 qk[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            qk[c][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (c > wave / 2) continue;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qk[c][b] = F16::mfma16(k_read(32 * c + pair_row(lr, b), s), qf[s], qk[c][b]);
+        }
+    __syncthreads();  // K is done with: A and T stand in its place
 
-    // A, by rows of tiles
-    {
-        u32x4 kf[KS];
+#pragma unroll 1
+    for (int h = h0; h < h0 + per; ++h) {
+        const int lane = fresh(tid & 63), lr = lane & 15, g4 = lane >> 4;  // no addresses kept over the loop
+        DeltaBlock& blk = reinterpret_cast<DeltaBlock*>(a.blocks)[int64_t(x) * a.hv + h];
+        if (wave == 0) {
+            const float g = lane < m ? bounded(gv) : 0.f, beta = lane < m ? bv : 0.f;
+            const uint64_t odd = __ballot(!(fabsf(g) < __builtin_inff() && fabsf(beta) < __builtin_inff()));
+            const int bad = min(kbad, odd ? __builtin_ctzll(odd) : kC);
+            // sums in FP64: behind strong decays b reaches thousands, and T and P take differences of neighbours
+            const double b = lane_scan(double(g) * 1.4426950408889634, 0., [](double p, double q) { return p + q; });
+            const int ke = HALF ? 0 : sm.kexp[lane];
+            const double all = __shfl(b, 63);
+            sm.b[lane] = float(b);
+            sm.lo[lane] = float(b - double(float(b)));
+            sm.beta[lane] = beta;
+            blk.s.xf[lane] = exp_b(b + double(ke));
+            blk.s.tf[lane] = exp_b(all - b + double(ke));
+            if (lane == 0) sm.bad = bad, blk.s.etot = exp_b(all), blk.s.bad = bad;
+        }
+        __syncthreads();
+        if (h + 1 < h0 + per) gates(h + 1);
+        const int bad = sm.bad;
+        // A
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kf[s] = k_read(16 * wave + lr, s);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > wave) break;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) acc = F16::mfma16(kf[s], k_read(16 * j + lr, s), acc);
-            const int cj = 16 * j + lr;
-            const double bj = sm.b[cj] - double(sm.kexp[cj]);
+        for (int z = 0; z < 3; ++z) {
+            if (z == 2 && wave > 1) break;
+            const int cj = 16 * bj[z] + lr, r0 = 16 * bi[z] + 4 * g4;
+            const float bjv = sm.b[cj], lj = sm.lo[cj];
+            const f32x4 bt = *reinterpret_cast<const f32x4*>(&sm.b[r0]), lt = *reinterpret_cast<const f32x4*>(&sm.lo[r0]);
+            const f32x4 be = *reinterpret_cast<const f32x4*>(&sm.beta[r0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 16 * wave + 4 * g4 + i;
-                const float v = acc[i] * sm.beta[t] * exp_b(sm.b[t] + double(sm.kexp[t]) - bj);
-                sm.A[t][cj] = cj < t && t < bad ? v : 0.f;
+                const int t = r0 + i, e = HALF ? 0 : sm.kexp[cj] + sm.kexp[t];
+                const float v = kk[z][i] * be[i] * decayed(bt[i], lt[i], bjv, lj, e);
+                A[t][cj] = only(cj < t && t < bad, v);
             }
         }
-    }
-    // (I + A)^-1 of this wave's diagonal tile: a lane makes one column
-    {
-        float col[16];
+        __builtin_amdgcn_sched_barrier(0);
+        // (I + A)^-1 of this wave's diagonal tile: of its 4 x 4 blocks by substitution, then twice blocks of double
+        // size, D - D O D with O the blocks of A between two that D has.  A step of the FP32 products takes one row of
+        // each lane group's four, so that a result is the next product's operand.
+        {
+            f32x4 d, row[3];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = lr == i ? 1.f : 0.f;
+            for (int i = 0; i < 3; ++i) row[i] = *reinterpret_cast<const f32x4*>(&A[16 * wave + 4 * g4 + i + 1][16 * wave + 4 * g4]);
+            const f32x4 ar = *reinterpret_cast<const f32x4*>(&A[16 * wave + lr][16 * wave + 4 * g4]);
 #pragma unroll
-            for (int q = 0; q < (i + 3) / 4; ++q) {
-                const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.A[16 * wave + i][16 * wave + 4 * q]);
+            for (int i = 0; i < 4; ++i) {
+                d[i] = (lr & 3) == i ? 1.f : 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * q + j < i) v = fmaf(-r[j], col[4 * q + j], v);
+                for (int j = 0; j < i; ++j) d[i] = fmaf(-row[i - 1][j], d[j], d[i]);
             }
-            col[i] = v;
-        }
+            d *= lr / 4 == g4 ? 1.f : 0.f;
+            auto keep = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (g4 == i / 4) sm.T[16 * wave + i][16 * wave + lr] = col[i];
-    }
-    __syncthreads();
-    // the tiles below it: T_ij = -T_ii sum_m A_im T_mj.  A step of the FP32 products takes one row of each lane
-    // group's four, so that a result is the next product's operand.
-    {
-        f32x4 tc[4];
+                for (int i = 0; i < 4; ++i) T[16 * wave + 4 * g4 + i][16 * wave + lr] = d[i];
+            };
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            if (j != wave) continue;
+            for (int z = 0; z < 2; ++z) {
+                keep();
+                const f32x4 dr = *reinterpret_cast<const f32x4*>(&T[16 * wave + lr][16 * wave + 4 * g4]);
+                const bool between = z == 0 ? (lr & 4) && g4 == (lr >> 2) - 1 : lr >= 8 && g4 < 2;
+                f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tc[j][i] = sm.T[16 * j + 4 * g4 + i][16 * j + lr];
+                for (int i = 0; i < 4; ++i) x = __builtin_amdgcn_mfma_f32_16x16x4f32(between ? ar[i] : 0.f, d[i], x, 0, 0, 0);
 #pragma unroll
-            for (int i = j + 1; i < 4; ++i) {
-                f32x4 y = {0.f, 0.f, 0.f, 0.f}, z = y;
-#pragma unroll
-                for (int k = j; k < i; ++k) {
-                    const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.A[16 * i + lr][16 * k + 4 * g4]);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) y = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], tc[k][s], y, 0, 0, 0);
-                }
-                const f32x4 r = *reinterpret_cast<const f32x4*>(&sm.T[16 * i + lr][16 * i + 4 * g4]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], -y[s], z, 0, 0, 0);
-                tc[i] = z;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) sm.T[16 * i + 4 * g4 + s][16 * j + lr] = z[s];
+                for (int i = 0; i < 4; ++i) y = __builtin_amdgcn_mfma_f32_16x16x4f32(dr[i], x[i], y, 0, 0, 0);
+                d -= y;
             }
+            keep();
         }
-    }
-    // P of this wave's queries, made as K Q^T: a lane has eight neighbouring keys of one query
-    {
-        const int t = 16 * wave + lr;
-        const double bt = sm.b[t] + double(qe);
-        float p[2][8], top = 0.f;
+        __builtin_amdgcn_sched_barrier(0);
+        // P
+        {
+            const int t = 16 * wave + lr;
+            const float bt = sm.b[t], lt = sm.lo[t];
+            float p[2][8], top = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c) {
+                if (c > wave / 2) break;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                if (c <= wave / 2) {
+                for (int b = 0; b < 2; ++b) {
+                    const int j0 = 32 * c + 8 * g4 + 4 * b;
+                    const f32x4 bjv = *reinterpret_cast<const f32x4*>(&sm.b[j0]), lj = *reinterpret_cast<const f32x4*>(&sm.lo[j0]);
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) acc = F16::mfma16(k_read(32 * c + pair_row(lr, b), s), qf[s], acc);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 32 * c + 8 * g4 + 4 * b + i;
-                    const float v = acc[i] * exp_b(bt - sm.b[j] + double(sm.kexp[j]));
-                    p[c][4 * b + i] = j <= t && j < bad ? v : 0.f;
-                    top = fmaxf(top, fabsf(p[c][4 * b + i]));
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = j0 + i, e = HALF ? 0 : qe + sm.kexp[j];
+                        const float v = qk[c][b][i] * decayed(bt, lt, bjv[i], lj[i], e);
+                        p[c][4 * b + i] = only(j <= t && j < bad, v);
+                        top = fmaxf(top, fabsf(p[c][4 * b + i]));
+                    }
                 }
             }
-        top = column_max(top);
-        const int e = top > 0.f ? min(max(14 - expo(top), -60), 60) : 0;
+            top = column_max(top);
+            const int e = top > 0.f ? min(max(14 - expo(top), -60), 60) : 0;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (c > wave / 2) break;
+            for (int c = 0; c < 2; ++c) {
+                if (c > wave / 2) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[c][i] *= pow2(e);
-            blk.o.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
-        }
-        if (g4 == 0) {
-            blk.o.qf[t] = exp_b(bt + double(e));
-            blk.o.pf[t] = a.scale * pow2(-e);
-        }
-    }
-    __syncthreads();
-    // T as operands
-    {
-        const int c1 = wave / 2, t = 32 * c1 + pair_row(lr, wave & 1);
-        float v[2][8], top = 0.f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = 32 * c + 8 * g4 + i;
-                v[c][i] = j <= t && j < bad ? sm.T[t][j] * sm.beta[j] : 0.f;
-                top = fmaxf(top, fabsf(v[c][i]));
+                for (int i = 0; i < 8; ++i) p[c][i] *= pow2(e);
+                blk.o.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
             }
-        top = column_max(top);
-        const int e = top > 0.f ? min(max(13 - expo(top), -120), 100) : 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (c > c1) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] *= pow2(e);
-            const u32x4 hi = pack_hi(v[c]);
-            const int at = wave < 2 ? wave : 2 * wave - 2 + c;
-            blk.s.th[at][lane] = hi;
-            blk.s.tl[at][lane] = pack_lo(v[c], hi, minus_one());
+            if (g4 == 0) {
+                blk.o.qf[t] = decayed(bt, lt, 0.f, 0.f, e + qe);
+                blk.o.pf[t] = a.scale * pow2(-e);
+            }
         }
-        if (g4 == 0) blk.s.uf[t] = pow2(-e);
-    }
-    if (wave == 0) {
-        const double all = sm.b[kC - 1], ke = double(sm.kexp[lane]);
-        blk.s.xf[lane] = exp_b(sm.b[lane] + ke);
-        blk.s.tf[lane] = exp_b(all - sm.b[lane] + ke);
-        if (lane == 0) blk.s.etot = exp_b(all), blk.s.bad = bad;
+        __syncthreads();
+        // the tiles below: T_ij = -T_ii sum_m A_im T_mj, a column of tiles a wave
+        {
+            f32x4 tc[4];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                if (j != wave) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc[j][i] = T[16 * j + 4 * g4 + i][16 * j + lr];
+#pragma unroll
+                for (int i = j + 1; i < 4; ++i) {
+                    f32x4 y = {0.f, 0.f, 0.f, 0.f}, z = y;
+#pragma unroll
+                    for (int k = j; k < i; ++k) {
+                        const f32x4 r = *reinterpret_cast<const f32x4*>(&A[16 * i + lr][16 * k + 4 * g4]);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) y = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], tc[k][s], y, 0, 0, 0);
+                    }
+                    const f32x4 r = *reinterpret_cast<const f32x4*>(&T[16 * i + lr][16 * i + 4 * g4]);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x4f32(r[s], -y[s], z, 0, 0, 0);
+                    tc[i] = z;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) T[16 * i + 4 * g4 + s][16 * j + lr] = z[s];
+                }
+            }
+        }
+        __syncthreads();
+        // T as operands
+        {
+            const int c1 = wave / 2, t = 32 * c1 + pair_row(lr, wave & 1);
+            float v[2][8], top = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (c > c1) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = 32 * c + 8 * g4 + i;
+                    v[c][i] = only(j <= t && j < bad, T[t][j] * sm.beta[j]);
+                    top = fmaxf(top, fabsf(v[c][i]));
+                }
+            }
+            top = column_max(top);
+            const int e = top > 0.f ? min(max(13 - expo(top), -120), 100) : 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (c > c1) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] *= pow2(e);
+                const u32x4 hi = pack_hi(v[c]);
+                const int at = wave < 2 ? wave : 2 * wave - 2 + c;
+                blk.s.th[at][lane] = hi;
+                blk.s.tl[at][lane] = pack_lo(v[c], hi, minus_one());
+            }
+            if (g4 == 0) blk.s.uf[t] = pow2(-e);
+        }
+        __syncthreads();  // b and beta are read
     }
 }
 
@@ -813,12 +874,14 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
 }
 
 template <class E, int DKP>
-void launch(DeltaArgs a, hipStream_t s) {
+void launch(DeltaArgs a, int cus, hipStream_t s) {
     constexpr int64_t most = 8 << 20;  // a launch holds fewer than 2^32 threads
     const int64_t units = int64_t(a.p.T) / kC + a.p.R + 1, heads = a.hv / a.hk, halves = (a.Dv + 63) / 64;
-    const int64_t prep = (units * a.hk + 7) / 8 * 8 * heads;
+    // all value heads of a key head in one workgroup where there are enough of those
+    const int per = units * a.hk >= 2 * cus ? int(heads) : 1;
+    const int64_t prep = (units * a.hk + 7) / 8 * 8 * (heads / per);
     for (a.id0 = 0; a.id0 < prep; a.id0 += most)
-        k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a);
+        k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a, per);
     const int64_t scan = (int64_t(a.p.R) * a.hk + 7) / 8 * 8 * heads * halves;
     for (a.id0 = 0; a.id0 < scan; a.id0 += most)
         k_delta_scan<E, DKP><<<unsigned(std::min(most, scan - a.id0)), 512, 0, s>>>(a);
@@ -827,11 +890,11 @@ void launch(DeltaArgs a, hipStream_t s) {
 }  // namespace
 
 template <class E>
-void launch_delta_chunks(const DeltaArgs& a, hipStream_t s) {
-    if (a.Dk <= 64) launch<E, 64>(a, s);
-    else launch<E, 128>(a, s);
+void launch_delta_chunks(const DeltaArgs& a, int cus, hipStream_t s) {
+    if (a.Dk <= 64) launch<E, 64>(a, cus, s);
+    else launch<E, 128>(a, cus, s);
 }
-template void launch_delta_chunks<F16>(const DeltaArgs&, hipStream_t);
-template void launch_delta_chunks<BF16>(const DeltaArgs&, hipStream_t);
+template void launch_delta_chunks<F16>(const DeltaArgs&, int, hipStream_t);
+template void launch_delta_chunks<BF16>(const DeltaArgs&, int, hipStream_t);
 
 }  // namespace vqmlp
