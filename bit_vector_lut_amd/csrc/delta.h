@@ -17,12 +17,21 @@ struct DeltaArgs {
     uint8_t* blocks;   // [unit][v_heads][kDeltaBlock]
     uint16_t* images;  // [unit][k_heads][k, q][64][Dk padded] in binary16 (of bfloat16 inputs only)
     int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_b;
+    // Of segments (NULL: whole requests): [unit][v_heads][Dk][Dv] states, then [unit][v_heads][Dk][Dk] factors.
+    float* seg;
+    int64_t seg_units;
     int64_t id0;       // number of the launch's first workgroup
+    int L;             // tokens of a segment
     int hk, hv, Dk, Dv;
     float scale;
+
+    __device__ float* ends(int64_t unit, int h) const { return seg + (unit * hv + h) * Dk * Dv; }
+    __device__ float* factor(int64_t unit, int h) const {
+        return seg + seg_units * hv * Dk * Dv + (unit * hv + h) * Dk * Dk;
+    }
 };
 
-// Chunks of 64 tokens on the matrix cores; units = T / 64 + R + 1.
+// Chunks of 64 tokens on the matrix cores.
 template <class E>
 void launch_delta_chunks(const DeltaArgs& a, int cus, hipStream_t s);
 

@@ -137,17 +137,39 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
 // ---------------------------------------------------------------- host half
 
 struct DeltaGeom {
-    bool step;
-    size_t images, bytes;  // where they start; in all
+    bool step, split;
+    int L;                     // tokens of a segment
+    size_t images, seg, bytes;  // where they start; in all
+    int64_t seg_units;
 };
 
-DeltaGeom delta_geom(const vqmlp_delta_desc& d) {
+DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     DeltaGeom G{};
     G.step = d.max_q <= kStepMaxQ;
     if (G.step) return G;
+    // not split: a segment holds all T tokens, so any request fits, whatever max_q says
+    G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
+    // In segments a request's chain is walked twice, a segment's length each time, with a join between (of a chunk's
+    // time a segment) and two more launches (6 chunks' time).  A compute unit holds one workgroup of 32 columns.
+    const int most = std::max(1, std::min(d.max_q, std::max(1, d.T))), chunks = (most + kDeltaC - 1) / kDeltaC;
+    const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
+    const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32;
+    auto rounds = [&](int64_t wgs) { return double((wgs * d.v_heads + cus - 1) / cus); };
+    // whole requests: the longest, or what all give each compute unit to do and a part of the other
+    const double share = double(d.T) / kDeltaC * vs * d.v_heads / cus;
+    double best = even ? rounds(d.R * vs) * chunks : std::max<double>(chunks, share) + 0.25 * std::min<double>(chunks, share);
+    for (int n = 4; n < chunks; ++n) {
+        const int64_t per = (chunks + n - 1) / n, units = even ? d.R * per : std::max<int64_t>(d.T / (n * kDeltaC) + d.R / 2, d.R);
+        const int64_t inner = units > d.R ? units - d.R : 0;  // segments but the last; M of those but the first
+        const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + per + 6;
+        if (cost < best) best = cost, G.split = true, G.L = n * kDeltaC;
+    }
     const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
     G.bytes = G.images = units * d.v_heads * kDeltaBlock;
     if (d.dtype == VQMLP_BF16) G.bytes += units * d.k_heads * (2 * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
+    G.seg = G.bytes;
+    G.seg_units = d.T / G.L + d.R + 1;
+    if (G.split) G.bytes += size_t(G.seg_units) * d.v_heads * d.Dk * (d.Dv + d.Dk) * 4;
     return G;
 }
 
@@ -184,7 +206,9 @@ extern "C" vqmlp_status vqmlp_delta_rule_workspace(const vqmlp_delta_desc* p, si
     using namespace vqmlp;
     OP_REQUIRE(bytes, "vqmlp_delta_rule_workspace: null pointer");
     if (const vqmlp_status st = delta_check(p, "vqmlp_delta_rule_workspace")) return st;
-    *bytes = delta_geom(*p).bytes;
+    int cus = 0;
+    if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
+    *bytes = delta_geom(*p, cus).bytes;
     return op_ok();
 }
 
@@ -213,7 +237,7 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
                        "v and y be multiples of 8");
     }
     if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
-    const DeltaGeom G = delta_geom(d);
+    const DeltaGeom G = delta_geom(d, cus);
     if (G.bytes) {
         OP_REQUIRE(workspace && op_aligned(workspace, 256), "vqmlp_delta_rule: the workspace is null or not 256-byte aligned");
         if (workspace_bytes < G.bytes)
@@ -235,6 +259,9 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
     a.scale = d.scale;
     a.blocks = static_cast<uint8_t*>(workspace);
     a.images = reinterpret_cast<uint16_t*>(a.blocks + G.images);
+    a.seg = G.split ? reinterpret_cast<float*>(a.blocks + G.seg) : nullptr;
+    a.seg_units = G.seg_units;
+    a.L = G.L;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (G.step) {
         if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
@@ -244,6 +271,7 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
         else launch_delta_chunks<BF16>(a, cus, s);
     }
     if (trace_enabled())
-        trace_line("delta_rule T=%d R=%d heads=%d/%d: %s", d.T, d.R, d.v_heads, d.k_heads, G.step ? "recurrence" : "chunks");
+        trace_line("delta_rule T=%d R=%d heads=%d/%d: %s of %d tokens", d.T, d.R, d.v_heads, d.k_heads,
+                   G.step ? "recurrence" : G.split ? "segment states, join, then segments" : "chunks, segments", G.step ? 1 : G.L);
     return op_launched("vqmlp_delta_rule");
 }

@@ -60,7 +60,6 @@ __device__ __forceinline__ int kkey(int r) {
 }
 template <int DKP>
 __device__ __forceinline__ int qkey(int r) { return DKP == 64 ? (r >> 1) & 7 : r & 15; }
-__device__ __forceinline__ int vkey(int r) { return (r & 3) << 1; }
 // Row m of tile b of a pair of row tiles: a lane's four results of both are eight neighbours.
 __device__ __forceinline__ int pair_row(int m, int b) { return 8 * (m >> 2) + 4 * b + (m & 3); }
 
@@ -82,18 +81,24 @@ __device__ __forceinline__ u32x4 pack_hi(const float* x) {
     }
     return w;
 }
-// minus: -1, unknown to the compiler, which then makes a mixed multiply-add that rounds to binary16 itself.
-__device__ __forceinline__ u32x4 pack_lo(const float* x, u32x4 hi, float minus) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = pack16<F16>(fmaf(lo16<F16>(hi[i]), minus, x[2 * i]), fmaf(hi16<F16>(hi[i]), minus, x[2 * i + 1]));
-    return w;
-}
-__device__ __forceinline__ float minus_one() {
-    float m = -1.f;
-    asm("" : "+v"(m));
-    return m;
+// By mixed multiply-adds, which round to binary16 themselves: half the instructions of what the compiler makes.
+// The halves of a word are written four instructions apart and read by a matrix-core step two or more behind;
+// what they read has been read by pack_hi, which waited for it.
+__device__ __forceinline__ u32x4 pack_lo(const float* x, u32x4 hi) {
+    uint32_t a, b, c, d;
+    asm("v_fma_mixlo_f16 %0, %4, -1.0, %8 op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixlo_f16 %1, %5, -1.0, %10 op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixlo_f16 %2, %6, -1.0, %12 op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixlo_f16 %3, %7, -1.0, %14 op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixhi_f16 %0, %4, -1.0, %9 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixhi_f16 %1, %5, -1.0, %11 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixhi_f16 %2, %6, -1.0, %13 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+        "v_fma_mixhi_f16 %3, %7, -1.0, %15 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+        "s_nop 1"
+        : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+        : "v"(hi[0]), "v"(hi[1]), "v"(hi[2]), "v"(hi[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(x[4]), "v"(x[5]),
+          "v"(x[6]), "v"(x[7]));
+    return u32x4{a, b, c, d};
 }
 
 // Largest bits of eight 16-bit magnitudes
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 const u32x4 hi = pack_hi(v[c]);
                 const int at = wave < 2 ? wave : 2 * wave - 2 + c;
                 blk.s.th[at][lane] = hi;
-                blk.s.tl[at][lane] = pack_lo(v[c], hi, minus_one());
+                blk.s.tl[at][lane] = pack_lo(v[c], hi);
             }
             if (g4 == 0) blk.s.uf[t] = pow2(-e);
         }
@@ -446,10 +451,12 @@ __device__ __forceinline__ int column_max(int v) {
     return max(int(y[0]), int(y[1]));
 }
 
+constexpr int kPairs = 2, kCols = 16 * kPairs;  // pairs of waves, value columns of a workgroup
+
 // What the state's chain reads of a chunk, what the outputs read, and what the chain hands to the outputs.
 template <int DKP>
 struct ChainStage {
-    __attribute__((aligned(1024))) uint16_t k[kC * DKP], v[kC * 64];
+    __attribute__((aligned(1024))) uint16_t k[kC * DKP], v[kC * kCols];
     StateBlock d;
 };
 template <int DKP>
@@ -461,34 +468,46 @@ template <int DKP>
 struct ScanSmem {
     ChainStage<DKP> chain[2];  // of this chunk and the next
     OutStage<DKP> out[2];      // of the chunk before and this one
-    u32x4 sh[4][DKP / 32][64], uo[4][2][64];  // of each wave: the state before the chunk, U
-    __attribute__((aligned(16))) int unit[64], from[64];  // of a column: e, first token without a number
+    u32x4 sh[kPairs][DKP / 32][64], uo[kPairs][2][64];  // of each wave: the state before the chunk, U
+    __attribute__((aligned(16))) int unit[kCols], from[kCols];  // of a column: e, first token without a number
 };
 
-// Two waves for each 16 columns of the state, on one SIMD: one has the chain from state to state, the other the
+// Two waves for each 16 columns of the state: one has the chain from state to state, the other the
 // outputs of the chunk before it and all loads.  A wave issues an instruction every four cycles at most: in one
 // wave outputs and loads took longer than the chain, with little under the matrix cores' steps.
-template <class E, int DKP>
-__global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
+//
+// Segments.  Few heads and few requests leave most compute units idle, so the chunks of a request may go through
+// in segments at once.  U and the state are linear in the state before a segment, S -> M S + B: a first launch
+// (OUT false) makes of each segment but the last B, from a state of zeros and with the values, and M, from
+// a state of ones on the diagonal and without (of the first segment its end from the request's own state); then
+// k_delta_join goes through the segments, and the second launch makes the outputs of all from their states.
+template <class E, int DKP, bool OUT>
+__global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
     constexpr int KS = DKP / 32;
     constexpr bool HALF = __is_same(E, F16);
     __shared__ ScanSmem<DKP> sm;
-    const int heads = a.hv / a.hk, halves = (a.Dv + 63) / 64, group = heads * halves;
-    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * group) * 8 + id % 8;
-    const int hk = int(pair % a.hk), j0 = int(id / 8 % group);
-    const int h = hk * heads + j0 / halves, v0 = j0 % halves * 64, r = int(pair / a.hk);
-    if (r >= a.p.R) return;
-    const int tid = threadIdx.x, lane = tid & 63, both = uniform(tid >> 6), wave = both & 3;
+    const int slices = (a.Dv + kCols - 1) / kCols, all = slices + (OUT ? 0 : (a.Dk + kCols - 1) / kCols);
+    // The slices of a head are 8 apart, on one XCD, one after another.  (Not all heads of a key head: with few units
+    // that gave some XCDs more workgroups than compute units, and the launch twice the time.)
+    const int64_t id = a.id0 + blockIdx.x, pair = id / (8 * all) * 8 + id % 8;
+    const int h = int(pair % a.hv), hk = h / (a.hv / a.hk), j0 = int(id / 8 % all), x = int(pair / a.hv);
+    const int v0 = j0 % slices * kCols;
+    const bool ones = !OUT && j0 >= slices;  // columns of M
+    const int i0 = ones ? (j0 - slices) * kCols : v0;
+    PackedUnit u;
+    if (!packed_unit(a.p, a.L, x, u) || u.r >= a.p.R) return;
+    if (!OUT && (u.seg == u.nseg - 1 || (ones && u.seg == 0))) return;
+    const int tid = threadIdx.x, lane = tid & 63, both = uniform(tid >> 6), wave = both % kPairs;
     const int lr = lane & 15, g4 = lane >> 4;
-    const int c0 = packed_row(a.p, r), n = max(0, packed_row(a.p, r + 1) - c0);
+    const int c0 = u.c0 + u.seg * a.L, n = min(u.n - u.seg * a.L, a.L);
     const int nch = (n + kC - 1) / kC;
 
-    if (both >= 4) {
+    if (both >= kPairs) {
         // ---- loads and outputs.  Loads straight to LDS, 1 KB each: bases that the wave shares plus 32-bit offsets of the
         // lanes, which stay the same from chunk to chunk.
-        constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / 4;
+        constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / kPairs, NV = kC * kCols / 512 / kPairs;
         const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldq = 2 * (HALF ? a.ld_q : DKP), ldv = 2 * a.ld_v;  // bytes
-        const int64_t unit0 = c0 / kC + r;  // number of the request's first unit
+        const int64_t unit0 = u.c0 / kC + u.r + u.seg * (a.L / kC);  // number of the first chunk's block
         const uint8_t *kp, *qp;             // of the next chunk to be loaded
         if constexpr (HALF) {
             kp = reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk;
@@ -501,7 +520,7 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
         const uint8_t *dp = a.blocks + (unit0 * a.hv + h) * kDeltaBlock, *pp = dp + sizeof(StateBlock);
         const int64_t kstep = HALF ? kC * ldk : int64_t(a.hk) * (2 * kC * DKP) * 2, qstep = HALF ? kC * ldq : kstep;
         const int64_t vstep = kC * ldv, dstep = int64_t(a.hv) * kDeltaBlock;
-        uint32_t koff[NI], qoff[NI], voff[2];
+        uint32_t koff[NI], qoff[NI], voff[NV];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int row = (wave * NI + i) * RPI + lane / LPR;
@@ -509,37 +528,40 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
             qoff[i] = uint32_t(row) * uint32_t(ldq) + 16 * uint32_t(lane % LPR ^ qkey<DKP>(row));
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = (wave * 2 + i) * 8 + lane / 8;
-            voff[i] = uint32_t(row) * uint32_t(ldv) + 16 * uint32_t(lane % 8 ^ vkey(row));
+        for (int i = 0; i < NV; ++i) {
+            const int at = (wave * NV + i) * 64 + lane;
+            voff[i] = uint32_t(at / (kCols / 8)) * uint32_t(ldv) + 16 * uint32_t(at % (kCols / 8));
         }
         const uint8_t* const zeros = reinterpret_cast<const uint8_t*>(kZeros);  // rows and columns that are not there
-        const bool kwide = !HALF || a.Dk == DKP, vwide = v0 + 64 <= a.Dv;
+        const bool kwide = !HALF || a.Dk == DKP, vwide = !ones && v0 + kCols <= a.Dv;
         auto load_chain = [&](int c) __attribute__((always_inline)) {
             const int m = min(kC, n - c * kC);
             const uint32_t at = lds_byte(&sm.chain[c & 1]);
-            if (__builtin_expect(kwide && vwide && m == kC, 1)) {
+            if (__builtin_expect(kwide && m == kC, 1)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) load_lds16(kp, koff[i], at + (wave * NI + i) * 1024);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    load_lds16(vp, voff[i], at + int(offsetof(ChainStage<DKP>, v)) + (wave * 2 + i) * 1024);
             } else {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const int row = (wave * NI + i) * RPI + lane / LPR, ch = lane % LPR ^ kkey<DKP>(row);
                     load_lds16(row < m && (!HALF || 8 * ch < a.Dk) ? kp + koff[i] : zeros, at + (wave * NI + i) * 1024);
                 }
+            }
+            const uint32_t vto = at + int(offsetof(ChainStage<DKP>, v)) + wave * NV * 1024;
+            if (__builtin_expect(vwide && m == kC, 1)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = (wave * 2 + i) * 8 + lane / 8, ch = lane % 8 ^ vkey(row);
-                    load_lds16(row < m && v0 + 8 * ch < a.Dv ? vp + voff[i] : zeros,
-                               at + int(offsetof(ChainStage<DKP>, v)) + (wave * 2 + i) * 1024);
+                for (int i = 0; i < NV; ++i) load_lds16(vp, voff[i], vto + i * 1024);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int j = (wave * NV + i) * 64 + lane;
+                    const bool there = !ones && j / (kCols / 8) < m && v0 + j % (kCols / 8) * 8 < a.Dv;
+                    load_lds16(there ? vp + voff[i] : zeros, vto + i * 1024);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = wave + 4 * i;
+            for (int i = 0; i < (12 + kPairs) / kPairs; ++i) {
+                const int j = wave + kPairs * i;
                 if (j < 13) load_lds16(dp + j * 1024, lane * 16, at + int(offsetof(ChainStage<DKP>, d)) + j * 1024);
             }
             kp += kstep, vp += vstep, dp += dstep;
@@ -558,8 +580,8 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = 3 - wave + 4 * i;  // the waves that have less of the chain's
+            for (int i = 0; i < (6 + kPairs) / kPairs; ++i) {
+                const int j = kPairs - 1 - wave + kPairs * i;  // the waves that have less of the chain's first
                 if (j < 7) load_lds16(pp + j * 1024, lane * 16, at + int(offsetof(OutStage<DKP>, d)) + j * 1024);
             }
             qp += qstep, pp += dstep;
@@ -572,9 +594,18 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
             load_chain(0);
             wait_loads();
         }
+        __syncthreads();
+        if constexpr (!OUT) {
+            for (int c = 0; c < nch; ++c) {
+                if (c + 1 < nch) load_chain(c + 1);
+                wait_loads();
+                __syncthreads();
+                __syncthreads();
+            }
+            return;
+        }
         for (int c = 0; c <= nch; ++c) {
-            __syncthreads();
-            const OutStage<DKP>& st = sm.out[c + 1 & 1];  // of chunk c - 1
+            // what the chain has handed over of chunk c - 1, which stands until the next barrier
             u32x4 sh[KS], uo[2];
 #pragma unroll
             for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
@@ -583,13 +614,12 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
             int unit[4], from[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) unit[i] = sm.unit[16 * wave + 4 * g4 + i], from[i] = sm.from[16 * wave + 4 * g4 + i];
-            __syncthreads();  // read: the chain may write the next
             if (c + 1 < nch) load_chain(c + 1);
             if (c < nch) load_out(c);
+            // queries 16 x + lr of columns 4 g4 + i
+            const OutStage<DKP>& st = sm.out[c + 1 & 1];
+            f32x4 o[4];
             if (c > 0) {
-                // queries 16 x + lr of columns 4 g4 + i
-                const int m = min(kC, n - (c - 1) * kC);
-                f32x4 o[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -602,6 +632,11 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], st.d.p[x < 2 ? x : 2 * x - 2 + k][lane], o[x]);
+            }
+            wait_loads();
+            if (c < nch) __syncthreads();  // the next chunk is there for the chain; what it handed over is read
+            if (c > 0) {
+                const int m = min(kC, n - (c - 1) * kC);
                 float down[4];
                 bool all = true;
 #pragma unroll
@@ -621,16 +656,27 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
                 }
                 yp += 2 * kC * a.ld_y;
             }
-            wait_loads();
+            if (c < nch) __syncthreads();  // the chain is done with chunk c
         }
         return;
     }
 
     // ---- the chain
     bool old;
-    const int slot = packed_slot(a.p, r, &old);
-    const int dv = v0 + 16 * wave + lr;
-    const int64_t sbase = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv + dv;
+    const int slot = packed_slot(a.p, u.r, &old);
+    const int dv = i0 + 16 * wave + lr, width = ones ? a.Dk : a.Dv;
+    const bool cin = dv < width;
+    const int64_t own = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv;
+    const float* from = nullptr;  // where the columns start
+    float* to = nullptr;          // and end
+    if (!OUT) {
+        to = ones ? a.factor(u.first + u.seg, h) : a.ends(u.first + u.seg, h);
+        if (u.seg == 0 && old) from = a.sin + own;
+    } else {
+        if (u.nseg > 1) from = a.ends(u.first + (u.seg ? u.seg : u.nseg) - 1, h);
+        else if (old) from = a.sin + own;
+        if (u.seg == u.nseg - 1 && slot >= 0) to = a.sout + own;
+    }
     // state element (p, b, i): dk = 32 p + 8 g4 + 4 b + i of column dv, in units of 2^-e
     f32x4 S[KS][2];
     int e = 0;
@@ -641,7 +687,8 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int dk = 32 * p + 8 * g4 + 4 * b + i;
-                S[p][b][i] = old && dv < a.Dv && dk < a.Dk ? a.sin[sbase + int64_t(dk) * a.Dv] : 0.f;
+                S[p][b][i] = ones && dk == dv ? 1.f : 0.f;
+                if (from && cin && dk < a.Dk) S[p][b][i] = from[int64_t(dk) * width + dv];
             }
     auto scale_state = [&](float by) __attribute__((always_inline)) {
 #pragma unroll
@@ -659,32 +706,32 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
     const int krow = pair_row(lr, 0), trow = 8 * g4 + lr / 4;
     const int kat = krow * 2 * DKP + 16 * (g4 ^ kkey<DKP>(krow));
     const int tat = trow * 2 * DKP + 16 * (lr % 4 ^ kkey<DKP>(trow));
-    const int vat = trow * 128 + 16 * ((2 * wave + lr % 4 / 2) ^ vkey(trow)) + lr % 2 * 8;
-    const float minus = minus_one();
+    const int vat = trow * 2 * kCols + 32 * wave + lr % 4 * 8;
     bool lost = false;  // the column has met something that is not finite
-    for (int c = 0; c < nch; ++c) {
-        __syncthreads();  // this chunk's loads are there
-        const ChainStage<DKP>& st = sm.chain[c & 1];
-        const uint8_t* const kb = reinterpret_cast<const uint8_t*>(st.k);
-        // values: token 32 p + 8 g4 + 4 b + i of the lane's column
-        u32x2 vb[2][2];
+    // values (token 32 p + 8 g4 + 4 b + i of the lane's column) and keys of the next chunk to be worked on
+    u32x2 vb[2][2];
+    u32x4 kf[KS][2][2];
+    auto read_next = [&](const ChainStage<DKP>& st) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) vb[p][b] = tr_read(reinterpret_cast<const uint8_t*>(st.v) + vat + (32 * p + 4 * b) * 128);
-        u32x4 kf[KS][2][2];
-        auto read_k = [&](int s0, int s1) __attribute__((always_inline)) {
+            for (int b = 0; b < 2; ++b) vb[p][b] = tr_read(reinterpret_cast<const uint8_t*>(st.v) + vat + (32 * p + 4 * b) * 2 * kCols);
 #pragma unroll
-            for (int s = s0; s < s1; ++s)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        kf[s][p][b] = *reinterpret_cast<const u32x4*>(kb + (kat ^ 64 * s) + (32 * p + 4 * b) * 2 * DKP);
-        };
-        read_k(0, 2);
+                for (int b = 0; b < 2; ++b)
+                    kf[s][p][b] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(st.k) + (kat ^ 64 * s) + (32 * p + 4 * b) * 2 * DKP);
+    };
+    __syncthreads();
+    if (nch > 0) read_next(sm.chain[0]);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // as behind a chunk's last barrier: the compiler then knows of no read in flight
+    for (int c = 0; c < nch; ++c) {
+        const ChainStage<DKP>& st = sm.chain[c & 1];
+        const uint8_t* const kb = reinterpret_cast<const uint8_t*>(st.k);
         int late = st.d.bad;  // first token that the column gets no number from
-        __syncthreads();  // the outputs' waves have taken the chunk before
+        const float etot = st.d.etot;
         // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
         float big = 0.f;
 #pragma unroll
@@ -718,148 +765,193 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
         int level = max(top > 0.f ? expo(top) + e : none, big > 0.f ? expo(big) : none);
         level = column_max(level);
         bool move = level >= 11 || (level < 5 && level != none);
-        int to = min(max(e + 10 - level, -120), 100);
+        int aim = min(max(e + 10 - level, -120), 100);
         f32x4 U[2][2];
-        u32x4 sh[KS];
+        u32x4 sh[KS], uh[2], ul[2], uo[2];
+        float unit, most;
         for (int again = 0;; ++again) {
             if (__builtin_expect(__any(move), 0)) {
-                const int by = min(max(move ? to - e : 0, -126), 126);
+                const int by = min(max(move ? aim - e : 0, -126), 126);
                 scale_state(pow2(by));
                 e += by;
             }
+            unit = pow2(e);
+            most = 0.f;
+            // K S, each step's parts of S made between the steps in front of it
             u32x4 sl[KS];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            auto split = [&](int s) __attribute__((always_inline)) {
                 const float x[8] = {S[s][0][0], S[s][0][1], S[s][0][2], S[s][0][3], S[s][1][0], S[s][1][1], S[s][1][2], S[s][1][3]};
                 sh[s] = pack_hi(x);
-                sl[s] = pack_lo(x, sh[s], minus);
-            }
-            if constexpr (KS > 2) read_k(2, KS);
-            const float unit = pow2(e);
+                sl[s] = pack_lo(x, sh[s]);
+            };
             f32x4 acc[2][2], xf[2][2];
+            u32x4 th[6], tl[6];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    acc[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    xf[p][b] = *reinterpret_cast<const f32x4*>(&st.d.xf[32 * p + 8 * g4 + 4 * b]);
+                for (int b = 0; b < 2; ++b) acc[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            split(0);
+            __builtin_amdgcn_sched_barrier(0);
+            each([&](auto sc) __attribute__((always_inline)) {
+                constexpr int s = decltype(sc)::value;
+                if constexpr (s + 1 < KS) split(s + 1);
+                // T is read meanwhile
+#pragma unroll
+                for (int i = 6 * s / KS; i < 6 * (s + 1) / KS; ++i) th[i] = st.d.th[i][lane], tl[i] = st.d.tl[i][lane];
+                if constexpr (s + 1 == KS) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) xf[p][b] = *reinterpret_cast<const f32x4*>(&st.d.xf[32 * p + 8 * g4 + 4 * b]);
                 }
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) acc[p][b] = F16::mfma16(kf[s][p][b], sl[s], acc[p][b]);
+                        for (int b = 0; b < 2; ++b) acc[p][b] = F16::mfma16(kf[s][p][b], z ? sh[s] : sl[s], acc[p][b]);
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) acc[p][b] = F16::mfma16(kf[s][p][b], sh[s], acc[p][b]);
-            }
-            u32x4 th[6], tl[6];
-#pragma unroll
-            for (int i = 0; i < 6; ++i) th[i] = st.d.th[i][lane], tl[i] = st.d.tl[i][lane];
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 8; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x80, 1, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }, std::make_integer_sequence<int, KS>{});
             u32x4 rh[2], rl[2];
-            float most = 0.f;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            auto rest = [&](int p) __attribute__((always_inline)) {  // V - e^b K S of the tokens 32 p ..
                 float x[8];
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = vb[p][b][i / 2];
-                        const float v = i & 1 ? hi16<E>(w) : lo16<E>(w);
-                        x[4 * b + i] = fmaf(v, unit, -xf[p][b][i] * acc[p][b][i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = uint32_t(fresh(int(vb[p][b][i])));  // or all conversions would be kept
+                        x[4 * b + 2 * i] = fmaf(lo16<E>(w), unit, -xf[p][b][2 * i] * acc[p][b][2 * i]);
+                        x[4 * b + 2 * i + 1] = fmaf(hi16<E>(w), unit, -xf[p][b][2 * i + 1] * acc[p][b][2 * i + 1]);
                     }
                 if (__builtin_expect(any_late, 0)) {
+                    const int to = fresh(late) - 32 * p - 8 * g4;  // here, not ahead of the branch
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = 32 * p + 8 * g4 + i >= late ? 0.f : x[i];
+                    for (int i = 0; i < 8; ++i) x[i] = i >= to ? 0.f : x[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(x[i]));
                 rh[p] = pack_hi(x);
-                rl[p] = pack_lo(x, rh[p], minus);
-            }
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) U[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
+                rl[p] = pack_lo(x, rh[p]);
+            };
+            auto updates = [&](int k, int p0, int p1) __attribute__((always_inline)) {  // T times those
 #pragma unroll
                 for (int z = 0; z < 3; ++z)
 #pragma unroll
-                    for (int p = k; p < 2; ++p)
+                    for (int p = p0; p < p1; ++p)
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int at = p ? 2 + 2 * b + k : b;
                             U[p][b] = F16::mfma16(z == 0 ? tl[at] : th[at], z == 1 ? rl[k] : rh[k], U[p][b]);
                         }
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
+            };
+            auto scaled = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     U[p][b] *= *reinterpret_cast<const f32x4*>(&st.d.uf[32 * p + 8 * g4 + 4 * b]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(U[p][b][i]));
                 }
+            };
+            auto parts = [&](int p) __attribute__((always_inline)) {
+                float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
+                uo[p] = pack_hi(x);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[4 * b + i] *= tf[i];
+                }
+                uh[p] = pack_hi(x);
+                ul[p] = pack_lo(x, uh[p]);
+            };
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) U[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            rest(0);
+            __builtin_amdgcn_sched_barrier(0);
+            rest(1);
+            updates(0, 0, 2);
+#pragma unroll
+            for (int i = 0; i < 12; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
+                __builtin_amdgcn_sched_group_barrier(0x2, 4, 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            scaled(0);
+            parts(0);
+            updates(1, 1, 2);
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 2);
+                __builtin_amdgcn_sched_group_barrier(0x2, 6, 2);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            scaled(1);
+            parts(1);
             // beyond binary16: once more in larger units
             move = most >= 32768.f && e > -120;
             if (__builtin_expect(!__any(move), 1) || again == 12) break;
             move = column_max(move);
-            to = max(e - 10, -120);
-            read_k(0, 2);
+            aim = max(e - 10, -120);
+            // the keys are still there
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        kf[s][p][b] = *reinterpret_cast<const u32x4*>(kb + (kat ^ 64 * s) + (32 * p + 4 * b) * 2 * DKP);
         }
-        u32x4 kt[2][KS][2];
-        auto read_kt = [&](int k) __attribute__((always_inline)) {
+        // K^T by columns
+        u32x4 kt[2 * KS * 2];
+        auto read_kt = [&](int z) __attribute__((always_inline)) {
+            const int k = z / (2 * KS), p = z / 2 % KS, b = z & 1;
 #pragma unroll
-            for (int p = 0; p < KS; ++p)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const u32x2 w = tr_read(kb + (tat ^ 64 * p) + (32 * k + 4 * z) * 2 * DKP + 8 * b);
-                        kt[k][p][b][2 * z] = w[0], kt[k][p][b][2 * z + 1] = w[1];
-                    }
-                }
-        };
-        read_kt(0);
-        u32x4 uo[2], uh[2], ul[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
-            uo[p] = pack_hi(x);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * b + i] *= tf[i];
+            for (int y = 0; y < 2; ++y) {
+                const u32x2 w = tr_read(kb + (tat ^ 64 * p) + (32 * k + 4 * y) * 2 * DKP + 8 * b);
+                kt[z][2 * y] = w[0], kt[z][2 * y + 1] = w[1];
             }
-            uh[p] = pack_hi(x);
-            ul[p] = pack_lo(x, uh[p], minus);
+        };
+#pragma unroll
+        for (int z = 0; z < 2 * KS; ++z) read_kt(z);
+        __syncthreads();  // the next chunk is there; the outputs' waves have taken what was handed over
+        if constexpr (OUT) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) sm.sh[wave][s][lane] = sh[s];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) sm.uo[wave][k][lane] = uo[k];
+            if (g4 == 0) sm.unit[16 * wave + lr] = e, sm.from[16 * wave + lr] = lost ? 0 : late;
         }
-#pragma unroll
-        for (int s = 0; s < KS; ++s) sm.sh[wave][s][lane] = sh[s];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) sm.uo[wave][k][lane] = uo[k];
-        if (g4 == 0) sm.unit[16 * wave + lr] = e, sm.from[16 * wave + lr] = lost ? 0 : late;
         lost |= late < kC;
-        scale_state(lost ? __builtin_nanf("") : st.d.etot);
-        read_kt(1);
+        const float keep = lost ? __builtin_nanf("") : etot;
+#pragma unroll
+        for (int z = 2 * KS; z < 4 * KS; ++z) read_kt(z);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int z = 0; z < 2 * KS; ++z) S[z / 2][z & 1] *= keep;
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+        for (int k = 0; k < 2; ++k) {
+            if (k == 1) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (c + 1 < nch) read_next(sm.chain[c + 1 & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-                for (int p = 0; p < KS; ++p)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) S[p][b] = F16::mfma16(kt[k][p][b], z ? uh[k] : ul[k], S[p][b]);
+                for (int z = 0; z < 2 * KS; ++z)
+                    S[z / 2][z & 1] = F16::mfma16(kt[2 * KS * k + z], y ? uh[k] : ul[k], S[z / 2][z & 1]);
+        }
+        __syncthreads();  // K is read
     }
-    __syncthreads();
-    __syncthreads();
-    if (slot >= 0 && dv < a.Dv) {
+    if (to && cin) {
         const float by = pow2(-e);
 #pragma unroll
         for (int p = 0; p < KS; ++p)
@@ -868,23 +960,92 @@ __global__ void __launch_bounds__(512, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int dk = 32 * p + 8 * g4 + 4 * b + i;
-                    if (dk < a.Dk) a.sout[sbase + int64_t(dk) * a.Dv] = S[p][b][i] * by;
+                    if (dk < a.Dk) to[int64_t(dk) * width + dv] = S[p][b][i] * by;
                 }
+    }
+}
+
+// The states in front of a request's segments, S_{g+1} = M_g S_g + B_g, in FP32.  A workgroup owns 16 columns, a wave
+// two tiles of 16 rows; a step of the products takes one row of each lane group's four, so that a result goes to
+// the next product as it stands, through LDS to the other waves.  The next M is on its way meanwhile.  S_{g+1} takes
+// the place of B_g; the place of the last segment, which has no B, gets the first state, since the second
+// launch may write the request's slot before a segment would read it.
+template <int DKP>
+__global__ void __launch_bounds__(32 * (DKP / 16)) k_delta_join(DeltaArgs a) {
+    constexpr int NT = DKP / 16;
+    __shared__ f32x4 sm[2][NT][64];  // S_g by tiles
+    const int r = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int lr = lane & 15, g4 = lane >> 4;
+    const int c0 = packed_row(a.p, r), n = max(0, packed_row(a.p, r + 1) - c0), nseg = (n + a.L - 1) / a.L;
+    if (nseg <= 1) return;
+    const int64_t first = c0 / a.L + r;
+    const int dv = blockIdx.z * 16 + lr;
+    bool old;
+    const int slot = packed_slot(a.p, r, &old);
+    f32x4 m[2][NT], B[2];
+    auto rows = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int dk = 16 * (2 * wave + t) + 4 * g4 + i;
+                f(t, i, int64_t(dk) * a.Dv + dv, dv < a.Dv && dk < a.Dk);
+            }
+    };
+    auto load = [&](int g) __attribute__((always_inline)) {
+        const float *const src = a.ends(first + g, h), *const M = a.factor(first + g, h);
+        rows([&](int t, int i, int64_t at, bool in) { B[t][i] = in ? src[at] : 0.f; });
+        if (g == 0) return;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                const int row = 16 * (2 * wave + t) + lr, col = 16 * k + 4 * g4;
+                m[t][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (row < a.Dk && col < a.Dk) m[t][k] = *reinterpret_cast<const f32x4*>(M + int64_t(row) * a.Dk + col);
+            }
+    };
+    load(0);
+    const float* const src = a.sin + (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv;
+    float* const last = a.ends(first + nseg - 1, h);
+    rows([&](int, int, int64_t at, bool in) { if (in) last[at] = old ? src[at] : 0.f; });
+    for (int g = 0; g + 2 < nseg; ++g) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sm[g & 1][2 * wave + t][lane] = B[t];
+        load(g + 1);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            const f32x4 s = sm[g & 1][k][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) B[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[t][k][i], s[i], B[t], 0, 0, 0);
+        }
+        float* const dst = a.ends(first + g + 1, h);
+        rows([&](int t, int i, int64_t at, bool in) { if (in) dst[at] = B[t][i]; });
     }
 }
 
 template <class E, int DKP>
 void launch(DeltaArgs a, int cus, hipStream_t s) {
     constexpr int64_t most = 8 << 20;  // a launch holds fewer than 2^32 threads
-    const int64_t units = int64_t(a.p.T) / kC + a.p.R + 1, heads = a.hv / a.hk, halves = (a.Dv + 63) / 64;
+    const int64_t units = int64_t(a.p.T) / kC + a.p.R + 1, heads = a.hv / a.hk, slices = (a.Dv + kCols - 1) / kCols;
     // all value heads of a key head in one workgroup where there are enough of those
     const int per = units * a.hk >= 2 * cus ? int(heads) : 1;
     const int64_t prep = (units * a.hk + 7) / 8 * 8 * (heads / per);
     for (a.id0 = 0; a.id0 < prep; a.id0 += most)
         k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a, per);
-    const int64_t scan = (int64_t(a.p.R) * a.hk + 7) / 8 * 8 * heads * halves;
-    for (a.id0 = 0; a.id0 < scan; a.id0 += most)
-        k_delta_scan<E, DKP><<<unsigned(std::min(most, scan - a.id0)), 512, 0, s>>>(a);
+    const int64_t segs = int64_t(a.p.T) / a.L + a.p.R + 1;
+    const int64_t scans = (segs * a.hv + 7) / 8 * 8;
+    if (a.seg) {
+        const int64_t most1 = scans * (slices + (a.Dk + kCols - 1) / kCols);
+        for (a.id0 = 0; a.id0 < most1; a.id0 += most)
+            k_delta_scan<E, DKP, false><<<unsigned(std::min(most, most1 - a.id0)), 128 * kPairs, 0, s>>>(a);
+        k_delta_join<DKP><<<dim3(a.p.R, a.hv, (a.Dv + 15) / 16), 32 * (DKP / 16), 0, s>>>(a);
+    }
+    for (a.id0 = 0; a.id0 < scans * slices; a.id0 += most)
+        k_delta_scan<E, DKP, true><<<unsigned(std::min(most, scans * slices - a.id0)), 128 * kPairs, 0, s>>>(a);
 }
 
 }  // namespace
