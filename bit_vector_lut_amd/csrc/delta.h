@@ -15,7 +15,7 @@ struct DeltaArgs {
     float* sout;
     Packed p;
     uint8_t* blocks;   // [unit][v_heads][kDeltaBlock]
-    uint16_t* images;  // [unit][k_heads][k, q][64][Dk padded] in binary16 (of bfloat16 inputs only)
+    uint16_t* images;  // [unit][k_heads] queries in binary16 as operands, of bfloat16 inputs also keys, [64][Dk padded] each
     int64_t ld_q, ld_k, ld_v, ld_y, ld_g, ld_b;
     // Of segments (NULL: whole requests): [unit][v_heads][Dk][Dv] states, then [unit][v_heads][Dk][Dk] factors.
     float* seg;
@@ -25,6 +25,9 @@ struct DeltaArgs {
     int hk, hv, Dk, Dv;
     float scale;
 
+    __device__ uint16_t* image(int64_t unit, int head, int dkp, bool half) const {
+        return images + (unit * hk + head) * ((half ? 1 : 2) * kDeltaC * dkp);
+    }
     __device__ float* ends(int64_t unit, int h) const { return seg + (unit * hv + h) * Dk * Dv; }
     __device__ float* factor(int64_t unit, int h) const {
         return seg + seg_units * hv * Dk * Dv + (unit * hv + h) * Dk * Dk;

@@ -150,23 +150,23 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
     // In segments a request's chain is walked twice, a segment's length each time, with a join between (of a chunk's
-    // time a segment) and two more launches (6 chunks' time).  A compute unit holds one workgroup of 32 columns.
+    // time a segment) and two more launches (6 chunks' time).  A compute unit holds two workgroups of 32 columns.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T))), chunks = (most + kDeltaC - 1) / kDeltaC;
     const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
-    const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32;
-    auto rounds = [&](int64_t wgs) { return double((wgs * d.v_heads + cus - 1) / cus); };
+    const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32, slots = cus;
+    auto rounds = [&](int64_t wgs) { return double((wgs * d.v_heads + slots - 1) / slots); };
     // whole requests: the longest, or what all give each compute unit to do and a part of the other
-    const double share = double(d.T) / kDeltaC * vs * d.v_heads / cus;
+    const double share = double(d.T) / kDeltaC * vs * d.v_heads / slots;
     double best = even ? rounds(d.R * vs) * chunks : std::max<double>(chunks, share) + 0.25 * std::min<double>(chunks, share);
     for (int n = 4; n < chunks; ++n) {
         const int64_t per = (chunks + n - 1) / n, units = even ? d.R * per : std::max<int64_t>(d.T / (n * kDeltaC) + d.R / 2, d.R);
         const int64_t inner = units > d.R ? units - d.R : 0;  // segments but the last; M of those but the first
-        const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + per + 6;
+        const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + 1.6 * per + 6;
         if (cost < best) best = cost, G.split = true, G.L = n * kDeltaC;
     }
     const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
     G.bytes = G.images = units * d.v_heads * kDeltaBlock;
-    if (d.dtype == VQMLP_BF16) G.bytes += units * d.k_heads * (2 * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
+    G.bytes += units * d.k_heads * ((d.dtype == VQMLP_BF16 ? 2 : 1) * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
     G.seg = G.bytes;
     G.seg_units = d.T / G.L + d.R + 1;
     if (G.split) G.bytes += size_t(G.seg_units) * d.v_heads * d.Dk * (d.Dv + d.Dk) * 4;

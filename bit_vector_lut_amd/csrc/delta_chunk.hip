@@ -58,8 +58,6 @@ template <int DKP>
 __device__ __forceinline__ int kkey(int r) {
     return DKP == 64 ? (r & 2) << 1 | (r >> 3 & 1) | (r >> 3 & 2) : (r & 3) << 2 | (r >> 3 & 3);
 }
-template <int DKP>
-__device__ __forceinline__ int qkey(int r) { return DKP == 64 ? (r >> 1) & 7 : r & 15; }
 // Row m of tile b of a pair of row tiles: a lane's four results of both are eight neighbours.
 __device__ __forceinline__ int pair_row(int m, int b) { return 8 * (m >> 2) + 4 * b + (m & 3); }
 
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
         return;
     }
     if (m <= 0) return;
-    uint16_t* const image = HALF ? nullptr : a.images + (int64_t(x) * a.hk + hk) * (2 * kC * DKP);
+    uint16_t* const image = a.image(x, hk, DKP, HALF);
     const bool first = h0 % heads == 0;
     const u32x4 none = {0, 0, 0, 0};
 
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             const int e = bf_expo(top);
             kr[i] = to_half(kr[i], pow2(-e));
             if (kc == 0) sm.kexp[r] = e;
-            if (first) *reinterpret_cast<u32x4*>(image + r * DKP + 8 * kc) = kr[i];
+            if (first) *reinterpret_cast<u32x4*>(image + kC * DKP + r * DKP + 8 * kc) = kr[i];
         }
         if (top >= kInf16<E>) atomicMin(&sm.kbad, r);
         *reinterpret_cast<u32x4*>(&sm.k[r * DKP + 8 * (kc ^ kkey<DKP>(r))]) = kr[i];
@@ -240,10 +238,11 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
         qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 32)));
         qe = bf_expo(qtop);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qf[s] = to_half(qf[s], pow2(-qe));
-            if (first) *reinterpret_cast<u32x4*>(image + kC * DKP + (16 * wave + lr) * DKP + 32 * s + 8 * g4) = qf[s];
-        }
+        for (int s = 0; s < KS; ++s) qf[s] = to_half(qf[s], pow2(-qe));
+    }
+    if (first) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) *reinterpret_cast<u32x4*>(image + ((wave * KS + s) * 64 + lane) * 8) = qf[s];
     }
     __syncthreads();
     const int kbad = sm.kbad;
@@ -460,17 +459,24 @@ struct ChainStage {
     StateBlock d;
 };
 template <int DKP>
-struct OutStage {
-    __attribute__((aligned(1024))) uint16_t q[kC * DKP];
-    OutBlock d;
-};
-template <int DKP>
 struct ScanSmem {
     ChainStage<DKP> chain[2];  // of this chunk and the next
-    OutStage<DKP> out[2];      // of the chunk before and this one
     u32x4 sh[kPairs][DKP / 32][64], uo[kPairs][2][64];  // of each wave: the state before the chunk, U
     __attribute__((aligned(16))) int unit[kCols], from[kCols];  // of a column: e, first token without a number
 };
+
+// Whole requests: the longest first, or a long one starts when the others are done.  Up to 64 requests.
+__device__ __forceinline__ int nth_longest(const Packed& p, int x) {
+    if (p.R > 64) return x;
+    const int lane = threadIdx.x & 63;
+    const int n = lane < p.R ? packed_row(p, lane + 1) - packed_row(p, lane) : -1;
+    int rank = 0;
+    for (int j = 0; j < p.R; ++j) {
+        const int m = __builtin_amdgcn_readlane(n, j);
+        rank += m > n || (m == n && j < lane);
+    }
+    return __builtin_ctzll(__ballot(rank == x && lane < p.R) | 1ull << 63);
+}
 
 // Two waves for each 16 columns of the state: one has the chain from state to state, the other the
 // outputs of the chunk before it and all loads.  A wave issues an instruction every four cycles at most: in one
@@ -482,7 +488,7 @@ struct ScanSmem {
 // a state of ones on the diagonal and without (of the first segment its end from the request's own state); then
 // k_delta_join goes through the segments, and the second launch makes the outputs of all from their states.
 template <class E, int DKP, bool OUT>
-__global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
+__global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
     constexpr int KS = DKP / 32;
     constexpr bool HALF = __is_same(E, F16);
     __shared__ ScanSmem<DKP> sm;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
     const bool ones = !OUT && j0 >= slices;  // columns of M
     const int i0 = ones ? (j0 - slices) * kCols : v0;
     PackedUnit u;
-    if (!packed_unit(a.p, a.L, x, u) || u.r >= a.p.R) return;
+    if (!packed_unit(a.p, a.L, a.seg || x >= a.p.R ? x : nth_longest(a.p, x), u) || u.r >= a.p.R) return;
     if (!OUT && (u.seg == u.nseg - 1 || (ones && u.seg == 0))) return;
     const int tid = threadIdx.x, lane = tid & 63, both = uniform(tid >> 6), wave = both % kPairs;
     const int lr = lane & 15, g4 = lane >> 4;
@@ -506,26 +512,19 @@ __global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
         // ---- loads and outputs.  Loads straight to LDS, 1 KB each: bases that the wave shares plus 32-bit offsets of the
         // lanes, which stay the same from chunk to chunk.
         constexpr int LPR = DKP / 8, RPI = 64 / LPR, NI = kC / RPI / kPairs, NV = kC * kCols / 512 / kPairs;
-        const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldq = 2 * (HALF ? a.ld_q : DKP), ldv = 2 * a.ld_v;  // bytes
+        const int64_t ldk = 2 * (HALF ? a.ld_k : DKP), ldv = 2 * a.ld_v;  // bytes
         const int64_t unit0 = u.c0 / kC + u.r + u.seg * (a.L / kC);  // number of the first chunk's block
-        const uint8_t *kp, *qp;             // of the next chunk to be loaded
-        if constexpr (HALF) {
-            kp = reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk;
-            qp = reinterpret_cast<const uint8_t*>(a.q + int64_t(hk) * a.Dk) + c0 * ldq;
-        } else {
-            kp = reinterpret_cast<const uint8_t*>(a.images + (unit0 * a.hk + hk) * (2 * kC * DKP));
-            qp = kp + kC * DKP * 2;
-        }
+        const uint8_t* qp = reinterpret_cast<const uint8_t*>(a.image(unit0, hk, DKP, HALF));
+        const uint8_t* kp = HALF ? reinterpret_cast<const uint8_t*>(a.k + int64_t(hk) * a.Dk) + c0 * ldk : qp + kC * DKP * 2;
         const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v + int64_t(h) * a.Dv + v0) + c0 * ldv;
         const uint8_t *dp = a.blocks + (unit0 * a.hv + h) * kDeltaBlock, *pp = dp + sizeof(StateBlock);
-        const int64_t kstep = HALF ? kC * ldk : int64_t(a.hk) * (2 * kC * DKP) * 2, qstep = HALF ? kC * ldq : kstep;
+        const int64_t qstep = int64_t(a.hk) * (HALF ? 1 : 2) * (kC * DKP * 2), kstep = HALF ? kC * ldk : qstep;
         const int64_t vstep = kC * ldv, dstep = int64_t(a.hv) * kDeltaBlock;
-        uint32_t koff[NI], qoff[NI], voff[NV];
+        uint32_t koff[NI], voff[NV];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int row = (wave * NI + i) * RPI + lane / LPR;
             koff[i] = uint32_t(row) * uint32_t(ldk) + 16 * uint32_t(lane % LPR ^ kkey<DKP>(row));
-            qoff[i] = uint32_t(row) * uint32_t(ldq) + 16 * uint32_t(lane % LPR ^ qkey<DKP>(row));
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -566,29 +565,25 @@ __global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
             }
             kp += kstep, vp += vstep, dp += dstep;
         };
-        auto load_out = [&](int c) __attribute__((always_inline)) {
-            const int m = min(kC, n - c * kC);
-            const uint32_t at = lds_byte(&sm.out[c & 1]);
-            if (__builtin_expect(kwide && m == kC, 1)) {
+        // queries and P straight to registers, as the matrix cores take them
+        u32x4 q[4][KS], p[6];
+        float qf[4], pf[4];
+        auto load_out = [&]() __attribute__((always_inline)) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) load_lds16(qp, qoff[i], at + (wave * NI + i) * 1024);
-            } else {
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int row = (wave * NI + i) * RPI + lane / LPR, ch = lane % LPR ^ qkey<DKP>(row);
-                    load_lds16(row < m && (!HALF || 8 * ch < a.Dk) ? qp + qoff[i] : zeros, at + (wave * NI + i) * 1024);
-                }
-            }
+                for (int s = 0; s < KS; ++s) q[x][s] = *reinterpret_cast<const u32x4*>(qp + ((x * KS + s) * 1024 + lane * 16));
 #pragma unroll
-            for (int i = 0; i < (6 + kPairs) / kPairs; ++i) {
-                const int j = kPairs - 1 - wave + kPairs * i;  // the waves that have less of the chain's first
-                if (j < 7) load_lds16(pp + j * 1024, lane * 16, at + int(offsetof(OutStage<DKP>, d)) + j * 1024);
+            for (int i = 0; i < 6; ++i) p[i] = *reinterpret_cast<const u32x4*>(pp + (i * 1024 + lane * 16));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                qf[x] = *reinterpret_cast<const float*>(pp + (int(offsetof(OutBlock, qf)) + (16 * x + lr) * 4));
+                pf[x] = *reinterpret_cast<const float*>(pp + (int(offsetof(OutBlock, pf)) + (16 * x + lr) * 4));
             }
             qp += qstep, pp += dstep;
         };
         uint8_t* yp = reinterpret_cast<uint8_t*>(a.y + c0 * a.ld_y + int64_t(h) * a.Dv + v0);
         const uint32_t yoff = uint32_t(lr) * uint32_t(2 * a.ld_y) + 2 * (16 * wave + 4 * g4);
-        const int qat = lr * 2 * DKP + 16 * (g4 ^ qkey<DKP>(lr));
         const bool inside = v0 + 16 * wave + 4 * g4 < a.Dv;
         if (nch > 0) {
             load_chain(0);
@@ -605,58 +600,66 @@ __global__ void __launch_bounds__(128 * kPairs, 1) k_delta_scan(DeltaArgs a) {
             return;
         }
         for (int c = 0; c <= nch; ++c) {
-            // what the chain has handed over of chunk c - 1, which stands until the next barrier
-            u32x4 sh[KS], uo[2];
-#pragma unroll
-            for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) uo[k] = sm.uo[wave][k][lane];
-            int unit[4], from[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) unit[i] = sm.unit[16 * wave + 4 * g4 + i], from[i] = sm.from[16 * wave + 4 * g4 + i];
+            // the chain's loads first: it waits for them in the middle of its chunk
             if (c + 1 < nch) load_chain(c + 1);
-            if (c < nch) load_out(c);
-            // queries 16 x + lr of columns 4 g4 + i
-            const OutStage<DKP>& st = sm.out[c + 1 & 1];
-            f32x4 o[4];
+            u32x2 y[4];
             if (c > 0) {
+                // what the chain has handed over of chunk c - 1, which stands until the next barrier
+                u32x4 sh[KS], uo[2];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
 #pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        o[x] = F16::mfma16(sh[s], *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(st.q) + (qat ^ 64 * s) + 32 * x * DKP), o[x]);
-                    o[x] *= st.d.qf[16 * x + lr];
-                }
+                for (int k = 0; k < 2; ++k) uo[k] = sm.uo[wave][k][lane];
+                typedef int i32x4 __attribute__((ext_vector_type(4)));
+                const i32x4 unit = *reinterpret_cast<const i32x4*>(&sm.unit[16 * wave + 4 * g4]);
+                const i32x4 from = *reinterpret_cast<const i32x4*>(&sm.from[16 * wave + 4 * g4]);
+                // queries 16 x + lr of columns 4 g4 + i
+                f32x4 o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(sh[s], q[x][s], o[x]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] *= qf[x];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], st.d.p[x < 2 ? x : 2 * x - 2 + k][lane], o[x]);
-            }
-            wait_loads();
-            if (c < nch) __syncthreads();  // the next chunk is there for the chain; what it handed over is read
-            if (c > 0) {
-                const int m = min(kC, n - (c - 1) * kC);
+                    for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
                 float down[4];
                 bool all = true;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) down[i] = pow2(-unit[i]), all &= from[i] >= kC;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float pf = st.d.pf[16 * x + lr];
                     float z[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf * down[i];
+                    for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf[x] * down[i];
                     if (__builtin_expect(__any(!all), 0)) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) z[i] = 16 * x + lr >= from[i] ? __builtin_nanf("") : z[i];
                     }
-                    if (16 * x + lr < m && inside)
-                        *reinterpret_cast<u32x2*>(yp + 32 * x * a.ld_y + yoff) = u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
+                    y[x] = u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
                 }
+            }
+            if (c < nch) {
+                load_out();
+                // the chain's loads, which are older than those: 16-byte loads of one wave cannot be made fewer
+                asm volatile("s_waitcnt vmcnt(%0)" :: "n"(4 * KS + 6) : "memory");
+                __syncthreads();  // the next chunk is there for the chain; what it handed over is read
+            }
+            if (c > 0) {
+                const int m = min(kC, n - (c - 1) * kC);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (16 * x + lr < m && inside) *reinterpret_cast<u32x2*>(yp + 32 * x * a.ld_y + yoff) = y[x];
                 yp += 2 * kC * a.ld_y;
             }
-            if (c < nch) __syncthreads();  // the chain is done with chunk c
+            if (c < nch) {
+                __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), known to the compiler: later it would wait for the chain's loads too
+                __syncthreads();  // the chain is done with chunk c
+            }
         }
         return;
     }
