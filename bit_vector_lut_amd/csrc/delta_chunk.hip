@@ -599,67 +599,69 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             }
             return;
         }
-        for (int c = 0; c <= nch; ++c) {
-            // the chain's loads first: it waits for them in the middle of its chunk
-            if (c + 1 < nch) load_chain(c + 1);
-            u32x2 y[4];
-            if (c > 0) {
-                // what the chain has handed over of chunk c - 1, which stands until the next barrier
-                u32x4 sh[KS], uo[2];
+        u32x2 y[4];
+        auto outputs = [&]() __attribute__((always_inline)) {
+            // what the chain has handed over of the chunk before, which stands until the next barrier
+            u32x4 sh[KS], uo[2];
 #pragma unroll
-                for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
+            for (int s = 0; s < KS; ++s) sh[s] = sm.sh[wave][s][lane];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) uo[k] = sm.uo[wave][k][lane];
-                typedef int i32x4 __attribute__((ext_vector_type(4)));
-                const i32x4 unit = *reinterpret_cast<const i32x4*>(&sm.unit[16 * wave + 4 * g4]);
-                const i32x4 from = *reinterpret_cast<const i32x4*>(&sm.from[16 * wave + 4 * g4]);
-                // queries 16 x + lr of columns 4 g4 + i
-                f32x4 o[4];
+            for (int k = 0; k < 2; ++k) uo[k] = sm.uo[wave][k][lane];
+            typedef int i32x4 __attribute__((ext_vector_type(4)));
+            const i32x4 unit = *reinterpret_cast<const i32x4*>(&sm.unit[16 * wave + 4 * g4]);
+            const i32x4 from = *reinterpret_cast<const i32x4*>(&sm.from[16 * wave + 4 * g4]);
+            // queries 16 x + lr of columns 4 g4 + i
+            f32x4 o[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int x = 0; x < 4; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(sh[s], q[x][s], o[x]);
+                for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(sh[s], q[x][s], o[x]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[x] *= qf[x];
+            for (int x = 0; x < 4; ++x) o[x] *= qf[x];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
-                float down[4];
-                bool all = true;
+                for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
+            float down[4];
+            bool all = true;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) down[i] = pow2(-unit[i]), all &= from[i] >= kC;
+            for (int i = 0; i < 4; ++i) down[i] = pow2(-unit[i]), all &= from[i] >= kC;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float z[4];
+            for (int x = 0; x < 4; ++x) {
+                float z[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf[x] * down[i];
-                    if (__builtin_expect(__any(!all), 0)) {
+                for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf[x] * down[i];
+                if (__builtin_expect(__any(!all), 0)) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z[i] = 16 * x + lr >= from[i] ? __builtin_nanf("") : z[i];
-                    }
-                    y[x] = u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
+                    for (int i = 0; i < 4; ++i) z[i] = 16 * x + lr >= from[i] ? __builtin_nanf("") : z[i];
                 }
+                y[x] = u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
             }
-            if (c < nch) {
-                load_out();
-                // the chain's loads, which are older than those: 16-byte loads of one wave cannot be made fewer
-                asm volatile("s_waitcnt vmcnt(%0)" :: "n"(4 * KS + 6) : "memory");
-                __syncthreads();  // the next chunk is there for the chain; what it handed over is read
-            }
-            if (c > 0) {
-                const int m = min(kC, n - (c - 1) * kC);
+        };
+        auto store = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (16 * x + lr < m && inside) *reinterpret_cast<u32x2*>(yp + 32 * x * a.ld_y + yoff) = y[x];
-                yp += 2 * kC * a.ld_y;
-            }
-            if (c < nch) {
-                __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), known to the compiler: later it would wait for the chain's loads too
-                __syncthreads();  // the chain is done with chunk c
-            }
+            for (int x = 0; x < 4; ++x)
+                if (16 * x + lr < m && inside) *reinterpret_cast<u32x2*>(yp + 32 * x * a.ld_y + yoff) = y[x];
+            yp += 2 * kC * a.ld_y;
+        };
+        // Phase c: the chain's loads of chunk c + 1, which it waits for in the middle of chunk c; outputs of chunk c - 1;
+        // loads for those of chunk c.
+        for (int c = 0; c < nch; ++c) {
+            if (c + 1 < nch) load_chain(c + 1);
+            if (c > 0) outputs();
+            load_out();
+            // the chain's loads, which are older than those: 16-byte loads of one wave cannot be made fewer
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(4 * KS + 6) : "memory");
+            __syncthreads();  // the next chunk is there for the chain; what it handed over is read
+            if (c > 0) store(kC);
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), known to the compiler: later it would wait for the chain's loads too
+            __syncthreads();  // the chain is done with chunk c
+        }
+        if (nch > 0) {
+            outputs();
+            store(n - (nch - 1) * kC);
         }
         return;
     }
