@@ -5,7 +5,16 @@
 //
 // A wave owns up to L tokens of one request and 512 channels (or as many whole heads as fit where
 // they are brought to length one), eight neighbouring channels a lane; the last W - 1 rows stay in
-// registers, so that every row of x is read once but for W - 1 rows in front of each unit.
+// registers, so that every row of x is read once but for the W - 1 rows in front of each unit, which a
+// neighbour has just read. Sums are FP32, the outputs' rounding is the only one to 16 bits.
+//
+// Bound by memory for prompts: 8,073 tokens of 10,240 FP16 channels, W = 4, 32 heads of 128 to length one,
+// in 66 us, 331 MB at 5.0 TB/s. What it took: whole rounds of four rows without a branch between
+// them, so that four rows are on their way and the sums over heads of four tokens are taken together
+// (104 -> 73 us); units of 16 tokens instead of 32 (-> 66; 64: 74). Eight rows on their way need 172
+// registers, and two waves on a SIMD instead of four cost more than the loads give (130 us).
+// Bound by latency for few tokens: the search for the unit, one round of loads, one row's sums.
+// 8 tokens in 4.5 us, 64 requests with a token each in 6.4 us.
 #include "op.h"
 
 #include <algorithm>
@@ -13,8 +22,6 @@
 namespace vqmlp {
 
 namespace {
-
-constexpr int kAhead = 4;  // rows on their way
 
 struct ConvArgs {
     const uint16_t *x, *w, *bias;
@@ -35,14 +42,33 @@ __device__ __forceinline__ void unpack8(u32x4 w, float* f) {
     for (int j = 0; j < 4; ++j) f[2 * j] = lo16<E>(w[j]), f[2 * j + 1] = hi16<E>(w[j]);
 }
 
+// Sum over the 2^n lanes of a head, n up to 5, of several tokens at once.
+template <int N>
+__device__ __forceinline__ void head_sums(float (&v)[N], int lanes) {
+    auto step = [&](auto ctrl) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] += __builtin_bit_cast(
+                float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v[j]), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    if (lanes > 1) step(std::integral_constant<int, 0xB1>{});   // the neighbour
+    if (lanes > 2) step(std::integral_constant<int, 0x4E>{});   // the other two of four
+    if (lanes > 4) step(std::integral_constant<int, 0x141>{});  // the other four of eight
+    if (lanes > 8) step(std::integral_constant<int, 0x140>{});  // the other eight of a row
+    if (lanes > 16)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] += __shfl_xor(v[j], 16);
+}
+
 template <class E, int W>
 __global__ void __launch_bounds__(256) k_short_conv(ConvArgs a) {
+    // rows on their way: a multiple of W, so that the last W rows stand where the unrolled loop finds them
+    constexpr int AHEAD = W == 3 ? 3 : 4;
     const int lane = threadIdx.x & 63;
     const int64_t id = a.id0 + blockIdx.x;
     const int groups = (a.sets + 3) / 4;
     const int set = uniform(int(id % groups) * 4 + (threadIdx.x >> 6));
-    PackedUnit u;
-    if (!packed_unit(a.p, a.L, int(id / groups), u) || set >= a.sets) return;
+    if (set >= a.sets) return;
     const bool unit = set < a.unit_sets;
     int c;  // first of the lane's channels
     bool in;
@@ -54,33 +80,38 @@ __global__ void __launch_bounds__(256) k_short_conv(ConvArgs a) {
         c = a.unit_heads * a.unit_dim + (set - a.unit_sets) * 512 + lane * 8;
         in = c < a.C;
     }
-    const int t0 = u.seg * a.L, t1 = min(u.n, t0 + a.L);
+    if (!in) c = 0;  // such lanes read the first channels, count nothing and write nothing
+    // the lane's 8 W filter taps lie one after another; on their way while the unit is looked for
     const u32x4 zero = {0, 0, 0, 0};
+    u32x4 taps[W], bits = zero;
+#pragma unroll
+    for (int j = 0; j < W; ++j) taps[j] = *reinterpret_cast<const u32x4*>(a.w + int64_t(c) * W + 8 * j);
+    if (a.bias) bits = *reinterpret_cast<const u32x4*>(a.bias + c);
+    PackedUnit u;
+    if (!packed_unit(a.p, a.L, int(id / groups), u)) return;
+    const int t0 = u.seg * a.L, t1 = min(u.n, t0 + a.L);
+    uint16_t* y = a.y + (u.c0 + t0) * a.ld_y + c;
     if (u.r == a.p.R) {  // rows behind the last request
-        for (int t = t0; t < t1; ++t)
-            if (in) *reinterpret_cast<u32x4*>(a.y + (u.c0 + t) * a.ld_y + c) = zero;
+        for (int t = t0; t < t1; ++t, y += a.ld_y)
+            if (in) *reinterpret_cast<u32x4*>(y) = zero;
         return;
     }
     bool old;
     const int slot = packed_slot(a.p, u.r, &old);
     const int64_t sbase = int64_t(max(slot, 0)) * (W - 1) * a.C + c;
     const uint16_t* const x = a.x + u.c0 * a.ld_x + c;
-    // row t of the request; from -(W - 1) on those of its state
+    // row t < n of the request; from -(W - 1) on those of its state
     auto row = [&](int t) __attribute__((always_inline)) {
-        u32x4 r = zero;
-        if (!in) return r;
-        if (t >= 0) {
-            if (t < u.n) r = *reinterpret_cast<const u32x4*>(x + t * a.ld_x);
-        } else if (old) {
-            r = *reinterpret_cast<const u32x4*>(a.sin + sbase + int64_t(t + W - 1) * a.C);
-        }
-        return r;
+        if (t >= 0) return *reinterpret_cast<const u32x4*>(x + t * a.ld_x);
+        return old ? *reinterpret_cast<const u32x4*>(a.sin + sbase + int64_t(t + W - 1) * a.C) : zero;
     };
-    u32x4 ring[kAhead], before[W - 1];
+    u32x4 ring[AHEAD], before[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) before[j] = row(t0 - (W - 1) + j);
+    if (t0 < t1) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) ring[j] = t0 + j < t1 ? row(t0 + j) : zero;
+        for (int j = 0; j < AHEAD; ++j) ring[j] = row(min(t0 + j, t1 - 1));
+    }
     // The unit with the request's first rows is the only one that reads its state, and so the one that
     // writes the new one, also where both are one array.
     if (u.seg == 0 && slot >= 0) {
@@ -91,54 +122,70 @@ __global__ void __launch_bounds__(256) k_short_conv(ConvArgs a) {
         for (int j = 0; j < W - 1; ++j)
             if (in) *reinterpret_cast<u32x4*>(a.sout + sbase + int64_t(j) * a.C) = next[j];
     }
-    float wt[W][8], bias[8], win[W][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bias[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)  // the lane's 8 W filter taps lie one after another
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wt[w][i] = 0.f;
-    if (in) {
+    float wt[W][8], bias[8], win[W][8];  // row t of the unit stands in win[t % W]
+    {
         float f[8 * W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) unpack8<E>(*reinterpret_cast<const u32x4*>(a.w + int64_t(c) * W + 8 * j), f + 8 * j);
+        for (int j = 0; j < W; ++j) unpack8<E>(taps[j], f + 8 * j);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int w = 0; w < W; ++w) wt[w][i] = f[i * W + w];
-        if (a.bias) unpack8<E>(*reinterpret_cast<const u32x4*>(a.bias + c), bias);
+        unpack8<E>(bits, bias);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) unpack8<E>(before[j], win[j + 1]);
-    for (int t = t0; t < t1; t += kAhead) {
+    auto rows = [&](auto count, int t) __attribute__((always_inline)) {
+        constexpr int N = decltype(count)::value;
+        float z[N][8];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (t + j >= t1) break;
-#pragma unroll
-            for (int w = 0; w < W - 1; ++w)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) win[w][i] = win[w + 1][i];
-            unpack8<E>(ring[j], win[W - 1]);
-            if (t + j + kAhead < t1) ring[j] = row(t + j + kAhead);
-            float z[8], sum = 0.f;
+        for (int j = 0; j < N; ++j) {
+            unpack8<E>(ring[j], win[j % W]);
+            ring[j] = *reinterpret_cast<const u32x4*>(x + min(t + j + AHEAD, t1 - 1) * a.ld_x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                z[i] = bias[i];
+                z[j][i] = bias[i];
 #pragma unroll
-                for (int w = 0; w < W; ++w) z[i] = fmaf(wt[w][i], win[w][i], z[i]);
-                if (a.silu) z[i] = silu(z[i]);
+                for (int w = 0; w < W; ++w) z[j][i] = fmaf(wt[w][i], win[(j + 1 + w) % W][i], z[j][i]);
+                if (a.silu) z[j][i] = silu(z[j][i]);
             }
-            if (unit) {
+        }
+        if (unit) {
+            float sum[N];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(z[i], z[i], sum);
-                for (int o = 1; o < a.lanes; o <<= 1) sum += __shfl_xor(sum, o);
-                const float by = 1.f / sqrtf(sum + a.eps);
+            for (int j = 0; j < N; ++j) {
+                sum[j] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] *= by;
+                for (int i = 0; i < 8; ++i) sum[j] = fmaf(z[j][i], z[j][i], sum[j]);
+                if (!in) sum[j] = 0.f;
             }
+            head_sums(sum, a.lanes);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float by = __builtin_amdgcn_rsqf(sum[j] + a.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[j][i] *= by;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
             if (in)
-                *reinterpret_cast<u32x4*>(a.y + (u.c0 + t + j) * a.ld_y + c) =
-                    u32x4{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3]), pack16<E>(z[4], z[5]), pack16<E>(z[6], z[7])};
+                *reinterpret_cast<u32x4*>(y) = u32x4{pack16<E>(z[j][0], z[j][1]), pack16<E>(z[j][2], z[j][3]),
+                                                     pack16<E>(z[j][4], z[j][5]), pack16<E>(z[j][6], z[j][7])};
+            y += a.ld_y;
+        }
+    };
+    int t = t0;
+    for (; t + AHEAD <= t1; t += AHEAD) rows(std::integral_constant<int, AHEAD>{}, t);
+    for (; t < t1; ++t) {
+        rows(std::integral_constant<int, 1>{}, t);
+#pragma unroll
+        for (int j = 0; j + 1 < AHEAD; ++j) ring[j] = ring[j + 1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int j = 1; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+            win[W - 1][i] = win[0][i];
         }
     }
 }
@@ -210,7 +257,12 @@ extern "C" vqmlp_status vqmlp_short_conv(const vqmlp_conv_desc* p, void* stream)
     while (a.lanes * 8 < a.unit_dim) a.lanes *= 2;
     a.unit_sets = (d.unit_heads * a.lanes + 63) / 64;
     a.sets = a.unit_sets + (d.C - d.unit_heads * a.unit_dim + 511) / 512;
-    a.L = 32;
+    // Tokens of a unit: 16 (15) where there are tokens enough for two waves on each of the card's SIMDs,
+    // in whole rounds of rows; with fewer tokens shorter units, down to one token (8 tokens of 10,240
+    // channels: 4.5 us with units of one, 10 us with one unit).
+    const int step = d.W == 3 ? 3 : 4;
+    a.L = int(std::min<int64_t>(16, std::max<int64_t>(1, int64_t(d.T) * a.sets / (8 * cus))));
+    if (a.L > step) a.L -= a.L % step;
     const int64_t units = d.T / a.L + d.R + 1, all = units * ((a.sets + 3) / 4);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (d.dtype == VQMLP_F16) launch_conv<F16>(a, d.W, all, s);
