@@ -42,24 +42,6 @@ __device__ __forceinline__ void unpack8(u32x4 w, float* f) {
     for (int j = 0; j < 4; ++j) f[2 * j] = lo16<E>(w[j]), f[2 * j + 1] = hi16<E>(w[j]);
 }
 
-// Sum over the 2^n lanes of a head, n up to 5, of several tokens at once.
-template <int N>
-__device__ __forceinline__ void head_sums(float (&v)[N], int lanes) {
-    auto step = [&](auto ctrl) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            v[j] += __builtin_bit_cast(
-                float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v[j]), decltype(ctrl)::value, 0xF, 0xF, false));
-    };
-    if (lanes > 1) step(std::integral_constant<int, 0xB1>{});   // the neighbour
-    if (lanes > 2) step(std::integral_constant<int, 0x4E>{});   // the other two of four
-    if (lanes > 4) step(std::integral_constant<int, 0x141>{});  // the other four of eight
-    if (lanes > 8) step(std::integral_constant<int, 0x140>{});  // the other eight of a row
-    if (lanes > 16)
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] += __shfl_xor(v[j], 16);
-}
-
 template <class E, int W>
 __global__ void __launch_bounds__(256) k_short_conv(ConvArgs a) {
     // rows on their way: a multiple of W, so that the last W rows stand where the unrolled loop finds them

@@ -115,6 +115,24 @@ __device__ __forceinline__ float exp_f32(float x) {
 // The log of a decay from kMinG on; NaN stays NaN.
 __device__ __forceinline__ float bounded(float g) { return g < kMinG ? kMinG : g; }
 
+// Sum over the 2^n lanes of a head, n up to 5, for several of them at once.
+template <int N>
+__device__ __forceinline__ void head_sums(float (&v)[N], int lanes) {
+    auto step = [&](auto ctrl) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] += __builtin_bit_cast(
+                float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v[j]), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    if (lanes > 1) step(std::integral_constant<int, 0xB1>{});   // the neighbour
+    if (lanes > 2) step(std::integral_constant<int, 0x4E>{});   // the other two of four
+    if (lanes > 4) step(std::integral_constant<int, 0x141>{});  // the other four of eight
+    if (lanes > 8) step(std::integral_constant<int, 0x140>{});  // the other eight of a row
+    if (lanes > 16)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] += __shfl_xor(v[j], 16);
+}
+
 // Prefix over the 64 lanes with data-parallel moves: within rows of 16 lanes, then across them.
 template <class T, class F>
 __device__ __forceinline__ T lane_scan(T v, T none, F&& op) {

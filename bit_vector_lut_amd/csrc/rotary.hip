@@ -1,7 +1,18 @@
 // rotary.hip -- norm and rotation of queries and keys, append of keys and values to the paged cache.
 //
+//   x' = x / sqrt(mean(x^2) + eps) (offset + w)          each head of q and k, where there are weights
+//   (a, b)' = (a cos f - b sin f, b cos f + a sin f)      f = position inv_freq[pair], pairs (a, b) of a head
+//
 // Roles of the workgroups of one launch: heads of q, heads of k (rows: norm, turn, write), heads of v
-// (64 tokens turned through LDS, since values lie transposed in their pages).
+// (64 tokens turned through LDS, since values lie transposed in their pages). The angle is a product of
+// FP64, brought to one turn before it is rounded: at position 10^6 an FP32 product would be off by 0.06.
+// Norm, turn and sums are FP32 and rounded once.
+//
+// Bound by memory for prompts: 8,192 tokens, 24 + 4 heads of 256 with 64 turned, in 46 us, 268 MB at
+// 5.8 TB/s (part of the writes still on the way to memory). One angle a thread, kept in LDS for the heads of
+// a workgroup, instead of each lane's own for each head, and four heads on their way at a time: 102 -> 46 us.
+// Few tokens: latency. 8 tokens in 3.6 us, 64 requests' single tokens in 5.4 us, 512 tokens of 40 + 8 heads
+// of 128 in 6.2 us, where the sines bound.
 #include "op.h"
 
 #include <algorithm>
@@ -10,7 +21,8 @@ namespace vqmlp {
 
 namespace {
 
-constexpr int kVTok = 64, kVD = 64;
+constexpr int kVTok = 64, kVD = 64;  // of a tile of values: two loads a thread
+constexpr int kHeads = 4;  // heads on their way at a time
 constexpr double kTurns = 0.15915494309189533577;  // 1 / (2 pi)
 
 struct AppendArgs {
@@ -26,85 +38,109 @@ struct AppendArgs {
     int rows;      // tokens of a row block
     int per;       // heads of a row block
     int qgroups, groups;
-    float eps, off;
+    float eps, off, inv_d;
 };
 
-// A lane's eight elements of a head are two runs of four: of a half-split rotation four pairs' first
-// and second elements, otherwise eight neighbours.
-template <class E>
-__device__ __forceinline__ void rows_role(const AppendArgs& a, int64_t id) {
+// HB heads at a time of one token for each group of lanes. A lane's eight elements of a head are two runs
+// of four: of a half-split rotation four pairs' first and second elements, otherwise eight neighbours.
+// The angles' sines and cosines are found once for all heads of the workgroup, one angle a thread at a
+// time, while the first heads are on their way.
+template <class E, int HB>
+__device__ __forceinline__ void rows_role(const AppendArgs& a, int64_t id, float2* trig) {
     const int group = int(id % a.groups);
     const int64_t t0 = id / a.groups * a.rows;
     const bool isk = group >= a.qgroups;
     const int h0 = (isk ? group - a.qgroups : group) * a.per;
     const int h1 = min(h0 + a.per, isk ? a.kv_heads : a.heads);
-    const int item = threadIdx.x % a.lanes, half = a.rot / 2;
+    const int item = threadIdx.x & (a.lanes - 1), i = threadIdx.x / a.lanes, half = a.rot / 2;
     const bool in = 8 * item < a.D, turn = 8 * item < a.rot;
-    const int e0 = turn && !a.next ? 4 * item : 8 * item, e1 = turn && !a.next ? half + 4 * item : 8 * item + 4;
+    // lanes behind the head's end and tokens behind the last read what is there and write nothing
+    const int first = in ? item : 0;
+    const int e0 = turn && !a.next ? 4 * first : 8 * first, e1 = turn && !a.next ? half + 4 * first : 8 * first + 4;
+    const int64_t t = min(t0 + i, int64_t(a.T) - 1);
     const uint16_t* const w = isk ? a.kw : a.qw;
-    float wt[8];
-    auto read = [&](const uint16_t* p, float* f) __attribute__((always_inline)) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(p + e0), y = *reinterpret_cast<const u32x2*>(p + e1);
-        f[0] = lo16<E>(x[0]), f[1] = hi16<E>(x[0]), f[2] = lo16<E>(x[1]), f[3] = hi16<E>(x[1]);
-        f[4] = lo16<E>(y[0]), f[5] = hi16<E>(y[0]), f[6] = lo16<E>(y[1]), f[7] = hi16<E>(y[1]);
+    const int64_t hs = isk ? a.hs_k : a.hs_q;
+    const uint16_t* const src = isk ? a.k + t * a.ld_k : a.q + t * a.ld_q;
+    struct Raw {
+        u32x2 lo, hi;
     };
-    if (w && in) {
-        read(w, wt);
+    auto read = [&](const uint16_t* p) __attribute__((always_inline)) {
+        return Raw{*reinterpret_cast<const u32x2*>(p + e0), *reinterpret_cast<const u32x2*>(p + e1)};
+    };
+    auto unpack = [&](const Raw& r, float* f) __attribute__((always_inline)) {
+        f[0] = lo16<E>(r.lo[0]), f[1] = hi16<E>(r.lo[0]), f[2] = lo16<E>(r.lo[1]), f[3] = hi16<E>(r.lo[1]);
+        f[4] = lo16<E>(r.hi[0]), f[5] = hi16<E>(r.hi[0]), f[6] = lo16<E>(r.hi[1]), f[7] = hi16<E>(r.hi[1]);
+    };
+    const int pos = a.pos[t];
+    const int64_t s = isk ? a.slot[t] : 0;
+    Raw raw[HB], weights{};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wt[i] += a.off;
+    for (int b = 0; b < HB; ++b) raw[b] = read(src + min(h0 + b, h1 - 1) * hs);
+    if (w) weights = read(w);
+    const int pairs = half * a.rows;
+    for (int n = threadIdx.x; n < pairs; n += 256) {
+        const int64_t tt = min(t0 + n / half, int64_t(a.T) - 1);
+        const double f = double(a.pos[tt]) * (double(a.freq[n % half]) * kTurns);
+        float2 v;
+        sincospif(float(2. * (f - rint(f))), &v.y, &v.x);
+        trig[n] = v;
     }
-    float freq[4];
+    __syncthreads();
+    float wt[8], c[4], sn[4];
+    unpack(weights, wt);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) freq[i] = turn ? a.freq[4 * item + i] : 0.f;
-    const int step = 256 / a.lanes;
-    for (int i = threadIdx.x / a.lanes; i < a.rows; i += step) {
-        const int64_t t = t0 + i;
-        if (t >= a.T) break;  // a head's lanes leave together
-        const int pos = a.pos[t];
-        if (pos < 0) continue;
-        int64_t s = 0;
-        if (isk) {
-            s = a.slot[t];
-            if (s < 0 || s >= a.slots) continue;
+    for (int j = 0; j < 8; ++j) wt[j] += a.off;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = turn ? trig[i * half + 4 * item + j] : float2{1.f, 0.f};
+        c[j] = v.x, sn[j] = v.y;
+    }
+    const bool write = in && t0 + i < a.T && pos >= 0 && s >= 0 && s < a.slots;
+    const int64_t page = s >> a.shift, at = s & ((1 << a.shift) - 1);
+    uint16_t* const dst = isk ? a.kc + ((page * a.kv_heads << a.shift) + at) * a.D : a.q_out + t * a.ld_qo;
+    const int64_t step = isk ? int64_t(a.D) << a.shift : a.D;
+    for (int h = h0; h < h1; h += HB) {
+        float f[HB][8];
+#pragma unroll
+        for (int b = 0; b < HB; ++b) {
+            unpack(raw[b], f[b]);
+            raw[b] = read(src + min(h + HB + b, h1 - 1) * hs);
         }
-        const int64_t page = s >> a.shift, at = s & ((1 << a.shift) - 1);
-        float c[4], sn[4];
-        if (turn) {
+        if (w) {
+            float sum[HB];
+#pragma unroll
+            for (int b = 0; b < HB; ++b) {
+                sum[b] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[b] = fmaf(f[b][j], f[b][j], sum[b]);
+                if (!in) sum[b] = 0.f;
+            }
+            head_sums(sum, a.lanes);
+#pragma unroll
+            for (int b = 0; b < HB; ++b) {
+                const float by = __builtin_amdgcn_rsqf(fmaf(sum[b], a.inv_d, a.eps));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[b][j] *= by * wt[j];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < HB; ++b) {
+            float z[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const double f = double(pos) * (double(freq[j]) * kTurns);
-                sincospif(float(2. * (f - rint(f))), &sn[j], &c[j]);
+                const float x = a.next ? f[b][2 * j] : f[b][j], y = a.next ? f[b][2 * j + 1] : f[b][j + 4];
+                z[j] = x * c[j] - y * sn[j];
+                z[j + 4] = y * c[j] + x * sn[j];
             }
-        }
-        for (int h = h0; h < h1; ++h) {
-            const uint16_t* const src = isk ? a.k + t * a.ld_k + h * a.hs_k : a.q + t * a.ld_q + h * a.hs_q;
-            uint16_t* const dst = isk ? a.kc + (((page * a.kv_heads + h) << a.shift) + at) * a.D
-                                      : a.q_out + t * a.ld_qo + int64_t(h) * a.D;
-            float f[8] = {};
-            if (in) read(src, f);
-            if (w) {
-                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
-                for (int o = 1; o < a.lanes; o <<= 1) sum += __shfl_xor(sum, o);
-                const float by = 1.f / sqrtf(sum / float(a.D) + a.eps);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f[j] * by * wt[j];
-            }
-            if (turn) {
-                float z[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = a.next ? f[2 * j] : f[j], y = a.next ? f[2 * j + 1] : f[j + 4];
-                    z[j] = x * c[j] - y * sn[j];
-                    z[j + 4] = y * c[j] + x * sn[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = a.next ? z[j / 2 + (j & 1) * 4] : z[j];
-            }
-            if (in) {
-                *reinterpret_cast<u32x2*>(dst + e0) = u32x2{pack16<E>(f[0], f[1]), pack16<E>(f[2], f[3])};
-                *reinterpret_cast<u32x2*>(dst + e1) = u32x2{pack16<E>(f[4], f[5]), pack16<E>(f[6], f[7])};
+            for (int j = 0; j < 8; ++j) z[j] = turn ? z[j] : f[b][j];
+            const bool next = a.next && turn;
+            if (write && h + b < h1) {
+                uint16_t* const p = dst + (h + b) * step;
+                *reinterpret_cast<u32x2*>(p + e0) = next ? u32x2{pack16<E>(z[0], z[4]), pack16<E>(z[1], z[5])}
+                                                         : u32x2{pack16<E>(z[0], z[1]), pack16<E>(z[2], z[3])};
+                *reinterpret_cast<u32x2*>(p + e1) = next ? u32x2{pack16<E>(z[2], z[6]), pack16<E>(z[3], z[7])}
+                                                         : u32x2{pack16<E>(z[4], z[5]), pack16<E>(z[6], z[7])};
             }
         }
     }
@@ -117,30 +153,50 @@ __device__ __forceinline__ void values_role(const AppendArgs& a, int64_t id, uin
     const int d0 = int(id % parts) * kVD, h = int(id / parts % a.kv_heads);
     const int64_t t0 = id / parts / a.kv_heads * kVTok;
     const int P = 1 << a.shift, nd = min(kVD, a.D - d0);
-    for (int i = threadIdx.x; i < kVTok * (kVD / 8); i += 256) {
-        const int tok = i / (kVD / 8), c = i % (kVD / 8) * 8;
-        if (t0 + tok >= a.T || c >= nd) continue;
-        const u32x4 x = *reinterpret_cast<const u32x4*>(a.v + (t0 + tok) * a.ld_v + h * a.hs_v + d0 + c);
-        uint32_t* const w = reinterpret_cast<uint32_t*>(&tile[tok][c]);
+    const int tok = threadIdx.x & 63;
+    const int64_t t = min(t0 + tok, int64_t(a.T) - 1);
+    const int pos = a.pos[t];
+    const int64_t s = a.slot[t];
+    u32x4 x[2] = {};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = x[j];
+    for (int n = 0; n < 2; ++n) {
+        const int i = threadIdx.x + 256 * n;
+        const int r = i / (kVD / 8), c = i % (kVD / 8) * 8;
+        if (t0 + r < a.T && c < nd) x[n] = *reinterpret_cast<const u32x4*>(a.v + (t0 + r) * a.ld_v + h * a.hs_v + d0 + c);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int i = threadIdx.x + 256 * n;
+        uint32_t* const w = reinterpret_cast<uint32_t*>(&tile[i / (kVD / 8)][i % (kVD / 8) * 8]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = x[n][j];
     }
     __syncthreads();
-    const int tok = threadIdx.x & 63;
-    if (t0 + tok >= a.T || a.pos[t0 + tok] < 0) return;
-    const int64_t s = a.slot[t0 + tok];
-    if (s < 0 || s >= a.slots) return;
+    if (t0 + tok >= a.T || pos < 0 || s < 0 || s >= a.slots) return;
     const int64_t page = s >> a.shift, off = s & (P - 1);
     uint16_t* const dst = a.vc + ((page * a.kv_heads + h) * a.D + d0) * P + off;
     for (int c = threadIdx.x >> 6; c < nd; c += 4) dst[int64_t(c) * P] = tile[tok][c];
 }
 
-template <class E>
+template <class E, int HB>
 __global__ void __launch_bounds__(256) k_paged_append(AppendArgs a) {
-    __shared__ uint16_t tile[kVTok][kVD + 2];  // a row stride of 33 words
+    __shared__ union {
+        uint16_t tile[kVTok][kVD + 2];  // a row stride of 33 words
+        float2 trig[1024];              // 256 / lanes tokens of up to 4 * lanes pairs
+    } lds;
     const int64_t id = a.id0 + blockIdx.x;
-    if (id < a.row_blocks) rows_role<E>(a, id);
-    else values_role(a, id - a.row_blocks, tile);
+    if (id < a.row_blocks) rows_role<E, HB>(a, id, lds.trig);
+    else values_role(a, id - a.row_blocks, lds.tile);
+}
+
+template <class E>
+void launch_append(AppendArgs a, int64_t all, hipStream_t s) {
+    constexpr int64_t most = 8 << 20;  // a launch holds fewer than 2^32 threads
+    for (a.id0 = 0; a.id0 < all; a.id0 += most) {
+        const unsigned grid = unsigned(std::min(most, all - a.id0));
+        if (a.per == 1) k_paged_append<E, 1><<<grid, 256, 0, s>>>(a);
+        else k_paged_append<E, kHeads><<<grid, 256, 0, s>>>(a);
+    }
 }
 
 }  // namespace
@@ -204,22 +260,22 @@ extern "C" vqmlp_status vqmlp_paged_append(const vqmlp_append_desc* p, void* str
     a.slots = int64_t(d.n_pages) << a.shift;
     a.T = d.T, a.heads = d.heads, a.kv_heads = d.kv_heads, a.D = d.D, a.rot = d.rot;
     a.next = d.pairs == VQMLP_PAIRS_NEXT;
-    a.eps = d.eps, a.off = d.w_offset;
+    a.eps = d.eps, a.off = d.w_offset, a.inv_d = 1.f / float(d.D);
     a.lanes = 1;
     while (a.lanes * 8 < d.D) a.lanes *= 2;
     a.rows = 256 / a.lanes;
-    a.per = 1;
+    const int64_t heads_each = (d.T + a.rows - 1) / a.rows * int64_t(d.heads + d.kv_heads);
+    // Heads that share a workgroup's sines: many once there are workgroups enough (512 tokens, 48 heads of 128:
+    // 8.7 us with one, 6.2 with four), one where the card would stand empty (64 tokens: 5.4 us).
+    a.per = heads_each < 2 * cus ? 1 : heads_each < 16 * cus ? kHeads : 2 * kHeads;
     a.qgroups = (d.heads + a.per - 1) / a.per;
     a.groups = a.qgroups + (d.kv_heads + a.per - 1) / a.per;
     a.row_blocks = int64_t((d.T + a.rows - 1) / a.rows) * a.groups;
     const int64_t values = int64_t((d.T + kVTok - 1) / kVTok) * d.kv_heads * ((d.D + kVD - 1) / kVD);
-    const int64_t all = a.row_blocks + values, most = 8 << 20;  // a launch holds fewer than 2^32 threads
+    const int64_t all = a.row_blocks + values;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    for (a.id0 = 0; a.id0 < all; a.id0 += most) {
-        const unsigned grid = unsigned(std::min(most, all - a.id0));
-        if (d.dtype == VQMLP_F16) k_paged_append<F16><<<grid, 256, 0, s>>>(a);
-        else k_paged_append<BF16><<<grid, 256, 0, s>>>(a);
-    }
+    if (d.dtype == VQMLP_F16) launch_append<F16>(a, all, s);
+    else launch_append<BF16>(a, all, s);
     if (trace_enabled())
         trace_line("paged_append T=%d heads=%d/%d D=%d rot=%d: %lld row workgroups of %d tokens x %d heads, %lld of values", d.T,
                    d.heads, d.kv_heads, d.D, d.rot, (long long)a.row_blocks, a.rows, a.per, (long long)values);
