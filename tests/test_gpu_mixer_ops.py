@@ -321,6 +321,107 @@ def test_delta_rule_strides_streams_and_graphs(vq, torch_dev):
         assert torch.equal(y2, y)
 
 
+def _in_segments(vq, dtype, T, R, hk, hv, dk, dv, max_q):
+    """Whether the workspace holds states and factors of segments besides the chunks' own."""
+    chunks = T // 64 + R + 1
+    own = chunks * (hv * 20480 + hk * (1 if dtype == "f16" else 2) * 64 * (64 if dk <= 64 else 128) * 2)
+    return vq.DeltaRule(hk, hv, dk, dv).workspace_bytes(T, R, max_q) > own
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv,extra", [
+    ([4000], 1, 1, 128, 128, {}),
+    ([3001, 0, 1700, 1], 1, 2, 128, 72, dict(ctx=[5, 1, 0, 9], index=[4, 0, 2, 1], n_states=5, pad=70)),
+    ([2560, 2560], 2, 2, 64, 64, dict(in_place=True)),
+    ([64, 5000, 130], 1, 1, 40, 16, dict(in_place=True, ctx=[1, 0, 3], index=[2, -1, 0], n_states=3)),
+    ([2113, 2049, 3071], 1, 2, 96, 104, dict(in_place=True)),
+])
+def test_delta_rule_segments(vq, torch_dev, dtype, lens, hk, hv, dk, dv, extra):
+    """Few heads and long requests: segments of a request at once."""
+    T = sum(lens) + extra.get("pad", 0)
+    assert _in_segments(vq, dtype, T, len(lens), hk, hv, dk, dv, max(lens))
+    _delta_check(vq, torch_dev, dtype, lens, hk, hv, dk, dv, max(lens), **extra)
+    # said to be as long as one of them when they are not
+    _delta_check(vq, torch_dev, dtype, lens, hk, hv, dk, dv, T, **extra)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_delta_rule_segments_decays_and_repeated_keys(vq, torch_dev, dtype):
+    torch = torch_dev
+    T = 4100
+    q, k, v, g, beta = _delta_inputs(torch, _t(torch, dtype), T, 1, 4, 64, 64, 11)
+    g[:, 0] = 0.0
+    g[:, 1] = -100.0
+    g[5::700, 2] = -math.inf
+    g[2000:2070, 3] = -30.0
+    beta[::3] = 0.0
+    beta[1::3] = 1.0
+    assert _in_segments(vq, dtype, T, 1, 1, 4, 64, 64, T)
+    _delta_check(vq, torch, dtype, [T], 1, 4, 64, 64, T, inputs=(q, k, v, g, beta))
+    k[:] = 0.0
+    k[:, :, 3] = 1.0
+    beta[:] = 1.0
+    _delta_check(vq, torch, dtype, [T], 1, 4, 64, 64, T, inputs=(q, k, v, g, beta))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("what", ["k", "v", "q", "g", "beta", "state"])
+def test_delta_rule_segments_values_that_are_not_finite(vq, torch_dev, dtype, what):
+    torch = torch_dev
+    n, T = 2600, 4300
+    q, k, v, g, beta = _delta_inputs(torch, _t(torch, dtype), T, 1, 2, 64, 72, 7)
+    args = [x.cuda() for x in (q, k, v, g, beta, _randn(torch, (2, 2, 64, 72), torch.float32, 9))]
+    op = vq.DeltaRule(1, 2, 64, 72)
+    cu = _i(torch, [0, n, T])
+    assert _in_segments(vq, dtype, T, 2, 1, 2, 64, 72, n)
+    y0, s0 = op.forward(*args, cu, max_q=n)
+    for t in (0, 1500, n - 1):
+        new = [x.clone() for x in args]
+        hit, lost = torch.zeros_like(y0, dtype=torch.bool), torch.zeros_like(s0, dtype=torch.bool)
+        if what == "state":
+            new[5][0, 1, 7, 20] = math.nan
+            hit[:n, 1, 20] = lost[0, 1, :, 20] = True
+        elif what == "v":
+            new[2][t, 1, 20] = math.nan
+            hit[t:n, 1, 20] = lost[0, 1, :, 20] = True
+        elif what == "k":
+            new[1][t, 0, 9] = math.nan
+            hit[t:n] = lost[0] = True
+        elif what == "q":
+            new[0][t, 0, 9] = math.nan
+            hit[t] = True
+        else:
+            new[3 if what == "g" else 4][t, 1] = math.nan
+            hit[t:n, 1] = lost[0, 1] = True
+        y, s = op.forward(*new, cu, max_q=n)
+        assert torch.equal(y[~hit], y0[~hit]) and y[hit].isnan().all(), t
+        assert torch.equal(s[~lost], s0[~lost]) and s[lost].isnan().all(), t
+
+
+def test_delta_rule_segments_in_a_graph(vq, torch_dev):
+    """A poisoned workspace, other lengths and values between the replays."""
+    torch = torch_dev
+    T, lens = 4200, [4200, 0]
+    op = vq.DeltaRule(1, 2, 64, 64)
+    args = [x.cuda() for x in _delta_inputs(torch, torch.bfloat16, T, 1, 2, 64, 64, 3)]
+    state, cu = torch.randn(2, 2, 64, 64, device="cuda"), _i(torch, _starts(lens))
+    work = torch.full((op.workspace_bytes(T, 2, T),), 255, dtype=torch.uint8, device="cuda")
+    assert _in_segments(vq, "bf16", T, 2, 1, 2, 64, 64, T)
+    y, s = torch.empty_like(args[2]), torch.empty_like(state)
+    op.forward(*args, state, cu, max_q=T, state_out=s, y=y, workspace=work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.forward(*args, state, cu, max_q=T, state_out=s, y=y, workspace=work)
+    for ls in (lens, [1000, 3200], [0, 4200], [4100, 63]):
+        cu.copy_(_i(torch, _starts(ls)))
+        args[2].mul_(0.5)
+        work.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        y1, s1 = op.forward(*args, state, cu, max_q=T)
+        assert torch.equal(y, y1) and torch.equal(s, s1), ls
+
+
 # ------------------------------------------------------------------ append
 
 
