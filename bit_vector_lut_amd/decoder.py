@@ -1,13 +1,15 @@
 """A small decoder stack out of the library's parts, served step by step (an example).
 
-    python -m bit_vector_lut_amd.decoder
+    python -m bit_vector_lut_amd.decoder [--mixer delta] [--rotary 64]
 
 makes a seeded random model, prefills three prompts in one step and then decodes tokens for all of
 them.  Every step takes the new tokens of all requests packed one after another:
 
     plan   PagePlanner        block tables, slots and row starts from the requests' lengths
-    mixer  LUTProjection      -> PagedCache.store and .attention (every `full_every`-th layer), or
-                              -> LinearAttention with its state per request (the other layers)
+    mixer  LUTProjection      -> PagedCache.store and .attention (every `full_every`-th layer; with `rotary`
+                              PagedCache.append, which norms and turns the heads of q and k on the way), or
+                              -> LinearAttention with its state per request (the other layers), or, with
+                              mixer "delta", ShortConv -> DeltaRule with theirs
     norm   BlockNorm          norm of the mixer's or MLP's output, FP32 residual sum, norm for the next
     MLP    MLP                the three-bit vector-LUT MLP
     head   LUTProjection.argmax
@@ -27,8 +29,13 @@ class Decoder:
 
     def __init__(self, H=1024, I=2816, layers=4, full_every=4, heads=8, kv_heads=2, D=128, k_heads=4,
                  v_heads=8, Dk=64, Dv=128, vocab=4096, requests=3, max_len=512, page_size=16, t_max=256,
-                 seed=0, device="cuda"):
+                 seed=0, device="cuda", mixer="linear", conv_width=4, rotary=0):
+        """mixer: "linear" or "delta"; rotary: leading elements of each attention head that are turned, with
+        norms of the heads in front (0: neither)."""
         import torch
+
+        if mixer not in ("linear", "delta"):
+            raise ValueError("unknown mixer %r" % (mixer,))
 
         rng = np.random.default_rng(seed)
         dev = torch.device(device, torch.cuda.current_device()) if device == "cuda" else torch.device(device)
@@ -64,6 +71,20 @@ class Decoder:
                 layer["into"] = project((heads + 2 * kv_heads) * D, H)
                 layer["out"] = project(H, heads * D)
                 layer["cache"] = vqmlp.PagedCache.empty(pages, kv_heads, page_size, D, torch.float16, dev)
+                if rotary:
+                    freq = torch.from_numpy((1e4 ** (-np.arange(0, rotary, 2) / rotary)).astype(np.float32)).to(dev)
+                    layer["rotary"] = vqmlp.Rotary(freq, q_weight=weight(D), k_weight=weight(D))
+            elif mixer == "delta":
+                n, heads_k = 2 * k_heads * Dk + v_heads * Dv, 2 * k_heads
+                layer["into"] = project(n + -(-2 * v_heads // 64) * 64, H)
+                layer["out"] = project(H, v_heads * Dv)
+                # q and k leave the convolution with length one
+                layer["conv"] = vqmlp.ShortConv(weight(n * conv_width, 0.0, conv_width ** -0.5).view(n, conv_width),
+                                                weight(n, 0.0), unit_heads=heads_k, unit_dim=Dk)
+                layer["rows"] = layer["conv"].state(requests)
+                layer["delta"] = vqmlp.DeltaRule(k_heads, v_heads, Dk, Dv)
+                layer["state"] = layer["delta"].state(requests, dev)
+                layer["bias"] = torch.from_numpy(rng.uniform(-5, 0, v_heads).astype(np.float32)).to(dev)
             else:
                 gates = -(-v_heads // 64) * 64
                 layer["into"] = project(2 * k_heads * Dk + v_heads * Dv + gates, H)
@@ -81,8 +102,12 @@ class Decoder:
     def _attend(self, layer, x, plan):
         h, k, D, T = self.heads, self.kv_heads, self.D, x.shape[0]
         qkv = layer["into"].forward(x).unflatten(1, (h + 2 * k, D))
-        layer["cache"].store(qkv[:, h:h + k], qkv[:, h + k:], plan.slot)
-        y = layer["cache"].attention(qkv[:, :h], self.table, plan.cu_q, plan.seq_len)
+        q = qkv[:, :h]
+        if "rotary" in layer:
+            q = layer["cache"].append(q, qkv[:, h:h + k], qkv[:, h + k:], plan.position, plan.slot, layer["rotary"])
+        else:
+            layer["cache"].store(qkv[:, h:h + k], qkv[:, h + k:], plan.slot)
+        y = layer["cache"].attention(q, self.table, plan.cu_q, plan.seq_len)
         return layer["out"].forward(y.view(T, h * D))
 
     def _recur(self, layer, x, plan, longest):
@@ -98,6 +123,22 @@ class Decoder:
                                        plan.cu_q, ctx_len=self.ctx_len, max_q=longest,
                                        state_out=layer["state"])
         return layer["out"].forward(y.view(T, self.v_heads * self.Dv))
+
+    def _correct(self, layer, x, plan, longest):
+        import torch
+
+        T, n, h = x.shape[0], self.k_heads * self.Dk, self.v_heads
+        z = layer["into"].forward(x)
+        C = layer["conv"].C
+        u, _ = layer["conv"].forward(z[:, :C], layer["rows"], plan.cu_q, ctx_len=self.ctx_len,
+                                     state_out=layer["rows"])
+        q, k = (u[:, at:at + n].unflatten(1, (self.k_heads, self.Dk)) for at in (0, n))
+        gates = z[:, C:C + 2 * h].float()
+        g = -torch.nn.functional.softplus(gates[:, :h] + layer["bias"])
+        y, _ = layer["delta"].forward(q, k, u[:, 2 * n:].unflatten(1, (h, self.Dv)), g, gates[:, h:].sigmoid(),
+                                      layer["state"], plan.cu_q, ctx_len=self.ctx_len, max_q=longest,
+                                      state_out=layer["state"])
+        return layer["out"].forward(y.view(T, h * self.Dv))
 
     def step(self, tokens, lens):
         """tokens: the requests' new tokens one after another (device, [sum of lens]); lens: how many each
@@ -118,7 +159,10 @@ class Decoder:
         r = self.embed[tokens].float()
         x = self._first(r)
         for layer in self.layers:
-            y = self._attend(layer, x, plan) if layer["full"] else self._recur(layer, x, plan, max(lens))
+            if layer["full"]:
+                y = self._attend(layer, x, plan)
+            else:
+                y = (self._correct if "delta" in layer else self._recur)(layer, x, plan, max(lens))
             r, x = layer["mid"].forward(y, r, residual_out=r)
             r, x = layer["end"].forward(layer["mlp"].forward(x), r, residual_out=r)
         self.ctx_len = plan.seq_len
@@ -137,11 +181,11 @@ class Decoder:
         return torch.where(end > plan.cu_q[:-1], tokens, -1)
 
 
-def main(steps=16, seed=0):
+def main(steps=16, seed=0, **options):
     import torch
 
     lens = [37, 5, 70]
-    model = Decoder(requests=len(lens), seed=seed)
+    model = Decoder(requests=len(lens), seed=seed, **options)
     tokens = torch.randint(0, 4096, (sum(lens),), device=model.device)
     out = []
     for i in range(steps + 1):
@@ -156,4 +200,9 @@ def main(steps=16, seed=0):
 
 
 if __name__ == "__main__":
-    main()
+    import argparse
+
+    parser = argparse.ArgumentParser()
+    parser.add_argument("--mixer", default="linear", choices=["linear", "delta"])
+    parser.add_argument("--rotary", type=int, default=0, help="leading elements of each attention head that are turned")
+    main(**vars(parser.parse_args()))

@@ -1007,24 +1007,26 @@ class ShortConv:
     the first unit_heads heads of unit_dim channels are brought to length one.  weight [C, W], bias [C] or
     None; activation "silu" or None."""
 
+    C, W = _fixed("C"), _fixed("W")
+
     def __init__(self, weight, bias=None, *, activation="silu", unit_heads=0, unit_dim=0, eps=1e-6):
         if activation not in ("silu", None):
             _bad("unknown activation %r" % (activation,))
         _need(weight, "weight", weight.device, None, (None, None))
         self._keep = weight, bias
-        self.C, self.W = weight.shape
-        _fits(self.C | self.W | unit_heads | unit_dim, "short convolution")
-        self._desc = _ConvDesc(dtype=_dtype(weight, "weight"), C=self.C, W=self.W, silu=int(activation == "silu"),
+        self._C, self._W = weight.shape
+        _fits(self._C | self._W | unit_heads | unit_dim, "short convolution")
+        self._desc = _ConvDesc(dtype=_dtype(weight, "weight"), C=self._C, W=self._W, silu=int(activation == "silu"),
                                unit_heads=unit_heads, unit_dim=unit_dim, eps=eps, weight=weight.data_ptr())
         if bias is not None:
-            self._desc.bias = _need(bias, "bias", weight.device, weight.dtype, (self.C,))
+            self._desc.bias = _need(bias, "bias", weight.device, weight.dtype, (self._C,))
 
     def state(self, n):
         """Zero states for n requests."""
         import torch
 
         w = self._keep[0]
-        return torch.zeros((n, self.W - 1, self.C), dtype=w.dtype, device=w.device)
+        return torch.zeros((n, self._W - 1, self._C), dtype=w.dtype, device=w.device)
 
     def forward(self, x, state, cu_q, *, ctx_len=None, state_index=None, state_out=None, y=None, stream=None):
         """x [T, C], state [slots, W - 1, C] of the weight's type (rows in front of a request's first, oldest
@@ -1041,16 +1043,16 @@ class ShortConv:
         if _dtype(x, "x") != d.dtype or _dtype(state, "state") != d.dtype:
             _bad("x, state and weight differ in type")
         d.T, d.R, d.n_states = T, R, state.shape[0]
-        d.x, d.ld_x = _rows(x, "x", dev, (T, self.C))
+        d.x, d.ld_x = _rows(x, "x", dev, (T, self._C))
         on = _OnStream(stream, dev)
         if y is None:
             y = on.like(x)
-            d.y, d.ld_y = y.data_ptr(), self.C
+            d.y, d.ld_y = y.data_ptr(), self._C
         else:
             if _dtype(y, "y") != d.dtype:
                 _bad("y and x differ in type")
-            d.y, d.ld_y = _rows(y, "y", dev, (T, self.C))
-        shape = (state.shape[0], self.W - 1, self.C)
+            d.y, d.ld_y = _rows(y, "y", dev, (T, self._C))
+        shape = (state.shape[0], self._W - 1, self._C)
         d.state_in = _need(state, "state", dev, None, shape)
         if state_out is None:
             state_out = _copy_of(state, on) if state_index is not None or shape[0] > R else on.like(state)
