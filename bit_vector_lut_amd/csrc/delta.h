@@ -22,6 +22,7 @@ struct DeltaArgs {
     int64_t seg_units;
     int64_t id0;       // number of the launch's first workgroup
     int L;             // tokens of a segment
+    int few;           // requests of up to so many tokens go through the recurrence, the others in chunks
     int hk, hv, Dk, Dv;
     float scale;
 

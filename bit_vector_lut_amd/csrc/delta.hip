@@ -4,13 +4,13 @@
 #include "delta.h"
 
 #include <algorithm>
+#include <climits>
 
 namespace vqmlp {
 
 namespace {
 
 constexpr int64_t kMaxLd = 1 << 24;
-constexpr int kStepMaxQ = 16;  // up to here token by token
 
 // ---------------------------------------------------------------- the recurrence
 // A wave owns a head's Dk x 32 (or 16) columns of the state: lane = (row block, four columns), a row block's
@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
         return;
     }
     const int c0 = packed_row(a.p, r), n = packed_row(a.p, r + 1) - c0;
+    if (n > a.few) return;
     bool old;
     const int slot = packed_slot(a.p, r, &old);
     const int64_t base = (int64_t(max(slot, 0)) * a.hv + h) * a.Dk * a.Dv;
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
 
 struct DeltaGeom {
     bool step, split;
+    int few;                   // with chunks: requests of up to so many tokens through the recurrence first
     int L;                     // tokens of a segment
     size_t images, seg, bytes;  // where they start; in all
     int64_t seg_units;
@@ -145,7 +147,13 @@ struct DeltaGeom {
 
 DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     DeltaGeom G{};
-    G.step = d.max_q <= kStepMaxQ;
+    // A token of the recurrence takes 0.6 us, or more where its waves fill the card; a chunk takes the same for one token
+    // as for 64.  They meet at 21 tokens for one request of up to 48 heads (20 us), 28 for eight (50 us) and
+    // 45 for 64 (370 us).  Requests of different lengths that fill the card with a chunk each (64 requests of 48
+    // heads, 63 of them with one token, one with 512: 377 us in chunks, 143 so) go each its own way.
+    const int64_t heads = int64_t(d.R) * d.v_heads;
+    const int few = heads >= 8 * cus ? 40 : heads >= cus ? 28 : 20;
+    G.step = d.max_q <= few;
     if (G.step) return G;
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
@@ -153,6 +161,7 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     // time a segment) and two more launches (6 chunks' time).  A compute unit holds two workgroups of 32 columns.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T))), chunks = (most + kDeltaC - 1) / kDeltaC;
     const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
+    G.few = heads >= cus && !even ? few : -1;
     const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32, slots = cus;
     auto rounds = [&](int64_t wgs) { return double((wgs * d.v_heads + slots - 1) / slots); };
     // whole requests: the longest, or what all give each compute unit to do and a part of the other
@@ -191,11 +200,18 @@ vqmlp_status delta_check(const vqmlp_delta_desc* p, const char* who) {
 
 template <class E>
 void launch_step(const DeltaArgs& a, int cus, hipStream_t s) {
-    const dim3 grid(a.p.R + 1, a.hv, (a.Dv + 31) / 32), narrow(a.p.R + 1, a.hv, (a.Dv + 15) / 16);
+    const int units = a.p.R + (a.few == INT_MAX);  // and the rows behind the last request, if no chunks follow
+    const dim3 grid(units, a.hv, (a.Dv + 31) / 32), narrow(units, a.hv, (a.Dv + 15) / 16);
     if (a.Dk <= 64) k_delta_step<E, 8, 8><<<grid, 64, 0, s>>>(a);
     // half the columns and rows a lane where waves of 32 columns are fewer than the chip's SIMDs
     else if (int64_t(a.p.R) * a.hv * grid.z <= 4 * int64_t(cus)) k_delta_step<E, 8, 16><<<narrow, 64, 0, s>>>(a);
     else k_delta_step<E, 16, 8><<<grid, 64, 0, s>>>(a);
+}
+
+template <class E>
+void launch_delta(const DeltaArgs& a, bool chunks, int cus, hipStream_t s) {
+    if (a.few > 0) launch_step<E>(a, cus, s);
+    if (chunks) launch_delta_chunks<E>(a, cus, s);
 }
 
 }  // namespace
@@ -262,16 +278,13 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
     a.seg = G.split ? reinterpret_cast<float*>(a.blocks + G.seg) : nullptr;
     a.seg_units = G.seg_units;
     a.L = G.L;
+    a.few = G.step ? INT_MAX : G.few;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (G.step) {
-        if (d.dtype == VQMLP_F16) launch_step<F16>(a, cus, s);
-        else launch_step<BF16>(a, cus, s);
-    } else {
-        if (d.dtype == VQMLP_F16) launch_delta_chunks<F16>(a, cus, s);
-        else launch_delta_chunks<BF16>(a, cus, s);
-    }
+    if (d.dtype == VQMLP_F16) launch_delta<F16>(a, !G.step, cus, s);
+    else launch_delta<BF16>(a, !G.step, cus, s);
     if (trace_enabled())
-        trace_line("delta_rule T=%d R=%d heads=%d/%d: %s of %d tokens", d.T, d.R, d.v_heads, d.k_heads,
+        trace_line("delta_rule T=%d R=%d heads=%d/%d: %s%s of %d tokens", d.T, d.R, d.v_heads, d.k_heads,
+                   G.few > 0 ? "recurrence of short requests, " : "",
                    G.step ? "recurrence" : G.split ? "segment states, join, then segments" : "chunks, segments", G.step ? 1 : G.L);
     return op_launched("vqmlp_delta_rule");
 }

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             *reinterpret_cast<u32x4*>(a.y + (t0 + i / row) * a.ld_y + int64_t(h0) * a.Dv + i % row * 8) = u32x4{0, 0, 0, 0};
         return;
     }
-    if (m <= 0) return;
+    if (m <= 0 || u.n <= a.few) return;
     uint16_t* const image = a.image(x, hk, DKP, HALF);
     const bool first = h0 % heads == 0;
     const u32x4 none = {0, 0, 0, 0};
@@ -465,17 +465,29 @@ struct ScanSmem {
     __attribute__((aligned(16))) int unit[kCols], from[kCols];  // of a column: e, first token without a number
 };
 
-// Whole requests: the longest first, or a long one starts when the others are done.  Up to 64 requests.
-__device__ __forceinline__ int nth_longest(const Packed& p, int x) {
-    if (p.R > 64) return x;
+// Whole requests: the longest first, or a long one starts when the others are done.  Up to 64 requests; of more the
+// x-th that the recurrence leaves, -1 where there is none.
+__device__ __forceinline__ int nth_request(const Packed& p, int few, int x) {
     const int lane = threadIdx.x & 63;
-    const int n = lane < p.R ? packed_row(p, lane + 1) - packed_row(p, lane) : -1;
-    int rank = 0;
-    for (int j = 0; j < p.R; ++j) {
-        const int m = __builtin_amdgcn_readlane(n, j);
-        rank += m > n || (m == n && j < lane);
+    auto length = [&](int r) { return r < p.R ? packed_row(p, r + 1) - packed_row(p, r) : -1; };
+    if (p.R <= 64) {
+        const int n = length(lane);
+        int rank = 0;
+        for (int j = 0; j < p.R; ++j) {
+            const int m = __builtin_amdgcn_readlane(n, j);
+            rank += m > n || (m == n && j < lane);
+        }
+        return __builtin_ctzll(__ballot(rank == x && lane < p.R) | 1ull << 63);
     }
-    return __builtin_ctzll(__ballot(rank == x && lane < p.R) | 1ull << 63);
+    if (few < 0) return x;
+    for (int r = 0; r < p.R; r += 64) {
+        const bool mine = length(r + lane) > few;
+        const uint64_t mask = __ballot(mine);
+        const int count = __builtin_popcountll(mask);
+        if (x < count) return r + __builtin_ctzll(__ballot(mine && __builtin_popcountll(mask & ((1ull << lane) - 1)) == x) | 1ull << 63);
+        x -= count;
+    }
+    return -1;
 }
 
 // Two waves for each 16 columns of the state: one has the chain from state to state, the other the
@@ -501,7 +513,8 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
     const bool ones = !OUT && j0 >= slices;  // columns of M
     const int i0 = ones ? (j0 - slices) * kCols : v0;
     PackedUnit u;
-    if (!packed_unit(a.p, a.L, a.seg || x >= a.p.R ? x : nth_longest(a.p, x), u) || u.r >= a.p.R) return;
+    const int number = a.seg || x >= a.p.R ? x : nth_request(a.p, a.few, x);
+    if (number < 0 || !packed_unit(a.p, a.L, number, u) || u.r >= a.p.R || u.n <= a.few) return;
     if (!OUT && (u.seg == u.nseg - 1 || (ones && u.seg == 0))) return;
     const int tid = threadIdx.x, lane = tid & 63, both = uniform(tid >> 6), wave = both % kPairs;
     const int lr = lane & 15, g4 = lane >> 4;
@@ -972,7 +985,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 
 // The states in front of a request's segments, S_{g+1} = M_g S_g + B_g, in FP32.  A workgroup owns 16 columns, a wave
 // two tiles of 16 rows; a step of the products takes one row of each lane group's four, so that a result goes to
-// the next product as it stands, through LDS to the other waves.  The next M is on its way meanwhile.  S_{g+1} takes
+// the next product as it stands, through LDS to the other waves.   S_{g+1} takes
 // the place of B_g; the place of the last segment, which has no B, gets the first state, since the second
 // launch may write the request's slot before a segment would read it.
 template <int DKP>
@@ -1041,7 +1054,8 @@ void launch(DeltaArgs a, int cus, hipStream_t s) {
     const int64_t prep = (units * a.hk + 7) / 8 * 8 * (heads / per);
     for (a.id0 = 0; a.id0 < prep; a.id0 += most)
         k_delta_prep<E, DKP><<<unsigned(std::min(most, prep - a.id0)), 256, 0, s>>>(a, per);
-    const int64_t segs = int64_t(a.p.T) / a.L + a.p.R + 1;
+    // beside the recurrence: no more requests than can be long enough
+    const int64_t segs = a.seg || a.few < 0 ? int64_t(a.p.T) / a.L + a.p.R + 1 : std::min<int64_t>(a.p.R, a.p.T / (a.few + 1));
     const int64_t scans = (segs * a.hv + 7) / 8 * 8;
     if (a.seg) {
         const int64_t most1 = scans * (slices + (a.Dk + kCols - 1) / kCols);

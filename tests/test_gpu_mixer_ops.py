@@ -283,6 +283,46 @@ def test_delta_rule_many_requests_find_their_rows(vq, torch_dev):
         _delta_check(vq, torch, "f16", lens, 1, 1, 8, 8, 64, seed=seed, pad=3)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hk,hv,dk,dv", [(2, 24, 64, 40), (12, 12, 128, 128)])
+def test_delta_rule_short_and_long_requests_together(vq, torch_dev, dtype, hk, hv, dk, dv):
+    """Enough heads and requests that the short ones go token by token beside the others' chunks."""
+    lens = [1, 0, 200, 1, 28, 29, 2, 64, 1, 0, 65, 3] + [1] * 20
+    R, n = len(lens), len(lens) + 3
+    index = [(11 * r + 2) % n for r in range(R)]  # 11 and n share no factor: no slot twice
+    index[0], index[2], index[8] = -1, n, n + 5
+    ctx = [r % 3 for r in range(R)]
+    _delta_check(vq, torch_dev, dtype, lens, hk, hv, dk, dv, 200, ctx=ctx, index=index, n_states=n, pad=7)
+    _delta_check(vq, torch_dev, dtype, lens, hk, hv, dk, dv, 200, ctx=ctx, in_place=True)
+    lens = [1] * 63 + [70, 1, 41] + [2, 0] * 90 + [29, 40, 130] + [1] * 10  # more than 64 requests
+    _delta_check(vq, torch_dev, dtype, lens, hk, hv, dk, dv, 200, in_place=True, pad=2)
+
+
+def test_delta_rule_recurrence_and_chunks_agree_in_a_graph(vq, torch_dev):
+    """Which requests are short may change between replays."""
+    torch = torch_dev
+    R, T = 40, 700
+    op = vq.DeltaRule(4, 8, 64, 64)
+    args = [x.cuda() for x in _delta_inputs(torch, torch.float16, T, 4, 8, 64, 64, 3)]
+    state, s = torch.randn(R, 8, 64, 64, device="cuda"), torch.empty(R, 8, 64, 64, device="cuda")
+    first, other = [1] * 39 + [661], [300, 361] + [1] * 37 + [0]
+    cu, y = _i(torch, _starts(first)), torch.empty_like(args[2])
+    work = torch.full((op.workspace_bytes(T, R, T),), 255, dtype=torch.uint8, device="cuda")
+    op.forward(*args, state, cu, max_q=T, state_out=s, y=y, workspace=work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.forward(*args, state, cu, max_q=T, state_out=s, y=y, workspace=work)
+    for lens in (first, other, [17] * 40, first):
+        cu.copy_(_i(torch, _starts(lens)))
+        y.fill_(7.0)
+        work.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        y1, s1 = op.forward(*args, state, cu, max_q=T)
+        assert torch.equal(y, y1) and torch.equal(s, s1), lens
+        assert (y[sum(lens):] == 0).all()
+
+
 def test_delta_rule_strides_streams_and_graphs(vq, torch_dev):
     torch = torch_dev
     op = vq.DeltaRule(2, 4, 64, 64)
