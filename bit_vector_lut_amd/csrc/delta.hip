@@ -17,6 +17,10 @@ constexpr int64_t kMaxLd = 1 << 24;
 // rows contiguous so that a token's q and k come as 16-byte chunks.  Both sums over the rows are taken over
 // the state before the token: y_t = scale (e^{g} S^T q + (k . q) u), so one round of lane moves serves both.
 // No LDS and no barrier.
+// Many requests: bound by reading and writing the states (64 requests of 48 heads of 128 x 128, a token each: 402 MB
+// in 73 to 87 us).  Few: by a wave's own instructions, 0.6 us a token behind 5 us for the launch, the search
+// and the state (8 tokens of one request, 48 heads: 9.6 us).  Half the columns a wave there; a quarter, with
+// 32 lanes to a column, was slower (12.1 us), and more tokens read ahead (8 instead of 2) gave nothing.
 template <class E, int RPL, int RB>  // rows per lane, row blocks: Dk <= RPL RB
 __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
     constexpr int CB = 64 / RB;
@@ -24,6 +28,7 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
     const int lane = threadIdx.x, cb = lane % CB, rb = lane / CB;
     const int col = (blockIdx.z * CB + cb) * 4, row0 = rb * RPL;
     const bool cin = col < a.Dv;
+    const int own = col + (lane >> 5) + (lane >> 3 & 2);  // the column whose sums a row of 16 lanes ends up with
     if (r == a.p.R) {  // rows behind the last request
         for (int64_t t = packed_row(a.p, r) + rb; t < a.p.T; t += RB)
             if (cin) *reinterpret_cast<u32x2*>(a.y + t * a.ld_y + int64_t(h) * a.Dv + col) = u32x2{0, 0};
@@ -39,7 +44,7 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
     constexpr int CH = RPL / 8, AHEAD = 2;
     struct Token {
         u32x4 k[CH], q[CH];
-        u32x2 v;
+        uint16_t v;
         float g, beta;
     } ring[AHEAD];
     auto fetch = [&](int t, Token& x) __attribute__((always_inline)) {
@@ -51,31 +56,49 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
                 x.q[c] = *reinterpret_cast<const u32x4*>(a.q + t * a.ld_q + int64_t(hk) * a.Dk + row0 + 8 * c);
             }
         }
-        x.v = u32x2{0, 0};
-        if (cin) x.v = *reinterpret_cast<const u32x2*>(a.v + t * a.ld_v + int64_t(h) * a.Dv + col);
+        x.v = 0;
+        if (cin) x.v = a.v[t * a.ld_v + int64_t(h) * a.Dv + own];
         x.g = a.g[t * a.ld_g + h];
         x.beta = a.beta[t * a.ld_b + h];
     };
-    // Sum over the row blocks, in all lanes.  The operands of a swap are two values to the compiler.
-    auto swapped = [](float v, auto&& swap) __attribute__((always_inline)) {
-        const int x = __builtin_bit_cast(int, v);
-        const auto z = swap(uint32_t(x), uint32_t(fresh(x)));
-        const uint32_t z0 = z[0], z1 = z[1];
-        return __builtin_bit_cast(float, z0) + __builtin_bit_cast(float, z1);
+    // Sums over the row blocks.  Of four columns at once each swap of halves or of rows halves how many a lane has,
+    // until it has one: 3 swaps instead of 8.
+    struct Two {
+        float x, y;
     };
-    auto half = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane32_swap(x, y, false, false); };
-    auto row = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_permlane16_swap(x, y, false, false); };
-    auto all = [&](float v) __attribute__((always_inline)) {
-        v = swapped(swapped(v, half), row);
+    auto half = [](float x, float y) __attribute__((always_inline)) {  // halves (x, y), in the other (x, y)
+        const auto z = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
+        const uint32_t z0 = z[0], z1 = z[1];
+        return Two{__builtin_bit_cast(float, z0), __builtin_bit_cast(float, z1)};
+    };
+    auto row = [](float x, float y) __attribute__((always_inline)) {  // rows of 16 lanes x, y, x, y
+        const auto z = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
+        const uint32_t z0 = z[0], z1 = z[1];
+        return Two{__builtin_bit_cast(float, z0), __builtin_bit_cast(float, z1)};
+    };
+    // one value twice: two values to the compiler, as a swap writes both
+    auto twice = [](float x) __attribute__((always_inline)) {
+        return __builtin_bit_cast(float, fresh(__builtin_bit_cast(int, x)));
+    };
+    auto in_row = [&](float v) __attribute__((always_inline)) {
         v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128, 0xF, 0xF, false));
         if constexpr (RB == 16)
             v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x124, 0xF, 0xF, false));
         return v;
     };
+    auto all = [&](float v) __attribute__((always_inline)) {
+        const Two p = half(v, twice(v));
+        const float w = p.x + p.y;
+        const Two q = row(w, twice(w));
+        return in_row(q.x + q.y);
+    };
+    auto each = [&](const f32x4& v) __attribute__((always_inline)) {  // of the lane's own column
+        const Two p = half(v[0], v[1]), q = half(v[2], v[3]), r = row(p.x + p.y, q.x + q.y);
+        return in_row(r.x + r.y);
+    };
     auto token = [&](int t, const Token& x) __attribute__((always_inline)) {
-        const f32x4 v = {lo16<E>(x.v[0]), hi16<E>(x.v[0]), lo16<E>(x.v[1]), hi16<E>(x.v[1])};
         const float e = exp_f32(bounded(x.g));
-        f32x4 sk = {0.f, 0.f, 0.f, 0.f}, sq = sk, u;
+        f32x4 sk = {0.f, 0.f, 0.f, 0.f}, sq = sk;
         float kq = 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -90,15 +113,11 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
                     sq[i] = fmaf(qq, s[8 * c + j][i], sq[i]);
                 }
             }
-        kq = all(kq);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u[i] = x.beta * fmaf(-e, all(sk[i]), v[i]);
-            sq[i] = a.scale * fmaf(kq, u[i], e * all(sq[i]));
-        }
-        if (rb == 0 && cin)
-            *reinterpret_cast<u32x2*>(a.y + int64_t(t) * a.ld_y + int64_t(h) * a.Dv + col) =
-                u32x2{pack16<E>(sq[0], sq[1]), pack16<E>(sq[2], sq[3])};
+        const float one = x.beta * fmaf(-e, each(sk), lo16<E>(x.v)), y = a.scale * fmaf(all(kq), one, e * each(sq));
+        if ((lane & 15) < CB && cin) a.y[int64_t(t) * a.ld_y + int64_t(h) * a.Dv + own] = uint16_t(pack16<E>(y, y));
+        // the four columns' u from the four rows
+        const Two p = row(one, twice(one)), u01 = half(p.x, twice(p.x)), u23 = half(p.y, twice(p.y));
+        const f32x4 u = {u01.x, u01.y, u23.x, u23.y};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
