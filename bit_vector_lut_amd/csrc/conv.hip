@@ -14,7 +14,7 @@
 // (104 -> 73 us); units of 16 tokens instead of 32 (-> 66; 64: 74). Eight rows on their way need 172
 // registers, and two waves on a SIMD instead of four cost more than the loads give (130 us).
 // Bound by latency for few tokens: the search for the unit, one round of loads, one row's sums.
-// 8 tokens in 4.5 us, 64 requests with a token each in 6.4 us.
+// 8 tokens in 5.1 us, 64 requests with a token each in 5.8 us.
 #include "op.h"
 
 #include <algorithm>
@@ -239,12 +239,10 @@ extern "C" vqmlp_status vqmlp_short_conv(const vqmlp_conv_desc* p, void* stream)
     while (a.lanes * 8 < a.unit_dim) a.lanes *= 2;
     a.unit_sets = (d.unit_heads * a.lanes + 63) / 64;
     a.sets = a.unit_sets + (d.C - d.unit_heads * a.unit_dim + 511) / 512;
-    // Tokens of a unit: 16 (15) where there are tokens enough for two waves on each of the card's SIMDs,
-    // in whole rounds of rows; with fewer tokens shorter units, down to one token (8 tokens of 10,240
-    // channels: 4.5 us with units of one, 10 us with one unit).
+    // Tokens of a unit: whole rounds of rows, 16 (15) where there are tokens enough for two waves on each of the card's
+    // SIMDs, fewer where not.  Never fewer than W - 1: the second unit would read the state that the first writes.
     const int step = d.W == 3 ? 3 : 4;
-    a.L = int(std::min<int64_t>(16, std::max<int64_t>(1, int64_t(d.T) * a.sets / (8 * cus))));
-    if (a.L > step) a.L -= a.L % step;
+    a.L = int(std::min<int64_t>(16 / step, std::max<int64_t>(1, int64_t(d.T) * a.sets / (8 * cus * step)))) * step;
     const int64_t units = d.T / a.L + d.R + 1, all = units * ((a.sets + 3) / 4);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (d.dtype == VQMLP_F16) launch_conv<F16>(a, d.W, all, s);
