@@ -21,6 +21,7 @@ struct DeltaArgs {
     float* seg;
     int64_t seg_units;
     int64_t id0;       // number of the launch's first workgroup
+    int h0;            // of the recurrence: the launch's first head
     int L;             // tokens of a segment
     int few;           // requests of up to so many tokens go through the recurrence, the others in chunks
     int hk, hv, Dk, Dv;

@@ -24,7 +24,7 @@ constexpr int64_t kMaxLd = 1 << 24;
 template <class E, int RPL, int RB>  // rows per lane, row blocks: Dk <= RPL RB
 __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
     constexpr int CB = 64 / RB;
-    const int r = blockIdx.x, h = blockIdx.y;
+    const int r = blockIdx.x, h = a.h0 + blockIdx.y;
     const int lane = threadIdx.x, cb = lane % CB, rb = lane / CB;
     const int col = (blockIdx.z * CB + cb) * 4, row0 = rb * RPL;
     const bool cin = col < a.Dv;
@@ -186,7 +186,7 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     // whole requests: the longest, or what all give each compute unit to do and a part of the other
     const double share = double(d.T) / kDeltaC * vs * d.v_heads / slots;
     double best = even ? rounds(d.R * vs) * chunks : std::max<double>(chunks, share) + 0.25 * std::min<double>(chunks, share);
-    for (int n = 4; n < chunks; ++n) {
+    for (int n = 4; n < chunks && heads < 64 * cus; ++n) {  // more of them fill the card in any case
         const int64_t per = (chunks + n - 1) / n, units = even ? d.R * per : std::max<int64_t>(d.T / (n * kDeltaC) + d.R / 2, d.R);
         const int64_t inner = units > d.R ? units - d.R : 0;  // segments but the last; M of those but the first
         const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + 1.6 * per + 6;
@@ -218,13 +218,18 @@ vqmlp_status delta_check(const vqmlp_delta_desc* p, const char* who) {
 }
 
 template <class E>
-void launch_step(const DeltaArgs& a, int cus, hipStream_t s) {
+void launch_step(DeltaArgs a, int cus, hipStream_t s) {
     const int units = a.p.R + (a.few == INT_MAX);  // and the rows behind the last request, if no chunks follow
-    const dim3 grid(units, a.hv, (a.Dv + 31) / 32), narrow(units, a.hv, (a.Dv + 15) / 16);
-    if (a.Dk <= 64) k_delta_step<E, 8, 8><<<grid, 64, 0, s>>>(a);
     // half the columns and rows a lane where waves of 32 columns are fewer than the chip's SIMDs
-    else if (int64_t(a.p.R) * a.hv * grid.z <= 4 * int64_t(cus)) k_delta_step<E, 8, 16><<<narrow, 64, 0, s>>>(a);
-    else k_delta_step<E, 16, 8><<<grid, 64, 0, s>>>(a);
+    const bool narrow = a.Dk > 64 && int64_t(a.p.R) * a.hv * ((a.Dv + 31) / 32) <= 4 * int64_t(cus);
+    const int cols = narrow ? (a.Dv + 15) / 16 : (a.Dv + 31) / 32;
+    const int most = int(((int64_t(1) << 25) / units + cols - 1) / cols);  // heads: a launch holds fewer than 2^32 threads
+    for (a.h0 = 0; a.h0 < a.hv; a.h0 += most) {
+        const dim3 grid(units, std::min(most, a.hv - a.h0), cols);
+        if (narrow) k_delta_step<E, 8, 16><<<grid, 64, 0, s>>>(a);
+        else if (a.Dk <= 64) k_delta_step<E, 8, 8><<<grid, 64, 0, s>>>(a);
+        else k_delta_step<E, 16, 8><<<grid, 64, 0, s>>>(a);
+    }
 }
 
 template <class E>

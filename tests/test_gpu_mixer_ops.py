@@ -323,6 +323,22 @@ def test_delta_rule_recurrence_and_chunks_agree_in_a_graph(vq, torch_dev):
         assert (y[sum(lens):] == 0).all()
 
 
+def test_delta_rule_more_threads_than_a_launch_holds(vq, torch_dev):
+    """65,535 requests of 1,200 heads: 5.0e9 threads for the recurrence."""
+    torch = torch_dev
+    R, hv = 65535, 1200
+    q, k, v, g, beta = _delta_inputs(torch, torch.float16, 3, 1, hv, 8, 8, 2)
+    cu = torch.zeros(R + 1, dtype=torch.int32)
+    cu[-1], cu[-2] = 3, 1  # the first token to the last request but one, two to the last
+    op = vq.DeltaRule(1, hv, 8, 8)
+    print("delta", R, hv, flush=True)
+    y, _ = op.forward(*(x.cuda() for x in (q, k, v, g, beta)), torch.empty(0, hv, 8, 8, device="cuda"), cu.cuda(), max_q=4)
+    state = torch.zeros(2, hv, 8, 8)
+    ry, B, Z, _, _ = _delta_ref(torch, q, k, v, g, beta, state, [0, 1, 3], None, None, op.scale)
+    u, c = _u(torch, torch.float16), 2 * (8 + 64) * W
+    _close(torch, y, ry, u * ry.abs() + (2 * u + c) * B + c * Z + 2.0 ** -25, "y")
+
+
 def test_delta_rule_strides_streams_and_graphs(vq, torch_dev):
     torch = torch_dev
     op = vq.DeltaRule(2, 4, 64, 64)
@@ -700,6 +716,21 @@ def test_short_conv_large_inputs(vq, torch_dev):
     y, s = op.forward(x, op.state(1), _i(torch, [0, 9]))
     bad = ~y.isfinite()
     assert bad[3:7, 9].all() and bad[4:8, 10].all() and int(bad.sum()) == 8
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_short_conv_few_tokens_in_place(vq, torch_dev, dtype, W):
+    """A request's later tokens read its old state too, while its new one is written."""
+    torch = torch_dev
+    dt, C = _t(torch, dtype), 2048
+    op = vq.ShortConv(_randn(torch, (C, W), dt, 1).cuda(), unit_heads=4, unit_dim=128)
+    for lens in ([1], [2], [3], [5], [2, 3, 1, 8], [2] * 40, [3, 4] * 100):
+        cu, T = _i(torch, _starts(lens)), sum(lens)
+        x, state = _randn(torch, (T, C), dt, 2).cuda(), _randn(torch, (len(lens), W - 1, C), dt, 3).cuda()
+        y, new = op.forward(x, state, cu)
+        y1, same = op.forward(x, state, cu, state_out=state)
+        assert same is state and torch.equal(y, y1) and torch.equal(state, new), lens
 
 
 def test_short_conv_strides_streams_and_graphs(vq, torch_dev):
