@@ -176,20 +176,26 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     if (G.step) return G;
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
-    // In segments a request's chain is walked twice, a segment's length each time, with a join between (of a chunk's
-    // time a segment) and two more launches (6 chunks' time).  A compute unit holds two workgroups of 32 columns.
+    // Costs in a chunk's time (1.9 us).  In segments a request's chain is walked twice, a segment's length each time, with
+    // a join between (3.3 us a segment) and two more launches.  A compute unit holds two workgroups of 32 columns,
+    // which then take a quarter longer; an XCD fills up before all of them do.  8,000 tokens of 6 heads of
+    // 128 x 128: 259 us whole, 121 in segments of 12 chunks, 129 of 21, 143 of 9; of 24 heads 282, 230 of 32, 271 of
+    // 18; of 48 heads 318, 412 of 32.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T))), chunks = (most + kDeltaC - 1) / kDeltaC;
     const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
     G.few = heads >= cus && !even ? few : -1;
-    const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32, slots = cus;
-    auto rounds = [&](int64_t wgs) { return double((wgs * d.v_heads + slots - 1) / slots); };
+    const int64_t vs = (d.Dv + 31) / 32, ks = (d.Dk + 31) / 32;
+    auto rounds = [&](int64_t wgs) {
+        const int64_t n = wgs * d.v_heads * 17 / 16, rest = n % (2 * cus);
+        return 1.25 * double(n / (2 * cus)) + (rest == 0 ? 0. : rest <= cus ? 1. : 1.25);
+    };
     // whole requests: the longest, or what all give each compute unit to do and a part of the other
-    const double share = double(d.T) / kDeltaC * vs * d.v_heads / slots;
+    const double share = 0.625 * double(d.T) / kDeltaC * vs * d.v_heads / cus;
     double best = even ? rounds(d.R * vs) * chunks : std::max<double>(chunks, share) + 0.25 * std::min<double>(chunks, share);
-    for (int n = 4; n < chunks && heads < 64 * cus; ++n) {  // more of them fill the card in any case
+    for (int n = 5; n < chunks && heads < 64 * cus; n += std::max(1, n / 8)) {  // more heads fill the card in any case
         const int64_t per = (chunks + n - 1) / n, units = even ? d.R * per : std::max<int64_t>(d.T / (n * kDeltaC) + d.R / 2, d.R);
         const int64_t inner = units > d.R ? units - d.R : 0;  // segments but the last; M of those but the first
-        const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + 1.6 * per + 6;
+        const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + 1.8 * per + 1;
         if (cost < best) best = cost, G.split = true, G.L = n * kDeltaC;
     }
     const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
