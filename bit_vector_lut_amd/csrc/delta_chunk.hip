@@ -16,6 +16,11 @@
 // binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  For
 // the outputs, which have 16 bits, P, U and S are one binary16 part.  The triangular system is
 // solved in FP32.
+//
+// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 256 us a call, where
+// the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
+// between them: 1.9 us alone on a compute unit, 2.5 beside another workgroup, of which the matrix cores work 0.6.
+// k_delta_prep (71 us of it) writes 151 MB and reads 66: 62% of a copy's rate, with LDS and the triangular solve.
 #include "delta.h"
 
 #include <algorithm>
@@ -987,7 +992,9 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 // two tiles of 16 rows; a step of the products takes one row of each lane group's four, so that a result goes to
 // the next product as it stands, through LDS to the other waves.   S_{g+1} takes
 // the place of B_g; the place of the last segment, which has no B, gets the first state, since the second
-// launch may write the request's slot before a segment would read it.
+// launch may write the request's slot before a segment would read it.  A step takes 3.3 us, of which the matrix cores
+// 1: a compute unit gets 64 KB of M at some 16 bytes a cycle.  The next M but one read ahead, and the slices of
+// a head on one XCD, gave 2 of 30 us.
 template <int DKP>
 __global__ void __launch_bounds__(32 * (DKP / 16)) k_delta_join(DeltaArgs a) {
     constexpr int NT = DKP / 16;

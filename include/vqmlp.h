@@ -492,7 +492,9 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  *   S_t = S' + k_t u_t^T,       y_t = scale * S_t^T q_t.
  * beta FP32 [T][v_heads] (token stride ld_beta).  Everything else as in the linear attention above: the arrays, their
  * strides and types, g and its bounds, states, slots, ctx_len, cu_q, rows behind the last request, max_q,
- * the workspace's rules and the limits.  Keys are meant to have length one and beta to lie in [0, 2];
+ * the workspace's rules and T and R's limits.  max_q up to 20 to 40, by how many heads and requests there are,
+ * takes the recurrence; above, short requests may take it beside the others' chunks, and few long ones go through
+ * their chunks in segments.  Keys are meant to have length one and beta to lie in [0, 2];
  * beyond, the recurrence itself may grow without bound.  What is not finite in k, g or beta makes the outputs
  * of its head from its token on and the state NaN, in v those of its column, in q its own outputs. */
 typedef struct {
