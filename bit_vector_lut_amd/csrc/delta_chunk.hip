@@ -14,12 +14,14 @@
 // are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
 // element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
 // binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  For
-// the outputs, which have 16 bits, P, U and S are one binary16 part.  The triangular system is
+// the outputs, which have 16 bits, P is one binary16 part, and so are U and S for bfloat16 ones: binary16 outputs
+// would be 1.6 times as far off as their own rounding leaves them (3.4e-4), so there U and S are two (2.7e-4; 257 -> 268
+// us for three prompts).  The second parts go to the outputs' waves in the place of T, which they load again.  The triangular system is
 // solved in FP32.
 //
-// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 256 us a call, where
+// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 268 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
-// between them: 1.9 us alone on a compute unit, 2.5 beside another workgroup, of which the matrix cores work 0.6.
+// between them: 1.9 us alone on a compute unit, 2.6 beside another workgroup, of which the matrix cores work 0.6.
 // k_delta_prep (71 us of it) writes 151 MB and reads 66: 62% of a copy's rate, with LDS and the triangular solve.
 #include "delta.h"
 
@@ -579,6 +581,8 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int i = 0; i < (12 + kPairs) / kPairs; ++i) {
                 const int j = wave + kPairs * i;
+                // the second parts of the chunk before lie there, in the place of the wave's own pieces
+                if (OUT && HALF && i == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (j < 13) load_lds16(dp + j * 1024, lane * 16, at + int(offsetof(ChainStage<DKP>, d)) + j * 1024);
             }
             kp += kstep, vp += vstep, dp += dstep;
@@ -618,6 +622,14 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             return;
         }
         u32x2 y[4];
+        u32x4 low[KS + 2];  // second parts of the state and of U, for binary16 outputs
+        auto take = [&](int c) __attribute__((always_inline)) {
+            if constexpr (HALF) {
+                const u32x4(*const at)[64] = reinterpret_cast<const u32x4(*)[64]>(&sm.chain[c & 1].d);
+#pragma unroll
+                for (int s = 0; s < KS + 2; ++s) low[s] = at[wave + kPairs * s][lane];
+            }
+        };
         auto outputs = [&]() __attribute__((always_inline)) {
             // what the chain has handed over of the chunk before, which stands until the next barrier
             u32x4 sh[KS], uo[2];
@@ -635,13 +647,18 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(sh[s], q[x][s], o[x]);
+                for (int z = 0; z < (HALF ? 2 : 1); ++z)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(z ? low[s] : sh[s], q[x][s], o[x]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[x] *= qf[x];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int z = 0; z < (HALF ? 2 : 1); ++z)
 #pragma unroll
-                for (int k = 0; k <= x / 2; ++k) o[x] = F16::mfma16(uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int k = 0; k <= x / 2; ++k)
+                        o[x] = F16::mfma16(z ? low[KS + k] : uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
             float down[4];
             bool all = true;
 #pragma unroll
@@ -667,6 +684,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         // Phase c: the chain's loads of chunk c + 1, which it waits for in the middle of chunk c; outputs of chunk c - 1;
         // loads for those of chunk c.
         for (int c = 0; c < nch; ++c) {
+            take(c + 1);  // of chunk c - 1, if there is one
             if (c + 1 < nch) load_chain(c + 1);
             if (c > 0) outputs();
             load_out();
@@ -678,6 +696,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             __syncthreads();  // the chain is done with chunk c
         }
         if (nch > 0) {
+            take(nch - 1);
             outputs();
             store(n - (nch - 1) * kC);
         }
@@ -790,7 +809,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         bool move = level >= 11 || (level < 5 && level != none);
         int aim = min(max(e + 10 - level, -120), 100);
         f32x4 U[2][2];
-        u32x4 sh[KS], uh[2], ul[2], uo[2];
+        u32x4 sh[KS], sl[KS], uh[2], ul[2], uo[2], uq[2];
         float unit, most;
         for (int again = 0;; ++again) {
             if (__builtin_expect(__any(move), 0)) {
@@ -801,7 +820,6 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             unit = pow2(e);
             most = 0.f;
             // K S, each step's parts of S made between the steps in front of it
-            u32x4 sl[KS];
             auto split = [&](int s) __attribute__((always_inline)) {
                 const float x[8] = {S[s][0][0], S[s][0][1], S[s][0][2], S[s][0][3], S[s][1][0], S[s][1][1], S[s][1][2], S[s][1][3]};
                 sh[s] = pack_hi(x);
@@ -884,6 +902,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             auto parts = [&](int p) __attribute__((always_inline)) {
                 float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
                 uo[p] = pack_hi(x);
+                if constexpr (OUT && HALF) uq[p] = pack_lo(x, uo[p]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
@@ -950,6 +969,11 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             for (int s = 0; s < KS; ++s) sm.sh[wave][s][lane] = sh[s];
 #pragma unroll
             for (int k = 0; k < 2; ++k) sm.uo[wave][k][lane] = uo[k];
+            if constexpr (HALF) {  // T is read; the outputs' wave loads these pieces of the next but one
+                u32x4(*const to)[64] = reinterpret_cast<u32x4(*)[64]>(&sm.chain[c & 1].d);
+#pragma unroll
+                for (int s = 0; s < KS + 2; ++s) to[wave + kPairs * s][lane] = s < KS ? sl[s] : uq[s - KS];
+            }
             if (g4 == 0) sm.unit[16 * wave + lr] = e, sm.from[16 * wave + lr] = lost ? 0 : late;
         }
         lost |= late < kC;
