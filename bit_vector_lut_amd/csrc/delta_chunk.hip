@@ -15,9 +15,9 @@
 // element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
 // binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  For
 // the outputs, which have 16 bits, P is one binary16 part, and so are U and S for bfloat16 ones: binary16 outputs
-// would be 1.6 times as far off as their own rounding leaves them (3.4e-4), so there U and S are two (2.7e-4; 257 -> 268
-// us for three prompts).  The second parts go to the outputs' waves in the place of T, which they load again.  The triangular system is
-// solved in FP32.
+// would be 1.6 times as far off as their own rounding leaves them (3.4e-4), so there U and S are two (2.7e-4;
+// 257 -> 268 us for three prompts).  The second parts go to the outputs' waves in the place of T, which they load
+// again.  The triangular system is solved in FP32.
 //
 // Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 268 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions

@@ -454,6 +454,30 @@ def test_delta_rule_segments_values_that_are_not_finite(vq, torch_dev, dtype, wh
         assert torch.equal(s[~lost], s0[~lost]) and s[lost].isnan().all(), t
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_delta_rule_segments_beside_short_requests(vq, torch_dev, dtype):
+    lens = [1] * 30 + [3000] + [5, 0, 300] * 5
+    R, n = len(lens), len(lens) + 1
+    assert _in_segments(vq, dtype, sum(lens), R, 1, 6, 64, 64, 3000)
+    index, ctx = [(5 * r + 3) % n for r in range(R)], [r % 4 for r in range(R)]  # 5 and 47 share no factor
+    assert len(set(index)) == R
+    _delta_check(vq, torch_dev, dtype, lens, 1, 6, 64, 64, 3000, ctx=ctx, index=index, n_states=n, pad=5)
+    _delta_check(vq, torch_dev, dtype, lens, 1, 6, 64, 64, 3000, ctx=ctx, in_place=True)
+
+
+@pytest.mark.parametrize("max_q", [1, 300])
+def test_no_tokens_at_all(vq, torch_dev, max_q):
+    """States pass through, or start from zero; nothing else happens."""
+    torch = torch_dev
+    _delta_check(vq, torch, "f16", [0, 0, 0], 2, 4, 64, 64, max_q, ctx=[1, 0, 2])
+    _delta_check(vq, torch, "bf16", [0, 0], 2, 4, 64, 64, max_q, pad=70, in_place=True)
+    conv = vq.ShortConv(torch.zeros(64, 4, dtype=torch.float16, device="cuda"))
+    state = torch.randn(2, 3, 64, device="cuda").half()
+    x = torch.empty(0, 64, dtype=torch.float16, device="cuda")
+    y, new = conv.forward(x, state, _i(torch, [0, 0, 0]), ctx_len=_i(torch, [1, 0]))
+    assert y.shape == (0, 64) and torch.equal(new[0], state[0]) and (new[1] == 0).all()
+
+
 def test_delta_rule_segments_in_a_graph(vq, torch_dev):
     """A poisoned workspace, other lengths and values between the replays."""
     torch = torch_dev
