@@ -605,8 +605,14 @@ def _rows(t, name, device, shape):
     """Pointer and token stride of [T, heads, D] (or [T, H]) whose rows are dense."""
     if t.device != device or t.shape != shape:
         _need(t, name, device, None, shape, contiguous=False)
-    inner = shape[1] if len(shape) == 2 else shape[1] * shape[2]
-    if t.is_contiguous():
+    st = t.stride()
+    if len(shape) == 2:
+        inner, dense = shape[1], st[1] == 1
+    else:
+        inner, dense = shape[1] * shape[2], st[2] == 1 and st[1] == shape[2]
+    if dense:
+        return t.data_ptr(), st[0] if shape[0] > 1 else inner
+    if t.is_contiguous():  # strides of dimensions of one element may be anything
         return t.data_ptr(), inner
     at = 1
     for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
@@ -872,22 +878,25 @@ class PagedCache:
 
         T, dev, i = k.shape[0], self._device, torch.int32
         _fits(T, "append")
-        if rotary.device != dev or rotary.dtype not in (None, self._dtype) or 2 * rotary.half > self._D:
+        if rotary._device != dev or rotary._dtype not in (None, self._dtype) or 2 * rotary._half > self._D:
             _bad("rotary does not fit the cache (device, type or D)")
         if _dtype(k, "k") != self._dtype or _dtype(v, "v") != self._dtype:
             _bad("k, v and the cache differ in type")
         d = _AppendDesc.from_buffer_copy(rotary._desc)
-        if rotary.D not in (None, self._D):
-            _bad("the norms' weights have %d elements for heads of %d" % (rotary.D, self._D))
+        if rotary._D not in (None, self._D):
+            _bad("the norms' weights have %d elements for heads of %d" % (rotary._D, self._D))
         d.dtype, d.T, d.kv_heads, d.D = self._dtype, T, self._kv_heads, self._D
         d.page_size, d.n_pages, d.k_cache, d.v_cache = self._page_size, self._n_pages, self._kp, self._vp
         shape = (T, self._kv_heads, self._D)
         d.k, d.ld_k, d.hs_k = _heads(k, "k", dev, shape)
         d.v, d.ld_v, d.hs_v = _heads(v, "v", dev, shape)
-        d.position = _need(position, "position", dev, i, (None,))
-        d.slot = _need(slot, "slot", dev, i, (None,))
-        if position.shape[0] < T or slot.shape[0] < T:
-            _bad("position has %d entries, slot %d for %d tokens" % (position.shape[0], slot.shape[0], T))
+        at, to = position.shape, slot.shape
+        if len(at) != 1 or len(to) != 1:
+            _bad("position and slot have to be [T]")
+        d.position = _need(position, "position", dev, i)
+        d.slot = _need(slot, "slot", dev, i)
+        if at[0] < T or to[0] < T:
+            _bad("position has %d entries, slot %d for %d tokens" % (at[0], to[0], T))
         if q is None and q_out is not None:
             _bad("q_out without q")
         on = _OnStream(stream, dev)
