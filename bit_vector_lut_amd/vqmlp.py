@@ -1022,7 +1022,7 @@ class ShortConv:
         if activation not in ("silu", None):
             _bad("unknown activation %r" % (activation,))
         _need(weight, "weight", weight.device, None, (None, None))
-        self._keep = weight, bias
+        self._keep, self._device, self._dtype = (weight, bias), weight.device, weight.dtype
         self._C, self._W = weight.shape
         _fits(self._C | self._W | unit_heads | unit_dim, "short convolution")
         self._desc = _ConvDesc(dtype=_dtype(weight, "weight"), C=self._C, W=self._W, silu=int(activation == "silu"),
@@ -1043,15 +1043,15 @@ class ShortConv:
         (y [T, C], state_out)."""
         import torch
 
-        dev, i, w = x.device, torch.int32, self._keep[0]
-        if x.dim() != 2 or w.device != dev:
+        dev, i, dt, size = x.device, torch.int32, self._dtype, x.shape
+        if len(size) != 2 or self._device != dev:
             _bad("x is [T, C] on the weight's device")
-        T, R = x.shape[0], cu_q.shape[0] - 1
-        _fits(T | R | state.shape[0], "short convolution")
+        T, R, n = size[0], cu_q.shape[0] - 1, state.shape[0]
+        _fits(T | R | n, "short convolution")
         d = _ConvDesc.from_buffer_copy(self._desc)
-        if _dtype(x, "x") != d.dtype or _dtype(state, "state") != d.dtype:
+        if (x.dtype != dt or state.dtype != dt) and (_dtype(x, "x") != d.dtype or _dtype(state, "state") != d.dtype):
             _bad("x, state and weight differ in type")
-        d.T, d.R, d.n_states = T, R, state.shape[0]
+        d.T, d.R, d.n_states = T, R, n
         d.x, d.ld_x = _rows(x, "x", dev, (T, self._C))
         on = _OnStream(stream, dev)
         if y is None:
@@ -1061,10 +1061,10 @@ class ShortConv:
             if _dtype(y, "y") != d.dtype:
                 _bad("y and x differ in type")
             d.y, d.ld_y = _rows(y, "y", dev, (T, self._C))
-        shape = (state.shape[0], self._W - 1, self._C)
+        shape = (n, self._W - 1, self._C)
         d.state_in = _need(state, "state", dev, None, shape)
         if state_out is None:
-            state_out = _copy_of(state, on) if state_index is not None or shape[0] > R else on.like(state)
+            state_out = _copy_of(state, on) if state_index is not None or n > R else on.like(state)
             d.state_out = state_out.data_ptr()
         else:
             if _dtype(state_out, "state_out") != d.dtype:
@@ -1222,30 +1222,30 @@ class DeltaRule:
         import torch
 
         dev, i, f = q.device, torch.int32, torch.float32
-        T, R = q.shape[0], cu_q.shape[0] - 1
+        T, R, n, kind = q.shape[0], cu_q.shape[0] - 1, state.shape[0], q.dtype
         dt = _dtype(q, "q")
-        if _dtype(k, "k") != dt or _dtype(v, "v") != dt:
+        if (k.dtype != kind or v.dtype != kind) and (_dtype(k, "k") != dt or _dtype(v, "v") != dt):
             _bad("q, k and v differ in type")
         if g.dtype != f or beta.dtype != f:
             _bad("g is %s and beta %s, not %s" % (g.dtype, beta.dtype, f))
         on = _OnStream(stream, dev)
-        d = self._desc(dt, T, R, state.shape[0], T if max_q is None else max_q)
+        d = self._desc(dt, T, R, n, T if max_q is None else max_q)
         d.q, d.ld_q = _rows(q, "q", dev, (T, self._k_heads, self._Dk))
         d.k, d.ld_k = _rows(k, "k", dev, (T, self._k_heads, self._Dk))
         d.v, d.ld_v = _rows(v, "v", dev, (T, self._v_heads, self._Dv))
         d.g, d.ld_g = _rows(g, "g", dev, (T, self._v_heads))
         d.beta, d.ld_beta = _rows(beta, "beta", dev, (T, self._v_heads))
         if y is None:
-            y = on.like(v) if v.dtype == q.dtype else on.empty(v.shape, q.dtype)
+            y = on.like(v) if v.dtype == kind else on.empty(v.shape, kind)
             d.y, d.ld_y = y.data_ptr(), self._v_heads * self._Dv
         else:
             if _dtype(y, "y") != dt:
                 _bad("y and q differ in type")
             d.y, d.ld_y = _rows(y, "y", dev, (T, self._v_heads, self._Dv))
-        shape = (state.shape[0], self._v_heads, self._Dk, self._Dv)
+        shape = (n, self._v_heads, self._Dk, self._Dv)
         d.state_in = _need(state, "state", dev, f, shape)
         if state_out is None:
-            state_out = _copy_of(state, on) if state_index is not None or shape[0] > R else on.like(state)
+            state_out = _copy_of(state, on) if state_index is not None or n > R else on.like(state)
             d.state_out = state_out.data_ptr()
         else:
             d.state_out = _need(state_out, "state_out", dev, f, shape)
