@@ -527,6 +527,7 @@ def _append_ref(torch, x, w, eps, off, freq, pos, next_):
     ("f16", 40, 9, 2, 64, 32, True, True, 1024), ("bf16", 33, 0, 2, 96, 96, True, False, 16),
     ("f16", 600, 40, 8, 128, 128, False, False, 16), ("bf16", 500, 24, 4, 256, 256, True, True, 64),
     ("f16", 9, 300, 70, 16, 8, False, True, 16),
+    ("bf16", 1100, 24, 9, 256, 64, False, True, 64), ("f16", 1100, 17, 17, 256, 256, True, False, 16),
 ])
 def test_paged_append(vq, torch_dev, dtype, T, heads, kv, D, rot, next_, norm, page):
     torch = torch_dev
@@ -720,6 +721,14 @@ def test_short_conv_many_requests(vq, torch_dev):
     lens = np.random.default_rng(3).integers(0, 4, 4500).tolist()
     _conv_check(vq, torch_dev, "f16", lens, 16, 4)
     _conv_check(vq, torch_dev, "f16", [31, 32, 33, 64, 65, 500, 1] * 10, 40, 3)
+
+
+@pytest.mark.parametrize("dtype,taps", [("f16", 2), ("bf16", 3), ("f16", 4), ("bf16", 4)])
+@pytest.mark.parametrize("scale", [1, 3])
+def test_short_conv_many_tokens(vq, torch_dev, dtype, taps, scale):
+    """Units of several rounds of rows, ends inside a round and a unit."""
+    lens = [683 * scale + 1, 0, 342 * scale, 15, 16, 17, 341 * scale + 3]
+    _conv_check(vq, torch_dev, dtype, lens, 4104, taps, 4, 128, ctx=[1, 1, 0, 2, 0, 3, 1], in_place=True, pad=9)
 
 
 def test_short_conv_large_inputs(vq, torch_dev):
