@@ -5,7 +5,7 @@
 namespace vqmlp {
 
 constexpr int kDeltaC = 64;  // tokens of a chunk
-constexpr int kDeltaBlock = 20480;  // bytes of a chunk and value head in the workspace
+constexpr int kDeltaBlock = 26624;  // bytes of a chunk and value head in the workspace
 
 struct DeltaArgs {
     const uint16_t *q, *k, *v;

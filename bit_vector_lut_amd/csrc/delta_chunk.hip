@@ -13,13 +13,13 @@
 // Precision.  What reaches the state keeps FP32 accuracy: matrix-core operands made here (S, V - K S, T, U)
 // are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
 // element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
-// binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  For
-// the outputs, which have 16 bits, P is one binary16 part, and so are U and S for bfloat16 ones: binary16 outputs
-// would be 1.6 times as far off as their own rounding leaves them (3.4e-4), so there U and S are two (2.7e-4;
-// 257 -> 268 us for three prompts).  The second parts go to the outputs' waves in the place of T, which they load
-// again.  The triangular system is solved in FP32.
+// binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  The
+// outputs are made of two parts of P, U and S too, so that their one rounding is at the end, as in the
+// recurrence: with one part of each they were 3.4e-4 off instead of 2.1e-4 (binary16), with one of P alone 2.7e-4
+// (257, 290 and 268 us for three prompts).  The second parts of U and S go to the outputs' waves in the place of T, which
+// they load again.  The triangular system is solved in FP32.
 //
-// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 268 us a call, where
+// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 290 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
 // between them: 1.9 us alone on a compute unit, 2.6 beside another workgroup, of which the matrix cores work 0.6.
 // k_delta_prep (71 us of it) writes 151 MB and reads 66: 62% of a copy's rate, with LDS and the triangular solve.
@@ -45,7 +45,7 @@ struct StateBlock {
     int pad[62];
 };
 struct OutBlock {
-    u32x4 p[6][64];
+    u32x4 ph[6][64], pl[6][64];
     float qf[kC];  // e^b 2^qexp in units of P's row: of Q S
     float pf[kC];  // scale times the unit of P's row
     int pad[128];
@@ -379,7 +379,10 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 if (c > wave / 2) break;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[c][i] *= pow2(e);
-                blk.o.p[wave < 2 ? wave : 2 * wave - 2 + c][lane] = pack_hi(p[c]);
+                const u32x4 hi = pack_hi(p[c]);
+                const int at = wave < 2 ? wave : 2 * wave - 2 + c;
+                blk.o.ph[at][lane] = hi;
+                blk.o.pl[at][lane] = pack_lo(p[c], hi);
             }
             if (g4 == 0) {
                 blk.o.qf[t] = decayed(bt, lt, 0.f, 0.f, e + qe);
@@ -582,13 +585,13 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             for (int i = 0; i < (12 + kPairs) / kPairs; ++i) {
                 const int j = wave + kPairs * i;
                 // the second parts of the chunk before lie there, in the place of the wave's own pieces
-                if (OUT && HALF && i == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (OUT && i == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if (j < 13) load_lds16(dp + j * 1024, lane * 16, at + int(offsetof(ChainStage<DKP>, d)) + j * 1024);
             }
             kp += kstep, vp += vstep, dp += dstep;
         };
         // queries and P straight to registers, as the matrix cores take them
-        u32x4 q[4][KS], p[6];
+        u32x4 q[4][KS], ph[6], pl[6];
         float qf[4], pf[4];
         auto load_out = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -596,7 +599,10 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s) q[x][s] = *reinterpret_cast<const u32x4*>(qp + ((x * KS + s) * 1024 + lane * 16));
 #pragma unroll
-            for (int i = 0; i < 6; ++i) p[i] = *reinterpret_cast<const u32x4*>(pp + (i * 1024 + lane * 16));
+            for (int i = 0; i < 6; ++i) {
+                ph[i] = *reinterpret_cast<const u32x4*>(pp + (i * 1024 + lane * 16));
+                pl[i] = *reinterpret_cast<const u32x4*>(pp + ((6 + i) * 1024 + lane * 16));
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 qf[x] = *reinterpret_cast<const float*>(pp + (int(offsetof(OutBlock, qf)) + (16 * x + lr) * 4));
@@ -622,13 +628,11 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             return;
         }
         u32x2 y[4];
-        u32x4 low[KS + 2];  // second parts of the state and of U, for binary16 outputs
+        u32x4 low[KS + 2];  // second parts of the state and of U
         auto take = [&](int c) __attribute__((always_inline)) {
-            if constexpr (HALF) {
-                const u32x4(*const at)[64] = reinterpret_cast<const u32x4(*)[64]>(&sm.chain[c & 1].d);
+            const u32x4(*const at)[64] = reinterpret_cast<const u32x4(*)[64]>(&sm.chain[c & 1].d);
 #pragma unroll
-                for (int s = 0; s < KS + 2; ++s) low[s] = at[wave + kPairs * s][lane];
-            }
+            for (int s = 0; s < KS + 2; ++s) low[s] = at[wave + kPairs * s][lane];
         };
         auto outputs = [&]() __attribute__((always_inline)) {
             // what the chain has handed over of the chunk before, which stands until the next barrier
@@ -647,18 +651,20 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int z = 0; z < (HALF ? 2 : 1); ++z)
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[x] = F16::mfma16(z ? low[s] : sh[s], q[x][s], o[x]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[x] *= qf[x];
 #pragma unroll
-            for (int z = 0; z < (HALF ? 2 : 1); ++z)
+            for (int z = 0; z < 3; ++z)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
-                    for (int k = 0; k <= x / 2; ++k)
-                        o[x] = F16::mfma16(z ? low[KS + k] : uo[k], p[x < 2 ? x : 2 * x - 2 + k], o[x]);
+                    for (int k = 0; k <= x / 2; ++k) {
+                        const int at = x < 2 ? x : 2 * x - 2 + k;
+                        o[x] = F16::mfma16(z == 1 ? low[KS + k] : uo[k], z == 2 ? pl[at] : ph[at], o[x]);
+                    }
             float down[4];
             bool all = true;
 #pragma unroll
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             if (c > 0) outputs();
             load_out();
             // the chain's loads, which are older than those: 16-byte loads of one wave cannot be made fewer
-            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(4 * KS + 6) : "memory");
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(4 * KS + 12) : "memory");
             __syncthreads();  // the next chunk is there for the chain; what it handed over is read
             if (c > 0) store(kC);
             __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), known to the compiler: later it would wait for the chain's loads too
@@ -902,7 +908,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             auto parts = [&](int p) __attribute__((always_inline)) {
                 float x[8] = {U[p][0][0], U[p][0][1], U[p][0][2], U[p][0][3], U[p][1][0], U[p][1][1], U[p][1][2], U[p][1][3]};
                 uo[p] = pack_hi(x);
-                if constexpr (OUT && HALF) uq[p] = pack_lo(x, uo[p]);
+                if constexpr (OUT) uq[p] = pack_lo(x, uo[p]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
@@ -969,11 +975,10 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             for (int s = 0; s < KS; ++s) sm.sh[wave][s][lane] = sh[s];
 #pragma unroll
             for (int k = 0; k < 2; ++k) sm.uo[wave][k][lane] = uo[k];
-            if constexpr (HALF) {  // T is read; the outputs' wave loads these pieces of the next but one
-                u32x4(*const to)[64] = reinterpret_cast<u32x4(*)[64]>(&sm.chain[c & 1].d);
+            // T is read; the outputs' wave loads these pieces of the next but one
+            u32x4(*const to)[64] = reinterpret_cast<u32x4(*)[64]>(&sm.chain[c & 1].d);
 #pragma unroll
-                for (int s = 0; s < KS + 2; ++s) to[wave + kPairs * s][lane] = s < KS ? sl[s] : uq[s - KS];
-            }
+            for (int s = 0; s < KS + 2; ++s) to[wave + kPairs * s][lane] = s < KS ? sl[s] : uq[s - KS];
             if (g4 == 0) sm.unit[16 * wave + lr] = e, sm.from[16 * wave + lr] = lost ? 0 : late;
         }
         lost |= late < kC;

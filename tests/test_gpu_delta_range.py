@@ -1,0 +1,82 @@
+"""GPU: the gated delta rule at the ends of its ranges, token by token (max_q 16) and in chunks (300).
+
+Tolerances.  u = eps / 2 of the 16-bit type is one rounding, W = 2^-24 one of FP32.  A token adds to a column of
+the state at most C W (|S'| + a), a = |k| beta (|v| + |k| |S'|): its own sums and, in chunks, those of the
+triangular system, C = 2 (Dk + 64).  Z sums that up with the decays, B the lengths |k| |u| that a column is made of.
+An output adds C W scale |q| (B + Z) and its one rounding.
+"""
+import math
+
+import pytest
+
+from test_gpu_block_ops import _close, _randn, _t, _u, torch_dev, vq  # noqa: F401
+from test_gpu_mixer_ops import W, _delta_inputs, _i, _starts
+
+pytestmark = pytest.mark.gpu
+
+TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}  # half a step of the smallest outputs
+
+
+def _ref(torch, q, k, v, g, beta, state, cu, scale):
+    """Outputs, their bounds B and Z, states and theirs, in 64 bits."""
+    T, hk, dk = q.shape
+    hv, dv = v.shape[1:]
+    y, yb = torch.zeros(T, hv, dv).double(), torch.zeros(T, hv, dv).double()
+    out, sb = torch.zeros(state.shape).double(), torch.zeros(state.shape).double()
+    kd, qd = (x.double().repeat_interleave(hv // hk, 1) for x in (k, q))
+    vd, e, bd = v.double(), torch.exp(g.double().clamp(min=-80.0))[..., None], beta.double()[..., None]
+    for r in range(len(cu) - 1):
+        S = state[r].double().clone()
+        B = S.norm(dim=1)
+        Z = torch.zeros_like(B)
+        for t in range(cu[r], cu[r + 1]):
+            S = e[t][..., None] * S
+            length = kd[t].norm(dim=1)[:, None]
+            u = bd[t] * (vd[t] - (S * kd[t][..., None]).sum(1))
+            s = S.norm(dim=1)
+            Z = e[t] * Z + s + length * bd[t] * (vd[t].abs() + length * s)
+            B = e[t] * B + length * u.abs()
+            S = S + kd[t][:, :, None] * u[:, None, :]
+            y[t] = scale * (S * qd[t][..., None]).sum(1)
+            yb[t] = abs(scale) * qd[t].norm(dim=1)[:, None] * (B + Z)
+        out[r], sb[r] = S, Z[:, None].expand_as(S)
+    return y, yb, out, sb
+
+
+def _check(vq, torch, dtype, lens, args, max_q, state=None, scale=None, work=None):
+    q, k, v, g, beta = args
+    hk, dk, hv, dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
+    cu = _starts(lens)
+    if state is None:
+        state = torch.zeros(len(lens), hv, dk, dv)
+    op = vq.DeltaRule(hk, hv, dk, dv, scale)
+    print("delta", dtype, lens, hk, hv, dk, dv, max_q, flush=True)
+    y, out = op.forward(*(x.cuda() for x in args), state.cuda(), _i(torch, cu), max_q=max_q, workspace=work)
+    torch.cuda.synchronize()
+    ry, yb, rs, sb = _ref(torch, *args, state, cu, op.scale)
+    c = 2 * (dk + 64) * W
+    _close(torch, y, ry, _u(torch, _t(torch, dtype)) * ry.abs() + c * yb + TINY[dtype], "y")
+    _close(torch, out, rs, c * sb + 2.0 ** -148, "state")
+    return y, out, ry
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv,max_q", [
+    ([150, 201], 2, 4, 64, 64, 16), ([150, 201], 2, 4, 64, 64, 300), ([400], 1, 3, 128, 128, 400), ([333, 64], 2, 2, 96, 72, 333),
+    ([2600], 1, 1, 64, 64, 2600),
+])
+def test_outputs_are_rounded_once(vq, torch_dev, dtype, lens, hk, hv, dk, dv, max_q):
+    """Many outputs are as far from the exact ones as those are from their own rounding; what the sums in front add is
+    independent of it, and its root mean square grows with the root of the number of terms: 4 sqrt(Dk + 64) W of
+    scale |q| |S|, so much for each of the tokens that a state of these decays remembers."""
+    torch = torch_dev
+    dt = _t(torch, dtype)
+    args = _delta_inputs(torch, dt, sum(lens), hk, hv, dk, dv, 21)
+    state = _randn(torch, (len(lens), hv, dk, dv), torch.float32, 22, 0.5)
+    y, _, ry = _check(vq, torch, dtype, lens, args, max_q, state)
+    own = (ry.to(dt).double() - ry).norm()
+    # |S| of a column from |y|: queries point anywhere, so |y| = scale |q| |S| / sqrt(Dk) in the mean
+    added = 4 * math.sqrt(dk + 64) * W * math.sqrt(dk) * ry.norm()
+    err = (y.cpu().double() - ry).norm()
+    print("%.4e of %.4e, %.1e" % (err / ry.norm(), own / ry.norm(), added / ry.norm()), flush=True)
+    assert err <= (own * own + added * added).sqrt()
