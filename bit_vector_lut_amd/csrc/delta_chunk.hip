@@ -13,7 +13,8 @@
 // Precision.  What reaches the state keeps FP32 accuracy: matrix-core operands made here (S, V - K S, T, U)
 // are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
 // element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
-// binary16 by a power of two for each row, which leaves out at most 2^-40 of the row's largest element.  The
+// binary16 by a power of two for each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14),
+// 2^-25 of a key's (brought to 1: K^T U is added to the state as it comes).  The
 // outputs are made of two parts of P, U and S too, so that their one rounding is at the end, as in the
 // recurrence: with one part of each they were 3.4e-4 off instead of 2.1e-4 (binary16), with one of P alone 2.7e-4
 // (257, 290 and 268 us for three prompts).  The second parts of U and S go to the outputs' waves in the place of T, which
@@ -46,8 +47,8 @@ struct StateBlock {
 };
 struct OutBlock {
     u32x4 ph[6][64], pl[6][64];
-    float qf[kC];  // e^b 2^qexp in units of P's row: of Q S
-    float pf[kC];  // scale times the unit of P's row
+    float qf[kC];  // e^b in units of P's row: of Q S
+    int pe[kC];    // exponent of the scale and of the units of P's row and of the query
     int pad[128];
 };
 struct DeltaBlock {
@@ -138,6 +139,10 @@ __device__ __forceinline__ u32x4 to_half(u32x4 x, float by) {
 }
 __device__ __forceinline__ int bf_expo(uint32_t top) {
     return top >= 0x80u && top < 0x7F80u ? int(top >> 7) - 127 : 0;
+}
+// The power of two that brings the largest of a row, of these bits, to 2^14 or as near as FP32 holds the factor.
+__device__ __forceinline__ int query_unit(uint32_t top) {
+    return top == 0 || top >= 0x7F80u ? 0 : min(14 + 127 - max(int(top >> 7), 1), 126);
 }
 
 template <int DKP>
@@ -236,16 +241,16 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
         if (top >= kInf16<E>) atomicMin(&sm.kbad, r);
         *reinterpret_cast<u32x4*>(&sm.k[r * DKP + 8 * (kc ^ kkey<DKP>(r))]) = kr[i];
     }
-    int qe = 0;
+    int qe = 0;  // the row of queries is in units of 2^-qe
     if constexpr (!HALF) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) qtop = max(qtop, top8(qf[s]));
         // the lanes of a row are 16 apart
         qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 16)));
         qtop = max(qtop, uint32_t(__shfl_xor(int(qtop), 32)));
-        qe = bf_expo(qtop);
+        qe = query_unit(qtop);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[s] = to_half(qf[s], pow2(-qe));
+        for (int s = 0; s < KS; ++s) qf[s] = to_half(qf[s], pow2(qe));
     }
     if (first) {
 #pragma unroll
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             keep();
         }
         __builtin_amdgcn_sched_barrier(0);
-        // P
+        // P, of the queries in their units
         {
             const int t = 16 * wave + lr;
             const float bt = sm.b[t], lt = sm.lo[t];
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                     const f32x4 bjv = *reinterpret_cast<const f32x4*>(&sm.b[j0]), lj = *reinterpret_cast<const f32x4*>(&sm.lo[j0]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = j0 + i, e = HALF ? 0 : qe + sm.kexp[j];
+                        const int j = j0 + i, e = HALF ? 0 : sm.kexp[j];
                         const float v = qk[c][b][i] * decayed(bt, lt, bjv[i], lj[i], e);
                         p[c][4 * b + i] = only(j <= t && j < bad, v);
                         top = fmaxf(top, fabsf(p[c][4 * b + i]));
@@ -373,6 +378,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 }
             }
             top = column_max(top);
+            // Q S, which is below 2^34 in its units, takes 2^e too
             const int e = top > 0.f ? min(max(14 - expo(top), -60), 60) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 blk.o.pl[at][lane] = pack_lo(p[c], hi);
             }
             if (g4 == 0) {
-                blk.o.qf[t] = decayed(bt, lt, 0.f, 0.f, e + qe);
-                blk.o.pf[t] = a.scale * pow2(-e);
+                blk.o.qf[t] = decayed(bt, lt, 0.f, 0.f, e);
+                blk.o.pe[t] = __builtin_amdgcn_frexp_expf(a.scale) - e - qe;
             }
         }
         __syncthreads();
@@ -592,7 +598,8 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         };
         // queries and P straight to registers, as the matrix cores take them
         u32x4 q[4][KS], ph[6], pl[6];
-        float qf[4], pf[4];
+        float qf[4];
+        int pe[4];
         auto load_out = [&]() __attribute__((always_inline)) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
@@ -606,7 +613,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 qf[x] = *reinterpret_cast<const float*>(pp + (int(offsetof(OutBlock, qf)) + (16 * x + lr) * 4));
-                pf[x] = *reinterpret_cast<const float*>(pp + (int(offsetof(OutBlock, pf)) + (16 * x + lr) * 4));
+                pe[x] = *reinterpret_cast<const int*>(pp + (int(offsetof(OutBlock, pe)) + (16 * x + lr) * 4));
             }
             qp += qstep, pp += dstep;
         };
@@ -627,6 +634,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             }
             return;
         }
+        const float scale = __builtin_amdgcn_frexp_mantf(a.scale);
         u32x2 y[4];
         u32x4 low[KS + 2];  // second parts of the state and of U
         auto take = [&](int c) __attribute__((always_inline)) {
@@ -665,15 +673,14 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
                         const int at = x < 2 ? x : 2 * x - 2 + k;
                         o[x] = F16::mfma16(z == 1 ? low[KS + k] : uo[k], z == 2 ? pl[at] : ph[at], o[x]);
                     }
-            float down[4];
             bool all = true;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) down[i] = pow2(-unit[i]), all &= from[i] >= kC;
+            for (int i = 0; i < 4; ++i) all &= from[i] >= kC;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 float z[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = o[x][i] * pf[x] * down[i];
+                for (int i = 0; i < 4; ++i) z[i] = __builtin_ldexpf(o[x][i] * scale, pe[x] - unit[i]);
                 if (__builtin_expect(__any(!all), 0)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) z[i] = 16 * x + lr >= from[i] ? __builtin_nanf("") : z[i];

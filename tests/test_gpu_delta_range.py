@@ -80,3 +80,45 @@ def test_outputs_are_rounded_once(vq, torch_dev, dtype, lens, hk, hv, dk, dv, ma
     err = (y.cpu().double() - ry).norm()
     print("%.4e of %.4e, %.1e" % (err / ry.norm(), own / ry.norm(), added / ry.norm()), flush=True)
     assert err <= (own * own + added * added).sqrt()
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("power", [-120, -90, -30, 30, 80, 120])
+def test_bfloat16_queries_of_any_length(vq, torch_dev, power, max_q):
+    torch = torch_dev
+    q, k, v, g, beta = _delta_inputs(torch, torch.bfloat16, 170, 2, 2, 64, 64, 34)
+    q = (q.double() * 2.0 ** power).to(torch.bfloat16)
+    state = _randn(torch, (1, 2, 64, 64), torch.float32, 35)
+    _check(vq, torch, "bf16", [170], (q, k, v, g, beta), max_q, state)
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+def test_bfloat16_queries_of_the_largest_elements(vq, torch_dev, max_q):
+    torch = torch_dev
+    # v and the state below 2^-1, so that a row of the state times 1.5 2^127 is an FP32 number
+    q, k, v, g, beta = _delta_inputs(torch, torch.bfloat16, 100, 1, 1, 64, 64, 36, 2.0 ** -4)
+    q = torch.zeros_like(q)
+    t = torch.arange(100)
+    q[t, 0, t % 64] = 1.5 * 2.0 ** 127
+    _check(vq, torch, "bf16", [100], (q, k, v, g, beta), max_q, _randn(torch, (1, 1, 64, 64), torch.float32, 37, 2.0 ** -4), scale=2.0 ** -8)
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("apart", [20, 26])
+def test_bfloat16_query_elements_far_apart(vq, torch_dev, apart, max_q):
+    """Each query's largest element meets a row of the state that is zero; the others are 2^-apart of it.  What is left
+    of an element is off by at most 2^-40 of the largest."""
+    torch = torch_dev
+    q, k, v, g, beta = _delta_inputs(torch, torch.bfloat16, 150, 1, 2, 64, 64, 38)
+    k[:, :, 0] = 0.0
+    q *= 2.0 ** -apart
+    q[:, :, 0] = 0.0
+    state = _randn(torch, (1, 2, 64, 64), torch.float32, 39)
+    state[:, :, 0] = 0.0
+    ry, yb, _, _ = _ref(torch, q, k, v, g, beta, state, [0, 150], 1.0)
+    q[:, :, 0] = 1.0
+    y, _ = vq.DeltaRule(1, 2, 64, 64, 1.0).forward(*(x.cuda() for x in (q, k, v, g, beta)), state.cuda(), _i(torch, [0, 150]),
+                                                   max_q=max_q)
+    # the sum of a column's magnitudes is at most sqrt(64) times its length, and B is no less than that
+    length = q[:, :, 1:].double().norm(dim=2)[..., None]
+    _close(torch, y, ry, 2.0 ** -8 * ry.abs() + 2 * 128 * W * yb + 2.0 ** -40 * 8 * yb / length + TINY["bf16"], "y")
