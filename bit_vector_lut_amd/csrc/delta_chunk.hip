@@ -12,7 +12,8 @@
 //
 // Precision.  What reaches the state keeps FP32 accuracy: matrix-core operands made here (S, V - K S, T, U)
 // are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
-// element into the upper range of binary16.  Keys and queries are binary16 as they are; bfloat16 ones become
+// element into the upper range of binary16.  The state and U may be smaller than the values by the sizes of the keys and of
+// beta: their units are 2^-(e + lift) and 2^-(e + ulift), the same for all columns of a chunk.  Keys and queries are binary16 as they are; bfloat16 ones become
 // binary16 by a power of two for each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14),
 // 2^-25 of a key's (brought to 1: K^T U is added to the state as it comes).  The
 // outputs are made of two parts of P, U and S too, so that their one rounding is at the end, as in the
@@ -38,17 +39,18 @@ constexpr int kC = kDeltaC;
 // factors for each token; what the state's chain takes, then what the outputs take.
 struct StateBlock {
     u32x4 th[6][64], tl[6][64];
-    float xf[kC];  // e^b 2^kexp: of K S
-    float uf[kC];  // the unit of T's row
-    float tf[kC];  // e^(b_64 - b) 2^kexp: of U where it joins the state
+    float xf[kC];  // e^b 2^(kexp - lift): of K S
+    float uf[kC];  // the unit of T's row, and 2^ulift
+    float tf[kC];  // e^(b_64 - b) 2^(kexp + lift - ulift): of U where it joins the state
     float etot;    // e^b_64
     int bad;       // first token with something not finite in k, g or beta, or 64
-    int pad[62];
+    int lift;      // the state is in units of 2^-lift of the values' here
+    int pad[61];
 };
 struct OutBlock {
     u32x4 ph[6][64], pl[6][64];
-    float qf[kC];  // e^b in units of P's row: of Q S
-    int pe[kC];    // exponent of the scale and of the units of P's row and of the query
+    float qf[kC];  // e^b in the units of P's row and U: of Q S
+    int pe[kC];    // exponent of the scale and of the units of P's row, of U and of the query
     int pad[128];
 };
 struct DeltaBlock {
@@ -137,8 +139,10 @@ __device__ __forceinline__ u32x4 to_half(u32x4 x, float by) {
     for (int i = 0; i < 4; ++i) f[2 * i] = lo16<BF16>(x[i]) * by, f[2 * i + 1] = hi16<BF16>(x[i]) * by;
     return pack_hi(f);
 }
-__device__ __forceinline__ int bf_expo(uint32_t top) {
-    return top >= 0x80u && top < 0x7F80u ? int(top >> 7) - 127 : 0;
+// The exponent of a key's largest element, of these bits; kNoKey of a key of zeros.
+constexpr int kNoKey = -200;
+__device__ __forceinline__ int key_expo(uint32_t top) {
+    return top == 0 ? kNoKey : top >= 0x7F80u ? 0 : min(max(int(top >> 7) - 127, -126), 126);
 }
 // The power of two that brings the largest of a row, of these bits, to 2^14 or as near as FP32 holds the factor.
 __device__ __forceinline__ int query_unit(uint32_t top) {
@@ -154,6 +158,7 @@ struct PrepSmem {
     float b[kC], lo[kC];  // b log2 e and what it lost in rounding
     float beta[kC];
     int kexp[kC];
+    int lift, ulift;
     int kbad, bad;  // first token with something not finite in k; or in g or beta
 };
 
@@ -163,10 +168,13 @@ __device__ __forceinline__ float only(bool c, float v) {
     return c ? v : 0.f;
 }
 
-// 2^(b_t - b_j + e) from the two parts of the b's
-__device__ __forceinline__ float decayed(float bt, float lt, float bj, float lj, int e) {
-    return __builtin_amdgcn_exp2f((bt - bj) + (lt - lj) + float(e));
+// 2^(b_t - b_j) from the two parts of the b's
+__device__ __forceinline__ float decayed(float bt, float lt, float bj, float lj) {
+    return __builtin_amdgcn_exp2f((bt - bj) + (lt - lj));
 }
+
+// Where 2^top in a band of 8 powers has to go to end up between 2^-4 and 2^4
+__device__ __forceinline__ int band(int top) { return -((top + 4) & ~7); }
 
 // A workgroup makes the blocks of `per` value heads that share a key head: K K^T and Q K^T are theirs together.
 // Tiles of 16 x 16: each wave has one on the diagonal of A and one or two of the six below.
@@ -233,8 +241,8 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
         if constexpr (!HALF) {
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1) top = max(top, uint32_t(__shfl_xor(int(top), o)));
-            const int e = bf_expo(top);
-            kr[i] = to_half(kr[i], pow2(-e));
+            const int e = key_expo(top);
+            kr[i] = to_half(kr[i], e == kNoKey ? 1.f : pow2(-e));
             if (kc == 0) sm.kexp[r] = e;
             if (first) *reinterpret_cast<u32x4*>(image + kC * DKP + r * DKP + 8 * kc) = kr[i];
         }
@@ -258,6 +266,11 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
     }
     __syncthreads();
     const int kbad = sm.kbad;
+    int kmax = 0;  // of the chunk's keys: P is made in its units
+    if constexpr (!HALF) {
+        kmax = __builtin_amdgcn_readlane(lane_scan(sm.kexp[lane], kNoKey, [](int p, int q) { return max(p, q); }), 63);
+        if (kmax == kNoKey) kmax = 0;
+    }
     auto k_read = [&](int r, int s) {
         return *reinterpret_cast<const u32x4*>(&sm.k[r * DKP + 8 * ((4 * s + g4) ^ kkey<DKP>(r))]);
     };
@@ -296,12 +309,30 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             const double b = lane_scan(double(g) * 1.4426950408889634, 0., [](double p, double q) { return p + q; });
             const int ke = HALF ? 0 : sm.kexp[lane];
             const double all = __shfl(b, 63);
+            // The state and U in units of their own, which follow the largest |k| beta and beta: from a state of zeros
+            // they are as much smaller than the values.  Bands keep the units the same from chunk to chunk.  The state's is
+            // bounded, since it may hold what other chunks left.
+            constexpr int none = -1000;
+            struct Two {
+                int key, beta;
+            };
+            const int be = lane < bad && beta != 0.f && ke != kNoKey ? expo(beta) : none;
+            const Two top = lane_scan(Two{be == none ? none : ke + be, be}, Two{none, none}, [](Two p, Two q) {
+                return Two{max(p.key, q.key), max(p.beta, q.beta)};
+            });
+            const int tk = __builtin_amdgcn_readlane(top.key, 63), tb = __builtin_amdgcn_readlane(top.beta, 63);
+            const int far = min(64, 126 - kmax);
+            const int lift = tk == none ? 0 : min(max(band(tk), max(-64, kmax - 126)), far);
+            const int ulift = tb == none ? 0 : min(max(band(tb), -64), 120);
             sm.b[lane] = float(b);
             sm.lo[lane] = float(b - double(float(b)));
             sm.beta[lane] = beta;
-            blk.s.xf[lane] = exp_b(b + double(ke));
-            blk.s.tf[lane] = exp_b(all - b + double(ke));
-            if (lane == 0) sm.bad = bad, blk.s.etot = exp_b(all), blk.s.bad = bad;
+            blk.s.xf[lane] = exp_b(b + double(ke - lift));
+            blk.s.tf[lane] = exp_b(all - b + double(ke + lift - ulift));
+            if (lane == 0) {
+                sm.bad = bad, sm.lift = lift, sm.ulift = ulift;
+                blk.s.etot = exp_b(all), blk.s.bad = bad, blk.s.lift = lift;
+            }
         }
         __syncthreads();
         if (h + 1 < h0 + per) gates(h + 1);
@@ -316,8 +347,9 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             const f32x4 be = *reinterpret_cast<const f32x4*>(&sm.beta[r0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = r0 + i, e = HALF ? 0 : sm.kexp[cj] + sm.kexp[t];
-                const float v = kk[z][i] * be[i] * decayed(bt[i], lt[i], bjv, lj, e);
+                const int t = r0 + i;
+                float v = kk[z][i] * be[i] * decayed(bt[i], lt[i], bjv, lj);
+                if constexpr (!HALF) v = __builtin_ldexpf(v, sm.kexp[cj] + sm.kexp[t]);
                 A[t][cj] = only(cj < t && t < bad, v);
             }
         }
@@ -370,16 +402,18 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                     const f32x4 bjv = *reinterpret_cast<const f32x4*>(&sm.b[j0]), lj = *reinterpret_cast<const f32x4*>(&sm.lo[j0]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = j0 + i, e = HALF ? 0 : sm.kexp[j];
-                        const float v = qk[c][b][i] * decayed(bt, lt, bjv[i], lj[i], e);
+                        const int j = j0 + i;
+                        float v = qk[c][b][i] * decayed(bt, lt, bjv[i], lj[i]);
+                        if constexpr (!HALF) v = __builtin_ldexpf(v, sm.kexp[j] - kmax);
                         p[c][4 * b + i] = only(j <= t && j < bad, v);
                         top = fmaxf(top, fabsf(p[c][4 * b + i]));
                     }
                 }
             }
             top = column_max(top);
-            // Q S, which is below 2^34 in its units, takes 2^e too
-            const int e = top > 0.f ? min(max(14 - expo(top), -60), 60) : 0;
+            // Q S, which is below 2^34 in its units, takes 2^(e + more) too
+            const int more = sm.ulift - sm.lift - kmax;
+            const int e = min(top > 0.f ? max(14 - expo(top), -60) : 0, 60 - max(more, 0));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (c > wave / 2) break;
@@ -391,8 +425,8 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 blk.o.pl[at][lane] = pack_lo(p[c], hi);
             }
             if (g4 == 0) {
-                blk.o.qf[t] = decayed(bt, lt, 0.f, 0.f, e);
-                blk.o.pe[t] = __builtin_amdgcn_frexp_expf(a.scale) - e - qe;
+                blk.o.qf[t] = __builtin_ldexpf(decayed(bt, lt, 0.f, 0.f), e + more);
+                blk.o.pe[t] = __builtin_amdgcn_frexp_expf(a.scale) - e - qe + kmax - sm.ulift;
             }
         }
         __syncthreads();
@@ -438,7 +472,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 }
             }
             top = column_max(top);
-            const int e = top > 0.f ? min(max(13 - expo(top), -120), 100) : 0;
+            const int e = top > 0.f ? min(max(13 - expo(top), -120), 126) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (c > c1) break;
@@ -449,7 +483,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
                 blk.s.th[at][lane] = hi;
                 blk.s.tl[at][lane] = pack_lo(v[c], hi);
             }
-            if (g4 == 0) blk.s.uf[t] = pow2(-e);
+            if (g4 == 0) blk.s.uf[t] = __builtin_ldexpf(1.f, sm.ulift - e);
         }
         __syncthreads();  // b and beta are read
     }
@@ -732,9 +766,9 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         else if (old) from = a.sin + own;
         if (u.seg == u.nseg - 1 && slot >= 0) to = a.sout + own;
     }
-    // state element (p, b, i): dk = 32 p + 8 g4 + 4 b + i of column dv, in units of 2^-e
+    // state element (p, b, i): dk = 32 p + 8 g4 + 4 b + i of column dv, in units of 2^-(e + lift), the values' being 2^-e
     f32x4 S[KS][2];
-    int e = 0;
+    int e = 0, lift = 0;
 #pragma unroll
     for (int p = 0; p < KS; ++p)
 #pragma unroll
@@ -787,6 +821,12 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         const uint8_t* const kb = reinterpret_cast<const uint8_t*>(st.k);
         int late = st.d.bad;  // first token that the column gets no number from
         const float etot = st.d.etot;
+        if (__builtin_expect(__any(st.d.lift != lift), 0)) {  // up to 2^128 in two steps
+            const int by = st.d.lift - lift;
+            scale_state(pow2(by / 2));
+            scale_state(pow2(by - by / 2));
+            lift += by;
+        }
         // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
         float big = 0.f;
 #pragma unroll
@@ -920,7 +960,10 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
                 for (int b = 0; b < 2; ++b) {
                     const f32x4 tf = *reinterpret_cast<const f32x4*>(&st.d.tf[32 * p + 8 * g4 + 4 * b]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[4 * b + i] *= tf[i];
+                    for (int i = 0; i < 4; ++i) {
+                        x[4 * b + i] *= tf[i];
+                        most = fmaxf(most, fabsf(x[4 * b + i]));
+                    }
                 }
                 uh[p] = pack_hi(x);
                 ul[p] = pack_lo(x, uh[p]);
@@ -1011,7 +1054,6 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         __syncthreads();  // K is read
     }
     if (to && cin) {
-        const float by = pow2(-e);
 #pragma unroll
         for (int p = 0; p < KS; ++p)
 #pragma unroll
@@ -1019,7 +1061,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int dk = 32 * p + 8 * g4 + 4 * b + i;
-                    if (dk < a.Dk) to[int64_t(dk) * width + dv] = S[p][b][i] * by;
+                    if (dk < a.Dk) to[int64_t(dk) * width + dv] = __builtin_ldexpf(S[p][b][i], -e - lift);
                 }
     }
 }

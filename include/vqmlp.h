@@ -495,7 +495,9 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  * the workspace's rules and T and R's limits.  max_q up to 20 to 40, by how many heads and requests there are,
  * takes the recurrence; above, short requests may take it beside the others' chunks, and few long ones go through
  * their chunks in segments.  Keys are meant to have length one and beta to lie in [0, 2];
- * beyond, the recurrence itself may grow without bound.  What is not finite in k, g or beta makes the outputs
+ * beyond, the recurrence itself may grow without bound.  Either way the state keeps FP32 accuracy measured by each
+ * column; chunks do so while the largest |k| beta of 64 tokens lies between 2^-64 and 2^64, and leave out elements of a
+ * BF16 key below 2^-25 of its largest.  What is not finite in k, g or beta makes the outputs
  * of its head from its token on and the state NaN, in v those of its column, in q its own outputs. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;

@@ -122,3 +122,66 @@ def test_bfloat16_query_elements_far_apart(vq, torch_dev, apart, max_q):
     # the sum of a column's magnitudes is at most sqrt(64) times its length, and B is no less than that
     length = q[:, :, 1:].double().norm(dim=2)[..., None]
     _close(torch, y, ry, 2.0 ** -8 * ry.abs() + 2 * 128 * W * yb + 2.0 ** -40 * 8 * yb / length + TINY["bf16"], "y")
+
+
+def _updates(torch, dtype, what, seed):
+    """Inputs whose updates |k| beta are small or whose keys are long, from a state of zeros."""
+    dt = _t(torch, dtype)
+    q, k, v, g, beta = _delta_inputs(torch, dt, 150, 1, 2, 128, 72, seed)
+    if what[0] == "k":
+        k = (k.double() * 2.0 ** what[1]).to(dt)
+    elif what[0] == "beta":
+        beta = beta * 2.0 ** what[1]
+    elif what[0] == "long":  # each key orthogonal to the others, so that nothing grows
+        k = torch.zeros_like(k)
+        t = torch.arange(128)
+        k[t, 0, (37 * t) % 128] = 2.0 ** what[1]
+        beta = (beta * 2.0 ** what[2]).clone()
+        beta[128:] = 0
+    return q, k, v, g, beta
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("dtype,what", [
+    ("bf16", ("k", -15)), ("bf16", ("k", -25)), ("bf16", ("k", -36)), ("bf16", ("k", -60)), ("f16", ("k", -9)),
+    ("bf16", ("beta", -12)), ("bf16", ("beta", -28)), ("f16", ("beta", -28)), ("f16", ("beta", -50)),
+    ("bf16", ("long", 6, 0)), ("bf16", ("long", 30, 0)), ("bf16", ("long", 100, -95)), ("bf16", ("long", 127, -120)),
+    ("f16", ("long", 6, 0)), ("f16", ("long", 12, 0)),
+])
+def test_updates_of_any_size(vq, torch_dev, dtype, what, max_q):
+    """From a state of zeros the updates are all that the state holds.  binary16 outputs of small ones are lifted by
+    the scale."""
+    small = min(0, what[1]) if dtype == "f16" else 0
+    _check(vq, torch_dev, dtype, [150], _updates(torch_dev, dtype, what, 31), max_q, scale=2.0 ** (-small - 4))
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_chunks_of_other_sizes(vq, torch_dev, dtype, max_q):
+    """Chunks of ordinary, small and no updates by turns, and keys of zero between short ones."""
+    torch = torch_dev
+    q, k, v, g, beta = _delta_inputs(torch, _t(torch, dtype), 500, 1, 2, 64, 64, 32)
+    beta[64:140] *= 2.0 ** -20
+    beta[200:270] = 0.0
+    beta[330:400, 0] *= 2.0 ** -40
+    beta[330:400, 1] *= 1e-37
+    if dtype == "bf16":
+        k[64:100] *= 2.0 ** -12
+        k[270:300] *= 2.0 ** -20
+        k[405:470] *= 2.0 ** -33
+    k[::5] = 0.0
+    state = _randn(torch, (2, 2, 64, 64), torch.float32, 33)
+    state[1] = 0.0
+    _check(vq, torch, dtype, [280, 220], (q, k, v, g, beta), max_q, state)
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("apart", [20, 26])
+def test_bfloat16_key_elements_far_apart(vq, torch_dev, apart, max_q):
+    """The elements of a key that are 2^-apart of its largest meet rows of the state 2^apart times the others'."""
+    torch = torch_dev
+    q, k, v, g, beta = _delta_inputs(torch, torch.bfloat16, 150, 1, 2, 64, 64, 40)
+    state = _randn(torch, (1, 2, 64, 64), torch.float32, 41)
+    k[:, :, 32:] *= 2.0 ** -apart
+    state[:, :, 32:] *= 2.0 ** apart
+    _check(vq, torch, "bf16", [150], (q, k, v, g, beta), max_q, state)
