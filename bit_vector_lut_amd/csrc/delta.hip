@@ -113,7 +113,9 @@ __global__ void __launch_bounds__(64) k_delta_step(DeltaArgs a) {
                     sq[i] = fmaf(qq, s[8 * c + j][i], sq[i]);
                 }
             }
-        const float one = x.beta * fmaf(-e, each(sk), lo16<E>(x.v)), y = a.scale * fmaf(all(kq), one, e * each(sq));
+        float one = x.beta * fmaf(-e, each(sk), lo16<E>(x.v));
+        one += one - one;  // NaN of what is not finite, as in chunks
+        const float y = a.scale * fmaf(all(kq), one, e * each(sq));
         if ((lane & 15) < CB && cin) a.y[int64_t(t) * a.ld_y + int64_t(h) * a.Dv + own] = uint16_t(pack16<E>(y, y));
         // the four columns' u from the four rows
         const Two p = row(one, twice(one)), u01 = half(p.x, twice(p.x)), u23 = half(p.y, twice(p.y));

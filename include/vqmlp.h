@@ -498,7 +498,8 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  * beyond, the recurrence itself may grow without bound.  Either way the state keeps FP32 accuracy measured by each
  * column; chunks do so while the largest |k| beta of 64 tokens lies between 2^-64 and 2^64, and leave out elements of a
  * BF16 key below 2^-25 of its largest.  What is not finite in k, g or beta makes the outputs
- * of its head from its token on and the state NaN, in v those of its column, in q its own outputs. */
+ * of its head from its token on and the state NaN, in v or the state those of its column; in q its own outputs are NaN or
+ * infinite. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
     float scale;

@@ -185,3 +185,34 @@ def test_bfloat16_key_elements_far_apart(vq, torch_dev, apart, max_q):
     k[:, :, 32:] *= 2.0 ** -apart
     state[:, :, 32:] *= 2.0 ** apart
     _check(vq, torch, "bf16", [150], (q, k, v, g, beta), max_q, state)
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("what", ["k", "v", "beta", "state"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_what_is_not_finite_gives_nan(vq, torch_dev, dtype, max_q, what, bad):
+    torch = torch_dev
+    args = [x.cuda() for x in _delta_inputs(torch, _t(torch, dtype), 150, 1, 2, 64, 72, 7)]
+    op = vq.DeltaRule(1, 2, 64, 72)
+    state = _randn(torch, (2, 2, 64, 72), torch.float32, 9).cuda()
+    cu = _i(torch, [0, 110, 150])
+    y0, s0 = op.forward(*args, state, cu, max_q=max_q)
+    for t in (0, 5, 63, 64, 109):
+        new, start = [x.clone() for x in args], state.clone()
+        hit, lost = torch.zeros_like(y0, dtype=torch.bool), torch.zeros_like(s0, dtype=torch.bool)
+        if what == "v":
+            new[2][t, 1, 20] = bad
+            hit[t:110, 1, 20] = lost[0, 1, :, 20] = True
+        elif what == "k":
+            new[1][t, 0, 9] = bad
+            hit[t:110] = lost[0] = True
+        elif what == "beta":
+            new[4][t, 1] = bad
+            hit[t:110, 1] = lost[0, 1] = True
+        else:
+            start[0, 1, t % 64, 20] = bad
+            hit[:110, 1, 20] = lost[0, 1, :, 20] = True
+        y, s = op.forward(*new, start, cu, max_q=max_q)
+        assert torch.equal(y[~hit], y0[~hit]) and y[hit].isnan().all(), t
+        assert torch.equal(s[~lost], s0[~lost]) and s[lost].isnan().all(), t
