@@ -166,15 +166,23 @@ struct DeltaGeom {
     int64_t seg_units;
 };
 
-DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
+// room: bytes of the caller's workspace, SIZE_MAX when the call's own wish is asked for.  A workspace that was made for
+// more tokens, requests and max_q holds the chunks of this call, but maybe not the segments that only this one would
+// take: then longer ones that fit, or whole requests.
+DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus, size_t room) {
     DeltaGeom G{};
     // A token of the recurrence takes 0.6 us, or more where its waves fill the card; a chunk takes the same for one token
     // as for 64.  They meet at 21 tokens for one request of up to 48 heads (20 us), 28 for eight (50 us) and
     // 45 for 64 (370 us).  Requests of different lengths that fill the card with a chunk each (64 requests of 48
     // heads, 63 of them with one token, one with 512: 377 us in chunks, 143 so) go each its own way.
     const int64_t heads = int64_t(d.R) * d.v_heads;
-    const int few = heads >= 8 * cus ? 40 : heads >= cus ? 28 : 20;
-    G.step = d.max_q <= few;
+    constexpr int most_few = 40;
+    const int few = heads >= 8 * cus ? most_few : heads >= cus ? 28 : 20;
+    const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
+    const size_t images = units * d.v_heads * kDeltaBlock;
+    const size_t chunks_bytes = images + units * d.k_heads * ((d.dtype == VQMLP_BF16 ? 2 : 1) * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
+    // more requests may leave max_q to the recurrence, and so their workspace empty, where fewer take chunks
+    G.step = d.max_q <= few || (d.max_q <= most_few && room < chunks_bytes);
     if (G.step) return G;
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
@@ -194,18 +202,18 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus) {
     // whole requests: the longest, or what all give each compute unit to do and a part of the other
     const double share = 0.625 * double(d.T) / kDeltaC * vs * d.v_heads / cus;
     double best = even ? rounds(d.R * vs) * chunks : std::max<double>(chunks, share) + 0.25 * std::min<double>(chunks, share);
+    auto seg_bytes = [&](int64_t L) { return (size_t(d.T / L) + d.R + 1) * d.v_heads * d.Dk * (d.Dv + d.Dk) * 4; };
     for (int n = 5; n < chunks && heads < 64 * cus; n += std::max(1, n / 8)) {  // more heads fill the card in any case
+        if (chunks_bytes > room || seg_bytes(n * kDeltaC) > room - chunks_bytes) continue;
         const int64_t per = (chunks + n - 1) / n, units = even ? d.R * per : std::max<int64_t>(d.T / (n * kDeltaC) + d.R / 2, d.R);
         const int64_t inner = units > d.R ? units - d.R : 0;  // segments but the last; M of those but the first
         const double cost = (rounds(inner * vs + std::max<int64_t>(0, inner - d.R) * ks) + rounds(units * vs)) * n + 1.8 * per + 1;
         if (cost < best) best = cost, G.split = true, G.L = n * kDeltaC;
     }
-    const size_t units = size_t(d.T) / kDeltaC + d.R + 1;
-    G.bytes = G.images = units * d.v_heads * kDeltaBlock;
-    G.bytes += units * d.k_heads * ((d.dtype == VQMLP_BF16 ? 2 : 1) * kDeltaC * (d.Dk <= 64 ? 64 : 128) * 2);
-    G.seg = G.bytes;
+    G.images = images;
+    G.seg = chunks_bytes;
     G.seg_units = d.T / G.L + d.R + 1;
-    if (G.split) G.bytes += size_t(G.seg_units) * d.v_heads * d.Dk * (d.Dv + d.Dk) * 4;
+    G.bytes = chunks_bytes + (G.split ? seg_bytes(G.L) : 0);
     return G;
 }
 
@@ -256,7 +264,7 @@ extern "C" vqmlp_status vqmlp_delta_rule_workspace(const vqmlp_delta_desc* p, si
     if (const vqmlp_status st = delta_check(p, "vqmlp_delta_rule_workspace")) return st;
     int cus = 0;
     if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
-    *bytes = delta_geom(*p, cus).bytes;
+    *bytes = delta_geom(*p, cus, SIZE_MAX).bytes;
     return op_ok();
 }
 
@@ -285,7 +293,7 @@ extern "C" vqmlp_status vqmlp_delta_rule(const vqmlp_delta_desc* p, void* worksp
                        "v and y be multiples of 8");
     }
     if (const int st = device_cus(&cus)) return static_cast<vqmlp_status>(st);
-    const DeltaGeom G = delta_geom(d, cus);
+    const DeltaGeom G = delta_geom(d, cus, workspace ? workspace_bytes : 0);
     if (G.bytes) {
         OP_REQUIRE(workspace && op_aligned(workspace, 256), "vqmlp_delta_rule: the workspace is null or not 256-byte aligned");
         if (workspace_bytes < G.bytes)

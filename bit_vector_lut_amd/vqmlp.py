@@ -1195,7 +1195,7 @@ class DeltaRule:
                           self._scale)
 
     def workspace_bytes(self, T, R, max_q):
-        """Bytes that hold for calls of either type on the current device."""
+        """Bytes that hold for calls of either type on the current device with no more tokens, requests and max_q."""
         n = [C.c_size_t(), C.c_size_t()]
         for dtype in (0, 1):
             _check(lib().vqmlp_delta_rule_workspace(C.byref(self._desc(dtype, T, R, 0, max_q)), C.byref(n[dtype])))

@@ -491,15 +491,21 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  *   S' = exp(g[t][h]) S_{t-1},  u_t = beta[t][h] (v_t - S'^T k_t),
  *   S_t = S' + k_t u_t^T,       y_t = scale * S_t^T q_t.
  * beta FP32 [T][v_heads] (token stride ld_beta).  Everything else as in the linear attention above: the arrays, their
- * strides and types, g and its bounds, states, slots, ctx_len, cu_q, rows behind the last request, max_q,
- * the workspace's rules and T and R's limits.  max_q up to 20 to 40, by how many heads and requests there are,
+ * strides and types, g and its bounds, states, slots, ctx_len, cu_q, rows behind the last request, max_q
+ * and T and R's limits.  max_q up to 20 to 40, by how many heads and requests there are,
  * takes the recurrence; above, short requests may take it beside the others' chunks, and few long ones go through
  * their chunks in segments.  Keys are meant to have length one and beta to lie in [0, 2];
  * beyond, the recurrence itself may grow without bound.  Either way the state keeps FP32 accuracy measured by each
  * column; chunks do so while the largest |k| beta of 64 tokens lies between 2^-64 and 2^64, and leave out elements of a
  * BF16 key below 2^-25 of its largest.  What is not finite in k, g or beta makes the outputs
  * of its head from its token on and the state NaN, in v or the state those of its column; in q its own outputs are NaN or
- * infinite. */
+ * infinite.
+ * The workspace (256-byte aligned, no zero fill) follows vqmlp_delta_rule_workspace of the same heads on the same device;
+ * two calls that overlap in time need one each.  The size for T, R and max_q holds for every call of that type with no more
+ * of each; a call that by itself would ask for more (segments, or chunks for few requests of up to 40 tokens) then
+ * does without, and its results may differ in their last bits.  Chunks take (T / 64 + R + 1) * (26624 * v_heads +
+ * b * k_heads) bytes, b = 8192 for F16 and Dk up to 64, twice that above 64 and twice that for BF16: 200 MB for 8,073 F16 tokens
+ * in 3 requests of 16 / 48 heads of 128, some 3 GB for 128K; segments up to as much again. */
 typedef struct {
     int dtype, T, R, k_heads, v_heads, Dk, Dv, n_states, max_q;
     float scale;

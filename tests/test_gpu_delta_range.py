@@ -216,3 +216,81 @@ def test_what_is_not_finite_gives_nan(vq, torch_dev, dtype, max_q, what, bad):
         y, s = op.forward(*new, start, cu, max_q=max_q)
         assert torch.equal(y[~hit], y0[~hit]) and y[hit].isnan().all(), t
         assert torch.equal(s[~lost], s0[~lost]) and s[lost].isnan().all(), t
+
+
+# ------------------------------------------------------------------ workspaces
+
+
+def _trace(capfd):
+    return [x for x in capfd.readouterr().err.splitlines() if "delta_rule" in x]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_one_workspace_for_smaller_calls(vq, torch_dev, dtype, capfd, monkeypatch):
+    """The size for the most tokens, requests and max_q holds for every call with no more of each, also where that
+    call by itself would ask for more."""
+    torch = torch_dev
+    monkeypatch.setenv("VQMLP_TRACE", "1")
+    op = vq.DeltaRule(2, 6, 64, 64)
+    for most, lens, max_q in (((4000, 4, 4000), [2000, 2000], 2000), ((900, 4, 900), [130, 70], 130),
+                              ((1280, 64, 32), [32, 32], 32), ((1280, 64, 32), [20, 32, 1], 25)):
+        work = torch.full((op.workspace_bytes(*most),), 255, dtype=torch.uint8, device="cuda")
+        args = _delta_inputs(torch, _t(torch, dtype), sum(lens), 2, 6, 64, 64, 51)
+        capfd.readouterr()
+        _check(vq, torch, dtype, lens, args, max_q, _randn(torch, (len(lens), 6, 64, 64), torch.float32, 52), work=work)
+        print(most, lens, op.workspace_bytes(sum(lens), len(lens), max_q), len(work), _trace(capfd), flush=True)
+
+
+def test_sizes_of_smaller_calls_are_accepted(vq, torch_dev):
+    """Sizes drawn over the whole range, each called with the workspace of a description that is no smaller in anything.
+    Nothing but zeros: no request has a token."""
+    import random
+
+    torch = torch_dev
+    rng = random.Random(5)
+    for _ in range(60):
+        hk, rep = rng.choice([1, 2, 4]), rng.choice([1, 2, 3])
+        op = vq.DeltaRule(hk, hk * rep, 8, 8)
+        T, R, m = rng.randint(1, 6000), rng.randint(1, 300), rng.randint(1, 6000)
+        need = op.workspace_bytes(T, R, m)
+        t, r, n = rng.randint(1, T), rng.randint(1, R), rng.randint(1, m)
+        q, v, g = (torch.zeros(s, device="cuda", dtype=d) for s, d in (
+            ((t, hk, 8), torch.bfloat16), ((t, hk * rep, 8), torch.bfloat16), ((t, hk * rep), torch.float32)))
+        print("delta", hk, rep, (T, R, m), (t, r, n), need, flush=True)
+        y, s = op.forward(q, q, v, g, g, torch.ones(r, hk * rep, 8, 8, device="cuda"), _i(torch, [0] * (r + 1)), max_q=n,
+                          workspace=torch.empty(max(1, need), dtype=torch.uint8, device="cuda"))
+        assert (y == 0).all() and (s == 1).all()
+
+
+def test_a_small_workspace_is_refused(vq, torch_dev):
+    torch = torch_dev
+    op = vq.DeltaRule(1, 2, 64, 64)
+    args = [x.cuda() for x in _delta_inputs(torch, torch.bfloat16, 300, 1, 2, 64, 64, 53)]  # the larger of both types' sizes
+    cu, state = _i(torch, [0, 300]), torch.zeros(1, 2, 64, 64, device="cuda")
+    need = op.workspace_bytes(300, 1, 300)
+    assert need > 0
+    with pytest.raises(vq.VqmlpError, match="needs"):
+        op.forward(*args, state, cu, max_q=300, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
+    y, s = op.forward(*args, state, cu, max_q=300, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(a, b) for a, b in zip((y, s), op.forward(*args, state, cu, max_q=300)))
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([4000], 1, 1, 128, 128), ([3001, 0, 1700, 1], 1, 2, 128, 72), ([2560, 2560], 2, 2, 64, 64),
+                                              ([64, 5000, 130], 1, 1, 40, 16), ([2113, 2049, 3071], 1, 2, 96, 104)])
+def test_which_calls_take_segments(vq, torch_dev, lens, hk, hv, dk, dv, capfd, monkeypatch):
+    """Few heads and long requests do, with a workspace that holds them; a workspace for the chunks alone is enough."""
+    torch = torch_dev
+    monkeypatch.setenv("VQMLP_TRACE", "1")
+    T, R = sum(lens), len(lens)
+    args = [x.cuda() for x in _delta_inputs(torch, torch.bfloat16, T, hk, hv, dk, dv, 54)]
+    op, cu, state = vq.DeltaRule(hk, hv, dk, dv), _i(torch, _starts(lens)), torch.zeros(R, hv, dk, dv, device="cuda")
+    chunks = (T // 64 + R + 1) * (26624 * hv + 8192 * (1 if dk <= 64 else 2) * 2 * hk)
+    assert op.workspace_bytes(T, R, max(lens)) > chunks
+    capfd.readouterr()
+    got = [op.forward(*args, state, cu, max_q=max(lens), workspace=w) for w in (
+        None, torch.full((chunks,), 255, dtype=torch.uint8, device="cuda"))]
+    torch.cuda.synchronize()
+    assert ["join" in x for x in _trace(capfd)] == [True, False]
+    # both within a rounding of the same values
+    (y, s), (y1, s1) = got
+    assert (s - s1).norm() <= 1e-5 * s.norm() and (y.float() - y1.float()).norm() <= 2.0 ** -8 * y.float().norm()
