@@ -30,10 +30,7 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # The fused T <= 8 kernel measured 1-2% faster per layer with the same scheduler (its product loop
 # then keeps more lookups in flight ahead of the matrix-core steps).
 SOURCE_FLAGS = {"vq3mm.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
-                "fused.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
-                # One workgroup a compute unit: left to itself the compiler keeps matrix-core results in
-                # accumulation registers and copies them (a quarter of the scan's vector instructions).
-                "delta_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+                "fused.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]}
 
 
 def build(verbose: bool = False) -> str:
