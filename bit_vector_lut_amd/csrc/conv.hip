@@ -12,9 +12,9 @@
 // in 66 us, 331 MB at 5.0 TB/s. What it took: whole rounds of four rows without a branch between
 // them, so that four rows are on their way and the sums over heads of four tokens are taken together
 // (104 -> 73 us); units of 16 tokens instead of 32 (-> 66; 64: 74). Eight rows on their way need 172
-// registers, and two waves on a SIMD instead of four cost more than the loads give (130 us).
+// registers, and two waves on a SIMD instead of three (binary16, W = 4: 134 registers) cost more than the loads give (130 us).
 // Bound by latency for few tokens: the search for the unit, one round of loads, one row's sums.
-// 8 tokens in 5.1 us, 64 requests with a token each in 5.8 us.
+// 8 tokens in 5.2 us, 64 requests with a token each in 5.8 us.
 #include "op.h"
 
 #include <algorithm>

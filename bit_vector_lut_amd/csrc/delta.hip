@@ -172,9 +172,12 @@ struct DeltaGeom {
 DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus, size_t room) {
     DeltaGeom G{};
     // A token of the recurrence takes 0.6 us, or more where its waves fill the card; a chunk takes the same for one token
-    // as for 64.  They meet at 21 tokens for one request of up to 48 heads (20 us), 28 for eight (50 us) and
-    // 45 for 64 (370 us).  Requests of different lengths that fill the card with a chunk each (64 requests of 48
-    // heads, 63 of them with one token, one with 512: 377 us in chunks, 143 so) go each its own way.
+    // as for 64.  They meet, for heads of 128 x 128, at 24 tokens for one request of 48 heads (19 us), 29 for eight (50 us)
+    // and 48 for 64 (370 us), of 8 heads at 25, 25 and 31; for heads of 64 x 64 at 20 (15 us), 40 (30 us) and
+    // over 48, of 8 heads at 18, 19 and 34: the bounds are those of 128 x 128, and smaller heads of many requests take up
+    // to 1.4 times as long between them and where they meet (64 requests of 41 tokens: 155 us in chunks, 111 by the recurrence).
+    // Requests of different lengths that fill the card with a chunk each (64 requests of 48
+    // heads, 63 of them with one token, one with 512: 377 us in chunks, 142 so) go each its own way.
     const int64_t heads = int64_t(d.R) * d.v_heads;
     constexpr int most_few = 40;
     const int few = heads >= 8 * cus ? most_few : heads >= cus ? 28 : 20;
@@ -186,11 +189,12 @@ DeltaGeom delta_geom(const vqmlp_delta_desc& d, int cus, size_t room) {
     if (G.step) return G;
     // not split: a segment holds all T tokens, so any request fits, whatever max_q says
     G.L = std::max(1, (d.T + kDeltaC - 1) / kDeltaC) * kDeltaC;
-    // Costs in a chunk's time (1.9 us).  In segments a request's chain is walked twice, a segment's length each time, with
+    // Costs in a chunk's time (some 2 us).  In segments a request's chain is walked twice, a segment's length each time, with
     // a join between (3.3 us a segment) and two more launches.  A compute unit holds two workgroups of 32 columns,
-    // which then take a quarter longer; an XCD fills up before all of them do.  8,000 tokens of 6 heads of
-    // 128 x 128: 259 us whole, 121 in segments of 12 chunks, 129 of 21, 143 of 9; of 24 heads 282, 230 of 32, 271 of
-    // 18; of 48 heads 318, 412 of 32.
+    // which then take a quarter longer; an XCD fills up before all of them do.  8,000 tokens, BF16, whole and in
+    // segments: 6 heads of 128 x 128 293 and 124 us, 24 heads 310 and 247, 48 heads 348 whole;
+    // of 64 x 64 226 and 85, 245 and 145, 275 and 263.  Near the border the choice may be the slower one: 1,500 tokens
+    // of 24 heads of 128 x 128 81 and 90 us, of 48 heads of 64 x 64 70 and 80.
     const int most = std::max(1, std::min(d.max_q, std::max(1, d.T))), chunks = (most + kDeltaC - 1) / kDeltaC;
     const bool even = d.T == int64_t(d.R) * most;  // all requests are as long as the longest
     G.few = heads >= cus && !even ? few : -1;

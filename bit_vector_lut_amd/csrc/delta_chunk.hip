@@ -17,14 +17,16 @@
 // binary16 by a power of two for each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14),
 // 2^-25 of a key's (brought to 1: K^T U is added to the state as it comes).  The
 // outputs are made of two parts of P, U and S too, so that their one rounding is at the end, as in the
-// recurrence: with one part of each they were 3.4e-4 off instead of 2.1e-4 (binary16), with one of P alone 2.7e-4
-// (257, 290 and 268 us for three prompts).  The second parts of U and S go to the outputs' waves in the place of T, which
+// recurrence: 2.1e-4 of their norm off (binary16), where one part of each gives 3.4e-4 and one of P alone 2.7e-4 (three
+// prompts: 281, 257 and 268 us).  The second parts of U and S go to the outputs' waves in the place of T, which
 // they load again.  The triangular system is solved in FP32.
 //
-// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 290 us a call, where
+// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 281 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
-// between them: 1.9 us alone on a compute unit, 2.6 beside another workgroup, of which the matrix cores work 0.6.
-// k_delta_prep (71 us of it) writes 151 MB and reads 66: 62% of a copy's rate, with LDS and the triangular solve.
+// between them: 2.2 us alone on a compute unit, 2.7 beside another workgroup, of which the matrix cores work 0.6.
+// k_delta_prep (75 us of it) writes 188 MB and reads 57: 67% of a copy's rate, with LDS and the triangular solve.
+// The scan with outputs has no register left for heads of 128: it takes all 256 and keeps 1 (binary16) or 24 (bfloat16)
+// in memory, outside the chunks' loop.
 #include "delta.h"
 
 #include <algorithm>

@@ -8,8 +8,8 @@
 // FP64, brought to one turn before it is rounded: at position 10^6 an FP32 product would be off by 0.06.
 // Norm, turn and sums are FP32 and rounded once.
 //
-// Bound by memory for prompts: 8,192 tokens, 24 + 4 heads of 256 with 64 turned, in 46 us, 268 MB at
-// 5.8 TB/s (part of the writes still on the way to memory). One angle a thread, kept in LDS for the heads of
+// Bound by memory for prompts: 8,192 tokens, 24 + 4 heads of 256 with 64 turned, in 45 us, 268 MB at
+// 5.9 TB/s (part of the writes still on the way to memory). One angle a thread, kept in LDS for the heads of
 // a workgroup, instead of each lane's own for each head, and four heads on their way at a time: 102 -> 46 us.
 // Few tokens: latency. 8 tokens in 3.6 us, 64 requests' single tokens in 5.4 us, 512 tokens of 40 + 8 heads
 // of 128 in 6.2 us, where the sines bound.

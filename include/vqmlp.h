@@ -495,9 +495,10 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  * and T and R's limits.  max_q up to 20 to 40, by how many heads and requests there are,
  * takes the recurrence; above, short requests may take it beside the others' chunks, and few long ones go through
  * their chunks in segments.  Keys are meant to have length one and beta to lie in [0, 2];
- * beyond, the recurrence itself may grow without bound.  Either way the state keeps FP32 accuracy measured by each
- * column; chunks do so while the largest |k| beta of 64 tokens lies between 2^-64 and 2^64, and leave out elements of a
- * BF16 key below 2^-25 of its largest.  What is not finite in k, g or beta makes the outputs
+ * beyond, the recurrence itself may grow without bound.  Token by token all is FP32.  Chunks keep FP32 accuracy
+ * measured by the largest of a column of the state and of the updates that 64 tokens make to it, |k| beta of the largest of these
+ * between 2^-64 and 2^64 of one; they leave out elements of a BF16 key below 2^-25 of its largest and of a BF16
+ * query below 2^-40.  Outputs are rounded to 16 bits once.  What is not finite in k, g or beta makes the outputs
  * of its head from its token on and the state NaN, in v or the state those of its column; in q its own outputs are NaN or
  * infinite.
  * The workspace (256-byte aligned, no zero fill) follows vqmlp_delta_rule_workspace of the same heads on the same device;
