@@ -12,21 +12,21 @@
 //
 // Precision.  What reaches the state keeps FP32 accuracy: matrix-core operands made here (S, V - K S, T, U)
 // are sums of two binary16 parts (22 bits) in units of 2^-e that put a column's (of T, a row's) largest
-// element into the upper range of binary16.  The state and U may be smaller than the values by the sizes of the keys and of
-// beta: their units are 2^-(e + lift) and 2^-(e + ulift), the same for all columns of a chunk.  Keys and queries are binary16 as they are; bfloat16 ones become
-// binary16 by a power of two for each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14),
-// 2^-25 of a key's (brought to 1: K^T U is added to the state as it comes).  The
-// outputs are made of two parts of P, U and S too, so that their one rounding is at the end, as in the
-// recurrence: 2.1e-4 of their norm off (binary16), where one part of each gives 3.4e-4 and one of P alone 2.7e-4 (three
-// prompts: 281, 257 and 268 us).  The second parts of U and S go to the outputs' waves in the place of T, which
-// they load again.  The triangular system is solved in FP32.
+// element into the upper range of binary16.  The state and U may be smaller than the values by the sizes of
+// the keys and of beta: their units are 2^-(e + lift) and 2^-(e + ulift), lift and ulift the same for all columns
+// of a chunk.  Keys and queries are binary16 as they are; bfloat16 ones become binary16 by a power of two for
+// each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14), 2^-25 of a key's (brought
+// to 1: K^T U is added to the state as it comes).  The outputs are made of two parts of P, U and S too, so that
+// their one rounding is at the end, as in the recurrence: 2.1e-4 of their norm off (binary16), where one part of
+// each gives 3.4e-4 and one of P alone 2.7e-4 (three prompts: 281, 257 and 268 us).  The second parts of U and S
+// go to the outputs' waves in the place of T, which they load again.  The triangular system is solved in FP32.
 //
 // Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 281 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
 // between them: 2.2 us alone on a compute unit, 2.7 beside another workgroup, of which the matrix cores work 0.6.
 // k_delta_prep (75 us of it) writes 188 MB and reads 57: 67% of a copy's rate, with LDS and the triangular solve.
-// The scan with outputs has no register left for heads of 128: it takes all 256 and keeps 1 (binary16) or 24 (bfloat16)
-// in memory, outside the chunks' loop.
+// The scan with outputs has no register left for heads of 128: it takes all 256 and keeps 8 (binary16) or 31 (bfloat16)
+// in memory, some of them from chunk to chunk.
 #include "delta.h"
 
 #include <algorithm>
@@ -36,6 +36,7 @@ namespace vqmlp {
 namespace {
 
 constexpr int kC = kDeltaC;
+constexpr int kIdle = 1 << 16;
 
 // A block of the workspace: parts of T and P as the lanes of the matrix cores take them (1 KB each) and
 // factors for each token; what the state's chain takes, then what the outputs take.
@@ -46,7 +47,7 @@ struct StateBlock {
     float tf[kC];  // e^(b_64 - b) 2^(kexp + lift - ulift): of U where it joins the state
     float etot;    // e^b_64
     int bad;       // first token with something not finite in k, g or beta, or 64
-    int lift;      // the state is in units of 2^-lift of the values' here
+    int lift;      // the state is in units of 2^-lift of the values' here; kIdle: of 1, and no token changes it
     int pad[61];
 };
 struct OutBlock {
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(256, 4) k_delta_prep(DeltaArgs a, int per) {
             blk.s.tf[lane] = exp_b(all - b + double(ke + lift - ulift));
             if (lane == 0) {
                 sm.bad = bad, sm.lift = lift, sm.ulift = ulift;
-                blk.s.etot = exp_b(all), blk.s.bad = bad, blk.s.lift = lift;
+                blk.s.etot = exp_b(all), blk.s.bad = bad, blk.s.lift = tb == none ? kIdle : lift;
             }
         }
         __syncthreads();
@@ -823,20 +824,7 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
         const uint8_t* const kb = reinterpret_cast<const uint8_t*>(st.k);
         int late = st.d.bad;  // first token that the column gets no number from
         const float etot = st.d.etot;
-        if (__builtin_expect(__any(st.d.lift != lift), 0)) {  // up to 2^128 in two steps
-            const int by = st.d.lift - lift;
-            scale_state(pow2(by / 2));
-            scale_state(pow2(by - by / 2));
-            lift += by;
-        }
-        // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
-        float big = 0.f;
-#pragma unroll
-        for (int p = 0; p < KS; ++p)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(S[p][b][i]));
+        const int next_lift = uniform(st.d.lift);
         uint32_t vtop = largest(vb);
         if (__builtin_expect(__any(vtop >= kInf16<E>), 0)) {
             // of the finite ones, and the first of the others
@@ -856,6 +844,28 @@ __global__ void __launch_bounds__(128 * kPairs, 2) k_delta_scan(DeltaArgs a) {
             late = min(late, __shfl_xor(late, 32));
             vtop = largest(vb);
         }
+        if (__builtin_expect(next_lift != lift, 0)) {
+            const bool idle = next_lift == kIdle;
+            const int by = (idle ? 0 : next_lift) - lift;
+            scale_state(pow2(by / 2));  // up to 2^128 in two steps
+            scale_state(pow2(by - by / 2));
+            lift += by;
+            if (idle) {  // the values count for nothing: the unit follows the state alone
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) vb[p][b] = u32x2{0, 0};
+                vtop = 0;
+            }
+        }
+        // the column's unit: S and V below 2^11 in it, the larger of them from 2^5 on
+        float big = 0.f;
+#pragma unroll
+        for (int p = 0; p < KS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(S[p][b][i]));
         const float top = lo16<E>(vtop);
         const bool any_late = __any(late < kC);
         const int none = -1000;

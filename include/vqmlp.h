@@ -406,7 +406,7 @@ vqmlp_status vqmlp_paged_attn(const vqmlp_attn_desc *desc, void *workspace, size
  * for the pairs p < rot / 2: VQMLP_PAIRS_HALF turns elements (p, p + rot / 2), VQMLP_PAIRS_NEXT (2p, 2p + 1);
  * elements from rot on are not turned.  rot is a multiple of 8 up to D (0: no rotation, inv_freq may be
  * NULL).  Angles are reduced in FP64, so that far positions keep their low digits; norm and rotation are
- * FP32, each output is rounded once; values are copied.
+ * FP32 (heads to be normed below 2^60, whose squares FP32 holds), each output is rounded once; values are copied.
  * q [T][heads][D], k and v [T][kv_heads][D] with token strides ld_* and head strides hs_* (elements,
  * multiples of 8, from 0 up to 2^40 and 2^24; 16-byte aligned); q_out [T][heads][D] with token stride
  * ld_q_out of at least heads * D; it may be q (the same strides), no other overlap.  heads 0: no queries
@@ -435,7 +435,7 @@ vqmlp_status vqmlp_paged_append(const vqmlp_append_desc *desc, void *stream);
  * Rows in front of a request's first are the last rows of its state, state_in [slots][W-1][C], oldest
  * first; state_out receives the last W - 1 rows of x (with the state's rows where the request has fewer
  * tokens), bit for bit.  The first unit_heads heads of unit_dim channels are brought to length one:
- *   y -> y / sqrt(sum over the head of y^2 + eps)
+ *   y -> y / sqrt(sum over the head of y^2 + eps),  the sum in FP32: |y| below 2^60
  * x, y [T][C] (F16 or BF16, token strides ld_*: multiples of 8 up to 2^24, 16-byte aligned), weight
  * [C][W], bias [C] or NULL and the states of the same type, 16-byte aligned.  C is a multiple of 8 up to
  * 2^20, unit_dim one up to 256, unit_heads * unit_dim at most C.  x and y do not overlap.
@@ -496,8 +496,8 @@ vqmlp_status vqmlp_linear_attn(const vqmlp_linear_desc *desc, void *workspace,
  * takes the recurrence; above, short requests may take it beside the others' chunks, and few long ones go through
  * their chunks in segments.  Keys are meant to have length one and beta to lie in [0, 2];
  * beyond, the recurrence itself may grow without bound.  Token by token all is FP32.  Chunks keep FP32 accuracy
- * measured by the largest of a column of the state and of the updates that 64 tokens make to it, |k| beta of the largest of these
- * between 2^-64 and 2^64 of one; they leave out elements of a BF16 key below 2^-25 of its largest and of a BF16
+ * measured by the larger of a column of the state and, of 64 tokens, the largest |k| beta (from 2^-64 to 2^64) times
+ * the column's largest |v|; they leave out elements of a BF16 key below 2^-25 of its largest and of a BF16
  * query below 2^-40.  Outputs are rounded to 16 bits once.  What is not finite in k, g or beta makes the outputs
  * of its head from its token on and the state NaN, in v or the state those of its column; in q its own outputs are NaN or
  * infinite.

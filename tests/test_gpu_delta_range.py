@@ -3,6 +3,8 @@
 Tolerances.  u = eps / 2 of the 16-bit type is one rounding, W = 2^-24 one of FP32.  A token adds to a column of
 the state at most C W (|S'| + a), a = |k| beta (|v| + |k| |S'|): its own sums and, in chunks, those of the
 triangular system, C = 2 (Dk + 64).  Z sums that up with the decays, B the lengths |k| |u| that a column is made of.
+Chunks of 64 tokens have one unit for all updates of a column: their largest is at least 2^5 2^-4 in it, and a binary16 part's
+last bit is 2^-24, so where tokens of a chunk differ a is the largest |k| beta times the largest |v| + |k| |S'|.
 An output adds C W scale |q| (B + Z) and its one rounding.
 """
 import math
@@ -17,7 +19,7 @@ pytestmark = pytest.mark.gpu
 TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}  # half a step of the smallest outputs
 
 
-def _ref(torch, q, k, v, g, beta, state, cu, scale):
+def _ref(torch, q, k, v, g, beta, state, cu, scale, chunks=False):
     """Outputs, their bounds B and Z, states and theirs, in 64 bits."""
     T, hk, dk = q.shape
     hv, dv = v.shape[1:]
@@ -30,11 +32,15 @@ def _ref(torch, q, k, v, g, beta, state, cu, scale):
         B = S.norm(dim=1)
         Z = torch.zeros_like(B)
         for t in range(cu[r], cu[r + 1]):
+            if chunks and (t - cu[r]) % 64 == 0:
+                c = slice(t, min(t + 64, cu[r + 1]))
+                lengths = kd[c].norm(dim=2)[..., None]
+                most = (lengths * bd[c]).amax(0) * (vd[c].abs().amax(0) + lengths.amax(0) * S.norm(dim=1))
             S = e[t][..., None] * S
             length = kd[t].norm(dim=1)[:, None]
             u = bd[t] * (vd[t] - (S * kd[t][..., None]).sum(1))
             s = S.norm(dim=1)
-            Z = e[t] * Z + s + length * bd[t] * (vd[t].abs() + length * s)
+            Z = e[t] * Z + s + (most if chunks else length * bd[t] * (vd[t].abs() + length * s))
             B = e[t] * B + length * u.abs()
             S = S + kd[t][:, :, None] * u[:, None, :]
             y[t] = scale * (S * qd[t][..., None]).sum(1)
@@ -43,7 +49,7 @@ def _ref(torch, q, k, v, g, beta, state, cu, scale):
     return y, yb, out, sb
 
 
-def _check(vq, torch, dtype, lens, args, max_q, state=None, scale=None, work=None):
+def _check(vq, torch, dtype, lens, args, max_q, state=None, scale=None, work=None, chunks=False):
     q, k, v, g, beta = args
     hk, dk, hv, dv = q.shape[1], q.shape[2], v.shape[1], v.shape[2]
     cu = _starts(lens)
@@ -53,7 +59,7 @@ def _check(vq, torch, dtype, lens, args, max_q, state=None, scale=None, work=Non
     print("delta", dtype, lens, hk, hv, dk, dv, max_q, flush=True)
     y, out = op.forward(*(x.cuda() for x in args), state.cuda(), _i(torch, cu), max_q=max_q, workspace=work)
     torch.cuda.synchronize()
-    ry, yb, rs, sb = _ref(torch, *args, state, cu, op.scale)
+    ry, yb, rs, sb = _ref(torch, *args, state, cu, op.scale, chunks)
     c = 2 * (dk + 64) * W
     _close(torch, y, ry, _u(torch, _t(torch, dtype)) * ry.abs() + c * yb + TINY[dtype], "y")
     _close(torch, out, rs, c * sb + 2.0 ** -148, "state")
@@ -216,6 +222,38 @@ def test_what_is_not_finite_gives_nan(vq, torch_dev, dtype, max_q, what, bad):
         y, s = op.forward(*new, start, cu, max_q=max_q)
         assert torch.equal(y[~hit], y0[~hit]) and y[hit].isnan().all(), t
         assert torch.equal(s[~lost], s0[~lost]) and s[lost].isnan().all(), t
+
+
+@pytest.mark.parametrize("max_q", [16, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_closed_gates(vq, torch_dev, dtype, max_q):
+    """A state that only decays, while the values go on: its outputs are measured by it alone."""
+    torch = torch_dev
+    q, k, v, g, beta = _delta_inputs(torch, _t(torch, dtype), 280, 1, 2, 64, 64, 44)
+    beta[70:, 0] = 0.0
+    beta[:, 1] = 0.0
+    g[:, 1] *= 0.1
+    state = _randn(torch, (1, 2, 64, 64), torch.float32, 45)
+    state[:, 1] *= 2.0 ** -30
+    for h, scale in ((0, None), (1, 2.0 ** 20)):  # of each within binary16
+        _check(vq, torch, dtype, [280], (q, k, *(x[:, h:h + 1].clone() for x in (v, g, beta))), max_q, state[:, h:h + 1].clone(),
+               scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_segments_of_other_sizes(vq, torch_dev, dtype):
+    """Units that change from chunk to chunk inside segments and at their ends, from a state of zeros and from another."""
+    torch = torch_dev
+    T = 4000
+    q, k, v, g, beta = _delta_inputs(torch, _t(torch, dtype), T, 1, 2, 64, 64, 42)
+    for at in range(0, T, 500):
+        beta[at:at + 130] *= 2.0 ** -(at // 100)
+        if dtype == "bf16":
+            k[at + 200:at + 330] *= 2.0 ** -(at // 100)
+    beta[700:1400, 1] = 0.0
+    assert vq.DeltaRule(1, 2, 64, 64).workspace_bytes(T, 1, T) > (T // 64 + 2) * (26624 * 2 + 16384)
+    for state in (None, _randn(torch, (1, 2, 64, 64), torch.float32, 43)):
+        _check(vq, torch, dtype, [T], (q, k, v, g, beta), T, state, chunks=True)
 
 
 # ------------------------------------------------------------------ workspaces
