@@ -18,10 +18,10 @@
 // each row, which leaves out at most 2^-40 of a query's largest element (brought to 2^14), 2^-25 of a key's (brought
 // to 1: K^T U is added to the state as it comes).  The outputs are made of two parts of P, U and S too, so that
 // their one rounding is at the end, as in the recurrence: 2.1e-4 of their norm off (binary16), where one part of
-// each gives 3.4e-4 and one of P alone 2.7e-4 (three prompts: 281, 257 and 268 us).  The second parts of U and S
+// each gives 3.4e-4 and one of P alone 2.7e-4 (three prompts: 282, 257 and 268 us).  The second parts of U and S
 // go to the outputs' waves in the place of T, which they load again.  The triangular system is solved in FP32.
 //
-// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 281 us a call, where
+// Bound: not by memory or the matrix cores (three prompts of 8,073 tokens, 48 heads of 128 x 128: 282 us a call, where
 // the bytes take 58 and the products 39), but by the chain.  A chunk's products depend on each other and on conversions
 // between them: 2.2 us alone on a compute unit, 2.7 beside another workgroup, of which the matrix cores work 0.6.
 // k_delta_prep (75 us of it) writes 188 MB and reads 57: 67% of a copy's rate, with LDS and the triangular solve.
